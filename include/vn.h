@@ -64,7 +64,8 @@ typedef enum vn_status {
   VN_ERR_TIMEOUT = 7,  /* a device-side bounded wait ran out (vn_device_status)     */
   VN_ERR_CUDA = 8,     /* a CUDA runtime call failed (vn_last_error_message)        */
   VN_ERR_DEVICE = 9,   /* the requested path needs a compute-capability 10.x GPU    */
-  VN_ERR_PATH = 10     /* the forced forward path cannot run these arguments        */
+  VN_ERR_PATH = 10,    /* the forced forward path cannot run these arguments        */
+  VN_ERR_WORKSPACE = 11 /* the workspace is smaller than the call's _workspace says  */
 } vn_status;
 
 typedef enum vn_dtype { VN_F32 = 0, VN_BF16 = 1 } vn_dtype;
@@ -88,8 +89,15 @@ typedef enum vn_noise {
                          /* u1 is within 2^-12 of 1 (G near 0), about 1e-6 elsewhere.        */
 } vn_noise;
 
-/* Element-wise activation applied to Y after the bias (vn_perturbed_linear_ex). */
-typedef enum vn_act { VN_ACT_NONE = 0, VN_ACT_TANH = 1 } vn_act;
+/* Element-wise activation applied to Y after the bias. The perturbed calls have the first
+ * two; vn_linear and vn_linear_backward have all of them. */
+typedef enum vn_act {
+  VN_ACT_NONE = 0,
+  VN_ACT_TANH = 1,
+  VN_ACT_RELU = 2,  /* max(z, 0)                                    */
+  VN_ACT_GELU = 3,  /* z Phi(z), Phi the normal distribution function */
+  VN_ACT_SILU = 4   /* z / (1 + exp(-z))                            */
+} vn_act;
 
 /*
  * vn_perturbed_linear -- "virtual_perturbed_linear" (API entry of the page):
@@ -300,6 +308,129 @@ vn_status vn_centered_ranks(const float* fitness, int64_t pop, float* out, void*
  * must not overlap.
  */
 vn_status vn_es_update(float* theta, const float* grad, int64_t n, double lr, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * The centre network. The entry points above perturb a network; those below run it
+ * unperturbed, give its gradients, and turn a gradient into a parameter step.
+ * ------------------------------------------------------------------------------------ */
+
+/*
+ * vn_linear -- a linear layer with bias, activation and residual in one epilogue:
+ *     z = x W^T + b,   y = act(z) + residual
+ * x [rows, in], w [out, in], residual [rows, out] or NULL, y [rows, out] and preact
+ * [rows, out] or NULL (receives z, for vn_linear_backward): all of type dt. b [out] of
+ * b_dt or NULL. Products are exact and sums are held in fp32; y and preact are each
+ * rounded once, y from the unrounded z. in == 0 gives z = b.
+ * workspace: vn_linear_workspace bytes of device memory, 256-byte aligned, in use until
+ * the call's work on `stream` is done (NULL when that is 0). With dt VN_F32 and larger
+ * sizes the matrices are split into three bf16 terms each there (exact: 8 + 8 + 8
+ * significant bits) and multiplied on the tensor cores by the six products of the terms
+ * that reach fp32's precision; there an infinity gives NaN where the exact sum would be
+ * infinite. Errors: VN_ERR_WORKSPACE, and those of vn_perturbed_linear. The tensor-core
+ * kernels bound their waits: results are valid only after vn_device_status returned VN_OK.
+ */
+vn_status vn_linear(const void* x, const void* w, vn_dtype dt, const void* b, vn_dtype b_dt,
+                    const void* residual, int64_t rows, int64_t in, int64_t out, vn_act act,
+                    void* y, void* preact, void* workspace, int64_t workspace_bytes,
+                    void* stream);
+
+/* Workspace of vn_linear in bytes, -1 for sizes or a dtype that it refuses. aligned: x and
+ * w start on 16-byte boundaries. */
+int64_t vn_linear_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, int aligned);
+
+/*
+ * vn_linear_backward -- the gradients of vn_linear:
+ *     d = grad * act'(z),  grad_x = d W,  grad_w = d^T x,  grad_b[j] = sum_m d[m, j]
+ * (the residual's gradient is grad itself). grad [rows, out], x [rows, in], w [out, in]
+ * and preact [rows, out] (z as vn_linear stored it; NULL with VN_ACT_NONE) of type dt;
+ * grad_x [rows, in] and grad_w [out, in] of type dt, either may be NULL (not computed);
+ * grad_b [out] of gb_dt or NULL. For bf16 matrices with an activation d is rounded once to bf16 before
+ * the two products (as the tensor cores take it); grad_b sums the unrounded d. Sums are held
+ * in fp32 in a fixed order. rows == 0 gives zero grad_w and grad_b. Workspace, errors and
+ * status as for vn_linear.
+ */
+vn_status vn_linear_backward(const void* grad, const void* x, const void* w, const void* preact,
+                             vn_dtype dt, int64_t rows, int64_t in, int64_t out, vn_act act,
+                             void* grad_x, void* grad_w, void* grad_b, vn_dtype gb_dt,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace of vn_linear_backward in bytes (an upper bound over which gradients are asked
+ * for), -1 for sizes or a dtype that it refuses. aligned: grad, x and w start on 16-byte
+ * boundaries. */
+int64_t vn_linear_backward_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt,
+                                     vn_act act, int aligned);
+
+/*
+ * vn_layer_norm -- each row to zero mean and unit variance, then scaled and shifted:
+ *     mean = sum_k x_k / n,  rstd = 1 / sqrt(sum_k (x_k - mean)^2 / n + eps),
+ *     y_k = (x_k - mean) rstd w_k + b_k
+ * x and y [rows, n] of dt; w and b [n] of w_dt, each may be NULL (1 and 0); mean and rstd
+ * [rows] fp32, each may be NULL (not stored). n >= 1; eps finite and >= 0. All arithmetic in fp32,
+ * the variance from the centred values; y is rounded once.
+ */
+vn_status vn_layer_norm(const void* x, vn_dtype dt, const void* w, const void* b, vn_dtype w_dt,
+                        int64_t rows, int64_t n, double eps, void* y, float* mean, float* rstd,
+                        void* stream);
+
+/*
+ * vn_layer_norm_backward -- the gradients of vn_layer_norm from its stored statistics:
+ *     h = (x - mean) rstd,  t = grad w,
+ *     grad_x = rstd (t - sum_k t_k / n - h sum_k t_k h_k / n),
+ *     grad_w[k] = sum_rows grad h,  grad_b[k] = sum_rows grad
+ * grad, x and grad_x [rows, n] of dt; w [n] of w_dt or NULL (1); grad_w and grad_b [n] of
+ * w_dt, each may be NULL (not computed). The sums over rows are held in fp32 in a fixed
+ * order. rows == 0 gives zero grad_w and grad_b. workspace: vn_layer_norm_backward_workspace
+ * bytes, 256-byte aligned.
+ */
+vn_status vn_layer_norm_backward(const void* grad, const void* x, vn_dtype dt, const float* mean,
+                                 const float* rstd, const void* w, vn_dtype w_dt, int64_t rows,
+                                 int64_t n, void* grad_x, void* grad_w, void* grad_b,
+                                 void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace of vn_layer_norm_backward in bytes, -1 for sizes that it refuses. */
+int64_t vn_layer_norm_backward_workspace(int64_t rows, int64_t n);
+
+/* One tensor of vn_adamw: its parameters, their gradient, and its two moments. With 8-bit
+ * moments exp_avg and exp_avg_sq hold one e4m3 code per element and the scales one fp32 per
+ * block of 256 elements (ceil(n / 256) of them); with 32 bits they are fp32 and the scales
+ * unused. */
+typedef struct vn_adamw_tensor {
+  void* param;             /* [n] of param_dt, updated in place          */
+  const void* grad;        /* [n] of grad_dt                             */
+  void* exp_avg;           /* [n], updated in place                      */
+  void* exp_avg_sq;        /* [n], updated in place                      */
+  float* exp_avg_scale;    /* [ceil(n / 256)], 8-bit moments only        */
+  float* exp_avg_sq_scale; /* [ceil(n / 256)], 8-bit moments only        */
+  int64_t n;
+  double weight_decay;
+} vn_adamw_tensor;
+
+/*
+ * vn_adamw -- one AdamW step over n_tensors tensors (a HOST array, read during the call):
+ *     g = maximize ? -grad : grad
+ *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *     p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in fp32, p rounded once to param_dt. maximize ascends: the direction of a fitness gradient
+ * (vn_gradient_ex and the others). step counts from 1. state_bits 32 or 8. With 8 bits a
+ * moment is stored per block of 256 elements of its tensor as the block's largest magnitude
+ * / 448 (its scale) and e4m3 codes in units of it; exp_avg_sq's codes are of sqrt(v), of
+ * which a positive one is never stored as 0 (it divides the next step): at least 2^-9. A block whose
+ * largest magnitude is below 1e-30 is stored as zeros. The step itself uses the unrounded moments;
+ * a gradient that is not finite makes its block's moments not finite. Tensors of a
+ * call may not overlap one another. 0 <= beta < 1, eps >= 0, all finite.
+ */
+vn_status vn_adamw(const vn_adamw_tensor* tensors, int64_t n_tensors, vn_dtype param_dt,
+                   vn_dtype grad_dt, int state_bits, double lr, double beta1, double beta2,
+                   double eps, int64_t step, int maximize, void* stream);
+
+/*
+ * vn_adamw_moments -- the values that 8-bit moments of n elements stand for:
+ *     m[e] = e4m3(exp_avg[e]) * exp_avg_scale[e / 256],
+ *     v[e] = (e4m3(exp_avg_sq[e]) * exp_avg_sq_scale[e / 256])^2      (fp32)
+ */
+vn_status vn_adamw_moments(const void* exp_avg, const void* exp_avg_sq, const float* exp_avg_scale,
+                           const float* exp_avg_sq_scale, int64_t n, float* m, float* v,
+                           void* stream);
 
 /* Synchronises `stream`, then reads and clears the current device's status
  * word: VN_ERR_TIMEOUT if a kernel of this library recorded an expired wait

@@ -18,14 +18,14 @@ VN_OK = 0
 STATUS_NAMES = {
     0: "VN_OK", 1: "VN_ERR_NULL", 2: "VN_ERR_SHAPE", 3: "VN_ERR_DTYPE", 4: "VN_ERR_VALUE",
     5: "VN_ERR_ALIGN", 6: "VN_ERR_OVERFLOW", 7: "VN_ERR_TIMEOUT", 8: "VN_ERR_CUDA",
-    9: "VN_ERR_DEVICE", 10: "VN_ERR_PATH",
+    9: "VN_ERR_DEVICE", 10: "VN_ERR_PATH", 11: "VN_ERR_WORKSPACE",
 }
 # vn_dtype
 VN_F32, VN_BF16 = 0, 1
 # vn_path
 VN_PATH_AUTO, VN_PATH_FFMA, VN_PATH_TC = 0, 1, 2
 # vn_act
-VN_ACT_NONE, VN_ACT_TANH = 0, 1
+VN_ACT_NONE, VN_ACT_TANH, VN_ACT_RELU, VN_ACT_GELU, VN_ACT_SILU = 0, 1, 2, 3, 4
 # vn_noise
 VN_NOISE_UNIFORM, VN_NOISE_GAUSSIAN = 0, 1
 
@@ -58,6 +58,15 @@ SIGNATURES = {
     "vn_last_error_message": (ctypes.c_char_p, []),
     "vn_perturbed_linear_path": (_I, [_P, _I, _I, _P, _I, _I64, _I64, _I64]),
     "vn_version": (_I, []),
+    "vn_linear": (_I, [_P, _P, _I, _P, _I, _P, _I64, _I64, _I64, _I, _P, _P, _P, _I64, _P]),
+    "vn_linear_workspace": (_I64, [_I64, _I64, _I64, _I, _I]),
+    "vn_linear_backward": (_I, [_P, _P, _P, _P, _I, _I64, _I64, _I64, _I, _P, _P, _P, _I, _P, _I64, _P]),
+    "vn_linear_backward_workspace": (_I64, [_I64, _I64, _I64, _I, _I, _I]),
+    "vn_layer_norm": (_I, [_P, _I, _P, _P, _I, _I64, _I64, _D, _P, _P, _P, _P]),
+    "vn_layer_norm_backward": (_I, [_P, _P, _I, _P, _P, _P, _I, _I64, _I64, _P, _P, _P, _P, _I64, _P]),
+    "vn_layer_norm_backward_workspace": (_I64, [_I64, _I64]),
+    "vn_adamw": (_I, [_P, _I64, _I, _I, _I, _D, _D, _D, _D, _I64, _I, _P]),
+    "vn_adamw_moments": (_I, [_P, _P, _P, _P, _I64, _P, _P, _P]),
 }
 
 _lock = threading.Lock()

@@ -122,6 +122,44 @@ vn_status check_linear(const void* x, vn_dtype x_dt, int x_shared, const void* w
   return VN_OK;
 }
 
+// The activations of the centre network's linear layer.
+bool linear_act_ok(vn_act act) { return act >= VN_ACT_NONE && act <= VN_ACT_SILU; }
+
+// rows x n elements of dt in bytes; false when the product does not fit in int64.
+bool bytes_of(int64_t rows, int64_t n, vn_dtype dt, int64_t* bytes) {
+  return mul(rows, n, bytes) && mul(*bytes, static_cast<int64_t>(dtype_size(dt)), bytes);
+}
+
+// A range of device memory that a call reads or writes.
+struct Range {
+  const void* p;
+  int64_t bytes;
+};
+// No output shares a byte with an input or with another output.
+template <int kOut, int kIn>
+bool disjoint(const Range (&outs)[kOut], const Range (&ins)[kIn]) {
+  for (int i = 0; i < kOut; ++i) {
+    for (int j = 0; j < kIn; ++j)
+      if (overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes)) return false;
+    for (int j = i + 1; j < kOut; ++j)
+      if (overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return false;
+  }
+  return true;
+}
+
+// The sizes of a linear layer: every matrix fits in 2^60 bytes, so that the workspace
+// sums of a few such matrices do not overflow.
+vn_status check_sizes(int64_t rows, int64_t in, int64_t out, vn_dtype dt) {
+  if (!dtype_ok(dt)) return VN_ERR_DTYPE;
+  if (rows < 0 || in < 0 || out < 0) return VN_ERR_SHAPE;
+  const int64_t most = int64_t{1} << 57;
+  int64_t t;
+  if (rows > most || in > most || out > most || !mul(rows, in, &t) || t > most || !mul(rows, out, &t) ||
+      t > most || !mul(out, in, &t) || t > most)
+    return VN_ERR_OVERFLOW;
+  return VN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -139,6 +177,7 @@ const char* vn_status_string(vn_status s) {
     case VN_ERR_CUDA: return "VN_ERR_CUDA: a CUDA runtime call failed";
     case VN_ERR_DEVICE: return "VN_ERR_DEVICE: this path needs a compute capability 10.x GPU";
     case VN_ERR_PATH: return "VN_ERR_PATH: the forced path cannot run these arguments";
+    case VN_ERR_WORKSPACE: return "VN_ERR_WORKSPACE: the workspace is too small";
   }
   return "unknown vn_status";
 }
@@ -460,6 +499,212 @@ vn_status vn_hash_probe(int64_t seed, uint64_t offset, int64_t n_sums, int64_t m
   if (!aligned(sums, 4)) return VN_ERR_ALIGN;
   return launched(vn::launch_hash_probe(static_cast<uint64_t>(seed), offset, n_sums, m, sums,
                                         static_cast<cudaStream_t>(stream)));
+}
+
+int64_t vn_linear_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, int al) {
+  if (check_sizes(rows, in, out, dt) != VN_OK) return -1;
+  return vn::dense_workspace(rows, in, out, dt, al != 0);
+}
+
+vn_status vn_linear(const void* x, const void* w, vn_dtype dt, const void* b, vn_dtype b_dt,
+                    const void* residual, int64_t rows, int64_t in, int64_t out, vn_act act,
+                    void* y, void* preact, void* workspace, int64_t workspace_bytes,
+                    void* stream) {
+  if (!dtype_ok(dt) || (b != nullptr && !dtype_ok(b_dt))) return VN_ERR_DTYPE;
+  if (!linear_act_ok(act)) return VN_ERR_VALUE;
+  const vn_status st = check_sizes(rows, in, out, dt);
+  if (st != VN_OK) return st;
+  if (rows == 0 || out == 0) return VN_OK;
+  if (y == nullptr || (in > 0 && (x == nullptr || w == nullptr))) return VN_ERR_NULL;
+  const size_t es = dtype_size(dt);
+  if (!aligned(x, es) || !aligned(w, es) || !aligned(y, es) || !aligned(preact, es) ||
+      !aligned(residual, es) || (b != nullptr && !aligned(b, dtype_size(b_dt))) || !aligned(workspace, 256))
+    return VN_ERR_ALIGN;
+  int64_t xb, wb, yb;
+  if (!bytes_of(rows, in, dt, &xb) || !bytes_of(out, in, dt, &wb) || !bytes_of(rows, out, dt, &yb))
+    return VN_ERR_OVERFLOW;
+  const int64_t need =
+      vn::dense_workspace(rows, in, out, dt, aligned(x, 16) && aligned(w, 16));
+  if (need > 0 && workspace == nullptr) return VN_ERR_WORKSPACE;
+  if (workspace_bytes < need) return VN_ERR_WORKSPACE;
+  const int64_t bb = b != nullptr ? out * static_cast<int64_t>(dtype_size(b_dt)) : 0;
+  const Range outs[] = {{y, yb}, {preact, yb}, {workspace, need}};
+  const Range ins[] = {{x, xb}, {w, wb}, {b, bb}, {residual, yb}};
+  if (!disjoint(outs, ins)) return VN_ERR_VALUE;
+  vn::DenseArgs a;
+  a.x = x; a.w = w; a.dt = dt; a.b = b; a.b_dt = b_dt; a.residual = residual;
+  a.rows = rows; a.in = in; a.out = out; a.act = act; a.y = y; a.preact = preact;
+  a.workspace = workspace;
+  return launched(vn::launch_dense(a, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t vn_linear_backward_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt,
+                                     vn_act act, int al) {
+  if (check_sizes(rows, in, out, dt) != VN_OK || !linear_act_ok(act)) return -1;
+  return vn::dense_backward_workspace(rows, in, out, dt, act, al != 0);
+}
+
+vn_status vn_linear_backward(const void* grad, const void* x, const void* w, const void* preact,
+                             vn_dtype dt, int64_t rows, int64_t in, int64_t out, vn_act act,
+                             void* grad_x, void* grad_w, void* grad_b, vn_dtype gb_dt,
+                             void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!dtype_ok(dt) || (grad_b != nullptr && !dtype_ok(gb_dt))) return VN_ERR_DTYPE;
+  if (!linear_act_ok(act)) return VN_ERR_VALUE;
+  const vn_status st = check_sizes(rows, in, out, dt);
+  if (st != VN_OK) return st;
+  const bool no_x = grad_x == nullptr || rows == 0 || in == 0;
+  const bool no_w = grad_w == nullptr || out == 0 || in == 0;
+  const bool no_b = grad_b == nullptr || out == 0;
+  if (no_x && no_w && no_b) return VN_OK;
+  const bool some = rows > 0 && out > 0;  // d has elements
+  if (some && (grad == nullptr || (act != VN_ACT_NONE && preact == nullptr) || (!no_x && w == nullptr) ||
+               (!no_w && x == nullptr)))
+    return VN_ERR_NULL;
+  const size_t es = dtype_size(dt);
+  if (!aligned(grad, es) || !aligned(x, es) || !aligned(w, es) || !aligned(preact, es) ||
+      !aligned(grad_x, es) || !aligned(grad_w, es) ||
+      (grad_b != nullptr && !aligned(grad_b, dtype_size(gb_dt))) || !aligned(workspace, 256))
+    return VN_ERR_ALIGN;
+  int64_t xb, wb, yb;
+  if (!bytes_of(rows, in, dt, &xb) || !bytes_of(out, in, dt, &wb) || !bytes_of(rows, out, dt, &yb))
+    return VN_ERR_OVERFLOW;
+  const int64_t need = vn::dense_backward_workspace(
+      rows, in, out, dt, act, aligned(grad, 16) && aligned(x, 16) && aligned(w, 16));
+  if (need > 0 && workspace == nullptr) return VN_ERR_WORKSPACE;
+  if (workspace_bytes < need) return VN_ERR_WORKSPACE;
+  const int64_t bb = grad_b != nullptr ? out * static_cast<int64_t>(dtype_size(gb_dt)) : 0;
+  const Range outs[] = {{grad_x, xb}, {grad_w, wb}, {grad_b, bb}, {workspace, need}};
+  const Range ins[] = {{grad, yb}, {x, xb}, {w, wb}, {act != VN_ACT_NONE ? preact : nullptr, yb}};
+  if (!disjoint(outs, ins)) return VN_ERR_VALUE;
+  vn::DenseGradArgs a;
+  a.grad = grad; a.x = x; a.w = w; a.preact = preact; a.dt = dt;
+  a.rows = rows; a.in = in; a.out = out; a.act = act;
+  a.grad_x = no_x ? nullptr : grad_x;
+  a.grad_w = no_w ? nullptr : grad_w;
+  a.grad_b = no_b ? nullptr : grad_b;
+  a.gb_dt = gb_dt; a.workspace = workspace;
+  return launched(vn::launch_dense_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+vn_status vn_layer_norm(const void* x, vn_dtype dt, const void* w, const void* b, vn_dtype w_dt,
+                        int64_t rows, int64_t n, double eps, void* y, float* mean, float* rstd,
+                        void* stream) {
+  if (!dtype_ok(dt) || ((w != nullptr || b != nullptr) && !dtype_ok(w_dt))) return VN_ERR_DTYPE;
+  float eps_f;
+  if (!float_sigma(eps, &eps_f) || eps_f < 0.f) return VN_ERR_VALUE;
+  if (rows < 0 || n < 1) return VN_ERR_SHAPE;
+  int64_t xb, wb, sb;
+  if (!bytes_of(rows, n, dt, &xb) || !bytes_of(1, n, w_dt, &wb) || !mul(rows, 4, &sb)) return VN_ERR_OVERFLOW;
+  if (rows == 0) return VN_OK;
+  if (x == nullptr || y == nullptr) return VN_ERR_NULL;
+  const size_t es = dtype_size(dt), ws = dtype_size(w_dt);
+  if (!aligned(x, es) || !aligned(y, es) || !aligned(w, ws) || !aligned(b, ws) || !aligned(mean, 4) ||
+      !aligned(rstd, 4))
+    return VN_ERR_ALIGN;
+  const Range outs[] = {{y, xb}, {mean, sb}, {rstd, sb}};
+  const Range ins[] = {{x, xb}, {w, wb}, {b, wb}};
+  if (!disjoint(outs, ins)) return VN_ERR_VALUE;
+  vn::NormArgs a;
+  a.x = x; a.dt = dt; a.w = w; a.b = b; a.w_dt = w_dt; a.rows = rows; a.n = n; a.eps = eps_f;
+  a.y = y; a.mean = mean; a.rstd = rstd;
+  return launched(vn::launch_layer_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t vn_layer_norm_backward_workspace(int64_t rows, int64_t n) {
+  int64_t bytes;
+  if (rows < 0 || n < 1 || !mul(vn::layer_norm_parts(rows), n, &bytes) || !mul(bytes, 8, &bytes)) return -1;
+  return bytes;
+}
+
+vn_status vn_layer_norm_backward(const void* grad, const void* x, vn_dtype dt, const float* mean,
+                                 const float* rstd, const void* w, vn_dtype w_dt, int64_t rows,
+                                 int64_t n, void* grad_x, void* grad_w, void* grad_b,
+                                 void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!dtype_ok(dt) || !dtype_ok(w_dt)) return VN_ERR_DTYPE;
+  if (rows < 0 || n < 1) return VN_ERR_SHAPE;
+  int64_t xb, wb, sb;
+  const int64_t need_sums = vn_layer_norm_backward_workspace(rows, n);
+  if (!bytes_of(rows, n, dt, &xb) || !bytes_of(1, n, w_dt, &wb) || !mul(rows, 4, &sb) || need_sums < 0)
+    return VN_ERR_OVERFLOW;
+  const bool sums = grad_w != nullptr || grad_b != nullptr;
+  if (rows == 0 && !sums) return VN_OK;
+  if (rows > 0 && (grad == nullptr || x == nullptr || mean == nullptr || rstd == nullptr || grad_x == nullptr))
+    return VN_ERR_NULL;
+  const size_t es = dtype_size(dt), ws = dtype_size(w_dt);
+  if (!aligned(grad, es) || !aligned(x, es) || !aligned(grad_x, es) || !aligned(w, ws) ||
+      !aligned(grad_w, ws) || !aligned(grad_b, ws) || !aligned(mean, 4) || !aligned(rstd, 4) ||
+      !aligned(workspace, 256))
+    return VN_ERR_ALIGN;
+  const int64_t need = sums ? need_sums : 0;
+  if (sums && workspace == nullptr) return VN_ERR_WORKSPACE;
+  if (workspace_bytes < need) return VN_ERR_WORKSPACE;
+  const Range outs[] = {{grad_x, xb}, {grad_w, wb}, {grad_b, wb}, {workspace, need}};
+  const Range ins[] = {{grad, xb}, {x, xb}, {mean, sb}, {rstd, sb}, {w, wb}};
+  if (!disjoint(outs, ins)) return VN_ERR_VALUE;
+  vn::NormGradArgs a;
+  a.grad = grad; a.x = x; a.dt = dt; a.mean = mean; a.rstd = rstd; a.w = w; a.w_dt = w_dt;
+  a.rows = rows; a.n = n; a.grad_x = grad_x; a.grad_w = grad_w; a.grad_b = grad_b;
+  a.part = static_cast<float*>(workspace);
+  return launched(vn::launch_layer_norm_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+vn_status vn_adamw(const vn_adamw_tensor* tensors, int64_t n_tensors, vn_dtype param_dt,
+                   vn_dtype grad_dt, int state_bits, double lr, double beta1, double beta2,
+                   double eps, int64_t step, int maximize, void* stream) {
+  if (!dtype_ok(param_dt) || !dtype_ok(grad_dt)) return VN_ERR_DTYPE;
+  if (state_bits != 8 && state_bits != 32) return VN_ERR_VALUE;
+  float f;
+  if (!float_sigma(lr, &f) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) ||
+      !float_sigma(eps, &f) || eps < 0.0 || step < 1)
+    return VN_ERR_VALUE;
+  if (n_tensors < 0) return VN_ERR_SHAPE;
+  if (n_tensors == 0) return VN_OK;
+  if (tensors == nullptr) return VN_ERR_NULL;
+  const bool eight = state_bits == 8;
+  const int64_t ps = static_cast<int64_t>(dtype_size(param_dt)), gs = static_cast<int64_t>(dtype_size(grad_dt));
+  for (int64_t i = 0; i < n_tensors; ++i) {
+    const vn_adamw_tensor& t = tensors[i];
+    if (t.n < 0) return VN_ERR_SHAPE;
+    if (!float_sigma(1.0 - lr * t.weight_decay, &f)) return VN_ERR_VALUE;
+    if (t.n > (int64_t{1} << 59)) return VN_ERR_OVERFLOW;
+    if (t.n == 0) continue;
+    if (t.param == nullptr || t.grad == nullptr || t.exp_avg == nullptr || t.exp_avg_sq == nullptr ||
+        (eight && (t.exp_avg_scale == nullptr || t.exp_avg_sq_scale == nullptr)))
+      return VN_ERR_NULL;
+    const size_t ss = eight ? 1 : 4;
+    if (!aligned(t.param, ps) || !aligned(t.grad, gs) || !aligned(t.exp_avg, ss) ||
+        !aligned(t.exp_avg_sq, ss) || (eight && (!aligned(t.exp_avg_scale, 4) || !aligned(t.exp_avg_sq_scale, 4))))
+      return VN_ERR_ALIGN;
+    const int64_t sb = t.n * static_cast<int64_t>(ss), cb = eight ? (t.n + 255) / 256 * 4 : 0;
+    const Range outs[] = {{t.param, t.n * ps}, {t.exp_avg, sb}, {t.exp_avg_sq, sb},
+                          {t.exp_avg_scale, cb}, {t.exp_avg_sq_scale, cb}};
+    const Range ins[] = {{t.grad, t.n * gs}};
+    if (!disjoint(outs, ins)) return VN_ERR_VALUE;
+  }
+  vn::AdamwArgs a;
+  a.tensors = tensors; a.count = n_tensors; a.param_dt = param_dt; a.grad_dt = grad_dt;
+  a.state_bits = state_bits; a.lr = lr; a.beta1 = beta1; a.beta2 = beta2; a.eps = eps;
+  a.step = step; a.maximize = maximize ? 1 : 0;
+  return launched(vn::launch_adamw(a, static_cast<cudaStream_t>(stream)));
+}
+
+vn_status vn_adamw_moments(const void* exp_avg, const void* exp_avg_sq, const float* exp_avg_scale,
+                           const float* exp_avg_sq_scale, int64_t n, float* m, float* v,
+                           void* stream) {
+  if (n < 0) return VN_ERR_SHAPE;
+  if (n > (int64_t{1} << 59)) return VN_ERR_OVERFLOW;
+  if (n == 0) return VN_OK;
+  if (exp_avg == nullptr || exp_avg_sq == nullptr || exp_avg_scale == nullptr || exp_avg_sq_scale == nullptr ||
+      m == nullptr || v == nullptr)
+    return VN_ERR_NULL;
+  if (!aligned(exp_avg_scale, 4) || !aligned(exp_avg_sq_scale, 4) || !aligned(m, 4) || !aligned(v, 4))
+    return VN_ERR_ALIGN;
+  const int64_t cb = (n + 255) / 256 * 4;
+  const Range outs[] = {{m, n * 4}, {v, n * 4}};
+  const Range ins[] = {{exp_avg, n}, {exp_avg_sq, n}, {exp_avg_scale, cb}, {exp_avg_sq_scale, cb}};
+  if (!disjoint(outs, ins)) return VN_ERR_VALUE;
+  return launched(vn::launch_adamw_moments(exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, n, m, v,
+                                           static_cast<cudaStream_t>(stream)));
 }
 
 vn_status vn_device_status(void* stream) {

@@ -110,6 +110,89 @@ cudaError_t launch_es_update(float* theta, const float* grad, int64_t n, float l
 cudaError_t launch_hash_probe(uint64_t seed, uint64_t offset, int64_t n_sums, int64_t m,
                               float* sums, cudaStream_t stream);
 
+// The centre network (arguments as in vn.h; sizes may be zero where it says so).
+struct DenseArgs {
+  const void* x;
+  const void* w;
+  vn_dtype dt;
+  const void* b;  // may be null
+  vn_dtype b_dt;
+  const void* residual;  // may be null
+  int64_t rows, in, out;
+  vn_act act;
+  void* y;
+  void* preact;  // may be null
+  void* workspace;
+};
+struct DenseGradArgs {
+  const void* grad;
+  const void* x;
+  const void* w;
+  const void* preact;  // null without an activation
+  vn_dtype dt;
+  int64_t rows, in, out;
+  vn_act act;
+  void* grad_x;  // may be null, and the other two
+  void* grad_w;
+  void* grad_b;
+  vn_dtype gb_dt;
+  void* workspace;
+};
+// Bytes of workspace; sizes have been checked (products of bytes fit in int64).
+int64_t dense_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, bool aligned);
+int64_t dense_backward_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, vn_act act,
+                                 bool aligned);
+cudaError_t launch_dense(const DenseArgs& a, cudaStream_t stream);
+cudaError_t launch_dense_backward(const DenseGradArgs& a, cudaStream_t stream);
+
+struct NormArgs {
+  const void* x;
+  vn_dtype dt;
+  const void* w;  // may be null, and b, mean and rstd
+  const void* b;
+  vn_dtype w_dt;
+  int64_t rows, n;
+  float eps;
+  void* y;
+  float* mean;
+  float* rstd;
+};
+struct NormGradArgs {
+  const void* grad;
+  const void* x;
+  vn_dtype dt;
+  const float* mean;
+  const float* rstd;
+  const void* w;  // may be null, and grad_w and grad_b
+  vn_dtype w_dt;
+  int64_t rows, n;
+  void* grad_x;
+  void* grad_w;
+  void* grad_b;
+  float* part;  // [layer_norm_parts(rows)][2][n]
+};
+cudaError_t launch_layer_norm(const NormArgs& a, cudaStream_t stream);
+int64_t layer_norm_parts(int64_t rows);
+cudaError_t launch_layer_norm_backward(const NormGradArgs& a, cudaStream_t stream);
+// o1[c] = sum_p part[p][c] for c < n, o2[c - n] for the columns from n on (width of them in
+// all), in fixed order, rounded to dt; o1 and o2 may be null.
+cudaError_t launch_column_sum(const float* part, int64_t parts, int64_t width, int64_t n, void* o1,
+                              void* o2, vn_dtype dt, cudaStream_t stream);
+
+struct AdamwArgs {
+  const vn_adamw_tensor* tensors;  // host
+  int64_t count;
+  vn_dtype param_dt, grad_dt;
+  int state_bits;
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  int maximize;
+};
+cudaError_t launch_adamw(const AdamwArgs& a, cudaStream_t stream);
+cudaError_t launch_adamw_moments(const void* exp_avg, const void* exp_avg_sq, const float* exp_avg_scale,
+                                 const float* exp_avg_sq_scale, int64_t n, float* m, float* v,
+                                 cudaStream_t stream);
+
 // Reads and clears the device status word of the bounded-wait kernels (0 = fine).
 cudaError_t take_device_status(unsigned int* status, cudaStream_t stream);
 

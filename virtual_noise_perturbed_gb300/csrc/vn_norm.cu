@@ -1,0 +1,531 @@
+// vn_norm.cu -- layer norm and its gradients.
+//
+//   mean = sum x / n, rstd = (sum (x - mean)^2 / n + eps)^-1/2, y = (x - mean) rstd w + b
+//   h = (x - mean) rstd, t = g w:  dx = rstd (t - mean(t) - h mean(t h)),
+//   dw = sum_rows g h, db = sum_rows g
+//
+// Forward: a row lives in the registers of T threads (T = 32, 128 or 512 by its length),
+// so it is read from memory once although the variance is taken from the centred
+// values (a second pass over registers, not the cancelling sum of squares).
+//
+// Backward: the two row means come from one reduction of two numbers. The sums over rows
+// stay in registers: a group of T threads walks over rows of its own (every G-th), each
+// thread on the same columns in each, and its column sums leave once at the end, as one
+// partial row per CTA; a second small kernel adds the partial rows in order. No atomics, so
+// the sums do not depend on the order in which CTAs run.
+//
+// Rows beyond what registers hold take the looping kernels at the end of this file.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "vn_internal.h"
+
+namespace vn {
+namespace {
+
+__device__ __forceinline__ float value(float x) { return x; }
+__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T narrow(float x);
+template <>
+__device__ __forceinline__ float narrow<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// V consecutive elements, as they are in memory: 16 bytes (V > 1) or one element.
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Pack {
+  T e[V];
+};
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_pack(const T* p) {
+  Pack<T, V> r;
+  if constexpr (V > 1) {
+    static_assert(sizeof(T) * V == 16, "16-byte packs");
+    *reinterpret_cast<uint4*>(&r) = __ldcs(reinterpret_cast<const uint4*>(p));
+  } else {
+    r.e[0] = p[0];
+  }
+  return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_pack(T* p, const float (&v)[V]) {
+  if constexpr (V > 1) {
+    Pack<T, V> r;
+#pragma unroll
+    for (int q = 0; q < V; ++q) r.e[q] = narrow<T>(v[q]);
+    __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&r));
+  } else {
+    p[0] = narrow<T>(v[0]);
+  }
+}
+// V consecutive parameters (fp32 or bf16, 16-byte aligned at multiples of V when V > 1).
+template <int V>
+__device__ __forceinline__ void load_param(const void* w, int bf16, int64_t i, float absent, float (&v)[V]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int q = 0; q < V; ++q) v[q] = absent;
+  } else if (bf16) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(w) + i;
+    if constexpr (V == 8) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+      const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[2 * q] = __uint_as_float(u[q] << 16);
+        v[2 * q + 1] = __uint_as_float(u[q] & 0xFFFF0000u);
+      }
+    } else if constexpr (V == 4) {
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
+      v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xFFFF0000u);
+      v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xFFFF0000u);
+    } else {
+      v[0] = __bfloat162float(p[0]);
+    }
+  } else {
+    const float* p = static_cast<const float*>(w) + i;
+    if constexpr (V > 1) {
+#pragma unroll
+      for (int q = 0; q < V; q += 4) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p + q));
+        v[q] = a.x; v[q + 1] = a.y; v[q + 2] = a.z; v[q + 3] = a.w;
+      }
+    } else {
+      v[0] = __ldg(p);
+    }
+  }
+}
+
+// Sums of N numbers over the T threads of a row (a warp, or the whole CTA), the same
+// in every thread. `scratch`: N * 32 floats, used by every other call (`turn`).
+template <int T, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float* scratch, int& turn) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+  if constexpr (T > 32) {
+    constexpr int kW = T / 32;
+    float* s = scratch + (turn & 1) * (N * 32);
+    ++turn;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0)
+#pragma unroll
+      for (int k = 0; k < N; ++k) s[k * 32 + warp] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      v[k] = lane < kW ? s[k * 32 + lane] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+    }
+  }
+}
+
+struct NormArgsK {
+  const void* x;
+  const void* w;
+  const void* b;
+  void* y;
+  float* mean;
+  float* rstd;
+  int64_t rows, n;
+  float eps, inv_n;
+  int w_bf16;
+};
+
+constexpr int cta_threads(int t) { return t < 128 ? 128 : t; }
+
+template <typename X, int T, int V, int NV>
+__global__ void __launch_bounds__(cta_threads(T)) norm_kernel(const NormArgsK a) {
+  constexpr int kRows = cta_threads(T) / T;
+  __shared__ float scratch[T > 32 ? 64 : 1];
+  int turn = 0;
+  const int t = threadIdx.x % T;
+  const int n = static_cast<int>(a.n);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T;
+  if (T == 32 && row >= a.rows) return;
+  const X* x = static_cast<const X*>(a.x) + row * a.n;
+  Pack<X, V> v[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = (j * T + t) * V;
+    if (i < n) v[j] = load_pack<X, V>(x + i);
+  }
+  float s[1] = {0.f};
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if ((j * T + t) * V < n)
+#pragma unroll
+      for (int q = 0; q < V; ++q) s[0] += value(v[j].e[q]);
+  row_sum<T, 1>(s, scratch, turn);
+  const float mean = s[0] * a.inv_n;
+  s[0] = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if ((j * T + t) * V < n)
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        const float c = value(v[j].e[q]) - mean;
+        s[0] = fmaf(c, c, s[0]);
+      }
+  row_sum<T, 1>(s, scratch, turn);
+  const float rstd = 1.f / sqrtf(s[0] * a.inv_n + a.eps);
+  X* y = static_cast<X*>(a.y) + row * a.n;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = (j * T + t) * V;
+    if (i < n) {
+      float w[V], b[V], o[V];
+      load_param<V>(a.w, a.w_bf16, i, 1.f, w);
+      load_param<V>(a.b, a.w_bf16, i, 0.f, b);
+#pragma unroll
+      for (int q = 0; q < V; ++q) o[q] = fmaf((value(v[j].e[q]) - mean) * rstd, w[q], b[q]);
+      store_pack<X, V>(y + i, o);
+    }
+  }
+  if (t == 0) {
+    if (a.mean != nullptr) a.mean[row] = mean;
+    if (a.rstd != nullptr) a.rstd[row] = rstd;
+  }
+}
+
+// Rows longer than the registers hold: three passes over the row (the second and third
+// mostly from L2).
+template <typename X>
+__global__ void __launch_bounds__(512) norm_long_kernel(const NormArgsK a) {
+  __shared__ float scratch[64];
+  int turn = 0;
+  const int64_t row = blockIdx.x;
+  const X* x = static_cast<const X*>(a.x) + row * a.n;
+  X* y = static_cast<X*>(a.y) + row * a.n;
+  float s[1] = {0.f};
+  for (int64_t i = threadIdx.x; i < a.n; i += 512) s[0] += value(x[i]);
+  row_sum<512, 1>(s, scratch, turn);
+  const float mean = s[0] * a.inv_n;
+  s[0] = 0.f;
+  for (int64_t i = threadIdx.x; i < a.n; i += 512) {
+    const float c = value(x[i]) - mean;
+    s[0] = fmaf(c, c, s[0]);
+  }
+  row_sum<512, 1>(s, scratch, turn);
+  const float rstd = 1.f / sqrtf(s[0] * a.inv_n + a.eps);
+  for (int64_t i = threadIdx.x; i < a.n; i += 512) {
+    float w[1], b[1];
+    load_param<1>(a.w, a.w_bf16, i, 1.f, w);
+    load_param<1>(a.b, a.w_bf16, i, 0.f, b);
+    y[i] = narrow<X>(fmaf((value(x[i]) - mean) * rstd, w[0], b[0]));
+  }
+  if (threadIdx.x == 0) {
+    if (a.mean != nullptr) a.mean[row] = mean;
+    if (a.rstd != nullptr) a.rstd[row] = rstd;
+  }
+}
+
+// ---------------------------------------------------------------- gradients
+struct NormGradK {
+  const void* g;
+  const void* x;
+  const float* mean;
+  const float* rstd;
+  const void* w;
+  void* dx;
+  float* part;  // [CTAs][2][n] column sums, or NULL
+  int64_t rows, n;
+  float inv_n;
+  int w_bf16;
+};
+
+template <typename X, int T, int V, int NV>
+__global__ void __launch_bounds__(cta_threads(T)) norm_grad_kernel(const NormGradK a) {
+  constexpr int kRows = cta_threads(T) / T;
+  __shared__ float scratch[T > 32 ? 128 : 1];
+  extern __shared__ float columns[];  // T == 32: kRows x 2 x n column sums to be added
+  int turn = 0;
+  const int t = threadIdx.x % T;
+  const int group = threadIdx.x / T;
+  const int n = static_cast<int>(a.n);
+  float w[NV][V], dw[NV][V], db[NV][V];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = (j * T + t) * V;
+#pragma unroll
+    for (int q = 0; q < V; ++q) w[j][q] = dw[j][q] = db[j][q] = 0.f;
+    if (i < n) load_param<V>(a.w, a.w_bf16, i, 1.f, w[j]);
+  }
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group; row < a.rows;
+       row += static_cast<int64_t>(gridDim.x) * kRows) {
+    const X* g = static_cast<const X*>(a.g) + row * a.n;
+    const X* x = static_cast<const X*>(a.x) + row * a.n;
+    Pack<X, V> gv[NV], xv[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = (j * T + t) * V;
+      if (i < n) {
+        gv[j] = load_pack<X, V>(g + i);
+        xv[j] = load_pack<X, V>(x + i);
+      }
+    }
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if ((j * T + t) * V < n)
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+          const float d = value(gv[j].e[q]), h = (value(xv[j].e[q]) - mean) * rstd;
+          const float u = d * w[j][q];
+          s[0] += u;
+          s[1] = fmaf(u, h, s[1]);
+          dw[j][q] = fmaf(d, h, dw[j][q]);
+          db[j][q] += d;
+        }
+    row_sum<T, 2>(s, scratch, turn);
+    const float m1 = s[0] * a.inv_n, m2 = s[1] * a.inv_n;
+    X* dx = static_cast<X*>(a.dx) + row * a.n;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = (j * T + t) * V;
+      if (i < n) {
+        float o[V];
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+          const float h = (value(xv[j].e[q]) - mean) * rstd;
+          o[q] = rstd * (fmaf(value(gv[j].e[q]), w[j][q], -m1) - h * m2);
+        }
+        store_pack<X, V>(dx + i, o);
+      }
+    }
+  }
+  if (a.part == nullptr) return;
+  float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.n;
+  if constexpr (T == 32) {  // the CTA's warps hold sums of the same columns
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        const int i = (j * T + t) * V + q;
+        if (i < n) {
+          columns[(group * 2) * n + i] = dw[j][q];
+          columns[(group * 2 + 1) * n + i] = db[j][q];
+        }
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * n; i += cta_threads(T)) {
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) s += columns[k * 2 * n + i];
+      out[i] = s;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        const int i = (j * T + t) * V + q;
+        if (i < n) {
+          out[i] = dw[j][q];
+          out[a.n + i] = db[j][q];
+        }
+      }
+  }
+}
+
+// Long rows: grad_x in two passes over the row ...
+template <typename X>
+__global__ void __launch_bounds__(512) norm_grad_long_kernel(const NormGradK a) {
+  __shared__ float scratch[128];
+  int turn = 0;
+  const int64_t row = blockIdx.x;
+  const X* g = static_cast<const X*>(a.g) + row * a.n;
+  const X* x = static_cast<const X*>(a.x) + row * a.n;
+  X* dx = static_cast<X*>(a.dx) + row * a.n;
+  const float mean = a.mean[row], rstd = a.rstd[row];
+  float s[2] = {0.f, 0.f};
+  for (int64_t i = threadIdx.x; i < a.n; i += 512) {
+    float w[1];
+    load_param<1>(a.w, a.w_bf16, i, 1.f, w);
+    const float u = value(g[i]) * w[0];
+    s[0] += u;
+    s[1] = fmaf(u, (value(x[i]) - mean) * rstd, s[1]);
+  }
+  row_sum<512, 2>(s, scratch, turn);
+  const float m1 = s[0] * a.inv_n, m2 = s[1] * a.inv_n;
+  for (int64_t i = threadIdx.x; i < a.n; i += 512) {
+    float w[1];
+    load_param<1>(a.w, a.w_bf16, i, 1.f, w);
+    const float h = (value(x[i]) - mean) * rstd;
+    dx[i] = narrow<X>(rstd * (fmaf(value(g[i]), w[0], -m1) - h * m2));
+  }
+}
+// ... and the column sums from a pass of their own: CTA (c, p) adds its 256 columns over
+// every gridDim.y-th row.
+template <typename X>
+__global__ void __launch_bounds__(256) norm_columns_kernel(const NormGradK a) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= a.n) return;
+  float dw = 0.f, db = 0.f;
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    const float d = value(static_cast<const X*>(a.g)[row * a.n + i]);
+    const float h = (value(static_cast<const X*>(a.x)[row * a.n + i]) - a.mean[row]) * a.rstd[row];
+    dw = fmaf(d, h, dw);
+    db += d;
+  }
+  float* out = a.part + static_cast<int64_t>(blockIdx.y) * 2 * a.n;
+  out[i] = dw;
+  out[a.n + i] = db;
+}
+
+// out[c] = sum over parts, in order, of part[p][c], c < n; a second output takes columns
+// n .. 2n-1. 32 columns a CTA; warp k adds every 8th part from k, then the warps' sums.
+__global__ void __launch_bounds__(256)
+column_sum_kernel(const float* __restrict__ part, int64_t parts, int64_t width, int64_t n, void* o1, void* o2,
+                  int bf16) {
+  __shared__ float s[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float v = 0.f;
+  if (c < width) {
+#pragma unroll 4
+    for (int64_t p = warp; p < parts; p += 8) v += part[p * width + c];
+  }
+  s[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && c < width) {
+    v = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v += s[k][lane];
+    void* o = c < n ? o1 : o2;
+    const int64_t i = c < n ? c : c - n;
+    if (o != nullptr) {
+      if (bf16) static_cast<__nv_bfloat16*>(o)[i] = __float2bfloat16_rn(v);
+      else static_cast<float*>(o)[i] = v;
+    }
+  }
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+template <typename X, int T, int V, int NV>
+cudaError_t run_norm(const NormArgsK& a, cudaStream_t stream) {
+  constexpr int kRows = cta_threads(T) / T;
+  const int64_t grid = (a.rows + kRows - 1) / kRows;
+  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  norm_kernel<X, T, V, NV><<<static_cast<unsigned>(grid), cta_threads(T), 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+// The threads of a row by its number of packs: a warp while its 8 packs a lane suffice
+// (no barrier), then 128 and 512 threads.
+template <typename X, int V>
+cudaError_t norm_by_length(const NormArgsK& a, cudaStream_t stream) {
+  const int64_t packs = (a.n + V - 1) / V;
+  if (packs <= 32) return run_norm<X, 32, V, 1>(a, stream);
+  if (packs <= 64) return run_norm<X, 32, V, 2>(a, stream);
+  if (packs <= 128) return run_norm<X, 32, V, 4>(a, stream);
+  if (packs <= 256) return run_norm<X, 32, V, 8>(a, stream);
+  if (packs <= 512) return run_norm<X, 128, V, 4>(a, stream);
+  if (packs <= 1024) return run_norm<X, 128, V, 8>(a, stream);
+  if (packs <= 2048) return run_norm<X, 512, V, 4>(a, stream);
+  if (packs <= 4096) return run_norm<X, 512, V, 8>(a, stream);
+  if (a.rows > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  norm_long_kernel<X><<<static_cast<unsigned>(a.rows), 512, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename X>
+cudaError_t norm_typed(const NormArgsK& a, cudaStream_t stream) {
+  constexpr int V = 16 / sizeof(X);
+  const bool vec = a.n % V == 0 && aligned16(a.x) && aligned16(a.y) && aligned16(a.w) && aligned16(a.b);
+  return vec ? norm_by_length<X, V>(a, stream) : norm_by_length<X, 1>(a, stream);
+}
+
+// Partial rows of the column sums: at most this many CTAs walk the rows.
+constexpr int64_t kMaxParts = 152 * 4;
+
+template <typename X, int T, int V, int NV>
+cudaError_t run_norm_grad(const NormGradK& a, int64_t parts, cudaStream_t stream) {
+  const size_t smem = T == 32 ? sizeof(float) * 2 * (cta_threads(T) / T) * a.n : 0;
+  norm_grad_kernel<X, T, V, NV><<<static_cast<unsigned>(parts), cta_threads(T), smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename X, int V>
+cudaError_t norm_grad_by_length(const NormGradK& a, int64_t* parts, cudaStream_t stream) {
+  // Up to 16 elements a thread: three fp32 registers for each (weight and both sums) and the row itself.
+  constexpr int kNv = 16 / V;
+  auto ctas = [&](int t) {
+    const int64_t rows = cta_threads(t) / t;
+    return std::max<int64_t>(1, std::min<int64_t>(kMaxParts, (a.rows + rows - 1) / rows));
+  };
+  if (a.n <= 32 * 16) {
+    *parts = ctas(32);
+    if constexpr (V > 1) {
+      if (a.n <= 32 * V) return run_norm_grad<X, 32, V, 1>(a, *parts, stream);
+      return run_norm_grad<X, 32, V, kNv>(a, *parts, stream);
+    } else {
+      if (a.n <= 32 * 4) return run_norm_grad<X, 32, V, 4>(a, *parts, stream);
+      return run_norm_grad<X, 32, V, kNv>(a, *parts, stream);
+    }
+  }
+  if (a.n <= 128 * 16) { *parts = ctas(128); return run_norm_grad<X, 128, V, kNv>(a, *parts, stream); }
+  if (a.n <= 256 * 16) { *parts = ctas(256); return run_norm_grad<X, 256, V, kNv>(a, *parts, stream); }
+  if (a.n <= 512 * 16) { *parts = ctas(512); return run_norm_grad<X, 512, V, kNv>(a, *parts, stream); }
+  if (a.rows > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  norm_grad_long_kernel<X><<<static_cast<unsigned>(a.rows), 512, 0, stream>>>(a);
+  cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess || a.part == nullptr) return err;
+  const int64_t tiles = (a.n + 255) / 256;
+  *parts = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(a.rows, kMaxParts), 4 * 152 / tiles));
+  norm_columns_kernel<X><<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(*parts)), 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename X>
+cudaError_t norm_grad_typed(const NormGradK& a, int64_t* parts, cudaStream_t stream) {
+  constexpr int V = 16 / sizeof(X);
+  const bool vec = a.n % V == 0 && aligned16(a.g) && aligned16(a.x) && aligned16(a.dx) && aligned16(a.w);
+  return vec ? norm_grad_by_length<X, V>(a, parts, stream) : norm_grad_by_length<X, 1>(a, parts, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_layer_norm(const NormArgs& a, cudaStream_t stream) {
+  NormArgsK k;
+  k.x = a.x; k.w = a.w; k.b = a.b; k.y = a.y; k.mean = a.mean; k.rstd = a.rstd;
+  k.rows = a.rows; k.n = a.n; k.eps = a.eps;
+  k.inv_n = static_cast<float>(1.0 / static_cast<double>(a.n));
+  k.w_bf16 = a.w_dt == VN_BF16;
+  return a.dt == VN_BF16 ? norm_typed<__nv_bfloat16>(k, stream) : norm_typed<float>(k, stream);
+}
+
+int64_t layer_norm_parts(int64_t rows) { return std::max<int64_t>(1, std::min(rows, kMaxParts)); }
+
+cudaError_t launch_column_sum(const float* part, int64_t parts, int64_t width, int64_t n, void* o1, void* o2,
+                                 vn_dtype dt, cudaStream_t stream) {
+  const int64_t grid = (width + 31) / 32;
+  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  column_sum_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(part, parts, width, n, o1, o2, dt == VN_BF16);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_layer_norm_backward(const NormGradArgs& a, cudaStream_t stream) {
+  NormGradK k;
+  k.g = a.grad; k.x = a.x; k.mean = a.mean; k.rstd = a.rstd; k.w = a.w; k.dx = a.grad_x;
+  k.part = (a.grad_w != nullptr || a.grad_b != nullptr) ? a.part : nullptr;
+  k.rows = a.rows; k.n = a.n;
+  k.inv_n = static_cast<float>(1.0 / static_cast<double>(a.n));
+  k.w_bf16 = a.w_dt == VN_BF16;
+  int64_t parts = 0;
+  if (a.rows > 0) {
+    const cudaError_t err = a.dt == VN_BF16 ? norm_grad_typed<__nv_bfloat16>(k, &parts, stream)
+                                            : norm_grad_typed<float>(k, &parts, stream);
+    if (err != cudaSuccess) return err;
+  }
+  if (k.part == nullptr) return cudaSuccess;
+  return launch_column_sum(k.part, parts, 2 * a.n, a.n, a.grad_w, a.grad_b, a.w_dt, stream);
+}
+
+}  // namespace vn
