@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "vn.h"
+#include "vn_dense.h"
 #include "vn_internal.h"
 
 namespace vn {
@@ -713,7 +714,10 @@ vn_status vn_device_status(void* stream) {
   unsigned int status = 0;
   err = vn::take_device_status(&status, static_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) return cuda_failure(err);
-  return status ? VN_ERR_TIMEOUT : VN_OK;
+  unsigned int dense = 0;
+  err = vn::take_dense_status(&dense, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_failure(err);
+  return (status | dense) ? VN_ERR_TIMEOUT : VN_OK;
 }
 
 }  // extern "C"

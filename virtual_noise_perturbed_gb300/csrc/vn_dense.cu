@@ -15,6 +15,7 @@
 #include <algorithm>
 
 #include "vn_act.cuh"
+#include "vn_dense.h"
 #include "vn_internal.h"
 
 namespace vn {
@@ -28,6 +29,8 @@ template <>
 __device__ __forceinline__ float narrow<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 constexpr int kTile = 64, kStep = 16, kThreads = 256;
 
@@ -100,32 +103,144 @@ __global__ void __launch_bounds__(kThreads) product_kernel(const Product d) {
     }
 }
 
-// d = g act'(z) (rounded to T), and column sums of the unrounded d over every
-// gridDim.y-th group of 8 rows.
-template <typename T>
-__global__ void __launch_bounds__(256)
-delta_kernel(const T* __restrict__ g, const T* __restrict__ z, int act, int64_t rows, int64_t n,
-             T* __restrict__ d, float* __restrict__ part) {
-  __shared__ float s[8][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  float sum = 0.f;
-  if (c < n) {
-    for (int64_t r = static_cast<int64_t>(blockIdx.y) * 8 + warp; r < rows; r += static_cast<int64_t>(gridDim.y) * 8) {
-      float v = value(g[r * n + c]);
-      if (act != VN_ACT_NONE) v *= slope(act, value(z[r * n + c]));
-      if (d != nullptr) d[r * n + c] = narrow<T>(v);
-      sum += v;
+// The three bf16 terms of an fp32 value, exactly: its top 8 significant bits, the next 8, the
+// last 8. Terms of an infinity or NaN are the value itself and zeros.
+__device__ __forceinline__ void split3(float v, uint32_t (&t)[3]) {
+  const uint32_t u = __float_as_uint(v);
+  t[0] = u >> 16;
+  if ((u & 0x7F800000u) == 0x7F800000u) {
+    if ((u & 0x007FFFFFu) != 0) t[0] |= 0x40u;  // a NaN stays one
+    t[1] = t[2] = 0;
+    return;
+  }
+  const float r1 = v - __uint_as_float(u & 0xFFFF0000u);
+  t[1] = __float_as_uint(r1) >> 16;
+  const float r2 = r1 - __uint_as_float(__float_as_uint(r1) & 0xFFFF0000u);
+  t[2] = __float_as_uint(r2) >> 16;
+}
+
+// Eight values to row-major memory. kPlanes 1: in T, 16-byte stores where they fit; 3: bf16
+// planes, `plane` elements apart, the whole group written (pitch is a multiple of 8).
+template <typename T, int kPlanes>
+__device__ __forceinline__ void store8(void* dst, int64_t at, int64_t plane, const float (&v)[8], int count, bool vec) {
+  if constexpr (kPlanes == 3) {
+    uint32_t w[3][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t a[3], b[3];
+      split3(v[2 * q], a);
+      split3(v[2 * q + 1], b);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) w[k][q] = a[k] | (b[k] << 16);
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dst) + k * plane + at) =
+          make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+  } else {
+    T* d = static_cast<T*>(dst) + at;
+    if (vec) {
+      if constexpr (sizeof(T) == 2) {
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
+          w[q] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        *reinterpret_cast<float4*>(d) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(d + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < count) d[q] = narrow<T>(v[q]);
     }
   }
-  s[warp][lane] = sum;
-  __syncthreads();
-  if (part != nullptr && warp == 0 && c < n) {
-    sum = 0.f;
+}
+// Eight values of a row (zeros beyond `count`); vec: 16-byte loads, count >= 8.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int count, bool vec, float (&v)[8]) {
+  if (vec) {
+    if constexpr (sizeof(T) == 2) {
+      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum += s[k][lane];
-    part[static_cast<int64_t>(blockIdx.y) * n + c] = sum;
+      for (int q = 0; q < 4; ++q) {
+        v[2 * q] = __uint_as_float(w[q] << 16);
+        v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+      }
+    } else {
+      const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = q < count ? value(p[q]) : 0.f;
   }
+}
+
+// A matrix as the tensor cores take it: rows padded to `pitch`, fp32 split into planes.
+template <typename T>
+__global__ void __launch_bounds__(256)
+convert_kernel(const T* __restrict__ src, int64_t rows, int64_t cols, void* __restrict__ dst, int64_t pitch,
+               int64_t plane, int vec) {
+  const int64_t groups = pitch / 8;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= rows * groups) return;
+  const int64_t r = i / groups, c = (i - r * groups) * 8;
+  float v[8];
+  load8(src + r * cols + c, static_cast<int>(min(static_cast<int64_t>(8), cols - c)), vec != 0, v);
+  if constexpr (sizeof(T) == 2) store8<T, 1>(dst, r * pitch + c, 0, v, 8, true);
+  else store8<T, 3>(dst, r * pitch + c, plane, v, 8, true);
+}
+
+// d = g act'(z), stored as the products take it, and column sums of the unrounded d: a
+// CTA's 8 warps walk over every 8 gridDim.y-th row of 256 columns.
+struct Delta {
+  const void* g;
+  const void* z;
+  void* d;      // NULL: only the sums
+  float* part;  // NULL: only d
+  int64_t rows, n, pitch, plane;
+  int act;
+  int vec_in, vec_out;
+};
+template <typename T, int kPlanes>
+__global__ void __launch_bounds__(256) delta_kernel(const Delta a) {
+  __shared__ float s[8][256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + lane * 8;
+  const int count = static_cast<int>(min(static_cast<int64_t>(8), a.n - c));
+  const T* g = static_cast<const T*>(a.g);
+  const T* z = static_cast<const T*>(a.z);
+  float sum[8] = {};
+  if (count > 0) {
+    for (int64_t r = static_cast<int64_t>(blockIdx.y) * 8 + warp; r < a.rows; r += static_cast<int64_t>(gridDim.y) * 8) {
+      float v[8];
+      load8(g + r * a.n + c, count, a.vec_in != 0, v);
+      if (a.act != VN_ACT_NONE) {
+        float u[8];
+        load8(z + r * a.n + c, count, a.vec_in != 0, u);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = q < count ? v[q] * slope(a.act, u[q]) : 0.f;
+      }
+      if (a.d != nullptr) store8<T, kPlanes>(a.d, r * a.pitch + c, a.plane, v, count, a.vec_out != 0);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) sum[q] += v[q];
+    }
+  }
+  if (a.part == nullptr) return;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) s[warp][q * 32 + lane] = sum[q];
+  __syncthreads();
+  float t = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) t += s[k][threadIdx.x];
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + (threadIdx.x & 31) * 8 + (threadIdx.x >> 5);
+  if (col < a.n) a.part[static_cast<int64_t>(blockIdx.y) * a.n + col] = t;
 }
 
 template <typename T>
@@ -144,24 +259,84 @@ cudaError_t product(const Product& d, vn_dtype dt, cudaStream_t stream) {
 
 constexpr int64_t kAlign = 256;
 int64_t rounded(int64_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
+int64_t pitch_of(int64_t cols) { return (cols + 7) / 8 * 8; }
+
+// Bytes of a matrix as the tensor cores take it.
+int64_t operand_bytes(int64_t rows, int64_t cols, vn_dtype dt) {
+  return rounded(rows * pitch_of(cols) * (dt == VN_BF16 ? 2 : 6));
+}
+// Whether a matrix can be taken as it is.
+bool as_is(vn_dtype dt, int64_t cols, bool aligned) { return dt == VN_BF16 && cols % 8 == 0 && aligned; }
+
+// Whether a layer's products go to the tensor cores: from the size on at which their launch
+// and, in fp32, the splitting pay.
+bool uses_tc(int64_t rows, int64_t in, int64_t out, vn_dtype dt) {
+  const int64_t most = (int64_t{1} << 31) - 512;
+  if (rows < 1 || in < 1 || out < 1 || rows > most || in > most || out > most) return false;
+  const double macs = static_cast<double>(rows) * static_cast<double>(in) * static_cast<double>(out);
+  return macs >= (dt == VN_BF16 ? 65536.0 : 67108864.0);
+}
 
 // Row groups that the column sums are split over.
-int64_t delta_parts(int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>(64, (rows + 63) / 64)); }
+int64_t delta_parts(int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>(64, (rows + 31) / 32)); }
+
+TcOperand operand(const void* p, int64_t rows, int64_t cols, bool mn) {
+  return TcOperand{p, rows, cols, cols, rows * cols, 1, mn};
+}
+// The matrix as the tensor cores take it: itself, or a converted copy at *work (advanced).
+cudaError_t prepare(const void* p, vn_dtype dt, int64_t rows, int64_t cols, bool aligned, bool mn, uint8_t** work,
+                    TcOperand* o, cudaStream_t stream) {
+  *o = operand(p, rows, cols, mn);
+  if (as_is(dt, cols, aligned)) return cudaSuccess;
+  o->p = *work;
+  o->pitch = pitch_of(cols);
+  o->plane = rows * o->pitch;
+  o->planes = dt == VN_BF16 ? 1 : 3;
+  *work += operand_bytes(rows, cols, dt);
+  const int64_t grid = (rows * (o->pitch / 8) + 255) / 256;
+  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  const int vec = cols % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+  void* dst = const_cast<void*>(o->p);
+  if (dt == VN_BF16)
+    convert_kernel<__nv_bfloat16><<<static_cast<unsigned>(grid), 256, 0, stream>>>(
+        static_cast<const __nv_bfloat16*>(p), rows, cols, dst, o->pitch, o->plane, vec);
+  else
+    convert_kernel<float><<<static_cast<unsigned>(grid), 256, 0, stream>>>(static_cast<const float*>(p), rows, cols,
+                                                                          dst, o->pitch, o->plane, vec);
+  return cudaGetLastError();
+}
 
 }  // namespace
 
 int64_t dense_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, bool aligned) {
-  (void)rows; (void)in; (void)out; (void)dt; (void)aligned;
-  return 0;
+  if (!uses_tc(rows, in, out, dt) || as_is(dt, in, aligned)) return 0;
+  return operand_bytes(rows, in, dt) + operand_bytes(out, in, dt);
 }
 
 int64_t dense_backward_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, vn_act act, bool aligned) {
-  (void)in; (void)aligned;
-  const int64_t size = dt == VN_BF16 ? 2 : 4;
-  return (act != VN_ACT_NONE ? rounded(rows * out * size) : 0) + rounded(delta_parts(rows) * out * 4);
+  const int64_t sums = rounded(delta_parts(rows) * out * 4);
+  if (!uses_tc(rows, in, out, dt))
+    return sums + (act != VN_ACT_NONE ? rounded(rows * out * (dt == VN_BF16 ? 2 : 4)) : 0);
+  int64_t bytes = sums;
+  if (act != VN_ACT_NONE || !as_is(dt, out, aligned)) bytes += operand_bytes(rows, out, dt);
+  if (!as_is(dt, in, aligned)) bytes += operand_bytes(rows, in, dt) + operand_bytes(out, in, dt);
+  return bytes;
 }
 
 cudaError_t launch_dense(const DenseArgs& a, cudaStream_t stream) {
+  if (uses_tc(a.rows, a.in, a.out, a.dt)) {
+    const bool al = aligned16(a.x) && aligned16(a.w);
+    uint8_t* work = static_cast<uint8_t*>(a.workspace);
+    TcProduct d = {};
+    cudaError_t err = prepare(a.w, a.dt, a.out, a.in, al, false, &work, &d.a, stream);
+    if (err != cudaSuccess) return err;
+    if ((err = prepare(a.x, a.dt, a.rows, a.in, al, false, &work, &d.b, stream)) != cudaSuccess) return err;
+    d.np = a.out; d.nq = a.rows; d.nk = a.in;
+    d.dt = a.dt;
+    d.bias = a.b; d.bias_bf16 = a.b_dt == VN_BF16; d.act = a.act;
+    d.residual = a.residual; d.out = a.y; d.preact = a.preact;
+    return launch_tc_product(d, stream);
+  }
   Product d = {};
   d.a = a.w; d.ap = a.in; d.ak = 1;
   d.b = a.x; d.bq = a.in; d.bk = 1;
@@ -172,37 +347,66 @@ cudaError_t launch_dense(const DenseArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_dense_backward(const DenseGradArgs& a, cudaStream_t stream) {
-  const int64_t size = a.dt == VN_BF16 ? 2 : 4;
-  uint8_t* work = static_cast<uint8_t*>(a.workspace);
-  void* delta = nullptr;
-  if (a.act != VN_ACT_NONE) {
-    delta = work;
-    work += rounded(a.rows * a.out * size);
-  }
-  float* part = a.grad_b != nullptr ? reinterpret_cast<float*>(work) : nullptr;
+  const bool tc = uses_tc(a.rows, a.in, a.out, a.dt);
+  const bool al = aligned16(a.grad) && aligned16(a.x) && aligned16(a.w);
   const bool products = a.grad_x != nullptr || a.grad_w != nullptr;
-  if (!products) delta = nullptr;
+  const bool keep = products && (a.act != VN_ACT_NONE || (tc && !as_is(a.dt, a.out, al)));  // d has to be stored
+  uint8_t* work = static_cast<uint8_t*>(a.workspace);
   cudaError_t err = cudaSuccess;
   const int64_t parts = a.rows > 0 ? delta_parts(a.rows) : 0;
-  if (a.rows > 0 && a.out > 0 && (delta != nullptr || part != nullptr)) {
-    const int64_t tiles = (a.out + 31) / 32;
+  float* part = reinterpret_cast<float*>(work);
+  work += rounded(delta_parts(a.rows) * a.out * 4);
+  TcOperand delta = operand(a.grad, a.rows, a.out, false);
+  if (keep) {
+    delta.p = work;
+    if (tc) {
+      delta.pitch = pitch_of(a.out);
+      delta.plane = a.rows * delta.pitch;
+      delta.planes = a.dt == VN_BF16 ? 1 : 3;
+      work += operand_bytes(a.rows, a.out, a.dt);
+    }
+  }
+  if (a.rows > 0 && a.out > 0 && (keep || a.grad_b != nullptr)) {
+    Delta k = {};
+    k.g = a.grad; k.z = a.preact;
+    k.d = keep ? const_cast<void*>(delta.p) : nullptr;
+    k.part = a.grad_b != nullptr ? part : nullptr;
+    k.rows = a.rows; k.n = a.out; k.pitch = delta.pitch; k.plane = delta.plane;
+    k.act = a.act;
+    k.vec_in = a.out % 8 == 0 && aligned16(a.grad) && (a.act == VN_ACT_NONE || aligned16(a.preact));
+    k.vec_out = delta.pitch % 8 == 0;
+    const int64_t tiles = (a.out + 255) / 256;
     if (tiles > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(parts));
-    if (a.dt == VN_BF16)
-      delta_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(
-          static_cast<const __nv_bfloat16*>(a.grad), static_cast<const __nv_bfloat16*>(a.preact), a.act, a.rows,
-          a.out, static_cast<__nv_bfloat16*>(delta), part);
-    else
-      delta_kernel<float><<<grid, 256, 0, stream>>>(static_cast<const float*>(a.grad),
-                                                    static_cast<const float*>(a.preact), a.act, a.rows, a.out,
-                                                    static_cast<float*>(delta), part);
+    if (a.dt == VN_BF16) delta_kernel<__nv_bfloat16, 1><<<grid, 256, 0, stream>>>(k);
+    else if (delta.planes == 3) delta_kernel<float, 3><<<grid, 256, 0, stream>>>(k);
+    else delta_kernel<float, 1><<<grid, 256, 0, stream>>>(k);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
   }
   if (a.grad_b != nullptr && a.out > 0 &&
       (err = launch_column_sum(part, parts, a.out, a.out, a.grad_b, nullptr, a.gb_dt, stream)) != cudaSuccess)
     return err;
+  if (tc) {
+    TcProduct d = {};
+    d.dt = a.dt;
+    d.b = delta;
+    if (a.grad_x != nullptr) {
+      if ((err = prepare(a.w, a.dt, a.out, a.in, al, true, &work, &d.a, stream)) != cudaSuccess) return err;
+      d.np = a.in; d.nq = a.rows; d.nk = a.out;
+      d.out = a.grad_x;
+      if ((err = launch_tc_product(d, stream)) != cudaSuccess) return err;
+    }
+    if (a.grad_w != nullptr) {
+      if ((err = prepare(a.x, a.dt, a.rows, a.in, al, true, &work, &d.a, stream)) != cudaSuccess) return err;
+      d.b.mn = true;
+      d.np = a.in; d.nq = a.out; d.nk = a.rows;
+      d.out = a.grad_w;
+      return launch_tc_product(d, stream);
+    }
+    return cudaSuccess;
+  }
   Product d = {};
-  d.b = delta != nullptr ? delta : a.grad;
+  d.b = delta.p;
   if (a.grad_x != nullptr) {
     d.a = a.w; d.ap = 1; d.ak = a.in;
     d.bq = a.out; d.bk = 1;

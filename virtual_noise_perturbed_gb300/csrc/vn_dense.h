@@ -1,0 +1,40 @@
+// vn_dense.h -- the product that the centre network's linear layer and its gradients are
+// made of, shared by its dispatcher (vn_dense.cu) and its tensor-core kernels (vn_dense_tc.cu).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "vn.h"
+
+namespace vn {
+
+// A bf16 operand of the tensor-core kernels: [planes][rows][pitch], of which the first `cols`
+// of each row count. mn: the contiguous dimension is p (or q), the rows are k; otherwise k is
+// contiguous. p is 16-byte aligned, pitch a multiple of 8, plane (elements) too.
+struct TcOperand {
+  const void* p;
+  int64_t rows, cols, pitch, plane;
+  int planes;  // 1, or 3: an fp32 matrix as the sum of three
+  bool mn;
+};
+
+// out[q, p] = act(sum_k A(p, k) B(q, k) + bias[p]) + residual[q, p], preact before act.
+// Layouts (a.mn, b.mn): (false, false), (true, false) and (true, true). nk >= 1; np, nq and nk
+// below 2^31 - 256.
+struct TcProduct {
+  TcOperand a, b;
+  int64_t np, nq, nk;
+  vn_dtype dt;  // of residual, out and preact
+  const void* bias;
+  int bias_bf16, act;
+  const void* residual;
+  void* out;
+  void* preact;
+};
+cudaError_t launch_tc_product(const TcProduct& d, cudaStream_t stream);
+
+// Reads and clears the status word of the tensor-core products (0 = fine).
+cudaError_t take_dense_status(unsigned int* status, cudaStream_t stream);
+
+}  // namespace vn

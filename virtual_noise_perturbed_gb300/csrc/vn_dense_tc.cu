@@ -1,0 +1,741 @@
+// vn_dense_tc.cu -- the centre network's products on the 5th-generation tensor cores.
+//
+//   D[q, p] = sum_k A(p, k) B(q, k), p the contiguous dimension of the result (see
+//   vn_dense.cu for the three products that take this form)
+//
+// MMA rows are p (128 TMEM lanes), MMA columns are q: lane l of a warp then holds output
+// p0 + l of every q, so a warp's stores are contiguous, straight from registers. A and B
+// are bf16 in memory, either with k contiguous or with p (q) contiguous: TMA writes
+// 128-byte-swizzled tiles of 64 elements of the contiguous dimension, and the MMA's
+// descriptors and transpose bits say which dimension that is, so no operand is ever transposed
+// by a pass of its own.
+//
+// fp32 operands come as three bf16 planes (8 + 8 + 8 significant bits); the k loop then runs over the
+// six products of planes that reach fp32's precision, the smallest first.
+//
+// Two kernels:
+//   pair   256 x 256 tiles, one per pair of CTAs (cta_group::2): each CTA stages 128 rows of
+//          A and of B, half of what single CTAs would stage for as many products, and L2
+//          carries half as much. Persistent; two accumulators of 256 columns in TMEM, so that a
+//          tile's epilogue runs under the next tile's products.
+//   single 128 x 16..256 tiles of one CTA, for problems that do not fill the GPU with
+//          pairs: the k loop is split over the CTAs of a cluster of up to 8, whose partial
+//          sums are added through distributed shared memory in rank order.
+//
+// Warp roles: 0 TMA producer, 1 TMEM allocation and MMA issue, 2..5 epilogue (one per TMEM
+// lane quarter). Every barrier wait is bounded; one that runs out records a status word,
+// stops the other roles, and the kernel drains what it has issued, frees TMEM and returns.
+#include <cooperative_groups.h>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include "vn_act.cuh"
+#include "vn_dense.h"
+#include "vn_internal.h"
+
+namespace vn {
+
+// Nonzero after a bounded wait of this file ran out (read and cleared by take_dense_status).
+__device__ unsigned int g_dense_status = 0;
+
+namespace {
+
+constexpr int kThreads = 6 * 32;
+constexpr int kK = 64;                          // k of a stage: 128 bytes of bf16, one swizzle atom
+constexpr uint32_t kABytes = 128 * 128;         // 128 rows (or 64 k x 2 blocks of 64 p)
+constexpr uint32_t kBlockBytes = kK * 128;      // one 64-wide block of a p- or q-contiguous operand
+constexpr int kMaxStages = 8;
+constexpr unsigned long long kTimeoutNs = 4000000000ull;
+
+struct Params {
+  const void* bias;
+  const void* residual;
+  void* out;
+  void* preact;
+  int64_t np, nq;
+  int bias_bf16, act;
+  int p_tiles, q_tiles;
+  int64_t units;
+  int k_chunks, iters;  // iterations of the k loop: k_chunks x pairs of planes
+  int stages;
+  uint32_t idesc;
+  unsigned long long timeout_ns;
+};
+
+struct Control {
+  int abort;
+  int pad;
+  unsigned long long timeout_ns;
+};
+
+// ---------------------------------------------------------------- PTX
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint64_t global_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The shared::cluster address of `addr` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float load_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait for the phase of this parity: false when it ran out (status and abort flag are
+// then set) or when another role of the CTA has aborted.
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile Control* c) {
+  const uint64_t t0 = global_ns();
+  const unsigned long long limit = c->timeout_ns;
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try(bar, parity)) return true;
+    if ((n & 63) == 0) {
+      if (c->abort) return false;
+      if (global_ns() - t0 > limit) {
+        atomicOr(&g_dense_status, 1u);
+        c->abort = 1;
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile Control* c) {
+  return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, c);
+}
+template <bool kPair>
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
+  if constexpr (kPair) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  if constexpr (kPair)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+template <bool kPair>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on the barrier (of both CTAs of a pair) once every MMA issued so far is complete.
+template <bool kPair>
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// 32 lanes x 16 consecutive columns: thread t gets lane base + t.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Shared-memory descriptor of a 128-byte-swizzled operand. k contiguous: rows of 128 bytes,
+// 8-row groups 1024 bytes apart; the leading offset is unused. p (q) contiguous: a
+// 64-wide block holds one 128-byte row per k, 8-k groups 1024 bytes apart (stride), and
+// the next 64 elements start kBlockBytes on (leading).
+template <bool kMn>
+__device__ __forceinline__ uint64_t descriptor(uint32_t addr) {
+  uint64_t d = static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(kMn ? kBlockBytes >> 4 : 1) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+// Bytes from one MMA's 16 k to the next within a stage.
+template <bool kMn>
+constexpr uint32_t kStepBytes = kMn ? 16 * 128 : 32;
+
+__device__ __forceinline__ float value(float x) { return x; }
+__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T narrow(float x);
+template <>
+__device__ __forceinline__ float narrow<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// The planes of A and B in the i-th of the six products: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0).
+__device__ __forceinline__ int plane_a(int i) { return (0b000001010010 >> (2 * i)) & 3; }
+__device__ __forceinline__ int plane_b(int i) { return (0b000100011000 >> (2 * i)) & 3; }
+
+// Tile of a unit: groups of 8 tiles along q, p fastest between them, so that the CTAs at
+// work at one time share few rows of A and of B.
+__device__ __forceinline__ void tile_of(const Params& p, int64_t unit, int* tp, int* tq) {
+  const int64_t band = static_cast<int64_t>(p.p_tiles) * 8;
+  const int64_t g = unit / band, r = unit - g * band;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(8), p.q_tiles - g * 8));
+  *tp = static_cast<int>(r / rows);
+  *tq = static_cast<int>(g * 8 + r % rows);
+}
+
+// Bias, activation, residual and the stores of up to 16 outputs of one p (columns q .. q + 15).
+template <typename T>
+__device__ __forceinline__ void finish(const Params& p, const float (&z)[16], int64_t q, int64_t pp, int count,
+                                       float bias) {
+  const int64_t at = q * p.np + pp;
+  float r[16];
+  if (p.residual != nullptr) {
+    const T* res = static_cast<const T*>(p.residual) + at;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = i < count ? value(res[i * p.np]) : 0.f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = 0.f;
+  }
+  T* out = static_cast<T*>(p.out) + at;
+  T* pre = p.preact != nullptr ? static_cast<T*>(p.preact) + at : nullptr;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (i < count) {
+      const float v = z[i] + bias;
+      if (pre != nullptr) pre[i * p.np] = narrow<T>(v);
+      out[i * p.np] = narrow<T>(activate(p.act, v) + r[i]);
+    }
+}
+__device__ __forceinline__ float bias_of(const Params& p, int64_t pp) {
+  if (p.bias == nullptr || pp >= p.np) return 0.f;
+  return p.bias_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[pp])
+                     : static_cast<const float*>(p.bias)[pp];
+}
+
+struct Ring {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++s == n) { s = 0; ph ^= 1u; }
+  }
+};
+
+// One stage: A's 128 rows and B's kRows rows (of this CTA) of 64 k.
+template <bool kAMn, bool kBMn, int kRows, bool kPair>
+__device__ __forceinline__ void load_stage(uint32_t dst, const CUtensorMap* am, const CUtensorMap* bm, uint32_t bar,
+                                           int p0, int q0, int k0, int pa, int pb) {
+  if constexpr (kAMn) {
+    tma_load<kPair>(dst, am, bar, p0, k0, pa);
+    tma_load<kPair>(dst + kBlockBytes, am, bar, p0 + 64, k0, pa);
+  } else {
+    tma_load<kPair>(dst, am, bar, k0, p0, pa);
+  }
+  dst += kABytes;
+  if constexpr (kBMn) {
+#pragma unroll
+    for (int b = 0; b < kRows / 64; ++b) tma_load<kPair>(dst + b * kBlockBytes, bm, bar, q0 + b * 64, k0, pb);
+  } else {
+    tma_load<kPair>(dst, bm, bar, k0, q0, pb);
+  }
+}
+
+template <bool kAMn, bool kBMn, bool kPair>
+__device__ __forceinline__ void issue_stage(uint32_t d, uint32_t stage, uint32_t idesc, bool first) {
+#pragma unroll
+  for (int ks = 0; ks < kK / 16; ++ks)
+    mma<kPair>(d, descriptor<kAMn>(stage + ks * kStepBytes<kAMn>),
+               descriptor<kBMn>(stage + kABytes + ks * kStepBytes<kBMn>), idesc, !(first && ks == 0));
+}
+
+// ---------------------------------------------------------------- pairs of CTAs
+// Barriers: full[S] (leader's, armed for both CTAs' bytes), empty[S], tmem_full[2],
+// tmem_empty[2] (leader's, both CTAs' epilogues), drain.
+template <typename T, bool kAMn, bool kBMn>
+__global__ void __launch_bounds__(kThreads, 1)
+pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const Params p) {
+  constexpr uint32_t kStageBytes = kABytes + 128 * 128;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int S = p.stages;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(S) * kStageBytes);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (S + s); };
+  auto tmem_full = [&](int b) { return bar0 + 8u * (2 * S + b); };
+  auto tmem_empty = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
+  const uint32_t drain = bar0 + 8u * (2 * S + 4);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+  volatile Control* ctl = reinterpret_cast<volatile Control*>(bars + 2 * S + 6);
+  const uint32_t stage0 = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tmem_full(b), 1);
+      mbar_init(tmem_empty(b), 2 * 128);
+    }
+    mbar_init(drain, 1);
+    ctl->abort = 0;
+    ctl->timeout_ns = p.timeout_ns;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc<true>(smem_u32(s_tmem), 512);
+  fence_before();
+  __syncthreads();
+  cluster_sync();
+  fence_after();
+  const uint32_t tmem = *s_tmem;
+  // The peer waits here from its start, so for the whole run of the leader's waits.
+  const unsigned long long drain_ns = 4 * p.timeout_ns;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      Ring rg;
+      bool ok = true;
+      for (int64_t u = pair; ok && u < p.units; u += pairs) {
+        int tp, tq;
+        tile_of(p, u, &tp, &tq);
+        const int p0 = tp * 256 + static_cast<int>(rank) * 128, q0 = tq * 256 + static_cast<int>(rank) * 128;
+        int kc = 0, pr = p.iters == p.k_chunks ? 5 : 0;
+        for (int it = 0; it < p.iters; ++it, rg.next(S)) {
+          if (!(ok = mbar_wait(empty(rg.s), rg.ph ^ 1u, ctl))) break;
+          if (rank == 0) mbar_expect_tx(full(rg.s), 2 * kStageBytes);
+          load_stage<kAMn, kBMn, 128, true>(stage0 + rg.s * kStageBytes, &amap, &bmap, map_rank(full(rg.s), 0), p0, q0,
+                                            kc * kK, plane_a(pr), plane_b(pr));
+          if (++kc == p.k_chunks) { kc = 0; ++pr; }
+        }
+      }
+      // The leader's last commits arrive on this CTA's barriers: be there for them.
+      for (int s = 0; ok && s < S; ++s, rg.next(S)) ok = mbar_wait(empty(rg.s), rg.ph ^ 1u, ctl);
+      if (!ok) {
+        // The copies in flight complete on the leader's barriers, which only the leader
+        // could wait on and may not have armed: give them far longer than a copy takes.
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < 2000000) __nanosleep(1000);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      Ring rg, tb;
+      bool ok = true;
+      for (int64_t u = pair; ok && u < p.units; u += pairs, tb.next(2)) {
+        if (!(ok = mbar_wait(tmem_empty(tb.s), tb.ph ^ 1u, ctl))) break;
+        fence_after();
+        for (int it = 0; it < p.iters; ++it, rg.next(S)) {
+          if (!(ok = mbar_wait(full(rg.s), rg.ph, ctl))) break;
+          fence_after();
+          issue_stage<kAMn, kBMn, true>(tmem + tb.s * 256, stage0 + rg.s * kStageBytes, p.idesc, it == 0);
+          mma_commit<true>(empty(rg.s));
+        }
+        if (ok) mma_commit<true>(tmem_full(tb.s));
+      }
+      mma_commit<true>(drain);
+    }
+    if (lane == 0) {  // both CTAs: every MMA of the pair is complete
+      const uint64_t t0 = global_ns();
+      while (!mbar_try(drain, 0) && global_ns() - t0 < drain_ns) {
+      }
+    }
+  } else {
+    const int quarter = warp & 3;
+    Ring tb;
+    for (int64_t u = pair; u < p.units; u += pairs, tb.next(2)) {
+      int tp, tq;
+      tile_of(p, u, &tp, &tq);
+      const int64_t pp = static_cast<int64_t>(tp) * 256 + rank * 128 + quarter * 32 + lane;
+      const int64_t q0 = static_cast<int64_t>(tq) * 256;
+      const float bias = bias_of(p, pp);
+      const bool ok = mbar_wait(tmem_full(tb.s), tb.ph, ctl);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      fence_after();
+      const uint32_t d = tmem + tb.s * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
+      const int cols = static_cast<int>(min(static_cast<int64_t>(256), p.nq - q0));
+      for (int c = 0; c < cols; c += 16) {
+        uint32_t v[16];
+        tmem_load16(d + c, v);
+        tmem_wait_load();
+        float z[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(v[i]);
+        if (pp < p.np) finish<T>(p, z, q0 + c, pp, cols - c, bias);
+      }
+      fence_before();
+      mbar_arrive_cluster(map_rank(tmem_empty(tb.s), 0));
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA's shared memory or TMEM goes while the other may use it
+  if (warp == 1) {
+    fence_after();
+    tmem_free<true>(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- single CTAs, k split
+// The unit's k iterations are split over the cluster's CTAs. Barriers: full[S], empty[S],
+// tmem_full.
+template <typename T, int BN, bool kAMn, bool kBMn>
+__global__ void __launch_bounds__(kThreads)
+single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const Params p,
+              const int split) {
+  constexpr uint32_t kStageBytes = kABytes + BN * 128;
+  constexpr uint32_t kCols = BN < 32 ? 32 : BN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int S = p.stages;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(S) * kStageBytes);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (S + s); };
+  const uint32_t tmem_full = bar0 + 8u * (2 * S);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * S + 1);
+  volatile Control* ctl = reinterpret_cast<volatile Control*>(bars + 2 * S + 2);
+  const uint32_t stage0 = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  int tp, tq;
+  tile_of(p, blockIdx.x / split, &tp, &tq);
+  const int first = static_cast<int>(static_cast<int64_t>(p.iters) * rank / split);
+  const int last = static_cast<int>(static_cast<int64_t>(p.iters) * (rank + 1) / split);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(tmem_full, 1);
+    ctl->abort = 0;
+    ctl->timeout_ns = p.timeout_ns;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc<false>(smem_u32(s_tmem), kCols);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *s_tmem;
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      Ring rg;
+      uint32_t issued = 0;
+      const bool planes = p.iters != p.k_chunks;
+      int pr = planes ? first / p.k_chunks : 5, kc = planes ? first % p.k_chunks : first;
+      for (int it = first; it < last; ++it, rg.next(S)) {
+        if (!(ok = mbar_wait(empty(rg.s), rg.ph ^ 1u, ctl))) break;
+        mbar_expect_tx(full(rg.s), kStageBytes);
+        load_stage<kAMn, kBMn, BN, false>(stage0 + rg.s * kStageBytes, &amap, &bmap, full(rg.s), tp * 128, tq * BN,
+                                          kc * kK, plane_a(pr), plane_b(pr));
+        ++issued;
+        if (++kc == p.k_chunks) { kc = 0; ++pr; }
+      }
+      if (!ok) {  // wait, bounded, for the copies in flight
+        for (uint32_t k = 0; k < static_cast<uint32_t>(S) && k < issued; ++k) {
+          const uint32_t j = issued - 1 - k;
+          const uint64_t t0 = global_ns();
+          while (!mbar_try(full(static_cast<int>(j % S)), (j / S) & 1u) && global_ns() - t0 < p.timeout_ns) {
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      Ring rg;
+      for (int it = first; it < last; ++it, rg.next(S)) {
+        if (!(ok = mbar_wait(full(rg.s), rg.ph, ctl))) break;
+        fence_after();
+        issue_stage<kAMn, kBMn, false>(tmem, stage0 + rg.s * kStageBytes, p.idesc, it == first);
+        mma_commit<false>(empty(rg.s));
+      }
+      mma_commit<false>(tmem_full);  // also after an abort: what was issued completes
+      const uint64_t t0 = global_ns();
+      while (!mbar_try(tmem_full, 0) && global_ns() - t0 < p.timeout_ns) {
+      }
+    }
+  } else {
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const int64_t pp = static_cast<int64_t>(tp) * 128 + row;
+    const int64_t q0 = static_cast<int64_t>(tq) * BN;
+    const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const int cols = static_cast<int>(min(static_cast<int64_t>(BN), p.nq - q0));
+    const float bias = bias_of(p, pp);
+    ok = mbar_wait(tmem_full, 0, ctl);
+    ok = __all_sync(0xFFFFFFFFu, ok) && !ctl->abort;
+    if (ok) {
+      fence_after();
+      for (int c = 0; c < cols; c += 16) {
+        uint32_t v[16];
+        tmem_load16(d + c, v);
+        tmem_wait_load();
+        if (split == 1) {
+          float z[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(v[i]);
+          if (pp < p.np) finish<T>(p, z, q0 + c, pp, cols - c, bias);
+        } else {
+          // Every copy has landed and every MMA has read it: the stages hold the partial sums now.
+          float* part = reinterpret_cast<float*>(smem) + row;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) part[(c + i) * 128] = __uint_as_float(v[i]);
+        }
+      }
+      fence_before();
+    }
+  }
+  if (split > 1) {
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 2 && !ctl->abort) {
+      const int row = (warp & 3) * 32 + lane;
+      const int64_t pp = static_cast<int64_t>(tp) * 128 + row;
+      const int64_t q0 = static_cast<int64_t>(tq) * BN;
+      const int cols = static_cast<int>(min(static_cast<int64_t>(BN), p.nq - q0));
+      const int c0 = cols * rank / split, c1 = cols * (rank + 1) / split;
+      const float bias = bias_of(p, pp);
+      if (pp < p.np) {
+        for (int c = c0; c < c1; c += 16) {
+          float z[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) z[i] = 0.f;
+          for (int r = 0; r < split; ++r) {
+            const uint32_t from = map_rank(stage0 + (c * 128 + row) * 4, r);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (c + i < c1) z[i] += load_cluster(from + i * 512);
+          }
+          finish<T>(p, z, q0 + c, pp, c1 - c, bias);
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    tmem_free<false>(tmem, kCols);
+  }
+}
+
+// ---------------------------------------------------------------- host
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+// [planes][rows][cols] of bf16, `pitch` elements a row; boxes of 64 x `box` rows.
+bool make_map(CUtensorMap* map, const TcOperand& o, int box) {
+  std::memset(map, 0, sizeof(*map));
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.cols), static_cast<cuuint64_t>(o.rows),
+                              static_cast<cuuint64_t>(o.planes)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.pitch) * 2, static_cast<cuuint64_t>(o.plane) * 2};
+  const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(box), 1};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p), dims, strides, boxes, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+uint32_t idesc_of(int m, int n, bool a_mn, bool b_mn) {
+  // fp32 accumulator, bf16 operands, transpose bits, N / 8, M / 16
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+constexpr size_t kFixed = 1024 + 8 * (2 * kMaxStages + 6) + sizeof(Control);
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*fn)(KArgs...), SmemRecord& record, int grid, int cluster, size_t smem,
+                           cudaStream_t stream, Args... args) {
+  const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(fn), smem, record);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+template <typename T, bool kAMn, bool kBMn>
+cudaError_t run_pair(const TcProduct& d, Params p, int sms, cudaStream_t stream) {
+  CUtensorMap am, bm;
+  if (!make_map(&am, d.a, kAMn ? 64 : 128) || !make_map(&bm, d.b, kBMn ? 64 : 128)) return cudaErrorInvalidValue;
+  p.p_tiles = static_cast<int>((d.np + 255) / 256);
+  p.q_tiles = static_cast<int>((d.nq + 255) / 256);
+  p.units = static_cast<int64_t>(p.p_tiles) * p.q_tiles;
+  p.stages = 6;
+  p.idesc = idesc_of(256, 256, kAMn, kBMn);
+  const int grid = static_cast<int>(std::min<int64_t>(2 * p.units, sms / 2 * 2));
+  static SmemRecord record;
+  return launch_cluster(pair_kernel<T, kAMn, kBMn>, record, grid, 2, kFixed + p.stages * (kABytes + 128 * 128), stream,
+                        am, bm, p);
+}
+
+template <typename T, int BN, bool kAMn, bool kBMn>
+cudaError_t run_single(const TcProduct& d, Params p, int split, cudaStream_t stream) {
+  constexpr uint32_t kStage = kABytes + BN * 128;
+  CUtensorMap am, bm;
+  if (!make_map(&am, d.a, kAMn ? 64 : 128) || !make_map(&bm, d.b, kBMn ? 64 : BN)) return cudaErrorInvalidValue;
+  p.p_tiles = static_cast<int>((d.np + 127) / 128);
+  p.q_tiles = static_cast<int>((d.nq + BN - 1) / BN);
+  p.units = static_cast<int64_t>(p.p_tiles) * p.q_tiles;
+  p.stages = static_cast<int>(std::min<uint32_t>(kMaxStages, 200 * 1024 / kStage));
+  p.idesc = idesc_of(128, BN, kAMn, kBMn);
+  if (p.units * split > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  static SmemRecord record;
+  return launch_cluster(single_kernel<T, BN, kAMn, kBMn>, record, static_cast<int>(p.units * split), split,
+                        kFixed + static_cast<size_t>(p.stages) * kStage, stream, am, bm, p, split);
+}
+
+template <typename T, bool kAMn, bool kBMn>
+cudaError_t run(const TcProduct& d, cudaStream_t stream) {
+  DeviceInfo dev;
+  cudaError_t err = device_info(&dev);
+  if (err != cudaSuccess) return err;
+  Params p = {};
+  p.bias = d.bias; p.bias_bf16 = d.bias_bf16; p.act = d.act;
+  p.residual = d.residual; p.out = d.out; p.preact = d.preact;
+  p.np = d.np; p.nq = d.nq;
+  p.k_chunks = static_cast<int>((d.nk + kK - 1) / kK);
+  p.iters = p.k_chunks * (d.a.planes == 3 ? 6 : 1);
+  p.timeout_ns = kTimeoutNs;
+  const int64_t pairs = ((d.np + 255) / 256) * ((d.nq + 255) / 256);
+  if (pairs * 2 >= dev.sm_count / 2) return run_pair<T, kAMn, kBMn>(d, p, dev.sm_count, stream);
+  // Columns a tile: all of q in one tile where 256 suffice, so that A is staged once; then as
+  // many CTAs on the k loop as leave each two stages and still fit the GPU at once.
+  const int64_t p_tiles = (d.np + 127) / 128;
+  const int bn = d.nq <= 16 ? 16 : d.nq <= 32 ? 32 : d.nq <= 64 ? 64 : 128;
+  const int64_t tiles = p_tiles * ((d.nq + bn - 1) / bn);
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= 2 * dev.sm_count && p.iters >= 2 * split * 2) split *= 2;
+  if constexpr (!kBMn) {
+    if (bn == 16) return run_single<T, 16, kAMn, kBMn>(d, p, split, stream);
+    if (bn == 32) return run_single<T, 32, kAMn, kBMn>(d, p, split, stream);
+  }
+  if (bn <= 64) return run_single<T, 64, kAMn, kBMn>(d, p, split, stream);
+  return run_single<T, 128, kAMn, kBMn>(d, p, split, stream);
+}
+
+template <typename T>
+cudaError_t run_layout(const TcProduct& d, cudaStream_t stream) {
+  if (!d.a.mn) return run<T, false, false>(d, stream);
+  return d.b.mn ? run<T, true, true>(d, stream) : run<T, true, false>(d, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_tc_product(const TcProduct& d, cudaStream_t stream) {
+  return d.dt == VN_BF16 ? run_layout<__nv_bfloat16>(d, stream) : run_layout<float>(d, stream);
+}
+
+cudaError_t take_dense_status(unsigned int* status, cudaStream_t stream) {
+  cudaError_t err =
+      cudaMemcpyFromSymbolAsync(status, g_dense_status, sizeof(unsigned int), 0, cudaMemcpyDeviceToHost, stream);
+  if (err != cudaSuccess) return err;
+  if ((err = cudaStreamSynchronize(stream)) != cudaSuccess || *status == 0) return err;
+  const unsigned int zero = 0;
+  err = cudaMemcpyToSymbolAsync(g_dense_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream);
+  return err == cudaSuccess ? cudaStreamSynchronize(stream) : err;
+}
+
+}  // namespace vn
