@@ -96,7 +96,9 @@ __global__ void __launch_bounds__(kThreads) product_kernel(const Product d) {
         if (d.bias != nullptr)
           z += d.bias_bf16 ? value(static_cast<const __nv_bfloat16*>(d.bias)[p]) : static_cast<const float*>(d.bias)[p];
         if (d.preact != nullptr) static_cast<T*>(d.preact)[q * d.np + p] = narrow<T>(z);
-        z = activate(d.act, z);
+        float v[1] = {z};
+        activate_all<false>(d.act, v);
+        z = v[0];
         if (d.residual != nullptr) z += value(static_cast<const T*>(d.residual)[q * d.np + p]);
         static_cast<T*>(d.out)[q * d.np + p] = narrow<T>(z);
       }
@@ -224,8 +226,7 @@ __global__ void __launch_bounds__(256) delta_kernel(const Delta a) {
       if (a.act != VN_ACT_NONE) {
         float u[8];
         load8(z + r * a.n + c, count, a.vec_in != 0, u);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = q < count ? v[q] * slope(a.act, u[q]) : 0.f;
+        slope_all<sizeof(T) == 2>(a.act, u, v);
       }
       if (a.d != nullptr) store8<T, kPlanes>(a.d, r * a.pitch + c, a.plane, v, count, a.vec_out != 0);
 #pragma unroll

@@ -22,8 +22,8 @@
 //          pairs: the k loop is split over the CTAs of a cluster of up to 8, whose partial
 //          sums are added through distributed shared memory in rank order.
 //
-// Warp roles: 0 TMA producer, 1 TMEM allocation and MMA issue, 2..5 epilogue (one per TMEM
-// lane quarter). Every barrier wait is bounded; one that runs out records a status word,
+// Warp roles: 0 TMA producer, 1 TMEM allocation and MMA issue, from 2 on epilogue (one or two
+// per TMEM lane quarter). Every barrier wait is bounded; one that runs out records a status word,
 // stops the other roles, and the kernel drains what it has issued, frees TMEM and returns.
 #include <cooperative_groups.h>
 #include <cuda.h>
@@ -46,7 +46,8 @@ __device__ unsigned int g_dense_status = 0;
 
 namespace {
 
-constexpr int kThreads = 6 * 32;
+constexpr int kThreads = 6 * 32;      // single: 4 epilogue warps
+constexpr int kPairThreads = 10 * 32;  // pair: 8, two for each lane quarter, 128 columns each
 constexpr int kK = 64;                          // k of a stage: 128 bytes of bf16, one swizzle atom
 constexpr uint32_t kABytes = 128 * 128;         // 128 rows (or 64 k x 2 blocks of 64 p)
 constexpr uint32_t kBlockBytes = kK * 128;      // one 64-wide block of a p- or q-contiguous operand
@@ -61,6 +62,7 @@ struct Params {
   int64_t np, nq;
   int bias_bf16, act;
   int p_tiles, q_tiles;
+  int bn;  // pair: columns of a tile, a multiple of 16
   int64_t units;
   int k_chunks, iters;  // iterations of the k loop: k_chunks x pairs of planes
   int stages;
@@ -157,6 +159,27 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, u
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(c0), "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 template <bool kPair>
 __device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
@@ -255,29 +278,41 @@ __device__ __forceinline__ void tile_of(const Params& p, int64_t unit, int* tp, 
   *tq = static_cast<int>(g * 8 + r % rows);
 }
 
-// Bias, activation, residual and the stores of up to 16 outputs of one p (columns q .. q + 15).
+// Sixteen outputs of one p, columns q .. q + 15 (the first `count` of them), in two steps: the
+// residual's loads, which the caller issues ahead of the sums, and the rest of the epilogue.
 template <typename T>
-__device__ __forceinline__ void finish(const Params& p, const float (&z)[16], int64_t q, int64_t pp, int count,
-                                       float bias) {
-  const int64_t at = q * p.np + pp;
-  float r[16];
-  if (p.residual != nullptr) {
-    const T* res = static_cast<const T*>(p.residual) + at;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = i < count ? value(res[i * p.np]) : 0.f;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = 0.f;
-  }
-  T* out = static_cast<T*>(p.out) + at;
-  T* pre = p.preact != nullptr ? static_cast<T*>(p.preact) + at : nullptr;
+struct Residual {
+  T v[16];
+};
+template <typename T>
+__device__ __forceinline__ void load_residual(const Params& p, int64_t q, int64_t pp, int count, Residual<T>* r) {
+  if (p.residual == nullptr || pp >= p.np) return;
+  const T* at = static_cast<const T*>(p.residual) + q * p.np + pp;
 #pragma unroll
   for (int i = 0; i < 16; ++i)
-    if (i < count) {
-      const float v = z[i] + bias;
-      if (pre != nullptr) pre[i * p.np] = narrow<T>(v);
-      out[i * p.np] = narrow<T>(activate(p.act, v) + r[i]);
-    }
+    if (i < count) r->v[i] = at[i * p.np];
+}
+template <typename T>
+__device__ __forceinline__ void finish(const Params& p, float (&z)[16], const Residual<T>& r, int64_t q, int64_t pp,
+                                       int count, float bias) {
+  const int64_t at = q * p.np + pp;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] += bias;
+  if (p.preact != nullptr) {
+    T* pre = static_cast<T*>(p.preact) + at;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < count) pre[i * p.np] = narrow<T>(z[i]);
+  }
+  activate_all<sizeof(T) == 2>(p.act, z);
+  if (p.residual != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] += value(r.v[i]);
+  }
+  T* out = static_cast<T*>(p.out) + at;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (i < count) out[i * p.np] = narrow<T>(z[i]);
 }
 __device__ __forceinline__ float bias_of(const Params& p, int64_t pp) {
   if (p.bias == nullptr || pp >= p.np) return 0.f;
@@ -293,10 +328,11 @@ struct Ring {
   }
 };
 
-// One stage: A's 128 rows and B's kRows rows (of this CTA) of 64 k.
-template <bool kAMn, bool kBMn, int kRows, bool kPair>
+// One stage: A's 128 rows and B's rows of this CTA (one box, or `blocks` 64-wide blocks) of
+// 64 k.
+template <bool kAMn, bool kBMn, bool kPair>
 __device__ __forceinline__ void load_stage(uint32_t dst, const CUtensorMap* am, const CUtensorMap* bm, uint32_t bar,
-                                           int p0, int q0, int k0, int pa, int pb) {
+                                           int p0, int q0, int k0, int pa, int pb, int blocks) {
   if constexpr (kAMn) {
     tma_load<kPair>(dst, am, bar, p0, k0, pa);
     tma_load<kPair>(dst + kBlockBytes, am, bar, p0 + 64, k0, pa);
@@ -305,8 +341,7 @@ __device__ __forceinline__ void load_stage(uint32_t dst, const CUtensorMap* am, 
   }
   dst += kABytes;
   if constexpr (kBMn) {
-#pragma unroll
-    for (int b = 0; b < kRows / 64; ++b) tma_load<kPair>(dst + b * kBlockBytes, bm, bar, q0 + b * 64, k0, pb);
+    for (int b = 0; b < blocks; ++b) tma_load<kPair>(dst + b * kBlockBytes, bm, bar, q0 + b * 64, k0, pb);
   } else {
     tma_load<kPair>(dst, bm, bar, k0, q0, pb);
   }
@@ -321,24 +356,42 @@ __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t stage, uint32_t
 }
 
 // ---------------------------------------------------------------- pairs of CTAs
+// Staged epilogue: each half of the epilogue warps (128 threads, half the tile's columns)
+// moves 16 columns x 128 p at a time through shared memory, residual in and outputs out by
+// TMA, double buffered: whole 256-byte rows travel, and no warp waits on a load of its own.
+// Straight 2-byte loads and stores of the same tile were the bound (455 us against 166 us without
+// residual and pre-activation, on 8192 x 4096 x 4096).
+template <typename T>
+constexpr uint32_t kChunkBytes = 16 * 128 * sizeof(T);
+template <typename T>
+constexpr uint32_t kStagingBytes = 2 * 6 * kChunkBytes<T>;  // halves x (y, z, residual) x 2
+template <typename T>
+constexpr int kPairStages = sizeof(T) == 2 ? 5 : 4;
+constexpr uint32_t kPairStageBytes = kABytes + 128 * 128;
+
 // Barriers: full[S] (leader's, armed for both CTAs' bytes), empty[S], tmem_full[2],
-// tmem_empty[2] (leader's, both CTAs' epilogues), drain.
-template <typename T, bool kAMn, bool kBMn>
-__global__ void __launch_bounds__(kThreads, 1)
-pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const Params p) {
-  constexpr uint32_t kStageBytes = kABytes + 128 * 128;
+// tmem_empty[2] (leader's, both CTAs' epilogues), drain, residual[2 halves][2].
+template <typename T, bool kAMn, bool kBMn, bool kStaged>
+__global__ void __launch_bounds__(kPairThreads, 1)
+pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+            const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap zmap,
+            const __grid_constant__ CUtensorMap rmap, const Params p) {
+  constexpr int S = kPairStages<T>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int S = p.stages;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(S) * kStageBytes);
+  uint8_t* staging = smem + S * kPairStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + (kStaged ? kStagingBytes<T> : 0));
   const uint32_t bar0 = smem_u32(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (S + s); };
   auto tmem_full = [&](int b) { return bar0 + 8u * (2 * S + b); };
   auto tmem_empty = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
   const uint32_t drain = bar0 + 8u * (2 * S + 4);
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
-  volatile Control* ctl = reinterpret_cast<volatile Control*>(bars + 2 * S + 6);
+  auto arrived = [&](int h, int b) { return bar0 + 8u * (2 * S + 5 + 2 * h + b); };
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * S + 9);
+  // Whether the half's leader saw its wait through: [half][tile's accumulator, or 2 for a residual].
+  volatile int* s_go = reinterpret_cast<volatile int*>(bars + 2 * S + 10);
+  volatile Control* ctl = reinterpret_cast<volatile Control*>(bars + 2 * S + 13);
   const uint32_t stage0 = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -351,9 +404,10 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tmem_full(b), 1);
-      mbar_init(tmem_empty(b), 2 * 128);
+      mbar_init(tmem_empty(b), 2 * 8);
     }
     mbar_init(drain, 1);
+    for (int b = 0; b < 4; ++b) mbar_init(arrived(b >> 1, b & 1), 1);
     ctl->abort = 0;
     ctl->timeout_ns = p.timeout_ns;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -366,21 +420,24 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
   const uint32_t tmem = *s_tmem;
   // The peer waits here from its start, so for the whole run of the leader's waits.
   const unsigned long long drain_ns = 4 * p.timeout_ns;
+  const int half_q = p.bn / 2;  // rows of B in each CTA
 
   if (warp == 0) {
     if (lane == 0) {
       Ring rg;
       bool ok = true;
+      const int blocks = (half_q + 63) / 64;
+      const uint32_t bytes = 2 * (kABytes + (kBMn ? blocks * kBlockBytes : half_q * 128u));
       for (int64_t u = pair; ok && u < p.units; u += pairs) {
         int tp, tq;
         tile_of(p, u, &tp, &tq);
-        const int p0 = tp * 256 + static_cast<int>(rank) * 128, q0 = tq * 256 + static_cast<int>(rank) * 128;
+        const int p0 = tp * 256 + static_cast<int>(rank) * 128, q0 = tq * p.bn + static_cast<int>(rank) * half_q;
         int kc = 0, pr = p.iters == p.k_chunks ? 5 : 0;
         for (int it = 0; it < p.iters; ++it, rg.next(S)) {
           if (!(ok = mbar_wait(empty(rg.s), rg.ph ^ 1u, ctl))) break;
-          if (rank == 0) mbar_expect_tx(full(rg.s), 2 * kStageBytes);
-          load_stage<kAMn, kBMn, 128, true>(stage0 + rg.s * kStageBytes, &amap, &bmap, map_rank(full(rg.s), 0), p0, q0,
-                                            kc * kK, plane_a(pr), plane_b(pr));
+          if (rank == 0) mbar_expect_tx(full(rg.s), bytes);
+          load_stage<kAMn, kBMn, true>(stage0 + rg.s * kPairStageBytes, &amap, &bmap, map_rank(full(rg.s), 0), p0, q0,
+                                       kc * kK, plane_a(pr), plane_b(pr), blocks);
           if (++kc == p.k_chunks) { kc = 0; ++pr; }
         }
       }
@@ -403,7 +460,7 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
         for (int it = 0; it < p.iters; ++it, rg.next(S)) {
           if (!(ok = mbar_wait(full(rg.s), rg.ph, ctl))) break;
           fence_after();
-          issue_stage<kAMn, kBMn, true>(tmem + tb.s * 256, stage0 + rg.s * kStageBytes, p.idesc, it == 0);
+          issue_stage<kAMn, kBMn, true>(tmem + tb.s * 256, stage0 + rg.s * kPairStageBytes, p.idesc, it == 0);
           mma_commit<true>(empty(rg.s));
         }
         if (ok) mma_commit<true>(tmem_full(tb.s));
@@ -417,30 +474,113 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
     }
   } else {
     const int quarter = warp & 3;
+    const int h = warp < 6 ? 0 : 1;
+    const int half = (p.bn / 16 + 1) / 2 * 16;  // columns of half 0
+    const int c0 = h * half, width = h ? p.bn - half : half;
+    const bool leader = quarter == 2 && lane == 0;  // warps 2 and 6
+    T* const buf = reinterpret_cast<T*>(staging + h * (kStagingBytes<T> / 2));
+    const uint32_t buf0 = smem_u32(buf);
+    constexpr int kChunk = 16 * 128;
+    const bool has_r = p.residual != nullptr, has_z = p.preact != nullptr;
     Ring tb;
-    for (int64_t u = pair; u < p.units; u += pairs, tb.next(2)) {
+    uint32_t jj = 0;  // chunks so far
+    bool go = true;
+    for (int64_t u = pair; go && u < p.units; u += pairs, tb.next(2)) {
       int tp, tq;
       tile_of(p, u, &tp, &tq);
-      const int64_t pp = static_cast<int64_t>(tp) * 256 + rank * 128 + quarter * 32 + lane;
-      const int64_t q0 = static_cast<int64_t>(tq) * 256;
+      const int p0 = tp * 256 + static_cast<int>(rank) * 128;
+      const int64_t pp = static_cast<int64_t>(p0) + quarter * 32 + lane;
+      const int64_t q0 = static_cast<int64_t>(tq) * p.bn + c0;
       const float bias = bias_of(p, pp);
-      const bool ok = mbar_wait(tmem_full(tb.s), tb.ph, ctl);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      fence_after();
-      const uint32_t d = tmem + tb.s * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
-      const int cols = static_cast<int>(min(static_cast<int64_t>(256), p.nq - q0));
-      for (int c = 0; c < cols; c += 16) {
-        uint32_t v[16];
-        tmem_load16(d + c, v);
-        tmem_wait_load();
-        float z[16];
+      const int cols = static_cast<int>(min(static_cast<int64_t>(width), p.nq - q0));
+      const uint32_t d = tmem + tb.s * 256 + c0 + (static_cast<uint32_t>(quarter * 32) << 16);
+      if constexpr (kStaged) {
+        auto fetch = [&](uint32_t j, int c) {
+          mbar_expect_tx(arrived(h, j & 1), kChunkBytes<T>);
+          tma_load_2d(buf0 + (4 + (j & 1)) * kChunkBytes<T>, &rmap, arrived(h, j & 1), p0, static_cast<int>(q0) + c);
+        };
+        if (leader) {
+          if (has_r && cols > 0) fetch(jj, 0);
+          s_go[3 * h + tb.s] = mbar_wait(tmem_full(tb.s), tb.ph, ctl);
+        }
+        named_barrier(1 + h, 128);
+        go = s_go[3 * h + tb.s] != 0;
+        if (!go) {  // the residual on its way has to land before the CTA ends
+          if (leader && has_r && cols > 0) mbar_wait(arrived(h, jj & 1), (jj >> 1) & 1u, ctl);
+          break;
+        }
+        fence_after();
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 16, ++jj) {
+          uint32_t v[16];
+          __syncwarp();
+          tmem_load16(d + c, v);
+          if (leader && has_r && c + 16 < cols) fetch(jj + 1, c + 16);
+          __syncwarp();
+          tmem_wait_load();
+          float z[16];
+          T pre[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(v[i]);
-        if (pp < p.np) finish<T>(p, z, q0 + c, pp, cols - c, bias);
+          for (int i = 0; i < 16; ++i) {
+            z[i] = __uint_as_float(v[i]) + bias;
+            pre[i] = narrow<T>(z[i]);
+          }
+          activate_all<sizeof(T) == 2>(p.act, z);
+          if (leader) {  // the outputs' buffers are free again, and the residual is there
+            bulk_wait_read<1>();
+            if (has_r) s_go[3 * h + 2] = mbar_wait(arrived(h, jj & 1), (jj >> 1) & 1u, ctl);
+          }
+          named_barrier(1 + h, 128);
+          const int row = quarter * 32 + lane;
+          if (has_r) {
+            if (!(go = s_go[3 * h + 2] != 0)) break;
+            (void)mbar_try(arrived(h, jj & 1), (jj >> 1) & 1u);
+            const T* r = buf + (4 + (jj & 1)) * kChunk + row;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[i] += value(r[i * 128]);
+          }
+          T* y = buf + (jj & 1) * kChunk + row;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i * 128] = narrow<T>(z[i]);
+          if (has_z) {
+            T* zo = buf + (2 + (jj & 1)) * kChunk + row;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) zo[i * 128] = pre[i];
+          }
+          fence_async_smem();
+          named_barrier(1 + h, 128);
+          if (leader) {
+            tma_store_2d(&ymap, buf0 + (jj & 1) * kChunkBytes<T>, p0, static_cast<int>(q0) + c);
+            if (has_z) tma_store_2d(&zmap, buf0 + (2 + (jj & 1)) * kChunkBytes<T>, p0, static_cast<int>(q0) + c);
+            bulk_commit();
+          }
+        }
+        if (!go) break;
+      } else {
+        Residual<T> r;
+        load_residual(p, q0, pp, cols, &r);
+        const bool ok = mbar_wait(tmem_full(tb.s), tb.ph, ctl);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        fence_after();
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 16) {
+          uint32_t v[16];
+          tmem_load16(d + c, v);
+          Residual<T> ahead;
+          load_residual(p, q0 + c + 16, pp, cols - c - 16, &ahead);
+          tmem_wait_load();
+          float z[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(v[i]);
+          if (pp < p.np) finish<T>(p, z, r, q0 + c, pp, cols - c, bias);
+          r = ahead;
+        }
       }
       fence_before();
-      mbar_arrive_cluster(map_rank(tmem_empty(tb.s), 0));
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_rank(tmem_empty(tb.s), 0));
     }
+    if (kStaged && leader) bulk_wait_read<0>();
   }
   __syncwarp();
   fence_before();
@@ -505,8 +645,8 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
       for (int it = first; it < last; ++it, rg.next(S)) {
         if (!(ok = mbar_wait(empty(rg.s), rg.ph ^ 1u, ctl))) break;
         mbar_expect_tx(full(rg.s), kStageBytes);
-        load_stage<kAMn, kBMn, BN, false>(stage0 + rg.s * kStageBytes, &amap, &bmap, full(rg.s), tp * 128, tq * BN,
-                                          kc * kK, plane_a(pr), plane_b(pr));
+        load_stage<kAMn, kBMn, false>(stage0 + rg.s * kStageBytes, &amap, &bmap, full(rg.s), tp * 128, tq * BN, kc * kK,
+                                      plane_a(pr), plane_b(pr), BN / 64);
         ++issued;
         if (++kc == p.k_chunks) { kc = 0; ++pr; }
       }
@@ -541,10 +681,13 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
     const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const int cols = static_cast<int>(min(static_cast<int64_t>(BN), p.nq - q0));
     const float bias = bias_of(p, pp);
+    Residual<T> r;
+    if (split == 1) load_residual(p, q0, pp, cols, &r);
     ok = mbar_wait(tmem_full, 0, ctl);
     ok = __all_sync(0xFFFFFFFFu, ok) && !ctl->abort;
     if (ok) {
       fence_after();
+#pragma unroll 1
       for (int c = 0; c < cols; c += 16) {
         uint32_t v[16];
         tmem_load16(d + c, v);
@@ -553,7 +696,10 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
           float z[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(v[i]);
-          if (pp < p.np) finish<T>(p, z, q0 + c, pp, cols - c, bias);
+          Residual<T> ahead;
+          load_residual(p, q0 + c + 16, pp, cols - c - 16, &ahead);
+          if (pp < p.np) finish<T>(p, z, r, q0 + c, pp, cols - c, bias);
+          r = ahead;
         } else {
           // Every copy has landed and every MMA has read it: the stages hold the partial sums now.
           float* part = reinterpret_cast<float*>(smem) + row;
@@ -579,13 +725,15 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
           float z[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) z[i] = 0.f;
+          Residual<T> res;
+          load_residual(p, q0 + c, pp, c1 - c, &res);
           for (int r = 0; r < split; ++r) {
             const uint32_t from = map_rank(stage0 + (c * 128 + row) * 4, r);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               if (c + i < c1) z[i] += load_cluster(from + i * 512);
           }
-          finish<T>(p, z, q0 + c, pp, c1 - c, bias);
+          finish<T>(p, z, res, q0 + c, pp, c1 - c, bias);
         }
       }
     }
@@ -629,22 +777,38 @@ bool make_map(CUtensorMap* map, const TcOperand& o, int box) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [nq][np] of the results' type, boxes of 128 x 16.
+bool make_result_map(CUtensorMap* map, const void* p, vn_dtype dt, int64_t np, int64_t nq) {
+  std::memset(map, 0, sizeof(*map));
+  if (p == nullptr) return true;
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(np), static_cast<cuuint64_t>(nq)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(np) * (dt == VN_BF16 ? 2 : 4)};
+  const cuuint32_t boxes[2] = {128, 16};
+  const cuuint32_t ones[2] = {1, 1};
+  return encode(map, dt == VN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                const_cast<void*>(p), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 uint32_t idesc_of(int m, int n, bool a_mn, bool b_mn) {
   // fp32 accumulator, bf16 operands, transpose bits, N / 8, M / 16
   return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-constexpr size_t kFixed = 1024 + 8 * (2 * kMaxStages + 6) + sizeof(Control);
+constexpr size_t kFixed = 1024 + 8 * (2 * kMaxStages + 14) + sizeof(Control);
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*fn)(KArgs...), SmemRecord& record, int grid, int cluster, size_t smem,
+cudaError_t launch_cluster(void (*fn)(KArgs...), SmemRecord& record, int grid, int threads, int cluster, size_t smem,
                            cudaStream_t stream, Args... args) {
   const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(fn), smem, record);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -656,19 +820,46 @@ cudaError_t launch_cluster(void (*fn)(KArgs...), SmemRecord& record, int grid, i
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
-template <typename T, bool kAMn, bool kBMn>
-cudaError_t run_pair(const TcProduct& d, Params p, int sms, cudaStream_t stream) {
-  CUtensorMap am, bm;
-  if (!make_map(&am, d.a, kAMn ? 64 : 128) || !make_map(&bm, d.b, kBMn ? 64 : 128)) return cudaErrorInvalidValue;
+// Columns of a pair's tile: of the multiples of 16 from 128 to 256, the one with the least
+// work on the busiest pair -- rounds of tiles x (columns + 16, for what a tile costs beside its
+// products). 4096 x 4096 results on 76 pairs: 4 rounds of 224 columns, not 4 of 256.
+int pair_columns(int64_t np, int64_t nq, int pairs) {
+  int best = 256;
+  int64_t cost = INT64_MAX;
+  for (int bn = 256; bn >= 128; bn -= 16) {
+    const int64_t tiles = ((np + 255) / 256) * ((nq + bn - 1) / bn);
+    const int64_t c = (tiles + pairs - 1) / pairs * (bn + 16);
+    if (c < cost) { cost = c; best = bn; }
+  }
+  return best;
+}
+
+template <typename T, bool kAMn, bool kBMn, bool kStaged>
+cudaError_t run_pair_typed(const TcProduct& d, Params p, int sms, cudaStream_t stream) {
+  const int pairs = sms / 2;
+  p.bn = pair_columns(d.np, d.nq, pairs);
+  CUtensorMap am, bm, ym, zm, rm;
+  if (!make_map(&am, d.a, kAMn ? 64 : 128) || !make_map(&bm, d.b, kBMn ? 64 : p.bn / 2)) return cudaErrorInvalidValue;
+  if (!make_result_map(&ym, kStaged ? d.out : nullptr, d.dt, d.np, d.nq) ||
+      !make_result_map(&zm, kStaged ? d.preact : nullptr, d.dt, d.np, d.nq) ||
+      !make_result_map(&rm, kStaged ? d.residual : nullptr, d.dt, d.np, d.nq))
+    return cudaErrorInvalidValue;
   p.p_tiles = static_cast<int>((d.np + 255) / 256);
-  p.q_tiles = static_cast<int>((d.nq + 255) / 256);
+  p.q_tiles = static_cast<int>((d.nq + p.bn - 1) / p.bn);
   p.units = static_cast<int64_t>(p.p_tiles) * p.q_tiles;
-  p.stages = 6;
-  p.idesc = idesc_of(256, 256, kAMn, kBMn);
-  const int grid = static_cast<int>(std::min<int64_t>(2 * p.units, sms / 2 * 2));
+  p.idesc = idesc_of(256, p.bn, kAMn, kBMn);
+  const int grid = static_cast<int>(std::min<int64_t>(2 * p.units, 2 * pairs));
   static SmemRecord record;
-  return launch_cluster(pair_kernel<T, kAMn, kBMn>, record, grid, 2, kFixed + p.stages * (kABytes + 128 * 128), stream,
-                        am, bm, p);
+  return launch_cluster(pair_kernel<T, kAMn, kBMn, kStaged>, record, grid, kPairThreads, 2,
+                        kFixed + kPairStages<T> * kPairStageBytes + (kStaged ? kStagingBytes<T> : 0), stream, am, bm, ym,
+                        zm, rm, p);
+}
+template <typename T, bool kAMn, bool kBMn>
+cudaError_t run_pair(const TcProduct& d, const Params& p, int sms, cudaStream_t stream) {
+  auto fits = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
+  const bool staged = d.np * sizeof(T) % 16 == 0 && fits(d.out) && fits(d.preact) && fits(d.residual);
+  return staged ? run_pair_typed<T, kAMn, kBMn, true>(d, p, sms, stream)
+                : run_pair_typed<T, kAMn, kBMn, false>(d, p, sms, stream);
 }
 
 template <typename T, int BN, bool kAMn, bool kBMn>
@@ -683,7 +874,7 @@ cudaError_t run_single(const TcProduct& d, Params p, int split, cudaStream_t str
   p.idesc = idesc_of(128, BN, kAMn, kBMn);
   if (p.units * split > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   static SmemRecord record;
-  return launch_cluster(single_kernel<T, BN, kAMn, kBMn>, record, static_cast<int>(p.units * split), split,
+  return launch_cluster(single_kernel<T, BN, kAMn, kBMn>, record, static_cast<int>(p.units * split), kThreads, split,
                         kFixed + static_cast<size_t>(p.stages) * kStage, stream, am, bm, p, split);
 }
 
