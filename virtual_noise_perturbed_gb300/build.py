@@ -5,8 +5,10 @@ Usage: ``python -m virtual_noise_perturbed_gb300.build [--force] [-v]``.
 Each ``csrc/*.cu`` file is compiled in parallel to ``_build/*.o`` and the
 objects are linked into ``virtual_noise_perturbed_gb300/libvn.so`` (CUDA
 runtime linked statically; the driver API is reached through the runtime's
-entry-point query, so no link against libcuda is needed). A rebuild happens
-only when a source or header is newer than the library. Builds take a file lock,
+entry-point query, so no link against libcuda is needed). ``csrc/vn_torch.cpp``, the
+centre network's calls on torch tensors, is compiled beside them with the host compiler
+into ``_binding.so``, which links to the library. A rebuild happens
+only when a source or header is newer than the libraries. Builds take a file lock,
 so processes that start together (the ranks of one job, test workers) build
 once: the others wait, then find the library current.
 """
@@ -17,10 +19,12 @@ import argparse
 import concurrent.futures as cf
 import fcntl
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,6 +32,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libvn.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -46,15 +51,19 @@ def sources() -> list:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def binding_source() -> str:
+    return os.path.join(CSRC, "vn_torch.cpp")
+
+
 def _inputs() -> list:
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
+    return sources() + [binding_source()] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
         + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
@@ -85,10 +94,24 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     return LIB
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch is required to build _binding.so")
+    return list(spec.submodule_search_locations)[0]
+
+
 def _compile_and_link(verbose: bool, extra_flags) -> None:
     cc = nvcc()
     flags = CFLAGS + list(extra_flags or [])
-    objs, cmds = [], []
+    torch_dir, cuda = _torch_dir(), os.path.dirname(os.path.dirname(os.path.realpath(cc)))
+    cxx = os.environ.get("CXX") or "g++"
+    bobj = os.path.join(BUILD, "vn_torch.o")
+    objs = []
+    cmds = [[cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-I", os.path.join(torch_dir, "include"),
+             "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+             "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+             "-c", binding_source(), "-o", bobj]]
     for src in sources():
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
@@ -96,8 +119,13 @@ def _compile_and_link(verbose: bool, extra_flags) -> None:
     with cf.ThreadPoolExecutor(max_workers=min(len(cmds), os.cpu_count() or 4)) as ex:
         list(ex.map(lambda c: _run(c, verbose), cmds))
     tmp = LIB + ".tmp"
-    _run([cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"], verbose)
+    _run([cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static", "-Xlinker", "-soname=libvn.so"], verbose)
     os.replace(tmp, LIB)
+    tmp = BINDING + ".tmp"
+    _run([cxx, "-shared", "-o", tmp, bobj, "-L", PKG, "-l:libvn.so", "-Wl,-rpath,$ORIGIN",
+          "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"],
+         verbose)
+    os.replace(tmp, BINDING)
 
 
 def main(argv=None) -> int:

@@ -5,12 +5,14 @@ gradient: these, or the population's estimate (``virtual_flat_gradient`` and the
 
 Like the rest of the package's Python, these functions only check and marshal arguments and
 call ``libvn.so`` on the current CUDA stream; all arithmetic runs in the library's kernels.
-Tensors must be on a CUDA device; there is no CPU path. Inputs that are not contiguous are
-copied first.
+They do it in a small extension module (``csrc/vn_torch.cpp``), since a call's time on the host is
+what a small layer costs. Tensors must be on a CUDA device; there is no CPU path. Inputs that
+are not contiguous are copied first.
 """
 
 from __future__ import annotations
 
+import os
 import struct
 from array import array
 from typing import Optional, Sequence, Tuple, Union
@@ -18,11 +20,28 @@ from typing import Optional, Sequence, Tuple, Union
 import torch
 
 from . import _lib
-from ._lib import check, load
-from .api import _DT, _cuda, _device, _dt, device_status
+from ._lib import load
+from .api import _device, _dt, device_status
 
 _ACTS = {None: _lib.VN_ACT_NONE, "none": _lib.VN_ACT_NONE, "tanh": _lib.VN_ACT_TANH, "relu": _lib.VN_ACT_RELU,
          "gelu": _lib.VN_ACT_GELU, "silu": _lib.VN_ACT_SILU}
+
+
+_binding = None
+
+
+def _native():
+    """The extension module over libvn.so; raise if it is missing (no fallback exists)."""
+    global _binding
+    if _binding is None:
+        load()
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is not built; build it with `python -m virtual_noise_perturbed_gb300.build` "
+                               "(needs nvcc)")
+        from . import _binding as module
+        _binding = module
+    return _binding
 
 
 def _act(activation: Optional[str]) -> int:
@@ -30,60 +49,6 @@ def _act(activation: Optional[str]) -> int:
         return _ACTS[activation]
     except (KeyError, TypeError):
         raise ValueError("activation must be None, 'tanh', 'relu', 'gelu' or 'silu'") from None
-
-
-def _at(t: Optional[torch.Tensor]) -> int:
-    return 0 if t is None else t.data_ptr()
-
-
-def _run(device: torch.device, where: str, fn, *args) -> None:
-    """fn(*args, stream) with ``device`` current, on its current stream."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        check(fn(*args, stream), where)
-    else:
-        with torch.cuda.device(device):
-            check(fn(*args, stream), where)
-
-
-def _same(t: torch.Tensor, name: str, shape, dtype: torch.dtype) -> torch.Tensor:
-    """``t`` contiguous, of this shape and dtype."""
-    t = _cuda(t, name)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return t
-
-
-def _workspace(bytes_: int, device: torch.device) -> Optional[torch.Tensor]:
-    return torch.empty(bytes_, dtype=torch.uint8, device=device) if bytes_ > 0 else None
-
-
-def _result(out: Optional[torch.Tensor], shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(out, torch.Tensor) or out.shape != shape or out.dtype != dtype or not out.is_contiguous() \
-            or out.device != device:
-        raise ValueError(f"out must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
-    return out
-
-
-def _layer(x: torch.Tensor, weight: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor, int, int, int, int]:
-    """x and weight checked; rows, in, out and the type of a linear layer on them."""
-    x = _cuda(x, "x")
-    weight = _cuda(weight, "weight")
-    if weight.dim() != 2:
-        raise ValueError("weight must be (out_features, in_features)")
-    n, k = weight.shape
-    if x.dim() < 1 or x.shape[-1] != k:
-        raise ValueError(f"x must be (..., {k}), got {tuple(x.shape)}")
-    if x.dtype != weight.dtype:
-        raise TypeError(f"x and weight must have one dtype, got {x.dtype} and {weight.dtype}")
-    rows = 1
-    for d in x.shape[:-1]:
-        rows *= d
-    return x, weight, rows, k, n, _dt(x, "x")
 
 
 def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
@@ -98,27 +63,10 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     value before the activation that ``linear_backward`` needs. ``check_status=True`` calls
     ``device_status()`` before returning (it synchronises): the tensor-core kernels bound
     their waits, and a wait that ran out leaves y unwritten."""
-    lib = load()
-    x, weight, rows, k, n, dt = _layer(x, weight)
-    shape = x.shape[:-1] + (n,)
-    if bias is not None:
-        bias = _cuda(bias, "bias")
-        if bias.shape != (n,):
-            raise ValueError(f"bias must have shape ({n},)")
-    if residual is not None:
-        residual = _same(residual, "residual", shape, x.dtype)
-    act = _act(activation)
-    dev = _device(x, weight, bias, residual)
-    y = _result(out, shape, x.dtype, dev)
-    z = torch.empty(shape, dtype=x.dtype, device=dev) if preact else None
-    px, pw = x.data_ptr(), weight.data_ptr()
-    need = lib.vn_linear_workspace(rows, k, n, dt, not (px | pw) & 15)
-    ws = _workspace(need, dev)
-    _run(dev, "vn_linear", lib.vn_linear, px, pw, dt, _at(bias), _dt(bias, "bias") if bias is not None else 0,
-         _at(residual), rows, k, n, act, y.data_ptr(), _at(z), _at(ws), max(need, 0))
+    y = (_binding or _native()).linear(x, weight, bias, _act(activation), residual, preact, out)
     if check_status:
-        device_status(dev)
-    return (y, z) if preact else y
+        device_status(x.device)
+    return y
 
 
 def linear_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
@@ -130,45 +78,10 @@ def linear_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     returned (not needed without an activation). The gradients have their tensors' shapes and
     dtypes, grad_bias the weight's (None with ``bias=False``). The residual's gradient is
     grad."""
-    lib = load()
-    x, weight, rows, k, n, dt = _layer(x, weight)
-    shape = x.shape[:-1] + (n,)
-    grad = _same(grad, "grad", shape, x.dtype)
-    act = _act(activation)
-    if act != _lib.VN_ACT_NONE:
-        if preact is None:
-            raise ValueError("the gradient through an activation needs preact")
-        preact = _same(preact, "preact", shape, x.dtype)
-    else:
-        preact = None
-    dev = _device(grad, x, weight, preact)
-    gx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    gw = torch.empty((n, k), dtype=x.dtype, device=dev)
-    gb = torch.empty(n, dtype=x.dtype, device=dev) if bias else None
-    pg, px, pw = grad.data_ptr(), x.data_ptr(), weight.data_ptr()
-    need = lib.vn_linear_backward_workspace(rows, k, n, dt, act, not (pg | px | pw) & 15)
-    ws = _workspace(need, dev)
-    _run(dev, "vn_linear_backward", lib.vn_linear_backward, pg, px, pw, _at(preact), dt, rows, k, n, act,
-         gx.data_ptr(), gw.data_ptr(), _at(gb), dt, _at(ws), max(need, 0))
+    grads = (_binding or _native()).linear_backward(grad, x, weight, preact, _act(activation), bias)
     if check_status:
-        device_status(dev)
-    return gx, gw, gb
-
-
-def _norm_params(weight: Optional[torch.Tensor], bias: Optional[torch.Tensor], n: int):
-    """Weight and bias of a norm over n elements, checked, and their one type."""
-    dts = []
-    out = []
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            t = _cuda(t, name)
-            if t.shape != (n,):
-                raise ValueError(f"{name} must have shape ({n},)")
-            dts.append(_dt(t, name))
-        out.append(t)
-    if len(set(dts)) > 1:
-        raise TypeError("weight and bias must have one dtype")
-    return out[0], out[1], dts[0] if dts else _lib.VN_F32
+        device_status(x.device)
+    return grads
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, *,
@@ -178,20 +91,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     bias (``vn_layer_norm``). x is float32 or bfloat16 and y like it; weight and bias (n,) are of
     either type, or None. mean and rstd are float32 of x's leading shape; ``layer_norm_backward``
     takes them."""
-    lib = load()
-    x = _cuda(x, "x")
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError("x must be (..., n) with n >= 1")
-    n = x.shape[-1]
-    weight, bias, wdt = _norm_params(weight, bias, n)
-    dev = _device(x, weight, bias)
-    y = _result(out, x.shape, x.dtype, dev)
-    lead = x.shape[:-1]
-    mean = torch.empty(lead, dtype=torch.float32, device=dev)
-    rstd = torch.empty(lead, dtype=torch.float32, device=dev)
-    _run(dev, "vn_layer_norm", lib.vn_layer_norm, x.data_ptr(), _dt(x, "x"), _at(weight), _at(bias), wdt,
-         mean.numel(), n, float(eps), y.data_ptr(), mean.data_ptr(), rstd.data_ptr())
-    return y, mean, rstd
+    return (_binding or _native()).layer_norm(x, weight, bias, eps, out)
 
 
 def layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
@@ -199,28 +99,7 @@ def layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
         -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
     """(grad_x, grad_weight, grad_bias) of ``layer_norm`` from its stored mean and rstd
     (``vn_layer_norm_backward``). The last two are (n,) of weight's dtype, None without a weight."""
-    lib = load()
-    x = _cuda(x, "x")
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError("x must be (..., n) with n >= 1")
-    n = x.shape[-1]
-    grad = _same(grad, "grad", x.shape, x.dtype)
-    mean = _same(mean, "mean", x.shape[:-1], torch.float32)
-    rstd = _same(rstd, "rstd", x.shape[:-1], torch.float32)
-    weight, _, wdt = _norm_params(weight, None, n)
-    dev = _device(grad, x, mean, rstd, weight)
-    gx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    gw = gb = ws = None
-    rows, need = mean.numel(), 0
-    if weight is not None:
-        gw = torch.empty(n, dtype=weight.dtype, device=dev)
-        gb = torch.empty(n, dtype=weight.dtype, device=dev)
-        need = lib.vn_layer_norm_backward_workspace(rows, n)
-        ws = _workspace(need, dev)
-    _run(dev, "vn_layer_norm_backward", lib.vn_layer_norm_backward, grad.data_ptr(), x.data_ptr(), _dt(x, "x"),
-         mean.data_ptr(), rstd.data_ptr(), _at(weight), wdt, rows, n, gx.data_ptr(), _at(gw), _at(gb), _at(ws),
-         max(need, 0))
-    return gx, gw, gb
+    return (_binding or _native()).layer_norm_backward(grad, x, mean, rstd, weight)
 
 
 class AdamW:
@@ -241,16 +120,17 @@ class AdamW:
     def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999),
                  eps: float = 1e-8, weight_decay: Union[float, Sequence[float]] = 0.01, *, state_bits: int = 32,
                  maximize: bool = False, state: Optional[dict] = None, step: int = 0):
-        self.params = list(params)
+        self.params = tuple(params)
         if not self.params:
             raise ValueError("at least one tensor is needed")
+        self._params = list(self.params)
         for i, p in enumerate(self.params):
             if not isinstance(p, torch.Tensor) or not p.is_cuda or not p.is_contiguous():
                 raise ValueError(f"params[{i}] must be a contiguous CUDA tensor (updated in place)")
             if p.dtype != self.params[0].dtype:
                 raise TypeError("the parameters must have one dtype")
         self.device = _device(*self.params)
-        self._dt = _dt(self.params[0], "params[0]")
+        _dt(self.params[0], "params[0]")
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
         n = len(self.params)
@@ -264,16 +144,21 @@ class AdamW:
         for s in self.sizes:
             self.offsets.append(total)
             total += -(-s // self.BLOCK) * self.BLOCK
-        self.state = self._state(total, state)
-        # One row of eight words a tensor, as the library's struct has them.
-        self._table = array("Q", bytes(64 * n))
-        self._table[6::8] = array("Q", self.sizes)
-        self._table[7::8] = array("Q", struct.pack(f"{n}d", *decay))
-        starts, at = [], 0
-        for s in self.sizes:
-            starts.append(at)
-            at += s
-        self._starts, self.total = starts, at
+        self._tensors = self._state(total, state)
+        # One row of eight words a tensor, as the library's struct has them: param, grad, both
+        # moments, their scales, the number of elements, the decay.
+        self._table = t = array("Q", bytes(64 * n))
+        held = self._tensors
+        m, v, size = held["m"].data_ptr(), held["v"].data_ptr(), state_bits // 8
+        t[2::8] = array("Q", [m + o * size for o in self.offsets])
+        t[3::8] = array("Q", [v + o * size for o in self.offsets])
+        if state_bits == 8:
+            m, v = held["m_scale"].data_ptr(), held["v_scale"].data_ptr()
+            t[4::8] = array("Q", [m + o // self.BLOCK * 4 for o in self.offsets])
+            t[5::8] = array("Q", [v + o // self.BLOCK * 4 for o in self.offsets])
+        t[6::8] = array("Q", self.sizes)
+        t[7::8] = array("Q", struct.pack(f"{n}d", *decay))
+        self._address = t.buffer_info()[0]
 
     def _state(self, total: int, given: Optional[dict]) -> dict:
         kind = torch.float32 if self.state_bits == 32 else torch.float8_e4m3fn
@@ -292,66 +177,28 @@ class AdamW:
                 raise ValueError(f"state['{k}'] must be a contiguous {d} tensor of shape ({size},) on {self.device}")
         return dict(given)
 
-    def _grads(self, grads) -> Tuple[list, torch.dtype, list]:
-        """Addresses of the tensors' gradients, their dtype, and what has to stay alive."""
-        if isinstance(grads, torch.Tensor):
-            grads = _cuda(grads, "grads")
-            if grads.shape != (self.total,):
-                raise ValueError(f"a flat gradient must have shape ({self.total},)")
-            _device(grads, self.params[0])
-            base, size = grads.data_ptr(), grads.element_size()
-            return [base + o * size for o in self._starts], grads.dtype, [grads]
-        grads = list(grads)
-        if len(grads) != len(self.params):
-            raise ValueError(f"{len(self.params)} tensors but {len(grads)} gradients")
-        kept, kind = [], None
-        for i, (g, p) in enumerate(zip(grads, self.params)):
-            if not isinstance(g, torch.Tensor) or g.shape != p.shape or g.device != p.device:
-                raise ValueError(f"grads[{i}] must have params[{i}]'s shape and device")
-            if kind is None:
-                kind = g.dtype
-            elif g.dtype != kind:
-                raise TypeError("the gradients must have one dtype")
-            kept.append(g if g.is_contiguous() else g.contiguous())
-        return [g.data_ptr() for g in kept], kind, kept
+    @property
+    def state(self) -> dict:
+        """The moments' tensors (a new dict of them: their addresses are the handle's)."""
+        return dict(self._tensors)
 
     def step(self, grads: Union[torch.Tensor, Sequence[torch.Tensor]], lr: Optional[float] = None) -> None:
         """One step of every tensor. ``grads``: a gradient for each tensor, or one flat tensor with
         all of them one after another (as ``virtual_flat_gradient`` lays them out); float32 or
         bfloat16. ``lr`` replaces the learning rate for this step."""
-        lib = load()
-        at, kind, kept = self._grads(grads)
-        if kind not in _DT:
-            raise TypeError(f"grads: dtype {kind} is not supported (float32 or bfloat16)")
-        t, s, o = self._table, self.state, self.offsets
-        t[0::8] = array("Q", [p.data_ptr() for p in self.params])
-        t[1::8] = array("Q", at)
-        m, v, size = s["m"].data_ptr(), s["v"].data_ptr(), self.state_bits // 8
-        t[2::8] = array("Q", [m + i * size for i in o])
-        t[3::8] = array("Q", [v + i * size for i in o])
-        if self.state_bits == 8:
-            m, v = s["m_scale"].data_ptr(), s["v_scale"].data_ptr()
-            t[4::8] = array("Q", [m + i // 64 for i in o])
-            t[5::8] = array("Q", [v + i // 64 for i in o])
-        _run(self.device, "vn_adamw", lib.vn_adamw, t.buffer_info()[0], len(self.params), self._dt, _DT[kind],
-             self.state_bits, self.lr if lr is None else float(lr), self.betas[0], self.betas[1], self.eps,
-             self.steps + 1, self.maximize)
+        if not isinstance(grads, (list, torch.Tensor)):
+            grads = list(grads)
+        (_binding or _native()).adamw(self._params, grads, self._address, self.state_bits, self.lr if lr is None else lr,
+                                      self.betas[0], self.betas[1], self.eps, self.steps + 1, self.maximize)
         self.steps += 1
-        del kept
 
     def moments(self) -> Tuple[torch.Tensor, torch.Tensor]:
         """The moments (m, v) as flat float32 tensors in ``offsets``' layout: the state itself with
         32 bits, with 8 the values that the codes stand for (``vn_adamw_moments``)."""
-        s = self.state
+        s = self._tensors
         if self.state_bits == 32:
             return s["m"], s["v"]
-        lib = load()
-        n = s["m"].numel()
-        m = torch.empty(n, dtype=torch.float32, device=self.device)
-        v = torch.empty(n, dtype=torch.float32, device=self.device)
-        _run(self.device, "vn_adamw_moments", lib.vn_adamw_moments, s["m"].data_ptr(), s["v"].data_ptr(),
-             s["m_scale"].data_ptr(), s["v_scale"].data_ptr(), n, m.data_ptr(), v.data_ptr())
-        return m, v
+        return (_binding or _native()).adamw_moments(s["m"], s["v"], s["m_scale"], s["v_scale"])
 
 
 __all__ = ["AdamW", "layer_norm", "layer_norm_backward", "linear", "linear_backward"]
