@@ -176,3 +176,19 @@ def test_oracle_e4m3_against_torch():
     assert np.array_equal(ora.e4m3(x.astype(np.float32).astype(np.float64)), want)
     q, s = ora.pack(np.array([0.0, 1.0, 1e-9, -1.0]), root=True)
     assert q[0] == 0 and q[1] == 448 and q[2] == 2.0 ** -9 and math.isclose(s[0], 1 / 448)
+
+
+def test_workspaces_cover_what_the_calls_lay_out(lib):
+    """Sizes on both sides of each route: a converted matrix is whole rows of a multiple of 8 elements,
+    bf16 as one plane, fp32 as three."""
+    w = lib.vn_linear_workspace
+    assert w(1021, 256, 256, 0, 1) == 0                                  # gathered
+    assert w(8192, 4096, 4096, 1, 1) == 0                                # taken as it is
+    assert w(8192, 4097, 4096, 1, 1) >= 2 * 4104 * (8192 + 4096)         # rows padded
+    assert w(8192, 4096, 4096, 1, 0) >= 2 * 4096 * (8192 + 4096)         # not aligned
+    assert w(8192, 1000, 4096, 0, 1) >= 6 * 1000 * (8192 + 4096)         # three planes
+    b = lib.vn_linear_backward_workspace
+    assert b(8192, 4096, 4096, 1, 0, 1) < 2 * 8192 * 4096                # only the bias's sums
+    assert b(8192, 4096, 4096, 1, 3, 1) >= 2 * 8192 * 4096               # and d
+    assert b(8192, 1000, 4096, 0, 3, 1) >= 6 * (8192 * 4096 + 1000 * (8192 + 4096))
+    assert b(100, 0, 8, 0, 0, 1) > 0 and b(0, 8, 8, 0, 0, 1) > 0

@@ -17,6 +17,7 @@
 #include "vn_act.cuh"
 #include "vn_dense.h"
 #include "vn_internal.h"
+#include "vn_split.cuh"
 
 namespace vn {
 namespace {
@@ -105,22 +106,6 @@ __global__ void __launch_bounds__(kThreads) product_kernel(const Product d) {
     }
 }
 
-// The three bf16 terms of an fp32 value, exactly: its top 8 significant bits, the next 8, the
-// last 8. Terms of an infinity or NaN are the value itself and zeros.
-__device__ __forceinline__ void split3(float v, uint32_t (&t)[3]) {
-  const uint32_t u = __float_as_uint(v);
-  t[0] = u >> 16;
-  if ((u & 0x7F800000u) == 0x7F800000u) {
-    if ((u & 0x007FFFFFu) != 0) t[0] |= 0x40u;  // a NaN stays one
-    t[1] = t[2] = 0;
-    return;
-  }
-  const float r1 = v - __uint_as_float(u & 0xFFFF0000u);
-  t[1] = __float_as_uint(r1) >> 16;
-  const float r2 = r1 - __uint_as_float(__float_as_uint(r1) & 0xFFFF0000u);
-  t[2] = __float_as_uint(r2) >> 16;
-}
-
 // Eight values to row-major memory. kPlanes 1: in T, 16-byte stores where they fit; 3: bf16
 // planes, `plane` elements apart, the whole group written (pitch is a multiple of 8).
 template <typename T, int kPlanes>
@@ -133,7 +118,7 @@ __device__ __forceinline__ void store8(void* dst, int64_t at, int64_t plane, con
       split3(v[2 * q], a);
       split3(v[2 * q + 1], b);
 #pragma unroll
-      for (int k = 0; k < 3; ++k) w[k][q] = a[k] | (b[k] << 16);
+      for (int k = 0; k < 3; ++k) w[k][q] = join_terms(a[k], b[k]);
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k)
@@ -269,13 +254,24 @@ int64_t operand_bytes(int64_t rows, int64_t cols, vn_dtype dt) {
 // Whether a matrix can be taken as it is.
 bool as_is(vn_dtype dt, int64_t cols, bool aligned) { return dt == VN_BF16 && cols % 8 == 0 && aligned; }
 
-// Whether a layer's products go to the tensor cores: from the size on at which their launch
-// and, in fp32, the splitting pay.
-bool uses_tc(int64_t rows, int64_t in, int64_t out, vn_dtype dt) {
+// How a layer, or its gradients, are computed.
+enum class Route {
+  kPlain,   // 64 x 64 tiles without tensor cores: sizes beyond 32-bit coordinates
+  kGather,  // one launch, operands gathered by threads: results of few tiles
+  kTiles,   // operands by TMA, in bf16 (converted where they are not): vn_dense_tc.cu
+};
+bool fits32(int64_t rows, int64_t in, int64_t out) {
   const int64_t most = (int64_t{1} << 31) - 512;
-  if (rows < 1 || in < 1 || out < 1 || rows > most || in > most || out > most) return false;
-  const double macs = static_cast<double>(rows) * static_cast<double>(in) * static_cast<double>(out);
-  return macs >= (dt == VN_BF16 ? 65536.0 : 67108864.0);
+  return rows <= most && in <= most && out <= most;
+}
+Route forward_route(int64_t rows, int64_t in, int64_t out, vn_dtype dt, bool aligned) {
+  if (!fits32(rows, in, out)) return Route::kPlain;
+  if (in > 0 && (fills_pairs(out, rows) || as_is(dt, in, aligned))) return Route::kTiles;
+  return Route::kGather;
+}
+Route backward_route(int64_t rows, int64_t in, int64_t out) {
+  if (!fits32(rows, in, out)) return Route::kPlain;
+  return rows > 0 && out > 0 && (fills_pairs(in, rows) || fills_pairs(in, out)) ? Route::kTiles : Route::kGather;
 }
 
 // Row groups that the column sums are split over.
@@ -310,13 +306,15 @@ cudaError_t prepare(const void* p, vn_dtype dt, int64_t rows, int64_t cols, bool
 }  // namespace
 
 int64_t dense_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, bool aligned) {
-  if (!uses_tc(rows, in, out, dt) || as_is(dt, in, aligned)) return 0;
+  if (forward_route(rows, in, out, dt, aligned) != Route::kTiles || as_is(dt, in, aligned)) return 0;
   return operand_bytes(rows, in, dt) + operand_bytes(out, in, dt);
 }
 
 int64_t dense_backward_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, vn_act act, bool aligned) {
+  const Route route = backward_route(rows, in, out);
   const int64_t sums = rounded(delta_parts(rows) * out * 4);
-  if (!uses_tc(rows, in, out, dt))
+  if (route == Route::kGather) return sums;
+  if (route == Route::kPlain)
     return sums + (act != VN_ACT_NONE ? rounded(rows * out * (dt == VN_BF16 ? 2 : 4)) : 0);
   int64_t bytes = sums;
   if (act != VN_ACT_NONE || !as_is(dt, out, aligned)) bytes += operand_bytes(rows, out, dt);
@@ -325,8 +323,10 @@ int64_t dense_backward_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype
 }
 
 cudaError_t launch_dense(const DenseArgs& a, cudaStream_t stream) {
-  if (uses_tc(a.rows, a.in, a.out, a.dt)) {
-    const bool al = aligned16(a.x) && aligned16(a.w);
+  const bool al = aligned16(a.x) && aligned16(a.w);
+  const Route route = forward_route(a.rows, a.in, a.out, a.dt, al);
+  if (route == Route::kGather) return launch_gather_forward(a, stream);
+  if (route == Route::kTiles) {
     uint8_t* work = static_cast<uint8_t*>(a.workspace);
     TcProduct d = {};
     cudaError_t err = prepare(a.w, a.dt, a.out, a.in, al, false, &work, &d.a, stream);
@@ -347,14 +347,56 @@ cudaError_t launch_dense(const DenseArgs& a, cudaStream_t stream) {
   return product(d, a.dt, stream);
 }
 
+namespace {
+
+// d into `delta` (where given) and the bias's gradient (where asked for) by way of `part`.
+cudaError_t delta_pass(const DenseGradArgs& a, const TcOperand* delta, float* part, cudaStream_t stream) {
+  const int64_t parts = a.rows > 0 ? delta_parts(a.rows) : 0;
+  if (a.rows > 0 && a.out > 0 && (delta != nullptr || a.grad_b != nullptr)) {
+    Delta k = {};
+    k.g = a.grad; k.z = a.preact;
+    k.part = a.grad_b != nullptr ? part : nullptr;
+    k.rows = a.rows; k.n = a.out;
+    if (delta != nullptr) {
+      k.d = const_cast<void*>(delta->p);
+      k.pitch = delta->pitch; k.plane = delta->plane;
+      k.vec_out = delta->pitch % 8 == 0;
+    }
+    k.act = a.act;
+    k.vec_in = a.out % 8 == 0 && aligned16(a.grad) && (a.act == VN_ACT_NONE || aligned16(a.preact));
+    const int64_t tiles = (a.out + 255) / 256;
+    if (tiles > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(parts));
+    if (a.dt == VN_BF16) delta_kernel<__nv_bfloat16, 1><<<grid, 256, 0, stream>>>(k);
+    else if (delta != nullptr && delta->planes == 3) delta_kernel<float, 3><<<grid, 256, 0, stream>>>(k);
+    else delta_kernel<float, 1><<<grid, 256, 0, stream>>>(k);
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+  }
+  if (a.grad_b == nullptr || a.out == 0) return cudaSuccess;
+  return launch_column_sum(part, parts, a.out, a.out, a.grad_b, nullptr, a.gb_dt, stream);
+}
+
+}  // namespace
+
 cudaError_t launch_dense_backward(const DenseGradArgs& a, cudaStream_t stream) {
-  const bool tc = uses_tc(a.rows, a.in, a.out, a.dt);
+  const Route route = backward_route(a.rows, a.in, a.out);
+  if (route == Route::kGather) {
+    // The gather kernel sums the bias's gradient beside the weight's; alone it is a pass over d.
+    DenseGradArgs rest = a;
+    if (a.grad_b != nullptr && a.grad_w == nullptr) {
+      const cudaError_t err = delta_pass(a, nullptr, static_cast<float*>(a.workspace), stream);
+      if (err != cudaSuccess || a.grad_x == nullptr) return err;
+      rest.grad_b = nullptr;
+    }
+    return launch_gather_backward(rest, stream);
+  }
+  const bool tc = route != Route::kPlain;
   const bool al = aligned16(a.grad) && aligned16(a.x) && aligned16(a.w);
   const bool products = a.grad_x != nullptr || a.grad_w != nullptr;
   const bool keep = products && (a.act != VN_ACT_NONE || (tc && !as_is(a.dt, a.out, al)));  // d has to be stored
   uint8_t* work = static_cast<uint8_t*>(a.workspace);
   cudaError_t err = cudaSuccess;
-  const int64_t parts = a.rows > 0 ? delta_parts(a.rows) : 0;
   float* part = reinterpret_cast<float*>(work);
   work += rounded(delta_parts(a.rows) * a.out * 4);
   TcOperand delta = operand(a.grad, a.rows, a.out, false);
@@ -367,26 +409,7 @@ cudaError_t launch_dense_backward(const DenseGradArgs& a, cudaStream_t stream) {
       work += operand_bytes(a.rows, a.out, a.dt);
     }
   }
-  if (a.rows > 0 && a.out > 0 && (keep || a.grad_b != nullptr)) {
-    Delta k = {};
-    k.g = a.grad; k.z = a.preact;
-    k.d = keep ? const_cast<void*>(delta.p) : nullptr;
-    k.part = a.grad_b != nullptr ? part : nullptr;
-    k.rows = a.rows; k.n = a.out; k.pitch = delta.pitch; k.plane = delta.plane;
-    k.act = a.act;
-    k.vec_in = a.out % 8 == 0 && aligned16(a.grad) && (a.act == VN_ACT_NONE || aligned16(a.preact));
-    k.vec_out = delta.pitch % 8 == 0;
-    const int64_t tiles = (a.out + 255) / 256;
-    if (tiles > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(parts));
-    if (a.dt == VN_BF16) delta_kernel<__nv_bfloat16, 1><<<grid, 256, 0, stream>>>(k);
-    else if (delta.planes == 3) delta_kernel<float, 3><<<grid, 256, 0, stream>>>(k);
-    else delta_kernel<float, 1><<<grid, 256, 0, stream>>>(k);
-    if ((err = cudaGetLastError()) != cudaSuccess) return err;
-  }
-  if (a.grad_b != nullptr && a.out > 0 &&
-      (err = launch_column_sum(part, parts, a.out, a.out, a.grad_b, nullptr, a.gb_dt, stream)) != cudaSuccess)
-    return err;
+  if ((err = delta_pass(a, keep ? &delta : nullptr, part, stream)) != cudaSuccess) return err;
   if (tc) {
     TcProduct d = {};
     d.dt = a.dt;

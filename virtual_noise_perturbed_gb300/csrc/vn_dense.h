@@ -34,6 +34,21 @@ struct TcProduct {
 };
 cudaError_t launch_tc_product(const TcProduct& d, cudaStream_t stream);
 
+// Whether a result has tiles enough (256 x 256) for at least half of a GB300's 76 pairs of
+// SMs; with fewer, 128-wide tiles whose k loop is split spread it further.
+inline bool fills_pairs(int64_t np, int64_t nq) {
+  return np > 0 && nq > 0 && ((np + 255) / 256) * ((nq + 255) / 256) >= 38;
+}
+
+// A layer, or all its gradients, in one launch, for any alignment and no workspace
+// (vn_dense_gather.cu). At least one of grad_x and grad_w is asked for, and grad_b only with
+// grad_w; rows, in and out from 1 to 2^31 - 512.
+struct DenseArgs;
+struct DenseGradArgs;
+cudaError_t launch_gather_forward(const DenseArgs& a, cudaStream_t stream);
+cudaError_t launch_gather_backward(const DenseGradArgs& a, cudaStream_t stream);
+cudaError_t take_gather_status(unsigned int* status, cudaStream_t stream);
+
 // Reads and clears the status word of the tensor-core products (0 = fine).
 cudaError_t take_dense_status(unsigned int* status, cudaStream_t stream);
 

@@ -25,7 +25,6 @@
 // Warp roles: 0 TMA producer, 1 TMEM allocation and MMA issue, from 2 on epilogue (one or two
 // per TMEM lane quarter). Every barrier wait is bounded; one that runs out records a status word,
 // stops the other roles, and the kernel drains what it has issued, frees TMEM and returns.
-#include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -38,29 +37,18 @@
 #include "vn_act.cuh"
 #include "vn_dense.h"
 #include "vn_internal.h"
+#include "vn_tc.cuh"
 
 namespace vn {
-
-// Nonzero after a bounded wait of this file ran out (read and cleared by take_dense_status).
-__device__ unsigned int g_dense_status = 0;
 
 namespace {
 
 constexpr int kThreads = 6 * 32;      // single: 4 epilogue warps
 constexpr int kPairThreads = 10 * 32;  // pair: 8, two for each lane quarter, 128 columns each
-constexpr int kK = 64;                          // k of a stage: 128 bytes of bf16, one swizzle atom
-constexpr uint32_t kABytes = 128 * 128;         // 128 rows (or 64 k x 2 blocks of 64 p)
-constexpr uint32_t kBlockBytes = kK * 128;      // one 64-wide block of a p- or q-contiguous operand
 constexpr int kMaxStages = 8;
-constexpr unsigned long long kTimeoutNs = 4000000000ull;
 
-struct Params {
-  const void* bias;
-  const void* residual;
-  void* out;
-  void* preact;
-  int64_t np, nq;
-  int bias_bf16, act;
+struct Params : Epilogue {
+  int64_t nq;
   int p_tiles, q_tiles;
   int bn;  // pair: columns of a tile, a multiple of 16
   int64_t units;
@@ -69,204 +57,6 @@ struct Params {
   uint32_t idesc;
   unsigned long long timeout_ns;
 };
-
-struct Control {
-  int abort;
-  int pad;
-  unsigned long long timeout_ns;
-};
-
-// ---------------------------------------------------------------- PTX
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ uint64_t global_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// The shared::cluster address of `addr` in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float load_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// Bounded wait for the phase of this parity: false when it ran out (status and abort flag are
-// then set) or when another role of the CTA has aborted.
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile Control* c) {
-  const uint64_t t0 = global_ns();
-  const unsigned long long limit = c->timeout_ns;
-  for (uint32_t n = 1;; ++n) {
-    if (mbar_try(bar, parity)) return true;
-    if ((n & 63) == 0) {
-      if (c->abort) return false;
-      if (global_ns() - t0 > limit) {
-        atomicOr(&g_dense_status, 1u);
-        c->abort = 1;
-        return false;
-      }
-    }
-  }
-}
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile Control* c) {
-  return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, c);
-}
-template <bool kPair>
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
-  if constexpr (kPair)
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
-      : "memory");
-}
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(src), "r"(c0), "r"(c1)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int kPending>
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
-}
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-  asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-template <bool kPair>
-__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
-  if constexpr (kPair) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  } else {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-}
-template <bool kPair>
-__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-  if constexpr (kPair)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
-  else
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
-}
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-template <bool kPair>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (kPair)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Arrive on the barrier (of both CTAs of a pair) once every MMA issued so far is complete.
-template <bool kPair>
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  if constexpr (kPair)
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-  else
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-// 32 lanes x 16 consecutive columns: thread t gets lane base + t.
-__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-// Shared-memory descriptor of a 128-byte-swizzled operand. k contiguous: rows of 128 bytes,
-// 8-row groups 1024 bytes apart; the leading offset is unused. p (q) contiguous: a
-// 64-wide block holds one 128-byte row per k, 8-k groups 1024 bytes apart (stride), and
-// the next 64 elements start kBlockBytes on (leading).
-template <bool kMn>
-__device__ __forceinline__ uint64_t descriptor(uint32_t addr) {
-  uint64_t d = static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(kMn ? kBlockBytes >> 4 : 1) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-// Bytes from one MMA's 16 k to the next within a stage.
-template <bool kMn>
-constexpr uint32_t kStepBytes = kMn ? 16 * 128 : 32;
-
-__device__ __forceinline__ float value(float x) { return x; }
-__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T>
-__device__ __forceinline__ T narrow(float x);
-template <>
-__device__ __forceinline__ float narrow<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
-// The planes of A and B in the i-th of the six products: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0).
-__device__ __forceinline__ int plane_a(int i) { return (0b000001010010 >> (2 * i)) & 3; }
-__device__ __forceinline__ int plane_b(int i) { return (0b000100011000 >> (2 * i)) & 3; }
 
 // Tile of a unit: groups of 8 tiles along q, p fastest between them, so that the CTAs at
 // work at one time share few rows of A and of B.
@@ -277,56 +67,6 @@ __device__ __forceinline__ void tile_of(const Params& p, int64_t unit, int* tp, 
   *tp = static_cast<int>(r / rows);
   *tq = static_cast<int>(g * 8 + r % rows);
 }
-
-// Sixteen outputs of one p, columns q .. q + 15 (the first `count` of them), in two steps: the
-// residual's loads, which the caller issues ahead of the sums, and the rest of the epilogue.
-template <typename T>
-struct Residual {
-  T v[16];
-};
-template <typename T>
-__device__ __forceinline__ void load_residual(const Params& p, int64_t q, int64_t pp, int count, Residual<T>* r) {
-  if (p.residual == nullptr || pp >= p.np) return;
-  const T* at = static_cast<const T*>(p.residual) + q * p.np + pp;
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (i < count) r->v[i] = at[i * p.np];
-}
-template <typename T>
-__device__ __forceinline__ void finish(const Params& p, float (&z)[16], const Residual<T>& r, int64_t q, int64_t pp,
-                                       int count, float bias) {
-  const int64_t at = q * p.np + pp;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) z[i] += bias;
-  if (p.preact != nullptr) {
-    T* pre = static_cast<T*>(p.preact) + at;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < count) pre[i * p.np] = narrow<T>(z[i]);
-  }
-  activate_all<sizeof(T) == 2>(p.act, z);
-  if (p.residual != nullptr) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] += value(r.v[i]);
-  }
-  T* out = static_cast<T*>(p.out) + at;
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (i < count) out[i * p.np] = narrow<T>(z[i]);
-}
-__device__ __forceinline__ float bias_of(const Params& p, int64_t pp) {
-  if (p.bias == nullptr || pp >= p.np) return 0.f;
-  return p.bias_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[pp])
-                     : static_cast<const float*>(p.bias)[pp];
-}
-
-struct Ring {
-  int s = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ void next(int n) {
-    if (++s == n) { s = 0; ph ^= 1u; }
-  }
-};
 
 // One stage: A's 128 rows and B's rows of this CTA (one box, or `blocks` 64-wide blocks) of
 // 64 k.
@@ -793,32 +533,7 @@ bool make_result_map(CUtensorMap* map, const void* p, vn_dtype dt, int64_t np, i
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-uint32_t idesc_of(int m, int n, bool a_mn, bool b_mn) {
-  // fp32 accumulator, bf16 operands, transpose bits, N / 8, M / 16
-  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
-         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
-}
-
 constexpr size_t kFixed = 1024 + 8 * (2 * kMaxStages + 14) + sizeof(Control);
-
-template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*fn)(KArgs...), SmemRecord& record, int grid, int threads, int cluster, size_t smem,
-                           cudaStream_t stream, Args... args) {
-  const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(fn), smem, record);
-  if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, args...);
-}
 
 // Columns of a pair's tile: of the multiples of 16 from 128 to 256, the one with the least
 // work on the busiest pair -- rounds of tiles x (columns + 16, for what a tile costs beside its
@@ -890,8 +605,7 @@ cudaError_t run(const TcProduct& d, cudaStream_t stream) {
   p.k_chunks = static_cast<int>((d.nk + kK - 1) / kK);
   p.iters = p.k_chunks * (d.a.planes == 3 ? 6 : 1);
   p.timeout_ns = kTimeoutNs;
-  const int64_t pairs = ((d.np + 255) / 256) * ((d.nq + 255) / 256);
-  if (pairs * 2 >= dev.sm_count / 2) return run_pair<T, kAMn, kBMn>(d, p, dev.sm_count, stream);
+  if (fills_pairs(d.np, d.nq)) return run_pair<T, kAMn, kBMn>(d, p, dev.sm_count, stream);
   // Columns a tile: all of q in one tile where 256 suffice, so that A is staged once; then as
   // many CTAs on the k loop as leave each two stages and still fit the GPU at once.
   const int64_t p_tiles = (d.np + 127) / 128;
@@ -919,14 +633,6 @@ cudaError_t launch_tc_product(const TcProduct& d, cudaStream_t stream) {
   return d.dt == VN_BF16 ? run_layout<__nv_bfloat16>(d, stream) : run_layout<float>(d, stream);
 }
 
-cudaError_t take_dense_status(unsigned int* status, cudaStream_t stream) {
-  cudaError_t err =
-      cudaMemcpyFromSymbolAsync(status, g_dense_status, sizeof(unsigned int), 0, cudaMemcpyDeviceToHost, stream);
-  if (err != cudaSuccess) return err;
-  if ((err = cudaStreamSynchronize(stream)) != cudaSuccess || *status == 0) return err;
-  const unsigned int zero = 0;
-  err = cudaMemcpyToSymbolAsync(g_dense_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream);
-  return err == cudaSuccess ? cudaStreamSynchronize(stream) : err;
-}
+cudaError_t take_dense_status(unsigned int* status, cudaStream_t stream) { return take_wait_status(status, stream); }
 
 }  // namespace vn
