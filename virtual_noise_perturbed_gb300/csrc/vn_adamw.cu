@@ -102,6 +102,12 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // The scale of a block whose largest magnitude has these bits, and the factor that takes
 // values to its units.
 __device__ __forceinline__ float block_scale(uint32_t top_bits, float* inv) {
@@ -174,7 +180,7 @@ __device__ __forceinline__ void step_block(const Table<kCap>& t, const Entry& e,
       const float m = __fadd_rn(__fmul_rn(mv[h][q], t.b1), __fmul_rn(g, t.c1));
       const float v = __fadd_rn(__fmul_rn(vv[h][q], t.b2), __fmul_rn(__fmul_rn(g, g), t.c2));
       const float root = __fsqrt_rn(v);
-      const float move = __fmul_rn(m / fmaf(root, t.inv_root, t.eps), t.size);
+      const float move = __fmul_rn(__fdividef(m, fmaf(root, t.inv_root, t.eps)), t.size);
       pv[h][q] = fmaf(pv[h][q], e.keep, -move);
       mv[h][q] = m;
       vv[h][q] = k8 ? root : v;
@@ -197,18 +203,16 @@ __device__ __forceinline__ void step_block(const Table<kCap>& t, const Entry& e,
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float mq[4], rq[4];
-      bool pos[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        mq[q] = ms == 0.f ? 0.f : __fmul_rn(mv[h][q], minv);
-        rq[q] = vs == 0.f ? 0.f : __fmul_rn(vv[h][q], rinv);
-        pos[q] = vv[h][q] > 0.f && vs > 0.f;
+        mq[q] = __fmul_rn(mv[h][q], minv);  // a block stored as zeros has factor 0
+        rq[q] = __fmul_rn(vv[h][q], rinv);
+        // A positive root takes code 1, 2^-9, at least (a NaN stays one).
+        const float least = max_nan(rq[q], 0x1p-9f);
+        rq[q] = vv[h][q] > 0.f && vs > 0.f ? least : rq[q];
       }
       const uint32_t mo = encode4(mq);
-      uint32_t ro = encode4(rq);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)  // code 1 is 2^-9, the smallest
-        if (pos[q] && ((ro >> (8 * q)) & 0xFFu) == 0u) ro |= 1u << (8 * q);
+      const uint32_t ro = encode4(rq);
       uint8_t* mp = static_cast<uint8_t*>(e.m) + base;
       uint8_t* vp = static_cast<uint8_t*>(e.v) + base;
       if constexpr (kVec) {

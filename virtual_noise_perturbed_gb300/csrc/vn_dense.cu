@@ -256,6 +256,7 @@ bool as_is(vn_dtype dt, int64_t cols, bool aligned) { return dt == VN_BF16 && co
 
 // How a layer, or its gradients, are computed.
 enum class Route {
+  kRows,    // up to 8 rows: vn_dense_rows.cu
   kPlain,   // 64 x 64 tiles without tensor cores: sizes beyond 32-bit coordinates
   kGather,  // one launch, operands gathered by threads: results of few tiles
   kTiles,   // operands by TMA, in bf16 (converted where they are not): vn_dense_tc.cu
@@ -265,6 +266,7 @@ bool fits32(int64_t rows, int64_t in, int64_t out) {
   return rows <= most && in <= most && out <= most;
 }
 Route forward_route(int64_t rows, int64_t in, int64_t out, vn_dtype dt, bool aligned) {
+  if (rows <= 8) return Route::kRows;
   if (!fits32(rows, in, out)) return Route::kPlain;
   if (in > 0 && (fills_pairs(out, rows) || as_is(dt, in, aligned))) return Route::kTiles;
   return Route::kGather;
@@ -325,6 +327,7 @@ int64_t dense_backward_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype
 cudaError_t launch_dense(const DenseArgs& a, cudaStream_t stream) {
   const bool al = aligned16(a.x) && aligned16(a.w);
   const Route route = forward_route(a.rows, a.in, a.out, a.dt, al);
+  if (route == Route::kRows) return launch_rows_forward(a, stream);
   if (route == Route::kGather) return launch_gather_forward(a, stream);
   if (route == Route::kTiles) {
     uint8_t* work = static_cast<uint8_t*>(a.workspace);

@@ -45,6 +45,7 @@ inline bool fills_pairs(int64_t np, int64_t nq) {
 // grad_w; rows, in and out from 1 to 2^31 - 512.
 struct DenseArgs;
 struct DenseGradArgs;
+cudaError_t launch_rows_forward(const DenseArgs& a, cudaStream_t stream);  // rows <= 8 (vn_dense_rows.cu)
 cudaError_t launch_gather_forward(const DenseArgs& a, cudaStream_t stream);
 cudaError_t launch_gather_backward(const DenseGradArgs& a, cudaStream_t stream);
 cudaError_t take_gather_status(unsigned int* status, cudaStream_t stream);

@@ -255,20 +255,35 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_grad_kernel(const NormGra
     for (int q = 0; q < V; ++q) w[j][q] = dw[j][q] = db[j][q] = 0.f;
     if (i < n) load_param<V>(a.w, a.w_bf16, i, 1.f, w[j]);
   }
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group; row < a.rows;
-       row += static_cast<int64_t>(gridDim.x) * kRows) {
-    const X* g = static_cast<const X*>(a.g) + row * a.n;
-    const X* x = static_cast<const X*>(a.x) + row * a.n;
-    Pack<X, V> gv[NV], xv[NV];
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group;
+  // The next row's loads are issued before this row's arithmetic.
+  Pack<X, V> gn[NV], xn[NV];
+  float mean_n = 0.f, rstd_n = 0.f;
+  auto fetch = [&](int64_t r) {
+    const X* g = static_cast<const X*>(a.g) + r * a.n;
+    const X* x = static_cast<const X*>(a.x) + r * a.n;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = (j * T + t) * V;
       if (i < n) {
-        gv[j] = load_pack<X, V>(g + i);
-        xv[j] = load_pack<X, V>(x + i);
+        gn[j] = load_pack<X, V>(g + i);
+        xn[j] = load_pack<X, V>(x + i);
       }
     }
-    const float mean = a.mean[row], rstd = a.rstd[row];
+    mean_n = a.mean[r];
+    rstd_n = a.rstd[r];
+  };
+  if (row < a.rows) fetch(row);
+  for (; row < a.rows; row += stride) {
+    Pack<X, V> gv[NV], xv[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      gv[j] = gn[j];
+      xv[j] = xn[j];
+    }
+    const float mean = mean_n, rstd = rstd_n;
+    if (row + stride < a.rows) fetch(row + stride);
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -379,24 +394,25 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormGradK a) {
 }
 
 // out[c] = sum over parts, in order, of part[p][c], c < n; a second output takes columns
-// n .. 2n-1. 32 columns a CTA; warp k adds every 8th part from k, then the warps' sums.
-__global__ void __launch_bounds__(256)
+// n .. 2n-1. 32 columns a CTA; warp k adds every 16th part from k, then the warps' sums.
+constexpr int kSumWarps = 16;
+__global__ void __launch_bounds__(kSumWarps * 32)
 column_sum_kernel(const float* __restrict__ part, int64_t parts, int64_t width, int64_t n, void* o1, void* o2,
                   int bf16) {
-  __shared__ float s[8][32];
+  __shared__ float s[kSumWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float v = 0.f;
   if (c < width) {
-#pragma unroll 4
-    for (int64_t p = warp; p < parts; p += 8) v += part[p * width + c];
+#pragma unroll 8
+    for (int64_t p = warp; p < parts; p += kSumWarps) v += part[p * width + c];
   }
   s[warp][lane] = v;
   __syncthreads();
   if (warp == 0 && c < width) {
     v = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v += s[k][lane];
+    for (int k = 0; k < kSumWarps; ++k) v += s[k][lane];
     void* o = c < n ? o1 : o2;
     const int64_t i = c < n ? c : c - n;
     if (o != nullptr) {
@@ -454,25 +470,25 @@ cudaError_t run_norm_grad(const NormGradK& a, int64_t parts, cudaStream_t stream
 
 template <typename X, int V>
 cudaError_t norm_grad_by_length(const NormGradK& a, int64_t* parts, cudaStream_t stream) {
-  // Up to 16 elements a thread: three fp32 registers for each (weight and both sums) and the row itself.
-  constexpr int kNv = 16 / V;
-  auto ctas = [&](int t) {
+  // Elements of a thread: each takes three fp32 registers (weight and both sums) besides the rows
+  // at work. 16 with 16-byte loads; 8 with single ones, for more loads in flight an SM.
+  constexpr int kNv = V > 1 ? 16 / V : 8;
+  auto ctas = [&](int t) {  // as many as are resident at once: 512 threads an SM
     const int64_t rows = cta_threads(t) / t;
-    return std::max<int64_t>(1, std::min<int64_t>(kMaxParts, (a.rows + rows - 1) / rows));
+    return std::max<int64_t>(1, std::min<int64_t>(kMaxParts * 128 / cta_threads(t), (a.rows + rows - 1) / rows));
   };
-  if (a.n <= 32 * 16) {
+  const int64_t per = kNv * V;
+  if (a.n <= 32 * per) {
     *parts = ctas(32);
-    if constexpr (V > 1) {
-      if (a.n <= 32 * V) return run_norm_grad<X, 32, V, 1>(a, *parts, stream);
-      return run_norm_grad<X, 32, V, kNv>(a, *parts, stream);
-    } else {
-      if (a.n <= 32 * 4) return run_norm_grad<X, 32, V, 4>(a, *parts, stream);
-      return run_norm_grad<X, 32, V, kNv>(a, *parts, stream);
-    }
+    if (a.n <= 32 * per / 2) return run_norm_grad<X, 32, V, kNv / 2>(a, *parts, stream);
+    return run_norm_grad<X, 32, V, kNv>(a, *parts, stream);
   }
-  if (a.n <= 128 * 16) { *parts = ctas(128); return run_norm_grad<X, 128, V, kNv>(a, *parts, stream); }
-  if (a.n <= 256 * 16) { *parts = ctas(256); return run_norm_grad<X, 256, V, kNv>(a, *parts, stream); }
-  if (a.n <= 512 * 16) { *parts = ctas(512); return run_norm_grad<X, 512, V, kNv>(a, *parts, stream); }
+  if (a.n <= 128 * per) { *parts = ctas(128); return run_norm_grad<X, 128, V, kNv>(a, *parts, stream); }
+  if (a.n <= 256 * per) { *parts = ctas(256); return run_norm_grad<X, 256, V, kNv>(a, *parts, stream); }
+  if (a.n <= 512 * per) { *parts = ctas(512); return run_norm_grad<X, 512, V, kNv>(a, *parts, stream); }
+  if constexpr (V == 1) {
+    if (a.n <= 512 * 16) { *parts = ctas(512); return run_norm_grad<X, 512, V, 16>(a, *parts, stream); }
+  }
   if (a.rows > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   norm_grad_long_kernel<X><<<static_cast<unsigned>(a.rows), 512, 0, stream>>>(a);
   cudaError_t err = cudaGetLastError();
@@ -507,7 +523,7 @@ cudaError_t launch_column_sum(const float* part, int64_t parts, int64_t width, i
                                  vn_dtype dt, cudaStream_t stream) {
   const int64_t grid = (width + 31) / 32;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  column_sum_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(part, parts, width, n, o1, o2, dt == VN_BF16);
+  column_sum_kernel<<<static_cast<unsigned>(grid), kSumWarps * 32, 0, stream>>>(part, parts, width, n, o1, o2, dt == VN_BF16);
   return cudaGetLastError();
 }
 
