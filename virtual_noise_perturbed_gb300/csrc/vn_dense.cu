@@ -205,17 +205,30 @@ __global__ void __launch_bounds__(256) delta_kernel(const Delta a) {
   const T* z = static_cast<const T*>(a.z);
   float sum[8] = {};
   if (count > 0) {
-    for (int64_t r = static_cast<int64_t>(blockIdx.y) * 8 + warp; r < a.rows; r += static_cast<int64_t>(gridDim.y) * 8) {
-      float v[8];
-      load8(g + r * a.n + c, count, a.vec_in != 0, v);
-      if (a.act != VN_ACT_NONE) {
-        float u[8];
-        load8(z + r * a.n + c, count, a.vec_in != 0, u);
-        slope_all<sizeof(T) == 2>(a.act, u, v);
-      }
-      if (a.d != nullptr) store8<T, kPlanes>(a.d, r * a.pitch + c, a.plane, v, count, a.vec_out != 0);
+    // Four rows at a time, their loads before the first use.
+    const int64_t step = static_cast<int64_t>(gridDim.y) * 8;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * 8 + warp; r0 < a.rows; r0 += 4 * step) {
+      float v[4][8], u[4][8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) sum[q] += v[q];
+      for (int i = 0; i < 4; ++i) {
+        const int64_t r = r0 + i * step;
+        const int have = r < a.rows ? count : 0;
+        if (have > 0 || a.vec_in == 0) {
+          load8(g + r * a.n + c, have, a.vec_in != 0, v[i]);
+          if (a.act != VN_ACT_NONE) load8(z + r * a.n + c, have, a.vec_in != 0, u[i]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[i][q] = u[i][q] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t r = r0 + i * step;
+        if (a.act != VN_ACT_NONE) slope_all<sizeof(T) == 2>(a.act, u[i], v[i]);
+        if (a.d != nullptr && r < a.rows) store8<T, kPlanes>(a.d, r * a.pitch + c, a.plane, v[i], count, a.vec_out != 0);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum[q] += v[i][q];
+      }
     }
   }
   if (a.part == nullptr) return;

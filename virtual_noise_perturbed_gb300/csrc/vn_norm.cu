@@ -98,30 +98,108 @@ __device__ __forceinline__ void load_param(const void* w, int bf16, int64_t i, f
   }
 }
 
-// Sums of N numbers over the T threads of a row (a warp, or the whole CTA), the same
-// in every thread. `scratch`: N * 32 floats, used by every other call (`turn`).
-template <int T, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float* scratch, int& turn) {
+// Sums over the T threads of a row (a warp, or the whole CTA), the same in every thread.
+// `scratch`: 64 floats for one sum, 128 for two, halves of which calls use in turn.
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float* scratch, int& turn) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   if constexpr (T > 32) {
     constexpr int kW = T / 32;
-    float* s = scratch + (turn & 1) * (N * 32);
-    ++turn;
+    float* s = scratch + (turn++ & 1) * 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0)
-#pragma unroll
-      for (int k = 0; k < N; ++k) s[k * 32 + warp] = v[k];
+    if (lane == 0) s[warp] = v;
     __syncthreads();
+    v = s[lane % kW];
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      v[k] = lane < kW ? s[k * 32 + lane] : 0.f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
-    }
+    for (int o = kW / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   }
+  return v;
+}
+// Two sums: the first step leaves each half of a warp with one of them.
+template <int T>
+__device__ __forceinline__ void row_sum2(float& v0, float& v1, float* scratch, int& turn) {
+  const int lane = threadIdx.x & 31;
+  const bool upper = lane >= 16;
+  float v = (upper ? v1 : v0) + __shfl_xor_sync(0xFFFFFFFFu, upper ? v0 : v1, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if constexpr (T > 32) {
+    constexpr int kW = T / 32;
+    static_assert(kW <= 16, "a half-warp takes a sum's partial sums");
+    float* s = scratch + (turn++ & 1) * 64 + (upper ? 32 : 0);
+    if ((lane & 15) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = s[lane % kW];
+#pragma unroll
+    for (int o = kW / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  }
+  v0 = __shfl_sync(0xFFFFFFFFu, v, 0);
+  v1 = __shfl_sync(0xFFFFFFFFu, v, 16);
+}
+
+// Two fp32 values in one register pair, and the two-lane instructions on them (each lane rounds as
+// the single instruction does). The norm's kernels are close to the issue limit: one of these does
+// the work of two.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void split(F2 v, float* a, float* b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float sum_of(F2 v) {
+  float a, b;
+  split(v, &a, &b);
+  return a + b;
+}
+// A 16-byte pack as pairs of fp32: 4 of bf16, 2 of fp32.
+template <typename X>
+constexpr int kPairs = 8 / sizeof(X);
+template <typename X>
+__device__ __forceinline__ void pairs_of(const uint4& p, F2 (&v)[kPairs<X>]) {
+  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+  if constexpr (sizeof(X) == 2) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = f2(__uint_as_float(w[q] << 16), __uint_as_float(w[q] & 0xFFFF0000u));
+  } else {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) v[q] = f2(__uint_as_float(w[2 * q]), __uint_as_float(w[2 * q + 1]));
+  }
+}
+template <typename X>
+__device__ __forceinline__ void store_pairs(X* p, const F2 (&v)[kPairs<X>]) {
+  float o[16 / sizeof(X)];
+#pragma unroll
+  for (int q = 0; q < kPairs<X>; ++q) split(v[q], &o[2 * q], &o[2 * q + 1]);
+  store_pack<X, 16 / sizeof(X)>(p, o);
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest `pending` groups of copies are complete.
+__device__ __forceinline__ void wait_copies(int pending) {
+  if (pending == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (pending == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else asm volatile("cp.async.wait_group 1;" ::: "memory");
 }
 
 struct NormArgsK {
@@ -154,25 +232,23 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_kernel(const NormArgsK a)
     const int i = (j * T + t) * V;
     if (i < n) v[j] = load_pack<X, V>(x + i);
   }
-  float s[1] = {0.f};
+  float s = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
     if ((j * T + t) * V < n)
 #pragma unroll
-      for (int q = 0; q < V; ++q) s[0] += value(v[j].e[q]);
-  row_sum<T, 1>(s, scratch, turn);
-  const float mean = s[0] * a.inv_n;
-  s[0] = 0.f;
+      for (int q = 0; q < V; ++q) s += value(v[j].e[q]);
+  const float mean = row_sum<T>(s, scratch, turn) * a.inv_n;
+  s = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
     if ((j * T + t) * V < n)
 #pragma unroll
       for (int q = 0; q < V; ++q) {
         const float c = value(v[j].e[q]) - mean;
-        s[0] = fmaf(c, c, s[0]);
+        s = fmaf(c, c, s);
       }
-  row_sum<T, 1>(s, scratch, turn);
-  const float rstd = 1.f / sqrtf(s[0] * a.inv_n + a.eps);
+  const float rstd = 1.f / sqrtf(row_sum<T>(s, scratch, turn) * a.inv_n + a.eps);
   X* y = static_cast<X*>(a.y) + row * a.n;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -192,6 +268,95 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_kernel(const NormArgsK a)
   }
 }
 
+// The same for longer rows of 16-byte packs: CTAs that stay, weight and bias in registers, and the
+// next rows on their way through shared memory. Each thread copies its own packs into its own
+// places (cp.async) and reads them back itself, so the ring needs no barrier of its own.
+template <typename X, int T, int NV>
+__global__ void __launch_bounds__(T) norm_ring_kernel(const NormArgsK a, const int depth) {
+  constexpr int V = 16 / sizeof(X), P = kPairs<X>;
+  extern __shared__ uint4 ring[];  // [depth][NV][T]
+  __shared__ float scratch[64];
+  int turn = 0;
+  const int t = threadIdx.x;
+  const int n = static_cast<int>(a.n);
+  F2 w[NV][P], b[NV][P];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = (j * T + t) * V;
+    float u[V] = {}, v[V] = {};
+    if (i < n) {
+      load_param<V>(a.w, a.w_bf16, i, 1.f, u);
+      load_param<V>(a.b, a.w_bf16, i, 0.f, v);
+    }
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      w[j][q] = f2(u[2 * q], u[2 * q + 1]);
+      b[j][q] = f2(v[2 * q], v[2 * q + 1]);
+    }
+  }
+  uint4* const mine = ring + t;
+  const int64_t stride = gridDim.x;
+  auto fetch = [&](int64_t row, int slot) {  // one group of copies, empty beyond the last row
+    if (row < a.rows) {
+      const X* x = static_cast<const X*>(a.x) + row * a.n;
+      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(mine + slot * (NV * T)));
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int i = (j * T + t) * V;
+        if (i < n) copy16(to + j * (T * 16), x + i);
+      }
+    }
+    commit_copies();
+  };
+  int64_t row = blockIdx.x;
+  for (int d = 0; d < depth - 1; ++d) fetch(row + d * stride, d);
+  int slot = 0;
+  for (; row < a.rows; row += stride) {
+    fetch(row + (depth - 1) * stride, slot == 0 ? depth - 1 : slot - 1);
+    wait_copies(depth - 1);
+    const uint4* const from = mine + slot * (NV * T);
+    slot = slot + 1 == depth ? 0 : slot + 1;
+    F2 x[NV][P];
+    F2 s2 = f2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if ((j * T + t) * V < n) {
+        pairs_of<X>(from[j * T], x[j]);
+#pragma unroll
+        for (int q = 0; q < P; ++q) s2 = add2(s2, x[j][q]);
+      }
+    const float mean = row_sum<T>(sum_of(s2), scratch, turn) * a.inv_n;
+    const F2 minus = f2(-mean, -mean);
+    s2 = f2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if ((j * T + t) * V < n) {
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+          x[j][q] = add2(x[j][q], minus);
+          s2 = fma2(x[j][q], x[j][q], s2);
+        }
+      }
+    const float rstd = 1.f / sqrtf(row_sum<T>(sum_of(s2), scratch, turn) * a.inv_n + a.eps);
+    const F2 r2 = f2(rstd, rstd);
+    X* y = static_cast<X*>(a.y) + row * a.n;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = (j * T + t) * V;
+      if (i < n) {
+        F2 o[P];
+#pragma unroll
+        for (int q = 0; q < P; ++q) o[q] = fma2(mul2(x[j][q], r2), w[j][q], b[j][q]);
+        store_pairs<X>(y + i, o);
+      }
+    }
+    if (t == 0) {
+      if (a.mean != nullptr) a.mean[row] = mean;
+      if (a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+  }
+}
+
 // Rows longer than the registers hold: three passes over the row (the second and third
 // mostly from L2).
 template <typename X>
@@ -201,17 +366,15 @@ __global__ void __launch_bounds__(512) norm_long_kernel(const NormArgsK a) {
   const int64_t row = blockIdx.x;
   const X* x = static_cast<const X*>(a.x) + row * a.n;
   X* y = static_cast<X*>(a.y) + row * a.n;
-  float s[1] = {0.f};
-  for (int64_t i = threadIdx.x; i < a.n; i += 512) s[0] += value(x[i]);
-  row_sum<512, 1>(s, scratch, turn);
-  const float mean = s[0] * a.inv_n;
-  s[0] = 0.f;
+  float s = 0.f;
+  for (int64_t i = threadIdx.x; i < a.n; i += 512) s += value(x[i]);
+  const float mean = row_sum<512>(s, scratch, turn) * a.inv_n;
+  s = 0.f;
   for (int64_t i = threadIdx.x; i < a.n; i += 512) {
     const float c = value(x[i]) - mean;
-    s[0] = fmaf(c, c, s[0]);
+    s = fmaf(c, c, s);
   }
-  row_sum<512, 1>(s, scratch, turn);
-  const float rstd = 1.f / sqrtf(s[0] * a.inv_n + a.eps);
+  const float rstd = 1.f / sqrtf(row_sum<512>(s, scratch, turn) * a.inv_n + a.eps);
   for (int64_t i = threadIdx.x; i < a.n; i += 512) {
     float w[1], b[1];
     load_param<1>(a.w, a.w_bf16, i, 1.f, w);
@@ -297,7 +460,7 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_grad_kernel(const NormGra
           dw[j][q] = fmaf(d, h, dw[j][q]);
           db[j][q] += d;
         }
-    row_sum<T, 2>(s, scratch, turn);
+    row_sum2<T>(s[0], s[1], scratch, turn);
     const float m1 = s[0] * a.inv_n, m2 = s[1] * a.inv_n;
     X* dx = static_cast<X*>(a.dx) + row * a.n;
 #pragma unroll
@@ -348,6 +511,123 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_grad_kernel(const NormGra
   }
 }
 
+// The same for longer rows of 16-byte packs, on the ring of the forward kernel: with
+// straight loads of one row ahead 32 KB an SM were on their way, 4 TB/s; and on pairs: 35
+// instructions an element were the next bound (193 us on 32768 x 4096 bf16).
+template <typename X, int T, int NV>
+__global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, const int depth) {
+  constexpr int V = 16 / sizeof(X), P = kPairs<X>;
+  extern __shared__ uint4 ring[];  // [depth][2][NV][T]
+  __shared__ float scratch[128];
+  int turn = 0;
+  const int t = threadIdx.x;
+  const int n = static_cast<int>(a.n);
+  F2 w[NV][P], dw[NV][P], db[NV][P];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = (j * T + t) * V;
+    float u[V] = {};
+    if (i < n) load_param<V>(a.w, a.w_bf16, i, 1.f, u);
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      w[j][q] = f2(u[2 * q], u[2 * q + 1]);
+      dw[j][q] = db[j][q] = f2(0.f, 0.f);
+    }
+  }
+  uint4* const mine = ring + t;
+  const int64_t stride = gridDim.x;
+  auto fetch = [&](int64_t row, int slot) {  // one group of copies, empty beyond the last row
+    if (row < a.rows) {
+      const X* g = static_cast<const X*>(a.g) + row * a.n;
+      const X* x = static_cast<const X*>(a.x) + row * a.n;
+      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(mine + slot * (2 * NV * T)));
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int i = (j * T + t) * V;
+        if (i < n) {
+          copy16(to + j * (T * 16), g + i);
+          copy16(to + (NV + j) * (T * 16), x + i);
+        }
+      }
+    }
+    commit_copies();
+  };
+  int64_t row = blockIdx.x;
+  for (int d = 0; d < depth - 1; ++d) fetch(row + d * stride, d);
+  int slot = 0;
+  float mean_n = 0.f, rstd_n = 0.f;  // the next row's, a row ahead
+  if (row < a.rows) {
+    mean_n = a.mean[row];
+    rstd_n = a.rstd[row];
+  }
+  for (; row < a.rows; row += stride) {
+    const float mean = mean_n, rstd = rstd_n;
+    if (row + stride < a.rows) {
+      mean_n = a.mean[row + stride];
+      rstd_n = a.rstd[row + stride];
+    }
+    fetch(row + (depth - 1) * stride, slot == 0 ? depth - 1 : slot - 1);
+    wait_copies(depth - 1);
+    const uint4* const from = mine + slot * (2 * NV * T);
+    slot = slot + 1 == depth ? 0 : slot + 1;
+    // h = (x - mean) rstd; in bf16, whose x is coarser than the rounding of mean rstd, as one
+    // multiply-add.
+    const F2 r2 = f2(rstd, rstd);
+    const F2 shift = sizeof(X) == 2 ? f2(-mean * rstd, -mean * rstd) : f2(-mean, -mean);
+    F2 g[NV][P], h[NV][P];
+    F2 s1 = f2(0.f, 0.f), s2 = f2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if ((j * T + t) * V < n) {
+        pairs_of<X>(from[j * T], g[j]);
+        pairs_of<X>(from[(NV + j) * T], h[j]);
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+          h[j][q] = sizeof(X) == 2 ? fma2(h[j][q], r2, shift) : mul2(add2(h[j][q], shift), r2);
+          db[j][q] = add2(db[j][q], g[j][q]);
+          const F2 gh = mul2(g[j][q], h[j][q]);
+          dw[j][q] = add2(dw[j][q], gh);
+          s2 = fma2(gh, w[j][q], s2);
+          g[j][q] = mul2(g[j][q], w[j][q]);
+          s1 = add2(s1, g[j][q]);
+        }
+      }
+    float m1 = sum_of(s1), m2 = sum_of(s2);
+    row_sum2<T>(m1, m2, scratch, turn);
+    // rstd (g w - m1 - h m2)
+    const F2 c1 = f2(-m1 * a.inv_n, -m1 * a.inv_n), c2 = f2(-m2 * a.inv_n, -m2 * a.inv_n);
+    X* dx = static_cast<X*>(a.dx) + row * a.n;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = (j * T + t) * V;
+      if (i < n) {
+        F2 o[P];
+#pragma unroll
+        for (int q = 0; q < P; ++q) o[q] = mul2(fma2(h[j][q], c2, add2(g[j][q], c1)), r2);
+        store_pairs<X>(dx + i, o);
+      }
+    }
+  }
+  if (a.part == nullptr) return;
+  float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.n;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = (j * T + t) * V;
+    if (i < n) {
+#pragma unroll
+      for (int q = 0; q < P; q += 2) {
+        float4 u, v;
+        split(dw[j][q], &u.x, &u.y);
+        split(dw[j][q + 1], &u.z, &u.w);
+        split(db[j][q], &v.x, &v.y);
+        split(db[j][q + 1], &v.z, &v.w);
+        *reinterpret_cast<float4*>(out + i + 2 * q) = u;
+        *reinterpret_cast<float4*>(out + a.n + i + 2 * q) = v;
+      }
+    }
+  }
+}
+
 // Long rows: grad_x in two passes over the row ...
 template <typename X>
 __global__ void __launch_bounds__(512) norm_grad_long_kernel(const NormGradK a) {
@@ -366,7 +646,7 @@ __global__ void __launch_bounds__(512) norm_grad_long_kernel(const NormGradK a) 
     s[0] += u;
     s[1] = fmaf(u, (value(x[i]) - mean) * rstd, s[1]);
   }
-  row_sum<512, 2>(s, scratch, turn);
+  row_sum2<512>(s[0], s[1], scratch, turn);
   const float m1 = s[0] * a.inv_n, m2 = s[1] * a.inv_n;
   for (int64_t i = threadIdx.x; i < a.n; i += 512) {
     float w[1];
@@ -433,10 +713,35 @@ cudaError_t run_norm(const NormArgsK& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+// Rows on their way at once: as many as fit 64 KB of shared memory, 2 to 4.
+constexpr int ring_depth(size_t row) { return row * 4 <= 65536 ? 4 : row * 3 <= 65536 ? 3 : 2; }
+
+// ctas: as many as are resident at once.
+template <typename X, int T, int NV>
+cudaError_t run_norm_ring(const NormArgsK& a, int64_t ctas, cudaStream_t stream) {
+  constexpr int kDepth = ring_depth(NV * T * sizeof(uint4));
+  constexpr size_t kSmem = NV * T * sizeof(uint4) * kDepth;
+  static SmemRecord record;
+  const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(norm_ring_kernel<X, T, NV>), kSmem, record);
+  if (err != cudaSuccess) return err;
+  norm_ring_kernel<X, T, NV><<<static_cast<unsigned>(std::min(a.rows, ctas)), T, kSmem, stream>>>(a, kDepth);
+  return cudaGetLastError();
+}
+
 // The threads of a row by its number of packs: a warp while its 8 packs a lane suffice
-// (no barrier), then 128 and 512 threads.
+// (no barrier), then 128 to 512 threads.
 template <typename X, int V>
 cudaError_t norm_by_length(const NormArgsK& a, cudaStream_t stream) {
+  if constexpr (V > 1) {
+    if (a.n > 256 * V && a.n <= 512 * 2 * V) {
+      DeviceInfo dev;
+      const cudaError_t err = device_info(&dev);
+      if (err != cudaSuccess) return err;
+      // 1,024 threads an SM
+      if (a.n <= 256 * 2 * V) return run_norm_ring<X, 256, 2>(a, 4 * dev.sm_count, stream);
+      return run_norm_ring<X, 512, 2>(a, 2 * dev.sm_count, stream);
+    }
+  }
   const int64_t packs = (a.n + V - 1) / V;
   if (packs <= 32) return run_norm<X, 32, V, 1>(a, stream);
   if (packs <= 64) return run_norm<X, 32, V, 2>(a, stream);
@@ -468,6 +773,18 @@ cudaError_t run_norm_grad(const NormGradK& a, int64_t parts, cudaStream_t stream
   return cudaGetLastError();
 }
 
+template <typename X, int T, int NV>
+cudaError_t run_norm_grad_ring(const NormGradK& a, int64_t parts, cudaStream_t stream) {
+  constexpr int kDepth = ring_depth(2 * NV * T * sizeof(uint4));
+  constexpr size_t kSmem = 2 * NV * T * sizeof(uint4) * kDepth;
+  static SmemRecord record;
+  const cudaError_t err =
+      ensure_dynamic_smem(reinterpret_cast<const void*>(norm_grad_ring_kernel<X, T, NV>), kSmem, record);
+  if (err != cudaSuccess) return err;
+  norm_grad_ring_kernel<X, T, NV><<<static_cast<unsigned>(parts), T, kSmem, stream>>>(a, kDepth);
+  return cudaGetLastError();
+}
+
 template <typename X, int V>
 cudaError_t norm_grad_by_length(const NormGradK& a, int64_t* parts, cudaStream_t stream) {
   // Elements of a thread: each takes three fp32 registers (weight and both sums) besides the rows
@@ -483,10 +800,14 @@ cudaError_t norm_grad_by_length(const NormGradK& a, int64_t* parts, cudaStream_t
     if (a.n <= 32 * per / 2) return run_norm_grad<X, 32, V, kNv / 2>(a, *parts, stream);
     return run_norm_grad<X, 32, V, kNv>(a, *parts, stream);
   }
-  if (a.n <= 128 * per) { *parts = ctas(128); return run_norm_grad<X, 128, V, kNv>(a, *parts, stream); }
-  if (a.n <= 256 * per) { *parts = ctas(256); return run_norm_grad<X, 256, V, kNv>(a, *parts, stream); }
-  if (a.n <= 512 * per) { *parts = ctas(512); return run_norm_grad<X, 512, V, kNv>(a, *parts, stream); }
-  if constexpr (V == 1) {
+  if constexpr (V > 1) {
+    if (a.n <= 128 * per) { *parts = ctas(128); return run_norm_grad_ring<X, 128, kNv>(a, *parts, stream); }
+    if (a.n <= 256 * per) { *parts = ctas(256); return run_norm_grad_ring<X, 256, kNv>(a, *parts, stream); }
+    if (a.n <= 512 * per) { *parts = ctas(512); return run_norm_grad_ring<X, 512, kNv>(a, *parts, stream); }
+  } else {
+    if (a.n <= 128 * per) { *parts = ctas(128); return run_norm_grad<X, 128, V, kNv>(a, *parts, stream); }
+    if (a.n <= 256 * per) { *parts = ctas(256); return run_norm_grad<X, 256, V, kNv>(a, *parts, stream); }
+    if (a.n <= 512 * per) { *parts = ctas(512); return run_norm_grad<X, 512, V, kNv>(a, *parts, stream); }
     if (a.n <= 512 * 16) { *parts = ctas(512); return run_norm_grad<X, 512, V, 16>(a, *parts, stream); }
   }
   if (a.rows > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
