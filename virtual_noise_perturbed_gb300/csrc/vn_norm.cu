@@ -197,7 +197,8 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the newest `pending` groups of copies are complete.
 __device__ __forceinline__ void wait_copies(int pending) {
-  if (pending == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  if (pending == 4) asm volatile("cp.async.wait_group 4;" ::: "memory");
+  else if (pending == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
   else if (pending == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
   else asm volatile("cp.async.wait_group 1;" ::: "memory");
 }
@@ -519,7 +520,6 @@ __global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, co
   constexpr int V = 16 / sizeof(X), P = kPairs<X>;
   extern __shared__ uint4 ring[];  // [depth][2][NV][T]
   __shared__ float scratch[128];
-  int turn = 0;
   const int t = threadIdx.x;
   const int n = static_cast<int>(a.n);
   F2 w[NV][P], dw[NV][P], db[NV][P];
@@ -552,61 +552,92 @@ __global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, co
     }
     commit_copies();
   };
-  int64_t row = blockIdx.x;
-  for (int d = 0; d < depth - 1; ++d) fetch(row + d * stride, d);
-  int slot = 0;
-  float mean_n = 0.f, rstd_n = 0.f;  // the next row's, a row ahead
-  if (row < a.rows) {
-    mean_n = a.mean[row];
-    rstd_n = a.rstd[row];
+  // Row k's sums and row k - 1's outputs share an iteration, with one barrier at its end: the
+  // reduction's latency is covered by the other row's arithmetic (in sequence, a row of 4096
+  // took a CTA 1.7 us, 0.9 of it waiting). Row k - 1 is read a second time from the ring.
+  const int64_t first = blockIdx.x;
+  const int64_t count = first < a.rows ? (a.rows - first + stride - 1) / stride : 0;
+  for (int d = 0; d < depth - 1; ++d) fetch(first + d * stride, d);
+  float mean = 0.f, rstd = 0.f, mean_n = 0.f, rstd_n = 0.f;  // row k's, and row k + 1's
+  if (count > 0) {
+    mean_n = a.mean[first];
+    rstd_n = a.rstd[first];
   }
-  for (; row < a.rows; row += stride) {
-    const float mean = mean_n, rstd = rstd_n;
-    if (row + stride < a.rows) {
-      mean_n = a.mean[row + stride];
-      rstd_n = a.rstd[row + stride];
+  const int warp = t >> 5, lane = t & 31;
+  int slot = 0;
+  F2 r2, shift;  // row k - 1's, then row k's
+  for (int64_t k = 0; k <= count; ++k) {
+    const F2 r2_old = r2, shift_old = shift;
+    const int old = slot == 0 ? depth - 1 : slot - 1;
+    if (k < count) {
+      mean = mean_n;
+      rstd = rstd_n;
+      if (k + 1 < count) {
+        mean_n = a.mean[first + (k + 1) * stride];
+        rstd_n = a.rstd[first + (k + 1) * stride];
+      }
+      // h = (x - mean) rstd; in bf16, whose x is coarser than the rounding of mean rstd, as
+      // one multiply-add.
+      r2 = f2(rstd, rstd);
+      shift = sizeof(X) == 2 ? f2(-mean * rstd, -mean * rstd) : f2(-mean, -mean);
+      wait_copies(depth - 2);
+      const uint4* const from = mine + slot * (2 * NV * T);
+      F2 s1 = f2(0.f, 0.f), s2 = f2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if ((j * T + t) * V < n) {
+          F2 g[P], h[P];
+          pairs_of<X>(from[j * T], g);
+          pairs_of<X>(from[(NV + j) * T], h);
+#pragma unroll
+          for (int q = 0; q < P; ++q) {
+            h[q] = sizeof(X) == 2 ? fma2(h[q], r2, shift) : mul2(add2(h[q], shift), r2);
+            db[j][q] = add2(db[j][q], g[q]);
+            const F2 gh = mul2(g[q], h[q]);
+            dw[j][q] = add2(dw[j][q], gh);
+            s1 = fma2(g[q], w[j][q], s1);
+            s2 = fma2(gh, w[j][q], s2);
+          }
+        }
+      // The warp's two sums, one in each half of its lanes, to its place.
+      const float v0 = sum_of(s1), v1 = sum_of(s2);
+      float v = (lane >= 16 ? v1 : v0) + __shfl_xor_sync(0xFFFFFFFFu, lane >= 16 ? v0 : v1, 16);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+      if ((lane & 15) == 0) scratch[(k & 1) * 64 + (lane >> 4) * 32 + warp] = v;
     }
-    fetch(row + (depth - 1) * stride, slot == 0 ? depth - 1 : slot - 1);
-    wait_copies(depth - 1);
-    const uint4* const from = mine + slot * (2 * NV * T);
-    slot = slot + 1 == depth ? 0 : slot + 1;
-    // h = (x - mean) rstd; in bf16, whose x is coarser than the rounding of mean rstd, as one
-    // multiply-add.
-    const F2 r2 = f2(rstd, rstd);
-    const F2 shift = sizeof(X) == 2 ? f2(-mean * rstd, -mean * rstd) : f2(-mean, -mean);
-    F2 g[NV][P], h[NV][P];
-    F2 s1 = f2(0.f, 0.f), s2 = f2(0.f, 0.f);
+    if (k > 0) {
+      constexpr int kW = T / 32;
+      float v = scratch[((k - 1) & 1) * 64 + (lane >> 4) * 32 + lane % kW];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if ((j * T + t) * V < n) {
-        pairs_of<X>(from[j * T], g[j]);
-        pairs_of<X>(from[(NV + j) * T], h[j]);
+      for (int o = kW / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+      const float m1 = -__shfl_sync(0xFFFFFFFFu, v, 0) * a.inv_n, m2 = -__shfl_sync(0xFFFFFFFFu, v, 16) * a.inv_n;
+      // rstd (g w - m1 - h m2)
+      const F2 c1 = f2(m1, m1), c2 = f2(m2, m2);
+      const uint4* const from = mine + old * (2 * NV * T);
+      X* dx = static_cast<X*>(a.dx) + (first + (k - 1) * stride) * a.n;
 #pragma unroll
-        for (int q = 0; q < P; ++q) {
-          h[j][q] = sizeof(X) == 2 ? fma2(h[j][q], r2, shift) : mul2(add2(h[j][q], shift), r2);
-          db[j][q] = add2(db[j][q], g[j][q]);
-          const F2 gh = mul2(g[j][q], h[j][q]);
-          dw[j][q] = add2(dw[j][q], gh);
-          s2 = fma2(gh, w[j][q], s2);
-          g[j][q] = mul2(g[j][q], w[j][q]);
-          s1 = add2(s1, g[j][q]);
+      for (int j = 0; j < NV; ++j) {
+        const int i = (j * T + t) * V;
+        if (i < n) {
+          F2 g[P], h[P], o[P];
+          pairs_of<X>(from[j * T], g);
+          pairs_of<X>(from[(NV + j) * T], h);
+#pragma unroll
+          for (int q = 0; q < P; ++q) {
+            h[q] = sizeof(X) == 2 ? fma2(h[q], r2_old, shift_old) : mul2(add2(h[q], shift_old), r2_old);
+            o[q] = mul2(fma2(h[q], c2, fma2(g[q], w[j][q], c1)), r2_old);
+          }
+          store_pairs<X>(dx + i, o);
         }
       }
-    float m1 = sum_of(s1), m2 = sum_of(s2);
-    row_sum2<T>(m1, m2, scratch, turn);
-    // rstd (g w - m1 - h m2)
-    const F2 c1 = f2(-m1 * a.inv_n, -m1 * a.inv_n), c2 = f2(-m2 * a.inv_n, -m2 * a.inv_n);
-    X* dx = static_cast<X*>(a.dx) + row * a.n;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = (j * T + t) * V;
-      if (i < n) {
-        F2 o[P];
-#pragma unroll
-        for (int q = 0; q < P; ++q) o[q] = mul2(fma2(h[j][q], c2, add2(g[j][q], c1)), r2);
-        store_pairs<X>(dx + i, o);
-      }
     }
+    // Row k - 1's place is free: the row `depth` after it.
+    if (k < count) {
+      fetch(first + (k + depth - 1) * stride, old);
+      slot = slot + 1 == depth ? 0 : slot + 1;
+    }
+    __syncthreads();
   }
   if (a.part == nullptr) return;
   float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.n;
@@ -775,8 +806,10 @@ cudaError_t run_norm_grad(const NormGradK& a, int64_t parts, cudaStream_t stream
 
 template <typename X, int T, int NV>
 cudaError_t run_norm_grad_ring(const NormGradK& a, int64_t parts, cudaStream_t stream) {
-  constexpr int kDepth = ring_depth(2 * NV * T * sizeof(uint4));
-  constexpr size_t kSmem = 2 * NV * T * sizeof(uint4) * kDepth;
+  // Two rows at work and up to four on their way, in an SM's 192 KB for 512 threads.
+  constexpr size_t kRow = 2 * NV * T * sizeof(uint4), kRoom = 384 * T;
+  constexpr int kDepth = kRow * 6 <= kRoom ? 6 : kRow * 5 <= kRoom ? 5 : kRow * 4 <= kRoom ? 4 : 3;
+  constexpr size_t kSmem = kRow * kDepth;
   static SmemRecord record;
   const cudaError_t err =
       ensure_dynamic_smem(reinterpret_cast<const void*>(norm_grad_ring_kernel<X, T, NV>), kSmem, record);
@@ -801,6 +834,7 @@ cudaError_t norm_grad_by_length(const NormGradK& a, int64_t* parts, cudaStream_t
     return run_norm_grad<X, 32, V, kNv>(a, *parts, stream);
   }
   if constexpr (V > 1) {
+    if (a.n <= 64 * per) { *parts = ctas(128); return run_norm_grad_ring<X, 128, kNv / 2>(a, *parts, stream); }
     if (a.n <= 128 * per) { *parts = ctas(128); return run_norm_grad_ring<X, 128, kNv>(a, *parts, stream); }
     if (a.n <= 256 * per) { *parts = ctas(256); return run_norm_grad_ring<X, 256, kNv>(a, *parts, stream); }
     if (a.n <= 512 * per) { *parts = ctas(512); return run_norm_grad_ring<X, 512, kNv>(a, *parts, stream); }
