@@ -146,28 +146,56 @@ __device__ __forceinline__ void store8(void* dst, int64_t at, int64_t plane, con
     }
   }
 }
-// Eight values of a row (zeros beyond `count`); vec: 16-byte loads, count >= 8.
+// Eight elements of a row as they are in memory (zeros beyond `count`); vec: 16-byte loads,
+// count >= 8 or none.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int count, bool vec, float (&v)[8]) {
-  if (vec) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int count, bool vec) {
+    a = make_uint4(0u, 0u, 0u, 0u);
+    if (vec) {
+      if (count > 0) a = __ldcs(reinterpret_cast<const uint4*>(p));
+    } else {
+      uint32_t h[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        v[2 * q] = __uint_as_float(w[q] << 16);
-        v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+      for (int q = 0; q < 8; ++q) h[q] = q < count ? static_cast<uint32_t>(__bfloat16_as_ushort(p[q])) : 0u;
+      a = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[2 * q] = __uint_as_float(w[q] << 16);
+      v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+    }
+  }
+};
+template <>
+struct Eight<float> {
+  float v8[8];
+  __device__ __forceinline__ void load(const float* p, int count, bool vec) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v8[q] = 0.f;
+    if (vec) {
+      if (count > 0) {
+        const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+        v8[0] = a.x; v8[1] = a.y; v8[2] = a.z; v8[3] = a.w;
+        v8[4] = b.x; v8[5] = b.y; v8[6] = b.z; v8[7] = b.w;
       }
     } else {
-      const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
-  } else {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = q < count ? value(p[q]) : 0.f;
+      for (int q = 0; q < 8; ++q)
+        if (q < count) v8[q] = p[q];
+    }
   }
-}
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = v8[q];
+  }
+};
 
 // A matrix as the tensor cores take it: rows padded to `pitch`, fp32 split into planes.
 template <typename T>
@@ -178,8 +206,10 @@ convert_kernel(const T* __restrict__ src, int64_t rows, int64_t cols, void* __re
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= rows * groups) return;
   const int64_t r = i / groups, c = (i - r * groups) * 8;
+  Eight<T> e;
   float v[8];
-  load8(src + r * cols + c, static_cast<int>(min(static_cast<int64_t>(8), cols - c)), vec != 0, v);
+  e.load(src + r * cols + c, static_cast<int>(min(static_cast<int64_t>(8), cols - c)), vec != 0);
+  e.get(v);
   if constexpr (sizeof(T) == 2) store8<T, 1>(dst, r * pitch + c, 0, v, 8, true);
   else store8<T, 3>(dst, r * pitch + c, plane, v, 8, true);
 }
@@ -205,29 +235,31 @@ __global__ void __launch_bounds__(256) delta_kernel(const Delta a) {
   const T* z = static_cast<const T*>(a.z);
   float sum[8] = {};
   if (count > 0) {
-    // Four rows at a time, their loads before the first use.
+    // A few rows at a time, their loads before the first use.
+    constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
     const int64_t step = static_cast<int64_t>(gridDim.y) * 8;
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * 8 + warp; r0 < a.rows; r0 += 4 * step) {
-      float v[4][8], u[4][8];
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * 8 + warp; r0 < a.rows; r0 += kAhead * step) {
+      Eight<T> eg[kAhead], ez[kAhead];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kAhead; ++i) {
         const int64_t r = r0 + i * step;
         const int have = r < a.rows ? count : 0;
-        if (have > 0 || a.vec_in == 0) {
-          load8(g + r * a.n + c, have, a.vec_in != 0, v[i]);
-          if (a.act != VN_ACT_NONE) load8(z + r * a.n + c, have, a.vec_in != 0, u[i]);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) v[i][q] = u[i][q] = 0.f;
-        }
+        eg[i].load(g + r * a.n + c, have, a.vec_in != 0);
+        if (a.act != VN_ACT_NONE) ez[i].load(z + r * a.n + c, have, a.vec_in != 0);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kAhead; ++i) {
         const int64_t r = r0 + i * step;
-        if (a.act != VN_ACT_NONE) slope_all<sizeof(T) == 2>(a.act, u[i], v[i]);
-        if (a.d != nullptr && r < a.rows) store8<T, kPlanes>(a.d, r * a.pitch + c, a.plane, v[i], count, a.vec_out != 0);
+        float v[8];
+        eg[i].get(v);
+        if (a.act != VN_ACT_NONE) {
+          float u[8];
+          ez[i].get(u);
+          slope_all<true>(a.act, u, v);
+        }
+        if (a.d != nullptr && r < a.rows) store8<T, kPlanes>(a.d, r * a.pitch + c, a.plane, v, count, a.vec_out != 0);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) sum[q] += v[i][q];
+        for (int q = 0; q < 8; ++q) sum[q] += v[q];
       }
     }
   }

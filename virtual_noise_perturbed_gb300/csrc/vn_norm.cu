@@ -21,6 +21,7 @@
 #include <algorithm>
 
 #include "vn_internal.h"
+#include "vn_pair.cuh"
 
 namespace vn {
 namespace {
@@ -138,38 +139,6 @@ __device__ __forceinline__ void row_sum2(float& v0, float& v1, float* scratch, i
   v1 = __shfl_sync(0xFFFFFFFFu, v, 16);
 }
 
-// Two fp32 values in one register pair, and the two-lane instructions on them (each lane rounds as
-// the single instruction does). The norm's kernels are close to the issue limit: one of these does
-// the work of two.
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 f2(float a, float b) {
-  F2 d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-  return d;
-}
-__device__ __forceinline__ void split(F2 v, float* a, float* b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ float sum_of(F2 v) {
-  float a, b;
-  split(v, &a, &b);
-  return a + b;
-}
 // A 16-byte pack as pairs of fp32: 4 of bf16, 2 of fp32.
 template <typename X>
 constexpr int kPairs = 8 / sizeof(X);
@@ -190,6 +159,14 @@ __device__ __forceinline__ void store_pairs(X* p, const F2 (&v)[kPairs<X>]) {
 #pragma unroll
   for (int q = 0; q < kPairs<X>; ++q) split(v[q], &o[2 * q], &o[2 * q + 1]);
   store_pack<X, 16 / sizeof(X)>(p, o);
+}
+// V consecutive parameters as pairs.
+template <int V>
+__device__ __forceinline__ void load_pairs(const void* w, int bf16, int64_t i, float absent, F2 (&v)[V / 2]) {
+  float u[V];
+  load_param<V>(w, bf16, i, absent, u);
+#pragma unroll
+  for (int q = 0; q < V / 2; ++q) v[q] = f2(u[2 * q], u[2 * q + 1]);
 }
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -215,8 +192,73 @@ struct NormArgsK {
   int w_bf16;
 };
 
-constexpr int cta_threads(int t) { return t < 128 ? 128 : t; }
+constexpr int cta_threads(int t) { return t < 64 ? 128 : t; }
 
+// Rows of 16-byte packs, NV of them a thread.
+template <typename X, int T, int NV>
+__global__ void __launch_bounds__(cta_threads(T)) norm_pairs_kernel(const NormArgsK a) {
+  constexpr int kRows = cta_threads(T) / T, V = 16 / sizeof(X), P = kPairs<X>;
+  __shared__ float scratch[T > 32 ? 64 : 1];
+  int turn = 0;
+  const int t = threadIdx.x % T;
+  const int n = static_cast<int>(a.n);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T;
+  if (T == 32 && row >= a.rows) return;
+  const X* in = static_cast<const X*>(a.x) + row * a.n;
+  uint4 raw[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = (j * T + t) * V;
+    if (i < n) raw[j] = __ldcs(reinterpret_cast<const uint4*>(in + i));
+  }
+  // The row stays as it was loaded and is unpacked in each pass: bf16 in half the registers
+  // that its fp32 values would take, for more rows at work (84 us against 116 us, 32768 x 4096).
+  F2 s = f2(0.f, 0.f);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if ((j * T + t) * V < n) {
+      F2 x[P];
+      pairs_of<X>(raw[j], x);
+#pragma unroll
+      for (int q = 0; q < P; ++q) s = add2(s, x[q]);
+    }
+  const float mean = row_sum<T>(sum_of(s), scratch, turn) * a.inv_n;
+  const F2 minus = f2(-mean, -mean);
+  s = f2(0.f, 0.f);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if ((j * T + t) * V < n) {
+      F2 x[P];
+      pairs_of<X>(raw[j], x);
+#pragma unroll
+      for (int q = 0; q < P; ++q) {
+        x[q] = add2(x[q], minus);
+        s = fma2(x[q], x[q], s);
+      }
+    }
+  const float rstd = 1.f / sqrtf(row_sum<T>(sum_of(s), scratch, turn) * a.inv_n + a.eps);
+  const F2 r2 = f2(rstd, rstd);
+  X* y = static_cast<X*>(a.y) + row * a.n;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int i = (j * T + t) * V;
+    if (i < n) {
+      F2 x[P], w[P], b[P];
+      load_pairs<V>(a.w, a.w_bf16, i, 1.f, w);
+      load_pairs<V>(a.b, a.w_bf16, i, 0.f, b);
+      pairs_of<X>(raw[j], x);
+#pragma unroll
+      for (int q = 0; q < P; ++q) x[q] = fma2(mul2(add2(x[q], minus), r2), w[q], b[q]);
+      store_pairs<X>(y + i, x);
+    }
+  }
+  if (t == 0) {
+    if (a.mean != nullptr) a.mean[row] = mean;
+    if (a.rstd != nullptr) a.rstd[row] = rstd;
+  }
+}
+
+// Rows that 16-byte packs do not divide: single elements, NV of them a thread.
 template <typename X, int T, int V, int NV>
 __global__ void __launch_bounds__(cta_threads(T)) norm_kernel(const NormArgsK a) {
   constexpr int kRows = cta_threads(T) / T;
@@ -266,95 +308,6 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_kernel(const NormArgsK a)
   if (t == 0) {
     if (a.mean != nullptr) a.mean[row] = mean;
     if (a.rstd != nullptr) a.rstd[row] = rstd;
-  }
-}
-
-// The same for longer rows of 16-byte packs: CTAs that stay, weight and bias in registers, and the
-// next rows on their way through shared memory. Each thread copies its own packs into its own
-// places (cp.async) and reads them back itself, so the ring needs no barrier of its own.
-template <typename X, int T, int NV>
-__global__ void __launch_bounds__(T) norm_ring_kernel(const NormArgsK a, const int depth) {
-  constexpr int V = 16 / sizeof(X), P = kPairs<X>;
-  extern __shared__ uint4 ring[];  // [depth][NV][T]
-  __shared__ float scratch[64];
-  int turn = 0;
-  const int t = threadIdx.x;
-  const int n = static_cast<int>(a.n);
-  F2 w[NV][P], b[NV][P];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int i = (j * T + t) * V;
-    float u[V] = {}, v[V] = {};
-    if (i < n) {
-      load_param<V>(a.w, a.w_bf16, i, 1.f, u);
-      load_param<V>(a.b, a.w_bf16, i, 0.f, v);
-    }
-#pragma unroll
-    for (int q = 0; q < P; ++q) {
-      w[j][q] = f2(u[2 * q], u[2 * q + 1]);
-      b[j][q] = f2(v[2 * q], v[2 * q + 1]);
-    }
-  }
-  uint4* const mine = ring + t;
-  const int64_t stride = gridDim.x;
-  auto fetch = [&](int64_t row, int slot) {  // one group of copies, empty beyond the last row
-    if (row < a.rows) {
-      const X* x = static_cast<const X*>(a.x) + row * a.n;
-      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(mine + slot * (NV * T)));
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int i = (j * T + t) * V;
-        if (i < n) copy16(to + j * (T * 16), x + i);
-      }
-    }
-    commit_copies();
-  };
-  int64_t row = blockIdx.x;
-  for (int d = 0; d < depth - 1; ++d) fetch(row + d * stride, d);
-  int slot = 0;
-  for (; row < a.rows; row += stride) {
-    fetch(row + (depth - 1) * stride, slot == 0 ? depth - 1 : slot - 1);
-    wait_copies(depth - 1);
-    const uint4* const from = mine + slot * (NV * T);
-    slot = slot + 1 == depth ? 0 : slot + 1;
-    F2 x[NV][P];
-    F2 s2 = f2(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if ((j * T + t) * V < n) {
-        pairs_of<X>(from[j * T], x[j]);
-#pragma unroll
-        for (int q = 0; q < P; ++q) s2 = add2(s2, x[j][q]);
-      }
-    const float mean = row_sum<T>(sum_of(s2), scratch, turn) * a.inv_n;
-    const F2 minus = f2(-mean, -mean);
-    s2 = f2(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if ((j * T + t) * V < n) {
-#pragma unroll
-        for (int q = 0; q < P; ++q) {
-          x[j][q] = add2(x[j][q], minus);
-          s2 = fma2(x[j][q], x[j][q], s2);
-        }
-      }
-    const float rstd = 1.f / sqrtf(row_sum<T>(sum_of(s2), scratch, turn) * a.inv_n + a.eps);
-    const F2 r2 = f2(rstd, rstd);
-    X* y = static_cast<X*>(a.y) + row * a.n;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = (j * T + t) * V;
-      if (i < n) {
-        F2 o[P];
-#pragma unroll
-        for (int q = 0; q < P; ++q) o[q] = fma2(mul2(x[j][q], r2), w[j][q], b[j][q]);
-        store_pairs<X>(y + i, o);
-      }
-    }
-    if (t == 0) {
-      if (a.mean != nullptr) a.mean[row] = mean;
-      if (a.rstd != nullptr) a.rstd[row] = rstd;
-    }
   }
 }
 
@@ -740,47 +693,24 @@ cudaError_t run_norm(const NormArgsK& a, cudaStream_t stream) {
   constexpr int kRows = cta_threads(T) / T;
   const int64_t grid = (a.rows + kRows - 1) / kRows;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  norm_kernel<X, T, V, NV><<<static_cast<unsigned>(grid), cta_threads(T), 0, stream>>>(a);
+  if constexpr (V > 1) norm_pairs_kernel<X, T, NV><<<static_cast<unsigned>(grid), cta_threads(T), 0, stream>>>(a);
+  else norm_kernel<X, T, V, NV><<<static_cast<unsigned>(grid), cta_threads(T), 0, stream>>>(a);
   return cudaGetLastError();
 }
 
-// Rows on their way at once: as many as fit 64 KB of shared memory, 2 to 4.
-constexpr int ring_depth(size_t row) { return row * 4 <= 65536 ? 4 : row * 3 <= 65536 ? 3 : 2; }
-
-// ctas: as many as are resident at once.
-template <typename X, int T, int NV>
-cudaError_t run_norm_ring(const NormArgsK& a, int64_t ctas, cudaStream_t stream) {
-  constexpr int kDepth = ring_depth(NV * T * sizeof(uint4));
-  constexpr size_t kSmem = NV * T * sizeof(uint4) * kDepth;
-  static SmemRecord record;
-  const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(norm_ring_kernel<X, T, NV>), kSmem, record);
-  if (err != cudaSuccess) return err;
-  norm_ring_kernel<X, T, NV><<<static_cast<unsigned>(std::min(a.rows, ctas)), T, kSmem, stream>>>(a, kDepth);
-  return cudaGetLastError();
-}
-
-// The threads of a row by its number of packs: a warp while its 8 packs a lane suffice
-// (no barrier), then 128 to 512 threads.
+// The threads of a row by its number of packs: as few as 8 packs a thread allow, so that many rows
+// are at work on an SM and few barriers join them (32768 x 4096 bf16: 81 us with 64 threads a
+// row, 84 with 128, 102 with 256; 16384 x 8192: 81 with 128, 88 with 256).
 template <typename X, int V>
 cudaError_t norm_by_length(const NormArgsK& a, cudaStream_t stream) {
-  if constexpr (V > 1) {
-    if (a.n > 256 * V && a.n <= 512 * 2 * V) {
-      DeviceInfo dev;
-      const cudaError_t err = device_info(&dev);
-      if (err != cudaSuccess) return err;
-      // 1,024 threads an SM
-      if (a.n <= 256 * 2 * V) return run_norm_ring<X, 256, 2>(a, 4 * dev.sm_count, stream);
-      return run_norm_ring<X, 512, 2>(a, 2 * dev.sm_count, stream);
-    }
-  }
   const int64_t packs = (a.n + V - 1) / V;
   if (packs <= 32) return run_norm<X, 32, V, 1>(a, stream);
   if (packs <= 64) return run_norm<X, 32, V, 2>(a, stream);
   if (packs <= 128) return run_norm<X, 32, V, 4>(a, stream);
   if (packs <= 256) return run_norm<X, 32, V, 8>(a, stream);
-  if (packs <= 512) return run_norm<X, 128, V, 4>(a, stream);
+  if (packs <= 512) return run_norm<X, 64, V, 8>(a, stream);
   if (packs <= 1024) return run_norm<X, 128, V, 8>(a, stream);
-  if (packs <= 2048) return run_norm<X, 512, V, 4>(a, stream);
+  if (packs <= 2048) return run_norm<X, 256, V, 8>(a, stream);
   if (packs <= 4096) return run_norm<X, 512, V, 8>(a, stream);
   if (a.rows > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   norm_long_kernel<X><<<static_cast<unsigned>(a.rows), 512, 0, stream>>>(a);
