@@ -52,6 +52,7 @@ struct Params : Epilogue {
   int p_tiles, q_tiles;
   int bn;  // pair: columns of a tile, a multiple of 16
   int64_t units;
+  uint32_t staging_bytes;  // pair: the epilogue's chunks, both halves
   int k_chunks, iters;  // iterations of the k loop: k_chunks x pairs of planes
   int stages;
   uint32_t idesc;
@@ -103,10 +104,6 @@ __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t stage, uint32_t
 // residual and pre-activation, on 8192 x 4096 x 4096).
 template <typename T>
 constexpr uint32_t kChunkBytes = 16 * 128 * sizeof(T);
-template <typename T>
-constexpr uint32_t kStagingBytes = 2 * 6 * kChunkBytes<T>;  // halves x (y, z, residual) x 2
-template <typename T>
-constexpr int kPairStages = sizeof(T) == 2 ? 5 : 4;
 constexpr uint32_t kPairStageBytes = kABytes + 128 * 128;
 
 // Barriers: full[S] (leader's, armed for both CTAs' bytes), empty[S], tmem_full[2],
@@ -116,11 +113,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
             const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap zmap,
             const __grid_constant__ CUtensorMap rmap, const Params p) {
-  constexpr int S = kPairStages<T>;
+  const int S = p.stages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* staging = smem + S * kPairStageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + (kStaged ? kStagingBytes<T> : 0));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + p.staging_bytes);
   const uint32_t bar0 = smem_u32(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (S + s); };
@@ -218,10 +215,12 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
     const int half = (p.bn / 16 + 1) / 2 * 16;  // columns of half 0
     const int c0 = h * half, width = h ? p.bn - half : half;
     const bool leader = quarter == 2 && lane == 0;  // warps 2 and 6
-    T* const buf = reinterpret_cast<T*>(staging + h * (kStagingBytes<T> / 2));
+    // Two chunks each of y, of the residual and of the pre-activation, the latter two where given.
+    T* const buf = reinterpret_cast<T*>(staging + h * (p.staging_bytes / 2));
     const uint32_t buf0 = smem_u32(buf);
     constexpr int kChunk = 16 * 128;
     const bool has_r = p.residual != nullptr, has_z = p.preact != nullptr;
+    const int z_at = has_r ? 4 : 2;
     Ring tb;
     uint32_t jj = 0;  // chunks so far
     bool go = true;
@@ -237,7 +236,7 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
       if constexpr (kStaged) {
         auto fetch = [&](uint32_t j, int c) {
           mbar_expect_tx(arrived(h, j & 1), kChunkBytes<T>);
-          tma_load_2d(buf0 + (4 + (j & 1)) * kChunkBytes<T>, &rmap, arrived(h, j & 1), p0, static_cast<int>(q0) + c);
+          tma_load_2d(buf0 + (2 + (j & 1)) * kChunkBytes<T>, &rmap, arrived(h, j & 1), p0, static_cast<int>(q0) + c);
         };
         if (leader) {
           if (has_r && cols > 0) fetch(jj, 0);
@@ -275,7 +274,7 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
           if (has_r) {
             if (!(go = s_go[3 * h + 2] != 0)) break;
             (void)mbar_try(arrived(h, jj & 1), (jj >> 1) & 1u);
-            const T* r = buf + (4 + (jj & 1)) * kChunk + row;
+            const T* r = buf + (2 + (jj & 1)) * kChunk + row;
 #pragma unroll
             for (int i = 0; i < 16; ++i) z[i] += value(r[i * 128]);
           }
@@ -283,7 +282,7 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
 #pragma unroll
           for (int i = 0; i < 16; ++i) y[i * 128] = narrow<T>(z[i]);
           if (has_z) {
-            T* zo = buf + (2 + (jj & 1)) * kChunk + row;
+            T* zo = buf + (z_at + (jj & 1)) * kChunk + row;
 #pragma unroll
             for (int i = 0; i < 16; ++i) zo[i * 128] = pre[i];
           }
@@ -291,7 +290,7 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
           named_barrier(1 + h, 128);
           if (leader) {
             tma_store_2d(&ymap, buf0 + (jj & 1) * kChunkBytes<T>, p0, static_cast<int>(q0) + c);
-            if (has_z) tma_store_2d(&zmap, buf0 + (2 + (jj & 1)) * kChunkBytes<T>, p0, static_cast<int>(q0) + c);
+            if (has_z) tma_store_2d(&zmap, buf0 + (z_at + (jj & 1)) * kChunkBytes<T>, p0, static_cast<int>(q0) + c);
             bulk_commit();
           }
         }
@@ -564,10 +563,14 @@ cudaError_t run_pair_typed(const TcProduct& d, Params p, int sms, cudaStream_t s
   p.units = static_cast<int64_t>(p.p_tiles) * p.q_tiles;
   p.idesc = idesc_of(256, p.bn, kAMn, kBMn);
   const int grid = static_cast<int>(std::min<int64_t>(2 * p.units, 2 * pairs));
+  const int chunks = kStaged ? 2 * (1 + (d.preact != nullptr) + (d.residual != nullptr)) : 0;
+  p.staging_bytes = 2 * chunks * kChunkBytes<T>;
+  // As many stages as the rest of the 227 KB holds: 4 to 6 (in bf16 6, or 5 with both a
+  // residual and a pre-activation). 4 instead of 6 cost 5 to 12 per cent.
+  p.stages = std::min<int>(kMaxStages, static_cast<int>((232448 - kFixed - p.staging_bytes) / kPairStageBytes));
   static SmemRecord record;
   return launch_cluster(pair_kernel<T, kAMn, kBMn, kStaged>, record, grid, kPairThreads, 2,
-                        kFixed + kPairStages<T> * kPairStageBytes + (kStaged ? kStagingBytes<T> : 0), stream, am, bm, ym,
-                        zm, rm, p);
+                        kFixed + p.stages * kPairStageBytes + p.staging_bytes, stream, am, bm, ym, zm, rm, p);
 }
 template <typename T, bool kAMn, bool kBMn>
 cudaError_t run_pair(const TcProduct& d, const Params& p, int sms, cudaStream_t stream) {
