@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "vn_act.cuh"
 #include "vn_dense.h"
@@ -299,26 +300,180 @@ int64_t operand_bytes(int64_t rows, int64_t cols, vn_dtype dt) {
 // Whether a matrix can be taken as it is.
 bool as_is(vn_dtype dt, int64_t cols, bool aligned) { return dt == VN_BF16 && cols % 8 == 0 && aligned; }
 
-// How a layer, or its gradients, are computed.
+// ---------------------------------------------------------------- which kernel
+// The times below are what the kernels took on a GB300, launch included, over sizes from 64 to 8192: a
+// few microseconds a launch, and a CTA's (or pair's) time per 64 of k. They are reckoned here, from
+// sizes alone, so that a call and its workspace agree without a device.
 enum class Route {
   kRows,    // up to 8 rows: vn_dense_rows.cu
   kPlain,   // 64 x 64 tiles without tensor cores: sizes beyond 32-bit coordinates
-  kGather,  // one launch, operands gathered by threads: results of few tiles
+  kGather,  // one launch, operands gathered by threads: vn_dense_gather.cu
   kTiles,   // operands by TMA, in bf16 (converted where they are not): vn_dense_tc.cu
 };
 bool fits32(int64_t rows, int64_t in, int64_t out) {
   const int64_t most = (int64_t{1} << 31) - 512;
   return rows <= most && in <= most && out <= most;
 }
-Route forward_route(int64_t rows, int64_t in, int64_t out, vn_dtype dt, bool aligned) {
-  if (rows <= 8) return Route::kRows;
-  if (!fits32(rows, in, out)) return Route::kPlain;
-  if (in > 0 && (fills_pairs(out, rows) || as_is(dt, in, aligned))) return Route::kTiles;
-  return Route::kGather;
+double tiles_of(int64_t n, int64_t tile) { return static_cast<double>((n + tile - 1) / tile); }
+// CTAs that the GPU holds at once in clusters of 2^log_cluster, `per_sm` to an SM: fewer than 152 SMs
+// have room for, as clusters stay within a part of the GPU.
+double resident(int log_cluster, int per_sm) {
+  static const double kOne[4] = {152, 152, 144, 120}, kTwo[4] = {304, 304, 296, 288};
+  return per_sm == 1 ? kOne[log_cluster] : kTwo[log_cluster];
 }
-Route backward_route(int64_t rows, int64_t in, int64_t out) {
-  if (!fits32(rows, in, out)) return Route::kPlain;
-  return rows > 0 && out > 0 && (fills_pairs(in, rows) || fills_pairs(in, out)) ? Route::kTiles : Route::kGather;
+
+// A product on tiles. iters: chunks of 64 k, six times as many of fp32's planes.
+TilePlan tile_plan(int64_t np, int64_t nq, int64_t nk, vn_dtype dt, bool b_mn) {
+  TilePlan best;
+  if (np == 0 || nq == 0) {
+    best.us = 0;
+    return best;
+  }
+  const double iters = tiles_of(nk, 64) * (dt == VN_BF16 ? 1 : 6);
+  // Pairs: rounds of tiles over 76 pairs x (k loop, bound by the loads of 128 rows of A and bn / 2 of B
+  // an SM rather than by its products, + what a tile costs besides). 4096 x 4096 results: 4 rounds of 224
+  // columns rather than 4 of 256; 1024 x 1024: one round of 64.
+  for (int bn = 256; bn >= 32; bn -= 16) {
+    const double rounds = std::ceil(tiles_of(np, 256) * tiles_of(nq, bn) / 76);
+    const double us = 5.0 + rounds * (iters * (420 + bn) + 1000 + 16 * bn) / 1900;
+    if (us < best.us) best = TilePlan{us, true, bn, 0};
+  }
+  // Single CTAs, two an SM, which then share its loads.
+  for (int bn : {16, 64, 128}) {
+    if (b_mn && bn == 16) continue;
+    const double stage = bn == 128 ? 0.36 : bn == 64 ? 0.27 : 0.22;
+    for (int l = 0; l < 4; ++l) {
+      const double ctas = tiles_of(np, 128) * tiles_of(nq, bn) * (1 << l);
+      const double rounds = std::ceil(ctas / resident(l, 2));
+      const double us = 5.0 + (l > 0 ? 1.0 + 0.015 * bn : 0.0) +
+                        rounds * (std::ceil(iters / (1 << l)) * stage * (ctas > 152 ? 1.9 : 1.0) + 2.0);
+      if (us < best.us) best = TilePlan{us, false, bn, l};
+    }
+  }
+  return best;
+}
+
+// Products (one, or a layer's two gradients) gathered in one launch: the time of the longest CTA, or of
+// all of them over those that run at once.
+struct Shape {
+  int64_t np, nq, nk;
+};
+GatherPlan gather_plan(const Shape (&shapes)[2], vn_dtype dt, bool backward, bool vectors) {
+  GatherPlan best;
+  const bool bf16 = dt == VN_BF16;
+  for (int bn : {16, 64, 128}) {
+    if (backward && bn == 16) continue;
+    const double stage = (vectors ? 1.0 : 1.6) *  // loads of single elements
+                         (backward    ? (bn == 128 ? (bf16 ? 2.9 : 3.3) : (bf16 ? 1.8 : 1.9))
+                          : bn == 128 ? (bf16 ? 1.8 : 1.9)
+                          : bn == 64  ? (bf16 ? 1.2 : 1.25)
+                                      : 0.9);
+    for (int l0 = 0; l0 < 4; ++l0)
+      for (int l1 = 0; l1 < (backward ? 4 : 1); ++l1) {
+        const int l[2] = {l0, l1};
+        double work = 0, longest = 0, ctas = 0;
+        for (int i = 0; i < 2; ++i) {
+          const Shape& s = shapes[i];
+          if (s.np == 0 || s.nq == 0) continue;
+          const double n = tiles_of(s.np, 128) * tiles_of(s.nq, bn) * (1 << l[i]);
+          const double t = std::ceil(tiles_of(s.nk, 64) / (1 << l[i])) * stage + 5.0 + (l[i] > 0 ? 1.5 : 0.0);
+          ctas += n;
+          work += n * t;
+          longest = std::max(longest, t);
+        }
+        const double room = resident(std::max(l0, l1), bf16 ? 2 : 1);
+        // Two CTAs of an SM share its threads' time.
+        const double crowd = bf16 && ctas > 152 ? 1.7 : 1.0;
+        const double us = crowd * (ctas <= room ? longest : std::max(longest, work / room) + 0.5 * longest);
+        if (us < best.us) {
+          best.us = us;
+          best.bn = bn;
+          best.log_split[0] = l0;
+          best.log_split[1] = l1;
+        }
+      }
+  }
+  return best;
+}
+// Converting a matrix for the tensor cores.
+double convert_us(int64_t rows, int64_t cols, vn_dtype dt, bool as_it_is) {
+  if (as_it_is) return 0;
+  return 2.5 + static_cast<double>(rows) * static_cast<double>(cols) * (dt == VN_BF16 ? 4 : 10) / 4e6;
+}
+
+struct ForwardPlan {
+  Route route;
+  GatherPlan gather;
+  TilePlan tiles;
+};
+ForwardPlan reckon_forward(int64_t rows, int64_t in, int64_t out, vn_dtype dt, bool aligned) {
+  ForwardPlan p;
+  p.route = Route::kRows;
+  if (rows <= 8) return p;
+  p.route = Route::kPlain;
+  if (!fits32(rows, in, out)) return p;
+  const Shape shapes[2] = {{out, rows, in}, {0, 0, 0}};
+  const int64_t vec = dt == VN_BF16 ? 8 : 4;
+  p.gather = gather_plan(shapes, dt, false, aligned && in % vec == 0);
+  p.route = Route::kGather;
+  if (in == 0) return p;
+  p.tiles = tile_plan(out, rows, in, dt, false);
+  const bool direct = as_is(dt, in, aligned);
+  if (p.tiles.us + convert_us(out, in, dt, direct) + convert_us(rows, in, dt, direct) < p.gather.us) p.route = Route::kTiles;
+  return p;
+}
+struct BackwardPlan {
+  Route route;
+  GatherPlan gather;
+  TilePlan dx, dw;
+};
+BackwardPlan reckon_backward(int64_t rows, int64_t in, int64_t out, vn_dtype dt, vn_act act, bool aligned) {
+  BackwardPlan p;
+  p.route = Route::kPlain;
+  if (!fits32(rows, in, out)) return p;
+  const Shape shapes[2] = {{in, rows, out}, {in, out, rows}};
+  const int64_t vec = dt == VN_BF16 ? 8 : 4;
+  p.gather = gather_plan(shapes, dt, true, aligned && in % vec == 0 && out % vec == 0);
+  p.route = Route::kGather;
+  if (rows == 0 || in == 0 || out == 0) return p;
+  p.dx = tile_plan(in, rows, out, dt, false);
+  p.dw = tile_plan(in, out, rows, dt, true);
+  const bool direct = as_is(dt, in, aligned), keeps = act != VN_ACT_NONE || !as_is(dt, out, aligned);
+  // d, and the bias's sums.
+  const double delta = 5.0 + (keeps ? 2.0 : 1.0) * static_cast<double>(rows) * static_cast<double>(out) * (dt == VN_BF16 ? 3 : 7) / 4e6;
+  if (p.dx.us + p.dw.us + delta + convert_us(out, in, dt, direct) + convert_us(rows, in, dt, direct) < p.gather.us)
+    p.route = Route::kTiles;
+  return p;
+}
+
+// A call asks for its plan three times (for its workspace, to check that, and to launch), and a program
+// for the same sizes again and again: each thread keeps the last one.
+struct Sizes {
+  int64_t rows, in, out;
+  int dt, act, aligned;
+  bool operator==(const Sizes& o) const {
+    return rows == o.rows && in == o.in && out == o.out && dt == o.dt && act == o.act && aligned == o.aligned;
+  }
+};
+ForwardPlan forward_plan(int64_t rows, int64_t in, int64_t out, vn_dtype dt, bool aligned) {
+  thread_local Sizes last = {-1, 0, 0, 0, 0, 0};
+  thread_local ForwardPlan plan;
+  const Sizes now = {rows, in, out, dt, 0, aligned};
+  if (!(now == last)) {
+    plan = reckon_forward(rows, in, out, dt, aligned);
+    last = now;
+  }
+  return plan;
+}
+BackwardPlan backward_plan(int64_t rows, int64_t in, int64_t out, vn_dtype dt, vn_act act, bool aligned) {
+  thread_local Sizes last = {-1, 0, 0, 0, 0, 0};
+  thread_local BackwardPlan plan;
+  const Sizes now = {rows, in, out, dt, act, aligned};
+  if (!(now == last)) {
+    plan = reckon_backward(rows, in, out, dt, act, aligned);
+    last = now;
+  }
+  return plan;
 }
 
 // Row groups that the column sums are split over.
@@ -353,12 +508,12 @@ cudaError_t prepare(const void* p, vn_dtype dt, int64_t rows, int64_t cols, bool
 }  // namespace
 
 int64_t dense_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, bool aligned) {
-  if (forward_route(rows, in, out, dt, aligned) != Route::kTiles || as_is(dt, in, aligned)) return 0;
+  if (forward_plan(rows, in, out, dt, aligned).route != Route::kTiles || as_is(dt, in, aligned)) return 0;
   return operand_bytes(rows, in, dt) + operand_bytes(out, in, dt);
 }
 
 int64_t dense_backward_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, vn_act act, bool aligned) {
-  const Route route = backward_route(rows, in, out);
+  const Route route = backward_plan(rows, in, out, dt, act, aligned).route;
   const int64_t sums = rounded(delta_parts(rows) * out * 4);
   if (route == Route::kGather) return sums;
   if (route == Route::kPlain)
@@ -371,10 +526,10 @@ int64_t dense_backward_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype
 
 cudaError_t launch_dense(const DenseArgs& a, cudaStream_t stream) {
   const bool al = aligned16(a.x) && aligned16(a.w);
-  const Route route = forward_route(a.rows, a.in, a.out, a.dt, al);
-  if (route == Route::kRows) return launch_rows_forward(a, stream);
-  if (route == Route::kGather) return launch_gather_forward(a, stream);
-  if (route == Route::kTiles) {
+  const ForwardPlan plan = forward_plan(a.rows, a.in, a.out, a.dt, al);
+  if (plan.route == Route::kRows) return launch_rows_forward(a, stream);
+  if (plan.route == Route::kGather) return launch_gather_forward(a, plan.gather, stream);
+  if (plan.route == Route::kTiles) {
     uint8_t* work = static_cast<uint8_t*>(a.workspace);
     TcProduct d = {};
     cudaError_t err = prepare(a.w, a.dt, a.out, a.in, al, false, &work, &d.a, stream);
@@ -384,7 +539,7 @@ cudaError_t launch_dense(const DenseArgs& a, cudaStream_t stream) {
     d.dt = a.dt;
     d.bias = a.b; d.bias_bf16 = a.b_dt == VN_BF16; d.act = a.act;
     d.residual = a.residual; d.out = a.y; d.preact = a.preact;
-    return launch_tc_product(d, stream);
+    return launch_tc_product(d, plan.tiles, stream);
   }
   Product d = {};
   d.a = a.w; d.ap = a.in; d.ak = 1;
@@ -428,8 +583,9 @@ cudaError_t delta_pass(const DenseGradArgs& a, const TcOperand* delta, float* pa
 }  // namespace
 
 cudaError_t launch_dense_backward(const DenseGradArgs& a, cudaStream_t stream) {
-  const Route route = backward_route(a.rows, a.in, a.out);
-  if (route == Route::kGather) {
+  const bool al = aligned16(a.grad) && aligned16(a.x) && aligned16(a.w);
+  const BackwardPlan plan = backward_plan(a.rows, a.in, a.out, a.dt, a.act, al);
+  if (plan.route == Route::kGather) {
     // The gather kernel sums the bias's gradient beside the weight's; alone it is a pass over d.
     DenseGradArgs rest = a;
     if (a.grad_b != nullptr && a.grad_w == nullptr) {
@@ -437,10 +593,9 @@ cudaError_t launch_dense_backward(const DenseGradArgs& a, cudaStream_t stream) {
       if (err != cudaSuccess || a.grad_x == nullptr) return err;
       rest.grad_b = nullptr;
     }
-    return launch_gather_backward(rest, stream);
+    return launch_gather_backward(rest, plan.gather, stream);
   }
-  const bool tc = route != Route::kPlain;
-  const bool al = aligned16(a.grad) && aligned16(a.x) && aligned16(a.w);
+  const bool tc = plan.route == Route::kTiles;
   const bool products = a.grad_x != nullptr || a.grad_w != nullptr;
   const bool keep = products && (a.act != VN_ACT_NONE || (tc && !as_is(a.dt, a.out, al)));  // d has to be stored
   uint8_t* work = static_cast<uint8_t*>(a.workspace);
@@ -466,14 +621,14 @@ cudaError_t launch_dense_backward(const DenseGradArgs& a, cudaStream_t stream) {
       if ((err = prepare(a.w, a.dt, a.out, a.in, al, true, &work, &d.a, stream)) != cudaSuccess) return err;
       d.np = a.in; d.nq = a.rows; d.nk = a.out;
       d.out = a.grad_x;
-      if ((err = launch_tc_product(d, stream)) != cudaSuccess) return err;
+      if ((err = launch_tc_product(d, plan.dx, stream)) != cudaSuccess) return err;
     }
     if (a.grad_w != nullptr) {
       if ((err = prepare(a.x, a.dt, a.rows, a.in, al, true, &work, &d.a, stream)) != cudaSuccess) return err;
       d.b.mn = true;
       d.np = a.in; d.nq = a.out; d.nk = a.rows;
       d.out = a.grad_w;
-      return launch_tc_product(d, stream);
+      return launch_tc_product(d, plan.dw, stream);
     }
     return cudaSuccess;
   }

@@ -9,6 +9,20 @@
 
 namespace vn {
 
+// How a product is tiled, and its time on a GB300 as the dispatcher reckons it (vn_dense.cu). bn: the
+// tile's columns; log_split: log2 of the CTAs that share a tile's k loop.
+struct TilePlan {
+  double us = 1e30;
+  bool pair = false;  // pairs of CTAs on 256 x bn tiles, else single CTAs on 128 x bn
+  int bn = 64;
+  int log_split = 0;
+};
+struct GatherPlan {
+  double us = 1e30;
+  int bn = 64;
+  int log_split[2] = {0, 0};  // of the forward product, or of grad_x's; of grad_w's
+};
+
 // A bf16 operand of the tensor-core kernels: [planes][rows][pitch], of which the first `cols`
 // of each row count. mn: the contiguous dimension is p (or q), the rows are k; otherwise k is
 // contiguous. p is 16-byte aligned, pitch a multiple of 8, plane (elements) too.
@@ -32,13 +46,7 @@ struct TcProduct {
   void* out;
   void* preact;
 };
-cudaError_t launch_tc_product(const TcProduct& d, cudaStream_t stream);
-
-// Whether a result has tiles enough (256 x 256) for at least half of a GB300's 76 pairs of
-// SMs; with fewer, 128-wide tiles whose k loop is split spread it further.
-inline bool fills_pairs(int64_t np, int64_t nq) {
-  return np > 0 && nq > 0 && ((np + 255) / 256) * ((nq + 255) / 256) >= 38;
-}
+cudaError_t launch_tc_product(const TcProduct& d, const TilePlan& plan, cudaStream_t stream);
 
 // A layer, or all its gradients, in one launch, for any alignment and no workspace
 // (vn_dense_gather.cu). At least one of grad_x and grad_w is asked for, and grad_b only with
@@ -46,8 +54,8 @@ inline bool fills_pairs(int64_t np, int64_t nq) {
 struct DenseArgs;
 struct DenseGradArgs;
 cudaError_t launch_rows_forward(const DenseArgs& a, cudaStream_t stream);  // rows <= 8 (vn_dense_rows.cu)
-cudaError_t launch_gather_forward(const DenseArgs& a, cudaStream_t stream);
-cudaError_t launch_gather_backward(const DenseGradArgs& a, cudaStream_t stream);
+cudaError_t launch_gather_forward(const DenseArgs& a, const GatherPlan& plan, cudaStream_t stream);
+cudaError_t launch_gather_backward(const DenseGradArgs& a, const GatherPlan& plan, cudaStream_t stream);
 cudaError_t take_gather_status(unsigned int* status, cudaStream_t stream);
 
 // Reads and clears the status word of the tensor-core products (0 = fine).

@@ -90,10 +90,10 @@ __device__ __forceinline__ void load_stage(uint32_t dst, const CUtensorMap* am, 
 
 template <bool kAMn, bool kBMn, bool kPair>
 __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t stage, uint32_t idesc, bool first) {
+  const uint64_t a = descriptor<kAMn>(stage), b = descriptor<kBMn>(stage + kABytes);
 #pragma unroll
   for (int ks = 0; ks < kK / 16; ++ks)
-    mma<kPair>(d, descriptor<kAMn>(stage + ks * kStepBytes<kAMn>),
-               descriptor<kBMn>(stage + kABytes + ks * kStepBytes<kBMn>), idesc, !(first && ks == 0));
+    mma<kPair>(d, further(a, ks * kStepBytes<kAMn>), further(b, ks * kStepBytes<kBMn>), idesc, !(first && ks == 0));
 }
 
 // ---------------------------------------------------------------- pairs of CTAs
@@ -534,24 +534,10 @@ bool make_result_map(CUtensorMap* map, const void* p, vn_dtype dt, int64_t np, i
 
 constexpr size_t kFixed = 1024 + 8 * (2 * kMaxStages + 14) + sizeof(Control);
 
-// Columns of a pair's tile: of the multiples of 16 from 128 to 256, the one with the least
-// work on the busiest pair -- rounds of tiles x (columns + 16, for what a tile costs beside its
-// products). 4096 x 4096 results on 76 pairs: 4 rounds of 224 columns, not 4 of 256.
-int pair_columns(int64_t np, int64_t nq, int pairs) {
-  int best = 256;
-  int64_t cost = INT64_MAX;
-  for (int bn = 256; bn >= 128; bn -= 16) {
-    const int64_t tiles = ((np + 255) / 256) * ((nq + bn - 1) / bn);
-    const int64_t c = (tiles + pairs - 1) / pairs * (bn + 16);
-    if (c < cost) { cost = c; best = bn; }
-  }
-  return best;
-}
-
 template <typename T, bool kAMn, bool kBMn, bool kStaged>
-cudaError_t run_pair_typed(const TcProduct& d, Params p, int sms, cudaStream_t stream) {
+cudaError_t run_pair_typed(const TcProduct& d, Params p, int sms, int bn, cudaStream_t stream) {
   const int pairs = sms / 2;
-  p.bn = pair_columns(d.np, d.nq, pairs);
+  p.bn = bn;
   CUtensorMap am, bm, ym, zm, rm;
   if (!make_map(&am, d.a, kAMn ? 64 : 128) || !make_map(&bm, d.b, kBMn ? 64 : p.bn / 2)) return cudaErrorInvalidValue;
   if (!make_result_map(&ym, kStaged ? d.out : nullptr, d.dt, d.np, d.nq) ||
@@ -573,11 +559,11 @@ cudaError_t run_pair_typed(const TcProduct& d, Params p, int sms, cudaStream_t s
                         kFixed + p.stages * kPairStageBytes + p.staging_bytes, stream, am, bm, ym, zm, rm, p);
 }
 template <typename T, bool kAMn, bool kBMn>
-cudaError_t run_pair(const TcProduct& d, const Params& p, int sms, cudaStream_t stream) {
+cudaError_t run_pair(const TcProduct& d, const Params& p, int sms, int bn, cudaStream_t stream) {
   auto fits = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
   const bool staged = d.np * sizeof(T) % 16 == 0 && fits(d.out) && fits(d.preact) && fits(d.residual);
-  return staged ? run_pair_typed<T, kAMn, kBMn, true>(d, p, sms, stream)
-                : run_pair_typed<T, kAMn, kBMn, false>(d, p, sms, stream);
+  return staged ? run_pair_typed<T, kAMn, kBMn, true>(d, p, sms, bn, stream)
+                : run_pair_typed<T, kAMn, kBMn, false>(d, p, sms, bn, stream);
 }
 
 template <typename T, int BN, bool kAMn, bool kBMn>
@@ -588,7 +574,7 @@ cudaError_t run_single(const TcProduct& d, Params p, int split, cudaStream_t str
   p.p_tiles = static_cast<int>((d.np + 127) / 128);
   p.q_tiles = static_cast<int>((d.nq + BN - 1) / BN);
   p.units = static_cast<int64_t>(p.p_tiles) * p.q_tiles;
-  p.stages = static_cast<int>(std::min<uint32_t>(kMaxStages, 200 * 1024 / kStage));
+  p.stages = static_cast<int>(std::min<uint32_t>(kMaxStages, 106496 / kStage));  // two CTAs an SM
   p.idesc = idesc_of(128, BN, kAMn, kBMn);
   if (p.units * split > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   static SmemRecord record;
@@ -597,7 +583,7 @@ cudaError_t run_single(const TcProduct& d, Params p, int split, cudaStream_t str
 }
 
 template <typename T, bool kAMn, bool kBMn>
-cudaError_t run(const TcProduct& d, cudaStream_t stream) {
+cudaError_t run(const TcProduct& d, const TilePlan& plan, cudaStream_t stream) {
   DeviceInfo dev;
   cudaError_t err = device_info(&dev);
   if (err != cudaSuccess) return err;
@@ -608,32 +594,25 @@ cudaError_t run(const TcProduct& d, cudaStream_t stream) {
   p.k_chunks = static_cast<int>((d.nk + kK - 1) / kK);
   p.iters = p.k_chunks * (d.a.planes == 3 ? 6 : 1);
   p.timeout_ns = kTimeoutNs;
-  if (fills_pairs(d.np, d.nq)) return run_pair<T, kAMn, kBMn>(d, p, dev.sm_count, stream);
-  // Columns a tile: all of q in one tile where 256 suffice, so that A is staged once; then as
-  // many CTAs on the k loop as leave each two stages and still fit the GPU at once.
-  const int64_t p_tiles = (d.np + 127) / 128;
-  const int bn = d.nq <= 16 ? 16 : d.nq <= 32 ? 32 : d.nq <= 64 ? 64 : 128;
-  const int64_t tiles = p_tiles * ((d.nq + bn - 1) / bn);
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= 2 * dev.sm_count && p.iters >= 2 * split * 2) split *= 2;
+  if (plan.pair) return run_pair<T, kAMn, kBMn>(d, p, dev.sm_count, plan.bn, stream);
+  const int split = 1 << plan.log_split;
   if constexpr (!kBMn) {
-    if (bn == 16) return run_single<T, 16, kAMn, kBMn>(d, p, split, stream);
-    if (bn == 32) return run_single<T, 32, kAMn, kBMn>(d, p, split, stream);
+    if (plan.bn == 16) return run_single<T, 16, kAMn, kBMn>(d, p, split, stream);
   }
-  if (bn <= 64) return run_single<T, 64, kAMn, kBMn>(d, p, split, stream);
+  if (plan.bn == 64) return run_single<T, 64, kAMn, kBMn>(d, p, split, stream);
   return run_single<T, 128, kAMn, kBMn>(d, p, split, stream);
 }
 
 template <typename T>
-cudaError_t run_layout(const TcProduct& d, cudaStream_t stream) {
-  if (!d.a.mn) return run<T, false, false>(d, stream);
-  return d.b.mn ? run<T, true, true>(d, stream) : run<T, true, false>(d, stream);
+cudaError_t run_layout(const TcProduct& d, const TilePlan& plan, cudaStream_t stream) {
+  if (!d.a.mn) return run<T, false, false>(d, plan, stream);
+  return d.b.mn ? run<T, true, true>(d, plan, stream) : run<T, true, false>(d, plan, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_tc_product(const TcProduct& d, cudaStream_t stream) {
-  return d.dt == VN_BF16 ? run_layout<__nv_bfloat16>(d, stream) : run_layout<float>(d, stream);
+cudaError_t launch_tc_product(const TcProduct& d, const TilePlan& plan, cudaStream_t stream) {
+  return d.dt == VN_BF16 ? run_layout<__nv_bfloat16>(d, plan, stream) : run_layout<float>(d, plan, stream);
 }
 
 cudaError_t take_dense_status(unsigned int* status, cudaStream_t stream) { return take_wait_status(status, stream); }

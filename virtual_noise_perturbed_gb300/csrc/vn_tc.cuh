@@ -59,6 +59,14 @@ __device__ __forceinline__ float load_cluster(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
@@ -209,6 +217,10 @@ __device__ __forceinline__ uint64_t descriptor(uint32_t addr) {
   d |= static_cast<uint64_t>(2) << 61;
   return d;
 }
+// An operand `bytes` further on (a multiple of 16): one addition, since no address carries out of
+// the descriptor's field. MMAs are issued by one thread, which building each descriptor
+// anew kept busy for longer than the MMAs take (3,100 cycles for the 24 of an fp32 chunk).
+__device__ __forceinline__ uint64_t further(uint64_t descriptor, uint32_t bytes) { return descriptor + (bytes >> 4); }
 // Bytes from one MMA's 16 k to the next within a stage.
 template <bool kMn>
 constexpr uint32_t kStepBytes = kMn ? 16 * 128 : 32;
@@ -223,8 +235,8 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 // The planes of A and B in the i-th of the six products: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0).
-__device__ __forceinline__ int plane_a(int i) { return (0b000001010010 >> (2 * i)) & 3; }
-__device__ __forceinline__ int plane_b(int i) { return (0b000100011000 >> (2 * i)) & 3; }
+__device__ __forceinline__ constexpr int plane_a(int i) { return (0b000001010010 >> (2 * i)) & 3; }
+__device__ __forceinline__ constexpr int plane_b(int i) { return (0b000100011000 >> (2 * i)) & 3; }
 
 struct Ring {
   int s = 0;
