@@ -255,3 +255,44 @@ def test_refusals():
     with pytest.raises(vn.VNError):
         opt.step([torch.ones(8, device=DEV)], lr=float("nan"))
     assert opt.steps == 0 and torch.equal(p, torch.ones(8, device=DEV))
+
+
+def _codes(x, root):
+    """The stored form of a flat moment in torch's fp32 operations, one rounding each."""
+    x = torch.nn.functional.pad(x, (0, -x.numel() % 256)).view(-1, 256)
+    top = x.abs().amax(1, keepdim=True)
+    scale = torch.where(top < 1e-30, torch.zeros_like(top), top * (1.0 / 448.0))
+    q = torch.where(scale == 0, torch.zeros_like(x), x * (torch.ones_like(scale) / scale))
+    q = q.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).float()
+    if root:
+        q = torch.where((q == 0) & (x > 0) & (scale > 0), torch.full_like(x, 2.0 ** -9), q)
+    return q, scale
+
+
+@pytest.mark.parametrize("maximize", [False, True])
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("n", [256 * 700, 256 * 700 + 19])
+def test_8_bit_codes_are_those_of_single_roundings(n, kind, maximize):
+    """Every operation on the way to a code is one fp32 rounding, so that the codes follow from the
+    formulas alone: bit for bit what torch's separate operations give, on aligned and ragged tensors."""
+    g = torch.Generator(device=DEV).manual_seed(n)
+    p = torch.randn(n, generator=g, device=DEV).to(KINDS[kind])
+    opt = vn.AdamW([p], lr=1e-3, betas=(0.9, 0.999), state_bits=8, maximize=maximize)
+    for _ in range(3):
+        s = opt.state
+        scale = lambda k: s[k].repeat_interleave(256)
+        m = s["m"].float() * scale("m_scale")
+        r = s["v"].float() * scale("v_scale")
+        gr = (torch.randn(n, generator=g, device=DEV) * torch.exp(3 * torch.randn(n, generator=g, device=DEV))).to(KINDS[kind])
+        opt.step([gr])
+        f = gr.float() * (-1.0 if maximize else 1.0)
+        m = m[:n] * 0.9 + f * (1 - 0.9)
+        v = (r * r)[:n] * 0.999 + (f * f) * (1 - 0.999)
+        for key, x, root in (("m", m, False), ("v", torch.sqrt(v), True)):
+            q, unit = _codes(x, root)
+            assert torch.equal(opt.state[key].float()[:n], q.view(-1)[:n]), key
+            assert torch.equal(opt.state[key + "_scale"], unit.view(-1)), key
+        em, ev = opt.moments()
+        assert torch.equal(em, opt.state["m"].float() * opt.state["m_scale"].repeat_interleave(256))
+        er = opt.state["v"].float() * opt.state["v_scale"].repeat_interleave(256)
+        assert torch.equal(ev, er * er)

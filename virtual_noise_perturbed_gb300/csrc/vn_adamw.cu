@@ -212,11 +212,16 @@ __device__ __forceinline__ void step_block(const Table<kCap>& t, const Entry& e,
         vv[q] = mul2(vv[q], f2(vs, vs));
         vv[q] = mul2(vv[q], vv[q]);
       }
-      mv[q] = add2(mul2(mv[q], f2(t.b1, t.b1)), mul2(gv[q], f2(t.c1, t.c1)));
-      vv[q] = add2(mul2(vv[q], f2(t.b2, t.b2)), mul2(mul2(gv[q], gv[q]), f2(t.c2, t.c2)));
-      float v0, v1, d0, d1;
-      split(vv[q], &v0, &v1);
-      split(mv[q], &m[h][2 * q], &m[h][2 * q + 1]);
+      // The sums as single instructions: two-lane ones the compiler contracts with the products.
+      float v0, v1, d0, d1, a0, a1;
+      split(mul2(mv[q], f2(t.b1, t.b1)), &v0, &v1);
+      split(mul2(gv[q], f2(t.c1, t.c1)), &a0, &a1);
+      m[h][2 * q] = __fadd_rn(v0, a0);
+      m[h][2 * q + 1] = __fadd_rn(v1, a1);
+      split(mul2(vv[q], f2(t.b2, t.b2)), &v0, &v1);
+      split(mul2(mul2(gv[q], gv[q]), f2(t.c2, t.c2)), &a0, &a1);
+      v0 = __fadd_rn(v0, a0);
+      v1 = __fadd_rn(v1, a1);
       const float r0 = __fsqrt_rn(v0), r1 = __fsqrt_rn(v1);
       split(fma2(f2(r0, r1), f2(t.inv_root, t.inv_root), f2(t.eps, t.eps)), &d0, &d1);
       const F2 move = mul2(f2(__fdividef(m[h][2 * q], d0), __fdividef(m[h][2 * q + 1], d1)), f2(t.size, t.size));
