@@ -25,6 +25,7 @@
 #include <cmath>
 
 #include "vn_internal.h"
+#include "vn_launch.cuh"
 #include "vn_pair.cuh"
 
 namespace vn {
@@ -296,6 +297,8 @@ __device__ __forceinline__ void step_block(const Table<kCap>& t, const Entry& e,
 // registers leave, 111 us with six.
 template <typename P, typename G, bool k8, int kCap>
 __global__ void __launch_bounds__(kThreads, 5) adamw_kernel(const __grid_constant__ Table<kCap> t) {
+  let_next();
+  after_previous();
   const int64_t chunk = blockIdx.x;
   int lo = 0, hi = t.count;  // the last entry whose first chunk is not beyond this one
   while (hi - lo > 1) {
@@ -313,8 +316,10 @@ __global__ void __launch_bounds__(kThreads, 5) adamw_kernel(const __grid_constan
 }
 
 __global__ void __launch_bounds__(kThreads)
-moments_kernel(const uint8_t* __restrict__ mc, const uint8_t* __restrict__ vc, const float* __restrict__ ms,
-               const float* __restrict__ vs, int64_t n, float* __restrict__ m, float* __restrict__ v, int vec) {
+moments_kernel(const uint8_t* mc, const uint8_t* vc, const float* ms,
+               const float* vs, int64_t n, float* m, float* v, int vec) {
+  let_next();
+  after_previous();
   const int64_t block = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int64_t base = block * kBlock;
   if (base >= n) return;
@@ -373,8 +378,8 @@ cudaError_t launch_table(const AdamwArgs& a, int64_t from, int64_t count, cudaSt
   }
   if (chunks == 0) return cudaSuccess;
   if (chunks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  adamw_kernel<P, G, k8, kCap><<<static_cast<unsigned>(chunks), kThreads, 0, stream>>>(t);
-  return cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>(chunks));
+  return launch_overlapped(adamw_kernel<P, G, k8, kCap>, grid, kThreads, 0, 0, stream, t);
 }
 
 // Tensors per launch: the table's 64 bytes a tensor must fit the 32,764 bytes of a kernel's
@@ -415,9 +420,8 @@ cudaError_t launch_adamw_moments(const void* mc, const void* vc, const float* ms
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   auto fits = [](const void* q, size_t bytes) { return reinterpret_cast<uintptr_t>(q) % bytes == 0; };
   const int vec = fits(mc, 4) && fits(vc, 4) && fits(m, 16) && fits(v, 16);
-  moments_kernel<<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(
-      static_cast<const uint8_t*>(mc), static_cast<const uint8_t*>(vc), ms, vs, n, m, v, vec);
-  return cudaGetLastError();
+  return launch_overlapped(moments_kernel, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream,
+                           static_cast<const uint8_t*>(mc), static_cast<const uint8_t*>(vc), ms, vs, n, m, v, vec);
 }
 
 }  // namespace vn

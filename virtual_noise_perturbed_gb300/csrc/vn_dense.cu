@@ -18,6 +18,7 @@
 #include "vn_act.cuh"
 #include "vn_dense.h"
 #include "vn_internal.h"
+#include "vn_launch.cuh"
 #include "vn_split.cuh"
 
 namespace vn {
@@ -52,6 +53,8 @@ struct Product {
 // 64 x 64 outputs a CTA, 4 x 4 a thread; 16 of k at a time through shared memory.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) product_kernel(const Product d) {
+  let_next();
+  after_previous();
   __shared__ float sa[kStep][kTile + 4], sb[kStep][kTile + 4];
   const int64_t p0 = static_cast<int64_t>(blockIdx.x % d.p_tiles) * kTile;
   const int64_t q0 = static_cast<int64_t>(blockIdx.x / d.p_tiles) * kTile;
@@ -201,8 +204,10 @@ struct Eight<float> {
 // A matrix as the tensor cores take it: rows padded to `pitch`, fp32 split into planes.
 template <typename T>
 __global__ void __launch_bounds__(256)
-convert_kernel(const T* __restrict__ src, int64_t rows, int64_t cols, void* __restrict__ dst, int64_t pitch,
+convert_kernel(const T* src, int64_t rows, int64_t cols, void* dst, int64_t pitch,
                int64_t plane, int vec) {
+  let_next();
+  after_previous();
   const int64_t groups = pitch / 8;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= rows * groups) return;
@@ -228,6 +233,8 @@ struct Delta {
 };
 template <typename T, int kPlanes>
 __global__ void __launch_bounds__(256) delta_kernel(const Delta a) {
+  let_next();
+  after_previous();
   __shared__ float s[8][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + lane * 8;
@@ -281,8 +288,8 @@ cudaError_t run_product(Product d, cudaStream_t stream) {
   d.p_tiles = (d.np + kTile - 1) / kTile;
   const int64_t q_tiles = (d.nq + kTile - 1) / kTile;
   if (d.p_tiles > 0x7FFFFFFFll / q_tiles) return cudaErrorInvalidConfiguration;
-  product_kernel<T><<<static_cast<unsigned>(d.p_tiles * q_tiles), kThreads, 0, stream>>>(d);
-  return cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>(d.p_tiles * q_tiles));
+  return launch_overlapped(product_kernel<T>, grid, kThreads, 0, 0, stream, d);
 }
 
 cudaError_t product(const Product& d, vn_dtype dt, cudaStream_t stream) {
@@ -440,7 +447,8 @@ BackwardPlan reckon_backward(int64_t rows, int64_t in, int64_t out, vn_dtype dt,
   p.dw = tile_plan(in, out, rows, dt, true);
   const bool direct = as_is(dt, in, aligned), keeps = act != VN_ACT_NONE || !as_is(dt, out, aligned);
   // d, and the bias's sums.
-  const double delta = 5.0 + (keeps ? 2.0 : 1.0) * static_cast<double>(rows) * static_cast<double>(out) * (dt == VN_BF16 ? 3 : 7) / 4e6;
+  const double elements = static_cast<double>(rows) * static_cast<double>(out);
+  const double delta = 5.0 + (keeps ? 2.0 : 1.0) * elements * (dt == VN_BF16 ? 3 : 7) / 4e6;
   if (p.dx.us + p.dw.us + delta + convert_us(out, in, dt, direct) + convert_us(rows, in, dt, direct) < p.gather.us)
     p.route = Route::kTiles;
   return p;
@@ -496,13 +504,12 @@ cudaError_t prepare(const void* p, vn_dtype dt, int64_t rows, int64_t cols, bool
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   const int vec = cols % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
   void* dst = const_cast<void*>(o->p);
+  const dim3 ctas(static_cast<unsigned>(grid));
   if (dt == VN_BF16)
-    convert_kernel<__nv_bfloat16><<<static_cast<unsigned>(grid), 256, 0, stream>>>(
-        static_cast<const __nv_bfloat16*>(p), rows, cols, dst, o->pitch, o->plane, vec);
-  else
-    convert_kernel<float><<<static_cast<unsigned>(grid), 256, 0, stream>>>(static_cast<const float*>(p), rows, cols,
-                                                                          dst, o->pitch, o->plane, vec);
-  return cudaGetLastError();
+    return launch_overlapped(convert_kernel<__nv_bfloat16>, ctas, 256, 0, 0, stream,
+                             static_cast<const __nv_bfloat16*>(p), rows, cols, dst, o->pitch, o->plane, vec);
+  return launch_overlapped(convert_kernel<float>, ctas, 256, 0, 0, stream, static_cast<const float*>(p), rows, cols, dst,
+                           o->pitch, o->plane, vec);
 }
 
 }  // namespace
@@ -570,10 +577,10 @@ cudaError_t delta_pass(const DenseGradArgs& a, const TcOperand* delta, float* pa
     const int64_t tiles = (a.out + 255) / 256;
     if (tiles > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(parts));
-    if (a.dt == VN_BF16) delta_kernel<__nv_bfloat16, 1><<<grid, 256, 0, stream>>>(k);
-    else if (delta != nullptr && delta->planes == 3) delta_kernel<float, 3><<<grid, 256, 0, stream>>>(k);
-    else delta_kernel<float, 1><<<grid, 256, 0, stream>>>(k);
-    const cudaError_t err = cudaGetLastError();
+    cudaError_t err;
+    if (a.dt == VN_BF16) err = launch_overlapped(delta_kernel<__nv_bfloat16, 1>, grid, 256, 0, 0, stream, k);
+    else if (delta != nullptr && delta->planes == 3) err = launch_overlapped(delta_kernel<float, 3>, grid, 256, 0, 0, stream, k);
+    else err = launch_overlapped(delta_kernel<float, 1>, grid, 256, 0, 0, stream, k);
     if (err != cudaSuccess) return err;
   }
   if (a.grad_b == nullptr || a.out == 0) return cudaSuccess;

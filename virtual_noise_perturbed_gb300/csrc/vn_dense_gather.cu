@@ -92,17 +92,17 @@ __device__ __forceinline__ Eight<float> load8(const float* base, int64_t rows, i
   const float* p = base + r * cols + c;
   const int left = static_cast<int>(min(static_cast<int64_t>(8), cols - c));
   if (vec) {
-    if (left > 0) e.a = __ldg(reinterpret_cast<const float4*>(p));
-    if (left > 4) e.b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    if (left > 0) e.a = fetch(reinterpret_cast<const float4*>(p));
+    if (left > 4) e.b = fetch(reinterpret_cast<const float4*>(p) + 1);
   } else {
-    if (left > 0) e.a.x = __ldg(p);
-    if (left > 1) e.a.y = __ldg(p + 1);
-    if (left > 2) e.a.z = __ldg(p + 2);
-    if (left > 3) e.a.w = __ldg(p + 3);
-    if (left > 4) e.b.x = __ldg(p + 4);
-    if (left > 5) e.b.y = __ldg(p + 5);
-    if (left > 6) e.b.z = __ldg(p + 6);
-    if (left > 7) e.b.w = __ldg(p + 7);
+    if (left > 0) e.a.x = fetch(p);
+    if (left > 1) e.a.y = fetch(p + 1);
+    if (left > 2) e.a.z = fetch(p + 2);
+    if (left > 3) e.a.w = fetch(p + 3);
+    if (left > 4) e.b.x = fetch(p + 4);
+    if (left > 5) e.b.y = fetch(p + 5);
+    if (left > 6) e.b.z = fetch(p + 6);
+    if (left > 7) e.b.w = fetch(p + 7);
   }
   return e;
 }
@@ -113,12 +113,12 @@ __device__ __forceinline__ Eight<__nv_bfloat16> load8(const __nv_bfloat16* base,
   if (r >= rows) return e;
   const int left = static_cast<int>(min(static_cast<int64_t>(8), cols - c));
   if (vec) {
-    if (left > 0) e.a = __ldg(reinterpret_cast<const uint4*>(base + r * cols + c));
+    if (left > 0) e.a = fetch(reinterpret_cast<const uint4*>(base + r * cols + c));
   } else {
     const unsigned short* p = reinterpret_cast<const unsigned short*>(base) + r * cols + c;
     uint32_t h[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) h[q] = q < left ? __ldg(p + q) : 0u;
+    for (int q = 0; q < 8; ++q) h[q] = q < left ? fetch(p + q) : 0u;
     e.a = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
   }
   return e;
@@ -153,13 +153,13 @@ __device__ __forceinline__ void store_planes(uint32_t addr, uint32_t plane, cons
 
 __device__ __forceinline__ Eight<float> load8(const float* p) {
   Eight<float> e;
-  e.a = __ldg(reinterpret_cast<const float4*>(p));
-  e.b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  e.a = fetch(reinterpret_cast<const float4*>(p));
+  e.b = fetch(reinterpret_cast<const float4*>(p) + 1);
   return e;
 }
 __device__ __forceinline__ Eight<__nv_bfloat16> load8(const __nv_bfloat16* p) {
   Eight<__nv_bfloat16> e;
-  e.a = __ldg(reinterpret_cast<const uint4*>(p));
+  e.a = fetch(reinterpret_cast<const uint4*>(p));
   return e;
 }
 
@@ -203,12 +203,12 @@ struct Gather {
 template <typename T>
 constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
 template <int BN>
-constexpr uint32_t kBBytes = BN < 64 ? BN * 128 : BN * 128;
+constexpr uint32_t kBBytes = BN * 128;
 template <typename T, int BN>
 constexpr uint32_t kStageBytes = kPlanes<T> * (kABytes + kBBytes<BN>);
 // Stages: in bf16 so that two CTAs share an SM.
 template <typename T, int BN>
-constexpr int kStages = sizeof(T) == 4 ? static_cast<int>(221184 / kStageBytes<T, BN>) : static_cast<int>(106496 / kStageBytes<T, BN>);
+constexpr int kStages = static_cast<int>((sizeof(T) == 4 ? 221184 : 106496) / kStageBytes<T, BN>);
 
 // Accumulators of a tile. MMAs into one accumulator follow each other at the latency of an MMA (about 100
 // cycles, three times what one with 64 columns takes), and each rounds its sum towards zero: n steps
@@ -480,6 +480,8 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   __syncthreads();
   fence_after();
   const uint32_t tmem = *s_tmem;
+  let_next();
+  after_previous();
   const int cta = g.cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int block = static_cast<int>(blockIdx.x);
   if constexpr (kBackward) {

@@ -15,6 +15,7 @@
 #include "vn_act.cuh"
 #include "vn_dense.h"
 #include "vn_internal.h"
+#include "vn_launch.cuh"
 
 namespace vn {
 namespace {
@@ -36,7 +37,7 @@ template <typename T, int V>
 struct Group {
   uint4 raw;
   __device__ __forceinline__ void load_stream(const T* p) { raw = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void load(const T* p) { raw = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load(const T* p) { raw = fetch(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void zero() { raw = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void get(float (&v)[V]) const {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -56,7 +57,7 @@ template <typename T>
 struct Group<T, 1> {
   T e;
   __device__ __forceinline__ void load_stream(const T* p) { e = __ldcs(p); }
-  __device__ __forceinline__ void load(const T* p) { e = __ldg(p); }
+  __device__ __forceinline__ void load(const T* p) { e = fetch(p); }
   __device__ __forceinline__ void zero() { e = narrow<T>(0.f); }
   __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = value(e); }
 };
@@ -64,6 +65,8 @@ struct Group<T, 1> {
 // kRows: rows rounded up to 1, 2, 4 or 8. slices: warps that share a pair of features.
 template <typename T, int V, int kRows>
 __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const DenseArgs a, int slices) {
+  let_next();
+  after_previous();
   constexpr int kDepth = kRows <= 2 ? 4 : 2;  // steps of k whose loads are in flight at once
   __shared__ float s[kWarps][kFeatures * kRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -145,8 +148,8 @@ cudaError_t run(const DenseArgs& a, int slices, cudaStream_t stream) {
   const int64_t per = kWarps / slices * kFeatures;
   const int64_t grid = (a.out + per - 1) / per;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  rows_kernel<T, V, kRows><<<static_cast<unsigned>(grid), kWarps * 32, 0, stream>>>(a, slices);
-  return cudaGetLastError();
+  return launch_overlapped(rows_kernel<T, V, kRows>, dim3(static_cast<unsigned>(grid)), kWarps * 32, 0, 0, stream, a,
+                           slices);
 }
 
 template <typename T, int V>

@@ -155,6 +155,8 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
   cluster_sync();
   fence_after();
   const uint32_t tmem = *s_tmem;
+  let_next();
+  after_previous();
   // The peer waits here from its start, so for the whole run of the leader's waits.
   const unsigned long long drain_ns = 4 * p.timeout_ns;
   const int half_q = p.bn / 2;  // rows of B in each CTA
@@ -373,6 +375,8 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
   __syncthreads();
   fence_after();
   const uint32_t tmem = *s_tmem;
+  let_next();
+  after_previous();
   bool ok = true;
 
   if (warp == 0) {

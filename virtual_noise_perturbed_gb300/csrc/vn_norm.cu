@@ -21,6 +21,7 @@
 #include <algorithm>
 
 #include "vn_internal.h"
+#include "vn_launch.cuh"
 #include "vn_pair.cuh"
 
 namespace vn {
@@ -71,7 +72,7 @@ __device__ __forceinline__ void load_param(const void* w, int bf16, int64_t i, f
   } else if (bf16) {
     const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(w) + i;
     if constexpr (V == 8) {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+      const uint4 a = fetch(reinterpret_cast<const uint4*>(p));
       const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -79,7 +80,7 @@ __device__ __forceinline__ void load_param(const void* w, int bf16, int64_t i, f
         v[2 * q + 1] = __uint_as_float(u[q] & 0xFFFF0000u);
       }
     } else if constexpr (V == 4) {
-      const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
+      const uint2 a = fetch(reinterpret_cast<const uint2*>(p));
       v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xFFFF0000u);
       v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xFFFF0000u);
     } else {
@@ -90,11 +91,11 @@ __device__ __forceinline__ void load_param(const void* w, int bf16, int64_t i, f
     if constexpr (V > 1) {
 #pragma unroll
       for (int q = 0; q < V; q += 4) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p + q));
+        const float4 a = fetch(reinterpret_cast<const float4*>(p + q));
         v[q] = a.x; v[q + 1] = a.y; v[q + 2] = a.z; v[q + 3] = a.w;
       }
     } else {
-      v[0] = __ldg(p);
+      v[0] = fetch(p);
     }
   }
 }
@@ -197,6 +198,8 @@ constexpr int cta_threads(int t) { return t < 64 ? 128 : t; }
 // Rows of 16-byte packs, NV of them a thread.
 template <typename X, int T, int NV>
 __global__ void __launch_bounds__(cta_threads(T)) norm_pairs_kernel(const NormArgsK a) {
+  let_next();
+  after_previous();
   constexpr int kRows = cta_threads(T) / T, V = 16 / sizeof(X), P = kPairs<X>;
   __shared__ float scratch[T > 32 ? 64 : 1];
   int turn = 0;
@@ -261,6 +264,8 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_pairs_kernel(const NormAr
 // Rows that 16-byte packs do not divide: single elements, NV of them a thread.
 template <typename X, int T, int V, int NV>
 __global__ void __launch_bounds__(cta_threads(T)) norm_kernel(const NormArgsK a) {
+  let_next();
+  after_previous();
   constexpr int kRows = cta_threads(T) / T;
   __shared__ float scratch[T > 32 ? 64 : 1];
   int turn = 0;
@@ -315,6 +320,8 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_kernel(const NormArgsK a)
 // mostly from L2).
 template <typename X>
 __global__ void __launch_bounds__(512) norm_long_kernel(const NormArgsK a) {
+  let_next();
+  after_previous();
   __shared__ float scratch[64];
   int turn = 0;
   const int64_t row = blockIdx.x;
@@ -357,6 +364,8 @@ struct NormGradK {
 
 template <typename X, int T, int V, int NV>
 __global__ void __launch_bounds__(cta_threads(T)) norm_grad_kernel(const NormGradK a) {
+  let_next();
+  after_previous();
   constexpr int kRows = cta_threads(T) / T;
   __shared__ float scratch[T > 32 ? 128 : 1];
   extern __shared__ float columns[];  // T == 32: kRows x 2 x n column sums to be added
@@ -470,6 +479,8 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_grad_kernel(const NormGra
 // instructions an element were the next bound (193 us on 32768 x 4096 bf16).
 template <typename X, int T, int NV>
 __global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, const int depth) {
+  let_next();
+  after_previous();
   constexpr int V = 16 / sizeof(X), P = kPairs<X>;
   extern __shared__ uint4 ring[];  // [depth][2][NV][T]
   __shared__ float scratch[128];
@@ -615,6 +626,8 @@ __global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, co
 // Long rows: grad_x in two passes over the row ...
 template <typename X>
 __global__ void __launch_bounds__(512) norm_grad_long_kernel(const NormGradK a) {
+  let_next();
+  after_previous();
   __shared__ float scratch[128];
   int turn = 0;
   const int64_t row = blockIdx.x;
@@ -643,6 +656,8 @@ __global__ void __launch_bounds__(512) norm_grad_long_kernel(const NormGradK a) 
 // every gridDim.y-th row.
 template <typename X>
 __global__ void __launch_bounds__(256) norm_columns_kernel(const NormGradK a) {
+  let_next();
+  after_previous();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= a.n) return;
   float dw = 0.f, db = 0.f;
@@ -661,8 +676,10 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormGradK a) {
 // n .. 2n-1. 32 columns a CTA; warp k adds every 16th part from k, then the warps' sums.
 constexpr int kSumWarps = 16;
 __global__ void __launch_bounds__(kSumWarps * 32)
-column_sum_kernel(const float* __restrict__ part, int64_t parts, int64_t width, int64_t n, void* o1, void* o2,
+column_sum_kernel(const float* part, int64_t parts, int64_t width, int64_t n, void* o1, void* o2,
                   int bf16) {
+  let_next();
+  after_previous();
   __shared__ float s[kSumWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
@@ -691,11 +708,11 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 template <typename X, int T, int V, int NV>
 cudaError_t run_norm(const NormArgsK& a, cudaStream_t stream) {
   constexpr int kRows = cta_threads(T) / T;
-  const int64_t grid = (a.rows + kRows - 1) / kRows;
-  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  if constexpr (V > 1) norm_pairs_kernel<X, T, NV><<<static_cast<unsigned>(grid), cta_threads(T), 0, stream>>>(a);
-  else norm_kernel<X, T, V, NV><<<static_cast<unsigned>(grid), cta_threads(T), 0, stream>>>(a);
-  return cudaGetLastError();
+  const int64_t ctas = (a.rows + kRows - 1) / kRows;
+  if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(ctas));
+  if constexpr (V > 1) return launch_overlapped(norm_pairs_kernel<X, T, NV>, grid, cta_threads(T), 0, 0, stream, a);
+  else return launch_overlapped(norm_kernel<X, T, V, NV>, grid, cta_threads(T), 0, 0, stream, a);
 }
 
 // The threads of a row by its number of packs: as few as 8 packs a thread allow, so that many rows
@@ -713,8 +730,7 @@ cudaError_t norm_by_length(const NormArgsK& a, cudaStream_t stream) {
   if (packs <= 2048) return run_norm<X, 256, V, 8>(a, stream);
   if (packs <= 4096) return run_norm<X, 512, V, 8>(a, stream);
   if (a.rows > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  norm_long_kernel<X><<<static_cast<unsigned>(a.rows), 512, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(norm_long_kernel<X>, dim3(static_cast<unsigned>(a.rows)), 512, 0, 0, stream, a);
 }
 
 template <typename X>
@@ -730,8 +746,8 @@ constexpr int64_t kMaxParts = 152 * 4;
 template <typename X, int T, int V, int NV>
 cudaError_t run_norm_grad(const NormGradK& a, int64_t parts, cudaStream_t stream) {
   const size_t smem = T == 32 ? sizeof(float) * 2 * (cta_threads(T) / T) * a.n : 0;
-  norm_grad_kernel<X, T, V, NV><<<static_cast<unsigned>(parts), cta_threads(T), smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(norm_grad_kernel<X, T, V, NV>, dim3(static_cast<unsigned>(parts)), cta_threads(T), 0, smem,
+                           stream, a);
 }
 
 template <typename X, int T, int NV>
@@ -744,8 +760,8 @@ cudaError_t run_norm_grad_ring(const NormGradK& a, int64_t parts, cudaStream_t s
   const cudaError_t err =
       ensure_dynamic_smem(reinterpret_cast<const void*>(norm_grad_ring_kernel<X, T, NV>), kSmem, record);
   if (err != cudaSuccess) return err;
-  norm_grad_ring_kernel<X, T, NV><<<static_cast<unsigned>(parts), T, kSmem, stream>>>(a, kDepth);
-  return cudaGetLastError();
+  return launch_overlapped(norm_grad_ring_kernel<X, T, NV>, dim3(static_cast<unsigned>(parts)), T, 0, kSmem, stream, a,
+                           kDepth);
 }
 
 template <typename X, int V>
@@ -775,13 +791,12 @@ cudaError_t norm_grad_by_length(const NormGradK& a, int64_t* parts, cudaStream_t
     if (a.n <= 512 * 16) { *parts = ctas(512); return run_norm_grad<X, 512, V, 16>(a, *parts, stream); }
   }
   if (a.rows > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  norm_grad_long_kernel<X><<<static_cast<unsigned>(a.rows), 512, 0, stream>>>(a);
-  cudaError_t err = cudaGetLastError();
+  cudaError_t err = launch_overlapped(norm_grad_long_kernel<X>, dim3(static_cast<unsigned>(a.rows)), 512, 0, 0, stream, a);
   if (err != cudaSuccess || a.part == nullptr) return err;
   const int64_t tiles = (a.n + 255) / 256;
   *parts = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(a.rows, kMaxParts), 4 * 152 / tiles));
-  norm_columns_kernel<X><<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(*parts)), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(*parts));
+  return launch_overlapped(norm_columns_kernel<X>, grid, 256, 0, 0, stream, a);
 }
 
 template <typename X>
@@ -808,8 +823,8 @@ cudaError_t launch_column_sum(const float* part, int64_t parts, int64_t width, i
                                  vn_dtype dt, cudaStream_t stream) {
   const int64_t grid = (width + 31) / 32;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  column_sum_kernel<<<static_cast<unsigned>(grid), kSumWarps * 32, 0, stream>>>(part, parts, width, n, o1, o2, dt == VN_BF16);
-  return cudaGetLastError();
+  return launch_overlapped(column_sum_kernel, dim3(static_cast<unsigned>(grid)), kSumWarps * 32, 0, 0, stream, part,
+                           parts, width, n, o1, o2, dt == VN_BF16);
 }
 
 cudaError_t launch_layer_norm_backward(const NormGradArgs& a, cudaStream_t stream) {

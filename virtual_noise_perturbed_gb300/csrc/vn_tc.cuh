@@ -13,6 +13,7 @@
 
 #include "vn_act.cuh"
 #include "vn_internal.h"
+#include "vn_launch.cuh"
 
 namespace vn {
 namespace {
@@ -311,18 +312,7 @@ cudaError_t launch_cluster(void (*fn)(KArgs...), SmemRecord& record, int grid, i
                            cudaStream_t stream, Args... args) {
   const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(fn), smem, record);
   if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, args...);
+  return launch_overlapped(fn, dim3(static_cast<unsigned>(grid)), threads, cluster, smem, stream, args...);
 }
 
 // Reads and clears this translation unit's status word.
