@@ -8,7 +8,9 @@
 //   forward  p = out, q = row, k = in    A = W (k contiguous)   B = x (k contiguous)
 //   dx       p = in,  q = row, k = out   A = W (p contiguous)   B = d (k contiguous)
 //   dw       p = in,  q = out, k = row   A = x (p contiguous)   B = d (q contiguous)
-// so one kernel with two stride pairs serves all three.
+// so every kernel serves all three. Which one a call goes to is reckoned from its sizes (below): few
+// rows, operands gathered by threads, or tiles by TMA, whose operands are converted first where TMA
+// cannot take them.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -308,9 +310,9 @@ int64_t operand_bytes(int64_t rows, int64_t cols, vn_dtype dt) {
 bool as_is(vn_dtype dt, int64_t cols, bool aligned) { return dt == VN_BF16 && cols % 8 == 0 && aligned; }
 
 // ---------------------------------------------------------------- which kernel
-// The times below are what the kernels took on a GB300, launch included, over sizes from 64 to 8192: a
-// few microseconds a launch, and a CTA's (or pair's) time per 64 of k. They are reckoned here, from
-// sizes alone, so that a call and its workspace agree without a device.
+// The times below are what calls one after the other took on a GB300, over sizes from 64 to 8192: a few
+// microseconds a launch, more of them the larger its tile, and a CTA's (or pair's) time per 64 of k.
+// They are reckoned here, from sizes alone, so that a call and its workspace agree without a device.
 enum class Route {
   kRows,    // up to 8 rows: vn_dense_rows.cu
   kPlain,   // 64 x 64 tiles without tensor cores: sizes beyond 32-bit coordinates
@@ -337,23 +339,25 @@ TilePlan tile_plan(int64_t np, int64_t nq, int64_t nk, vn_dtype dt, bool b_mn) {
     return best;
   }
   const double iters = tiles_of(nk, 64) * (dt == VN_BF16 ? 1 : 6);
-  // Pairs: rounds of tiles over 76 pairs x (k loop, bound by the loads of 128 rows of A and bn / 2 of B
-  // an SM rather than by its products, + what a tile costs besides). 4096 x 4096 results: 4 rounds of 224
-  // columns rather than 4 of 256; 1024 x 1024: one round of 64.
+  // Pairs: rounds of tiles over 76 pairs. Up to 128 columns the four MMAs of 64 k take as long as each
+  // other's latency; with every SM at work, operands come slower. 256 x 4096 to 4096 in bf16: one
+  // round of 64 columns 14.8 us, of 128 15.5, of 256 24.7; 4096 cubed: 4 rounds of 224 columns 76, 4 of
+  // 256 81, 7 of 128 95.
   for (int bn = 256; bn >= 32; bn -= 16) {
     const double rounds = std::ceil(tiles_of(np, 256) * tiles_of(nq, bn) / 76);
-    const double us = 5.0 + rounds * (iters * (420 + bn) + 1000 + 16 * bn) / 1900;
+    const double stage = rounds > 1 ? 0.135 + 0.00059 * bn : std::max(0.15, 0.00104 * bn);
+    const double us = 4.0 + rounds * iters * stage + (rounds - 1) * 0.8 + 0.0165 * bn;
     if (us < best.us) best = TilePlan{us, true, bn, 0};
   }
   // Single CTAs, two an SM, which then share its loads.
   for (int bn : {16, 64, 128}) {
     if (b_mn && bn == 16) continue;
-    const double stage = bn == 128 ? 0.36 : bn == 64 ? 0.27 : 0.22;
+    const double stage = bn == 128 ? 0.29 : bn == 64 ? 0.25 : 0.22;
     for (int l = 0; l < 4; ++l) {
       const double ctas = tiles_of(np, 128) * tiles_of(nq, bn) * (1 << l);
       const double rounds = std::ceil(ctas / resident(l, 2));
-      const double us = 5.0 + (l > 0 ? 1.0 + 0.015 * bn : 0.0) +
-                        rounds * (std::ceil(iters / (1 << l)) * stage * (ctas > 152 ? 1.9 : 1.0) + 2.0);
+      const double us = (bn == 128 ? 5.3 : bn == 64 ? 2.6 : 1.9) + (l > 0 ? 0.4 + 1.4 * l : 0.0) +
+                        rounds * (std::ceil(iters / (1 << l)) * stage * (ctas > 152 ? 1.6 : 1.0) + 2.0);
       if (us < best.us) best = TilePlan{us, false, bn, l};
     }
   }
@@ -370,11 +374,12 @@ GatherPlan gather_plan(const Shape (&shapes)[2], vn_dtype dt, bool backward, boo
   const bool bf16 = dt == VN_BF16;
   for (int bn : {16, 64, 128}) {
     if (backward && bn == 16) continue;
-    const double stage = (vectors ? 1.0 : 1.6) *  // loads of single elements
-                         (backward    ? (bn == 128 ? (bf16 ? 2.9 : 3.3) : (bf16 ? 1.8 : 1.9))
-                          : bn == 128 ? (bf16 ? 1.8 : 1.9)
-                          : bn == 64  ? (bf16 ? 1.2 : 1.25)
-                                      : 0.9);
+    const double stage = (vectors ? 1.0 : bf16 ? 3.5 : 1.7) *  // loads of single elements
+                         (backward    ? (bn == 128 ? (bf16 ? 2.2 : 3.1) : (bf16 ? 1.2 : 1.7))
+                          : bn == 128 ? (bf16 ? 0.9 : 1.4)
+                          : bn == 64  ? (bf16 ? 0.65 : 1.2)
+                                      : (bf16 ? 0.75 : 0.95));
+    const double launch = backward ? (bf16 || bn == 128 ? 5.3 : 6.7) : bn == 128 ? 8.5 : bn == 64 ? 6.0 : 3.5;
     for (int l0 = 0; l0 < 4; ++l0)
       for (int l1 = 0; l1 < (backward ? 4 : 1); ++l1) {
         const int l[2] = {l0, l1};
@@ -383,14 +388,15 @@ GatherPlan gather_plan(const Shape (&shapes)[2], vn_dtype dt, bool backward, boo
           const Shape& s = shapes[i];
           if (s.np == 0 || s.nq == 0) continue;
           const double n = tiles_of(s.np, 128) * tiles_of(s.nq, bn) * (1 << l[i]);
-          const double t = std::ceil(tiles_of(s.nk, 64) / (1 << l[i])) * stage + 5.0 + (l[i] > 0 ? 1.5 : 0.0);
+          const double t = std::ceil(tiles_of(s.nk, 64) / (1 << l[i])) * stage + launch + (l[i] > 0 ? 1.5 : 0.0) +
+                           (backward && bn == 128 ? 2.0 * l[i] : 0.0);
           ctas += n;
           work += n * t;
           longest = std::max(longest, t);
         }
         const double room = resident(std::max(l0, l1), bf16 ? 2 : 1);
         // Two CTAs of an SM share its threads' time.
-        const double crowd = bf16 && ctas > 152 ? 1.7 : 1.0;
+        const double crowd = bf16 && ctas > resident(std::max(l0, l1), 1) ? 1.7 : 1.0;
         const double us = crowd * (ctas <= room ? longest : std::max(longest, work / room) + 0.5 * longest);
         if (us < best.us) {
           best.us = us;
@@ -448,7 +454,7 @@ BackwardPlan reckon_backward(int64_t rows, int64_t in, int64_t out, vn_dtype dt,
   const bool direct = as_is(dt, in, aligned), keeps = act != VN_ACT_NONE || !as_is(dt, out, aligned);
   // d, and the bias's sums.
   const double elements = static_cast<double>(rows) * static_cast<double>(out);
-  const double delta = 5.0 + (keeps ? 2.0 : 1.0) * elements * (dt == VN_BF16 ? 3 : 7) / 4e6;
+  const double delta = 8.0 + (keeps ? 2.0 : 1.0) * elements * (dt == VN_BF16 ? 3 : 7) / 4e6;
   if (p.dx.us + p.dw.us + delta + convert_us(out, in, dt, direct) + convert_us(rows, in, dt, direct) < p.gather.us)
     p.route = Route::kTiles;
   return p;

@@ -235,7 +235,7 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (S + s); };
   const uint32_t done = bar0 + 8u * (2 * S);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   // `cta` is this CTA's rank in the cluster, `base` that of the first CTA on the same tile.
   const int split = 1 << d.log_split, rank = cta & (split - 1), base = cta - rank;
   const int unit = ((block - cta) >> d.log_split) + (cta >> d.log_split);
@@ -306,7 +306,7 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
         rg.next(S);
       }
     }
-  } else if (lane == 0) {
+  } else if (elect_one()) {
     const uint32_t idesc = idesc_of(128, BN, kAMn, kBMn);
     Ring rg;
     for (int it = first; it < last; ++it, rg.next(S)) {
@@ -329,9 +329,7 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
       mma_commit<false>(empty(rg.s));
     }
     mma_commit<false>(done);  // also after an abort: what was issued completes
-    const uint64_t t0 = global_ns();
-    while (!mbar_try(done, 0) && global_ns() - t0 < g.timeout_ns) {
-    }
+    settle(done, 0, g.timeout_ns);
   }
   __syncwarp();
   fence_before();
@@ -367,7 +365,7 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
           uint32_t v[16];
           __syncwarp();
           tmem_load16(at + acc * BN + c, v);
-          tmem_wait_load();
+          tmem_wait_load(v);
 #pragma unroll
           for (int i = 0; i < 16; ++i) z[i] += __uint_as_float(v[i]);
         }
@@ -458,8 +456,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   const int warp = threadIdx.x >> 5;
   {
     // Every warp reads one 64-byte line of the parameters: their misses in the constant cache
-    // then overlap each other and the setup, instead of meeting the epilogue one by one (3,300
-    // cycles of 14,000 on 1024 x 256 x 256).
+    // then overlap each other and the setup, instead of meeting the epilogue one by one.
     static_assert(sizeof(GatherParams) <= 9 * 64, "a line of the parameters for each of 9 warps");
     const int at = min(warp * 16, static_cast<int>(sizeof(GatherParams) / 4) - 1);
     asm volatile("" ::"r"(reinterpret_cast<const uint32_t*>(&g)[at]));

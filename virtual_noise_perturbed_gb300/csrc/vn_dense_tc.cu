@@ -18,9 +18,13 @@
 //          A and of B, half of what single CTAs would stage for as many products, and L2
 //          carries half as much. Persistent; two accumulators of 256 columns in TMEM, so that a
 //          tile's epilogue runs under the next tile's products.
-//   single 128 x 16..256 tiles of one CTA, for problems that do not fill the GPU with
-//          pairs: the k loop is split over the CTAs of a cluster of up to 8, whose partial
-//          sums are added through distributed shared memory in rank order.
+//   single 128 x 16, 64 or 128 tiles of one CTA, two CTAs an SM, for problems that do not fill the
+//          GPU with pairs: the k loop is split over the CTAs of a cluster of up to 8, whose
+//          partial sums are added through distributed shared memory in rank order.
+// What bounds the pairs (8192 x 4096 to 4096 in bf16, 141 us, cuBLAS 138): the tensor cores, at 519 cycles
+// for 64 k of a 256 x 256 tile where its MMAs take 512, under the power cap's clock of 1.75 GHz. With a
+// GELU, a residual and the pre-activation (180 us) the epilogue's copies and instructions
+// get in the way of the operands' and the MMAs': 620 cycles.
 //
 // Warp roles: 0 TMA producer, 1 TMEM allocation and MMA issue, from 2 on epilogue (one or two
 // per TMEM lane quarter). Every barrier wait is bounded; one that runs out records a status word,
@@ -99,15 +103,18 @@ __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t stage, uint32_t
 // ---------------------------------------------------------------- pairs of CTAs
 // Staged epilogue: each half of the epilogue warps (128 threads, half the tile's columns)
 // moves 16 columns x 128 p at a time through shared memory, residual in and outputs out by
-// TMA, double buffered: whole 256-byte rows travel, and no warp waits on a load of its own.
-// Straight 2-byte loads and stores of the same tile were the bound (455 us against 166 us without
-// residual and pre-activation, on 8192 x 4096 x 4096).
+// TMA: whole 256-byte rows travel, and no warp waits on a load of its own. Straight 2-byte loads
+// and stores of the same tile were the bound (455 us against 166 us without
+// residual and pre-activation, on 8192 x 4096 x 4096). A chunk has one of three buffers, where an output
+// takes its residual's place, and there are three for the pre-activation: with two, a chunk took
+// as long as its predecessor's copy out of shared memory.
+constexpr int kBuffers = 3;
 template <typename T>
 constexpr uint32_t kChunkBytes = 16 * 128 * sizeof(T);
 constexpr uint32_t kPairStageBytes = kABytes + 128 * 128;
 
 // Barriers: full[S] (leader's, armed for both CTAs' bytes), empty[S], tmem_full[2],
-// tmem_empty[2] (leader's, both CTAs' epilogues), drain, residual[2 halves][2].
+// tmem_empty[2] (leader's, both CTAs' epilogues), drain, residual[2 halves][kBuffers].
 template <typename T, bool kAMn, bool kBMn, bool kStaged>
 __global__ void __launch_bounds__(kPairThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
@@ -124,13 +131,13 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
   auto tmem_full = [&](int b) { return bar0 + 8u * (2 * S + b); };
   auto tmem_empty = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
   const uint32_t drain = bar0 + 8u * (2 * S + 4);
-  auto arrived = [&](int h, int b) { return bar0 + 8u * (2 * S + 5 + 2 * h + b); };
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * S + 9);
-  // Whether the half's leader saw its wait through: [half][tile's accumulator, or 2 for a residual].
-  volatile int* s_go = reinterpret_cast<volatile int*>(bars + 2 * S + 10);
-  volatile Control* ctl = reinterpret_cast<volatile Control*>(bars + 2 * S + 13);
+  auto arrived = [&](int h, int b) { return bar0 + 8u * (2 * S + 5 + kBuffers * h + b); };
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 2 * kBuffers);
+  // Whether the half's leader saw its wait for the tile through: [half][accumulator].
+  volatile int* s_go = reinterpret_cast<volatile int*>(bars + 2 * S + 6 + 2 * kBuffers);
+  volatile Control* ctl = reinterpret_cast<volatile Control*>(bars + 2 * S + 8 + 2 * kBuffers);
   const uint32_t stage0 = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
@@ -144,7 +151,7 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
       mbar_init(tmem_empty(b), 2 * 8);
     }
     mbar_init(drain, 1);
-    for (int b = 0; b < 4; ++b) mbar_init(arrived(b >> 1, b & 1), 1);
+    for (int b = 0; b < 2 * kBuffers; ++b) mbar_init(arrived(0, b), 1);
     ctl->abort = 0;
     ctl->timeout_ns = p.timeout_ns;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -162,7 +169,7 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
   const int half_q = p.bn / 2;  // rows of B in each CTA
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       Ring rg;
       bool ok = true;
       const int blocks = (half_q + 63) / 64;
@@ -190,26 +197,28 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       Ring rg, tb;
-      bool ok = true;
+      bool ok = true, ready = false;
       for (int64_t u = pair; ok && u < p.units; u += pairs, tb.next(2)) {
         if (!(ok = mbar_wait(tmem_empty(tb.s), tb.ph ^ 1u, ctl))) break;
         fence_after();
-        for (int it = 0; it < p.iters; ++it, rg.next(S)) {
-          if (!(ok = mbar_wait(full(rg.s), rg.ph, ctl))) break;
+        for (int it = 0; it < p.iters; ++it) {
+          if (!ready && !(ok = mbar_wait(full(rg.s), rg.ph, ctl))) break;
           fence_after();
-          issue_stage<kAMn, kBMn, true>(tmem + tb.s * 256, stage0 + rg.s * kPairStageBytes, p.idesc, it == 0);
-          mma_commit<true>(empty(rg.s));
+          const int s = rg.s;
+          rg.next(S);
+          ready = mbar_done(full(rg.s), rg.ph);  // the next stage, while this one's MMAs are issued
+          issue_stage<kAMn, kBMn, true>(tmem + tb.s * 256, stage0 + s * kPairStageBytes, p.idesc, it == 0);
+          mma_commit<true>(empty(s));
         }
         if (ok) mma_commit<true>(tmem_full(tb.s));
       }
       mma_commit<true>(drain);
     }
-    if (lane == 0) {  // both CTAs: every MMA of the pair is complete
-      const uint64_t t0 = global_ns();
-      while (!mbar_try(drain, 0) && global_ns() - t0 < drain_ns) {
-      }
+    __syncwarp();
+    if (elect_one()) {  // both CTAs: every MMA of the pair is complete
+      settle(drain, 0, drain_ns);
     }
   } else {
     const int quarter = warp & 3;
@@ -217,16 +226,13 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
     const int half = (p.bn / 16 + 1) / 2 * 16;  // columns of half 0
     const int c0 = h * half, width = h ? p.bn - half : half;
     const bool leader = quarter == 2 && lane == 0;  // warps 2 and 6
-    // Two chunks each of y, of the residual and of the pre-activation, the latter two where given.
+    // The chunks' buffers, then the pre-activation's.
     T* const buf = reinterpret_cast<T*>(staging + h * (p.staging_bytes / 2));
     const uint32_t buf0 = smem_u32(buf);
     constexpr int kChunk = 16 * 128;
     const bool has_r = p.residual != nullptr, has_z = p.preact != nullptr;
-    const int z_at = has_r ? 4 : 2;
-    Ring tb;
-    uint32_t jj = 0;  // chunks so far
-    bool go = true;
-    for (int64_t u = pair; go && u < p.units; u += pairs, tb.next(2)) {
+    Ring tb, ck;  // accumulators, chunks' buffers
+    for (int64_t u = pair; u < p.units; u += pairs, tb.next(2)) {
       int tp, tq;
       tile_of(p, u, &tp, &tq);
       const int p0 = tp * 256 + static_cast<int>(rank) * 128;
@@ -236,67 +242,74 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
       const int cols = static_cast<int>(min(static_cast<int64_t>(width), p.nq - q0));
       const uint32_t d = tmem + tb.s * 256 + c0 + (static_cast<uint32_t>(quarter * 32) << 16);
       if constexpr (kStaged) {
-        auto fetch = [&](uint32_t j, int c) {
-          mbar_expect_tx(arrived(h, j & 1), kChunkBytes<T>);
-          tma_load_2d(buf0 + (2 + (j & 1)) * kChunkBytes<T>, &rmap, arrived(h, j & 1), p0, static_cast<int>(q0) + c);
+        auto fetch = [&](int b, int c) {
+          mbar_expect_tx(arrived(h, b), kChunkBytes<T>);
+          tma_load_2d(buf0 + b * kChunkBytes<T>, &rmap, arrived(h, b), p0, static_cast<int>(q0) + c);
         };
+        Ring second = ck;
+        second.next(kBuffers);
         if (leader) {
-          if (has_r && cols > 0) fetch(jj, 0);
-          s_go[3 * h + tb.s] = mbar_wait(tmem_full(tb.s), tb.ph, ctl);
+          if (has_r) {  // the outputs that were in these buffers have left
+            bulk_wait_read<1>();
+            if (cols > 0) fetch(ck.s, 0);
+            if (cols > 16) fetch(second.s, 16);
+          }
+          s_go[2 * h + tb.s] = mbar_wait(tmem_full(tb.s), tb.ph, ctl);
         }
         named_barrier(1 + h, 128);
-        go = s_go[3 * h + tb.s] != 0;
-        if (!go) {  // the residual on its way has to land before the CTA ends
-          if (leader && has_r && cols > 0) mbar_wait(arrived(h, jj & 1), (jj >> 1) & 1u, ctl);
+        if (s_go[2 * h + tb.s] == 0) {  // the residual on its way has to land before the CTA ends
+          if (leader && has_r && cols > 0) settle(arrived(h, ck.s), ck.ph, p.timeout_ns);
+          if (leader && has_r && cols > 16) settle(arrived(h, second.s), second.ph, p.timeout_ns);
           break;
         }
         fence_after();
+        __syncwarp();
+        uint32_t v[16];
+        if (cols > 0) tmem_load16(d, v);
 #pragma unroll 1
-        for (int c = 0; c < cols; c += 16, ++jj) {
-          uint32_t v[16];
-          __syncwarp();
-          tmem_load16(d + c, v);
-          if (leader && has_r && c + 16 < cols) fetch(jj + 1, c + 16);
-          __syncwarp();
-          tmem_wait_load();
+        for (int c = 0; c < cols; c += 16, ck.next(kBuffers)) {
           float z[16];
           T pre[16];
+          __syncwarp();
+          tmem_wait_load(v);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             z[i] = __uint_as_float(v[i]) + bias;
             pre[i] = narrow<T>(z[i]);
           }
+          __syncwarp();
+          if (c + 16 < cols) tmem_load16(d + c + 16, v);
           activate_all<sizeof(T) == 2>(p.act, z);
-          if (leader) {  // the outputs' buffers are free again, and the residual is there
-            bulk_wait_read<1>();
-            if (has_r) s_go[3 * h + 2] = mbar_wait(arrived(h, jj & 1), (jj >> 1) & 1u, ctl);
-          }
-          named_barrier(1 + h, 128);
-          const int row = quarter * 32 + lane;
+          T* const y = buf + ck.s * kChunk + quarter * 32 + lane;
           if (has_r) {
-            if (!(go = s_go[3 * h + 2] != 0)) break;
-            (void)mbar_try(arrived(h, jj & 1), (jj >> 1) & 1u);
-            const T* r = buf + (2 + (jj & 1)) * kChunk + row;
+            // A wait that ran out ends no thread here, where the others would miss it at the
+            // barrier: the products have ended with it, and the next tile's wait is the last.
+            mbar_wait(arrived(h, ck.s), ck.ph, ctl);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) z[i] += value(r[i * 128]);
+            for (int i = 0; i < 16; ++i) z[i] += value(y[i * 128]);
           }
-          T* y = buf + (jj & 1) * kChunk + row;
 #pragma unroll
           for (int i = 0; i < 16; ++i) y[i * 128] = narrow<T>(z[i]);
           if (has_z) {
-            T* zo = buf + (z_at + (jj & 1)) * kChunk + row;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) zo[i * 128] = pre[i];
+            for (int i = 0; i < 16; ++i) y[kBuffers * kChunk + i * 128] = pre[i];
           }
           fence_async_smem();
+          // One barrier a chunk: it is written, and the next one's buffers have been read out (the
+          // leader waits for all copies but the last one's here).
+          if (leader) bulk_wait_read<1>();
           named_barrier(1 + h, 128);
           if (leader) {
-            tma_store_2d(&ymap, buf0 + (jj & 1) * kChunkBytes<T>, p0, static_cast<int>(q0) + c);
-            if (has_z) tma_store_2d(&zmap, buf0 + (z_at + (jj & 1)) * kChunkBytes<T>, p0, static_cast<int>(q0) + c);
+            const uint32_t from = buf0 + ck.s * kChunkBytes<T>;
+            tma_store_2d(&ymap, from, p0, static_cast<int>(q0) + c);
+            if (has_z) tma_store_2d(&zmap, from + kBuffers * kChunkBytes<T>, p0, static_cast<int>(q0) + c);
             bulk_commit();
+            if (has_r && c + 32 < cols) {
+              bulk_wait_read<1>();  // the chunk before this one, whose buffer it is
+              fetch(ck.s == 0 ? kBuffers - 1 : ck.s - 1, c + 32);
+            }
           }
         }
-        if (!go) break;
       } else {
         Residual<T> r;
         load_residual(p, q0, pp, cols, &r);
@@ -309,7 +322,7 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
           tmem_load16(d + c, v);
           Residual<T> ahead;
           load_residual(p, q0 + c + 16, pp, cols - c - 16, &ahead);
-          tmem_wait_load();
+          tmem_wait_load(v);
           float z[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(v[i]);
@@ -353,7 +366,7 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * S + 1);
   volatile Control* ctl = reinterpret_cast<volatile Control*>(bars + 2 * S + 2);
   const uint32_t stage0 = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
   int tp, tq;
   tile_of(p, blockIdx.x / split, &tp, &tq);
@@ -380,7 +393,7 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
   bool ok = true;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       Ring rg;
       uint32_t issued = 0;
       const bool planes = p.iters != p.k_chunks;
@@ -396,14 +409,12 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
       if (!ok) {  // wait, bounded, for the copies in flight
         for (uint32_t k = 0; k < static_cast<uint32_t>(S) && k < issued; ++k) {
           const uint32_t j = issued - 1 - k;
-          const uint64_t t0 = global_ns();
-          while (!mbar_try(full(static_cast<int>(j % S)), (j / S) & 1u) && global_ns() - t0 < p.timeout_ns) {
-          }
+          settle(full(static_cast<int>(j % S)), (j / S) & 1u, p.timeout_ns);
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       Ring rg;
       for (int it = first; it < last; ++it, rg.next(S)) {
         if (!(ok = mbar_wait(full(rg.s), rg.ph, ctl))) break;
@@ -412,9 +423,7 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
         mma_commit<false>(empty(rg.s));
       }
       mma_commit<false>(tmem_full);  // also after an abort: what was issued completes
-      const uint64_t t0 = global_ns();
-      while (!mbar_try(tmem_full, 0) && global_ns() - t0 < p.timeout_ns) {
-      }
+      settle(tmem_full, 0, p.timeout_ns);
     }
   } else {
     const int quarter = warp & 3;
@@ -434,7 +443,7 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
       for (int c = 0; c < cols; c += 16) {
         uint32_t v[16];
         tmem_load16(d + c, v);
-        tmem_wait_load();
+        tmem_wait_load(v);
         if (split == 1) {
           float z[16];
 #pragma unroll
@@ -536,7 +545,7 @@ bool make_result_map(CUtensorMap* map, const void* p, vn_dtype dt, int64_t np, i
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr size_t kFixed = 1024 + 8 * (2 * kMaxStages + 14) + sizeof(Control);
+constexpr size_t kFixed = 1024 + 8 * (2 * kMaxStages + 8 + 2 * kBuffers) + sizeof(Control);
 
 template <typename T, bool kAMn, bool kBMn, bool kStaged>
 cudaError_t run_pair_typed(const TcProduct& d, Params p, int sms, int bn, cudaStream_t stream) {
@@ -553,10 +562,10 @@ cudaError_t run_pair_typed(const TcProduct& d, Params p, int sms, int bn, cudaSt
   p.units = static_cast<int64_t>(p.p_tiles) * p.q_tiles;
   p.idesc = idesc_of(256, p.bn, kAMn, kBMn);
   const int grid = static_cast<int>(std::min<int64_t>(2 * p.units, 2 * pairs));
-  const int chunks = kStaged ? 2 * (1 + (d.preact != nullptr) + (d.residual != nullptr)) : 0;
+  const int chunks = kStaged ? kBuffers * (d.preact != nullptr ? 2 : 1) : 0;
   p.staging_bytes = 2 * chunks * kChunkBytes<T>;
-  // As many stages as the rest of the 227 KB holds: 4 to 6 (in bf16 6, or 5 with both a
-  // residual and a pre-activation). 4 instead of 6 cost 5 to 12 per cent.
+  // As many stages as the rest of the 227 KB holds: 4 to 6 (in bf16 6, or 5 with a pre-activation). 4
+  // instead of 6 cost 5 to 12 per cent.
   p.stages = std::min<int>(kMaxStages, static_cast<int>((232448 - kFixed - p.staging_bytes) / kPairStageBytes));
   static SmemRecord record;
   return launch_cluster(pair_kernel<T, kAMn, kBMn, kStaged>, record, grid, kPairThreads, 2,

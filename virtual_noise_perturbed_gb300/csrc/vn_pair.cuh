@@ -5,10 +5,10 @@
 
 namespace vn {
 
-// Two fp32 values in one register pair, and the two-lane instructions on them. The compiler may contract
-// a product and a sum of them to a multiply-add, .rn or not: where every rounding counts, sums are
-// taken as single instructions. One of these does the
-// work of two where issue slots are what a kernel runs out of.
+// Two fp32 values in one register pair, and the two-lane instructions on them: one does the work of two
+// where issue slots are what a kernel runs out of. The compiler may contract a product and a sum of
+// them to a multiply-add, .rn or not: where every rounding counts, sums are taken as single
+// instructions.
 using F2 = unsigned long long;
 __device__ __forceinline__ F2 f2(float a, float b) {
   F2 d;
