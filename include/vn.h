@@ -319,15 +319,17 @@ vn_status vn_es_update(float* theta, const float* grad, int64_t n, double lr, vo
  *     z = x W^T + b,   y = act(z) + residual
  * x [rows, in], w [out, in], residual [rows, out] or NULL, y [rows, out] and preact
  * [rows, out] or NULL (receives z, for vn_linear_backward): all of type dt. b [out] of
- * b_dt or NULL. Products are exact and sums are held in fp32; y and preact are each
- * rounded once, y from the unrounded z. in == 0 gives z = b.
+ * b_dt or NULL. Sums are held in fp32; act is good to 2^-20 (1 + |z|) or better; y and
+ * preact are each rounded once, y from the unrounded z. in == 0 gives z = b.
  * workspace: vn_linear_workspace bytes of device memory, 256-byte aligned, in use until
- * the call's work on `stream` is done (NULL when that is 0). With dt VN_F32 and larger
- * sizes the matrices are split into three bf16 terms each there (exact: 8 + 8 + 8
- * significant bits) and multiplied on the tensor cores by the six products of the terms
- * that reach fp32's precision; there an infinity gives NaN where the exact sum would be
- * infinite. Errors: VN_ERR_WORKSPACE, and those of vn_perturbed_linear. The tensor-core
- * kernels bound their waits: results are valid only after vn_device_status returned VN_OK.
+ * the call's work on `stream` is done (NULL when that is 0). With dt VN_F32 and more than
+ * 8 rows the matrices are split into three bf16 terms each (exact: 8 + 8 + 8 significant
+ * bits; in the workspace for larger sizes) and multiplied on the tensor cores by the six
+ * products of the terms that reach fp32's precision; there an infinity gives NaN where the
+ * exact sum would be infinite. Errors: VN_ERR_WORKSPACE, and those of vn_perturbed_linear.
+ * The tensor-core kernels bound their waits: results are valid only after vn_device_status
+ * returned VN_OK. This call's kernels, and those of the other calls of this part, may start
+ * while the kernel before them on `stream` ends; they touch memory after it.
  */
 vn_status vn_linear(const void* x, const void* w, vn_dtype dt, const void* b, vn_dtype b_dt,
                     const void* residual, int64_t rows, int64_t in, int64_t out, vn_act act,
@@ -344,9 +346,9 @@ int64_t vn_linear_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, 
  * (the residual's gradient is grad itself). grad [rows, out], x [rows, in], w [out, in]
  * and preact [rows, out] (z as vn_linear stored it; NULL with VN_ACT_NONE) of type dt;
  * grad_x [rows, in] and grad_w [out, in] of type dt, either may be NULL (not computed);
- * grad_b [out] of gb_dt or NULL. For bf16 matrices with an activation d is rounded once to bf16 before
- * the two products (as the tensor cores take it); grad_b sums the unrounded d. Sums are held
- * in fp32 in a fixed order. rows == 0 gives zero grad_w and grad_b. Workspace, errors and
+ * grad_b [out] of gb_dt or NULL. For bf16 matrices with an activation d is rounded once to
+ * bf16 before the two products (as the tensor cores take it); grad_b sums the unrounded d.
+ * Sums are held in fp32 in a fixed order. rows == 0 gives zero grad_w and grad_b. Workspace, errors and
  * status as for vn_linear.
  */
 vn_status vn_linear_backward(const void* grad, const void* x, const void* w, const void* preact,
@@ -365,8 +367,8 @@ int64_t vn_linear_backward_workspace(int64_t rows, int64_t in, int64_t out, vn_d
  *     mean = sum_k x_k / n,  rstd = 1 / sqrt(sum_k (x_k - mean)^2 / n + eps),
  *     y_k = (x_k - mean) rstd w_k + b_k
  * x and y [rows, n] of dt; w and b [n] of w_dt, each may be NULL (1 and 0); mean and rstd
- * [rows] fp32, each may be NULL (not stored). n >= 1; eps finite and >= 0. All arithmetic in fp32,
- * the variance from the centred values; y is rounded once.
+ * [rows] fp32, each may be NULL (not stored). n >= 1; eps finite and >= 0. All arithmetic in
+ * fp32, the variance from the centred values; y is rounded once.
  */
 vn_status vn_layer_norm(const void* x, vn_dtype dt, const void* w, const void* b, vn_dtype w_dt,
                         int64_t rows, int64_t n, double eps, void* y, float* mean, float* rstd,
@@ -414,10 +416,10 @@ typedef struct vn_adamw_tensor {
  * (vn_gradient_ex and the others). step counts from 1. state_bits 32 or 8. With 8 bits a
  * moment is stored per block of 256 elements of its tensor as the block's largest magnitude
  * / 448 (its scale) and e4m3 codes in units of it; exp_avg_sq's codes are of sqrt(v), of
- * which a positive one is never stored as 0 (it divides the next step): at least 2^-9. A block whose
- * largest magnitude is below 1e-30 is stored as zeros. The step itself uses the unrounded moments;
- * a gradient that is not finite makes its block's moments not finite. Tensors of a
- * call may not overlap one another. 0 <= beta < 1, eps >= 0, all finite.
+ * which a positive one is never stored as 0 (it divides the next step): at least 2^-9. A
+ * block whose largest magnitude is below 1e-30 is stored as zeros. The step itself uses the
+ * unrounded moments; a gradient that is not finite makes its block's moments not finite.
+ * Tensors of a call may not overlap one another. 0 <= beta < 1, eps >= 0, all finite.
  */
 vn_status vn_adamw(const vn_adamw_tensor* tensors, int64_t n_tensors, vn_dtype param_dt,
                    vn_dtype grad_dt, int state_bits, double lr, double beta1, double beta2,
