@@ -374,7 +374,8 @@ GatherPlan gather_plan(const Shape (&shapes)[2], vn_dtype dt, bool backward, boo
   const bool bf16 = dt == VN_BF16;
   for (int bn : {16, 64, 128}) {
     if (backward && bn == 16) continue;
-    const double stage = (vectors ? 1.0 : bf16 ? 3.5 : 1.7) *  // loads of single elements
+    if (backward && bf16 && !vectors && bn == 128) continue;  // not built
+    const double stage = (vectors ? 1.0 : !bf16 ? 1.7 : backward ? 2.4 : 2.0) *  // rows that start anywhere
                          (backward    ? (bn == 128 ? (bf16 ? 2.2 : 3.1) : (bf16 ? 1.2 : 1.7))
                           : bn == 128 ? (bf16 ? 0.9 : 1.4)
                           : bn == 64  ? (bf16 ? 0.65 : 1.2)
@@ -383,20 +384,23 @@ GatherPlan gather_plan(const Shape (&shapes)[2], vn_dtype dt, bool backward, boo
     for (int l0 = 0; l0 < 4; ++l0)
       for (int l1 = 0; l1 < (backward ? 4 : 1); ++l1) {
         const int l[2] = {l0, l1};
-        double work = 0, longest = 0, ctas = 0;
+        double work = 0, longest = 0, ctas = 0, chunks = 0;
         for (int i = 0; i < 2; ++i) {
           const Shape& s = shapes[i];
           if (s.np == 0 || s.nq == 0) continue;
           const double n = tiles_of(s.np, 128) * tiles_of(s.nq, bn) * (1 << l[i]);
+          chunks = std::max(chunks, std::ceil(tiles_of(s.nk, 64) / (1 << l[i])));
           const double t = std::ceil(tiles_of(s.nk, 64) / (1 << l[i])) * stage + launch + (l[i] > 0 ? 1.5 : 0.0) +
                            (backward && bn == 128 ? 2.0 * l[i] : 0.0);
           ctas += n;
           work += n * t;
           longest = std::max(longest, t);
         }
-        const double room = resident(std::max(l0, l1), bf16 ? 2 : 1);
+        const int per_sm = bf16 && (vectors || bn < 128) ? 2 : 1;
+        const double room = resident(std::max(l0, l1), per_sm);
         // Two CTAs of an SM share its threads' time.
-        const double crowd = bf16 && ctas > resident(std::max(l0, l1), 1) ? 1.7 : 1.0;
+        double crowd = per_sm == 2 && ctas > resident(std::max(l0, l1), 1) ? 1.7 : 1.0;
+        if (!backward) crowd = (longest + (crowd - 1) * 0.4 * chunks * stage) / std::max(longest, 1e-9);
         const double us = crowd * (ctas <= room ? longest : std::max(longest, work / room) + 0.5 * longest);
         if (us < best.us) {
           best.us = us;
@@ -411,7 +415,7 @@ GatherPlan gather_plan(const Shape (&shapes)[2], vn_dtype dt, bool backward, boo
 // Converting a matrix for the tensor cores.
 double convert_us(int64_t rows, int64_t cols, vn_dtype dt, bool as_it_is) {
   if (as_it_is) return 0;
-  return 2.5 + static_cast<double>(rows) * static_cast<double>(cols) * (dt == VN_BF16 ? 4 : 10) / 4e6;
+  return 3.2 + static_cast<double>(rows) * static_cast<double>(cols) * (dt == VN_BF16 ? 4 : 10) / 4e6;
 }
 
 struct ForwardPlan {

@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "vn_act.cuh"
 #include "vn_dense.h"
@@ -76,6 +77,7 @@ struct Eight<float> {
 template <>
 struct Eight<__nv_bfloat16> {
   uint4 a;
+  __device__ __forceinline__ uint4 words() const { return a; }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -107,19 +109,56 @@ __device__ __forceinline__ Eight<float> load8(const float* base, int64_t rows, i
   return e;
 }
 __device__ __forceinline__ Eight<__nv_bfloat16> load8(const __nv_bfloat16* base, int64_t rows, int64_t cols, int64_t r,
-                                                      int64_t c, int vec) {
+                                                      int64_t c, int) {
   Eight<__nv_bfloat16> e;
   e.a = make_uint4(0u, 0u, 0u, 0u);
-  if (r >= rows) return e;
-  const int left = static_cast<int>(min(static_cast<int64_t>(8), cols - c));
-  if (vec) {
-    if (left > 0) e.a = fetch(reinterpret_cast<const uint4*>(base + r * cols + c));
-  } else {
-    const unsigned short* p = reinterpret_cast<const unsigned short*>(base) + r * cols + c;
-    uint32_t h[8];
+  if (r < rows && c < cols) e.a = fetch(reinterpret_cast<const uint4*>(base + r * cols + c));
+  return e;
+}
+// Eight bf16 elements that start anywhere, as the two aligned 16-byte words that hold them (where those
+// lie within the matrix; else the elements one by one): put in place when they are used, so
+// that the loads of a chunk are all on their way at once. In the gradients 64 of k take 2.9 us a CTA,
+// where loads of single elements took 4.4 (1.2 where rows start on 16 bytes).
+struct Shifted {
+  uint4 a, b;
+  uint32_t how;  // elements of a before the first, and 16 times the number of elements (8: all)
+  __device__ __forceinline__ uint4 words() const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t x[6], y[5], z[4];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) h[q] = q < left ? fetch(p + q) : 0u;
-    e.a = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+    for (int i = 0; i < 6; ++i) x[i] = how & 4 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) y[i] = how & 2 ? x[i + 1] : x[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] = __funnelshift_r(y[i], y[i + 1], (how & 1) * 16);
+    const int left = static_cast<int>(how >> 4);
+    if (left < 8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[i] = left >= 2 * i + 2 ? z[i] : left > 2 * i ? z[i] & 0xFFFFu : 0u;
+    }
+    return make_uint4(z[0], z[1], z[2], z[3]);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { Eight<__nv_bfloat16>{words()}.get(v); }
+};
+__device__ __forceinline__ Shifted load_shifted(const __nv_bfloat16* base, int64_t rows, int64_t cols, int64_t r, int64_t c) {
+  Shifted e;
+  e.a = e.b = make_uint4(0u, 0u, 0u, 0u);
+  e.how = 0;
+  if (r >= rows || c >= cols) return e;
+  const int left = static_cast<int>(min(static_cast<int64_t>(8), cols - c));
+  const int64_t at = r * cols + c;
+  const __nv_bfloat16* p = base + at;
+  const int before = static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16 / 2);
+  if (at >= before && at - before + (before > 0 ? 16 : 8) <= rows * cols) {
+    const uint4* q = reinterpret_cast<const uint4*>(p - before);
+    e.a = fetch(q);
+    if (before > 0) e.b = fetch(q + 1);
+    e.how = static_cast<uint32_t>(before | (left << 4));
+  } else {
+    const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+    auto one = [&](int q) { return q < left ? static_cast<uint32_t>(fetch(h + q)) : 0u; };
+    e.a = make_uint4(one(0) | (one(1) << 16), one(2) | (one(3) << 16), one(4) | (one(5) << 16), one(6) | (one(7) << 16));
+    e.how = 8u << 4;
   }
   return e;
 }
@@ -151,6 +190,19 @@ __device__ __forceinline__ void store_planes(uint32_t addr, uint32_t plane, cons
   }
 }
 
+// A group as it was loaded: in bf16 a copy.
+template <typename T, typename E>
+__device__ __forceinline__ void store_group(uint32_t addr, uint32_t plane, const E& e) {
+  if constexpr (sizeof(T) == 2) {
+    const uint4 w = e.words();
+    st_shared16(addr, w.x, w.y, w.z, w.w);
+  } else {
+    float v[8];
+    e.get(v);
+    store_planes<T>(addr, plane, v);
+  }
+}
+
 __device__ __forceinline__ Eight<float> load8(const float* p) {
   Eight<float> e;
   e.a = fetch(reinterpret_cast<const float4*>(p));
@@ -166,14 +218,14 @@ __device__ __forceinline__ Eight<__nv_bfloat16> load8(const __nv_bfloat16* p) {
 // A tile's operand of kRows rows x 64 k, gathered by 256 threads, kCount groups of eight each.
 // Group g of thread t is number g * 256 + t; eight lanes take one 128-byte row of the tile
 // (16 lanes 128 elements of p or q).
-template <typename T, bool kMn, int kRows>
+template <typename T, bool kMn, int kRows, bool kShift>
 struct Gather {
   static constexpr int kCount = kRows * 8 / kGatherThreads > 0 ? kRows * 8 / kGatherThreads : 1;
   static constexpr bool kAll = kRows * 8 >= kGatherThreads;  // every thread has a group
   static constexpr int kAcross = kMn ? kRows / 8 : 8;        // groups along the contiguous dimension
   static constexpr int kNext = kGatherThreads / kAcross;     // tile rows from one group of a thread to its next
   static_assert(kGatherThreads % kAcross == 0, "a thread's groups share their place along a row");
-  Eight<T> v[kCount];
+  std::conditional_t<kShift, Shifted, Eight<T>> v[kCount];
 
   // All of the tile's rows, and all of its 64 k, lie inside: plain vector loads.
   static __device__ __forceinline__ bool inside(const Source& s, int64_t base, int64_t k0) {
@@ -183,7 +235,10 @@ struct Gather {
     if (!kAll && t >= kRows * 8) return;
     const int row = t / kAcross, col = t % kAcross;
     const int64_t r = (kMn ? k0 : base) + row, c = (kMn ? base : k0) + col * 8;
-    if (inside(s, base, k0)) {
+    if constexpr (kShift) {
+#pragma unroll
+      for (int g = 0; g < kCount; ++g) v[g] = load_shifted(p, s.rows, s.cols, r + g * kNext, c);
+    } else if (inside(s, base, k0)) {
       const T* at = p + r * s.cols + c;
       const int64_t next = kNext * s.cols;
 #pragma unroll
@@ -226,7 +281,7 @@ constexpr uint32_t kTmemCols = (kLead<T, BN> + kRest<T, BN>) * BN <= 32    ? 32
 
 // One product's tile. kSum: also the sums of B over k (the bias's gradient), by the tiles of p's
 // first 128. Called by every thread of the CTA.
-template <typename T, int BN, bool kAMn, bool kBMn, bool kSum>
+template <typename T, int BN, bool kShift, bool kAMn, bool kBMn, bool kSum>
 __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8_t* smem, uint64_t* bars, uint32_t tmem,
                                      volatile Control* ctl, int block, int cta) {
   constexpr int S = kStages<T, BN>;
@@ -251,8 +306,8 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
 
   if (warp < 8) {
     const int t = threadIdx.x;
-    Gather<T, kAMn, 128> ga;
-    Gather<T, kBMn, BN> gb, gz;
+    Gather<T, kAMn, 128, kShift> ga;
+    Gather<T, kBMn, BN, kShift> gb, gz;
     const T* ap = static_cast<const T*>(d.a.p);
     const T* bp = static_cast<const T*>(d.b.p);
     const T* zp = static_cast<const T*>(d.b.z);
@@ -271,13 +326,16 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
         const uint32_t stage = stage0 + rg.s * kStage;
 #pragma unroll
         for (int i = 0; i < ga.kCount; ++i) {
-          float v[8];
-          ga.v[i].get(v);
-          store_planes<T>(stage + ga.offset(i, t), kABytes, v);
+          store_group<T>(stage + ga.offset(i, t), kABytes, ga.v[i]);
         }
         if (gb.kAll || t < BN * 8) {
 #pragma unroll
           for (int i = 0; i < gb.kCount; ++i) {
+            const uint32_t at = stage + kPlanes<T> * kABytes + gb.offset(i, t);
+            if (!kSum && !sloped) {
+              store_group<T>(at, kBBytes<BN>, gb.v[i]);
+              continue;
+            }
             float v[8];
             gb.v[i].get(v);
             if (sloped) {
@@ -289,7 +347,7 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
 #pragma unroll
               for (int q = 0; q < 8; ++q) sum[q] += v[q];
             }
-            store_planes<T>(stage + kPlanes<T> * kABytes + gb.offset(i, t), kBBytes<BN>, v);
+            store_planes<T>(at, kBBytes<BN>, v);
           }
         }
       }
@@ -444,8 +502,10 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
 
 // kBackward: parts 0 and 1 are dx (A = W, B = d) and dw (A = x, B = d^T, with the bias's sums);
 // otherwise part 0 is the forward product.
-template <typename T, int BN, bool kBackward>
-__global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ GatherParams g) {
+// In bf16 the registers of two CTAs fit an SM, as their stages do (but not with 128 columns of shifted groups).
+template <typename T, int BN, bool kBackward, bool kShift>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !(kShift && BN == 128) ? 2 : 1)
+gather_kernel(const __grid_constant__ GatherParams g) {
   constexpr int S = kStages<T, BN>;
   constexpr uint32_t kCols = kTmemCols<T, BN>;
   extern __shared__ uint8_t smem_raw[];
@@ -484,11 +544,11 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   if constexpr (kBackward) {
     // The weight's gradient first: its k loop, over the rows, tends to be the longer one.
     if (block < g.part[1].blocks)
-      tile<T, BN, true, true, true>(g.part[1], g, smem, bars, tmem, ctl, block, cta);
+      tile<T, BN, kShift, true, true, true>(g.part[1], g, smem, bars, tmem, ctl, block, cta);
     else
-      tile<T, BN, true, false, false>(g.part[0], g, smem, bars, tmem, ctl, block - g.part[1].blocks, cta);
+      tile<T, BN, kShift, true, false, false>(g.part[0], g, smem, bars, tmem, ctl, block - g.part[1].blocks, cta);
   } else {
-    tile<T, BN, false, false, false>(g.part[0], g, smem, bars, tmem, ctl, block, cta);
+    tile<T, BN, kShift, false, false, false>(g.part[0], g, smem, bars, tmem, ctl, block, cta);
   }
   __syncwarp();
   fence_before();
@@ -503,7 +563,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
 template <typename T, int BN, bool kBackward>
 constexpr size_t kSmemBytes = 1024 + kStages<T, BN> * kStageBytes<T, BN> + 8 * (2 * kStages<T, BN> + 2) + sizeof(Control);
 
-template <typename T, int BN, bool kBackward>
+template <typename T, int BN, bool kBackward, bool kShift>
 cudaError_t run(GatherParams& g, const int (&log_split)[2], cudaStream_t stream) {
   int64_t blocks = 0;
   g.cluster = 1 << std::max(log_split[0], log_split[1]);
@@ -523,17 +583,29 @@ cudaError_t run(GatherParams& g, const int (&log_split)[2], cudaStream_t stream)
   constexpr int S = kStages<T, BN>;
   static_assert(S >= 2 && S * kStageBytes<T, BN> >= (BN + 4) * 512 + 8192, "the partial sums lie in the stages");
   static SmemRecord record;
-  return launch_cluster(gather_kernel<T, BN, kBackward>, record, static_cast<int>(blocks), kThreads, g.cluster,
+  return launch_cluster(gather_kernel<T, BN, kBackward, kShift>, record, static_cast<int>(blocks), kThreads, g.cluster,
                         kSmemBytes<T, BN, kBackward>, stream, g);
 }
 
+template <typename T, bool kBackward, bool kShift>
+cudaError_t run_tile(GatherParams& g, const GatherPlan& plan, cudaStream_t stream) {
+  if constexpr (!kBackward) {
+    if (plan.bn == 16) return run<T, 16, kBackward, kShift>(g, plan.log_split, stream);
+  }
+  // Gradients of 128 columns would hold 108 registers of shifted groups.
+  if constexpr (!(kBackward && kShift)) {
+    if (plan.bn == 128) return run<T, 128, kBackward, kShift>(g, plan.log_split, stream);
+  }
+  return run<T, 64, kBackward, kShift>(g, plan.log_split, stream);
+}
 template <typename T, bool kBackward>
 cudaError_t run_plan(GatherParams& g, const GatherPlan& plan, cudaStream_t stream) {
-  if constexpr (!kBackward) {
-    if (plan.bn == 16) return run<T, 16, kBackward>(g, plan.log_split, stream);
+  if constexpr (sizeof(T) == 2) {
+    bool vec = true;
+    for (const Part& d : g.part) vec = vec && (d.np == 0 || d.nq == 0 || (d.a.vec && d.b.vec));
+    if (!vec) return run_tile<T, kBackward, true>(g, plan, stream);
   }
-  return plan.bn == 64 ? run<T, 64, kBackward>(g, plan.log_split, stream)
-                       : run<T, 128, kBackward>(g, plan.log_split, stream);
+  return run_tile<T, kBackward, false>(g, plan, stream);
 }
 
 Source source(const void* p, const void* z, int64_t rows, int64_t cols, vn_dtype dt) {
