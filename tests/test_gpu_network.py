@@ -445,3 +445,72 @@ def test_refusals():
         vn.layer_norm_backward(x, x, torch.ones(4, device=DEV), torch.ones(3, device=DEV))
     with pytest.raises(TypeError):
         vn.layer_norm_backward(x, x, torch.ones(3, device=DEV).double(), torch.ones(3, device=DEV))
+
+
+# Rows that start anywhere: lengths beside every boundary of the kernels' choices, and tensors that start
+# on any element between others' memory.
+ANY_N = (3, 9, 17, 31, 65, 127, 129, 250, 257, 301, 511, 513, 1023, 1025, 2047, 2049, 4095, 4097, 8191, 8193, 16383)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("n", ANY_N)
+def test_layer_norm_of_any_length(n, kind):
+    for rows in (1, 5, 1300):
+        if rows * n > 4_000_000:
+            continue
+        test_layer_norm(rows, n, kind, "fp32")
+        check_norm_backward(rows, n, kind, "fp32")
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("n", (7, 61, 255, 517, 1021, 3001))
+def test_layer_norm_does_not_depend_on_the_place(n, kind):
+    """NaN around the inputs reaches nothing, and what lies around the outputs stays. (Odd lengths: where
+    16-byte loads divide a row, aligned tensors have a kernel, and an order of sums, of their own.)"""
+    g, x, w, b = norm_inputs(19, n, kind, "fp32")
+    d = normal(g, (19, n), kind)
+    y, mean, rstd = vn.layer_norm(x, w, b)
+    grads = None
+    for o in range(1, 9):
+        def placed(t):
+            big = torch.full((t.numel() + 32,), float("nan"), dtype=t.dtype, device=DEV)
+            view = big[o:o + t.numel()].view(t.shape)
+            view.copy_(t)
+            return view
+
+        big = torch.full((x.numel() + 32,), 7.0, dtype=x.dtype, device=DEV)
+        out = big[o + 3:o + 3 + x.numel()].view(x.shape)
+        y2, mean2, rstd2 = vn.layer_norm(placed(x), w, b, out=out)
+        assert torch.equal(y2, y) and torch.equal(mean2, mean) and torch.equal(rstd2, rstd)
+        assert bool((big[:o + 3] == 7).all()) and bool((big[o + 3 + x.numel():] == 7).all())
+        again = vn.layer_norm_backward(placed(d), placed(x), mean, rstd, w)
+        if grads is None:
+            grads = again
+        for p, q in zip(again, grads):
+            assert torch.equal(p, q)
+    ref = vn.layer_norm_backward(d, x, mean, rstd, w)
+    for p, q in zip(grads, ref):
+        assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("rows,n_in,n_out", [(9, 7, 5), (33, 65, 63), (130, 127, 129), (257, 191, 70), (64, 250, 38)])
+def test_linear_bf16_does_not_depend_on_the_place(rows, n_in, n_out):
+    """As above, for operands that are gathered."""
+    g = torch.Generator().manual_seed(31)
+    x, w = normal(g, (rows, n_in), "bf16"), normal(g, (n_out, n_in), "bf16", 0.2)
+    d, z = normal(g, (rows, n_out), "bf16"), normal(g, (rows, n_out), "bf16")
+    first = None
+    for o in range(1, 9):
+        def placed(t):
+            big = torch.full((t.numel() + 32,), float("nan"), dtype=t.dtype, device=DEV)
+            view = big[o:o + t.numel()].view(t.shape)
+            view.copy_(t)
+            return view
+
+        got = (vn.linear(placed(x), placed(w)),) + tuple(
+            vn.linear_backward(placed(d), placed(x), placed(w), placed(z), activation="silu"))
+        assert all(bool(torch.isfinite(t).all()) for t in got)
+        if first is None:
+            first = got
+        for p, q in zip(got, first):
+            assert torch.equal(p, q)

@@ -100,12 +100,12 @@ __device__ __forceinline__ void load_param(const void* w, int bf16, int64_t i, f
   }
 }
 
-// Sums over the T threads of a row (a warp, or the whole CTA), the same in every thread.
+// Sums over the T threads of a row (a part of a warp, a warp, or the whole CTA), the same in every thread.
 // `scratch`: 64 floats for one sum, 128 for two, halves of which calls use in turn.
 template <int T>
 __device__ __forceinline__ float row_sum(float v, float* scratch, int& turn) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  for (int o = (T < 32 ? T : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   if constexpr (T > 32) {
     constexpr int kW = T / 32;
     float* s = scratch + (turn++ & 1) * 32;
@@ -161,13 +161,135 @@ __device__ __forceinline__ void store_pairs(X* p, const F2 (&v)[kPairs<X>]) {
   for (int q = 0; q < kPairs<X>; ++q) split(v[q], &o[2 * q], &o[2 * q + 1]);
   store_pack<X, 16 / sizeof(X)>(p, o);
 }
+// The first `left` of V consecutive parameters, 0 beyond.
+template <int V>
+__device__ __forceinline__ void load_params(const void* w, int bf16, int64_t i, int left, float absent, float (&v)[V]) {
+  if (left >= V) {
+    load_param<V>(w, bf16, i, absent, v);
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < V; ++q) {
+    float one[1] = {0.f};
+    if (q < left) load_param<1>(w, bf16, i + q, absent, one);
+    v[q] = one[0];
+  }
+}
 // V consecutive parameters as pairs.
 template <int V>
-__device__ __forceinline__ void load_pairs(const void* w, int bf16, int64_t i, float absent, F2 (&v)[V / 2]) {
+__device__ __forceinline__ void load_pairs(const void* w, int bf16, int64_t i, int left, float absent, F2 (&v)[V / 2]) {
   float u[V];
-  load_param<V>(w, bf16, i, absent, u);
+  load_params<V>(w, bf16, i, left, absent, u);
 #pragma unroll
   for (int q = 0; q < V / 2; ++q) v[q] = f2(u[2 * q], u[2 * q + 1]);
+}
+// Rows that start anywhere. Their elements are taken in packs of 16 bytes all the same: a pack comes from
+// the two aligned words that hold it, and leaves as one aligned word with the end of the pack
+// before it, which the lane below has. Single elements are moved at the ends of a row and of a
+// warp, and where an aligned word would pass the tensor's ends.
+//
+// 16 bytes from element e of a and b on.
+template <typename X>
+__device__ __forceinline__ uint4 pick(const uint4& a, const uint4& b, int e) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  constexpr int kOne = sizeof(X) == 2 ? 2 : 1, kTwo = 2 * kOne;
+  uint32_t x[6], y[5];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) x[i] = e & kTwo ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) y[i] = e & kOne ? x[i + 1] : x[i];
+  if constexpr (sizeof(X) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __funnelshift_r(y[i], y[i + 1], (e & 1) * 16);
+  }
+  return make_uint4(y[0], y[1], y[2], y[3]);
+}
+template <typename X>
+__device__ __forceinline__ int misplaced(const X* p) {  // elements since the last 16-byte boundary
+  return static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(X));
+}
+template <typename X>
+__device__ __forceinline__ int misplaced(const void* tensor, int64_t row, int n) {  // of row `row`
+  return (misplaced(static_cast<const X*>(tensor)) + static_cast<uint32_t>(row) * static_cast<uint32_t>(n)) & (16 / sizeof(X) - 1);
+}
+// The first `left` elements of a pack, 0 beyond.
+template <typename X>
+__device__ __forceinline__ uint4 keep(const uint4& v, int left) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(X) == 2) w[i] = left >= 2 * i + 2 ? w[i] : left > 2 * i ? w[i] & 0xFFFFu : 0u;
+    else w[i] = left > i ? w[i] : 0u;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename X>
+__device__ __forceinline__ uint4 gather_pack(const X* p, int left) {
+  uint32_t w[4] = {};
+  if constexpr (sizeof(X) == 2) {
+    const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < left) w[q / 2] |= static_cast<uint32_t>(fetch(h + q)) << (q % 2 * 16);
+  } else {
+    const uint32_t* h = reinterpret_cast<const uint32_t*>(p);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q < left) w[q] = fetch(h + q);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Whether the aligned words of a row's `packs` packs, whose first element is `at`, lie within the tensor.
+template <typename X>
+__device__ __forceinline__ bool within(int64_t at, int packs, int64_t elements) {
+  constexpr int V = 16 / sizeof(X);
+  return at >= V && at + static_cast<int64_t>(packs + 1) * V <= elements;
+}
+// One pack of outputs, the row's elements from i on, by all lanes of the warp. `before`: the group's pack
+// ahead of its first lane's; `first` and `last`: this lane's pack is the group's first or last of the row,
+// whose neighbour is not at hand. m: misplaced(row).
+template <typename X, int kGroup>
+__device__ __forceinline__ void store_any(X* row, int m, int i, int n, bool first, bool last, const uint4& before, const uint4& o) {
+  constexpr int V = 16 / sizeof(X);
+  const int lane = threadIdx.x & (kGroup - 1);
+  const bool top = lane == kGroup - 1;
+  const int from = (lane + kGroup - 1) & (kGroup - 1);
+  uint4 below;
+  below.x = __shfl_sync(0xFFFFFFFFu, top ? before.x : o.x, from, kGroup);
+  below.y = __shfl_sync(0xFFFFFFFFu, top ? before.y : o.y, from, kGroup);
+  below.z = __shfl_sync(0xFFFFFFFFu, top ? before.z : o.z, from, kGroup);
+  below.w = __shfl_sync(0xFFFFFFFFu, top ? before.w : o.w, from, kGroup);
+  const int left = n - i;
+  if (left <= 0) return;
+  const bool whole = left >= V - m && (m == 0 || !first);  // this lane's aligned word
+  const bool above = left - V >= V - m && !last;           // the next one, by the lane above
+  if (whole) __stcs(reinterpret_cast<uint4*>(row + i - m), m == 0 ? o : pick<X>(below, o, V - m));
+  if (!whole || (m > 0 && !above)) {
+    const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      if (q >= left || (q < V - m ? whole : above)) continue;
+      if constexpr (sizeof(X) == 2) reinterpret_cast<unsigned short*>(row + i)[q] = static_cast<unsigned short>(w[q / 2] >> (q % 2 * 16));
+      else reinterpret_cast<uint32_t*>(row + i)[q] = w[q];
+    }
+  }
+}
+template <typename X>
+__device__ __forceinline__ uint4 pack_of(const F2 (&v)[kPairs<X>]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < kPairs<X>; ++q) {
+    float a, b;
+    split(v[q], &a, &b);
+    if constexpr (sizeof(X) == 2) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      w[q] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      w[2 * q] = __float_as_uint(a);
+      w[2 * q + 1] = __float_as_uint(b);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -195,8 +317,8 @@ struct NormArgsK {
 
 constexpr int cta_threads(int t) { return t < 64 ? 128 : t; }
 
-// Rows of 16-byte packs, NV of them a thread.
-template <typename X, int T, int NV>
+// Rows of 16-byte packs, NV of them a thread; kAny: that start anywhere and end within a pack.
+template <typename X, int T, int NV, bool kAny>
 __global__ void __launch_bounds__(cta_threads(T)) norm_pairs_kernel(const NormArgsK a) {
   let_next();
   after_previous();
@@ -204,22 +326,61 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_pairs_kernel(const NormAr
   __shared__ float scratch[T > 32 ? 64 : 1];
   int turn = 0;
   const int t = threadIdx.x % T;
-  const int n = static_cast<int>(a.n);
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T;
   if (T == 32 && row >= a.rows) return;
+  const bool live = row < a.rows;  // below a warp a row, its lanes stay together
+  if (!live) row = a.rows - 1;
+  const int n = live ? static_cast<int>(a.n) : 0;
   const X* in = static_cast<const X*>(a.x) + row * a.n;
   uint4 raw[NV];
+  // The thread's packs: every T-th, or in a warp's groups one after the other, so that all
+  // neighbours but a warp's first and last are at hand.
+  constexpr int kGroup = T < 32 ? T : 32;
+  auto at = [&](int j) { return (kAny && T > 32 ? ((t >> 5) * NV + j) * 32 + (t & 31) : j * T + t) * V; };
+  if constexpr (kAny) {
+    const int m = misplaced<X>(a.x, row, static_cast<int>(a.n));
+    bool inside = within<X>(row * a.n, static_cast<int>((a.n + V - 1) / V), a.rows * a.n);
+    if (T < 32) inside = __all_sync(0xFFFFFFFFu, inside);  // a warp's rows go one way
+    if (inside) {
+      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+      const bool top = (t & (kGroup - 1)) == kGroup - 1;
+      uint4 beyond = none;  // the word after the thread's last group's
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int i = (j * T + t) * V;
-    if (i < n) raw[j] = __ldcs(reinterpret_cast<const uint4*>(in + i));
+      for (int j = 0; j < NV; ++j) raw[j] = at(j) < n + m ? fetch(reinterpret_cast<const uint4*>(in - m + at(j))) : none;
+      if (top && at(NV - 1) + V < n + m) beyond = fetch(reinterpret_cast<const uint4*>(in - m + at(NV - 1) + V));
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        // The next word: the lane above's, or the next group's first.
+        const uint4 next = j + 1 < NV ? raw[j + 1] : beyond;
+        const bool low = (t & (kGroup - 1)) == 0;
+        uint4 high;
+        const int from = (t + 1) & (kGroup - 1);
+        high.x = __shfl_sync(0xFFFFFFFFu, low && j + 1 < NV ? next.x : raw[j].x, from, kGroup);
+        high.y = __shfl_sync(0xFFFFFFFFu, low && j + 1 < NV ? next.y : raw[j].y, from, kGroup);
+        high.z = __shfl_sync(0xFFFFFFFFu, low && j + 1 < NV ? next.z : raw[j].z, from, kGroup);
+        high.w = __shfl_sync(0xFFFFFFFFu, low && j + 1 < NV ? next.w : raw[j].w, from, kGroup);
+        if (j + 1 == NV && top) high = beyond;
+        raw[j] = pick<X>(raw[j], high, m);
+        const int left = n - at(j);
+        if (left < V) raw[j] = keep<X>(raw[j], left);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) raw[j] = gather_pack(in + at(j), n - at(j));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = at(j);
+      if (i < n) raw[j] = __ldcs(reinterpret_cast<const uint4*>(in + i));
+    }
   }
   // The row stays as it was loaded and is unpacked in each pass: bf16 in half the registers
   // that its fp32 values would take, for more rows at work (84 us against 116 us, 32768 x 4096).
   F2 s = f2(0.f, 0.f);
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    if ((j * T + t) * V < n) {
+    if (at(j) < n) {
       F2 x[P];
       pairs_of<X>(raw[j], x);
 #pragma unroll
@@ -230,38 +391,53 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_pairs_kernel(const NormAr
   s = f2(0.f, 0.f);
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    if ((j * T + t) * V < n) {
+    if (at(j) < n) {
       F2 x[P];
       pairs_of<X>(raw[j], x);
+      const int left = n - at(j);
 #pragma unroll
       for (int q = 0; q < P; ++q) {
         x[q] = add2(x[q], minus);
+        if (kAny && left < V) {
+          float u, v;
+          split(x[q], &u, &v);
+          x[q] = f2(2 * q < left ? u : 0.f, 2 * q + 1 < left ? v : 0.f);
+        }
         s = fma2(x[q], x[q], s);
       }
     }
   const float rstd = 1.f / sqrtf(row_sum<T>(sum_of(s), scratch, turn) * a.inv_n + a.eps);
   const F2 r2 = f2(rstd, rstd);
   X* y = static_cast<X*>(a.y) + row * a.n;
+  uint4 before = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int i = (j * T + t) * V;
+    const int i = at(j);
+    uint4 o = make_uint4(0u, 0u, 0u, 0u);
     if (i < n) {
       F2 x[P], w[P], b[P];
-      load_pairs<V>(a.w, a.w_bf16, i, 1.f, w);
-      load_pairs<V>(a.b, a.w_bf16, i, 0.f, b);
+      const int left = kAny ? n - i : V;
+      load_pairs<V>(a.w, a.w_bf16, i, left, 1.f, w);
+      load_pairs<V>(a.b, a.w_bf16, i, left, 0.f, b);
       pairs_of<X>(raw[j], x);
 #pragma unroll
       for (int q = 0; q < P; ++q) x[q] = fma2(mul2(add2(x[q], minus), r2), w[q], b[q]);
-      store_pairs<X>(y + i, x);
+      if constexpr (kAny) o = pack_of<X>(x);
+      else store_pairs<X>(y + i, x);
+    }
+    if constexpr (kAny) {
+      const int lane = t & (kGroup - 1);
+      store_any<X, kGroup>(y, misplaced(y), i, n, j == 0 && lane == 0, j == NV - 1 && lane == kGroup - 1, before, o);
+      before = o;
     }
   }
-  if (t == 0) {
+  if (t == 0 && live) {
     if (a.mean != nullptr) a.mean[row] = mean;
     if (a.rstd != nullptr) a.rstd[row] = rstd;
   }
 }
 
-// Rows that 16-byte packs do not divide: single elements, NV of them a thread.
+// Parameters that do not start on 16 bytes: single elements, NV of them a thread.
 template <typename X, int T, int V, int NV>
 __global__ void __launch_bounds__(cta_threads(T)) norm_kernel(const NormArgsK a) {
   let_next();
@@ -362,11 +538,15 @@ struct NormGradK {
   int w_bf16;
 };
 
+// Threads of a CTA: 16 warps where a warp has a row, for few partial sums. Up to four elements a thread leave
+// registers for two such CTAs an SM (60000 x 63 bf16: FEW us for 25.3).
+constexpr int grad_threads(int t) { return t < 64 ? 512 : t; }
+
 template <typename X, int T, int V, int NV>
-__global__ void __launch_bounds__(cta_threads(T)) norm_grad_kernel(const NormGradK a) {
+__global__ void __launch_bounds__(grad_threads(T), T < 64 && V * NV <= 4 ? 2 : 1) norm_grad_kernel(const NormGradK a) {
   let_next();
   after_previous();
-  constexpr int kRows = cta_threads(T) / T;
+  constexpr int kRows = grad_threads(T) / T;
   __shared__ float scratch[T > 32 ? 128 : 1];
   extern __shared__ float columns[];  // T == 32: kRows x 2 x n column sums to be added
   int turn = 0;
@@ -454,7 +634,7 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_grad_kernel(const NormGra
         }
       }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * n; i += cta_threads(T)) {
+    for (int i = threadIdx.x; i < 2 * n; i += grad_threads(T)) {
       float s = 0.f;
 #pragma unroll
       for (int k = 0; k < kRows; ++k) s += columns[k * 2 * n + i];
@@ -486,10 +666,13 @@ __global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, co
   __shared__ float scratch[128];
   const int t = threadIdx.x;
   const int n = static_cast<int>(a.n);
+  // The thread's packs: a warp's NV groups of 32 follow one another, so that it reads and writes in few
+  // places (32768 x 4096 fp32: 235 us, with every T-th pack 272).
+  const int mine = (t >> 5) * (NV * 32) + (t & 31);
   F2 w[NV][P], dw[NV][P], db[NV][P];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int i = (j * T + t) * V;
+    const int i = (mine + j * 32) * V;
     float u[V] = {};
     if (i < n) load_param<V>(a.w, a.w_bf16, i, 1.f, u);
 #pragma unroll
@@ -498,19 +681,18 @@ __global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, co
       dw[j][q] = db[j][q] = f2(0.f, 0.f);
     }
   }
-  uint4* const mine = ring + t;
   const int64_t stride = gridDim.x;
   auto fetch = [&](int64_t row, int slot) {  // one group of copies, empty beyond the last row
     if (row < a.rows) {
       const X* g = static_cast<const X*>(a.g) + row * a.n;
       const X* x = static_cast<const X*>(a.x) + row * a.n;
-      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(mine + slot * (2 * NV * T)));
+      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(ring + slot * (2 * NV * T) + mine));
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int i = (j * T + t) * V;
+        const int i = (mine + j * 32) * V;
         if (i < n) {
-          copy16(to + j * (T * 16), g + i);
-          copy16(to + (NV + j) * (T * 16), x + i);
+          copy16(to + j * 512, g + i);
+          copy16(to + (NV * T + j * 32) * 16, x + i);
         }
       }
     }
@@ -545,14 +727,14 @@ __global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, co
       r2 = f2(rstd, rstd);
       shift = sizeof(X) == 2 ? f2(-mean * rstd, -mean * rstd) : f2(-mean, -mean);
       wait_copies(depth - 2);
-      const uint4* const from = mine + slot * (2 * NV * T);
+      const uint4* const from = ring + slot * (2 * NV * T) + mine;
       F2 s1 = f2(0.f, 0.f), s2 = f2(0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if ((j * T + t) * V < n) {
+        if ((mine + j * 32) * V < n) {
           F2 g[P], h[P];
-          pairs_of<X>(from[j * T], g);
-          pairs_of<X>(from[(NV + j) * T], h);
+          pairs_of<X>(from[j * 32], g);
+          pairs_of<X>(from[NV * T + j * 32], h);
 #pragma unroll
           for (int q = 0; q < P; ++q) {
             h[q] = sizeof(X) == 2 ? fma2(h[q], r2, shift) : mul2(add2(h[q], shift), r2);
@@ -578,15 +760,15 @@ __global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, co
       const float m1 = -__shfl_sync(0xFFFFFFFFu, v, 0) * a.inv_n, m2 = -__shfl_sync(0xFFFFFFFFu, v, 16) * a.inv_n;
       // rstd (g w - m1 - h m2)
       const F2 c1 = f2(m1, m1), c2 = f2(m2, m2);
-      const uint4* const from = mine + old * (2 * NV * T);
+      const uint4* const from = ring + old * (2 * NV * T) + mine;
       X* dx = static_cast<X*>(a.dx) + (first + (k - 1) * stride) * a.n;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int i = (j * T + t) * V;
+        const int i = (mine + j * 32) * V;
         if (i < n) {
           F2 g[P], h[P], o[P];
-          pairs_of<X>(from[j * T], g);
-          pairs_of<X>(from[(NV + j) * T], h);
+          pairs_of<X>(from[j * 32], g);
+          pairs_of<X>(from[NV * T + j * 32], h);
 #pragma unroll
           for (int q = 0; q < P; ++q) {
             h[q] = sizeof(X) == 2 ? fma2(h[q], r2_old, shift_old) : mul2(add2(h[q], shift_old), r2_old);
@@ -607,7 +789,7 @@ __global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, co
   float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.n;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int i = (j * T + t) * V;
+    const int i = (mine + j * 32) * V;
     if (i < n) {
 #pragma unroll
       for (int q = 0; q < P; q += 2) {
@@ -705,30 +887,37 @@ column_sum_kernel(const float* part, int64_t parts, int64_t width, int64_t n, vo
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-template <typename X, int T, int V, int NV>
+template <typename X, int T, int V, int NV, bool kAny>
 cudaError_t run_norm(const NormArgsK& a, cudaStream_t stream) {
   constexpr int kRows = cta_threads(T) / T;
   const int64_t ctas = (a.rows + kRows - 1) / kRows;
   if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(ctas));
-  if constexpr (V > 1) return launch_overlapped(norm_pairs_kernel<X, T, NV>, grid, cta_threads(T), 0, 0, stream, a);
+  if constexpr (V > 1) return launch_overlapped(norm_pairs_kernel<X, T, NV, kAny>, grid, cta_threads(T), 0, 0, stream, a);
   else return launch_overlapped(norm_kernel<X, T, V, NV>, grid, cta_threads(T), 0, 0, stream, a);
 }
 
 // The threads of a row by its number of packs: as few as 8 packs a thread allow, so that many rows
 // are at work on an SM and few barriers join them (32768 x 4096 bf16: 81 us with 64 threads a
-// row, 84 with 128, 102 with 256; 16384 x 8192: 81 with 128, 88 with 256).
-template <typename X, int V>
+// row, 84 with 128, 102 with 256; 16384 x 8192: 81 with 128, 88 with 256); eight lanes for short rows
+// (60000 x 63 bf16: 9.7 us, 17.0 with a warp a row).
+template <typename X, int V, bool kAny>
 cudaError_t norm_by_length(const NormArgsK& a, cudaStream_t stream) {
   const int64_t packs = (a.n + V - 1) / V;
-  if (packs <= 32) return run_norm<X, 32, V, 1>(a, stream);
-  if (packs <= 64) return run_norm<X, 32, V, 2>(a, stream);
-  if (packs <= 128) return run_norm<X, 32, V, 4>(a, stream);
-  if (packs <= 256) return run_norm<X, 32, V, 8>(a, stream);
-  if (packs <= 512) return run_norm<X, 64, V, 8>(a, stream);
-  if (packs <= 1024) return run_norm<X, 128, V, 8>(a, stream);
-  if (packs <= 2048) return run_norm<X, 256, V, 8>(a, stream);
-  if (packs <= 4096) return run_norm<X, 512, V, 8>(a, stream);
+  if constexpr (V > 1) {
+    if (packs <= 8) return run_norm<X, 8, V, 1, kAny>(a, stream);
+    if (packs <= 16) return run_norm<X, 8, V, 2, kAny>(a, stream);
+    if (packs <= 32) return run_norm<X, 8, V, 4, kAny>(a, stream);
+  } else {
+    if (packs <= 32) return run_norm<X, 32, V, 1, kAny>(a, stream);
+  }
+  if (packs <= 64) return run_norm<X, 32, V, 2, kAny>(a, stream);
+  if (packs <= 128) return run_norm<X, 32, V, 4, kAny>(a, stream);
+  if (packs <= 256) return run_norm<X, 32, V, 8, kAny>(a, stream);
+  if (packs <= 512) return run_norm<X, 64, V, 8, kAny>(a, stream);
+  if (packs <= 1024) return run_norm<X, 128, V, 8, kAny>(a, stream);
+  if (packs <= 2048) return run_norm<X, 256, V, 8, kAny>(a, stream);
+  if (packs <= 4096) return run_norm<X, 512, V, 8, kAny>(a, stream);
   if (a.rows > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   return launch_overlapped(norm_long_kernel<X>, dim3(static_cast<unsigned>(a.rows)), 512, 0, 0, stream, a);
 }
@@ -736,8 +925,12 @@ cudaError_t norm_by_length(const NormArgsK& a, cudaStream_t stream) {
 template <typename X>
 cudaError_t norm_typed(const NormArgsK& a, cudaStream_t stream) {
   constexpr int V = 16 / sizeof(X);
-  const bool vec = a.n % V == 0 && aligned16(a.x) && aligned16(a.y) && aligned16(a.w) && aligned16(a.b);
-  return vec ? norm_by_length<X, V>(a, stream) : norm_by_length<X, 1>(a, stream);
+  if (!aligned16(a.w) || !aligned16(a.b)) return norm_by_length<X, 1, false>(a, stream);
+  if (a.n % V == 0 && aligned16(a.x) && aligned16(a.y)) return norm_by_length<X, V, false>(a, stream);
+  // Rows that start anywhere: bf16, 60000 x 63 9.7 us in packs, 17.0 in single elements; 65536 x 511 60 and
+  // 69; 4099 x 1021 9.7 and 8.2; 32768 x 4095 175 and 154, as shifting a pack then costs more than
+  // the loads it saves; 16384 x 8191 169 and 202.
+  return a.n <= 512 || a.n > 4096 ? norm_by_length<X, V, true>(a, stream) : norm_by_length<X, 1, false>(a, stream);
 }
 
 // Partial rows of the column sums: at most this many CTAs walk the rows.
@@ -745,8 +938,11 @@ constexpr int64_t kMaxParts = 152 * 4;
 
 template <typename X, int T, int V, int NV>
 cudaError_t run_norm_grad(const NormGradK& a, int64_t parts, cudaStream_t stream) {
-  const size_t smem = T == 32 ? sizeof(float) * 2 * (cta_threads(T) / T) * a.n : 0;
-  return launch_overlapped(norm_grad_kernel<X, T, V, NV>, dim3(static_cast<unsigned>(parts)), cta_threads(T), 0, smem,
+  const size_t smem = T == 32 ? sizeof(float) * 2 * (grad_threads(T) / T) * a.n : 0;
+  static SmemRecord record;
+  const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(norm_grad_kernel<X, T, V, NV>), smem, record);
+  if (err != cudaSuccess) return err;
+  return launch_overlapped(norm_grad_kernel<X, T, V, NV>, dim3(static_cast<unsigned>(parts)), grad_threads(T), 0, smem,
                            stream, a);
 }
 
@@ -769,26 +965,32 @@ cudaError_t norm_grad_by_length(const NormGradK& a, int64_t* parts, cudaStream_t
   // Elements of a thread: each takes three fp32 registers (weight and both sums) besides the rows
   // at work. 16 with 16-byte loads; 8 with single ones, for more loads in flight an SM.
   constexpr int kNv = V > 1 ? 16 / V : 8;
-  auto ctas = [&](int t) {  // as many as are resident at once: 512 threads an SM
-    const int64_t rows = cta_threads(t) / t;
-    return std::max<int64_t>(1, std::min<int64_t>(kMaxParts * 128 / cta_threads(t), (a.rows + rows - 1) / rows));
+  auto ctas = [&](int t, int64_t an_sm) {  // as many as are resident at once
+    const int64_t rows = grad_threads(t) / t;
+    return std::max<int64_t>(1, std::min<int64_t>(152 * an_sm, (a.rows + rows - 1) / rows));
   };
   const int64_t per = kNv * V;
   if (a.n <= 32 * per) {
-    *parts = ctas(32);
-    if (a.n <= 32 * per / 2) return run_norm_grad<X, 32, V, kNv / 2>(a, *parts, stream);
+    if constexpr (V == 1) {
+      if (a.n <= 64) { *parts = ctas(32, 2); return run_norm_grad<X, 32, V, 2>(a, *parts, stream); }
+    }
+    if (a.n <= 32 * per / 2) {
+      *parts = ctas(32, per <= 8 ? 2 : 1);
+      return run_norm_grad<X, 32, V, kNv / 2>(a, *parts, stream);
+    }
+    *parts = ctas(32, 1);
     return run_norm_grad<X, 32, V, kNv>(a, *parts, stream);
   }
   if constexpr (V > 1) {
-    if (a.n <= 64 * per) { *parts = ctas(128); return run_norm_grad_ring<X, 128, kNv / 2>(a, *parts, stream); }
-    if (a.n <= 128 * per) { *parts = ctas(128); return run_norm_grad_ring<X, 128, kNv>(a, *parts, stream); }
-    if (a.n <= 256 * per) { *parts = ctas(256); return run_norm_grad_ring<X, 256, kNv>(a, *parts, stream); }
-    if (a.n <= 512 * per) { *parts = ctas(512); return run_norm_grad_ring<X, 512, kNv>(a, *parts, stream); }
+    if (a.n <= 64 * per) { *parts = ctas(128, 4); return run_norm_grad_ring<X, 128, kNv / 2>(a, *parts, stream); }
+    if (a.n <= 128 * per) { *parts = ctas(128, 4); return run_norm_grad_ring<X, 128, kNv>(a, *parts, stream); }
+    if (a.n <= 256 * per) { *parts = ctas(256, 2); return run_norm_grad_ring<X, 256, kNv>(a, *parts, stream); }
+    if (a.n <= 512 * per) { *parts = ctas(512, 1); return run_norm_grad_ring<X, 512, kNv>(a, *parts, stream); }
   } else {
-    if (a.n <= 128 * per) { *parts = ctas(128); return run_norm_grad<X, 128, V, kNv>(a, *parts, stream); }
-    if (a.n <= 256 * per) { *parts = ctas(256); return run_norm_grad<X, 256, V, kNv>(a, *parts, stream); }
-    if (a.n <= 512 * per) { *parts = ctas(512); return run_norm_grad<X, 512, V, kNv>(a, *parts, stream); }
-    if (a.n <= 512 * 16) { *parts = ctas(512); return run_norm_grad<X, 512, V, 16>(a, *parts, stream); }
+    if (a.n <= 128 * per) { *parts = ctas(128, 4); return run_norm_grad<X, 128, V, kNv>(a, *parts, stream); }
+    if (a.n <= 256 * per) { *parts = ctas(256, 2); return run_norm_grad<X, 256, V, kNv>(a, *parts, stream); }
+    if (a.n <= 512 * per) { *parts = ctas(512, 1); return run_norm_grad<X, 512, V, kNv>(a, *parts, stream); }
+    if (a.n <= 512 * 16) { *parts = ctas(512, 1); return run_norm_grad<X, 512, V, 16>(a, *parts, stream); }
   }
   if (a.rows > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   cudaError_t err = launch_overlapped(norm_grad_long_kernel<X>, dim3(static_cast<unsigned>(a.rows)), 512, 0, 0, stream, a);
