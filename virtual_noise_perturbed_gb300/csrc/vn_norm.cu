@@ -4,7 +4,7 @@
 //   h = (x - mean) rstd, t = g w:  dx = rstd (t - mean(t) - h mean(t h)),
 //   dw = sum_rows g h, db = sum_rows g
 //
-// Forward: a row lives in the registers of T threads (T = 32, 128 or 512 by its length),
+// Forward: a row lives in the registers of T threads (8 to 512 by its length),
 // so it is read from memory once although the variance is taken from the centred
 // values (a second pass over registers, not the cancelling sum of squares).
 //
@@ -539,7 +539,7 @@ struct NormGradK {
 };
 
 // Threads of a CTA: 16 warps where a warp has a row, for few partial sums. Up to four elements a thread leave
-// registers for two such CTAs an SM (60000 x 63 bf16: FEW us for 25.3).
+// registers for two such CTAs an SM (60000 x 63 bf16: 12.8 us for 25.3).
 constexpr int grad_threads(int t) { return t < 64 ? 512 : t; }
 
 template <typename X, int T, int V, int NV>
@@ -666,13 +666,13 @@ __global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, co
   __shared__ float scratch[128];
   const int t = threadIdx.x;
   const int n = static_cast<int>(a.n);
-  // The thread's packs: a warp's NV groups of 32 follow one another, so that it reads and writes in few
-  // places (32768 x 4096 fp32: 235 us, with every T-th pack 272).
-  const int mine = (t >> 5) * (NV * 32) + (t & 31);
+  // The number of the thread's pack j: a warp's NV groups of 32 follow one another, so that it reads and
+  // writes in few places (32768 x 4096 fp32: 235 us, with every T-th pack 273).
+  auto at = [&](int j) { return ((t >> 5) * NV + j) * 32 + (t & 31); };
   F2 w[NV][P], dw[NV][P], db[NV][P];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int i = (mine + j * 32) * V;
+    const int i = at(j) * V;
     float u[V] = {};
     if (i < n) load_param<V>(a.w, a.w_bf16, i, 1.f, u);
 #pragma unroll
@@ -686,13 +686,13 @@ __global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, co
     if (row < a.rows) {
       const X* g = static_cast<const X*>(a.g) + row * a.n;
       const X* x = static_cast<const X*>(a.x) + row * a.n;
-      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(ring + slot * (2 * NV * T) + mine));
+      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(ring + slot * (2 * NV * T)));
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int i = (mine + j * 32) * V;
+        const int i = at(j) * V;
         if (i < n) {
-          copy16(to + j * 512, g + i);
-          copy16(to + (NV * T + j * 32) * 16, x + i);
+          copy16(to + at(j) * 16, g + at(j) * V);
+          copy16(to + (NV * T + at(j)) * 16, x + at(j) * V);
         }
       }
     }
@@ -727,14 +727,14 @@ __global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, co
       r2 = f2(rstd, rstd);
       shift = sizeof(X) == 2 ? f2(-mean * rstd, -mean * rstd) : f2(-mean, -mean);
       wait_copies(depth - 2);
-      const uint4* const from = ring + slot * (2 * NV * T) + mine;
+      const uint4* const from = ring + slot * (2 * NV * T);
       F2 s1 = f2(0.f, 0.f), s2 = f2(0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if ((mine + j * 32) * V < n) {
+        if (at(j) * V < n) {
           F2 g[P], h[P];
-          pairs_of<X>(from[j * 32], g);
-          pairs_of<X>(from[NV * T + j * 32], h);
+          pairs_of<X>(from[at(j)], g);
+          pairs_of<X>(from[NV * T + at(j)], h);
 #pragma unroll
           for (int q = 0; q < P; ++q) {
             h[q] = sizeof(X) == 2 ? fma2(h[q], r2, shift) : mul2(add2(h[q], shift), r2);
@@ -760,15 +760,15 @@ __global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, co
       const float m1 = -__shfl_sync(0xFFFFFFFFu, v, 0) * a.inv_n, m2 = -__shfl_sync(0xFFFFFFFFu, v, 16) * a.inv_n;
       // rstd (g w - m1 - h m2)
       const F2 c1 = f2(m1, m1), c2 = f2(m2, m2);
-      const uint4* const from = ring + old * (2 * NV * T) + mine;
+      const uint4* const from = ring + old * (2 * NV * T);
       X* dx = static_cast<X*>(a.dx) + (first + (k - 1) * stride) * a.n;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int i = (mine + j * 32) * V;
+        const int i = at(j) * V;
         if (i < n) {
           F2 g[P], h[P], o[P];
-          pairs_of<X>(from[j * 32], g);
-          pairs_of<X>(from[NV * T + j * 32], h);
+          pairs_of<X>(from[at(j)], g);
+          pairs_of<X>(from[NV * T + at(j)], h);
 #pragma unroll
           for (int q = 0; q < P; ++q) {
             h[q] = sizeof(X) == 2 ? fma2(h[q], r2_old, shift_old) : mul2(add2(h[q], shift_old), r2_old);
@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, co
   float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.n;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int i = (mine + j * 32) * V;
+    const int i = at(j) * V;
     if (i < n) {
 #pragma unroll
       for (int q = 0; q < P; q += 2) {
