@@ -311,23 +311,31 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
           }
         }
       } else {
-        Residual<T> r;
-        load_residual(p, q0, pp, cols, &r);
+        // The residual's loads run two chunks ahead, from three sets of registers: one that was moved to
+        // another would be waited for.
+        Residual<T> r0, r1, r2;
+        load_residual(p, q0, pp, cols, &r0);
+        load_residual(p, q0 + 16, pp, cols - 16, &r1);
         const bool ok = mbar_wait(tmem_full(tb.s), tb.ph, ctl);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         fence_after();
-#pragma unroll 1
-        for (int c = 0; c < cols; c += 16) {
+        auto chunk = [&](int c, const Residual<T>& r, Residual<T>* ahead) {
+          if (c >= cols) return;
           uint32_t v[16];
           tmem_load16(d + c, v);
-          Residual<T> ahead;
-          load_residual(p, q0 + c + 16, pp, cols - c - 16, &ahead);
+          load_residual(p, q0 + c + 32, pp, cols - c - 32, ahead);
           tmem_wait_load(v);
           float z[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(v[i]);
           if (pp < p.np) finish<T>(p, z, r, q0 + c, pp, cols - c, bias);
-          r = ahead;
+          __syncwarp();
+        };
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 48) {
+          chunk(c, r0, &r2);
+          chunk(c + 16, r1, &r0);
+          chunk(c + 32, r2, &r1);
         }
       }
       fence_before();
