@@ -375,7 +375,7 @@ GatherPlan gather_plan(const Shape (&shapes)[2], vn_dtype dt, bool backward, boo
   for (int bn : {16, 64, 128}) {
     if (backward && bn == 16) continue;
     if (backward && bf16 && !vectors && bn == 128) continue;  // not built
-    const double stage = (vectors ? 1.0 : !bf16 ? 1.7 : backward ? 2.4 : 2.0) *  // rows that start anywhere
+    const double stage = (vectors ? 1.0 : !bf16 ? 1.7 : bn > 16 ? 2.4 : 2.0) *  // rows that start anywhere
                          (backward    ? (bn == 128 ? (bf16 ? 2.2 : 3.1) : (bf16 ? 1.2 : 1.7))
                           : bn == 128 ? (bf16 ? 0.9 : 1.4)
                           : bn == 64  ? (bf16 ? 0.65 : 1.2)
