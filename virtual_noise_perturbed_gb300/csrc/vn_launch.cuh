@@ -19,6 +19,9 @@ namespace vn {
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// A line on its way to L2, which may be asked for before after_previous(): it is no read.
+__device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // A load of what a kernel before this one may have written: never through the read-only path, whose
 // data has to stay as it is from the launch on (so none of these kernels' pointers is __restrict__
 // either).
