@@ -314,7 +314,7 @@ bool as_is(vn_dtype dt, int64_t cols, bool aligned) { return dt == VN_BF16 && co
 // microseconds a launch, more of them the larger its tile, and a CTA's (or pair's) time per 64 of k.
 // They are reckoned here, from sizes alone, so that a call and its workspace agree without a device.
 enum class Route {
-  kRows,    // up to 8 rows: vn_dense_rows.cu
+  kRows,    // few rows, at most 8: vn_dense_rows.cu
   kPlain,   // 64 x 64 tiles without tensor cores: sizes beyond 32-bit coordinates
   kGather,  // one launch, operands gathered by threads: vn_dense_gather.cu
   kTiles,   // operands by TMA, in bf16 (converted where they are not): vn_dense_tc.cu
@@ -426,7 +426,14 @@ struct ForwardPlan {
 ForwardPlan reckon_forward(int64_t rows, int64_t in, int64_t out, vn_dtype dt, bool aligned) {
   ForwardPlan p;
   p.route = Route::kRows;
-  if (rows <= 8) return p;
+  // fp32 keeps its products unsplit up to 8 rows; in bf16 the tensor cores take over where they are faster
+  // (4096 to 4096: one row 6.2 us, eight 20.0 and on tiles 11.3; 4095 to 4095: one row 23.6, eight 49.1 and
+  // gathered 18.6).
+  if (rows <= 8 && (dt == VN_F32 || in == 0 || !fits32(rows, in, out))) return p;
+  const double few = rows > 8 ? 1e30
+                              : 3.2 + static_cast<double>(in) * static_cast<double>(out) / 16.8e6 *
+                                          (aligned && in % 8 == 0 ? 1.2 + 2.0 * static_cast<double>(rows)
+                                                                  : 16.0 + 4.5 * static_cast<double>(rows));
   p.route = Route::kPlain;
   if (!fits32(rows, in, out)) return p;
   const Shape shapes[2] = {{out, rows, in}, {0, 0, 0}};
@@ -436,7 +443,9 @@ ForwardPlan reckon_forward(int64_t rows, int64_t in, int64_t out, vn_dtype dt, b
   if (in == 0) return p;
   p.tiles = tile_plan(out, rows, in, dt, false);
   const bool direct = as_is(dt, in, aligned);
-  if (p.tiles.us + convert_us(out, in, dt, direct) + convert_us(rows, in, dt, direct) < p.gather.us) p.route = Route::kTiles;
+  const double tiles = p.tiles.us + convert_us(out, in, dt, direct) + convert_us(rows, in, dt, direct);
+  if (tiles < p.gather.us) p.route = Route::kTiles;
+  if (few <= std::min(tiles, p.gather.us)) p.route = Route::kRows;
   return p;
 }
 struct BackwardPlan {
