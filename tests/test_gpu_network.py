@@ -514,3 +514,48 @@ def test_linear_bf16_does_not_depend_on_the_place(rows, n_in, n_out):
             first = got
         for p, q in zip(got, first):
             assert torch.equal(p, q)
+
+
+def _chain(x, w, gain, n):
+    """n residual steps; each call's input is what the call before it wrote."""
+    for _ in range(n):
+        h, _, _ = vn.layer_norm(x, gain, gain)
+        x = vn.linear(h, w, activation="tanh", residual=x)
+    return x
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,n", [(3, 64), (130, 96), (1000, 264), (700, 129)])
+def test_calls_that_follow_one_another_see_each_other(rows, n, kind):
+    """Launches overlap the end of the one before: the same bits with a wait after every call, without,
+    over two streams joined by events, and replayed from a graph."""
+    g = torch.Generator().manual_seed(41)
+    x, w, gain = normal(g, (rows, n), kind), normal(g, (n, n), kind, 0.1), normal(g, (n,), "fp32", 0.1, 1.0)
+    want = x
+    for _ in range(30):
+        want = _chain(want, w, gain, 1)
+        torch.cuda.synchronize()
+    for _ in range(5):
+        assert torch.equal(_chain(x, w, gain, 30), want)
+
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    y, kept = x, []
+    for i in range(30):
+        here, there = streams[i % 2], streams[(i + 1) % 2]
+        with torch.cuda.stream(here):
+            y = _chain(y, w, gain, 1)
+            kept.append(y)
+        there.wait_stream(here)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+
+    graph, out = torch.cuda.CUDAGraph(), None
+    with torch.cuda.graph(graph):
+        out = _chain(x, w, gain, 30)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
