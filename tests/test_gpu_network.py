@@ -559,3 +559,10 @@ def test_calls_that_follow_one_another_see_each_other(rows, n, kind):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,n_in,n_out", [(4096, 64, 64), (4500, 33, 70), (8192, 130, 60), (30001, 16, 8)])
+def test_linear_backward_over_many_rows(rows, n_in, n_out, kind):
+    """Sums over rows that are long enough to be split over the largest clusters."""
+    check_backward(rows, n_in, n_out, kind, "silu")

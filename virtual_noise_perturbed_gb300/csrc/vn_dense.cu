@@ -327,7 +327,7 @@ double tiles_of(int64_t n, int64_t tile) { return static_cast<double>((n + tile 
 // CTAs that the GPU holds at once in clusters of 2^log_cluster, `per_sm` to an SM: fewer than 152 SMs
 // have room for, as clusters stay within a part of the GPU.
 double resident(int log_cluster, int per_sm) {
-  static const double kOne[4] = {152, 152, 144, 120}, kTwo[4] = {304, 304, 296, 288};
+  static const double kOne[5] = {152, 152, 144, 120, 112}, kTwo[5] = {304, 304, 296, 288, 224};
   return per_sm == 1 ? kOne[log_cluster] : kTwo[log_cluster];
 }
 
@@ -382,7 +382,8 @@ GatherPlan gather_plan(const Shape (&shapes)[2], vn_dtype dt, bool backward, boo
                                       : (bf16 ? 0.75 : 0.95));
     const double launch = backward ? (bf16 || bn == 128 ? 5.3 : 6.7) : bn == 128 ? 8.5 : bn == 64 ? 6.0 : 3.5;
     for (int l0 = 0; l0 < 4; ++l0)
-      for (int l1 = 0; l1 < (backward ? 4 : 1); ++l1) {
+      // Clusters of 16, where the sums over rows are long.
+      for (int l1 = 0; l1 < (!backward ? 1 : shapes[1].nk >= 4096 ? 5 : 4); ++l1) {
         const int l[2] = {l0, l1};
         double work = 0, longest = 0, ctas = 0, chunks = 0;
         for (int i = 0; i < 2; ++i) {
@@ -390,7 +391,7 @@ GatherPlan gather_plan(const Shape (&shapes)[2], vn_dtype dt, bool backward, boo
           if (s.np == 0 || s.nq == 0) continue;
           const double n = tiles_of(s.np, 128) * tiles_of(s.nq, bn) * (1 << l[i]);
           chunks = std::max(chunks, std::ceil(tiles_of(s.nk, 64) / (1 << l[i])));
-          const double t = std::ceil(tiles_of(s.nk, 64) / (1 << l[i])) * stage + launch + (l[i] > 0 ? 1.5 : 0.0) +
+          const double t = std::ceil(tiles_of(s.nk, 64) / (1 << l[i])) * stage + launch + (l[i] > 3 ? 2.5 : l[i] > 0 ? 1.5 : 0.0) +
                            (backward && bn == 128 ? 2.0 * l[i] : 0.0);
           ctas += n;
           work += n * t;
@@ -400,6 +401,7 @@ GatherPlan gather_plan(const Shape (&shapes)[2], vn_dtype dt, bool backward, boo
         const double room = resident(std::max(l0, l1), per_sm);
         // Two CTAs of an SM share its threads' time.
         double crowd = per_sm == 2 && ctas > resident(std::max(l0, l1), 1) ? 1.7 : 1.0;
+        if (backward && ctas > 0) crowd = 1 + (crowd - 1) * work / (ctas * longest);  // short ones leave soon
         if (!backward) crowd = (longest + (crowd - 1) * 0.4 * chunks * stage) / std::max(longest, 1e-9);
         const double us = crowd * (ctas <= room ? longest : std::max(longest, work / room) + 0.5 * longest);
         if (us < best.us) {

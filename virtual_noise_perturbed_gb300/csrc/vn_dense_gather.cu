@@ -14,7 +14,7 @@
 // (grads of 1021 x 256 x 256 in fp32: 13.9 us, latency of loads, MMAs and instruction fetches; in
 // single launches on tiles 30).
 //
-// The k loop is split over the CTAs of a cluster of up to 8; partial sums are added through
+// The k loop is split over the CTAs of a cluster of up to 16; partial sums are added through
 // distributed shared memory in rank order. Warps 0..7 gather, then run the epilogue; warp 8
 // allocates TMEM and issues the MMAs. Waits are bounded as in vn_dense_tc.cu.
 #include <cuda_bf16.h>
@@ -460,7 +460,7 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
 #pragma unroll 1
     for (int c = c0 + (warp >> 2) * 4; c < c1; c += 8) {
       const int64_t o = (q0 + c) * d.np + pp;
-      float r[4] = {}, z[4];
+      float r[4] = {}, z[4] = {};
       float4 v[8];
       if (res != nullptr) {
 #pragma unroll
@@ -468,15 +468,17 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
           if (c + i < c1) r[i] = value(res[o + i * d.np]);
       }
       // Of a last step's columns beyond c1, whatever lies there: they are not stored.
+#pragma unroll 1
+      for (int b = 0; b < split; b += 8) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < split) v[k] = load_cluster4(map_rank(stage0 + (row * kPitch + c) * 4, base + k));
-      z[0] = v[0].x; z[1] = v[0].y; z[2] = v[0].z; z[3] = v[0].w;
+        for (int k = 0; k < 8; ++k)
+          if (b + k < split) v[k] = load_cluster4(map_rank(stage0 + (row * kPitch + c) * 4, base + b + k));
 #pragma unroll
-      for (int k = 1; k < 8; ++k)
-        if (k < split) {
-          z[0] += v[k].x; z[1] += v[k].y; z[2] += v[k].z; z[3] += v[k].w;
-        }
+        for (int k = 0; k < 8; ++k)
+          if (b + k < split) {
+            z[0] += v[k].x; z[1] += v[k].y; z[2] += v[k].z; z[3] += v[k].w;
+          }
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) z[i] += bias;
       if (pre != nullptr) {
@@ -583,6 +585,19 @@ cudaError_t run(GatherParams& g, const int (&log_split)[2], cudaStream_t stream)
   constexpr int S = kStages<T, BN>;
   static_assert(S >= 2 && S * kStageBytes<T, BN> >= (BN + 4) * 512 + 8192, "the partial sums lie in the stages");
   static SmemRecord record;
+  if (g.cluster > 8) {
+    static SmemRecord wide;  // per device: clusters beyond the portable size are allowed
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (wide[dev].load(std::memory_order_acquire) == 0) {
+      err = cudaFuncSetAttribute(reinterpret_cast<const void*>(gather_kernel<T, BN, kBackward, kShift>),
+                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (err != cudaSuccess) return err;
+      wide[dev].store(1, std::memory_order_release);
+    }
+  }
   return launch_cluster(gather_kernel<T, BN, kBackward, kShift>, record, static_cast<int>(blocks), kThreads, g.cluster,
                         kSmemBytes<T, BN, kBackward>, stream, g);
 }
