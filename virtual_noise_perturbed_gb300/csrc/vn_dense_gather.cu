@@ -460,7 +460,7 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
 #pragma unroll 1
     for (int c = c0 + (warp >> 2) * 4; c < c1; c += 8) {
       const int64_t o = (q0 + c) * d.np + pp;
-      float r[4] = {}, z[4] = {};
+      float r[4] = {}, z[4];
       float4 v[8];
       if (res != nullptr) {
 #pragma unroll
@@ -468,16 +468,24 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
           if (c + i < c1) r[i] = value(res[o + i * d.np]);
       }
       // Of a last step's columns beyond c1, whatever lies there: they are not stored.
-#pragma unroll 1
-      for (int b = 0; b < split; b += 8) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (b + k < split) v[k] = load_cluster4(map_rank(stage0 + (row * kPitch + c) * 4, base + b + k));
+      for (int k = 0; k < 8; ++k)
+        if (k < split) v[k] = load_cluster4(map_rank(stage0 + (row * kPitch + c) * 4, base + k));
+      z[0] = v[0].x; z[1] = v[0].y; z[2] = v[0].z; z[3] = v[0].w;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (b + k < split) {
+      for (int k = 1; k < 8; ++k)
+        if (k < split) {
+          z[0] += v[k].x; z[1] += v[k].y; z[2] += v[k].z; z[3] += v[k].w;
+        }
+      if constexpr (kSum) {  // only these are split 16 ways
+        if (split > 8) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = load_cluster4(map_rank(stage0 + (row * kPitch + c) * 4, base + 8 + k));
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
             z[0] += v[k].x; z[1] += v[k].y; z[2] += v[k].z; z[3] += v[k].w;
           }
+        }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) z[i] += bias;
