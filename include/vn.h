@@ -475,6 +475,19 @@ vn_status vn_testhook_linear_tc_withhold(const void* x, vn_dtype x_dt, int x_sha
                                          void* y, vn_dtype y_dt, int64_t withhold_stage,
                                          double timeout_ms, void* stream);
 
+/* The same for vn_linear's tensor-core kernels. kernel: 0 operands gathered by threads, 1 tiles
+ * of single CTAs (both with k split over clusters of 2), 2 tiles of pairs of CTAs. Runs
+ * y = x W^T + residual (and preact) in bf16 with every wait limited to `timeout_ms`, while the
+ * first CTA withholds its handover of operands number `withhold` (from 0) to the MMAs, or, in kernel 0
+ * and beyond its last handover, the arrival that its epilogue waits for. Results are then not
+ * valid, and vn_device_status() reports VN_ERR_TIMEOUT. With a `withhold` beyond what the first CTA
+ * hands over, kernels 1 and 2 complete normally. in >= 128; in and out multiples of 8
+ * (VN_ERR_SHAPE), pointers on 16 bytes. */
+vn_status vn_testhook_linear_withhold(int kernel, const void* x, const void* w, const void* residual,
+                                      int64_t rows, int64_t in, int64_t out, void* y,
+                                      void* preact, int64_t withhold, double timeout_ms,
+                                      void* stream);
+
 /* A static, human-readable name for a status code. */
 const char* vn_status_string(vn_status status);
 

@@ -1,0 +1,70 @@
+"""Bounded waits of the centre network's tensor-core kernels that run out, without a GPU fault.
+
+Through the library's test hook the first CTA withholds one handover of operands (or, in the kernel of
+gathered operands, the arrival that its epilogue waits for), so that a wait of 50 ms runs out. Each kernel
+records the time-out, stops, frees its tensor memory and returns; the status is read and cleared on the
+host, and an ordinary call right after is correct."""
+
+import ctypes
+
+import pytest
+import torch
+
+import virtual_noise_perturbed_gb300 as vn
+from virtual_noise_perturbed_gb300 import _lib
+from virtual_noise_perturbed_gb300.build import build
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+P = ctypes.c_void_p
+
+
+def ptr(t):
+    return P(0 if t is None else t.data_ptr())
+
+
+# rows, in, out: of the first CTA's handovers there are two or more in each kernel (128 of k to each of
+# two CTAs in the first two); pairs run more than one tile each in the last size.
+@pytest.mark.parametrize("kernel,rows,k,n,withhold", [
+    (0, 70, 256, 200, 0), (0, 70, 256, 200, 1), (0, 70, 256, 200, 2),
+    (1, 70, 512, 200, 0), (1, 70, 512, 200, 3),
+    (2, 300, 512, 520, 0), (2, 300, 512, 520, 7), (2, 5000, 512, 2048, 5)])
+def test_a_wait_that_runs_out_is_recorded(kernel, rows, k, n, withhold):
+    build()
+    lib = _lib.load()
+    g = torch.Generator().manual_seed(withhold + k)
+    x, w, r = (torch.randn(s, generator=g).bfloat16().to(DEV) for s in ((rows, k), (n, k), (rows, n)))
+    y, z = torch.empty_like(r), torch.empty_like(r)
+    stream = P(torch.cuda.current_stream().cuda_stream)
+    vn.device_status()
+    want = x.double() @ w.double().t()
+    bound = (2 * k + 18) * 2.0 ** -24 * (x.double().abs() @ w.double().abs().t())
+
+    def call(at):
+        assert lib.vn_testhook_linear_withhold(kernel, ptr(x), ptr(w), ptr(r), rows, k, n, ptr(y), ptr(z), at, 50.0, stream) == 0
+
+    def right(y, z):
+        full = want + r.double()
+        assert bool(((z.double() - want).abs() <= bound + 2.0 ** -8 * 1.01 * want.abs()).all())
+        assert bool(((y.double() - full).abs() <= bound + 2.0 ** -24 * r.double().abs() * 2 + 2.0 ** -8 * 1.01 * full.abs()).all())
+
+    if kernel > 0:
+        call(1 << 20)                                   # nothing withheld: the kernels as they are
+        assert lib.vn_device_status(stream) == 0
+        right(y, z)
+    call(withhold)
+    assert lib.vn_device_status(stream) == 7            # VN_ERR_TIMEOUT
+    assert lib.vn_device_status(stream) == 0            # and cleared
+    right(*vn.linear(x, w, residual=r, preact=True, check_status=True))
+
+
+def test_hook_refuses_bad_arguments():
+    build()
+    f = _lib.load().vn_testhook_linear_withhold
+    a = 0x100000
+
+    def call(kernel=0, x=a, w=a + 0x10000, r=0, rows=8, k=128, n=8, y=a + 0x20000, z=0, at=0, ms=50.0):
+        return f(kernel, P(x), P(w), P(r), rows, k, n, P(y), P(z), at, ms, P(0))
+    assert call(kernel=3) == 4 and call(at=-1) == 4 and call(ms=0.0) == 4
+    assert call(k=64) == 2 and call(k=132) == 2 and call(n=7) == 2 and call(rows=0) == 2
+    assert call(x=0) == 1 and call(y=a + 0x20008) == 5 and call(y=a) == 4

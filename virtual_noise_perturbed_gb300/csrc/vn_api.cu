@@ -539,6 +539,30 @@ vn_status vn_linear(const void* x, const void* w, vn_dtype dt, const void* b, vn
   return launched(vn::launch_dense(a, static_cast<cudaStream_t>(stream)));
 }
 
+vn_status vn_testhook_linear_withhold(int kernel, const void* x, const void* w, const void* residual, int64_t rows,
+                                      int64_t in, int64_t out, void* y, void* preact, int64_t withhold,
+                                      double timeout_ms, void* stream) {
+  if (kernel < 0 || kernel > 2 || !(timeout_ms > 0.0) || !(timeout_ms <= 60000.0) || withhold < 0 || withhold > (1 << 30))
+    return VN_ERR_VALUE;
+  const vn_status st = check_sizes(rows, in, out, VN_BF16);
+  if (st != VN_OK) return st;
+  const int64_t most = int64_t{1} << 30;
+  if (rows < 1 || out < 1 || in < 128 || in % 8 != 0 || out % 8 != 0 || rows > most || in > most || out > most)
+    return VN_ERR_SHAPE;
+  if (x == nullptr || w == nullptr || y == nullptr) return VN_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(preact, 16))
+    return VN_ERR_ALIGN;
+  const int64_t xb = rows * in * 2, wb = out * in * 2, yb = rows * out * 2;
+  const Range outs[] = {{y, yb}, {preact, yb}};
+  const Range ins[] = {{x, xb}, {w, wb}, {residual, yb}};
+  if (!disjoint(outs, ins)) return VN_ERR_VALUE;
+  vn::DenseArgs a = {};
+  a.x = x; a.w = w; a.dt = VN_BF16; a.residual = residual;
+  a.rows = rows; a.in = in; a.out = out; a.act = VN_ACT_NONE; a.y = y; a.preact = preact;
+  return launched(vn::launch_dense_hook(a, kernel, static_cast<int>(withhold),
+                                        static_cast<unsigned long long>(timeout_ms * 1e6), static_cast<cudaStream_t>(stream)));
+}
+
 int64_t vn_linear_backward_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt,
                                      vn_act act, int al) {
   if (check_sizes(rows, in, out, dt) != VN_OK || !linear_act_ok(act)) return -1;

@@ -578,6 +578,26 @@ cudaError_t launch_dense(const DenseArgs& a, cudaStream_t stream) {
   return product(d, a.dt, stream);
 }
 
+cudaError_t launch_dense_hook(const DenseArgs& a, int kernel, int at, unsigned long long timeout_ns, cudaStream_t stream) {
+  const Withhold hook = {at, timeout_ns};
+  if (kernel == 0) {
+    GatherPlan plan;
+    plan.log_split[0] = 1;
+    return launch_gather_forward(a, plan, stream, &hook);
+  }
+  TcProduct d = {};
+  d.a = operand(a.w, a.out, a.in, false);
+  d.b = operand(a.x, a.rows, a.in, false);
+  d.np = a.out; d.nq = a.rows; d.nk = a.in;
+  d.dt = a.dt;
+  d.residual = a.residual; d.out = a.y; d.preact = a.preact;
+  TilePlan plan;
+  plan.pair = kernel == 2;
+  plan.bn = kernel == 2 ? 128 : 64;
+  plan.log_split = kernel == 2 ? 0 : 1;
+  return launch_tc_product(d, plan, stream, &hook);
+}
+
 namespace {
 
 // d into `delta` (where given) and the bias's gradient (where asked for) by way of `part`.

@@ -46,15 +46,26 @@ struct TcProduct {
   void* out;
   void* preact;
 };
-cudaError_t launch_tc_product(const TcProduct& d, const TilePlan& plan, cudaStream_t stream);
+// A test's limit on every wait of a launch, and what it withholds so that one of them runs out: of the
+// first CTA's handovers of operands to the MMAs that number `at` (from 0).
+struct Withhold {
+  int at;
+  unsigned long long timeout_ns;
+};
+// hook: bf16 and k-contiguous operands only; single tiles of 64 columns, pairs whose rows TMA can store.
+cudaError_t launch_tc_product(const TcProduct& d, const TilePlan& plan, cudaStream_t stream, const Withhold* hook = nullptr);
 
 // A layer, or all its gradients, in one launch, for any alignment and no workspace
 // (vn_dense_gather.cu). At least one of grad_x and grad_w is asked for, and grad_b only with
-// grad_w; rows, in and out from 1 to 2^31 - 512.
+// grad_w; rows, in and out up to 2^31 - 512. A sum over nothing is zero: in may be 0 in the forward
+// product, rows or out in the gradients.
 struct DenseArgs;
 struct DenseGradArgs;
 cudaError_t launch_rows_forward(const DenseArgs& a, cudaStream_t stream);  // rows <= 8 (vn_dense_rows.cu)
-cudaError_t launch_gather_forward(const DenseArgs& a, const GatherPlan& plan, cudaStream_t stream);
+// hook: bf16 whose rows start on 16 bytes, on 64 columns. Beyond a CTA's last chunk, `at` is the commit
+// that the epilogue waits for.
+cudaError_t launch_gather_forward(const DenseArgs& a, const GatherPlan& plan, cudaStream_t stream,
+                                  const Withhold* hook = nullptr);
 cudaError_t launch_gather_backward(const DenseGradArgs& a, const GatherPlan& plan, cudaStream_t stream);
 cudaError_t take_gather_status(unsigned int* status, cudaStream_t stream);
 

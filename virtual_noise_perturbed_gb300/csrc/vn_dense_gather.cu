@@ -60,6 +60,7 @@ struct Part {
 struct GatherParams {
   Part part[2];
   int cluster;
+  int withhold;  // test hook: the chunk that CTA 0's first warp never hands over; beyond its last, the final commit
   unsigned long long timeout_ns;
 };
 
@@ -281,7 +282,7 @@ constexpr uint32_t kTmemCols = (kLead<T, BN> + kRest<T, BN>) * BN <= 32    ? 32
 
 // One product's tile. kSum: also the sums of B over k (the bias's gradient), by the tiles of p's
 // first 128. Called by every thread of the CTA.
-template <typename T, int BN, bool kShift, bool kAMn, bool kBMn, bool kSum>
+template <typename T, int BN, bool kShift, bool kAMn, bool kBMn, bool kSum, bool kHook>
 __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8_t* smem, uint64_t* bars, uint32_t tmem,
                                      volatile Control* ctl, int block, int cta) {
   constexpr int S = kStages<T, BN>;
@@ -360,7 +361,7 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
       if (have) {
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full(rg.s));
+        if (lane == 0 && !(kHook && block == 0 && warp == 0 && it - 1 - first == g.withhold)) mbar_arrive(full(rg.s));
         rg.next(S);
       }
     }
@@ -386,8 +387,10 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
       }
       mma_commit<false>(empty(rg.s));
     }
-    mma_commit<false>(done);  // also after an abort: what was issued completes
-    settle(done, 0, g.timeout_ns);
+    if (!(kHook && block == 0 && last - first <= g.withhold)) mma_commit<false>(done);  // also after an abort
+    // The epilogue's sums depend on this wait: one that runs out is recorded and skips them. What was issued
+    // still gets its time to complete.
+    if (!mbar_wait(done, 0, ctl)) settle(done, 0, g.timeout_ns);
   }
   __syncwarp();
   fence_before();
@@ -513,7 +516,8 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
 // kBackward: parts 0 and 1 are dx (A = W, B = d) and dw (A = x, B = d^T, with the bias's sums);
 // otherwise part 0 is the forward product.
 // In bf16 the registers of two CTAs fit an SM, as their stages do (but not with 128 columns of shifted groups).
-template <typename T, int BN, bool kBackward, bool kShift>
+// kHook: the instance whose waits a test makes run out.
+template <typename T, int BN, bool kBackward, bool kShift, bool kHook = false>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !(kShift && BN == 128) ? 2 : 1)
 gather_kernel(const __grid_constant__ GatherParams g) {
   constexpr int S = kStages<T, BN>;
@@ -554,11 +558,11 @@ gather_kernel(const __grid_constant__ GatherParams g) {
   if constexpr (kBackward) {
     // The weight's gradient first: its k loop, over the rows, tends to be the longer one.
     if (block < g.part[1].blocks)
-      tile<T, BN, kShift, true, true, true>(g.part[1], g, smem, bars, tmem, ctl, block, cta);
+      tile<T, BN, kShift, true, true, true, kHook>(g.part[1], g, smem, bars, tmem, ctl, block, cta);
     else
-      tile<T, BN, kShift, true, false, false>(g.part[0], g, smem, bars, tmem, ctl, block - g.part[1].blocks, cta);
+      tile<T, BN, kShift, true, false, false, kHook>(g.part[0], g, smem, bars, tmem, ctl, block - g.part[1].blocks, cta);
   } else {
-    tile<T, BN, kShift, false, false, false>(g.part[0], g, smem, bars, tmem, ctl, block, cta);
+    tile<T, BN, kShift, false, false, false, kHook>(g.part[0], g, smem, bars, tmem, ctl, block, cta);
   }
   __syncwarp();
   fence_before();
@@ -573,7 +577,7 @@ gather_kernel(const __grid_constant__ GatherParams g) {
 template <typename T, int BN, bool kBackward>
 constexpr size_t kSmemBytes = 1024 + kStages<T, BN> * kStageBytes<T, BN> + 8 * (2 * kStages<T, BN> + 2) + sizeof(Control);
 
-template <typename T, int BN, bool kBackward, bool kShift>
+template <typename T, int BN, bool kBackward, bool kShift, bool kHook = false>
 cudaError_t run(GatherParams& g, const int (&log_split)[2], cudaStream_t stream) {
   int64_t blocks = 0;
   g.cluster = 1 << std::max(log_split[0], log_split[1]);
@@ -589,7 +593,7 @@ cudaError_t run(GatherParams& g, const int (&log_split)[2], cudaStream_t stream)
     d.blocks = static_cast<int>(all);
   }
   if (blocks == 0) return cudaSuccess;
-  g.timeout_ns = kTimeoutNs;
+  if (!kHook) g.timeout_ns = kTimeoutNs;
   constexpr int S = kStages<T, BN>;
   static_assert(S >= 2 && S * kStageBytes<T, BN> >= (BN + 4) * 512 + 8192, "the partial sums lie in the stages");
   static SmemRecord record;
@@ -600,13 +604,13 @@ cudaError_t run(GatherParams& g, const int (&log_split)[2], cudaStream_t stream)
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     if (wide[dev].load(std::memory_order_acquire) == 0) {
-      err = cudaFuncSetAttribute(reinterpret_cast<const void*>(gather_kernel<T, BN, kBackward, kShift>),
+      err = cudaFuncSetAttribute(reinterpret_cast<const void*>(gather_kernel<T, BN, kBackward, kShift, kHook>),
                                  cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (err != cudaSuccess) return err;
       wide[dev].store(1, std::memory_order_release);
     }
   }
-  return launch_cluster(gather_kernel<T, BN, kBackward, kShift>, record, static_cast<int>(blocks), kThreads, g.cluster,
+  return launch_cluster(gather_kernel<T, BN, kBackward, kShift, kHook>, record, static_cast<int>(blocks), kThreads, g.cluster,
                         kSmemBytes<T, BN, kBackward>, stream, g);
 }
 
@@ -639,7 +643,7 @@ int chunks_of(int64_t nk) { return static_cast<int>((nk + kK - 1) / kK); }
 
 }  // namespace
 
-cudaError_t launch_gather_forward(const DenseArgs& a, const GatherPlan& plan, cudaStream_t stream) {
+cudaError_t launch_gather_forward(const DenseArgs& a, const GatherPlan& plan, cudaStream_t stream, const Withhold* hook) {
   GatherParams g = {};
   Part& d = g.part[0];
   d.a = source(a.w, nullptr, a.out, a.in, a.dt);
@@ -647,6 +651,11 @@ cudaError_t launch_gather_forward(const DenseArgs& a, const GatherPlan& plan, cu
   d.np = a.out; d.nq = a.rows; d.chunks = chunks_of(a.in);
   d.bias = a.b; d.bias_bf16 = a.b_dt == VN_BF16; d.act = a.act;
   d.residual = a.residual; d.out = a.y; d.preact = a.preact;
+  if (hook != nullptr) {
+    g.withhold = hook->at;
+    g.timeout_ns = hook->timeout_ns;
+    return run<__nv_bfloat16, 64, false, false, true>(g, plan.log_split, stream);
+  }
   return a.dt == VN_BF16 ? run_plan<__nv_bfloat16, false>(g, plan, stream)
                          : run_plan<float, false>(g, plan, stream);
 }

@@ -60,6 +60,7 @@ struct Params : Epilogue {
   int k_chunks, iters;  // iterations of the k loop: k_chunks x pairs of planes
   int stages;
   uint32_t idesc;
+  int withhold;  // test hook: the stage of the first CTA that expects more bytes than its copies bring
   unsigned long long timeout_ns;
 };
 
@@ -115,7 +116,8 @@ constexpr uint32_t kPairStageBytes = kABytes + 128 * 128;
 
 // Barriers: full[S] (leader's, armed for both CTAs' bytes), empty[S], tmem_full[2],
 // tmem_empty[2] (leader's, both CTAs' epilogues), drain, residual[2 halves][kBuffers].
-template <typename T, bool kAMn, bool kBMn, bool kStaged>
+// kHook: the instance whose waits a test makes run out.
+template <typename T, bool kAMn, bool kBMn, bool kStaged, bool kHook = false>
 __global__ void __launch_bounds__(kPairThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
             const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap zmap,
@@ -181,7 +183,7 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
         int kc = 0, pr = p.iters == p.k_chunks ? 5 : 0;
         for (int it = 0; it < p.iters; ++it, rg.next(S)) {
           if (!(ok = mbar_wait(empty(rg.s), rg.ph ^ 1u, ctl))) break;
-          if (rank == 0) mbar_expect_tx(full(rg.s), bytes);
+          if (rank == 0) mbar_expect_tx(full(rg.s), bytes + (kHook && pair == 0 && it == p.withhold ? 16 : 0));
           load_stage<kAMn, kBMn, true>(stage0 + rg.s * kPairStageBytes, &amap, &bmap, map_rank(full(rg.s), 0), p0, q0,
                                        kc * kK, plane_a(pr), plane_b(pr), blocks);
           if (++kc == p.k_chunks) { kc = 0; ++pr; }
@@ -357,7 +359,7 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
 // ---------------------------------------------------------------- single CTAs, k split
 // The unit's k iterations are split over the cluster's CTAs. Barriers: full[S], empty[S],
 // tmem_full.
-template <typename T, int BN, bool kAMn, bool kBMn>
+template <typename T, int BN, bool kAMn, bool kBMn, bool kHook = false>
 __global__ void __launch_bounds__(kThreads)
 single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const Params p,
               const int split) {
@@ -408,7 +410,7 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
       int pr = planes ? first / p.k_chunks : 5, kc = planes ? first % p.k_chunks : first;
       for (int it = first; it < last; ++it, rg.next(S)) {
         if (!(ok = mbar_wait(empty(rg.s), rg.ph ^ 1u, ctl))) break;
-        mbar_expect_tx(full(rg.s), kStageBytes);
+        mbar_expect_tx(full(rg.s), kStageBytes + (kHook && blockIdx.x == 0 && it - first == p.withhold ? 16 : 0));
         load_stage<kAMn, kBMn, false>(stage0 + rg.s * kStageBytes, &amap, &bmap, full(rg.s), tp * 128, tq * BN, kc * kK,
                                       plane_a(pr), plane_b(pr), BN / 64);
         ++issued;
@@ -555,7 +557,7 @@ bool make_result_map(CUtensorMap* map, const void* p, vn_dtype dt, int64_t np, i
 
 constexpr size_t kFixed = 1024 + 8 * (2 * kMaxStages + 8 + 2 * kBuffers) + sizeof(Control);
 
-template <typename T, bool kAMn, bool kBMn, bool kStaged>
+template <typename T, bool kAMn, bool kBMn, bool kStaged, bool kHook = false>
 cudaError_t run_pair_typed(const TcProduct& d, Params p, int sms, int bn, cudaStream_t stream) {
   const int pairs = sms / 2;
   p.bn = bn;
@@ -576,7 +578,7 @@ cudaError_t run_pair_typed(const TcProduct& d, Params p, int sms, int bn, cudaSt
   // instead of 6 cost 5 to 12 per cent.
   p.stages = std::min<int>(kMaxStages, static_cast<int>((232448 - kFixed - p.staging_bytes) / kPairStageBytes));
   static SmemRecord record;
-  return launch_cluster(pair_kernel<T, kAMn, kBMn, kStaged>, record, grid, kPairThreads, 2,
+  return launch_cluster(pair_kernel<T, kAMn, kBMn, kStaged, kHook>, record, grid, kPairThreads, 2,
                         kFixed + p.stages * kPairStageBytes + p.staging_bytes, stream, am, bm, ym, zm, rm, p);
 }
 template <typename T, bool kAMn, bool kBMn>
@@ -587,7 +589,7 @@ cudaError_t run_pair(const TcProduct& d, const Params& p, int sms, int bn, cudaS
                 : run_pair_typed<T, kAMn, kBMn, false>(d, p, sms, bn, stream);
 }
 
-template <typename T, int BN, bool kAMn, bool kBMn>
+template <typename T, int BN, bool kAMn, bool kBMn, bool kHook = false>
 cudaError_t run_single(const TcProduct& d, Params p, int split, cudaStream_t stream) {
   constexpr uint32_t kStage = kABytes + BN * 128;
   CUtensorMap am, bm;
@@ -599,12 +601,12 @@ cudaError_t run_single(const TcProduct& d, Params p, int split, cudaStream_t str
   p.idesc = idesc_of(128, BN, kAMn, kBMn);
   if (p.units * split > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   static SmemRecord record;
-  return launch_cluster(single_kernel<T, BN, kAMn, kBMn>, record, static_cast<int>(p.units * split), kThreads, split,
+  return launch_cluster(single_kernel<T, BN, kAMn, kBMn, kHook>, record, static_cast<int>(p.units * split), kThreads, split,
                         kFixed + static_cast<size_t>(p.stages) * kStage, stream, am, bm, p, split);
 }
 
 template <typename T, bool kAMn, bool kBMn>
-cudaError_t run(const TcProduct& d, const TilePlan& plan, cudaStream_t stream) {
+cudaError_t run(const TcProduct& d, const TilePlan& plan, cudaStream_t stream, const Withhold* hook) {
   DeviceInfo dev;
   cudaError_t err = device_info(&dev);
   if (err != cudaSuccess) return err;
@@ -615,6 +617,14 @@ cudaError_t run(const TcProduct& d, const TilePlan& plan, cudaStream_t stream) {
   p.k_chunks = static_cast<int>((d.nk + kK - 1) / kK);
   p.iters = p.k_chunks * (d.a.planes == 3 ? 6 : 1);
   p.timeout_ns = kTimeoutNs;
+  if constexpr (sizeof(T) == 2 && !kAMn && !kBMn) {
+    if (hook != nullptr) {
+      p.withhold = hook->at;
+      p.timeout_ns = hook->timeout_ns;
+      return plan.pair ? run_pair_typed<T, false, false, true, true>(d, p, dev.sm_count, plan.bn, stream)
+                       : run_single<T, 64, false, false, true>(d, p, 1 << plan.log_split, stream);
+    }
+  }
   if (plan.pair) return run_pair<T, kAMn, kBMn>(d, p, dev.sm_count, plan.bn, stream);
   const int split = 1 << plan.log_split;
   if constexpr (!kBMn) {
@@ -625,15 +635,15 @@ cudaError_t run(const TcProduct& d, const TilePlan& plan, cudaStream_t stream) {
 }
 
 template <typename T>
-cudaError_t run_layout(const TcProduct& d, const TilePlan& plan, cudaStream_t stream) {
-  if (!d.a.mn) return run<T, false, false>(d, plan, stream);
-  return d.b.mn ? run<T, true, true>(d, plan, stream) : run<T, true, false>(d, plan, stream);
+cudaError_t run_layout(const TcProduct& d, const TilePlan& plan, cudaStream_t stream, const Withhold* hook) {
+  if (!d.a.mn) return run<T, false, false>(d, plan, stream, hook);
+  return d.b.mn ? run<T, true, true>(d, plan, stream, hook) : run<T, true, false>(d, plan, stream, hook);
 }
 
 }  // namespace
 
-cudaError_t launch_tc_product(const TcProduct& d, const TilePlan& plan, cudaStream_t stream) {
-  return d.dt == VN_BF16 ? run_layout<__nv_bfloat16>(d, plan, stream) : run_layout<float>(d, plan, stream);
+cudaError_t launch_tc_product(const TcProduct& d, const TilePlan& plan, cudaStream_t stream, const Withhold* hook) {
+  return d.dt == VN_BF16 ? run_layout<__nv_bfloat16>(d, plan, stream, hook) : run_layout<float>(d, plan, stream, hook);
 }
 
 cudaError_t take_dense_status(unsigned int* status, cudaStream_t stream) { return take_wait_status(status, stream); }
