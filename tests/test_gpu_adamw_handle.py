@@ -1,0 +1,82 @@
+"""AdamW's handle: what it holds, and what happens to it beside its steps."""
+
+import copy
+import io
+import pickle
+
+import pytest
+import torch
+
+import virtual_noise_perturbed_gb300 as vn
+from virtual_noise_perturbed_gb300.build import build
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build()
+
+
+def make(bits, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    params = [torch.randn(s, generator=g).to(DEV) for s in ((70, 30), (70,), (5, 70))]
+    grads = [torch.randn(p.shape, generator=g).to(DEV) for p in params]
+    return vn.AdamW(params, lr=1e-2, weight_decay=[0.1, 0.0, 0.2], state_bits=bits, maximize=True), grads
+
+
+def bits_of(opt):
+    return [t.clone() for t in opt.params] + [t.view(torch.uint8).clone() for _, t in sorted(opt.state.items())]
+
+
+def same(a, b):
+    return all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def saved(opt):
+    f = io.BytesIO()
+    torch.save(opt, f)
+    f.seek(0)
+    return torch.load(f, weights_only=False)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("twin", [copy.deepcopy, lambda o: pickle.loads(pickle.dumps(o)), saved])
+def test_a_copy_steps_on_its_own_tensors(twin, bits):
+    opt, grads = make(bits)
+    opt.step(grads)
+    before = bits_of(opt)
+    other = twin(opt)
+    assert other.steps == 1 and same(bits_of(other), before)
+    other.step(grads)
+    assert same(bits_of(opt), before)                       # nothing of the first has moved
+    after = bits_of(other)
+    assert not any(torch.equal(p, q) for p, q in zip(after[:3], before[:3])) and not same(after[3:], before[3:])
+    assert same([t.reshape(-1) for t in other.moments()], [t.reshape(-1) for t in saved(other).moments()])
+    opt.step(grads)
+    assert same(bits_of(opt), after) and opt.steps == other.steps == 2
+    del opt
+    other.step(grads)                                       # the first is gone
+    third, _ = make(bits)
+    for _ in range(3):
+        third.step(grads)
+    assert same(bits_of(other), bits_of(third))
+
+
+def test_a_copy_of_a_policy_and_its_handle_keep_their_views():
+    """Parameters that are views of one vector stay views of one vector in a deep copy of both."""
+    flat = torch.arange(600, dtype=torch.float32, device=DEV)
+    opt = vn.AdamW([flat[:256].view(16, 16), flat[300:]], lr=0.1)
+    flat2, opt2 = copy.deepcopy((flat, opt))
+    opt2.step([torch.ones(16, 16, device=DEV), torch.ones(300, device=DEV)])
+    assert torch.equal(flat, torch.arange(600, dtype=torch.float32, device=DEV))
+    assert bool((flat2[:256] != flat[:256]).all()) and torch.equal(flat2[256:300], flat[256:300])
+
+
+def test_a_handle_loaded_off_the_gpu_is_refused():
+    f = io.BytesIO()
+    torch.save(make(32)[0], f)
+    f.seek(0)
+    with pytest.raises(ValueError, match="CUDA"):
+        torch.load(f, weights_only=False, map_location="cpu")

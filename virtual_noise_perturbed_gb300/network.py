@@ -113,7 +113,8 @@ class AdamW:
     ``state`` holds the moments in flat tensors: "m" and "v", and with 8 bits "m_scale" and
     "v_scale" (v's codes are of its root). Tensor i's moments are the ``params[i].numel()``
     elements from ``offsets[i]`` on, a multiple of 256. To resume, pass the saved ``state`` and
-    ``steps``; the tensors passed are used and updated as they are."""
+    ``steps``; the tensors passed are used and updated as they are. A deep copy, and a pickled handle,
+    have parameters and moments of their own."""
 
     BLOCK = 256
 
@@ -124,13 +125,7 @@ class AdamW:
         if not self.params:
             raise ValueError("at least one tensor is needed")
         self._params = list(self.params)
-        for i, p in enumerate(self.params):
-            if not isinstance(p, torch.Tensor) or not p.is_cuda or not p.is_contiguous():
-                raise ValueError(f"params[{i}] must be a contiguous CUDA tensor (updated in place)")
-            if p.dtype != self.params[0].dtype:
-                raise TypeError("the parameters must have one dtype")
-        self.device = _device(*self.params)
-        _dt(self.params[0], "params[0]")
+        self._check_params()
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
         n = len(self.params)
@@ -144,21 +139,50 @@ class AdamW:
         for s in self.sizes:
             self.offsets.append(total)
             total += -(-s // self.BLOCK) * self.BLOCK
+        self._decay, self._total = decay, total
         self._tensors = self._state(total, state)
-        # One row of eight words a tensor, as the library's struct has them: param, grad, both
-        # moments, their scales, the number of elements, the decay.
+        self._lay_out()
+
+    def _lay_out(self) -> None:
+        """The table that the library reads: one row of eight words a tensor, as its struct has them:
+        param, grad, both moments, their scales, the number of elements, the decay."""
+        n = len(self.params)
         self._table = t = array("Q", bytes(64 * n))
         held = self._tensors
-        m, v, size = held["m"].data_ptr(), held["v"].data_ptr(), state_bits // 8
+        m, v, size = held["m"].data_ptr(), held["v"].data_ptr(), self.state_bits // 8
         t[2::8] = array("Q", [m + o * size for o in self.offsets])
         t[3::8] = array("Q", [v + o * size for o in self.offsets])
-        if state_bits == 8:
+        if self.state_bits == 8:
             m, v = held["m_scale"].data_ptr(), held["v_scale"].data_ptr()
             t[4::8] = array("Q", [m + o // self.BLOCK * 4 for o in self.offsets])
             t[5::8] = array("Q", [v + o // self.BLOCK * 4 for o in self.offsets])
         t[6::8] = array("Q", self.sizes)
-        t[7::8] = array("Q", struct.pack(f"{n}d", *decay))
+        t[7::8] = array("Q", struct.pack(f"{n}d", *self._decay))
         self._address = t.buffer_info()[0]
+
+    def __getstate__(self) -> dict:
+        kept = dict(self.__dict__)
+        del kept["_table"], kept["_address"]
+        # Codes travel as bytes: plain pickle does not know torch's 8-bit types.
+        kept["_tensors"] = {k: t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t for k, t in self._tensors.items()}
+        return kept
+
+    def __setstate__(self, kept: dict) -> None:
+        # A copy has tensors, and so addresses, of its own.
+        self.__dict__.update(kept)
+        self._tensors = {k: t.view(torch.float8_e4m3fn) if t.dtype == torch.uint8 else t for k, t in kept["_tensors"].items()}
+        self._check_params()
+        self._state(self._total, self._tensors)
+        self._lay_out()
+
+    def _check_params(self) -> None:
+        for i, p in enumerate(self.params):
+            if not isinstance(p, torch.Tensor) or not p.is_cuda or not p.is_contiguous():
+                raise ValueError(f"params[{i}] must be a contiguous CUDA tensor (updated in place)")
+            if p.dtype != self.params[0].dtype:
+                raise TypeError("the parameters must have one dtype")
+        self.device = _device(*self.params)
+        _dt(self.params[0], "params[0]")
 
     def _state(self, total: int, given: Optional[dict]) -> dict:
         kind = torch.float32 if self.state_bits == 32 else torch.float8_e4m3fn
