@@ -419,7 +419,8 @@ typedef struct vn_adamw_tensor {
  * which a positive one is never stored as 0 (it divides the next step): at least 2^-9. A
  * block whose largest magnitude is below 1e-30 is stored as zeros. The step itself uses the
  * unrounded moments; a gradient that is not finite makes its block's moments not finite.
- * Tensors of a call may not overlap one another. 0 <= beta < 1, eps >= 0, all finite.
+ * Captured in a graph, every replay has this call's step, lr and addresses, so bias corrections do not
+ * advance. Tensors of a call may not overlap one another. 0 <= beta < 1, eps >= 0, all finite.
  */
 vn_status vn_adamw(const vn_adamw_tensor* tensors, int64_t n_tensors, vn_dtype param_dt,
                    vn_dtype grad_dt, int state_bits, double lr, double beta1, double beta2,

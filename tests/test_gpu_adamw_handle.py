@@ -80,3 +80,21 @@ def test_a_handle_loaded_off_the_gpu_is_refused():
     f.seek(0)
     with pytest.raises(ValueError, match="CUDA"):
         torch.load(f, weights_only=False, map_location="cpu")
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_step_is_not_captured(bits):
+    """Replays would repeat the capture's step number: refused, and neither counted nor launched."""
+    opt, grads = make(bits)
+    opt.step(grads)
+    before = bits_of(opt)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError, match="captured"):
+            opt.step(grads)
+        kept = grads[0] + 1                                 # the capture itself goes on
+    graph.replay()
+    torch.cuda.synchronize()
+    assert opt.steps == 1 and same(bits_of(opt), before) and torch.equal(kept, grads[0] + 1)
+    opt.step(grads)
+    assert opt.steps == 2

@@ -9,6 +9,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -376,6 +377,9 @@ PyObject* adamw(PyObject* const* a, Py_ssize_t count) {
   const int maximize = truth(a[9]);
   {
     const On on(first);
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
+      raise(PyExc_RuntimeError, "AdamW.step cannot be captured in a graph: its step number and learning rate would be "
+                                "those of the capture in every replay");
     check(vn_adamw(table, n, dtype_of(first, "params"), kind == at::kBFloat16 ? VN_BF16 : VN_F32, bits, lr, beta1, beta2,
                    eps, step, maximize, on.stream),
           "vn_adamw");

@@ -209,7 +209,8 @@ class AdamW:
     def step(self, grads: Union[torch.Tensor, Sequence[torch.Tensor]], lr: Optional[float] = None) -> None:
         """One step of every tensor. ``grads``: a gradient for each tensor, or one flat tensor with
         all of them one after another (as ``virtual_flat_gradient`` lays them out); float32 or
-        bfloat16. ``lr`` replaces the learning rate for this step."""
+        bfloat16. ``lr`` replaces the learning rate for this step. A step cannot be captured in a graph
+        (RuntimeError): replays would repeat the step number and learning rate of the capture."""
         if not isinstance(grads, (list, torch.Tensor)):
             grads = list(grads)
         (_binding or _native()).adamw(self._params, grads, self._address, self.state_bits, self.lr if lr is None else lr,
