@@ -98,3 +98,27 @@ def test_a_step_is_not_captured(bits):
     assert opt.steps == 1 and same(bits_of(opt), before) and torch.equal(kept, grads[0] + 1)
     opt.step(grads)
     assert opt.steps == 2
+
+
+def test_autograd_notices_a_step_between_forward_and_backward():
+    w = torch.ones(4, 4, device=DEV, requires_grad=True)
+    x = torch.ones(4, 4, device=DEV, requires_grad=True)
+    loss = (x @ w).sum()
+    vn.AdamW([w]).step([torch.ones(4, 4, device=DEV)])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        frozen = torch.ones(4, device=DEV)
+    vn.AdamW([frozen]).step([torch.ones(4, device=DEV)])
+    assert bool((frozen < 1).all())
+
+
+def test_autograd_notices_an_output_buffer_written_over():
+    a, b = torch.ones(3, 8, device=DEV), torch.ones(4, 8, device=DEV)
+    for write in (lambda out: vn.linear(a, b, out=out), lambda out: vn.layer_norm(torch.ones(3, 4, device=DEV), out=out)):
+        out = torch.ones(3, 4, device=DEV)
+        scale = torch.ones(3, 4, device=DEV, requires_grad=True)
+        loss = (scale * out).sum()
+        write(out)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()

@@ -96,11 +96,18 @@ void vector_of(const std::optional<at::Tensor>& t, const char* name, int64_t n, 
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& x) {
   return at::detail::empty_cuda(shape, type, x.device(), std::nullopt);
 }
+// What a call writes over counts as changed in place, for autograd's check of what it has saved.
+void changed(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 at::Tensor result(PyObject* out, at::IntArrayRef shape, const at::Tensor& x) {
   if (out == Py_None) return empty(shape, x.scalar_type(), x);
   if (THPVariable_Check(out)) {
     const at::Tensor& t = THPVariable_Unpack(out);
-    if (t.sizes() == shape && t.scalar_type() == x.scalar_type() && t.is_contiguous() && t.device() == x.device()) return t;
+    if (t.sizes() == shape && t.scalar_type() == x.scalar_type() && t.is_contiguous() && t.device() == x.device()) {
+      changed(t);
+      return t;
+    }
   }
   raise(PyExc_ValueError, "out must be a contiguous " + text_of(x.scalar_type()) + " tensor of shape " + text_of(shape) +
                               " on " + text_of(x.device()));
@@ -384,6 +391,7 @@ PyObject* adamw(PyObject* const* a, Py_ssize_t count) {
                    eps, step, maximize, on.stream),
           "vn_adamw");
   }
+  for (Py_ssize_t i = 0; i < n; ++i) changed(THPVariable_Unpack(PyList_GET_ITEM(params, i)));
   Py_RETURN_NONE;
 }
 

@@ -7,7 +7,9 @@ Like the rest of the package's Python, these functions only check and marshal ar
 call ``libvn.so`` on the current CUDA stream; all arithmetic runs in the library's kernels.
 They do it in a small extension module (``csrc/vn_torch.cpp``), since a call's time on the host is
 what a small layer costs. Tensors must be on a CUDA device; there is no CPU path. Inputs that
-are not contiguous are copied first.
+are not contiguous are copied first. Nothing here is recorded by autograd: results carry no gradient function,
+and gradients come from the ``..._backward`` calls. What a call writes over (``out``, the
+parameters of a step) counts as changed in place, so autograd refuses to use what it has saved of it.
 """
 
 from __future__ import annotations
