@@ -122,3 +122,16 @@ def test_autograd_notices_an_output_buffer_written_over():
         write(out)
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             loss.backward()
+
+
+def test_tensors_that_share_memory_are_refused():
+    flat = torch.ones(2048, device=DEV)
+    m, v = torch.zeros(1024, device=DEV), torch.zeros(1024, device=DEV)
+    for params in ([flat[:10], flat[:10]], [flat[5:20], flat[:6]], [flat[:100], flat[50:60], flat[200:]]):
+        with pytest.raises(ValueError, match="share memory"):
+            vn.AdamW(params)
+    for state in ({"m": m, "v": m}, {"m": flat[:1024], "v": v}, {"m": flat[1023:2047], "v": v}):
+        with pytest.raises(ValueError, match="share memory"):
+            vn.AdamW([flat[:1024]], state=state)
+    vn.AdamW([flat[:10], flat[10:20], flat[20:20], flat[15:15], flat[20:]])
+    vn.AdamW([flat[:1024]], state={"m": flat[1024:], "v": v})

@@ -107,8 +107,8 @@ def layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
 class AdamW:
     """AdamW over many tensors, one launch a step (``vn_adamw``).
 
-    ``params``: contiguous CUDA tensors of one dtype (float32 or bfloat16) on one device,
-    updated in place by ``step``. ``weight_decay``: one number, or one for each tensor.
+    ``params``: contiguous CUDA tensors of one dtype (float32 or bfloat16) on one device that share no
+    memory, updated in place by ``step``. ``weight_decay``: one number, or one for each tensor.
     ``maximize=True`` ascends: the direction of a fitness gradient. ``state_bits``: 32, or 8 for
     moments held as e4m3 codes with a float32 scale for each 256 elements of a tensor.
 
@@ -149,6 +149,7 @@ class AdamW:
         """The table that the library reads: one row of eight words a tensor, as its struct has them:
         param, grad, both moments, their scales, the number of elements, the decay."""
         n = len(self.params)
+        self._refuse_overlaps()
         self._table = t = array("Q", bytes(64 * n))
         held = self._tensors
         m, v, size = held["m"].data_ptr(), held["v"].data_ptr(), self.state_bits // 8
@@ -161,6 +162,16 @@ class AdamW:
         t[6::8] = array("Q", self.sizes)
         t[7::8] = array("Q", struct.pack(f"{n}d", *self._decay))
         self._address = t.buffer_info()[0]
+
+    def _refuse_overlaps(self) -> None:
+        # Blocks of all tensors are updated at once: memory that two of them shared would hold either's result.
+        named = [(f"params[{i}]", p) for i, p in enumerate(self.params)] + [(f"state['{k}']", t) for k, t in self._tensors.items()]
+        end, last = 0, ""
+        for start, size, name in sorted((t.data_ptr(), t.numel() * t.element_size(), name) for name, t in named):
+            if size and start < end:
+                raise ValueError(f"{last} and {name} share memory")
+            if size:
+                end, last = start + size, name
 
     def __getstate__(self) -> dict:
         kept = dict(self.__dict__)
