@@ -8,7 +8,8 @@ runtime linked statically; the driver API is reached through the runtime's
 entry-point query, so no link against libcuda is needed). ``csrc/vn_torch.cpp``, the
 centre network's calls on torch tensors, is compiled beside them with the host compiler
 into ``_binding.so``, which links to the library. A rebuild happens
-only when a source or header is newer than the libraries. Builds take a file lock,
+only when a source or header is newer than the libraries, or when ``_binding.so`` was built for another
+Python or torch than this one. Builds take a file lock,
 so processes that start together (the ranks of one job, test workers) build
 once: the others wait, then find the library current.
 """
@@ -19,6 +20,7 @@ import argparse
 import concurrent.futures as cf
 import fcntl
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -60,8 +62,27 @@ def _inputs() -> list:
         + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
+def _made_for() -> str:
+    """What _binding.so is tied to: the interpreter's ABI, and torch's version and place."""
+    try:
+        torch_version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch_version = "?"
+    return f"{sys.version} {sysconfig.get_config_var('SOABI')} torch {torch_version} in {_torch_dir()}"
+
+
+def _stamp() -> str:
+    return os.path.join(BUILD, "binding.made_for")
+
+
 def up_to_date() -> bool:
     if not os.path.exists(LIB) or not os.path.exists(BINDING):
+        return False
+    try:
+        with open(_stamp()) as f:
+            if f.read() != _made_for():
+                return False
+    except FileNotFoundError:
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _inputs())
@@ -121,11 +142,15 @@ def _compile_and_link(verbose: bool, extra_flags) -> None:
     tmp = LIB + ".tmp"
     _run([cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static", "-Xlinker", "-soname=libvn.so"], verbose)
     os.replace(tmp, LIB)
+    if os.path.exists(_stamp()):
+        os.remove(_stamp())
     tmp = BINDING + ".tmp"
     _run([cxx, "-shared", "-o", tmp, bobj, "-L", PKG, "-l:libvn.so", "-Wl,-rpath,$ORIGIN",
           "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"],
          verbose)
     os.replace(tmp, BINDING)
+    with open(_stamp(), "w") as f:
+        f.write(_made_for())
 
 
 def main(argv=None) -> int:
