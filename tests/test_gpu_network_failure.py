@@ -6,6 +6,7 @@ records the time-out, stops, frees its tensor memory and returns; the status is 
 host, and an ordinary call right after is correct."""
 
 import ctypes
+import time
 
 import pytest
 import torch
@@ -68,3 +69,22 @@ def test_hook_refuses_bad_arguments():
     assert call(kernel=3) == 4 and call(at=-1) == 4 and call(ms=0.0) == 4
     assert call(k=64) == 2 and call(k=132) == 2 and call(n=7) == 2 and call(rows=0) == 2
     assert call(x=0) == 1 and call(y=a + 0x20008) == 5 and call(y=a) == 4
+
+
+def test_the_status_of_all_kernels_is_one_read():
+    """Every kernel sets the same word: a check of the status costs about one read of a few bytes (a word
+    for each of the three tensor-core kernels cost twice that)."""
+    build()
+    x = torch.zeros(8, device=DEV)
+
+    def median(call):
+        times = []
+        for _ in range(301):
+            t = time.perf_counter()
+            call()
+            times.append(time.perf_counter() - t)
+        return sorted(times)[150]
+
+    median(vn.device_status)
+    ratio = min(median(vn.device_status) / median(x[0].item) for _ in range(5))
+    assert ratio < 1.7, ratio

@@ -8,7 +8,6 @@
 #include <mutex>
 
 #include "vn.h"
-#include "vn_dense.h"
 #include "vn_internal.h"
 
 namespace vn {
@@ -738,11 +737,7 @@ vn_status vn_device_status(void* stream) {
   unsigned int status = 0;
   err = vn::take_device_status(&status, static_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) return cuda_failure(err);
-  unsigned int dense = 0, gather = 0;
-  err = vn::take_dense_status(&dense, static_cast<cudaStream_t>(stream));
-  if (err == cudaSuccess) err = vn::take_gather_status(&gather, static_cast<cudaStream_t>(stream));
-  if (err != cudaSuccess) return cuda_failure(err);
-  return (status | dense | gather) ? VN_ERR_TIMEOUT : VN_OK;
+  return status ? VN_ERR_TIMEOUT : VN_OK;
 }
 
 }  // extern "C"

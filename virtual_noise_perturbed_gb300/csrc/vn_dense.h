@@ -67,9 +67,5 @@ cudaError_t launch_rows_forward(const DenseArgs& a, cudaStream_t stream);  // ro
 cudaError_t launch_gather_forward(const DenseArgs& a, const GatherPlan& plan, cudaStream_t stream,
                                   const Withhold* hook = nullptr);
 cudaError_t launch_gather_backward(const DenseGradArgs& a, const GatherPlan& plan, cudaStream_t stream);
-cudaError_t take_gather_status(unsigned int* status, cudaStream_t stream);
-
-// Reads and clears the status word of the tensor-core products (0 = fine).
-cudaError_t take_dense_status(unsigned int* status, cudaStream_t stream);
 
 }  // namespace vn

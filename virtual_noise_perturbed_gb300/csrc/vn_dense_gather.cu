@@ -62,6 +62,7 @@ struct GatherParams {
   int cluster;
   int withhold;  // test hook: the chunk that CTA 0's first warp never hands over; beyond its last, the final commit
   unsigned long long timeout_ns;
+  unsigned int* status;
 };
 
 // Eight consecutive elements of an operand as they are in memory.
@@ -544,6 +545,7 @@ gather_kernel(const __grid_constant__ GatherParams g) {
     mbar_init(bar0 + 8u * (2 * S), 1);
     ctl->abort = 0;
     ctl->timeout_ns = g.timeout_ns;
+    ctl->status = g.status;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 8) tmem_alloc<false>(smem_u32(s_tmem), kCols);
@@ -594,6 +596,8 @@ cudaError_t run(GatherParams& g, const int (&log_split)[2], cudaStream_t stream)
   }
   if (blocks == 0) return cudaSuccess;
   if (!kHook) g.timeout_ns = kTimeoutNs;
+  const cudaError_t err = device_status_word(&g.status);
+  if (err != cudaSuccess) return err;
   constexpr int S = kStages<T, BN>;
   static_assert(S >= 2 && S * kStageBytes<T, BN> >= (BN + 4) * 512 + 8192, "the partial sums lie in the stages");
   static SmemRecord record;
@@ -683,7 +687,5 @@ cudaError_t launch_gather_backward(const DenseGradArgs& a, const GatherPlan& pla
   return a.dt == VN_BF16 ? run_plan<__nv_bfloat16, true>(g, plan, stream)
                          : run_plan<float, true>(g, plan, stream);
 }
-
-cudaError_t take_gather_status(unsigned int* status, cudaStream_t stream) { return take_wait_status(status, stream); }
 
 }  // namespace vn

@@ -62,6 +62,7 @@ struct Params : Epilogue {
   uint32_t idesc;
   int withhold;  // test hook: the stage of the first CTA that expects more bytes than its copies bring
   unsigned long long timeout_ns;
+  unsigned int* status;
 };
 
 // Tile of a unit: groups of 8 tiles along q, p fastest between them, so that the CTAs at
@@ -156,6 +157,7 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
     for (int b = 0; b < 2 * kBuffers; ++b) mbar_init(arrived(0, b), 1);
     ctl->abort = 0;
     ctl->timeout_ns = p.timeout_ns;
+    ctl->status = p.status;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<true>(smem_u32(s_tmem), 512);
@@ -391,6 +393,7 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
     mbar_init(tmem_full, 1);
     ctl->abort = 0;
     ctl->timeout_ns = p.timeout_ns;
+    ctl->status = p.status;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<false>(smem_u32(s_tmem), kCols);
@@ -617,6 +620,7 @@ cudaError_t run(const TcProduct& d, const TilePlan& plan, cudaStream_t stream, c
   p.k_chunks = static_cast<int>((d.nk + kK - 1) / kK);
   p.iters = p.k_chunks * (d.a.planes == 3 ? 6 : 1);
   p.timeout_ns = kTimeoutNs;
+  if ((err = device_status_word(&p.status)) != cudaSuccess) return err;
   if constexpr (sizeof(T) == 2 && !kAMn && !kBMn) {
     if (hook != nullptr) {
       p.withhold = hook->at;
@@ -645,7 +649,5 @@ cudaError_t run_layout(const TcProduct& d, const TilePlan& plan, cudaStream_t st
 cudaError_t launch_tc_product(const TcProduct& d, const TilePlan& plan, cudaStream_t stream, const Withhold* hook) {
   return d.dt == VN_BF16 ? run_layout<__nv_bfloat16>(d, plan, stream, hook) : run_layout<float>(d, plan, stream, hook);
 }
-
-cudaError_t take_dense_status(unsigned int* status, cudaStream_t stream) { return take_wait_status(status, stream); }
 
 }  // namespace vn

@@ -196,6 +196,8 @@ cudaError_t launch_adamw_moments(const void* exp_avg, const void* exp_avg_sq, co
                                  const float* exp_avg_sq_scale, int64_t n, float* m, float* v,
                                  cudaStream_t stream);
 
+// The current device's status word, which every bounded wait that runs out sets.
+cudaError_t device_status_word(unsigned int** word);
 // Reads and clears the device status word of the bounded-wait kernels (0 = fine).
 cudaError_t take_device_status(unsigned int* status, cudaStream_t stream);
 

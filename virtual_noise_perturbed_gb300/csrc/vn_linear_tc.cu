@@ -38,6 +38,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 #include <mutex>
 #include <type_traits>
@@ -47,8 +48,8 @@
 
 namespace vn {
 
-// Nonzero after a bounded wait ran out in a kernel of this file (read and
-// cleared by take_device_status). Bits: 1 = barrier wait timed out.
+// Nonzero after a bounded wait ran out, in a kernel of this file or in one that has this word's address
+// from device_status_word (read and cleared by take_device_status). Bits: 1 = barrier wait timed out.
 __device__ unsigned int g_device_status = 0;
 
 namespace {
@@ -1020,6 +1021,21 @@ cudaError_t launch_linear_tc_hook(const LinearArgs& a, cudaStream_t stream, long
                : launch_typed<1, true, false, false>(xmap, wmap, p, atoms, grid, smem, stream);
   }
   return launch_typed<1, false, false, false>(xmap, wmap, p, atoms, grid, smem, stream);
+}
+
+cudaError_t device_status_word(unsigned int** word) {
+  static std::atomic<unsigned int*> known[kMaxDevices];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  *word = known[dev].load(std::memory_order_acquire);
+  if (*word != nullptr) return cudaSuccess;
+  void* p = nullptr;
+  if ((err = cudaGetSymbolAddress(&p, g_device_status)) != cudaSuccess) return err;
+  *word = static_cast<unsigned int*>(p);
+  known[dev].store(*word, std::memory_order_release);
+  return cudaSuccess;
 }
 
 cudaError_t take_device_status(unsigned int* status, cudaStream_t stream) {

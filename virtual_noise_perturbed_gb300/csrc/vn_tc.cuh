@@ -1,8 +1,7 @@
 // vn_tc.cuh -- what the tensor-core kernels of the centre network share: the PTX they issue,
 // bounded barrier waits, operand descriptors, the epilogue's types and cluster launches.
 //
-// Everything here has internal linkage: each translation unit that includes it has a status
-// word of its own, which its take_..._status function reads.
+// Everything here has internal linkage.
 #pragma once
 
 #include <cuda.h>
@@ -18,9 +17,6 @@
 namespace vn {
 namespace {
 
-// Nonzero after a bounded wait of this translation unit ran out.
-__device__ unsigned int g_wait_status = 0;
-
 constexpr int kK = 64;                          // k of a stage: 128 bytes of bf16, one swizzle atom
 constexpr uint32_t kABytes = 128 * 128;         // 128 rows (or 64 k x 2 blocks of 64 p)
 constexpr uint32_t kBlockBytes = kK * 128;      // one 64-wide block of a p- or q-contiguous operand
@@ -30,6 +26,7 @@ struct Control {
   int abort;
   int pad;
   unsigned long long timeout_ns;
+  unsigned int* status;  // the device's status word, which a wait that ran out sets
 };
 
 // ---------------------------------------------------------------- PTX
@@ -114,7 +111,7 @@ __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volat
     if ((n & 63) == 0) {
       if (c->abort) return false;
       if (global_ns() - t0 > limit) {
-        atomicOr(&g_wait_status, 1u);
+        atomicOr(c->status, 1u);
         c->abort = 1;
         return false;
       }
@@ -349,17 +346,6 @@ cudaError_t launch_cluster(void (*fn)(KArgs...), SmemRecord& record, int grid, i
   const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(fn), smem, record);
   if (err != cudaSuccess) return err;
   return launch_overlapped(fn, dim3(static_cast<unsigned>(grid)), threads, cluster, smem, stream, args...);
-}
-
-// Reads and clears this translation unit's status word.
-cudaError_t take_wait_status(unsigned int* status, cudaStream_t stream) {
-  cudaError_t err =
-      cudaMemcpyFromSymbolAsync(status, g_wait_status, sizeof(unsigned int), 0, cudaMemcpyDeviceToHost, stream);
-  if (err != cudaSuccess) return err;
-  if ((err = cudaStreamSynchronize(stream)) != cudaSuccess || *status == 0) return err;
-  const unsigned int zero = 0;
-  err = cudaMemcpyToSymbolAsync(g_wait_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream);
-  return err == cudaSuccess ? cudaStreamSynchronize(stream) : err;
 }
 
 }  // namespace
