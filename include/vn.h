@@ -489,6 +489,14 @@ vn_status vn_testhook_linear_withhold(int kernel, const void* x, const void* w, 
                                       void* preact, int64_t withhold, double timeout_ms,
                                       void* stream);
 
+/* Which kernels vn_linear (or, with `backward`, vn_linear_backward) takes for these sizes, for tests that
+ * mean to reach each of them; launches nothing and needs no device. aligned: as for the workspaces.
+ * plan[10]: the route (0 few rows, 1 beyond 32-bit sizes, 2 gathered, 3 tiles); the gathered
+ * kernel's columns and log2 of its splits (of the forward product or grad_x's, of grad_w's); and for tiles
+ * of the forward product (or grad_x's), then of grad_w's: 1 for pairs, columns, log2 of the split. */
+vn_status vn_testhook_linear_plan(int64_t rows, int64_t in, int64_t out, vn_dtype dt, vn_act act,
+                                  int aligned, int backward, int32_t* plan);
+
 /* A static, human-readable name for a status code. */
 const char* vn_status_string(vn_status status);
 

@@ -3,6 +3,7 @@
 // touches the device; a failing check returns its status and launches nothing.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <mutex>
@@ -536,6 +537,18 @@ vn_status vn_linear(const void* x, const void* w, vn_dtype dt, const void* b, vn
   a.rows = rows; a.in = in; a.out = out; a.act = act; a.y = y; a.preact = preact;
   a.workspace = workspace;
   return launched(vn::launch_dense(a, static_cast<cudaStream_t>(stream)));
+}
+
+vn_status vn_testhook_linear_plan(int64_t rows, int64_t in, int64_t out, vn_dtype dt, vn_act act, int al, int backward,
+                                  int32_t* plan) {
+  const vn_status st = check_sizes(rows, in, out, dt);
+  if (st != VN_OK) return st;
+  if (!linear_act_ok(act)) return VN_ERR_VALUE;
+  if (plan == nullptr) return VN_ERR_NULL;
+  int32_t p[10];
+  vn::dense_plan(rows, in, out, dt, act, al != 0, backward != 0, p);
+  std::copy(p, p + 10, plan);
+  return VN_OK;
 }
 
 vn_status vn_testhook_linear_withhold(int kernel, const void* x, const void* w, const void* residual, int64_t rows,

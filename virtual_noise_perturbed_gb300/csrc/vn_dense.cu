@@ -578,6 +578,21 @@ cudaError_t launch_dense(const DenseArgs& a, cudaStream_t stream) {
   return product(d, a.dt, stream);
 }
 
+void dense_plan(int64_t rows, int64_t in, int64_t out, vn_dtype dt, vn_act act, bool aligned, bool backward, int32_t (&p)[10]) {
+  auto fill = [&](Route route, const GatherPlan& g, const TilePlan& t0, const TilePlan& t1) {
+    const int32_t all[10] = {static_cast<int32_t>(route), g.bn, g.log_split[0], g.log_split[1], t0.pair, t0.bn,
+                             t0.log_split, t1.pair, t1.bn, t1.log_split};
+    std::copy(all, all + 10, p);
+  };
+  if (backward) {
+    const BackwardPlan b = backward_plan(rows, in, out, dt, act, aligned);
+    fill(b.route, b.gather, b.dx, b.dw);
+  } else {
+    const ForwardPlan f = forward_plan(rows, in, out, dt, aligned);
+    fill(f.route, f.gather, f.tiles, TilePlan());
+  }
+}
+
 cudaError_t launch_dense_hook(const DenseArgs& a, int kernel, int at, unsigned long long timeout_ns, cudaStream_t stream) {
   const Withhold hook = {at, timeout_ns};
   if (kernel == 0) {
