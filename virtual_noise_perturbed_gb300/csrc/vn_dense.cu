@@ -374,7 +374,9 @@ GatherPlan gather_plan(const Shape (&shapes)[2], vn_dtype dt, bool backward, boo
   const bool bf16 = dt == VN_BF16;
   for (int bn : {16, 64, 128}) {
     if (backward && bn == 16) continue;
-    if (backward && bf16 && !vectors && bn == 128) continue;  // not built
+    // Not built: what would hold too many registers, and forward products in bf16 of more columns, which a
+    // sweep over sizes never chose (tiles by TMA are faster where rows start on 16 bytes).
+    if (bf16 && bn > (backward ? (vectors ? 128 : 64) : (vectors ? 16 : 64))) continue;
     const double stage = (vectors ? 1.0 : !bf16 ? 1.7 : bn > 16 ? 2.4 : 2.0) *  // rows that start anywhere
                          (backward    ? (bn == 128 ? (bf16 ? 2.2 : 3.1) : (bf16 ? 1.2 : 1.7))
                           : bn == 128 ? (bf16 ? 0.9 : 1.4)
@@ -397,7 +399,7 @@ GatherPlan gather_plan(const Shape (&shapes)[2], vn_dtype dt, bool backward, boo
           work += n * t;
           longest = std::max(longest, t);
         }
-        const int per_sm = bf16 && (vectors || bn < 128) ? 2 : 1;
+        const int per_sm = bf16 ? 2 : 1;
         const double room = resident(std::max(l0, l1), per_sm);
         // Two CTAs of an SM share its threads' time.
         double crowd = per_sm == 2 && ctas > resident(std::max(l0, l1), 1) ? 1.7 : 1.0;

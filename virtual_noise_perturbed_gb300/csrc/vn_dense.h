@@ -62,7 +62,7 @@ cudaError_t launch_tc_product(const TcProduct& d, const TilePlan& plan, cudaStre
 struct DenseArgs;
 struct DenseGradArgs;
 cudaError_t launch_rows_forward(const DenseArgs& a, cudaStream_t stream);  // rows <= 8 (vn_dense_rows.cu)
-// hook: bf16 whose rows start on 16 bytes, on 64 columns. Beyond a CTA's last chunk, `at` is the commit
+// hook: bf16 whose rows start on 16 bytes, on 16 columns. Beyond a CTA's last chunk, `at` is the commit
 // that the epilogue waits for.
 cudaError_t launch_gather_forward(const DenseArgs& a, const GatherPlan& plan, cudaStream_t stream,
                                   const Withhold* hook = nullptr);

@@ -516,10 +516,10 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
 
 // kBackward: parts 0 and 1 are dx (A = W, B = d) and dw (A = x, B = d^T, with the bias's sums);
 // otherwise part 0 is the forward product.
-// In bf16 the registers of two CTAs fit an SM, as their stages do (but not with 128 columns of shifted groups).
+// In bf16 the registers of two CTAs fit an SM, as their stages do.
 // kHook: the instance whose waits a test makes run out.
 template <typename T, int BN, bool kBackward, bool kShift, bool kHook = false>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && !(kShift && BN == 128) ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
 gather_kernel(const __grid_constant__ GatherParams g) {
   constexpr int S = kStages<T, BN>;
   constexpr uint32_t kCols = kTmemCols<T, BN>;
@@ -623,11 +623,13 @@ cudaError_t run_tile(GatherParams& g, const GatherPlan& plan, cudaStream_t strea
   if constexpr (!kBackward) {
     if (plan.bn == 16) return run<T, 16, kBackward, kShift>(g, plan.log_split, stream);
   }
-  // Gradients of 128 columns would hold 108 registers of shifted groups.
-  if constexpr (!(kBackward && kShift)) {
+  // In bf16: gradients of 128 columns would hold 108 registers of shifted groups; no forward product is
+  // planned on 128 columns, nor on 64 where its rows start on 16 bytes.
+  if constexpr (sizeof(T) == 4 || (kBackward && !kShift)) {
     if (plan.bn == 128) return run<T, 128, kBackward, kShift>(g, plan.log_split, stream);
   }
-  return run<T, 64, kBackward, kShift>(g, plan.log_split, stream);
+  if constexpr (sizeof(T) == 2 && !kBackward && !kShift) return cudaErrorInvalidValue;
+  else return run<T, 64, kBackward, kShift>(g, plan.log_split, stream);
 }
 template <typename T, bool kBackward>
 cudaError_t run_plan(GatherParams& g, const GatherPlan& plan, cudaStream_t stream) {
@@ -658,7 +660,7 @@ cudaError_t launch_gather_forward(const DenseArgs& a, const GatherPlan& plan, cu
   if (hook != nullptr) {
     g.withhold = hook->at;
     g.timeout_ns = hook->timeout_ns;
-    return run<__nv_bfloat16, 64, false, false, true>(g, plan.log_split, stream);
+    return run<__nv_bfloat16, 16, false, false, true>(g, plan.log_split, stream);
   }
   return a.dt == VN_BF16 ? run_plan<__nv_bfloat16, false>(g, plan, stream)
                          : run_plan<float, false>(g, plan, stream);
