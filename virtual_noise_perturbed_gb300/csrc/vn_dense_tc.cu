@@ -11,7 +11,8 @@
 // by a pass of its own.
 //
 // fp32 operands come as three bf16 planes (8 + 8 + 8 significant bits); the k loop then runs over the
-// six products of planes that reach fp32's precision, the smallest first.
+// six products of planes that reach fp32's precision, the smallest first, and no accumulator takes more
+// of it than a short piece before it is added to sums in registers.
 //
 // Two kernels:
 //   pair   256 x 256 tiles, one per pair of CTAs (cta_group::2): each CTA stages 128 rows of
@@ -115,6 +116,20 @@ template <typename T>
 constexpr uint32_t kChunkBytes = 16 * 128 * sizeof(T);
 constexpr uint32_t kPairStageBytes = kABytes + 128 * 128;
 
+// fp32: the accumulator rounds each step's sum towards zero, which over n steps of one sign shrinks it by
+// about n 2^-25 (8e-6 of the result at k = 4096, 2e-4 at 65,536). So an accumulator takes one piece of the
+// k loop, kDrain stages of 4 steps; then the epilogue's warps add it to sums in their registers while the
+// MMAs go on in the other one. The five smaller products' sums are below 2^-6 of the result and take
+// longer pieces. An accumulator is read in about 3,000 cycles beside MMAs, 8 stages of 256 columns take
+// 4,150: 4096 cubed 482 us (without pieces 477, and off by 8e-6 of sums of one sign where it is now off by
+// 3.4e-7; pieces of 6 stages 497 us and 2.6e-7, of 4 513 us and 1.3e-7).
+constexpr int kDrain = 8, kLongDrain = 128;
+// Where the piece ends that begins with iteration `at`.
+__device__ __forceinline__ int piece_end(const Params& p, int at) {
+  const int leading = 5 * p.k_chunks;
+  return at < leading ? min(at + kLongDrain, leading) : min(at + kDrain, p.iters);
+}
+
 // Barriers: full[S] (leader's, armed for both CTAs' bytes), empty[S], tmem_full[2],
 // tmem_empty[2] (leader's, both CTAs' epilogues), drain, residual[2 halves][kBuffers].
 // kHook: the instance whose waits a test makes run out.
@@ -204,19 +219,26 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
     if (rank == 0 && elect_one()) {
       Ring rg, tb;
       bool ok = true, ready = false;
-      for (int64_t u = pair; ok && u < p.units; u += pairs, tb.next(2)) {
+      int at = 0;  // of a tile's iterations, where its next piece begins
+      for (int64_t u = pair; ok && u < p.units; tb.next(2)) {
         if (!(ok = mbar_wait(tmem_empty(tb.s), tb.ph ^ 1u, ctl))) break;
         fence_after();
-        for (int it = 0; it < p.iters; ++it) {
+        const int end = sizeof(T) == 4 ? piece_end(p, at) : p.iters;
+        for (int it = at; it < end; ++it) {
           if (!ready && !(ok = mbar_wait(full(rg.s), rg.ph, ctl))) break;
           fence_after();
           const int s = rg.s;
           rg.next(S);
           ready = mbar_done(full(rg.s), rg.ph);  // the next stage, while this one's MMAs are issued
-          issue_stage<kAMn, kBMn, true>(tmem + tb.s * 256, stage0 + s * kPairStageBytes, p.idesc, it == 0);
+          issue_stage<kAMn, kBMn, true>(tmem + tb.s * 256, stage0 + s * kPairStageBytes, p.idesc, it == at);
           mma_commit<true>(empty(s));
         }
         if (ok) mma_commit<true>(tmem_full(tb.s));
+        at = end;
+        if (end == p.iters) {
+          at = 0;
+          u += pairs;
+        }
       }
       mma_commit<true>(drain);
     }
@@ -236,7 +258,40 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
     constexpr int kChunk = 16 * 128;
     const bool has_r = p.residual != nullptr, has_z = p.preact != nullptr;
     Ring tb, ck;  // accumulators, chunks' buffers
-    for (int64_t u = pair; u < p.units; u += pairs, tb.next(2)) {
+    constexpr bool kPieces = sizeof(T) == 4;
+    float sum[kPieces ? 128 : 1];  // fp32: this lane's sums of the tile
+    // All pieces of a tile into `sum`; false after a wait that ran out.
+    auto add_pieces = [&](int cols) {
+#pragma unroll
+      for (int i = 0; i < (kPieces ? 128 : 1); ++i) sum[i] = 0.f;
+      for (int at = 0; at < p.iters; at = piece_end(p, at), tb.next(2)) {
+        const bool ok = mbar_wait(tmem_full(tb.s), tb.ph, ctl);
+        if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+        fence_after();
+        const uint32_t from = tmem + tb.s * 256 + c0 + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll
+        for (int c = 0; c < (kPieces ? 128 : 0); c += 16)
+          if (c < cols) {
+            uint32_t v[16];
+            tmem_load16(from + c, v);
+            tmem_wait_load(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
+          }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_rank(tmem_empty(tb.s), 0));
+      }
+      return true;
+    };
+    // The first 16 sums, which the others move up to replace.
+    auto next_sums = [&](float (&z)[16]) {
+#pragma unroll
+      for (int i = 0; i < (kPieces ? 16 : 0); ++i) z[i] = sum[i];
+#pragma unroll
+      for (int i = 0; i < (kPieces ? 112 : 0); ++i) sum[i] = sum[i + 16];
+    };
+    for (int64_t u = pair; u < p.units; u += pairs) {
       int tp, tq;
       tile_of(p, u, &tp, &tq);
       const int p0 = tp * 256 + static_cast<int>(rank) * 128;
@@ -258,10 +313,17 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
             if (cols > 0) fetch(ck.s, 0);
             if (cols > 16) fetch(second.s, 16);
           }
-          s_go[2 * h + tb.s] = mbar_wait(tmem_full(tb.s), tb.ph, ctl);
+          if (!kPieces) s_go[2 * h + tb.s] = mbar_wait(tmem_full(tb.s), tb.ph, ctl);
         }
-        named_barrier(1 + h, 128);
-        if (s_go[2 * h + tb.s] == 0) {  // the residual on its way has to land before the CTA ends
+        bool go;
+        if constexpr (kPieces) {
+          __syncwarp();
+          go = named_barrier_and(1 + h, 128, add_pieces(cols));
+        } else {
+          named_barrier(1 + h, 128);
+          go = s_go[2 * h + tb.s] != 0;
+        }
+        if (!go) {  // the residual on its way has to land before the CTA ends
           if (leader && has_r && cols > 0) settle(arrived(h, ck.s), ck.ph, p.timeout_ns);
           if (leader && has_r && cols > 16) settle(arrived(h, second.s), second.ph, p.timeout_ns);
           break;
@@ -269,22 +331,32 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
         fence_after();
         __syncwarp();
         uint32_t v[16];
-        if (cols > 0) tmem_load16(d, v);
+        if (!kPieces && cols > 0) tmem_load16(d, v);
 #pragma unroll 1
         for (int c = 0; c < cols; c += 16, ck.next(kBuffers)) {
           float z[16];
-          T pre[16];
-          __syncwarp();
-          tmem_wait_load(v);
+          T pre[kPieces ? 1 : 16];
+          if constexpr (kPieces) {
+            next_sums(z);
+          } else {
+            __syncwarp();
+            tmem_wait_load(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(v[i]);
+          }
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            z[i] = __uint_as_float(v[i]) + bias;
-            pre[i] = narrow<T>(z[i]);
+            z[i] += bias;
+            if constexpr (!kPieces) pre[i] = narrow<T>(z[i]);
           }
           __syncwarp();
-          if (c + 16 < cols) tmem_load16(d + c + 16, v);
-          activate_all<sizeof(T) == 2>(p.act, z);
+          if (!kPieces && c + 16 < cols) tmem_load16(d + c + 16, v);
           T* const y = buf + ck.s * kChunk + quarter * 32 + lane;
+          if (kPieces && has_z) {  // at once: the sums leave no registers to keep it in
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[kBuffers * kChunk + i * 128] = narrow<T>(z[i]);
+          }
+          activate_all<sizeof(T) == 2>(p.act, z);
           if (has_r) {
             // A wait that ran out ends no thread here, where the others would miss it at the
             // barrier: the products have ended with it, and the next tile's wait is the last.
@@ -294,9 +366,9 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i) y[i * 128] = narrow<T>(z[i]);
-          if (has_z) {
+          if (!kPieces && has_z) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[kBuffers * kChunk + i * 128] = pre[i];
+            for (int i = 0; i < 16; ++i) y[kBuffers * kChunk + i * 128] = pre[kPieces ? 0 : i];
           }
           fence_async_smem();
           // One barrier a chunk: it is written, and the next one's buffers have been read out (the
@@ -315,36 +387,55 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
           }
         }
       } else {
-        // The residual's loads run two chunks ahead, from three sets of registers: one that was moved to
-        // another would be waited for.
-        Residual<T> r0, r1, r2;
-        load_residual(p, q0, pp, cols, &r0);
-        load_residual(p, q0 + 16, pp, cols - 16, &r1);
-        const bool ok = mbar_wait(tmem_full(tb.s), tb.ph, ctl);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        fence_after();
-        auto chunk = [&](int c, const Residual<T>& r, Residual<T>* ahead) {
-          if (c >= cols) return;
-          uint32_t v[16];
-          tmem_load16(d + c, v);
-          load_residual(p, q0 + c + 32, pp, cols - c - 32, ahead);
-          tmem_wait_load(v);
-          float z[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(v[i]);
-          if (pp < p.np) finish<T>(p, z, r, q0 + c, pp, cols - c, bias);
-          __syncwarp();
-        };
+        if constexpr (kPieces) {
+          if (!add_pieces(cols)) break;
 #pragma unroll 1
-        for (int c = 0; c < cols; c += 48) {
-          chunk(c, r0, &r2);
-          chunk(c + 16, r1, &r0);
-          chunk(c + 32, r2, &r1);
+          for (int c = 0; c < cols; c += 16) {
+            float z[16];
+            next_sums(z);
+#pragma unroll
+            for (int g = 0; g < 16; g += 4) {  // few at a time, beside the sums
+              Residual<T, 4> r;
+              float some[4] = {z[g], z[g + 1], z[g + 2], z[g + 3]};
+              load_residual(p, q0 + c + g, pp, cols - c - g, &r);
+              if (pp < p.np) finish<T>(p, some, r, q0 + c + g, pp, cols - c - g, bias);
+            }
+          }
+        } else {
+          // The residual's loads run two chunks ahead, from three sets of registers: one that was moved to
+          // another would be waited for.
+          Residual<T> r0, r1, r2;
+          load_residual(p, q0, pp, cols, &r0);
+          load_residual(p, q0 + 16, pp, cols - 16, &r1);
+          const bool ok = mbar_wait(tmem_full(tb.s), tb.ph, ctl);
+          if (!__all_sync(0xFFFFFFFFu, ok)) break;
+          fence_after();
+          auto chunk = [&](int c, const Residual<T>& r, Residual<T>* ahead) {
+            if (c >= cols) return;
+            uint32_t v[16];
+            tmem_load16(d + c, v);
+            load_residual(p, q0 + c + 32, pp, cols - c - 32, ahead);
+            tmem_wait_load(v);
+            float z[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(v[i]);
+            if (pp < p.np) finish<T>(p, z, r, q0 + c, pp, cols - c, bias);
+            __syncwarp();
+          };
+#pragma unroll 1
+          for (int c = 0; c < cols; c += 48) {
+            chunk(c, r0, &r2);
+            chunk(c + 16, r1, &r0);
+            chunk(c + 32, r2, &r1);
+          }
         }
       }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_rank(tmem_empty(tb.s), 0));
+      if constexpr (!kPieces) {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_rank(tmem_empty(tb.s), 0));
+        tb.next(2);
+      }
     }
     if (kStaged && leader) bulk_wait_read<0>();
   }

@@ -163,6 +163,17 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// The same, and whether `value` held in all of the threads.
+__device__ __forceinline__ bool named_barrier_and(int id, int threads, bool value) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "barrier.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(value))
+      : "memory");
+  return all != 0;
+}
 template <bool kPair>
 __device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
   if constexpr (kPair) {
@@ -290,40 +301,40 @@ struct Epilogue {
   int bias_bf16, act;
 };
 
-// Sixteen outputs of one p, columns q .. q + 15 (the first `count` of them), in two steps: the
+// N outputs of one p, columns q .. q + N - 1 (the first `count` of them), in two steps: the
 // residual's loads, which the caller issues ahead of the sums, and the rest of the epilogue.
-template <typename T>
+template <typename T, int N = 16>
 struct Residual {
-  T v[16];
+  T v[N];
 };
-template <typename T>
-__device__ __forceinline__ void load_residual(const Epilogue& p, int64_t q, int64_t pp, int count, Residual<T>* r) {
+template <typename T, int N>
+__device__ __forceinline__ void load_residual(const Epilogue& p, int64_t q, int64_t pp, int count, Residual<T, N>* r) {
   if (p.residual == nullptr || pp >= p.np) return;
   const T* at = static_cast<const T*>(p.residual) + q * p.np + pp;
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < N; ++i)
     if (i < count) r->v[i] = at[i * p.np];
 }
-template <typename T>
-__device__ __forceinline__ void finish(const Epilogue& p, float (&z)[16], const Residual<T>& r, int64_t q, int64_t pp,
+template <typename T, int N>
+__device__ __forceinline__ void finish(const Epilogue& p, float (&z)[N], const Residual<T, N>& r, int64_t q, int64_t pp,
                                        int count, float bias) {
   const int64_t at = q * p.np + pp;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) z[i] += bias;
+  for (int i = 0; i < N; ++i) z[i] += bias;
   if (p.preact != nullptr) {
     T* pre = static_cast<T*>(p.preact) + at;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < N; ++i)
       if (i < count) pre[i * p.np] = narrow<T>(z[i]);
   }
   activate_all<sizeof(T) == 2>(p.act, z);
   if (p.residual != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] += value(r.v[i]);
+    for (int i = 0; i < N; ++i) z[i] += value(r.v[i]);
   }
   T* out = static_cast<T*>(p.out) + at;
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < N; ++i)
     if (i < count) out[i * p.np] = narrow<T>(z[i]);
 }
 __device__ __forceinline__ float bias_of(const Epilogue& p, int64_t pp) {
