@@ -56,3 +56,18 @@ def test_pairs_of_ctas(rows, k, n):
     p = plan(rows, k, n, "fp32", False)
     assert p[0] == 3 and p[4] == 1
     check_forward(rows, k, n)
+
+
+@pytest.mark.parametrize("rows,k,n", [(128, 16390, 130), (130, 16390, 1000), (147, 44719, 211), (64, 36970, 64), (270, 4957, 704)])
+def test_single_ctas(rows, k, n):
+    build()
+    p = plan(rows, k, n, "fp32", False)
+    assert p[0] == 3 and p[4] == 0
+    check_forward(rows, k, n)
+
+
+@pytest.mark.parametrize("rows,k,n", [(16384, 1024, 1024), (65536, 256, 256), (65536, 1024, 1021), (100000, 130, 130)])
+def test_gradients_over_many_rows_on_tiles(rows, k, n):
+    build()
+    assert plan(rows, k, n, "fp32", True)[0] == 3
+    check_backward(rows, k, n)

@@ -451,13 +451,14 @@ pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CU
 
 // ---------------------------------------------------------------- single CTAs, k split
 // The unit's k iterations are split over the cluster's CTAs. Barriers: full[S], empty[S],
-// tmem_full.
+// tmem_full[2], tmem_empty[2] (fp32's pieces, in two accumulators), drain.
 template <typename T, int BN, bool kAMn, bool kBMn, bool kHook = false>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 1)
 single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const Params p,
               const int split) {
   constexpr uint32_t kStageBytes = kABytes + BN * 128;
-  constexpr uint32_t kCols = BN < 32 ? 32 : BN;
+  constexpr bool kPieces = sizeof(T) == 4;
+  constexpr uint32_t kCols = kPieces ? 2 * BN : BN < 32 ? 32 : BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int S = p.stages;
@@ -465,9 +466,11 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
   const uint32_t bar0 = smem_u32(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (S + s); };
-  const uint32_t tmem_full = bar0 + 8u * (2 * S);
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * S + 1);
-  volatile Control* ctl = reinterpret_cast<volatile Control*>(bars + 2 * S + 2);
+  auto tmem_full = [&](int b) { return bar0 + 8u * (2 * S + b); };
+  auto tmem_empty = [&](int b) { return bar0 + 8u * (2 * S + 2 + b); };
+  const uint32_t drain = bar0 + 8u * (2 * S + 4);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
+  volatile Control* ctl = reinterpret_cast<volatile Control*>(bars + 2 * S + 6);
   const uint32_t stage0 = smem_u32(smem);
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -481,7 +484,11 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    mbar_init(tmem_full, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tmem_full(b), 1);
+      mbar_init(tmem_empty(b), 4);
+    }
+    mbar_init(drain, 1);
     ctl->abort = 0;
     ctl->timeout_ns = p.timeout_ns;
     ctl->status = p.status;
@@ -519,15 +526,24 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
     }
   } else if (warp == 1) {
     if (elect_one()) {
-      Ring rg;
-      for (int it = first; it < last; ++it, rg.next(S)) {
-        if (!(ok = mbar_wait(full(rg.s), rg.ph, ctl))) break;
-        fence_after();
-        issue_stage<kAMn, kBMn, false>(tmem, stage0 + rg.s * kStageBytes, p.idesc, it == first);
-        mma_commit<false>(empty(rg.s));
+      Ring rg, tb;
+      for (int at = first; ok && at < last; tb.next(2)) {
+        if (kPieces) {
+          if (!(ok = mbar_wait(tmem_empty(tb.s), tb.ph ^ 1u, ctl))) break;
+          fence_after();
+        }
+        const int end = kPieces ? min(piece_end(p, at), last) : last;
+        for (int it = at; it < end; ++it, rg.next(S)) {
+          if (!(ok = mbar_wait(full(rg.s), rg.ph, ctl))) break;
+          fence_after();
+          issue_stage<kAMn, kBMn, false>(tmem + tb.s * BN, stage0 + rg.s * kStageBytes, p.idesc, it == at);
+          mma_commit<false>(empty(rg.s));
+        }
+        if (ok) mma_commit<false>(tmem_full(tb.s));
+        at = end;
       }
-      mma_commit<false>(tmem_full);  // also after an abort: what was issued completes
-      settle(tmem_full, 0, p.timeout_ns);
+      mma_commit<false>(drain);  // also after an abort: what was issued completes
+      settle(drain, 0, p.timeout_ns);
     }
   } else {
     const int quarter = warp & 3;
@@ -537,33 +553,85 @@ single_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ 
     const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const int cols = static_cast<int>(min(static_cast<int64_t>(BN), p.nq - q0));
     const float bias = bias_of(p, pp);
-    Residual<T> r;
-    if (split == 1) load_residual(p, q0, pp, cols, &r);
-    ok = mbar_wait(tmem_full, 0, ctl);
-    ok = __all_sync(0xFFFFFFFFu, ok) && !ctl->abort;
-    if (ok) {
-      fence_after();
-#pragma unroll 1
-      for (int c = 0; c < cols; c += 16) {
-        uint32_t v[16];
-        tmem_load16(d + c, v);
-        tmem_wait_load(v);
+    if constexpr (kPieces) {
+      // fp32: pieces as in the pairs' kernel.
+      float sum[BN];
+#pragma unroll
+      for (int i = 0; i < BN; ++i) sum[i] = 0.f;
+      Ring tb;
+      for (int at = first; ok && at < last; at = piece_end(p, at), tb.next(2)) {
+        ok = mbar_wait(tmem_full(tb.s), tb.ph, ctl);
+        if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+        fence_after();
+#pragma unroll
+        for (int c = 0; c < BN; c += 16)
+          if (c < cols) {
+            uint32_t v[16];
+            tmem_load16(d + tb.s * BN + c, v);
+            tmem_wait_load(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
+          }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tmem_empty(tb.s));
+      }
+      if (ok) {
+        // Every copy has landed and every MMA has read it: the stages hold the sums now, and the registers
+        // are free for the epilogue.
+        float* part = reinterpret_cast<float*>(smem) + row;
+        Residual<T> r;
+        if (split == 1) load_residual(p, q0, pp, cols, &r);
+#pragma unroll
+        for (int c = 0; c < BN; c += 16)
+          if (c < cols) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) part[(c + i) * 128] = sum[c + i];
+          }
         if (split == 1) {
-          float z[16];
+#pragma unroll 1
+          for (int c = 0; c < cols; c += 16) {
+            float z[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(v[i]);
-          Residual<T> ahead;
-          load_residual(p, q0 + c + 16, pp, cols - c - 16, &ahead);
-          if (pp < p.np) finish<T>(p, z, r, q0 + c, pp, cols - c, bias);
-          r = ahead;
-        } else {
-          // Every copy has landed and every MMA has read it: the stages hold the partial sums now.
-          float* part = reinterpret_cast<float*>(smem) + row;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) part[(c + i) * 128] = __uint_as_float(v[i]);
+            for (int i = 0; i < 16; ++i) z[i] = part[(c + i) * 128];
+            Residual<T> ahead;
+            load_residual(p, q0 + c + 16, pp, cols - c - 16, &ahead);
+            if (pp < p.np) finish<T>(p, z, r, q0 + c, pp, cols - c, bias);
+            r = ahead;
+          }
         }
       }
-      fence_before();
+    } else {
+      Residual<T> r;
+      if (split == 1) load_residual(p, q0, pp, cols, &r);
+      if (first < last) ok = mbar_wait(tmem_full(0), 0, ctl);
+      ok = __all_sync(0xFFFFFFFFu, ok) && !ctl->abort;
+      if (ok) {
+        fence_after();
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 16) {
+          uint32_t v[16] = {};  // of a CTA without a share of k
+          if (first < last) {
+            tmem_load16(d + c, v);
+            tmem_wait_load(v);
+          }
+          if (split == 1) {
+            float z[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[i] = __uint_as_float(v[i]);
+            Residual<T> ahead;
+            load_residual(p, q0 + c + 16, pp, cols - c - 16, &ahead);
+            if (pp < p.np) finish<T>(p, z, r, q0 + c, pp, cols - c, bias);
+            r = ahead;
+          } else {
+            // Every copy has landed and every MMA has read it: the stages hold the partial sums now.
+            float* part = reinterpret_cast<float*>(smem) + row;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) part[(c + i) * 128] = __uint_as_float(v[i]);
+          }
+        }
+        fence_before();
+      }
     }
   }
   if (split > 1) {
