@@ -325,7 +325,8 @@ vn_status vn_es_update(float* theta, const float* grad, int64_t n, double lr, vo
  * the call's work on `stream` is done (NULL when that is 0). With dt VN_F32 and more than
  * 8 rows the matrices are split into three bf16 terms each (exact: 8 + 8 + 8 significant
  * bits; in the workspace for larger sizes) and multiplied on the tensor cores by the six
- * products of the terms that reach fp32's precision; there an infinity gives NaN where the
+ * products of the terms that reach fp32's precision, summed in pieces of k so that what the tensor cores'
+ * rounding towards zero takes from sums of one sign (under 6e-7 of them) does not grow with k; there an infinity gives NaN where the
  * exact sum would be infinite. Errors: VN_ERR_WORKSPACE, and those of vn_perturbed_linear.
  * The tensor-core kernels bound their waits: results are valid only after vn_device_status
  * returned VN_OK. This call's kernels, and those of the other calls of this part, may start

@@ -8,12 +8,15 @@ from virtual_noise_perturbed_gb300 import _lib
 # (type, gradients?) -> (rows, in, out), aligned, each for a kernel that none of the others takes.
 SIZES = {
     ("fp32", False): [
+        (32, 18264, 32), (32, 17474, 31), (280, 16480, 32), (408, 18281, 35), (2344, 4440, 32), (1113, 8382, 30),
+        (10, 9, 63281),
         (64, 64, 64), (64, 79, 65), (64, 36970, 64), (68, 75, 11004), (72, 64, 31168), (91, 64, 33027),
         (147, 44719, 211), (168, 66, 11074), (192, 64, 11162), (270, 4957, 704), (300, 257, 130), (344, 69, 10347),
         (520, 130, 2056), (1000, 72, 4104), (2880, 64, 64), (12566, 64, 64), (18816, 64, 192), (19015, 87, 142),
         (29568, 69, 78),
     ],
     ("fp32", True): [
+        (37312, 40, 32), (5232, 32, 1032), (2464, 56, 4649),
         (1, 23090, 1), (64, 64, 64), (64, 65, 22454), (64, 79, 65), (64, 100, 19776), (64, 131, 3368),
         (64, 600, 6010), (64, 47299, 70), (70, 1231, 421), (72, 4095, 512), (72, 4095, 1031), (72, 7040, 64),
         (76, 416, 2734), (152, 64, 9173), (960, 2120, 65), (2056, 130, 640), (2240, 576, 74), (3136, 361, 64),
@@ -55,8 +58,11 @@ def kernels(rows, n_in, n_out, kind, backward, aligned=True, act=0):
     if p[0] == 1:
         return {(kind, "plain")}
     if p[0] == 2:
+        # fp32 sums over a long share of k are taken in pieces.
+        shares = [-(-n // 64 >> l) for n, l in ((n_out if backward else n_in, p[2]), (rows if backward else 0, p[3]))]
+        long = kind == "fp32" and max(shares) > (16 if p[1] == 128 else 32)
         packs = aligned and n_in % per == 0 and (not backward or n_out % per == 0)
-        return {(kind, "gather", "gradients" if backward else "forward", p[1], "packs" if packs else "any")}
+        return {(kind, "gather", "gradients" if backward else "forward", p[1], "packs" if packs else "any", "pieces" if long else "whole")}
     found = set()
     products = [("dx", p[4:7], n_in, rows), ("dw", p[7:10], n_in, n_out)] if backward else [("y", p[4:7], n_out, rows)]
     for name, (pair, columns, split), np, nq in products:

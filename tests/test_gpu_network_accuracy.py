@@ -71,3 +71,19 @@ def test_gradients_over_many_rows_on_tiles(rows, k, n):
     build()
     assert plan(rows, k, n, "fp32", True)[0] == 3
     check_backward(rows, k, n)
+
+
+@pytest.mark.parametrize("rows,k,n,columns", [(2048, 16384, 1024, 128), (640, 16390, 130, 128), (130, 16390, 600, 64),
+                                              (9, 65536, 520, 16), (1021, 4099, 256, 64)])
+def test_gathered(rows, k, n, columns):
+    build()
+    assert plan(rows, k, n, "fp32", False)[:2] == [2, columns]
+    check_forward(rows, k, n)
+
+
+@pytest.mark.parametrize("rows,k,n,columns", [(262144, 64, 64, 64), (1000003, 16, 8, 64), (20000, 300, 100, 128),
+                                              (40000, 200, 128, 64), (1021, 256, 256, 64)])
+def test_gradients_over_many_rows_gathered(rows, k, n, columns):
+    build()
+    assert plan(rows, k, n, "fp32", True)[:2] == [2, columns]
+    check_backward(rows, k, n)

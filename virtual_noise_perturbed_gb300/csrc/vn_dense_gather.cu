@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "vn_act.cuh"
@@ -271,19 +272,62 @@ constexpr int kStages = static_cast<int>((sizeof(T) == 4 ? 221184 : 106496) / kS
 // cycles, three times what one with 64 columns takes), and each rounds its sum towards zero: n steps
 // shrink it by about n 2^-25. So the leading products of a chunk's four steps of k rotate over
 // kLead accumulators and the five smaller products of fp32 over kRest; the epilogue adds them up.
+// In fp32 sums over more than kShort chunks are taken in pieces (kPieces), whose sums a further accumulator
+// holds, rounded to nearest: the leading accumulators are added to it after 32 steps each, the others, below
+// 2^-6 of the result, after at most 427, so that what is lost does not grow with k (sums of one sign over
+// 262,144 rows: 4e-7 of the result, where one piece lost 9e-6). The MMAs stand still meanwhile: 2.3 us for
+// each 8 chunks of 128 columns, 0.3 for each 32 of 64. Shorter sums have kernels without it, whose code is
+// what small calls wait for (gradients of 1021 x 256 to 256 13.8 us, 14.3 with it).
 template <typename T, int BN>
-constexpr int kLead = sizeof(T) == 2 ? 2 : BN == 128 ? 2 : 4;
+constexpr int kShort = sizeof(T) == 2 ? INT_MAX : BN == 128 ? 16 : 32;
+template <typename T, int BN, bool kPieces>
+constexpr int kLead = sizeof(T) == 2 ? 2 : BN == 128 ? (kPieces ? 1 : 2) : 4;
 template <typename T, int BN>
 constexpr int kRest = sizeof(T) == 2 ? 0 : BN == 128 ? 2 : 3;
-template <typename T, int BN>
-constexpr uint32_t kTmemCols = (kLead<T, BN> + kRest<T, BN>) * BN <= 32    ? 32
-                               : (kLead<T, BN> + kRest<T, BN>) * BN <= 128 ? 128
-                               : (kLead<T, BN> + kRest<T, BN>) * BN <= 256 ? 256
-                                                                           : 512;
+template <typename T, int BN, bool kPieces>
+constexpr int kAccumulators = kLead<T, BN, kPieces> + kRest<T, BN>;
+template <typename T, int BN, bool kPieces>
+constexpr uint32_t kTmemNeed = (kAccumulators<T, BN, kPieces> + kPieces) * BN;
+template <typename T, int BN, bool kPieces>
+constexpr uint32_t kTmemCols = kTmemNeed<T, BN, kPieces> <= 32    ? 32
+                               : kTmemNeed<T, BN, kPieces> <= 128 ? 128
+                               : kTmemNeed<T, BN, kPieces> <= 256 ? 256
+                                                                  : 512;
+template <int BN>
+constexpr int kPiece = BN == 128 ? 8 : 32;  // chunks
+template <int BN>
+constexpr int kLongPiece = BN == 128 ? 32 : 64;  // of the smaller products
+
+// The sums of 16 columns from `at` on in the first `count` accumulators, and in column `total` on, if any.
+template <int BN>
+__device__ __forceinline__ void sums_of(uint32_t at, int count, int total, float (&z)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+#pragma unroll 1
+  for (int acc = count - (total > 0 ? 0 : 1); acc >= 0; --acc) {  // the smaller products' first
+    uint32_t v[16];
+    __syncwarp();
+    tmem_load16(at + (acc == count ? total : acc * BN), v);
+    tmem_wait_load(v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] += __uint_as_float(v[i]);
+  }
+}
+// A piece's end: this warp's columns of the first `count` accumulators into those from `total` on.
+template <int BN>
+__device__ __forceinline__ void end_piece(uint32_t at, int count, int total, bool more) {
+#pragma unroll 1
+  for (int c = static_cast<int>(threadIdx.x >> 7) * 16; c < BN; c += 32) {
+    float z[16];
+    sums_of<BN>(at + c, count, more ? total : 0, z);
+    tmem_store16(at + total + c, z);
+  }
+  tmem_wait_store();
+}
 
 // One product's tile. kSum: also the sums of B over k (the bias's gradient), by the tiles of p's
 // first 128. Called by every thread of the CTA.
-template <typename T, int BN, bool kShift, bool kAMn, bool kBMn, bool kSum, bool kHook>
+template <typename T, int BN, bool kShift, bool kAMn, bool kBMn, bool kSum, bool kPieces, bool kHook>
 __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8_t* smem, uint64_t* bars, uint32_t tmem,
                                      volatile Control* ctl, int block, int cta) {
   constexpr int S = kStages<T, BN>;
@@ -305,6 +349,9 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
   const int last = idle ? first : first + share + (rank < more ? 1 : 0);
   const bool sums = kSum && d.sum != nullptr && tp == 0 && !idle;
   float sum[8] = {};
+  // Warp w has p from 32 (w % 4) on, and of 32 columns the first or the last 16.
+  const uint32_t tmem_row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  constexpr int kAccs = kAccumulators<T, BN, kPieces>, kTotal = kAccs * BN;
 
   if (warp < 8) {
     const int t = threadIdx.x;
@@ -318,53 +365,69 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
     bool ok = true;
     // Iteration `it` stores chunk it - 1, which the one before loaded, and loads chunk it: one
     // copy of the code for either, since fetching instructions is what small calls wait for.
+    // fp32: the iterations after which a piece's MMAs are waited for and added up, ahead of the next chunk.
+    int it = first, halt = kPieces ? min(last, first + kPiece<BN>) : last;
 #pragma unroll 1
-    for (int it = first; it <= last; ++it) {
-      const bool have = it > first;
-      if (have) {
-        if (lane == 0) ok = mbar_wait(empty(rg.s), rg.ph ^ 1u, ctl);
-        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-        if (!ok) break;
-        const uint32_t stage = stage0 + rg.s * kStage;
+    for (;;) {
+#pragma unroll 1
+      for (; it <= halt; ++it) {
+        const bool have = it > first;
+        if (have) {
+          if (lane == 0) ok = mbar_wait(empty(rg.s), rg.ph ^ 1u, ctl);
+          ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+          if (!ok) break;
+          const uint32_t stage = stage0 + rg.s * kStage;
 #pragma unroll
-        for (int i = 0; i < ga.kCount; ++i) {
-          store_group<T>(stage + ga.offset(i, t), kABytes, ga.v[i]);
-        }
-        if (gb.kAll || t < BN * 8) {
+          for (int i = 0; i < ga.kCount; ++i) {
+            store_group<T>(stage + ga.offset(i, t), kABytes, ga.v[i]);
+          }
+          if (gb.kAll || t < BN * 8) {
 #pragma unroll
-          for (int i = 0; i < gb.kCount; ++i) {
-            const uint32_t at = stage + kPlanes<T> * kABytes + gb.offset(i, t);
-            if (!kSum && !sloped) {
-              store_group<T>(at, kBBytes<BN>, gb.v[i]);
-              continue;
-            }
-            float v[8];
-            gb.v[i].get(v);
-            if (sloped) {
-              float z[8];
-              gz.v[i].get(z);
-              slope_all<true>(d.slope, z, v);
-            }
-            if (kSum) {
+            for (int i = 0; i < gb.kCount; ++i) {
+              const uint32_t at = stage + kPlanes<T> * kABytes + gb.offset(i, t);
+              if (!kSum && !sloped) {
+                store_group<T>(at, kBBytes<BN>, gb.v[i]);
+                continue;
+              }
+              float v[8];
+              gb.v[i].get(v);
+              if (sloped) {
+                float z[8];
+                gz.v[i].get(z);
+                slope_all<true>(d.slope, z, v);
+              }
+              if (kSum) {
 #pragma unroll
-              for (int q = 0; q < 8; ++q) sum[q] += v[q];
+                for (int q = 0; q < 8; ++q) sum[q] += v[q];
+              }
+              store_planes<T>(at, kBBytes<BN>, v);
             }
-            store_planes<T>(at, kBBytes<BN>, v);
           }
         }
+        if (it < last) {
+          const int64_t k = static_cast<int64_t>(it) * kK;
+          ga.load(ap, d.a, p0, k, t);
+          gb.load(bp, d.b, q0, k, t);
+          if (sloped) gz.load(zp, d.b, q0, k, t);
+        }
+        if (have) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0 && !(kHook && block == 0 && warp == 0 && it - 1 - first == g.withhold)) mbar_arrive(full(rg.s));
+          rg.next(S);
+        }
       }
-      if (it < last) {
-        const int64_t k = static_cast<int64_t>(it) * kK;
-        ga.load(ap, d.a, p0, k, t);
-        gb.load(bp, d.b, q0, k, t);
-        if (sloped) gz.load(zp, d.b, q0, k, t);
-      }
-      if (have) {
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0 && !(kHook && block == 0 && warp == 0 && it - 1 - first == g.withhold)) mbar_arrive(full(rg.s));
-        rg.next(S);
-      }
+      if (!kPieces || !ok || halt == last) break;
+      // The chunk stored last was a piece's last: its MMAs have to be complete.
+      const bool wrapped = rg.s == 0;
+      ok = mbar_wait(empty(wrapped ? S - 1 : rg.s - 1), wrapped ? rg.ph ^ 1u : rg.ph, ctl);
+      if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+      fence_after();
+      const int count = (halt - first) % kLongPiece<BN> == 0 ? kAccs : kLead<T, BN, kPieces>;
+      end_piece<BN>(tmem_row, count, kTotal, halt - first > kPiece<BN>);
+      fence_before();
+      __syncwarp();
+      halt = min(last, halt + kPiece<BN>);
     }
   } else if (elect_one()) {
     const uint32_t idesc = idesc_of(128, BN, kAMn, kBMn);
@@ -374,16 +437,18 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
       fence_after();
       const uint32_t a0 = stage0 + rg.s * kStage, b0 = a0 + kPlanes<T> * kABytes;
       const uint64_t a = descriptor<kAMn>(a0), b = descriptor<kBMn>(b0);
-      const bool fresh = it == first;
+      const bool fresh = kPieces ? (it - first) % kPiece<BN> == 0 : it == first;
+      const bool fresh_rest = kPieces ? (it - first) % kLongPiece<BN> == 0 : it == first;
 #pragma unroll
       for (int ks = 0; ks < kK / 16; ++ks) {
 #pragma unroll
         for (int pr = sizeof(T) == 4 ? 0 : 5; pr < 6; ++pr) {
           const int step = pr == 5 ? ks : ks * 5 + pr;  // among its accumulators' steps of this chunk
-          const int ring = pr == 5 ? kLead<T, BN> : (kRest<T, BN> > 0 ? kRest<T, BN> : 1);
-          const int acc = (pr == 5 ? 0 : kLead<T, BN>) + step % ring;
+          const int ring = pr == 5 ? kLead<T, BN, kPieces> : (kRest<T, BN> > 0 ? kRest<T, BN> : 1);
+          const int acc = (pr == 5 ? 0 : kLead<T, BN, kPieces>) + step % ring;
           mma<false>(tmem + acc * BN, further(a, plane_a(pr) * kABytes + ks * kStepBytes<kAMn>),
-                     further(b, plane_b(pr) * kBBytes<BN> + ks * kStepBytes<kBMn>), idesc, !fresh || step >= ring);
+                     further(b, plane_b(pr) * kBBytes<BN> + ks * kStepBytes<kBMn>), idesc,
+                     !(pr == 5 ? fresh : fresh_rest) || step >= ring);
         }
       }
       mma_commit<false>(empty(rg.s));
@@ -414,24 +479,10 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
     bias = d.bias_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(d.bias)[pp])
                        : static_cast<const float*>(d.bias)[pp];
   if (warp < 8 && !stop) {
-    const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    constexpr int kAccs = kLead<T, BN> + kRest<T, BN>;
 #pragma unroll 1
     for (int c = (warp >> 2) * 16; c < cols; c += 32) {
-      float z[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) z[i] = 0.f;
-      if (first < last) {
-#pragma unroll 1
-        for (int acc = kAccs - 1; acc >= 0; --acc) {  // the smaller products' first
-          uint32_t v[16];
-          __syncwarp();
-          tmem_load16(at + acc * BN + c, v);
-          tmem_wait_load(v);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) z[i] += __uint_as_float(v[i]);
-        }
-      }
+      float z[16] = {};
+      if (first < last) sums_of<BN>(tmem_row + c, kAccs, kPieces && last - first > kPiece<BN> ? kTotal : 0, z);
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
         *reinterpret_cast<float4*>(part + row * kPitch + c + i) = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
@@ -518,11 +569,11 @@ __device__ __forceinline__ void tile(const Part& d, const GatherParams& g, uint8
 // otherwise part 0 is the forward product.
 // In bf16 the registers of two CTAs fit an SM, as their stages do.
 // kHook: the instance whose waits a test makes run out.
-template <typename T, int BN, bool kBackward, bool kShift, bool kHook = false>
+template <typename T, int BN, bool kBackward, bool kShift, bool kPieces = false, bool kHook = false>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
 gather_kernel(const __grid_constant__ GatherParams g) {
   constexpr int S = kStages<T, BN>;
-  constexpr uint32_t kCols = kTmemCols<T, BN>;
+  constexpr uint32_t kCols = kTmemCols<T, BN, kPieces>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * kStageBytes<T, BN>);
@@ -560,11 +611,11 @@ gather_kernel(const __grid_constant__ GatherParams g) {
   if constexpr (kBackward) {
     // The weight's gradient first: its k loop, over the rows, tends to be the longer one.
     if (block < g.part[1].blocks)
-      tile<T, BN, kShift, true, true, true, kHook>(g.part[1], g, smem, bars, tmem, ctl, block, cta);
+      tile<T, BN, kShift, true, true, true, kPieces, kHook>(g.part[1], g, smem, bars, tmem, ctl, block, cta);
     else
-      tile<T, BN, kShift, true, false, false, kHook>(g.part[0], g, smem, bars, tmem, ctl, block - g.part[1].blocks, cta);
+      tile<T, BN, kShift, true, false, false, kPieces, kHook>(g.part[0], g, smem, bars, tmem, ctl, block - g.part[1].blocks, cta);
   } else {
-    tile<T, BN, kShift, false, false, false, kHook>(g.part[0], g, smem, bars, tmem, ctl, block, cta);
+    tile<T, BN, kShift, false, false, false, kPieces, kHook>(g.part[0], g, smem, bars, tmem, ctl, block, cta);
   }
   __syncwarp();
   fence_before();
@@ -579,7 +630,7 @@ gather_kernel(const __grid_constant__ GatherParams g) {
 template <typename T, int BN, bool kBackward>
 constexpr size_t kSmemBytes = 1024 + kStages<T, BN> * kStageBytes<T, BN> + 8 * (2 * kStages<T, BN> + 2) + sizeof(Control);
 
-template <typename T, int BN, bool kBackward, bool kShift, bool kHook = false>
+template <typename T, int BN, bool kBackward, bool kShift, bool kPieces = false, bool kHook = false>
 cudaError_t run(GatherParams& g, const int (&log_split)[2], cudaStream_t stream) {
   int64_t blocks = 0;
   g.cluster = 1 << std::max(log_split[0], log_split[1]);
@@ -608,28 +659,38 @@ cudaError_t run(GatherParams& g, const int (&log_split)[2], cudaStream_t stream)
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     if (wide[dev].load(std::memory_order_acquire) == 0) {
-      err = cudaFuncSetAttribute(reinterpret_cast<const void*>(gather_kernel<T, BN, kBackward, kShift, kHook>),
+      err = cudaFuncSetAttribute(reinterpret_cast<const void*>(gather_kernel<T, BN, kBackward, kShift, kPieces, kHook>),
                                  cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (err != cudaSuccess) return err;
       wide[dev].store(1, std::memory_order_release);
     }
   }
-  return launch_cluster(gather_kernel<T, BN, kBackward, kShift, kHook>, record, static_cast<int>(blocks), kThreads, g.cluster,
+  return launch_cluster(gather_kernel<T, BN, kBackward, kShift, kPieces, kHook>, record, static_cast<int>(blocks), kThreads, g.cluster,
                         kSmemBytes<T, BN, kBackward>, stream, g);
 }
 
+// fp32: with pieces where a CTA's share of k is long.
+template <typename T, int BN, bool kBackward, bool kShift>
+cudaError_t run_columns(GatherParams& g, const GatherPlan& plan, cudaStream_t stream) {
+  if constexpr (sizeof(T) == 4) {
+    for (int i = 0; i < 2; ++i)
+      if (((g.part[i].chunks - 1) >> plan.log_split[i]) + 1 > kShort<T, BN>)
+        return run<T, BN, kBackward, kShift, true>(g, plan.log_split, stream);
+  }
+  return run<T, BN, kBackward, kShift>(g, plan.log_split, stream);
+}
 template <typename T, bool kBackward, bool kShift>
 cudaError_t run_tile(GatherParams& g, const GatherPlan& plan, cudaStream_t stream) {
   if constexpr (!kBackward) {
-    if (plan.bn == 16) return run<T, 16, kBackward, kShift>(g, plan.log_split, stream);
+    if (plan.bn == 16) return run_columns<T, 16, kBackward, kShift>(g, plan, stream);
   }
   // In bf16: gradients of 128 columns would hold 108 registers of shifted groups; no forward product is
   // planned on 128 columns, nor on 64 where its rows start on 16 bytes.
   if constexpr (sizeof(T) == 4 || (kBackward && !kShift)) {
-    if (plan.bn == 128) return run<T, 128, kBackward, kShift>(g, plan.log_split, stream);
+    if (plan.bn == 128) return run_columns<T, 128, kBackward, kShift>(g, plan, stream);
   }
   if constexpr (sizeof(T) == 2 && !kBackward && !kShift) return cudaErrorInvalidValue;
-  else return run<T, 64, kBackward, kShift>(g, plan.log_split, stream);
+  else return run_columns<T, 64, kBackward, kShift>(g, plan, stream);
 }
 template <typename T, bool kBackward>
 cudaError_t run_plan(GatherParams& g, const GatherPlan& plan, cudaStream_t stream) {
@@ -660,7 +721,7 @@ cudaError_t launch_gather_forward(const DenseArgs& a, const GatherPlan& plan, cu
   if (hook != nullptr) {
     g.withhold = hook->at;
     g.timeout_ns = hook->timeout_ns;
-    return run<__nv_bfloat16, 16, false, false, true>(g, plan.log_split, stream);
+    return run<__nv_bfloat16, 16, false, false, false, true>(g, plan.log_split, stream);
   }
   return a.dt == VN_BF16 ? run_plan<__nv_bfloat16, false>(g, plan, stream)
                          : run_plan<float, false>(g, plan, stream);
