@@ -46,3 +46,13 @@ def test_the_widths_of_the_gpu_tests_are_all_widths():
     assert [p[0] for p in plans] == [3] * len(WIDTHS) and [p[7] for p in plans] == [1] * len(WIDTHS)
     assert [p[8] for p in plans] == list(range(32, 257, 16))
     assert {plan(*s, "fp32", True)[8] for s in WIDTHS} >= set(range(64, 257, 16))
+
+
+def test_every_cta_of_a_split_tile_has_a_share_of_k():
+    rng = random.Random(7)
+    for _ in range(20000):
+        rows, n_in, n_out = (max(1, int(2 ** rng.uniform(0, 16))) for _ in range(3))
+        kind, backward = rng.choice(("fp32", "bf16")), rng.random() < 0.5
+        p = plan(rows, n_in, n_out, kind, backward)
+        for (pair, _, split), nk in zip((p[4:7], p[7:10]), (n_out, rows) if backward else (n_in,)):
+            assert pair or 1 << split <= -(-nk // 64) * (6 if kind == "fp32" else 1)

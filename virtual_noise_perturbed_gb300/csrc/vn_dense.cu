@@ -353,7 +353,7 @@ TilePlan tile_plan(int64_t np, int64_t nq, int64_t nk, vn_dtype dt, bool b_mn) {
   for (int bn : {16, 64, 128}) {
     if (b_mn && bn == 16) continue;
     const double stage = bn == 128 ? 0.29 : bn == 64 ? 0.25 : 0.22;
-    for (int l = 0; l < 4; ++l) {
+    for (int l = 0; l < 4 && (1 << l) <= iters; ++l) {  // each CTA has a share of k
       const double ctas = tiles_of(np, 128) * tiles_of(nq, bn) * (1 << l);
       const double rounds = std::ceil(ctas / resident(l, 2));
       const double us = (bn == 128 ? 5.3 : bn == 64 ? 2.6 : 1.9) + (l > 0 ? 0.4 + 1.4 * l : 0.0) +
