@@ -325,9 +325,11 @@ vn_status vn_es_update(float* theta, const float* grad, int64_t n, double lr, vo
  * the call's work on `stream` is done (NULL when that is 0). With dt VN_F32 and more than
  * 8 rows the matrices are split into three bf16 terms each (exact: 8 + 8 + 8 significant
  * bits; in the workspace for larger sizes) and multiplied on the tensor cores by the six
- * products of the terms that reach fp32's precision, summed in pieces of k so that what the tensor cores'
- * rounding towards zero takes from sums of one sign (under 6e-7 of them) does not grow with k; there an infinity gives NaN where the
- * exact sum would be infinite. Errors: VN_ERR_WORKSPACE, and those of vn_perturbed_linear.
+ * products of the terms that reach fp32's precision. They are summed in pieces of k, so that
+ * what the tensor cores' rounding towards zero takes from sums of one sign (under 6e-7 of
+ * them) does not grow with k. An infinity gives NaN there, where the exact sum would be
+ * infinite. Errors: VN_ERR_WORKSPACE, and those of vn_perturbed_linear; more than
+ * 2^31 - 512 features (in or out) of more than 8 rows are VN_ERR_OVERFLOW.
  * The tensor-core kernels bound their waits: results are valid only after vn_device_status
  * returned VN_OK. This call's kernels, and those of the other calls of this part, may start
  * while the kernel before them on `stream` ends; they touch memory after it.
@@ -350,7 +352,8 @@ int64_t vn_linear_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, 
  * grad_b [out] of gb_dt or NULL. For bf16 matrices with an activation d is rounded once to
  * bf16 before the two products (as the tensor cores take it); grad_b sums the unrounded d.
  * Sums are held in fp32 in a fixed order. rows == 0 gives zero grad_w and grad_b. Workspace, errors and
- * status as for vn_linear.
+ * status as for vn_linear; more than 2^31 - 512 features, or rows with grad_w or grad_b, are VN_ERR_OVERFLOW
+ * (sums over more rows are the caller's to make from slices).
  */
 vn_status vn_linear_backward(const void* grad, const void* x, const void* w, const void* preact,
                              vn_dtype dt, int64_t rows, int64_t in, int64_t out, vn_act act,
@@ -492,7 +495,7 @@ vn_status vn_testhook_linear_withhold(int kernel, const void* x, const void* w, 
 
 /* Which kernels vn_linear (or, with `backward`, vn_linear_backward) takes for these sizes, for tests that
  * mean to reach each of them; launches nothing and needs no device. aligned: as for the workspaces.
- * plan[10]: the route (0 few rows, 1 beyond 32-bit sizes, 2 gathered, 3 tiles); the gathered
+ * plan[10]: the route (0 few rows, 2 gathered, 3 tiles); the gathered
  * kernel's columns and log2 of its splits (of the forward product or grad_x's, of grad_w's); and for tiles
  * of the forward product (or grad_x's), then of grad_w's: 1 for pairs, columns, log2 of the split. */
 vn_status vn_testhook_linear_plan(int64_t rows, int64_t in, int64_t out, vn_dtype dt, vn_act act,

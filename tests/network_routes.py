@@ -55,8 +55,6 @@ def kernels(rows, n_in, n_out, kind, backward, aligned=True, act=0):
     per = 8 if kind == "bf16" else 4
     if p[0] == 0:
         return {(kind, "rows", aligned and n_in % per == 0)}
-    if p[0] == 1:
-        return {(kind, "plain")}
     if p[0] == 2:
         # fp32 sums over a long share of k are taken in pieces.
         shares = [-(-n // 64 >> l) for n, l in ((n_out if backward else n_in, p[2]), (rows if backward else 0, p[3]))]

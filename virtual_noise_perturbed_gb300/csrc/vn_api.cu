@@ -161,6 +161,11 @@ vn_status check_sizes(int64_t rows, int64_t in, int64_t out, vn_dtype dt) {
   return VN_OK;
 }
 
+// Few rows take any number of features; other kernels' coordinates have 32 bits.
+bool features_ok(int64_t rows, int64_t in, int64_t out) {
+  return rows <= 8 || (in <= vn::kDenseMost && out <= vn::kDenseMost);
+}
+
 }  // namespace
 
 extern "C" {
@@ -503,7 +508,7 @@ vn_status vn_hash_probe(int64_t seed, uint64_t offset, int64_t n_sums, int64_t m
 }
 
 int64_t vn_linear_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, int al) {
-  if (check_sizes(rows, in, out, dt) != VN_OK) return -1;
+  if (check_sizes(rows, in, out, dt) != VN_OK || !features_ok(rows, in, out)) return -1;
   return vn::dense_workspace(rows, in, out, dt, al != 0);
 }
 
@@ -516,6 +521,7 @@ vn_status vn_linear(const void* x, const void* w, vn_dtype dt, const void* b, vn
   const vn_status st = check_sizes(rows, in, out, dt);
   if (st != VN_OK) return st;
   if (rows == 0 || out == 0) return VN_OK;
+  if (!features_ok(rows, in, out)) return VN_ERR_OVERFLOW;
   if (y == nullptr || (in > 0 && (x == nullptr || w == nullptr))) return VN_ERR_NULL;
   const size_t es = dtype_size(dt);
   if (!aligned(x, es) || !aligned(w, es) || !aligned(y, es) || !aligned(preact, es) ||
@@ -544,6 +550,7 @@ vn_status vn_testhook_linear_plan(int64_t rows, int64_t in, int64_t out, vn_dtyp
   const vn_status st = check_sizes(rows, in, out, dt);
   if (st != VN_OK) return st;
   if (!linear_act_ok(act)) return VN_ERR_VALUE;
+  if (rows > vn::kDenseMost || !features_ok(backward ? 9 : rows, in, out)) return VN_ERR_OVERFLOW;
   if (plan == nullptr) return VN_ERR_NULL;
   int32_t p[10];
   vn::dense_plan(rows, in, out, dt, act, al != 0, backward != 0, p);
@@ -577,7 +584,7 @@ vn_status vn_testhook_linear_withhold(int kernel, const void* x, const void* w, 
 
 int64_t vn_linear_backward_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt,
                                      vn_act act, int al) {
-  if (check_sizes(rows, in, out, dt) != VN_OK || !linear_act_ok(act)) return -1;
+  if (check_sizes(rows, in, out, dt) != VN_OK || !features_ok(9, in, out) || !linear_act_ok(act)) return -1;
   return vn::dense_backward_workspace(rows, in, out, dt, act, al != 0);
 }
 
@@ -593,6 +600,7 @@ vn_status vn_linear_backward(const void* grad, const void* x, const void* w, con
   const bool no_w = grad_w == nullptr || out == 0 || in == 0;
   const bool no_b = grad_b == nullptr || out == 0;
   if (no_x && no_w && no_b) return VN_OK;
+  if (!features_ok(9, in, out) || (rows > vn::kDenseMost && !(no_w && no_b))) return VN_ERR_OVERFLOW;
   const bool some = rows > 0 && out > 0;  // d has elements
   if (some && (grad == nullptr || (act != VN_ACT_NONE && preact == nullptr) || (!no_x && w == nullptr) ||
                (!no_w && x == nullptr)))

@@ -26,8 +26,6 @@
 namespace vn {
 namespace {
 
-__device__ __forceinline__ float value(float x) { return x; }
-__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <typename T>
 __device__ __forceinline__ T narrow(float x);
 template <>
@@ -36,81 +34,6 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
-constexpr int kTile = 64, kStep = 16, kThreads = 256;
-
-struct Product {
-  const void* a;
-  const void* b;
-  int64_t ap, ak, bq, bk;  // element strides
-  int64_t np, nq, nk;
-  const void* bias;        // [np] or NULL
-  int bias_bf16, act;
-  const void* residual;    // [nq, np] or NULL
-  void* out;               // [nq, np]
-  void* preact;            // [nq, np] or NULL
-  int64_t p_tiles;
-};
-
-// 64 x 64 outputs a CTA, 4 x 4 a thread; 16 of k at a time through shared memory.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) product_kernel(const Product d) {
-  let_next();
-  after_previous();
-  __shared__ float sa[kStep][kTile + 4], sb[kStep][kTile + 4];
-  const int64_t p0 = static_cast<int64_t>(blockIdx.x % d.p_tiles) * kTile;
-  const int64_t q0 = static_cast<int64_t>(blockIdx.x / d.p_tiles) * kTile;
-  const int tp = threadIdx.x % 16, tq = threadIdx.x / 16;
-  const T* a = static_cast<const T*>(d.a);
-  const T* b = static_cast<const T*>(d.b);
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < d.nk; k0 += kStep) {
-#pragma unroll
-    for (int r = 0; r < kTile * kStep / kThreads; ++r) {
-      const int e = r * kThreads + threadIdx.x;
-      {
-        const int k = d.ak == 1 ? e % kStep : e / kTile, p = d.ak == 1 ? e / kStep : e % kTile;
-        sa[k][p] = (k0 + k < d.nk && p0 + p < d.np) ? value(a[(p0 + p) * d.ap + (k0 + k) * d.ak]) : 0.f;
-      }
-      {
-        const int k = d.bk == 1 ? e % kStep : e / kTile, q = d.bk == 1 ? e / kStep : e % kTile;
-        sb[k][q] = (k0 + k < d.nk && q0 + q < d.nq) ? value(b[(q0 + q) * d.bq + (k0 + k) * d.bk]) : 0.f;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kStep; ++k) {
-      float av[4], bv[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        av[i] = sa[k][tp * 4 + i];
-        bv[i] = sb[k][tq * 4 + i];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(bv[i], av[j], acc[i][j]);
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t q = q0 + tq * 4 + i, p = p0 + tp * 4 + j;
-      if (q < d.nq && p < d.np) {
-        float z = acc[i][j];
-        if (d.bias != nullptr)
-          z += d.bias_bf16 ? value(static_cast<const __nv_bfloat16*>(d.bias)[p]) : static_cast<const float*>(d.bias)[p];
-        if (d.preact != nullptr) static_cast<T*>(d.preact)[q * d.np + p] = narrow<T>(z);
-        float v[1] = {z};
-        activate_all<false>(d.act, v);
-        z = v[0];
-        if (d.residual != nullptr) z += value(static_cast<const T*>(d.residual)[q * d.np + p]);
-        static_cast<T*>(d.out)[q * d.np + p] = narrow<T>(z);
-      }
-    }
-}
 
 // Eight values to row-major memory. kPlanes 1: in T, 16-byte stores where they fit; 3: bf16
 // planes, `plane` elements apart, the whole group written (pitch is a multiple of 8).
@@ -284,20 +207,6 @@ __global__ void __launch_bounds__(256) delta_kernel(const Delta a) {
   if (col < a.n) a.part[static_cast<int64_t>(blockIdx.y) * a.n + col] = t;
 }
 
-template <typename T>
-cudaError_t run_product(Product d, cudaStream_t stream) {
-  if (d.np == 0 || d.nq == 0) return cudaSuccess;
-  d.p_tiles = (d.np + kTile - 1) / kTile;
-  const int64_t q_tiles = (d.nq + kTile - 1) / kTile;
-  if (d.p_tiles > 0x7FFFFFFFll / q_tiles) return cudaErrorInvalidConfiguration;
-  const dim3 grid(static_cast<unsigned>(d.p_tiles * q_tiles));
-  return launch_overlapped(product_kernel<T>, grid, kThreads, 0, 0, stream, d);
-}
-
-cudaError_t product(const Product& d, vn_dtype dt, cudaStream_t stream) {
-  return dt == VN_BF16 ? run_product<__nv_bfloat16>(d, stream) : run_product<float>(d, stream);
-}
-
 constexpr int64_t kAlign = 256;
 int64_t rounded(int64_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
 int64_t pitch_of(int64_t cols) { return (cols + 7) / 8 * 8; }
@@ -314,15 +223,12 @@ bool as_is(vn_dtype dt, int64_t cols, bool aligned) { return dt == VN_BF16 && co
 // microseconds a launch, more of them the larger its tile, and a CTA's (or pair's) time per 64 of k.
 // They are reckoned here, from sizes alone, so that a call and its workspace agree without a device.
 enum class Route {
-  kRows,    // few rows, at most 8: vn_dense_rows.cu
-  kPlain,   // 64 x 64 tiles without tensor cores: sizes beyond 32-bit coordinates
-  kGather,  // one launch, operands gathered by threads: vn_dense_gather.cu
-  kTiles,   // operands by TMA, in bf16 (converted where they are not): vn_dense_tc.cu
+  kRows = 0,    // few rows, at most 8: vn_dense_rows.cu
+  kGather = 2,  // one launch, operands gathered by threads: vn_dense_gather.cu
+  kTiles = 3,   // operands by TMA, in bf16 (converted where they are not): vn_dense_tc.cu
 };
-bool fits32(int64_t rows, int64_t in, int64_t out) {
-  const int64_t most = (int64_t{1} << 31) - 512;
-  return rows <= most && in <= most && out <= most;
-}
+// More rows than 32-bit coordinates reach are taken in slices.
+constexpr int64_t kSlice = int64_t{1} << 30;
 double tiles_of(int64_t n, int64_t tile) { return static_cast<double>((n + tile - 1) / tile); }
 // CTAs that the GPU holds at once in clusters of 2^log_cluster, `per_sm` to an SM: fewer than 152 SMs
 // have room for, as clusters stay within a part of the GPU.
@@ -433,13 +339,11 @@ ForwardPlan reckon_forward(int64_t rows, int64_t in, int64_t out, vn_dtype dt, b
   // fp32 keeps its products unsplit up to 8 rows; in bf16 the tensor cores take over where they are faster
   // (4096 to 4096: one row 6.2 us, eight 20.0 and on tiles 11.3; 4095 to 4095: one row 23.6, eight 49.1 and
   // gathered 18.6).
-  if (rows <= 8 && (dt == VN_F32 || in == 0 || !fits32(rows, in, out))) return p;
+  if (rows <= 8 && (dt == VN_F32 || in == 0 || in > kDenseMost || out > kDenseMost)) return p;
   const double few = rows > 8 ? 1e30
                               : 3.2 + static_cast<double>(in) * static_cast<double>(out) / 16.8e6 *
                                           (aligned && in % 8 == 0 ? 1.2 + 2.0 * static_cast<double>(rows)
                                                                   : 16.0 + 4.5 * static_cast<double>(rows));
-  p.route = Route::kPlain;
-  if (!fits32(rows, in, out)) return p;
   const Shape shapes[2] = {{out, rows, in}, {0, 0, 0}};
   const int64_t vec = dt == VN_BF16 ? 8 : 4;
   p.gather = gather_plan(shapes, dt, false, aligned && in % vec == 0);
@@ -459,8 +363,6 @@ struct BackwardPlan {
 };
 BackwardPlan reckon_backward(int64_t rows, int64_t in, int64_t out, vn_dtype dt, vn_act act, bool aligned) {
   BackwardPlan p;
-  p.route = Route::kPlain;
-  if (!fits32(rows, in, out)) return p;
   const Shape shapes[2] = {{in, rows, out}, {in, out, rows}};
   const int64_t vec = dt == VN_BF16 ? 8 : 4;
   p.gather = gather_plan(shapes, dt, true, aligned && in % vec == 0 && out % vec == 0);
@@ -538,16 +440,19 @@ cudaError_t prepare(const void* p, vn_dtype dt, int64_t rows, int64_t cols, bool
 }  // namespace
 
 int64_t dense_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, bool aligned) {
+  if (rows > kDenseMost)
+    return std::max(dense_workspace(kSlice, in, out, dt, aligned), dense_workspace((rows - 1) % kSlice + 1, in, out, dt, aligned));
   if (forward_plan(rows, in, out, dt, aligned).route != Route::kTiles || as_is(dt, in, aligned)) return 0;
   return operand_bytes(rows, in, dt) + operand_bytes(out, in, dt);
 }
 
 int64_t dense_backward_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, vn_act act, bool aligned) {
+  if (rows > kDenseMost)
+    return std::max(dense_backward_workspace(kSlice, in, out, dt, act, aligned),
+                    dense_backward_workspace((rows - 1) % kSlice + 1, in, out, dt, act, aligned));
   const Route route = backward_plan(rows, in, out, dt, act, aligned).route;
   const int64_t sums = rounded(delta_parts(rows) * out * 4);
   if (route == Route::kGather) return sums;
-  if (route == Route::kPlain)
-    return sums + (act != VN_ACT_NONE ? rounded(rows * out * (dt == VN_BF16 ? 2 : 4)) : 0);
   int64_t bytes = sums;
   if (act != VN_ACT_NONE || !as_is(dt, out, aligned)) bytes += operand_bytes(rows, out, dt);
   if (!as_is(dt, in, aligned)) bytes += operand_bytes(rows, in, dt) + operand_bytes(out, in, dt);
@@ -555,29 +460,37 @@ int64_t dense_backward_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype
 }
 
 cudaError_t launch_dense(const DenseArgs& a, cudaStream_t stream) {
+  if (a.rows > kDenseMost) {
+    const int64_t es = a.dt == VN_BF16 ? 2 : 4;
+    auto at = [&](const void* p, int64_t elements) -> void* {
+      return p != nullptr ? static_cast<uint8_t*>(const_cast<void*>(p)) + elements * es : nullptr;
+    };
+    for (int64_t r = 0; r < a.rows; r += kSlice) {
+      DenseArgs one = a;
+      one.rows = std::min(kSlice, a.rows - r);
+      one.x = at(a.x, r * a.in);
+      one.residual = at(a.residual, r * a.out);
+      one.y = at(a.y, r * a.out);
+      one.preact = at(a.preact, r * a.out);
+      const cudaError_t err = launch_dense(one, stream);
+      if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+  }
   const bool al = aligned16(a.x) && aligned16(a.w);
   const ForwardPlan plan = forward_plan(a.rows, a.in, a.out, a.dt, al);
   if (plan.route == Route::kRows) return launch_rows_forward(a, stream);
   if (plan.route == Route::kGather) return launch_gather_forward(a, plan.gather, stream);
-  if (plan.route == Route::kTiles) {
-    uint8_t* work = static_cast<uint8_t*>(a.workspace);
-    TcProduct d = {};
-    cudaError_t err = prepare(a.w, a.dt, a.out, a.in, al, false, &work, &d.a, stream);
-    if (err != cudaSuccess) return err;
-    if ((err = prepare(a.x, a.dt, a.rows, a.in, al, false, &work, &d.b, stream)) != cudaSuccess) return err;
-    d.np = a.out; d.nq = a.rows; d.nk = a.in;
-    d.dt = a.dt;
-    d.bias = a.b; d.bias_bf16 = a.b_dt == VN_BF16; d.act = a.act;
-    d.residual = a.residual; d.out = a.y; d.preact = a.preact;
-    return launch_tc_product(d, plan.tiles, stream);
-  }
-  Product d = {};
-  d.a = a.w; d.ap = a.in; d.ak = 1;
-  d.b = a.x; d.bq = a.in; d.bk = 1;
+  uint8_t* work = static_cast<uint8_t*>(a.workspace);
+  TcProduct d = {};
+  cudaError_t err = prepare(a.w, a.dt, a.out, a.in, al, false, &work, &d.a, stream);
+  if (err != cudaSuccess) return err;
+  if ((err = prepare(a.x, a.dt, a.rows, a.in, al, false, &work, &d.b, stream)) != cudaSuccess) return err;
   d.np = a.out; d.nq = a.rows; d.nk = a.in;
+  d.dt = a.dt;
   d.bias = a.b; d.bias_bf16 = a.b_dt == VN_BF16; d.act = a.act;
   d.residual = a.residual; d.out = a.y; d.preact = a.preact;
-  return product(d, a.dt, stream);
+  return launch_tc_product(d, plan.tiles, stream);
 }
 
 void dense_plan(int64_t rows, int64_t in, int64_t out, vn_dtype dt, vn_act act, bool aligned, bool backward, int32_t (&p)[10]) {
@@ -648,6 +561,19 @@ cudaError_t delta_pass(const DenseGradArgs& a, const TcOperand* delta, float* pa
 }  // namespace
 
 cudaError_t launch_dense_backward(const DenseGradArgs& a, cudaStream_t stream) {
+  if (a.rows > kDenseMost) {  // only grad_x is asked for
+    const int64_t es = a.dt == VN_BF16 ? 2 : 4;
+    for (int64_t r = 0; r < a.rows; r += kSlice) {
+      DenseGradArgs one = a;
+      one.rows = std::min(kSlice, a.rows - r);
+      one.grad = static_cast<const uint8_t*>(a.grad) + r * a.out * es;
+      one.preact = a.preact != nullptr ? static_cast<const uint8_t*>(a.preact) + r * a.out * es : nullptr;
+      one.grad_x = static_cast<uint8_t*>(a.grad_x) + r * a.in * es;
+      const cudaError_t err = launch_dense_backward(one, stream);
+      if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+  }
   const bool al = aligned16(a.grad) && aligned16(a.x) && aligned16(a.w);
   const BackwardPlan plan = backward_plan(a.rows, a.in, a.out, a.dt, a.act, al);
   if (plan.route == Route::kGather) {
@@ -660,9 +586,8 @@ cudaError_t launch_dense_backward(const DenseGradArgs& a, cudaStream_t stream) {
     }
     return launch_gather_backward(rest, plan.gather, stream);
   }
-  const bool tc = plan.route == Route::kTiles;
   const bool products = a.grad_x != nullptr || a.grad_w != nullptr;
-  const bool keep = products && (a.act != VN_ACT_NONE || (tc && !as_is(a.dt, a.out, al)));  // d has to be stored
+  const bool keep = products && (a.act != VN_ACT_NONE || !as_is(a.dt, a.out, al));  // d has to be stored
   uint8_t* work = static_cast<uint8_t*>(a.workspace);
   cudaError_t err = cudaSuccess;
   float* part = reinterpret_cast<float*>(work);
@@ -670,50 +595,29 @@ cudaError_t launch_dense_backward(const DenseGradArgs& a, cudaStream_t stream) {
   TcOperand delta = operand(a.grad, a.rows, a.out, false);
   if (keep) {
     delta.p = work;
-    if (tc) {
-      delta.pitch = pitch_of(a.out);
-      delta.plane = a.rows * delta.pitch;
-      delta.planes = a.dt == VN_BF16 ? 1 : 3;
-      work += operand_bytes(a.rows, a.out, a.dt);
-    }
+    delta.pitch = pitch_of(a.out);
+    delta.plane = a.rows * delta.pitch;
+    delta.planes = a.dt == VN_BF16 ? 1 : 3;
+    work += operand_bytes(a.rows, a.out, a.dt);
   }
   if ((err = delta_pass(a, keep ? &delta : nullptr, part, stream)) != cudaSuccess) return err;
-  if (tc) {
-    TcProduct d = {};
-    d.dt = a.dt;
-    d.b = delta;
-    if (a.grad_x != nullptr) {
-      if ((err = prepare(a.w, a.dt, a.out, a.in, al, true, &work, &d.a, stream)) != cudaSuccess) return err;
-      d.np = a.in; d.nq = a.rows; d.nk = a.out;
-      d.out = a.grad_x;
-      if ((err = launch_tc_product(d, plan.dx, stream)) != cudaSuccess) return err;
-    }
-    if (a.grad_w != nullptr) {
-      if ((err = prepare(a.x, a.dt, a.rows, a.in, al, true, &work, &d.a, stream)) != cudaSuccess) return err;
-      d.b.mn = true;
-      d.np = a.in; d.nq = a.out; d.nk = a.rows;
-      d.out = a.grad_w;
-      return launch_tc_product(d, plan.dw, stream);
-    }
-    return cudaSuccess;
-  }
-  Product d = {};
-  d.b = delta.p;
+  TcProduct d = {};
+  d.dt = a.dt;
+  d.b = delta;
   if (a.grad_x != nullptr) {
-    d.a = a.w; d.ap = 1; d.ak = a.in;
-    d.bq = a.out; d.bk = 1;
+    if ((err = prepare(a.w, a.dt, a.out, a.in, al, true, &work, &d.a, stream)) != cudaSuccess) return err;
     d.np = a.in; d.nq = a.rows; d.nk = a.out;
     d.out = a.grad_x;
-    if ((err = product(d, a.dt, stream)) != cudaSuccess) return err;
+    if ((err = launch_tc_product(d, plan.dx, stream)) != cudaSuccess) return err;
   }
   if (a.grad_w != nullptr) {
-    d.a = a.x; d.ap = 1; d.ak = a.in;
-    d.bq = 1; d.bk = a.out;
+    if ((err = prepare(a.x, a.dt, a.rows, a.in, al, true, &work, &d.a, stream)) != cudaSuccess) return err;
+    d.b.mn = true;
     d.np = a.in; d.nq = a.out; d.nk = a.rows;
     d.out = a.grad_w;
-    if ((err = product(d, a.dt, stream)) != cudaSuccess) return err;
+    err = launch_tc_product(d, plan.dw, stream);
   }
-  return cudaSuccess;
+  return err;
 }
 
 }  // namespace vn

@@ -111,6 +111,9 @@ cudaError_t launch_hash_probe(uint64_t seed, uint64_t offset, int64_t n_sums, in
                               float* sums, cudaStream_t stream);
 
 // The centre network (arguments as in vn.h; sizes may be zero where it says so).
+// The most features of a layer of more than 8 rows, and the most rows that its gradients sum over: the kernels'
+// coordinates have 32 bits.
+constexpr int64_t kDenseMost = (int64_t{1} << 31) - 512;
 struct DenseArgs {
   const void* x;
   const void* w;
