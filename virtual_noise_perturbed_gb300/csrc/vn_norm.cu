@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(grad_threads(T), T < 64 && V * NV <= 4 ? 2 : 1
   }
 }
 
-// The same for longer rows of 16-byte packs, on the ring of the forward kernel: with
+// The same for longer rows of 16-byte packs, which come through a ring of rows in shared memory: with
 // straight loads of one row ahead 32 KB an SM were on their way, 4 TB/s; and on pairs: 35
 // instructions an element were the next bound (193 us on 32768 x 4096 bf16).
 template <typename X, int T, int NV>
@@ -938,10 +938,15 @@ cudaError_t norm_typed(const NormArgsK& a, cudaStream_t stream) {
   constexpr int V = 16 / sizeof(X);
   if (!aligned16(a.w) || !aligned16(a.b)) return norm_by_length<X, 1, false>(a, stream);
   if (a.n % V == 0 && aligned16(a.x) && aligned16(a.y)) return norm_by_length<X, V, false>(a, stream);
-  // Rows that start anywhere: bf16, 60000 x 63 9.7 us in packs, 17.0 in single elements; 65536 x 511 60 and
-  // 69; 4099 x 1021 9.7 and 8.2; 32768 x 4095 175 and 154, as shifting a pack then costs more than
-  // the loads it saves; 16384 x 8191 169 and 202.
-  return a.n <= 512 || a.n > 4096 ? norm_by_length<X, V, true>(a, stream) : norm_by_length<X, 1, false>(a, stream);
+  // Rows that start anywhere. In packs their loads are fewer, but each is shifted into place, and how many of a
+  // thread's packs a length fills matters; single elements run out of registers at 4096 and read a longer row
+  // three times. 40 M elements, packs and single elements, us: fp32 127 69 82, 129 153 81, 255 87 48, 257
+  // 114 158, 511 69 81, 513 106 82, 4097 127 79, 8191 80 74, 12289 79 78, 16383 69 82; bf16 127 73 81, 129 94 81,
+  // 255 57 43, 257 117 158, 511 70 81, 513 91 81, 4097 86 75, 6001 66 80, 8191 55 62, 8193 86 58, 12289 70 57,
+  // 16383 60 64.
+  const int64_t n = a.n;
+  const bool packs = n <= 128 || (n > 256 && n <= 512) || n > 14000 || (sizeof(X) == 2 && n > 5000 && n <= 8192);
+  return packs ? norm_by_length<X, V, true>(a, stream) : norm_by_length<X, 1, false>(a, stream);
 }
 
 // Partial rows of the column sums: at most this many CTAs walk the rows.
