@@ -805,7 +805,8 @@ __global__ void __launch_bounds__(T) norm_grad_ring_kernel(const NormGradK a, co
   }
 }
 
-// Long rows: grad_x in two passes over the row ...
+// Long rows, beyond 8192 elements: grad_x in two passes over the row, of single elements (16384 x 8200 bf16 541 us
+// with the column sums, 568 in fp32, where 16384 x 8192 on the ring takes 151 and 206) ...
 template <typename X>
 __global__ void __launch_bounds__(512) norm_grad_long_kernel(const NormGradK a) {
   let_next();

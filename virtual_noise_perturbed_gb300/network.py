@@ -62,7 +62,9 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     x is (..., in), weight (out, in), residual (..., out), all float32 or all bfloat16; bias
     (out,) of either type. ``activation``: None, "tanh", "relu", "gelu" (z times the normal
     distribution function of z) or "silu". With ``preact=True`` the result is (y, z), z the
-    value before the activation that ``linear_backward`` needs. ``check_status=True`` calls
+    value before the activation that ``linear_backward`` needs. Activations are good to 2^-20 (1 + |z|),
+    with up to 8 float32 rows to a few roundings. An infinity in x or weight gives NaN with more than 8
+    float32 rows, whose products are sums over three bfloat16 terms. ``check_status=True`` calls
     ``device_status()`` before returning (it synchronises): the tensor-core kernels bound
     their waits, and a wait that ran out leaves y unwritten."""
     y = (_binding or _native()).linear(x, weight, bias, _act(activation), residual, preact, out)
@@ -79,7 +81,9 @@ def linear_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     grad is the gradient of y, (..., out); preact the z that ``linear(..., preact=True)``
     returned (not needed without an activation). The gradients have their tensors' shapes and
     dtypes, grad_bias the weight's (None with ``bias=False``). The residual's gradient is
-    grad."""
+    grad. With bfloat16 and an activation, grad times the activation's slope is rounded once to bfloat16
+    before the two products (grad_bias sums it unrounded). Infinities are as for ``linear``; slopes are
+    good to 2^-20."""
     grads = (_binding or _native()).linear_backward(grad, x, weight, preact, _act(activation), bias)
     if check_status:
         device_status(x.device)
