@@ -483,11 +483,12 @@ vn_status vn_testhook_linear_tc_withhold(const void* x, vn_dtype x_dt, int x_sha
 /* The same for vn_linear's tensor-core kernels. kernel: 0 operands gathered by threads, 1 tiles
  * of single CTAs (both with k split over clusters of 2), 2 tiles of pairs of CTAs. Runs
  * y = x W^T + residual (and preact) in bf16 with every wait limited to `timeout_ms`, while the
- * first CTA withholds its handover of operands number `withhold` (from 0) to the MMAs, or, in kernel 0
+ * first CTA withholds its handover of operands number `withhold` (from 0) to the MMAs, or, in kernel 0 (or 4)
  * and beyond its last handover, the arrival that its epilogue waits for. Results are then not
  * valid, and vn_device_status() reports VN_ERR_TIMEOUT. With a `withhold` beyond what the first CTA
- * hands over, kernels 1 and 2 complete normally. in >= 128; in and out multiples of 8
- * (VN_ERR_SHAPE), pointers on 16 bytes. */
+ * hands over, the kernels of tiles complete normally. Kernels 4, 5 and 6 are the same three in fp32, with
+ * their sums in pieces; 5 and 6 take x and w as three bf16 terms each, [3][rows][in] and [3][out][in].
+ * in >= 128; in and out multiples of 8 (VN_ERR_SHAPE), pointers on 16 bytes. */
 vn_status vn_testhook_linear_withhold(int kernel, const void* x, const void* w, const void* residual,
                                       int64_t rows, int64_t in, int64_t out, void* y,
                                       void* preact, int64_t withhold, double timeout_ms,

@@ -88,3 +88,50 @@ def test_the_status_of_all_kernels_is_one_read():
     median(vn.device_status)
     ratio = min(median(vn.device_status) / median(x[0].item) for _ in range(5))
     assert ratio < 1.7, ratio
+
+
+def terms(t):
+    """An fp32 matrix as three bf16 ones that add up to it: its top 8 significant bits, the next, the last."""
+    out = []
+    for _ in range(3):
+        top = (t.view(torch.int32) & -65536).view(torch.float32)
+        out.append(top.bfloat16())
+        t = t - top
+    return torch.stack(out)
+
+
+# In fp32 sums are taken in pieces of k: the first CTA hands over to several of them (64 of k each; on tiles six
+# times as often, once for each product of terms).
+@pytest.mark.parametrize("kernel,rows,k,n,withhold", [
+    (4, 70, 8192, 200, 0), (4, 70, 8192, 200, 40), (4, 70, 8192, 200, 64),
+    (5, 70, 2048, 200, 0), (5, 70, 2048, 200, 95), (5, 70, 8192, 200, 200),
+    (6, 300, 2048, 520, 0), (6, 300, 2048, 520, 165), (6, 300, 2048, 520, 191), (6, 5000, 512, 2048, 45)])
+def test_a_wait_that_runs_out_is_recorded_in_fp32(kernel, rows, k, n, withhold):
+    build()
+    lib = _lib.load()
+    g = torch.Generator().manual_seed(withhold + k)
+    x, w, r = (torch.randn(s, generator=g).to(DEV) for s in ((rows, k), (n, k), (rows, n)))
+    xs, ws = (x, w) if kernel == 4 else (terms(x), terms(w))
+    y, z = torch.empty_like(r), torch.empty_like(r)
+    stream = P(torch.cuda.current_stream().cuda_stream)
+    vn.device_status()
+    want = x.double() @ w.double().t()
+    bound = (2 * k + 18) * 2.0 ** -24 * (x.double().abs() @ w.double().abs().t())
+
+    def call(at):
+        assert lib.vn_testhook_linear_withhold(kernel, ptr(xs), ptr(ws), ptr(r), rows, k, n, ptr(y), ptr(z), at, 50.0,
+                                               stream) == 0
+
+    def right(y, z):
+        full = want + r.double()
+        assert bool(((z.double() - want).abs() <= bound).all())
+        assert bool(((y.double() - full).abs() <= bound + 2.0 ** -23 * (r.double().abs() + full.abs())).all())
+
+    if kernel > 4:
+        call(1 << 20)
+        assert lib.vn_device_status(stream) == 0
+        right(y, z)
+    call(withhold)
+    assert lib.vn_device_status(stream) == 7
+    assert lib.vn_device_status(stream) == 0
+    right(*vn.linear(x, w, residual=r, preact=True, check_status=True))

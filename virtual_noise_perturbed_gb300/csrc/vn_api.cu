@@ -561,7 +561,7 @@ vn_status vn_testhook_linear_plan(int64_t rows, int64_t in, int64_t out, vn_dtyp
 vn_status vn_testhook_linear_withhold(int kernel, const void* x, const void* w, const void* residual, int64_t rows,
                                       int64_t in, int64_t out, void* y, void* preact, int64_t withhold,
                                       double timeout_ms, void* stream) {
-  if (kernel < 0 || kernel > 2 || !(timeout_ms > 0.0) || !(timeout_ms <= 60000.0) || withhold < 0 || withhold > (1 << 30))
+  if (kernel < 0 || kernel == 3 || kernel > 6 || !(timeout_ms > 0.0) || !(timeout_ms <= 60000.0) || withhold < 0 || withhold > (1 << 30))
     return VN_ERR_VALUE;
   const vn_status st = check_sizes(rows, in, out, VN_BF16);
   if (st != VN_OK) return st;
@@ -571,12 +571,14 @@ vn_status vn_testhook_linear_withhold(int kernel, const void* x, const void* w, 
   if (x == nullptr || w == nullptr || y == nullptr) return VN_ERR_NULL;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(preact, 16))
     return VN_ERR_ALIGN;
-  const int64_t xb = rows * in * 2, wb = out * in * 2, yb = rows * out * 2;
+  const bool fp32 = kernel > 2;
+  const int64_t es = fp32 ? 4 : 2, is = kernel > 4 ? 6 : es;  // of results and of operands
+  const int64_t xb = rows * in * is, wb = out * in * is, yb = rows * out * es;
   const Range outs[] = {{y, yb}, {preact, yb}};
   const Range ins[] = {{x, xb}, {w, wb}, {residual, yb}};
   if (!disjoint(outs, ins)) return VN_ERR_VALUE;
   vn::DenseArgs a = {};
-  a.x = x; a.w = w; a.dt = VN_BF16; a.residual = residual;
+  a.x = x; a.w = w; a.dt = fp32 ? VN_F32 : VN_BF16; a.residual = residual;
   a.rows = rows; a.in = in; a.out = out; a.act = VN_ACT_NONE; a.y = y; a.preact = preact;
   return launched(vn::launch_dense_hook(a, kernel, static_cast<int>(withhold),
                                         static_cast<unsigned long long>(timeout_ms * 1e6), static_cast<cudaStream_t>(stream)));

@@ -510,7 +510,7 @@ void dense_plan(int64_t rows, int64_t in, int64_t out, vn_dtype dt, vn_act act, 
 
 cudaError_t launch_dense_hook(const DenseArgs& a, int kernel, int at, unsigned long long timeout_ns, cudaStream_t stream) {
   const Withhold hook = {at, timeout_ns};
-  if (kernel == 0) {
+  if (kernel % 4 == 0) {
     GatherPlan plan;
     plan.log_split[0] = 1;
     return launch_gather_forward(a, plan, stream, &hook);
@@ -518,13 +518,14 @@ cudaError_t launch_dense_hook(const DenseArgs& a, int kernel, int at, unsigned l
   TcProduct d = {};
   d.a = operand(a.w, a.out, a.in, false);
   d.b = operand(a.x, a.rows, a.in, false);
+  if (a.dt == VN_F32) d.a.planes = d.b.planes = 3;  // given as the tensor cores take them
   d.np = a.out; d.nq = a.rows; d.nk = a.in;
   d.dt = a.dt;
   d.residual = a.residual; d.out = a.y; d.preact = a.preact;
   TilePlan plan;
-  plan.pair = kernel == 2;
-  plan.bn = kernel == 2 ? 128 : 64;
-  plan.log_split = kernel == 2 ? 0 : 1;
+  plan.pair = kernel % 4 == 2;
+  plan.bn = plan.pair ? 128 : 64;
+  plan.log_split = plan.pair ? 0 : 1;
   return launch_tc_product(d, plan, stream, &hook);
 }
 

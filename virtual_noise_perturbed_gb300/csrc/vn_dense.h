@@ -52,7 +52,7 @@ struct Withhold {
   int at;
   unsigned long long timeout_ns;
 };
-// hook: bf16 and k-contiguous operands only; single tiles of 64 columns, pairs whose rows TMA can store.
+// hook: k-contiguous operands only; single tiles of 64 columns, pairs whose rows TMA can store.
 cudaError_t launch_tc_product(const TcProduct& d, const TilePlan& plan, cudaStream_t stream, const Withhold* hook = nullptr);
 
 // A layer, or all its gradients, in one launch, for any alignment and no workspace
@@ -62,7 +62,7 @@ cudaError_t launch_tc_product(const TcProduct& d, const TilePlan& plan, cudaStre
 struct DenseArgs;
 struct DenseGradArgs;
 cudaError_t launch_rows_forward(const DenseArgs& a, cudaStream_t stream);  // rows <= 8 (vn_dense_rows.cu)
-// hook: bf16 whose rows start on 16 bytes, on 16 columns. Beyond a CTA's last chunk, `at` is the commit
+// hook: rows that start on 16 bytes, on 16 columns, fp32 in pieces. Beyond a CTA's last chunk, `at` is the commit
 // that the epilogue waits for.
 cudaError_t launch_gather_forward(const DenseArgs& a, const GatherPlan& plan, cudaStream_t stream,
                                   const Withhold* hook = nullptr);

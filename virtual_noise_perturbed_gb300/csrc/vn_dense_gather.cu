@@ -721,7 +721,8 @@ cudaError_t launch_gather_forward(const DenseArgs& a, const GatherPlan& plan, cu
   if (hook != nullptr) {
     g.withhold = hook->at;
     g.timeout_ns = hook->timeout_ns;
-    return run<__nv_bfloat16, 16, false, false, false, true>(g, plan.log_split, stream);
+    return a.dt == VN_BF16 ? run<__nv_bfloat16, 16, false, false, false, true>(g, plan.log_split, stream)
+                           : run<float, 16, false, false, true, true>(g, plan.log_split, stream);
   }
   return a.dt == VN_BF16 ? run_plan<__nv_bfloat16, false>(g, plan, stream)
                          : run_plan<float, false>(g, plan, stream);

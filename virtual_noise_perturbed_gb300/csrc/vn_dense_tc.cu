@@ -780,7 +780,7 @@ cudaError_t run(const TcProduct& d, const TilePlan& plan, cudaStream_t stream, c
   p.iters = p.k_chunks * (d.a.planes == 3 ? 6 : 1);
   p.timeout_ns = kTimeoutNs;
   if ((err = device_status_word(&p.status)) != cudaSuccess) return err;
-  if constexpr (sizeof(T) == 2 && !kAMn && !kBMn) {
+  if constexpr (!kAMn && !kBMn) {
     if (hook != nullptr) {
       p.withhold = hook->at;
       p.timeout_ns = hook->timeout_ns;

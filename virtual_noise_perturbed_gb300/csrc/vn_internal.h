@@ -149,7 +149,7 @@ cudaError_t launch_dense(const DenseArgs& a, cudaStream_t stream);
 cudaError_t launch_dense_backward(const DenseGradArgs& a, cudaStream_t stream);
 // The test hook of vn_testhook_linear_plan (vn.h).
 void dense_plan(int64_t rows, int64_t in, int64_t out, vn_dtype dt, vn_act act, bool aligned, bool backward, int32_t (&p)[10]);
-// The test hook of vn_testhook_linear_withhold (vn.h): bf16, in a multiple of 8 and at least 128, out a
+// The test hook of vn_testhook_linear_withhold (vn.h): in a multiple of 8 and at least 128, out a
 // multiple of 8, every pointer on 16 bytes.
 cudaError_t launch_dense_hook(const DenseArgs& a, int kernel, int at, unsigned long long timeout_ns, cudaStream_t stream);
 
