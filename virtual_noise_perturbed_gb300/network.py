@@ -57,7 +57,8 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
            activation: Optional[str] = None, residual: Optional[torch.Tensor] = None, preact: bool = False,
            out: Optional[torch.Tensor] = None,
            check_status: bool = False) -> Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]]:
-    """act(x W^T + b) + residual, shape (..., out), in one epilogue (``vn_linear``).
+    """act(x W^T + b) + residual, shape (..., out), in one epilogue (``vn_linear``); not recorded by
+    autograd.
 
     x is (..., in), weight (out, in), residual (..., out), all float32 or all bfloat16; bias
     (out,) of either type. ``activation``: None, "tanh", "relu", "gelu" (z times the normal
@@ -96,7 +97,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     """(y, mean, rstd): each row of x (..., n) to zero mean and unit variance, times weight plus
     bias (``vn_layer_norm``). x is float32 or bfloat16 and y like it; weight and bias (n,) are of
     either type, or None. mean and rstd are float32 of x's leading shape; ``layer_norm_backward``
-    takes them."""
+    takes them. Not recorded by autograd."""
     return (_binding or _native()).layer_norm(x, weight, bias, eps, out)
 
 
