@@ -439,6 +439,48 @@ vn_status vn_adamw_moments(const void* exp_avg, const void* exp_avg_sq, const fl
                            const float* exp_avg_sq_scale, int64_t n, float* m, float* v,
                            void* stream);
 
+/* One tensor of vn_gradient_norm and vn_clip_gradients. */
+typedef struct vn_gradient {
+  const void* grad; /* [n] of dt                                                        */
+  void* out;        /* [n] of dt: the scaled gradient, may be grad (vn_clip_gradients)  */
+  int64_t n;
+} vn_gradient;
+
+/*
+ * vn_gradient_norm -- the norm over all elements of n_tensors tensors (a HOST array, read during the
+ * call), norm = sqrt(sum g^2), one fp32 on the device: the exact norm rounded once, but for a last bit
+ * where it falls next to a border. A norm beyond fp32's largest value is infinite, one of a gradient with a
+ * NaN is NaN; no tensors, or empty ones, have norm 0. Sums have a fixed order.
+ * workspace: vn_gradient_norm_workspace bytes, 256-byte aligned. n_tensors up to 2^32.
+ */
+vn_status vn_gradient_norm(const vn_gradient* tensors, int64_t n_tensors, vn_dtype dt, float* norm,
+                           void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * vn_clip_gradients -- the same, and out = g * factor with
+ *     factor = norm <= max_norm ? 1 : max_norm / norm       (norm before its rounding; factor one fp32)
+ * for every element, rounded once to dt. out may be the tensor's own grad (in place; nothing is written where
+ * factor is 1); else no out may share memory with any grad, and no two outs may. max_norm >= 0 (infinite: never
+ * clips). An infinite norm gives factor 0 (NaN where the gradient is infinite), a NaN gives NaN everywhere.
+ */
+vn_status vn_clip_gradients(const vn_gradient* tensors, int64_t n_tensors, vn_dtype dt,
+                            double max_norm, float* norm, void* workspace,
+                            int64_t workspace_bytes, void* stream);
+
+/* Workspace of vn_gradient_norm, vn_clip_gradients and vn_adamw_clipped in bytes, -1 for a count
+ * that they refuse. */
+int64_t vn_gradient_norm_workspace(int64_t n_tensors);
+
+/*
+ * vn_adamw_clipped -- vn_adamw with vn_clip_gradients' factor (of all tensors' gradients) times grad,
+ * rounded once to fp32, in grad's place; the gradients themselves are not written. norm, max_norm and
+ * workspace as there. Everything the call writes is checked against everything it reads or writes.
+ */
+vn_status vn_adamw_clipped(const vn_adamw_tensor* tensors, int64_t n_tensors, vn_dtype param_dt,
+                           vn_dtype grad_dt, int state_bits, double lr, double beta1, double beta2,
+                           double eps, int64_t step, int maximize, double max_norm, float* norm,
+                           void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears the current device's status
  * word: VN_ERR_TIMEOUT if a kernel of this library recorded an expired wait
  * since the last call, VN_ERR_CUDA if synchronisation failed, else VN_OK. */

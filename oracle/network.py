@@ -125,3 +125,14 @@ def pack(x, root=False):
 
 def unpack(q, scale):
     return q * np.repeat(scale, BLOCK)[:q.size]
+
+
+def gradient_norm(grads):
+    """The norm over all elements of a sequence of arrays."""
+    return float(np.sqrt(sum(float(np.sum(np.square(np.asarray(g, dtype=np.float64)))) for g in grads)))
+
+
+def clip_factor(norm, max_norm):
+    """What ``clip_gradients`` multiplies by."""
+    with np.errstate(divide="ignore", invalid="ignore"):
+        return 1.0 if norm <= max_norm else float(np.float64(max_norm) / np.float64(norm))

@@ -29,6 +29,8 @@ from .api import (  # noqa: F401
 )
 from .network import (  # noqa: F401
     AdamW,
+    clip_gradients,
+    gradient_norm,
     layer_norm,
     layer_norm_backward,
     linear,
@@ -36,7 +38,7 @@ from .network import (  # noqa: F401
 )
 
 __all__ = [
-    "AdamW", "VNError", "centered_ranks", "compute_offsets", "device_status", "es_update", "gradient_update", "hash_probe", "layer_norm",
+    "AdamW", "VNError", "centered_ranks", "clip_gradients", "compute_offsets", "device_status", "es_update", "gradient_norm", "gradient_update", "hash_probe", "layer_norm",
     "layer_norm_backward", "linear", "linear_backward", "noise_dump", "perturbed_linear_path",
     "virtual_bias_gradient", "virtual_flat_gradient", "virtual_perturbed_linear", "virtual_perturbed_mlp",
     "virtual_reduce_metric",

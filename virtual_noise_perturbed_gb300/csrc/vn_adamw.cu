@@ -57,6 +57,7 @@ struct Table {
   float b1, c1, b2, c2;     // beta and 1 - beta; c1 negative to ascend
   float inv_root, eps;      // 1 / sqrt(1 - beta2^t), eps
   float size;               // -lr / (1 - beta1^t)
+  const float* factor;      // of a clipped gradient
   Entry e[kCap];
 };
 
@@ -163,7 +164,7 @@ struct Moment<true> {
 // (kVec), or the elements l, l + 32, .. (any alignment, and the last block of a tensor). The
 // operands stay as they were loaded until their group's turn, in few registers: what is in
 // flight per SM is what bounds this kernel.
-template <typename P, typename G, bool k8, bool kVec, int kCap>
+template <typename P, typename G, bool k8, bool kVec, bool kClip, int kCap>
 __device__ __forceinline__ void step_block(const Table<kCap>& t, const Entry& e, int64_t block, int lane) {
   using M = typename Moment<k8>::Element;
   using Four = typename Moment<k8>::Four;
@@ -176,6 +177,7 @@ __device__ __forceinline__ void step_block(const Table<kCap>& t, const Entry& e,
   Raw<P> rp[2];
   Raw<G> rg[2];
   Four rm[2], rv[2];
+  const float factor = kClip ? fetch(t.factor) : 1.f;
   float ms = 0.f, vs = 0.f;
   if constexpr (k8) {
     ms = e.ms[block];
@@ -208,6 +210,7 @@ __device__ __forceinline__ void step_block(const Table<kCap>& t, const Entry& e,
     float np[4];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
+      if constexpr (kClip) gv[q] = mul2(gv[q], f2(factor, factor));
       if constexpr (k8) {
         mv[q] = mul2(mv[q], f2(ms, ms));
         vv[q] = mul2(vv[q], f2(vs, vs));
@@ -295,7 +298,7 @@ __device__ __forceinline__ void step_block(const Table<kCap>& t, const Entry& e,
 
 // Five CTAs an SM: 105 us on 54.5 M parameters with 8 bits, 114 us with the four that 56
 // registers leave, 111 us with six.
-template <typename P, typename G, bool k8, int kCap>
+template <typename P, typename G, bool k8, bool kClip, int kCap>
 __global__ void __launch_bounds__(kThreads, 5) adamw_kernel(const __grid_constant__ Table<kCap> t) {
   let_next();
   after_previous();
@@ -310,9 +313,9 @@ __global__ void __launch_bounds__(kThreads, 5) adamw_kernel(const __grid_constan
   if (block * kBlock >= e.n) return;
   const int lane = threadIdx.x & 31;
   if (e.vec && (block + 1) * kBlock <= e.n)
-    step_block<P, G, k8, true>(t, e, block, lane);
+    step_block<P, G, k8, true, kClip>(t, e, block, lane);
   else
-    step_block<P, G, k8, false>(t, e, block, lane);
+    step_block<P, G, k8, false, kClip>(t, e, block, lane);
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -359,6 +362,7 @@ cudaError_t launch_table(const AdamwArgs& a, int64_t from, int64_t count, cudaSt
   const double s = static_cast<double>(a.step);
   t.inv_root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(a.beta2, s)));
   t.eps = static_cast<float>(a.eps);
+  t.factor = a.factor;
   t.size = static_cast<float>(-a.lr / (1.0 - std::pow(a.beta1, s)));
   int64_t chunks = 0;
   auto fits = [](const void* q, size_t bytes) { return reinterpret_cast<uintptr_t>(q) % bytes == 0; };
@@ -379,7 +383,8 @@ cudaError_t launch_table(const AdamwArgs& a, int64_t from, int64_t count, cudaSt
   if (chunks == 0) return cudaSuccess;
   if (chunks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(chunks));
-  return launch_overlapped(adamw_kernel<P, G, k8, kCap>, grid, kThreads, 0, 0, stream, t);
+  return launch_overlapped(a.factor != nullptr ? adamw_kernel<P, G, k8, true, kCap> : adamw_kernel<P, G, k8, false, kCap>, grid,
+                           kThreads, 0, 0, stream, t);
 }
 
 // Tensors per launch: the table's 64 bytes a tensor must fit the 32,764 bytes of a kernel's

@@ -6,7 +6,9 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
+#include <memory>
 #include <mutex>
+#include <new>
 
 #include "vn.h"
 #include "vn_internal.h"
@@ -164,6 +166,84 @@ vn_status check_sizes(int64_t rows, int64_t in, int64_t out, vn_dtype dt) {
 // Few rows take any number of features; other kernels' coordinates have 32 bits.
 bool features_ok(int64_t rows, int64_t in, int64_t out) {
   return rows <= 8 || (in <= vn::kDenseMost && out <= vn::kDenseMost);
+}
+
+// The memory of a call over many tensors: whether anything that is written shares a byte with anything else.
+struct Span {
+  uintptr_t start, end;
+  bool written;
+};
+class Spans {
+ public:
+  explicit Spans(int64_t most) : s_(new (std::nothrow) Span[static_cast<size_t>(most)]) {}
+  bool ok() const { return s_ != nullptr; }
+  void add(const void* p, int64_t bytes, bool written) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    if (p != nullptr && bytes > 0) s_[count_++] = {a, a + static_cast<uintptr_t>(bytes), written};
+  }
+  bool clash() {
+    std::sort(s_.get(), s_.get() + count_, [](const Span& a, const Span& b) { return a.start < b.start; });
+    uintptr_t any = 0, written = 0;  // ends of those so far
+    for (int64_t i = 0; i < count_; ++i) {
+      const Span& s = s_[i];
+      if (s.start < (s.written ? any : written)) return true;
+      any = std::max(any, s.end);
+      if (s.written) written = std::max(written, s.end);
+    }
+    return false;
+  }
+
+ private:
+  std::unique_ptr<Span[]> s_;
+  int64_t count_ = 0;
+};
+class Pieces {
+ public:
+  explicit Pieces(int64_t count) : p_(new (std::nothrow) vn_gradient[static_cast<size_t>(count)]) {}
+  bool ok() const { return p_ != nullptr; }
+  vn_gradient& operator[](int64_t i) { return p_[i]; }
+  const vn_gradient* get() const { return p_.get(); }
+
+ private:
+  std::unique_ptr<vn_gradient[]> p_;
+};
+
+constexpr int64_t kMostTensors = int64_t{1} << 32;
+
+vn_status check_norm(int64_t n_tensors, double max_norm, const float* norm, const void* workspace, int64_t workspace_bytes) {
+  if (!(max_norm >= 0.0)) return VN_ERR_VALUE;
+  if (n_tensors > kMostTensors) return VN_ERR_OVERFLOW;
+  if (norm == nullptr) return VN_ERR_NULL;
+  if (!aligned(norm, 4) || !aligned(workspace, 256)) return VN_ERR_ALIGN;
+  if (workspace == nullptr || workspace_bytes < vn::clip_workspace(n_tensors)) return VN_ERR_WORKSPACE;
+  return VN_OK;
+}
+
+vn_status clip(const vn_gradient* tensors, int64_t n_tensors, vn_dtype dt, double max_norm, float* norm, void* workspace,
+               int64_t workspace_bytes, bool scale, void* stream) {
+  if (!dtype_ok(dt)) return VN_ERR_DTYPE;
+  if (n_tensors < 0) return VN_ERR_SHAPE;
+  const vn_status st = check_norm(n_tensors, max_norm, norm, workspace, workspace_bytes);
+  if (st != VN_OK) return st;
+  if (n_tensors > 0 && tensors == nullptr) return VN_ERR_NULL;
+  Spans spans(2 * n_tensors + 2);
+  if (!spans.ok()) return VN_ERR_OVERFLOW;
+  spans.add(norm, 4, true);
+  spans.add(workspace, vn::clip_workspace(n_tensors), true);
+  const int64_t size = static_cast<int64_t>(dtype_size(dt));
+  for (int64_t i = 0; i < n_tensors; ++i) {
+    const vn_gradient& t = tensors[i];
+    if (t.n < 0) return VN_ERR_SHAPE;
+    if (t.n > (int64_t{1} << 59)) return VN_ERR_OVERFLOW;
+    if (t.n == 0) continue;
+    if (t.grad == nullptr || (scale && t.out == nullptr)) return VN_ERR_NULL;
+    if (!aligned(t.grad, size) || (scale && !aligned(t.out, size))) return VN_ERR_ALIGN;
+    if (scale) spans.add(t.out, t.n * size, true);
+    if (!scale || t.out != t.grad) spans.add(t.grad, t.n * size, false);
+  }
+  if (spans.clash()) return VN_ERR_VALUE;
+  vn::ClipArgs c = {tensors, n_tensors, dt, max_norm, norm, scale, false, workspace};
+  return launched(vn::launch_clip(c, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -695,9 +775,8 @@ vn_status vn_layer_norm_backward(const void* grad, const void* x, vn_dtype dt, c
   return launched(vn::launch_layer_norm_backward(a, static_cast<cudaStream_t>(stream)));
 }
 
-vn_status vn_adamw(const vn_adamw_tensor* tensors, int64_t n_tensors, vn_dtype param_dt,
-                   vn_dtype grad_dt, int state_bits, double lr, double beta1, double beta2,
-                   double eps, int64_t step, int maximize, void* stream) {
+static vn_status check_adamw(const vn_adamw_tensor* tensors, int64_t n_tensors, vn_dtype param_dt, vn_dtype grad_dt,
+                             int state_bits, double lr, double beta1, double beta2, double eps, int64_t step) {
   if (!dtype_ok(param_dt) || !dtype_ok(grad_dt)) return VN_ERR_DTYPE;
   if (state_bits != 8 && state_bits != 32) return VN_ERR_VALUE;
   float f;
@@ -728,11 +807,76 @@ vn_status vn_adamw(const vn_adamw_tensor* tensors, int64_t n_tensors, vn_dtype p
     const Range ins[] = {{t.grad, t.n * gs}};
     if (!disjoint(outs, ins)) return VN_ERR_VALUE;
   }
+  return VN_OK;
+}
+
+static vn::AdamwArgs adamw_args(const vn_adamw_tensor* tensors, int64_t n_tensors, vn_dtype param_dt, vn_dtype grad_dt,
+                                int state_bits, double lr, double beta1, double beta2, double eps, int64_t step,
+                                int maximize) {
   vn::AdamwArgs a;
   a.tensors = tensors; a.count = n_tensors; a.param_dt = param_dt; a.grad_dt = grad_dt;
   a.state_bits = state_bits; a.lr = lr; a.beta1 = beta1; a.beta2 = beta2; a.eps = eps;
   a.step = step; a.maximize = maximize ? 1 : 0;
+  return a;
+}
+
+vn_status vn_adamw(const vn_adamw_tensor* tensors, int64_t n_tensors, vn_dtype param_dt,
+                   vn_dtype grad_dt, int state_bits, double lr, double beta1, double beta2,
+                   double eps, int64_t step, int maximize, void* stream) {
+  const vn_status st = check_adamw(tensors, n_tensors, param_dt, grad_dt, state_bits, lr, beta1, beta2, eps, step);
+  if (st != VN_OK || n_tensors == 0) return st;
+  return launched(vn::launch_adamw(adamw_args(tensors, n_tensors, param_dt, grad_dt, state_bits, lr, beta1, beta2, eps, step,
+                                              maximize),
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+vn_status vn_adamw_clipped(const vn_adamw_tensor* tensors, int64_t n_tensors, vn_dtype param_dt, vn_dtype grad_dt,
+                           int state_bits, double lr, double beta1, double beta2, double eps, int64_t step, int maximize,
+                           double max_norm, float* norm, void* workspace, int64_t workspace_bytes, void* stream) {
+  vn_status st = check_adamw(tensors, n_tensors, param_dt, grad_dt, state_bits, lr, beta1, beta2, eps, step);
+  if (st != VN_OK) return st;
+  st = check_norm(n_tensors, max_norm, norm, workspace, workspace_bytes);
+  if (st != VN_OK) return st;
+  Spans spans(6 * n_tensors + 2);
+  Pieces pieces(n_tensors);
+  if (!spans.ok() || !pieces.ok()) return VN_ERR_OVERFLOW;
+  const int64_t ps = static_cast<int64_t>(dtype_size(param_dt)), gs = static_cast<int64_t>(dtype_size(grad_dt));
+  spans.add(norm, 4, true);
+  spans.add(workspace, vn::clip_workspace(n_tensors), true);
+  for (int64_t i = 0; i < n_tensors; ++i) {
+    const vn_adamw_tensor& t = tensors[i];
+    pieces[i] = {t.grad, nullptr, t.n};
+    spans.add(t.grad, t.n * gs, false);
+    spans.add(t.param, t.n * ps, true);
+    const int64_t sb = t.n * (state_bits == 8 ? 1 : 4);
+    spans.add(t.exp_avg, sb, true);
+    spans.add(t.exp_avg_sq, sb, true);
+    if (state_bits == 8) {
+      spans.add(t.exp_avg_scale, (t.n + 255) / 256 * 4, true);
+      spans.add(t.exp_avg_sq_scale, (t.n + 255) / 256 * 4, true);
+    }
+  }
+  if (spans.clash()) return VN_ERR_VALUE;
+  vn::ClipArgs c = {pieces.get(), n_tensors, grad_dt, max_norm, norm, false, true, workspace};
+  const cudaError_t err = vn::launch_clip(c, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess || n_tensors == 0) return launched(err);
+  vn::AdamwArgs a = adamw_args(tensors, n_tensors, param_dt, grad_dt, state_bits, lr, beta1, beta2, eps, step, maximize);
+  a.factor = static_cast<const float*>(workspace);
   return launched(vn::launch_adamw(a, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t vn_gradient_norm_workspace(int64_t n_tensors) {
+  return n_tensors < 0 || n_tensors > kMostTensors ? -1 : vn::clip_workspace(n_tensors);
+}
+
+vn_status vn_gradient_norm(const vn_gradient* tensors, int64_t n_tensors, vn_dtype dt, float* norm, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  return clip(tensors, n_tensors, dt, HUGE_VAL, norm, workspace, workspace_bytes, false, stream);
+}
+
+vn_status vn_clip_gradients(const vn_gradient* tensors, int64_t n_tensors, vn_dtype dt, double max_norm, float* norm,
+                            void* workspace, int64_t workspace_bytes, void* stream) {
+  return clip(tensors, n_tensors, dt, max_norm, norm, workspace, workspace_bytes, true, stream);
 }
 
 vn_status vn_adamw_moments(const void* exp_avg, const void* exp_avg_sq, const float* exp_avg_scale,

@@ -1,0 +1,296 @@
+// vn_clip.cu -- the norm of a gradient over many tensors, and the gradient scaled to a bound of it:
+//
+//   norm = sqrt(sum over all tensors of g^2),   factor = norm <= bound ? 1 : bound / norm,   out = g factor
+//
+// The norm reads every element once and the scaling reads and writes it, so the bound is memory (the
+// second reading comes from L2 where the gradient fits there). Sums: eight squares in fp32, those sums
+// in pairs of fp32 that carry each other's rounding (exact but for the last bits of the second), a thread's
+// pair, a CTA's threads and the CTAs in 64 bits, in a fixed order: results do not depend on the order
+// of CTAs, and the norm is the exact one rounded once but where that falls within 2^-36 of a border.
+// Eight squares whose sum leaves what fp32 holds to full precision are taken in 64 bits, so the norm is
+// right over the whole range of the types (fp64 has 1/64 of fp32's rate here: no other element sees it).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "vn_internal.h"
+#include "vn_launch.cuh"
+#include "vn_pair.cuh"
+
+namespace vn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kGroup = 8;                      // elements that are squared and summed in fp32
+constexpr int kLoads = 4;                      // 16-byte loads of a thread in flight
+template <typename T>
+constexpr int kChunkOf = kThreads * kLoads * 16 / static_cast<int>(sizeof(T));  // elements of a CTA's turn
+constexpr int kPerSm = 4;                      // CTAs an SM
+constexpr int kSmall = 16, kLarge = 896;       // tensors of a launch
+
+struct Piece {
+  const void* g;
+  void* out;
+  int64_t n;
+  int64_t first;  // first chunk of this tensor within the launch
+};
+template <int kCap>
+struct Table {
+  int count;
+  int64_t chunks;
+  Piece e[kCap];
+};
+static_assert(sizeof(Table<kLarge>) + 64 <= 32764, "kernel parameters");
+
+__device__ __forceinline__ float value(float x) { return x; }
+__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// A sum of squares: a pair of fp32, and what fp32 cannot hold.
+struct Sum {
+  float hi = 0.f, lo = 0.f;
+  double wide = 0.0;
+  __device__ __forceinline__ void add(const float (&x)[kGroup]) {
+    F2 s = mul2(f2(x[0], x[1]), f2(x[0], x[1]));
+#pragma unroll
+    for (int q = 2; q < kGroup; q += 2) s = fma2(f2(x[q], x[q + 1]), f2(x[q], x[q + 1]), s);
+    const float v = sum_of(s);
+    // Below 2^-90 the squares that fp32 cannot hold would count (they are below 2^-126); from 2^100 on the pair
+    // could pass its largest value; a NaN is neither.
+    if (v >= 0x1p-90f && v < 0x1p100f) {
+      const float t = __fadd_rn(hi, v), b = __fsub_rn(t, hi);
+      lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(v, b)));
+      hi = t;
+    } else {
+      add_wide(x);
+    }
+  }
+  __device__ __noinline__ void add_wide(const float (&x)[kGroup]) {
+    for (int q = 0; q < kGroup; ++q)
+      if (x[q] != 0.f) wide += static_cast<double>(x[q]) * static_cast<double>(x[q]);
+  }
+  __device__ __forceinline__ double total() const { return static_cast<double>(hi) + static_cast<double>(lo) + wide; }
+};
+
+// The sum over a CTA's threads, in every one of them.
+__device__ __forceinline__ double cta_sum(double v) {
+  __shared__ double s[kThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double r = s[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 32; ++w) r += s[w];
+  return r;
+}
+
+// What a launch reads per thread and 16 bytes.
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& raw, float* x) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      x[2 * q] = __uint_as_float(w[q] << 16);
+      x[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = __uint_as_float(w[q]);
+  }
+}
+
+template <int kCap>
+__device__ __forceinline__ const Piece& piece_of(const Table<kCap>& t, int64_t chunk) {
+  int lo = 0, hi = t.count;  // the last piece whose first chunk is not beyond this one
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (t.e[mid].first <= chunk) lo = mid; else hi = mid;
+  }
+  return t.e[lo];
+}
+
+// A chunk's elements one at a time, 256 apart: any alignment, and the last chunk of a tensor.
+template <typename T, typename F>
+__device__ __forceinline__ void each_single(const T* g, int64_t left, F f) {
+  constexpr int kChunk = kChunkOf<T>;
+  const int end = static_cast<int>(min(static_cast<int64_t>(kChunk), left));
+  for (int i = threadIdx.x; i < end; i += kThreads * kGroup) {
+    float x[kGroup];
+#pragma unroll
+    for (int q = 0; q < kGroup; ++q) x[q] = i + q * kThreads < end ? value(fetch(g + i + q * kThreads)) : 0.f;
+    f(i, end, x);
+  }
+}
+
+template <typename T, int kCap>
+__global__ void __launch_bounds__(kThreads) square_kernel(const __grid_constant__ Table<kCap> t, double* parts) {
+  let_next();
+  after_previous();
+  constexpr int kChunk = kChunkOf<T>;
+  Sum sum;
+  for (int64_t chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
+    const Piece& e = piece_of(t, chunk);
+    const int64_t base = (chunk - e.first) * kChunk;
+    const T* g = static_cast<const T*>(e.g) + base;
+    if (base + kChunk <= e.n && reinterpret_cast<uintptr_t>(g) % 16 == 0) {
+      uint4 raw[kLoads];
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) raw[u] = fetch(reinterpret_cast<const uint4*>(g) + u * kThreads + threadIdx.x);
+      constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+      for (int u = 0; u < kLoads; u += kGroup / kPer) {
+        float x[kGroup];
+#pragma unroll
+        for (int k = 0; k < kGroup / kPer; ++k) unpack<T>(raw[u + k], x + k * kPer);
+        sum.add(x);
+      }
+    } else {
+      each_single(g, e.n - base, [&](int, int, const float(&x)[kGroup]) { sum.add(x); });
+    }
+  }
+  const double total = cta_sum(sum.total());
+  if (threadIdx.x == 0) parts[blockIdx.x] = total;
+}
+
+// The parts of all launches to the norm and the factor: one CTA.
+__global__ void __launch_bounds__(kThreads) join_kernel(const double* parts, int64_t count, double bound, float* norm, float* factor) {
+  let_next();
+  after_previous();
+  double v = 0.0;
+  for (int64_t i = threadIdx.x; i < count; i += kThreads) v += fetch(parts + i);
+  v = cta_sum(v);
+  if (threadIdx.x != 0) return;
+  const double n = sqrt(v);
+  if (norm != nullptr) *norm = static_cast<float>(n);
+  if (factor != nullptr) *factor = n <= bound ? 1.f : static_cast<float>(bound / n);
+}
+
+template <typename T, int kCap>
+__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<kCap> t, const float* factor) {
+  let_next();
+  after_previous();
+  constexpr int kChunk = kChunkOf<T>;
+  const float f = fetch(factor);
+  // From the last chunk to the first: what the norm's launch read last is still in L2.
+  for (int64_t chunk = t.chunks - 1 - blockIdx.x; chunk >= 0; chunk -= gridDim.x) {
+    const Piece& e = piece_of(t, chunk);
+    if (f == 1.f && e.out == e.g) continue;
+    const int64_t base = (chunk - e.first) * kChunk;
+    const T* g = static_cast<const T*>(e.g) + base;
+    T* o = static_cast<T*>(e.out) + base;
+    if (base + kChunk <= e.n && (reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(o)) % 16 == 0) {
+      uint4 raw[kLoads];
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) raw[u] = fetch(reinterpret_cast<const uint4*>(g) + u * kThreads + threadIdx.x);
+      constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        float x[kPer];
+        unpack<T>(raw[u], x);
+        uint32_t w[4];
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__fmul_rn(x[2 * q], f), __fmul_rn(x[2 * q + 1], f));
+            w[q] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) w[q] = __float_as_uint(__fmul_rn(x[q], f));
+        }
+        __stcs(reinterpret_cast<uint4*>(o) + u * kThreads + threadIdx.x, make_uint4(w[0], w[1], w[2], w[3]));
+      }
+    } else {
+      each_single(g, e.n - base, [&](int i, int end, const float(&x)[kGroup]) {
+#pragma unroll
+        for (int q = 0; q < kGroup; ++q)
+          if (i + q * kThreads < end) put(o + i + q * kThreads, __fmul_rn(x[q], f));
+      });
+    }
+  }
+}
+
+template <typename T, int kCap>
+void fill(const ClipArgs& a, int64_t from, int64_t count, Table<kCap>* t) {
+  t->count = 0;
+  t->chunks = 0;
+  for (int64_t i = from; i < from + count; ++i) {
+    const vn_gradient& x = a.tensors[i];
+    if (x.n == 0) continue;
+    Piece& e = t->e[t->count++];
+    e.g = x.grad;
+    e.out = x.out;
+    e.n = x.n;
+    e.first = t->chunks;
+    t->chunks += (x.n + kChunkOf<T> - 1) / kChunkOf<T>;
+  }
+}
+
+// Calls f with the table of every launch's tensors.
+template <typename T, typename F>
+cudaError_t each_table(const ClipArgs& a, F f) {
+  for (int64_t from = 0; from < a.count; from += kLarge) {
+    const int64_t count = std::min<int64_t>(kLarge, a.count - from);
+    cudaError_t err;
+    if (count <= kSmall) {
+      Table<kSmall> t;
+      fill<T>(a, from, count, &t);
+      err = f(t);
+    } else {
+      Table<kLarge> t;
+      fill<T>(a, from, count, &t);
+      err = f(t);
+    }
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+template <typename T, int kCap>
+cudaError_t launch_square(const Table<kCap>& t, int64_t grid, double* parts, cudaStream_t stream) {
+  return launch_overlapped(square_kernel<T, kCap>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream, t, parts);
+}
+template <typename T, int kCap>
+cudaError_t launch_scale(const Table<kCap>& t, int64_t grid, const float* factor, cudaStream_t stream) {
+  return launch_overlapped(scale_kernel<T, kCap>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream, t, factor);
+}
+
+template <typename T>
+cudaError_t run(const ClipArgs& a, cudaStream_t stream) {
+  DeviceInfo dev;
+  cudaError_t err = device_info(&dev);
+  if (err != cudaSuccess) return err;
+  const int64_t most = std::min<int64_t>(static_cast<int64_t>(dev.sm_count) * kPerSm, kClipParts);
+  float* const factor = static_cast<float*>(a.workspace);
+  double* const parts = static_cast<double*>(a.workspace) + 1;  // the factor's place comes first
+  int64_t done = 0;
+  err = each_table<T>(a, [&](const auto& t) {
+    const int64_t grid = std::min(t.chunks, most);
+    if (grid == 0) return cudaSuccess;
+    double* const to = parts + done;
+    done += grid;
+    return launch_square<T>(t, grid, to, stream);
+  });
+  if (err != cudaSuccess) return err;
+  err = launch_overlapped(join_kernel, dim3(1), kThreads, 0, 0, stream, static_cast<const double*>(parts), done, a.bound,
+                          a.norm, a.scale || a.factor_only ? factor : nullptr);
+  if (err != cudaSuccess || !a.scale) return err;
+  return each_table<T>(a, [&](const auto& t) {
+    const int64_t grid = std::min(t.chunks, most);
+    return grid == 0 ? cudaSuccess : launch_scale<T>(t, grid, factor, stream);
+  });
+}
+
+}  // namespace
+
+int64_t clip_workspace(int64_t count) { return 8 * (1 + (count + kLarge - 1) / kLarge * kClipParts); }
+
+cudaError_t launch_clip(const ClipArgs& a, cudaStream_t stream) {
+  return a.dt == VN_BF16 ? run<__nv_bfloat16>(a, stream) : run<float>(a, stream);
+}
+
+}  // namespace vn

@@ -187,6 +187,21 @@ cudaError_t launch_layer_norm_backward(const NormGradArgs& a, cudaStream_t strea
 cudaError_t launch_column_sum(const float* part, int64_t parts, int64_t width, int64_t n, void* o1,
                               void* o2, vn_dtype dt, cudaStream_t stream);
 
+// The norm of a gradient, and what is done with it.
+constexpr int kClipParts = 1216;  // partial sums of a launch at most
+struct ClipArgs {
+  const vn_gradient* tensors;  // host
+  int64_t count;
+  vn_dtype dt;
+  double bound;
+  float* norm;       // may be null
+  bool scale;        // write each tensor's out
+  bool factor_only;  // leave the factor as the workspace's first float
+  void* workspace;   // clip_workspace(count) bytes
+};
+int64_t clip_workspace(int64_t count);
+cudaError_t launch_clip(const ClipArgs& a, cudaStream_t stream);
+
 struct AdamwArgs {
   const vn_adamw_tensor* tensors;  // host
   int64_t count;
@@ -195,6 +210,7 @@ struct AdamwArgs {
   double lr, beta1, beta2, eps;
   int64_t step;
   int maximize;
+  const float* factor = nullptr;  // device: what gradients are multiplied by, 1 if null
 };
 cudaError_t launch_adamw(const AdamwArgs& a, cudaStream_t stream);
 cudaError_t launch_adamw_moments(const void* exp_avg, const void* exp_avg_sq, const float* exp_avg_scale,

@@ -324,11 +324,81 @@ PyObject* layer_norm_backward(PyObject* const* a, Py_ssize_t count) {
   return tuple(gx, gw, gb);
 }
 
-// adamw(params, grads, table, state_bits, lr, beta1, beta2, eps, step, maximize): one step of the
+// The tensors of a gradient: one, or a list of them, of one dtype on one device.
+struct Gradient {
+  // written: they are written over, so they have to be contiguous; else those that are not are copied.
+  Gradient(PyObject* o, const char* name, bool written) {
+    const bool one = THPVariable_Check(o);
+    if (!one && (!PyList_Check(o) || PyList_GET_SIZE(o) == 0))
+      raise(PyExc_TypeError, std::string(name) + " must be a tensor or a sequence of at least one tensor");
+    const Py_ssize_t n = one ? 1 : PyList_GET_SIZE(o);
+    tensors.reserve(static_cast<size_t>(n));
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      PyObject* item = one ? o : PyList_GET_ITEM(o, i);
+      const std::string which = one ? std::string(name) : std::string(name) + "[" + std::to_string(i) + "]";
+      if (written && (!THPVariable_Check(item) || !THPVariable_Unpack(item).is_cuda() || !THPVariable_Unpack(item).is_contiguous()))
+        raise(PyExc_ValueError, which + " must be a contiguous CUDA tensor (written over)");
+      tensors.push_back(input(item, which.c_str()));
+      const at::Tensor& t = tensors.back();
+      dt = dtype_of(t, which.c_str());
+      if (t.scalar_type() != tensors[0].scalar_type()) raise(PyExc_TypeError, std::string(name) + " must have one dtype");
+      beside(t, tensors[0]);
+    }
+  }
+  std::vector<at::Tensor> tensors;
+  vn_dtype dt;
+};
+
+// clip_gradients(grads, max_norm, out, norm) -> norm. max_norm None: the norm alone. out None: in place.
+PyObject* clip_gradients(PyObject* const* a, Py_ssize_t count) {
+  counted(count, 4, "clip_gradients");
+  const bool scale = a[1] != Py_None, in_place = scale && a[2] == Py_None;
+  const double max_norm = scale ? real(a[1]) : 0.0;
+  const Gradient g(a[0], "grads", in_place);
+  std::optional<Gradient> to;
+  if (scale && !in_place) {
+    to.emplace(a[2], "out", true);
+    if (to->tensors.size() != g.tensors.size())
+      raise(PyExc_ValueError, std::to_string(g.tensors.size()) + " gradients but " + std::to_string(to->tensors.size()) + " in out");
+    for (size_t i = 0; i < g.tensors.size(); ++i)
+      like(to->tensors[i], ("out[" + std::to_string(i) + "]").c_str(), g.tensors[i].sizes(), g.tensors[i]);
+  }
+  const at::Tensor& first = g.tensors[0];
+  const int64_t n = static_cast<int64_t>(g.tensors.size());
+  std::vector<vn_gradient> table(g.tensors.size());
+  for (size_t i = 0; i < table.size(); ++i)
+    table[i] = {at_(g.tensors[i]), to ? at_(to->tensors[i]) : at_(g.tensors[i]), g.tensors[i].numel()};
+  at::Tensor norm;
+  if (a[3] == Py_None) {
+    norm = empty({}, at::kFloat, first);
+  } else {
+    if (!THPVariable_Check(a[3]) || THPVariable_Unpack(a[3]).dim() != 0 || THPVariable_Unpack(a[3]).scalar_type() != at::kFloat ||
+        THPVariable_Unpack(a[3]).device() != first.device())
+      raise(PyExc_ValueError, "out must be a torch.float32 tensor of shape () on " + text_of(first.device()));
+    norm = THPVariable_Unpack(a[3]);
+    changed(norm);
+  }
+  const int64_t need = vn_gradient_norm_workspace(n);
+  const auto ws = workspace(need, first);
+  {
+    const On on(first);
+    if (scale)
+      check(vn_clip_gradients(table.data(), n, g.dt, max_norm, static_cast<float*>(at_(norm)), at_(ws), need, on.stream),
+            "vn_clip_gradients");
+    else
+      check(vn_gradient_norm(table.data(), n, g.dt, static_cast<float*>(at_(norm)), at_(ws), need, on.stream), "vn_gradient_norm");
+  }
+  if (scale)
+    for (const at::Tensor& t : to ? to->tensors : g.tensors) changed(t);
+  return wrap(norm);
+}
+
+// adamw(params, grads, table, state_bits, lr, beta1, beta2, eps, step, maximize, max_norm): one step of the
 // tensors in the list `params`. grads: a list of as many, or one flat tensor. table: the
-// address of a row of vn_adamw_tensor for each, in which only param and grad are set here.
+// address of a row of vn_adamw_tensor for each, in which only param and grad are set here. max_norm: None,
+// or a bound of the gradients' norm, which is then returned.
 PyObject* adamw(PyObject* const* a, Py_ssize_t count) {
-  counted(count, 10, "adamw");
+  counted(count, 11, "adamw");
   PyObject* params = a[0];
   const Py_ssize_t n = PyList_GET_SIZE(params);
   auto* table = static_cast<vn_adamw_tensor*>(PyLong_AsVoidPtr(a[2]));
@@ -382,17 +452,28 @@ PyObject* adamw(PyObject* const* a, Py_ssize_t count) {
   const double lr = real(a[4]), beta1 = real(a[5]), beta2 = real(a[6]), eps = real(a[7]);
   const int64_t step = whole(a[8]);
   const int maximize = truth(a[9]);
+  const bool clip = a[10] != Py_None;
+  const double max_norm = clip ? real(a[10]) : 0.0;
+  std::optional<at::Tensor> norm, ws;
+  const int64_t need = clip ? vn_gradient_norm_workspace(n) : 0;
   {
     const On on(first);
     if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
       raise(PyExc_RuntimeError, "AdamW.step cannot be captured in a graph: its step number and learning rate would be "
                                 "those of the capture in every replay");
-    check(vn_adamw(table, n, dtype_of(first, "params"), kind == at::kBFloat16 ? VN_BF16 : VN_F32, bits, lr, beta1, beta2,
-                   eps, step, maximize, on.stream),
-          "vn_adamw");
+    const vn_dtype dt = dtype_of(first, "params"), gdt = kind == at::kBFloat16 ? VN_BF16 : VN_F32;
+    if (clip) {
+      norm = empty({}, at::kFloat, first);
+      ws = workspace(need, first);
+      check(vn_adamw_clipped(table, n, dt, gdt, bits, lr, beta1, beta2, eps, step, maximize, max_norm,
+                             static_cast<float*>(at_(norm)), at_(ws), need, on.stream),
+            "vn_adamw_clipped");
+    } else {
+      check(vn_adamw(table, n, dt, gdt, bits, lr, beta1, beta2, eps, step, maximize, on.stream), "vn_adamw");
+    }
   }
   for (Py_ssize_t i = 0; i < n; ++i) changed(THPVariable_Unpack(PyList_GET_ITEM(params, i)));
-  Py_RETURN_NONE;
+  return wrap(norm);
 }
 
 // adamw_moments(m, v, m_scale, v_scale) -> (m, v) in fp32
@@ -428,6 +509,7 @@ PyMethodDef method(const char* name) {
 PyMethodDef g_methods[] = {
     method<linear>("linear"),         method<linear_backward>("linear_backward"),
     method<layer_norm>("layer_norm"), method<layer_norm_backward>("layer_norm_backward"),
+    method<clip_gradients>("clip_gradients"),
     method<adamw>("adamw"),           method<adamw_moments>("adamw_moments"),
     {nullptr, nullptr, 0, nullptr},
 };

@@ -109,6 +109,32 @@ def layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     return (_binding or _native()).layer_norm_backward(grad, x, mean, rstd, weight)
 
 
+Gradients = Union[torch.Tensor, Sequence[torch.Tensor]]
+
+
+def _listed(tensors: Gradients) -> Union[torch.Tensor, list]:
+    return tensors if isinstance(tensors, (list, torch.Tensor)) else list(tensors)
+
+
+def gradient_norm(grads: Gradients, *, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The norm over all elements of ``grads``, a tensor or a sequence of them (float32 or bfloat16, one
+    dtype), as a float32 tensor of shape () (``vn_gradient_norm``): the exact norm rounded once, but for
+    a last bit next to a border."""
+    return (_binding or _native()).clip_gradients(_listed(grads), None, None, out)
+
+
+def clip_gradients(grads: Gradients, max_norm: float, *, out: Optional[Gradients] = None) -> torch.Tensor:
+    """Scale ``grads`` to a norm of at most ``max_norm``, and return the norm that they had
+    (``vn_clip_gradients``): each element times max_norm / norm where norm > max_norm, rounded once.
+
+    ``grads``: a tensor or a sequence of them, contiguous, of one dtype, written over in place, or with
+    ``out``, tensors like them that take the result, only read. An infinite norm makes the factor 0 (NaN where the
+    gradient is infinite), a NaN makes it NaN. Nothing synchronises: the norm stays on the device."""
+    if max_norm is None:
+        raise TypeError("max_norm must be a number")
+    return (_binding or _native()).clip_gradients(_listed(grads), max_norm, None if out is None else _listed(out), None)
+
+
 class AdamW:
     """AdamW over many tensors, one launch a step (``vn_adamw``).
 
@@ -224,16 +250,20 @@ class AdamW:
         """The moments' tensors (a new dict of them: their addresses are the handle's)."""
         return dict(self._tensors)
 
-    def step(self, grads: Union[torch.Tensor, Sequence[torch.Tensor]], lr: Optional[float] = None) -> None:
+    def step(self, grads: Gradients, lr: Optional[float] = None, *, max_norm: Optional[float] = None) -> Optional[torch.Tensor]:
         """One step of every tensor. ``grads``: a gradient for each tensor, or one flat tensor with
         all of them one after another (as ``virtual_flat_gradient`` lays them out); float32 or
         bfloat16. ``lr`` replaces the learning rate for this step. A step cannot be captured in a graph
-        (RuntimeError): replays would repeat the step number and learning rate of the capture."""
-        if not isinstance(grads, (list, torch.Tensor)):
-            grads = list(grads)
-        (_binding or _native()).adamw(self._params, grads, self._address, self.state_bits, self.lr if lr is None else lr,
-                                      self.betas[0], self.betas[1], self.eps, self.steps + 1, self.maximize)
+        (RuntimeError): replays would repeat the step number and learning rate of the capture.
+
+        With ``max_norm`` the step takes the gradients scaled to a norm of at most that, as
+        ``clip_gradients`` would leave them but in float32 (``vn_adamw_clipped``; the gradients themselves stay
+        as they are), and returns the norm that they had, a float32 tensor of shape ()."""
+        norm = (_binding or _native()).adamw(self._params, _listed(grads), self._address, self.state_bits,
+                                             self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps,
+                                             self.steps + 1, self.maximize, max_norm)
         self.steps += 1
+        return norm
 
     def moments(self) -> Tuple[torch.Tensor, torch.Tensor]:
         """The moments (m, v) as flat float32 tensors in ``offsets``' layout: the state itself with
@@ -244,4 +274,4 @@ class AdamW:
         return (_binding or _native()).adamw_moments(s["m"], s["v"], s["m_scale"], s["v_scale"])
 
 
-__all__ = ["AdamW", "layer_norm", "layer_norm_backward", "linear", "linear_backward"]
+__all__ = ["AdamW", "clip_gradients", "gradient_norm", "layer_norm", "layer_norm_backward", "linear", "linear_backward"]
