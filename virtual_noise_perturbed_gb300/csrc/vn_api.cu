@@ -242,7 +242,7 @@ vn_status clip(const vn_gradient* tensors, int64_t n_tensors, vn_dtype dt, doubl
     if (!scale || t.out != t.grad) spans.add(t.grad, t.n * size, false);
   }
   if (spans.clash()) return VN_ERR_VALUE;
-  vn::ClipArgs c = {tensors, n_tensors, dt, max_norm, norm, scale, false, workspace};
+  vn::ClipArgs c = {tensors, n_tensors, dt, max_norm, norm, scale, workspace};
   return launched(vn::launch_clip(c, static_cast<cudaStream_t>(stream)));
 }
 
@@ -857,7 +857,7 @@ vn_status vn_adamw_clipped(const vn_adamw_tensor* tensors, int64_t n_tensors, vn
     }
   }
   if (spans.clash()) return VN_ERR_VALUE;
-  vn::ClipArgs c = {pieces.get(), n_tensors, grad_dt, max_norm, norm, false, true, workspace};
+  vn::ClipArgs c = {pieces.get(), n_tensors, grad_dt, max_norm, norm, false, workspace};
   const cudaError_t err = vn::launch_clip(c, static_cast<cudaStream_t>(stream));
   if (err != cudaSuccess || n_tensors == 0) return launched(err);
   vn::AdamwArgs a = adamw_args(tensors, n_tensors, param_dt, grad_dt, state_bits, lr, beta1, beta2, eps, step, maximize);

@@ -194,10 +194,9 @@ struct ClipArgs {
   int64_t count;
   vn_dtype dt;
   double bound;
-  float* norm;       // may be null
-  bool scale;        // write each tensor's out
-  bool factor_only;  // leave the factor as the workspace's first float
-  void* workspace;   // clip_workspace(count) bytes
+  float* norm;
+  bool scale;       // write each tensor's out
+  void* workspace;  // clip_workspace(count) bytes; the factor is left as its first float
 };
 int64_t clip_workspace(int64_t count);
 cudaError_t launch_clip(const ClipArgs& a, cudaStream_t stream);

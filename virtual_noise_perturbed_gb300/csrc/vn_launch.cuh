@@ -14,6 +14,8 @@
 
 #include <cuda_runtime.h>
 
+#include "vn_smem.h"
+
 namespace vn {
 
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -45,6 +47,18 @@ cudaError_t launch_overlapped(void (*fn)(KArgs...), dim3 grid, int threads, int 
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, fn, static_cast<KArgs>(args)...);
+}
+
+// Lets `fn` run in clusters of more than the portable 8 CTAs on the current device (once a device: done).
+inline cudaError_t allow_wide_clusters(const void* fn, SmemRecord& done) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_acquire) != 0) return cudaSuccess;
+  err = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (err == cudaSuccess) done[dev].store(1, std::memory_order_release);
+  return err;
 }
 
 }  // namespace vn
