@@ -481,6 +481,27 @@ vn_status vn_adamw_clipped(const vn_adamw_tensor* tensors, int64_t n_tensors, vn
                            double eps, int64_t step, int maximize, double max_norm, float* norm,
                            void* workspace, int64_t workspace_bytes, void* stream);
 
+/*
+ * vn_sample -- an index for each row of logits [rows, n] of dt, drawn with the row's random number u [rows]:
+ *     w_i = exp((x_i - max x) / temperature);  order: x descending, of equal ones (-0 = +0) the lower index first
+ *     kept: the first top_k of the order; of those the ones before which less than top_p times their sum lies
+ *           (the first one always); of those the ones with w_i >= min_p
+ *     index = the smallest i, in index order, with  sum_{j <= i, kept} w_j > u S,   S = sum_kept w
+ *     logprob = ln(w_index / S)                                       (fp32 [rows], or NULL)
+ * index [rows] int64. The index is float64's but where u S, or a border of a filter, lies within about
+ * 1e-11 of it: weights are whole numbers in units of 2^-42, and weights below half a unit are never drawn.
+ * temperature <= 0 takes the largest logit; top_k <= 0 or >= n, top_p >= 1 and min_p <= 0 filter nothing;
+ * top_p <= 0 and min_p >= 1 keep the first and the largest ones; u below 0 is 0, u >= 1 the last index of the sum.
+ * A logit of -infinity is never drawn, infinite ones share all of the probability. A row with a NaN, without any
+ * logit above -infinity, or with a NaN among its parameters gets index -1 and logprob NaN.
+ * temperatures, top_ps and min_ps (fp32 [rows]) and top_ks (int64 [rows]) replace the scalar for each row, or are
+ * NULL. The scalars are finite (VN_ERR_VALUE). 1 <= n <= 524288 (VN_ERR_SHAPE).
+ */
+vn_status vn_sample(const void* logits, vn_dtype dt, int64_t rows, int64_t n, const float* u,
+                    double temperature, const float* temperatures, int64_t top_k,
+                    const int64_t* top_ks, double top_p, const float* top_ps, double min_p,
+                    const float* min_ps, int64_t* index, float* logprob, void* stream);
+
 /* Synchronises `stream`, then reads and clears the current device's status
  * word: VN_ERR_TIMEOUT if a kernel of this library recorded an expired wait
  * since the last call, VN_ERR_CUDA if synchronisation failed, else VN_OK. */

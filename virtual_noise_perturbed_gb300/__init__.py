@@ -35,11 +35,12 @@ from .network import (  # noqa: F401
     layer_norm_backward,
     linear,
     linear_backward,
+    sample,
 )
 
 __all__ = [
     "AdamW", "VNError", "centered_ranks", "clip_gradients", "compute_offsets", "device_status", "es_update", "gradient_norm", "gradient_update", "hash_probe", "layer_norm",
-    "layer_norm_backward", "linear", "linear_backward", "noise_dump", "perturbed_linear_path",
+    "layer_norm_backward", "linear", "linear_backward", "noise_dump", "perturbed_linear_path", "sample",
     "virtual_bias_gradient", "virtual_flat_gradient", "virtual_perturbed_linear", "virtual_perturbed_mlp",
     "virtual_reduce_metric",
     "virtual_weight_gradient",

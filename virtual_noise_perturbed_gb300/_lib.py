@@ -72,6 +72,7 @@ SIGNATURES = {
     "vn_clip_gradients": (_I, [_P, _I64, _I, _D, _P, _P, _I64, _P]),
     "vn_gradient_norm_workspace": (_I64, [_I64]),
     "vn_adamw_clipped": (_I, [_P, _I64, _I, _I, _I, _D, _D, _D, _D, _I64, _I, _D, _P, _P, _I64, _P]),
+    "vn_sample": (_I, [_P, _I, _I64, _I64, _P, _D, _P, _I64, _P, _D, _P, _D, _P, _P, _P, _P]),
     "vn_adamw_moments": (_I, [_P, _P, _P, _P, _I64, _P, _P, _P]),
 }
 

@@ -898,6 +898,30 @@ vn_status vn_adamw_moments(const void* exp_avg, const void* exp_avg_sq, const fl
                                            static_cast<cudaStream_t>(stream)));
 }
 
+vn_status vn_sample(const void* logits, vn_dtype dt, int64_t rows, int64_t n, const float* u, double temperature,
+                    const float* temperatures, int64_t top_k, const int64_t* top_ks, double top_p, const float* top_ps,
+                    double min_p, const float* min_ps, int64_t* index, float* logprob, void* stream) {
+  if (!dtype_ok(dt)) return VN_ERR_DTYPE;
+  if (!std::isfinite(temperature) || !std::isfinite(top_p) || !std::isfinite(min_p)) return VN_ERR_VALUE;
+  if (rows < 0 || n < 1 || n > vn::kSampleMost) return VN_ERR_SHAPE;
+  int64_t xb, r8;
+  if (!bytes_of(rows, n, dt, &xb) || !mul(rows, 8, &r8)) return VN_ERR_OVERFLOW;
+  if (rows == 0) return VN_OK;
+  if (logits == nullptr || u == nullptr || index == nullptr) return VN_ERR_NULL;
+  if (!aligned(logits, dtype_size(dt)) || !aligned(u, 4) || !aligned(temperatures, 4) || !aligned(top_ks, 8) ||
+      !aligned(top_ps, 4) || !aligned(min_ps, 4) || !aligned(index, 8) || !aligned(logprob, 4))
+    return VN_ERR_ALIGN;
+  const Range outs[] = {{index, r8}, {logprob, r8 / 2}};
+  const Range ins[] = {{logits, xb}, {u, r8 / 2}, {temperatures, r8 / 2}, {top_ks, r8}, {top_ps, r8 / 2}, {min_ps, r8 / 2}};
+  if (!disjoint(outs, ins)) return VN_ERR_VALUE;
+  vn::SampleArgs a;
+  a.logits = logits; a.dt = dt; a.rows = rows; a.n = n; a.u = u;
+  a.temperature = temperature; a.top_p = top_p; a.min_p = min_p; a.top_k = top_k;
+  a.temperatures = temperatures; a.top_ks = top_ks; a.top_ps = top_ps; a.min_ps = min_ps;
+  a.index = index; a.logprob = logprob;
+  return launched(vn::launch_sample(a, static_cast<cudaStream_t>(stream)));
+}
+
 vn_status vn_device_status(void* stream) {
   cudaError_t err = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) return cuda_failure(err);

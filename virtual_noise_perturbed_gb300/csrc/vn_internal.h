@@ -216,6 +216,24 @@ cudaError_t launch_adamw_moments(const void* exp_avg, const void* exp_avg_sq, co
                                  const float* exp_avg_sq_scale, int64_t n, float* m, float* v,
                                  cudaStream_t stream);
 
+// An index for each row of logits.
+constexpr int64_t kSampleMost = int64_t{1} << 19;  // logits of a row: what a cluster of 16 CTAs holds in shared memory
+struct SampleArgs {
+  const void* logits;
+  vn_dtype dt;
+  int64_t rows, n;
+  const float* u;
+  double temperature, top_p, min_p;
+  int64_t top_k;
+  const float* temperatures;  // of each row, in the scalar's place; may be null, and the other three
+  const int64_t* top_ks;
+  const float* top_ps;
+  const float* min_ps;
+  int64_t* index;
+  float* logprob;  // may be null
+};
+cudaError_t launch_sample(const SampleArgs& a, cudaStream_t stream);
+
 // The current device's status word, which every bounded wait that runs out sets.
 cudaError_t device_status_word(unsigned int** word);
 // Reads and clears the device status word of the bounded-wait kernels (0 = fine).

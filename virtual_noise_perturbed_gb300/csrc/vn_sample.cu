@@ -1,0 +1,845 @@
+// vn_sample.cu -- an index for each row of logits, drawn with a given random number:
+//
+//   w_i = exp((x_i - max x) / T);   order: x descending, index ascending
+//   kept = the first top_k of the order, of those the ones before which less than top_p of the sum lies,
+//          and w_i >= min_p                                      (all three are prefixes of the order)
+//   index = the smallest i, in index order, with  sum_{j <= i, kept} w_j > u S,  S the sum of all kept w
+//
+// Which index it is hangs on sums next to a border, so a weight is a whole number: w in units of 2^-42, good
+// to 2^-35 of itself. Sums of whole numbers are exact in any order, whatever adds them: lanes, CTAs of
+// a cluster, atomics. (With sums of fp32 one row in a hundred of 4,096 would differ from float64's index.)
+//
+// A row is read once, into registers or shared memory, and every later pass goes over that copy. Up to 256
+// logits a warp has a row. Beyond, a CTA or a cluster of CTAs has one: each warp holds a contiguous
+// stretch of it and each lane every 32nd 16 bytes of that, the ones that it read itself. The value that ends a
+// prefix is found by bisection in the warp and by a histogram of 256 bins elsewhere: first over x in units
+// of T, then over what is left in the bin that the border falls into.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "vn_internal.h"
+#include "vn_launch.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace vn {
+namespace {
+
+using u64 = unsigned long long;
+constexpr int kUnit = 42;                // weights are in units of 2^-42
+constexpr u64 kOne = 1ull << kUnit;
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 256;
+
+// 2^(-j/32) in units of 2^-42.
+__constant__ const u64 kPowersInit[32] = {
+    4398046511104ull, 4303805443529ull, 4211583767698ull, 4121338212211ull, 4033026432885ull, 3946606992882ull,
+    3862039343274ull, 3779283804012ull, 3698301545306ull, 3619054569413ull, 3541505692798ull, 3465618528697ull,
+    3391357470036ull, 3318687672730ull, 3247575039328ull, 3177986203020ull, 3109888511975ull, 3043250014027ull,
+    2978039441675ull, 2914226197418ull, 2851780339397ull, 2790672567345ull, 2730874208839ull, 2672357205845ull,
+    2615094101559ull, 2559058027516ull, 2504222690988ull, 2450562362647ull, 2398051864490ull, 2346666558027ull,
+    2296382332721ull, 2247175594673ull};
+
+__device__ __forceinline__ float value(float x) { return x; }
+__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Bits of a float in its order, -0 as +0; below kLowest for the NaN that stands for no logit (a sign and all
+// other bits, in bf16 those of its upper half).
+__device__ __forceinline__ uint32_t key_of(float x) {
+  uint32_t b = __float_as_uint(x);
+  b = b == 0x80000000u ? 0u : b;
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float absent() { return __uint_as_float(0xFFFFFFFFu); }
+constexpr uint32_t kLowest = 0x10000;  // below every logit's key
+
+struct Rows {
+  const void* x;
+  int64_t rows, n;
+  const float* u;
+  double temperature, top_p, min_p;
+  int64_t top_k;
+  const float* temperatures;
+  const int64_t* top_ks;
+  const float* top_ps;
+  const float* min_ps;
+  int64_t* index;
+  float* logprob;
+  float ch, cl;   // 32 log2(e) / temperature
+  u64 min_units;  // min_p in units, rounded up
+};
+
+// p 2^42 rounded up, of p in (0, 1].
+__device__ __forceinline__ u64 units_of(float p) {
+  const uint32_t b = __float_as_uint(p);
+  const int up = static_cast<int>(b >> 23) - 150 + kUnit;  // p = mantissa 2^(up - 42)
+  const u64 mantissa = (b & 0x7FFFFFu) | 0x800000u;
+  if (up >= 0) return mantissa << min(up, 40);
+  return up < -24 ? 1 : (mantissa + (1ull << -up) - 1) >> -up;
+}
+
+// What a row asks for.
+struct Wish {
+  float u, temperature, min_p;
+  float ch, cl;    // 32 log2(e) / T in two parts
+  double top_p;
+  int64_t top_k;
+  u64 min_units;   // min_p in units, rounded up
+  bool bad;        // a parameter is not a number
+};
+
+__device__ __forceinline__ Wish wish_of(const Rows& a, int64_t row) {
+  Wish w;
+  w.u = fetch(a.u + row);
+  w.temperature = static_cast<float>(a.temperature);
+  w.ch = a.ch;
+  w.cl = a.cl;
+  w.top_p = a.top_p;
+  w.min_p = static_cast<float>(a.min_p);
+  w.top_k = a.top_k;
+  if (a.temperatures != nullptr) {
+    const float t = fetch(a.temperatures + row);
+    w.temperature = t;
+    constexpr double k = 46.16624130844683;  // 32 log2(e)
+    constexpr float kh = static_cast<float>(k), kl = static_cast<float>(k - static_cast<double>(kh));
+    w.ch = __fdiv_rn(kh, t);
+    w.cl = __fdiv_rn(__fadd_rn(__fmaf_rn(-w.ch, t, kh), kl), t);
+    if (!(fabsf(w.cl) < INFINITY)) w.cl = 0.f;  // an infinite temperature, or one whose reciprocal is
+  }
+  if (a.top_ks != nullptr) w.top_k = fetch(a.top_ks + row);
+  if (a.top_ps != nullptr) w.top_p = static_cast<double>(fetch(a.top_ps + row));
+  w.min_units = a.min_units;
+  if (a.min_ps != nullptr) {
+    w.min_p = fetch(a.min_ps + row);
+    w.min_units = units_of(w.min_p);
+  }
+  w.bad = w.u != w.u || w.temperature != w.temperature || w.top_p != w.top_p || w.min_p != w.min_p;
+  if (!(w.temperature > 0.f)) {  // the largest
+    w.top_k = 1;
+    w.ch = 46.16624130844683f;
+    w.cl = 0.f;
+  }
+  if (w.top_k <= 0 || w.top_k > a.n) w.top_k = a.n;
+  if (!(w.top_p > 0.0)) w.top_p = 0.0;
+  if (w.min_p > 1.f) {
+    w.min_p = 1.f;
+    w.min_units = kOne;
+  }
+  return w;
+}
+
+// (m - x) 32 log2(e) / T in two parts. What both subtractions round off is carried along.
+__device__ __forceinline__ float distance(float x, float m, const Wish& w, float* low) {
+  const float d = __fsub_rn(m, x), b = __fsub_rn(d, m);
+  const float dl = __fsub_rn(__fsub_rn(m, __fsub_rn(d, b)), __fadd_rn(x, b));
+  const float p = __fmul_rn(d, w.ch);
+  *low = __fmaf_rn(dl, w.ch, __fmaf_rn(d, w.cl, __fmaf_rn(d, w.ch, -p)));
+  return p;
+}
+
+// exp((x - m) / T) in units of 2^-42: 2^-(k + j / 32) from the table and 2^-(r / 32) - 1, |r| <= 1/2, from its Taylor
+// series to r^4 (the next term is 2^-39), whose first term is taken in two parts; in all 2e-11 of the weight.
+__device__ __forceinline__ u64 weight(float x, float m, const Wish& w, const u64* powers) {
+  if (x == m) return kOne;
+  float e;
+  const float p = distance(x, m, w, &e);
+  if (!(p < 43.f * 32.f)) return 0;  // below half a unit (and no logit, and -inf)
+  const float shifted = __fadd_rn(p, 12582912.f);
+  const int32_t kj = __float_as_int(shifted) - 0x4B400000;
+  const float r0 = __fsub_rn(p, __fsub_rn(shifted, 12582912.f));
+  const float r = __fadd_rn(r0, e), rl = __fadd_rn(__fsub_rn(r0, r), e);
+  constexpr double b = -0.021660849392498290;  // -ln 2 / 32
+  constexpr float bh = static_cast<float>(b), bl = static_cast<float>(b - static_cast<double>(bh));
+  constexpr float b2 = static_cast<float>(b * b / 2), b3 = static_cast<float>(b * b * b / 6),
+                  b4 = static_cast<float>(b * b * b * b / 24);
+  const float first = __fmul_rn(bh, r);
+  float rest = __fmaf_rn(bh, rl, __fmaf_rn(bl, r, __fmaf_rn(bh, r, -first)));
+  const float s = __fmaf_rn(__fmaf_rn(b4, r, b3), r, b2);
+  rest = __fmaf_rn(__fmul_rn(s, r), r, rest);
+  // In units of 2^-36: the first part as it is, the rest, below 2^22 of them, by its bits.
+  const int32_t q = __float2int_rn(__fmul_rn(first, 0x1p36f)) + __float_as_int(__fmaf_rn(rest, 0x1p36f, 12582912.f)) - 0x4B400000;
+  const u64 t = powers[kj & 31];
+  const int64_t part = (static_cast<int64_t>(static_cast<int32_t>(t >> 12)) * q) >> 24;
+  const u64 v = t + static_cast<u64>(part);
+  const int k = kj >> 5;
+  return k > 0 ? (v + (1ull << (k - 1))) >> k : v;
+}
+
+// floor(u s) for u of [0, 1), the last unit for more, 0 for less.
+__device__ __forceinline__ u64 share(float u, u64 s) {
+  if (!(u > 0.f)) return 0;
+  if (u >= 1.f) return s - 1;
+  const uint32_t b = __float_as_uint(u);
+  const int e = static_cast<int>(b >> 23);                               // u = mantissa 2^(e - 150)
+  if (e < 64) return 0;                                                  // u s is below 1
+  const u64 mantissa = (b & 0x7FFFFFu) | 0x800000u;
+  const u64 hi = __umul64hi(s, mantissa), lo = s * mantissa;
+  const int down = 150 - e;                                              // 24 .. 86
+  return down < 64 ? (lo >> down) | (hi << (64 - down)) : hi >> (down - 64);
+}
+// The smallest whole number that is not below p s.
+__device__ __forceinline__ u64 nucleus(double p, u64 s) {
+  return static_cast<u64>(ceil(p * static_cast<double>(s)));
+}
+
+// The log of a kept logit's share: -(m - x) / T - ln(S), S in units of the largest weight.
+__device__ __forceinline__ float logprob_of(float x, float m, const Wish& w, u64 s) {
+  float d = 0.f;
+  if (x != m) {
+    float e;
+    const float p = distance(x, m, w, &e);
+    d = __fmul_rn(__fadd_rn(p, e), 0.021660849392498290f);
+  }
+  return -d - log1pf(static_cast<float>(s - kOne) * 0x1p-42f);
+}
+
+// Where the min-p prefix ends, for logits next to its border by their weights. The estimate is off by a few
+// roundings of |m| and T ln(min_p); `sure` is 2^-20 of them.
+struct Floor {
+  float at, sure;
+  __device__ __forceinline__ Floor(float m, const Wish& w) {
+    const float drop = logf(w.min_p) * w.temperature;
+    at = m + drop;
+    sure = 0x1p-20f * (fabsf(m) + fabsf(drop)) + 1e-37f;
+  }
+  __device__ __forceinline__ bool above(float x, float m, const Wish& w, const u64* powers) const {
+    if (x == m || x >= at + sure) return true;
+    if (!(x >= at - sure)) return false;
+    return weight(x, m, w, powers) >= w.min_units;
+  }
+};
+
+__device__ __forceinline__ u64 warp_sum(u64 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+__device__ __forceinline__ u64 warp_scan(u64 v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 t = __shfl_up_sync(kAll, v, o);
+    if (lane >= o) v += t;
+  }
+  return v;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+// What is kept so far: keys above `key`, and of those equal to it the ones at an index up to `last`.
+struct Kept {
+  uint32_t key = kLowest;
+  int32_t last = 0x7FFFFFFF;
+  __device__ __forceinline__ bool holds(uint32_t k, int32_t at) const { return k > key || (k == key && at <= last); }
+};
+
+// ---------------------------------------------------------------- a warp a row
+// Lane l holds the logits l, l + 32, ..
+template <typename T, int R>
+__global__ void __launch_bounds__(kThreads) warp_kernel(const Rows a) {
+  __shared__ u64 powers[32];
+  let_next();
+  if (threadIdx.x < 32) powers[threadIdx.x] = kPowersInit[threadIdx.x];
+  __syncthreads();
+  after_previous();
+  const int lane = threadIdx.x & 31;
+  const int n = static_cast<int>(a.n);
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); row < a.rows;
+       row += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const T* x = static_cast<const T*>(a.x) + row * n;
+    float v[R];
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      v[j] = j * 32 + lane < n ? value(fetch(x + j * 32 + lane)) : absent();
+      if (j * 32 + lane < n) m = max_nan(m, v[j]);
+    }
+    m = warp_max(m);
+    const Wish w = wish_of(a, row);
+    if (w.bad || m != m || m == -INFINITY) {
+      if (lane == 0) {
+        a.index[row] = -1;
+        if (a.logprob != nullptr) a.logprob[row] = NAN;
+      }
+      continue;
+    }
+    u64 weights[R];
+    uint32_t keys[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      keys[j] = key_of(v[j]);
+      weights[j] = weight(v[j], m, w, powers);
+    }
+    Kept kept;
+    // The index of the tie number `count` (from 1) of kept.key.
+    auto tie = [&](int count) {
+      kept.last = 0x7FFFFFFF;
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const uint32_t same = __ballot_sync(kAll, keys[j] == kept.key);
+        const bool it = keys[j] == kept.key && __popc(same & ((1u << lane) - 1u)) == count - 1;
+        const uint32_t hit = __ballot_sync(kAll, it);
+        if (hit != 0) kept.last = j * 32 + __ffs(hit) - 1;
+        count -= __popc(same);
+      }
+    };
+    constexpr int kBits = sizeof(T) == 2 ? 16 : 32;
+    auto shown = [&](uint32_t k) { return sizeof(T) == 2 ? k >> 16 : k; };
+    if (w.top_k < n) {
+      // The largest key that at least top_k logits reach.
+      uint32_t key = 0;
+      if (w.top_k == 1) {
+        key = shown(key_of(m));
+      } else {
+        for (int b = kBits - 1; b >= 0; --b) {
+          const uint32_t c = key | (1u << b);
+          int count = 0;
+#pragma unroll
+          for (int j = 0; j < R; ++j) count += shown(keys[j]) >= c;
+          if (static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(count))) >= w.top_k) key = c;
+        }
+      }
+      int above = 0;
+      uint32_t exact = 0;
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        above += shown(keys[j]) > key;
+        if (shown(keys[j]) == key) exact = keys[j];
+      }
+      kept.key = __reduce_max_sync(kAll, exact);
+      tie(static_cast<int>(w.top_k) - static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(above))));
+    }
+    auto sum_of = [&](auto take) {
+      u64 s = 0;
+#pragma unroll
+      for (int j = 0; j < R; ++j) s += take(j) ? weights[j] : 0;
+      return warp_sum(s);
+    };
+    if (w.top_p < 1.0 && w.top_k > 1) {
+      const Kept before = kept;
+      auto in = [&](int j) { return before.holds(keys[j], j * 32 + lane); };
+      u64 p = nucleus(w.top_p, sum_of(in));
+      if (p == 0) p = 1;
+      // The largest key whose logits and those above reach the nucleus.
+      uint32_t key = 0;
+      for (int b = kBits - 1; b >= 0; --b) {
+        const uint32_t c = key | (1u << b);
+        if (sum_of([&](int j) { return in(j) && shown(keys[j]) >= c; }) >= p) key = c;
+      }
+      const u64 above = sum_of([&](int j) { return in(j) && shown(keys[j]) > key; });
+      uint32_t exact = 0;
+      u64 each = 0;
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+        if (in(j) && shown(keys[j]) == key) { exact = keys[j]; each = weights[j]; }
+      kept.key = __reduce_max_sync(kAll, exact);
+      const int owner = __ffs(__ballot_sync(kAll, each != 0)) - 1;
+      each = __shfl_sync(kAll, each, owner < 0 ? 0 : owner);
+      const u64 ties = each == 0 ? 1 : (p - above + each - 1) / each;
+      tie(ties > static_cast<u64>(n) ? n : static_cast<int>(ties));
+      if (kept.key == before.key && before.last < kept.last) kept.last = before.last;
+    }
+    if (w.min_p > 0.f) {
+      const Floor floor(m, w);
+      uint32_t least = kAll;
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+        if (floor.above(v[j], m, w, powers)) least = min(least, keys[j]);
+      least = __reduce_min_sync(kAll, least);
+      if (least > kept.key) {
+        kept.key = least;
+        kept.last = 0x7FFFFFFF;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+      if (!kept.holds(keys[j], j * 32 + lane)) weights[j] = 0;
+    const u64 s = sum_of([](int) { return true; });
+    u64 r = share(w.u, s);
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      if (found) continue;
+      const u64 scan = warp_scan(weights[j], lane);
+      const uint32_t over = __ballot_sync(kAll, scan > r);
+      if (over != 0) {
+        found = true;
+        if (lane == __ffs(over) - 1) {
+          a.index[row] = j * 32 + lane;
+          if (a.logprob != nullptr) a.logprob[row] = logprob_of(v[j], m, w, s);
+        }
+      }
+      r -= __shfl_sync(kAll, scan, 31);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- a CTA, or a cluster of them, a row
+template <typename T>
+constexpr int kVec = 16 / static_cast<int>(sizeof(T));  // logits of 16 bytes
+
+// A CTA's shared memory but for its logits.
+struct Shared {
+  u64 powers[32];
+  u64 sums[kBins];
+  uint32_t counts[kBins];
+  u64 warps[2][kWarps];   // of the two reductions at work at most
+  u64 mine[2];            // what this CTA hands to the others of its cluster
+  float warps_max[kWarps];
+  uint32_t warps_key[2][kWarps];
+  // Of the bin that a border falls into:
+  int bin;
+  u64 above_sum, bin_sum, target;
+  uint32_t above_count, bin_count;
+  uint32_t low, high;
+};
+
+// A row's share in a CTA: `vectors` 16-byte words a lane from `mine` on, 32 apart, position = word * kVec + element.
+template <typename T>
+struct Part {
+  const uint4* mine;  // this lane's first word
+  int words;          // of a lane
+  int first;          // index of this lane's first word's first logit within the row (may be negative)
+  __device__ __forceinline__ void unpack(int it, float (&v)[kVec<T>]) const {
+    const uint4 raw = mine[it * 32];
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[2 * q] = __uint_as_float(w[q] << 16);
+        v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = __uint_as_float(w[q]);
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    for (int it = 0; it < words; ++it) {
+      float v[kVec<T>];
+      unpack(it, v);
+#pragma unroll
+      for (int q = 0; q < kVec<T>; ++q) f(v[q], first + it * 32 * kVec<T> + q);
+    }
+  }
+};
+
+template <bool kCluster>
+struct Team {
+  Shared& s;
+  int ranks, rank, turn = 0;
+  __device__ __forceinline__ Team(Shared& shared) : s(shared) {
+    ranks = kCluster ? static_cast<int>(cg::this_cluster().num_blocks()) : 1;
+    rank = kCluster ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
+  }
+  __device__ __forceinline__ void sync() const {
+    if constexpr (kCluster) cg::this_cluster().sync(); else __syncthreads();
+  }
+  template <typename V>
+  __device__ __forceinline__ V of_rank(V* p, int r) const {
+    if constexpr (kCluster) return *cg::this_cluster().map_shared_rank(p, r);
+    return *p;
+  }
+  // The sum over all threads; *before: over those of the CTAs and warps before this one. Two places taken
+  // in turn: none is written again before everyone has read it, as a whole round lies between.
+  __device__ __forceinline__ u64 sum(u64 v, u64* before) {
+    const int warp = threadIdx.x >> 5;
+    const u64 w = warp_sum(v);
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) s.warps[turn][warp] = w;
+    __syncthreads();
+    u64 mine = 0, ahead = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const u64 t = s.warps[turn][i];
+      if (i < warp) ahead += t;
+      mine += t;
+    }
+    if constexpr (!kCluster) {
+      *before = ahead;
+      return mine;
+    }
+    if (threadIdx.x == 0) s.mine[turn] = mine;
+    sync();
+    u64 total = 0;
+    for (int r = 0; r < ranks; ++r) {
+      const u64 t = of_rank(&s.mine[turn], r);
+      if (r < rank) ahead += t;
+      total += t;
+    }
+    *before = ahead;
+    return total;
+  }
+  // Of every thread's 64 bits the largest.
+  __device__ __forceinline__ u64 largest(u64 v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const u64 t = __shfl_xor_sync(kAll, v, o);
+      v = t > v ? t : v;
+    }
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) s.warps[turn][threadIdx.x >> 5] = v;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) v = s.warps[turn][i] > v ? s.warps[turn][i] : v;
+    if constexpr (kCluster) {
+      if (threadIdx.x == 0) s.mine[turn] = v;
+      sync();
+      for (int r = 0; r < ranks; ++r) {
+        const u64 t = of_rank(&s.mine[turn], r);
+        v = t > v ? t : v;
+      }
+    }
+    return v;
+  }
+};
+
+// The index, within the row, of the first logit whose weights up to it pass r; before: the weights ahead of this warp.
+// Only the warp that has it writes.
+template <typename T, typename W, typename F>
+__device__ __forceinline__ void walk(const Part<T>& part, u64 r, u64 before, u64 mine, W weigh, F found) {
+  const int lane = threadIdx.x & 31;
+  const u64 total = warp_sum(mine);
+  if (r < before || r >= before + total) return;
+  r -= before;
+  for (int it = 0; it < part.words; ++it) {
+    float v[kVec<T>];
+    part.unpack(it, v);
+    u64 w[kVec<T>], own = 0;
+#pragma unroll
+    for (int q = 0; q < kVec<T>; ++q) {
+      w[q] = weigh(v[q], part.first + it * 32 * kVec<T> + q);
+      own += w[q];
+    }
+    const u64 scan = warp_scan(own, lane);
+    const u64 all = __shfl_sync(kAll, scan, 31);
+    if (r < all) {
+      const uint32_t over = __ballot_sync(kAll, scan > r);
+      if (lane == __ffs(over) - 1) {
+        u64 at = scan - own;
+        int which = -1;
+#pragma unroll
+        for (int q = 0; q < kVec<T>; ++q) {
+          at += w[q];
+          if (which < 0 && at > r) which = q;
+        }
+#pragma unroll
+        for (int q = 0; q < kVec<T>; ++q)
+          if (q == which) found(v[q], part.first + it * 32 * kVec<T> + q);
+      }
+      return;
+    }
+    r -= all;
+  }
+}
+
+// The bin of s.counts and s.sums, over all ranks, that the border falls into: by count, the first whose counts from bin 0
+// on reach `target`; by sum likewise.
+template <bool kCluster>
+__device__ __forceinline__ void find_bin(Team<kCluster>& team, bool by_sum, u64 target_count, double top_p) {
+  Shared& s = team.s;
+  team.sync();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    u64 own[kBins / 32], sums[kBins / 32];
+    u64 total = 0;
+#pragma unroll
+    for (int b = 0; b < kBins / 32; ++b) {
+      const int bin = lane * (kBins / 32) + b;
+      u64 c = 0, w = 0;
+      for (int r = 0; r < team.ranks; ++r) {
+        c += team.of_rank(&s.counts[bin], r);
+        if (by_sum) w += team.of_rank(&s.sums[bin], r);
+      }
+      own[b] = c;
+      sums[b] = w;
+      total += by_sum ? w : c;
+    }
+    const u64 scan = warp_scan(total, lane);
+    u64 target = target_count;
+    if (by_sum && top_p >= 0.0) {
+      target = nucleus(top_p, __shfl_sync(kAll, scan, 31));
+      if (target == 0) target = 1;
+    }
+    const uint32_t reach = __ballot_sync(kAll, scan >= target);
+    if (reach != 0 && lane == __ffs(reach) - 1) {
+      u64 at = scan - total;
+      int hit = -1;
+#pragma unroll
+      for (int b = 0; b < kBins / 32; ++b) {
+        const u64 step = by_sum ? sums[b] : own[b];
+        if (hit < 0) {
+          if (at + step >= target) {
+            hit = b;
+            s.bin = lane * (kBins / 32) + b;
+            s.bin_count = static_cast<uint32_t>(own[b]);
+            s.above_sum = at;
+          } else {
+            at += step;
+          }
+        }
+      }
+      s.target = target;
+    }
+  }
+  team.sync();
+}
+
+template <bool kCluster>
+__device__ __forceinline__ void clear_bins(Shared& s) {
+  for (int b = threadIdx.x; b < kBins; b += kThreads) {
+    s.counts[b] = 0;
+    s.sums[b] = 0;
+  }
+  __syncthreads();
+}
+
+// Cuts `kept` to its first `count` logits, or (by_sum) to those before which less than top_p of its sum lies.
+template <typename T, bool kCluster>
+__device__ __forceinline__ void cut(Team<kCluster>& team, const Part<T>& part, float m, const Wish& w, Kept* kept, bool by_sum, u64 count,
+                                    double top_p) {
+  Shared& s = team.s;
+  const Kept in = *kept;
+  uint32_t low = kLowest, high = kAll;  // keys of the bin
+  u64 target = count, above = 0;        // still to be reached within it, and ahead of it
+  if (!by_sum && count == 1) {
+    low = high = key_of(m);
+  } else {
+    // Bins of an eighth of a binary order of the weights, the last one with all that is below.
+    const float scale = w.ch * 0.25f;
+    auto bin_of = [&](float x) { return x == m ? 0 : min(kBins - 1, __float2int_rd((m - x) * scale)); };
+    clear_bins<kCluster>(s);
+    part.each([&](float x, int at) {
+      if (!in.holds(key_of(x), at)) return;
+      const int b = bin_of(x);
+      atomicAdd(&s.counts[b], 1u);
+      if (by_sum) atomicAdd(&s.sums[b], weight(x, m, w, s.powers));
+    });
+    find_bin<kCluster>(team, by_sum, target, by_sum ? top_p : -1.0);
+    int bin = s.bin;
+    above = s.above_sum;
+    target = s.target;
+    // The keys of its logits.
+    u64 most = 0, least = 0;  // the smallest as its complement's largest
+    part.each([&](float x, int at) {
+      const uint32_t k = key_of(x);
+      if (in.holds(k, at) && bin_of(x) == bin) {
+        most = max(most, static_cast<u64>(k));
+        least = max(least, static_cast<u64>(~k));
+      }
+    });
+    high = static_cast<uint32_t>(team.largest(most));
+    low = ~static_cast<uint32_t>(team.largest(least));
+    while (low < high) {
+      const int shift = max(0, 32 - __clz(high - low) - 8);
+      clear_bins<kCluster>(s);
+      part.each([&](float x, int at) {
+        const uint32_t k = key_of(x);
+        if (k < low || k > high || !in.holds(k, at)) return;
+        atomicAdd(&s.counts[(high - k) >> shift], 1u);
+        if (by_sum) atomicAdd(&s.sums[(high - k) >> shift], weight(x, m, w, s.powers));
+      });
+      find_bin<kCluster>(team, by_sum, target - above, -1.0);
+      bin = s.bin;
+      above += s.above_sum;
+      const uint32_t top = high - (static_cast<uint32_t>(bin) << shift);
+      if (shift == 0) {
+        low = high = top;
+      } else {
+        const uint32_t bottom = top - ((1u << shift) - 1);
+        most = least = 0;
+        part.each([&](float x, int at) {
+          const uint32_t k = key_of(x);
+          if (k <= top && k >= bottom && k >= low && in.holds(k, at)) {
+            most = max(most, static_cast<u64>(k));
+            least = max(least, static_cast<u64>(~k));
+          }
+        });
+        high = static_cast<uint32_t>(team.largest(most));
+        low = ~static_cast<uint32_t>(team.largest(least));
+      }
+    }
+  }
+  // Of the logits with that key, how many, and the index of the last one.
+  kept->key = high;
+  kept->last = 0x7FFFFFFF;
+  const float edge = __uint_as_float(high & 0x80000000u ? high ^ 0x80000000u : ~high);
+  u64 ties = target - above;
+  if (by_sum) {
+    const u64 each = weight(edge, m, w, s.powers);
+    ties = each == 0 ? 1 : (ties + each - 1) / each;
+  }
+  u64 mine = 0, before;
+  part.each([&](float x, int at) { mine += key_of(x) == high && in.holds(high, at); });
+  const u64 all = team.sum(mine, &before);
+  if (ties < all) {
+    walk(part, ties - 1, before, mine, [&](float x, int at) { return static_cast<u64>(key_of(x) == high && in.holds(high, at)); },
+         [&](float, int at) {
+           for (int r = 0; r < team.ranks; ++r) {
+             if constexpr (kCluster) *cg::this_cluster().map_shared_rank(&s.bin, r) = at;
+             else s.bin = at;
+           }
+         });
+    team.sync();
+    kept->last = s.bin;
+    team.sync();
+  } else if (in.key == high) {
+    kept->last = in.last;
+  }
+}
+
+// per: 16-byte words of a warp's lane; the CTA's logits take kWarps * 32 * per of them.
+template <typename T, bool kCluster>
+__global__ void __launch_bounds__(kThreads) cta_kernel(const Rows a, int per) {
+  extern __shared__ uint4 logits[];
+  __shared__ Shared s;
+  let_next();
+  if (threadIdx.x < 32) s.powers[threadIdx.x] = kPowersInit[threadIdx.x];
+  Team<kCluster> team(s);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = static_cast<int>(a.n);
+  after_previous();
+  for (int64_t row = blockIdx.x / team.ranks; row < a.rows; row += gridDim.x / team.ranks) {
+    const T* x = static_cast<const T*>(a.x) + row * n;
+    // Words are those of memory: the first starts up to 15 bytes before the row.
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
+    uint4* mine = logits + warp * 32 * per + lane;
+    Part<T> part;
+    part.mine = mine;
+    part.words = per;
+    part.first = ((team.rank * kWarps + warp) * per * 32 + lane) * kVec<T> - shift;
+    float m = -INFINITY;
+    for (int it = 0; it < per; ++it) {
+      const int at = part.first + it * 32 * kVec<T>;
+      if (at >= 0 && at + kVec<T> <= n) {
+        mine[it * 32] = __ldcs(reinterpret_cast<const uint4*>(x + at));
+      } else {
+        T* to = reinterpret_cast<T*>(mine + it * 32);
+        for (int q = 0; q < kVec<T>; ++q) {
+          if (at + q >= 0 && at + q < n) {
+            to[q] = fetch(x + at + q);
+          } else if constexpr (sizeof(T) == 2) {
+            reinterpret_cast<uint16_t*>(to)[q] = 0xFFFFu;
+          } else {
+            reinterpret_cast<uint32_t*>(to)[q] = 0xFFFFFFFFu;
+          }
+        }
+      }
+    }
+    // A NaN of the row is told from the places without a logit by its index.
+    bool nan = false;
+    part.each([&](float v, int at) {
+      if (v > m) m = v;
+      if (v != v && at >= 0 && at < n) nan = true;
+    });
+    __syncthreads();  // the powers, in the first round
+    const Wish w = wish_of(a, row);
+    {
+      const u64 top = team.largest(nan ? ~0ull : static_cast<u64>(key_of(m)));
+      nan = top == ~0ull;
+      const uint32_t k = static_cast<uint32_t>(top);
+      m = __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+    }
+    if (w.bad || nan || m == -INFINITY) {
+      if (threadIdx.x == 0 && team.rank == 0) {
+        a.index[row] = -1;
+        if (a.logprob != nullptr) a.logprob[row] = NAN;
+      }
+      continue;
+    }
+    Kept kept;
+    if (w.top_k < n) cut<T, kCluster>(team, part, m, w, &kept, false, static_cast<u64>(w.top_k), -1.0);
+    if (w.top_p < 1.0 && w.top_k > 1) cut<T, kCluster>(team, part, m, w, &kept, true, 0, w.top_p);
+    if (w.min_p > 0.f) {
+      const Floor floor(m, w);
+      u64 least = 0;
+      part.each([&](float v, int) {
+        if (floor.above(v, m, w, s.powers)) least = max(least, static_cast<u64>(~key_of(v)));
+      });
+      const uint32_t key = ~static_cast<uint32_t>(team.largest(least));
+      if (key > kept.key) {
+        kept.key = key;
+        kept.last = 0x7FFFFFFF;
+      }
+    }
+    auto weigh = [&](float v, int at) { return kept.holds(key_of(v), at) ? weight(v, m, w, s.powers) : 0; };
+    u64 own = 0, before;
+    part.each([&](float v, int at) { own += weigh(v, at); });
+    const u64 total = team.sum(own, &before);
+    walk(part, share(w.u, total), before, own, weigh, [&](float v, int at) {
+      a.index[row] = at;
+      if (a.logprob != nullptr) a.logprob[row] = logprob_of(v, m, w, total);
+    });
+  }
+  if constexpr (kCluster) team.sync();  // no CTA ends while another may read its shared memory
+}
+
+template <typename T, int R>
+cudaError_t run_warp(const Rows& a, cudaStream_t stream) {
+  const int64_t grid = std::min<int64_t>((a.rows + kWarps - 1) / kWarps, 0x7FFFFFFFll);
+  return launch_overlapped(warp_kernel<T, R>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream, a);
+}
+
+template <typename T, bool kCluster>
+cudaError_t run_cta(const Rows& a, int cluster, cudaStream_t stream) {
+  static SmemRecord record, wide;
+  const int64_t words = (a.n + kVec<T> - 1) / kVec<T> + 1;  // with a row that starts within a word
+  const int64_t lanes = static_cast<int64_t>(cluster) * kThreads;
+  const int per = static_cast<int>((words + lanes - 1) / lanes);
+  const size_t smem = static_cast<size_t>(per) * kThreads * 16;
+  const void* fn = reinterpret_cast<const void*>(cta_kernel<T, kCluster>);
+  cudaError_t err = ensure_dynamic_smem(fn, smem, record);
+  if (err == cudaSuccess && cluster > 8) err = allow_wide_clusters(fn, wide);
+  if (err != cudaSuccess) return err;
+  const int64_t rows = std::min<int64_t>(a.rows, (int64_t{1} << 30) / cluster);
+  return launch_overlapped(cta_kernel<T, kCluster>, dim3(static_cast<unsigned>(rows * cluster)), kThreads, kCluster ? cluster : 0, smem,
+                           stream, a, per);
+}
+
+template <typename T>
+cudaError_t run(const Rows& a, cudaStream_t stream) {
+  if (a.n <= 32) return run_warp<T, 1>(a, stream);
+  if (a.n <= 64) return run_warp<T, 2>(a, stream);
+  if (a.n <= 128) return run_warp<T, 4>(a, stream);
+  if (a.n <= 256) return run_warp<T, 8>(a, stream);
+  DeviceInfo dev;
+  const cudaError_t err = device_info(&dev);
+  if (err != cudaSuccess) return err;
+  // CTAs a row: until the rows fill the SMs, while a lane has four words or more; at least what holds the row.
+  const int64_t words = (a.n + kVec<T> - 1) / kVec<T> + 1;
+  int cluster = 1;
+  while (cluster < 16 && a.rows * cluster * 2 <= dev.sm_count && words >= static_cast<int64_t>(cluster) * kThreads * 8) cluster *= 2;
+  while (cluster < 16 && words * 16 > static_cast<int64_t>(cluster) * 160 * 1024) cluster *= 2;
+  return cluster == 1 ? run_cta<T, false>(a, 1, stream) : run_cta<T, true>(a, cluster, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_sample(const SampleArgs& g, cudaStream_t stream) {
+  Rows a;
+  a.x = g.logits; a.rows = g.rows; a.n = g.n; a.u = g.u;
+  a.temperature = g.temperature; a.top_p = g.top_p; a.min_p = g.min_p; a.top_k = g.top_k;
+  a.temperatures = g.temperatures; a.top_ks = g.top_ks; a.top_ps = g.top_ps; a.min_ps = g.min_ps;
+  a.index = g.index; a.logprob = g.logprob;
+  a.min_units = static_cast<u64>(std::ceil(std::min(std::max(g.min_p, 0.0), 1.0) * 0x1p42));
+  const double c = g.temperature > 0.0 ? 46.16624130844683 / g.temperature : 46.16624130844683;
+  a.ch = static_cast<float>(c);
+  a.cl = static_cast<float>(c - static_cast<double>(a.ch));
+  return g.dt == VN_BF16 ? run<__nv_bfloat16>(a, stream) : run<float>(a, stream);
+}
+
+}  // namespace vn

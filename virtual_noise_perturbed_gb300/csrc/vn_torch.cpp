@@ -16,6 +16,7 @@
 
 #include <optional>
 #include <string>
+#include <type_traits>
 #include <vector>
 
 #include "vn.h"
@@ -490,6 +491,65 @@ PyObject* adamw_moments(PyObject* const* a, Py_ssize_t count) {
   return tuple(mo, vo);
 }
 
+// A parameter of a draw: a number, None (which stands for `without`), or a tensor with one for each row.
+template <typename V>
+struct PerRow {
+  PerRow(PyObject* o, const char* name, V without, at::IntArrayRef shape, const at::Tensor& x) : number(without) {
+    if (o == Py_None) return;
+    if (!THPVariable_Check(o)) {
+      if constexpr (std::is_same_v<V, int64_t>) number = whole(o); else number = real(o);
+      return;
+    }
+    each = input(o, name);
+    shaped(*each, name, shape);
+    beside(*each, x);
+    const at::ScalarType want = std::is_same_v<V, int64_t> ? at::kLong : at::kFloat;
+    if (each->scalar_type() != want)
+      raise(PyExc_TypeError, std::string(name) + " must be a number or a torch." + (want == at::kLong ? "int64" : "float32") + " tensor");
+  }
+  V number;
+  std::optional<at::Tensor> each;
+};
+
+// sample(logits, uniforms, temperature, top_k, top_p, min_p, logprobs, out) -> index or (index, logprob)
+PyObject* sample(PyObject* const* a, Py_ssize_t count) {
+  counted(count, 8, "sample");
+  const at::Tensor x = input(a[0], "logits"), u = input(a[1], "uniforms");
+  if (x.dim() < 1 || x.size(-1) < 1) raise(PyExc_ValueError, "logits must be (..., n) with n >= 1");
+  const vn_dtype dt = dtype_of(x, "logits");
+  const at::IntArrayRef lead = x.sizes().slice(0, x.dim() - 1);
+  int64_t rows = 1;
+  for (int64_t d : lead) rows *= d;
+  shaped(u, "uniforms", lead);
+  if (u.scalar_type() != at::kFloat) raise(PyExc_TypeError, "uniforms must be torch.float32");
+  beside(u, x);
+  const PerRow<double> temperature(a[2], "temperature", 1.0, lead, x);
+  const PerRow<int64_t> top_k(a[3], "top_k", 0, lead, x);
+  const PerRow<double> top_p(a[4], "top_p", 1.0, lead, x), min_p(a[5], "min_p", 0.0, lead, x);
+  at::Tensor index;
+  if (a[7] == Py_None) {
+    index = empty(lead, at::kLong, x);
+  } else {
+    if (!THPVariable_Check(a[7]) || THPVariable_Unpack(a[7]).sizes() != lead || THPVariable_Unpack(a[7]).scalar_type() != at::kLong ||
+        !THPVariable_Unpack(a[7]).is_contiguous() || THPVariable_Unpack(a[7]).device() != x.device())
+      raise(PyExc_ValueError, "out must be a contiguous torch.int64 tensor of shape " + text_of(lead) + " on " + text_of(x.device()));
+    index = THPVariable_Unpack(a[7]);
+    changed(index);
+  }
+  std::optional<at::Tensor> logprob;
+  if (truth(a[6])) logprob = empty(lead, at::kFloat, x);
+  {
+    const On on(x);
+    check(vn_sample(at_(x), dt, rows, x.size(-1), static_cast<const float*>(at_(u)), temperature.number,
+                    static_cast<const float*>(at_(temperature.each)), top_k.number, static_cast<const int64_t*>(at_(top_k.each)),
+                    top_p.number, static_cast<const float*>(at_(top_p.each)), min_p.number,
+                    static_cast<const float*>(at_(min_p.each)), static_cast<int64_t*>(at_(index)),
+                    static_cast<float*>(at_(logprob)), on.stream),
+          "vn_sample");
+  }
+  return logprob ? tuple(index, logprob) : wrap(index);
+}
+
 template <PyObject* (*kFn)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t count) {
   HANDLE_TH_ERRORS
@@ -509,7 +569,7 @@ PyMethodDef method(const char* name) {
 PyMethodDef g_methods[] = {
     method<linear>("linear"),         method<linear_backward>("linear_backward"),
     method<layer_norm>("layer_norm"), method<layer_norm_backward>("layer_norm_backward"),
-    method<clip_gradients>("clip_gradients"),
+    method<clip_gradients>("clip_gradients"), method<sample>("sample"),
     method<adamw>("adamw"),           method<adamw_moments>("adamw_moments"),
     {nullptr, nullptr, 0, nullptr},
 };

@@ -274,4 +274,25 @@ class AdamW:
         return (_binding or _native()).adamw_moments(s["m"], s["v"], s["m_scale"], s["v_scale"])
 
 
-__all__ = ["AdamW", "clip_gradients", "gradient_norm", "layer_norm", "layer_norm_backward", "linear", "linear_backward"]
+PerRow = Union[float, torch.Tensor, None]
+
+
+def sample(logits: torch.Tensor, uniforms: torch.Tensor, *, temperature: PerRow = 1.0, top_k: Union[int, torch.Tensor, None] = None,
+           top_p: PerRow = None, min_p: PerRow = None, logprobs: bool = False,
+           out: Optional[torch.Tensor] = None) -> Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]]:
+    """An index for each row of ``logits`` (..., n), drawn with that row's random number of [0, 1) in
+    ``uniforms`` (...), as int64 (...) (``vn_sample``): actions from a policy's logits.
+
+    The weights are exp(logits / temperature). ``top_k`` keeps the k largest logits (of equal ones those with the lower
+    index), ``top_p`` of those the largest ones until their sum reaches that share, ``min_p`` those whose weight is at
+    least that share of the largest's. The index is the first at which the sum of the kept weights passes
+    ``uniforms`` times the whole: float64's index, whatever the sizes. Each parameter is a number, None (no filter) or a
+    tensor of the leading shape (float32, ``top_k`` int64). A temperature of 0 takes the largest logit. With ``logprobs=True`` the result is
+    (index, log of the kept weights' share that it has), the latter float32.
+
+    logits are float32 or bfloat16, n up to 524,288. A row with a NaN, or with nothing above -infinity, gets
+    the index -1 (and a NaN)."""
+    return (_binding or _native()).sample(logits, uniforms, temperature, top_k, top_p, min_p, logprobs, out)
+
+
+__all__ = ["AdamW", "clip_gradients", "gradient_norm", "layer_norm", "layer_norm_backward", "linear", "linear_backward", "sample"]
