@@ -482,6 +482,41 @@ vn_status vn_adamw_clipped(const vn_adamw_tensor* tensors, int64_t n_tensors, vn
                            void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
+ * vn_pack_weight -- a layer's weights w [out, in] of dt in 4 bits, with a scale for each `group` consecutive k of a row
+ * (32, 64 or 128; the last group of a row may be shorter):
+ *     scale = max |w| / 7, rounded to dt;   code = the whole number next to w / scale (halves to even) within -7 .. 7,
+ *     0 where scale is 0. The value it stands for is code * scale; a group with an infinity or a NaN stands for NaN.
+ * scales [out, ceil(in / group)] of dt; codes: out rows of vn_packed_row_bytes(in) bytes, 16-byte aligned. Their
+ * order within a row is the library's own.
+ */
+vn_status vn_pack_weight(const void* w, vn_dtype dt, int64_t out, int64_t in, int group,
+                         void* codes, void* scales, void* stream);
+
+/* Bytes of a row of codes, -1 for a size that vn_pack_weight refuses. */
+int64_t vn_packed_row_bytes(int64_t in);
+
+/* vn_unpack_weight -- the values w [out, in] that codes and scales stand for, each rounded once to dt. */
+vn_status vn_unpack_weight(const void* codes, const void* scales, vn_dtype dt, int64_t out, int64_t in,
+                           int group, void* w, void* stream);
+
+/*
+ * vn_linear_packed -- vn_linear on packed weights, without preact:
+ *     y[r, j] = act(sum_k x[r, k] code[j, k] scale[j, k / group] + b[j]) + residual[r, j]
+ * x [rows, in], scales, residual and y [rows, out] of dt, b [out] of b_dt or NULL. Up to 64 rows (fp32: 21) the products of x
+ * and the codes are summed exactly rounded per group and scaled in fp32; with more rows the values are unpacked into
+ * the workspace first, in bf16 each rounded to bf16. In fp32 an infinity in x gives NaN. workspace:
+ * vn_linear_packed_workspace bytes, 256-byte aligned; errors and status as for vn_linear.
+ */
+vn_status vn_linear_packed(const void* x, const void* codes, const void* scales, vn_dtype dt, int group,
+                           const void* b, vn_dtype b_dt, const void* residual, int64_t rows,
+                           int64_t in, int64_t out, vn_act act, void* y, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
+/* Workspace of vn_linear_packed in bytes, -1 for sizes or a dtype that it refuses. aligned: x starts on a
+ * 16-byte boundary. */
+int64_t vn_linear_packed_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, int aligned);
+
+/*
  * vn_sample -- an index for each row of logits [rows, n] of dt, drawn with the row's random number u [rows]:
  *     w_i = exp((x_i - max x) / temperature);  order: x descending, of equal ones (-0 = +0) the lower index first
  *     kept: the first top_k of the order; of those the ones before which less than top_p times their sum lies

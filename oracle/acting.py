@@ -46,3 +46,24 @@ def sample(x, u, **filters):
     last = int(np.flatnonzero(w)[-1])
     i = min(int(np.searchsorted(c, max(u, 0.0) * c[-1], side="right")), last)
     return i, math.log(w[i] / c[-1])
+
+
+def pack4(w, group, rounded):
+    """(codes, scales) of weights (out, in); ``rounded`` rounds an array to the scales' type."""
+    w = np.asarray(w, dtype=np.float64)
+    n, k = w.shape
+    codes, scales = np.zeros((n, k)), np.zeros((n, -(-k // group)))
+    for i in range(scales.shape[1]):
+        part = w[:, i * group:(i + 1) * group]
+        with np.errstate(invalid="ignore", divide="ignore"):
+            s = rounded(np.abs(part).max(axis=1, initial=0.0) / 7)
+            q = np.rint(part / s[:, None])
+        usable = (s > 0) & np.isfinite(s)
+        codes[:, i * group:(i + 1) * group] = np.where(usable[:, None], np.clip(q, -7, 7), 0.0)
+        scales[:, i] = s
+    return codes, scales
+
+
+def values4(codes, scales, group):
+    with np.errstate(invalid="ignore"):
+        return codes * np.repeat(scales, group, axis=1)[:, :codes.shape[1]]

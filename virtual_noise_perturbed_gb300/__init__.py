@@ -29,18 +29,21 @@ from .api import (  # noqa: F401
 )
 from .network import (  # noqa: F401
     AdamW,
+    Weight4,
     clip_gradients,
     gradient_norm,
     layer_norm,
     layer_norm_backward,
     linear,
+    linear4,
     linear_backward,
+    pack4,
     sample,
 )
 
 __all__ = [
-    "AdamW", "VNError", "centered_ranks", "clip_gradients", "compute_offsets", "device_status", "es_update", "gradient_norm", "gradient_update", "hash_probe", "layer_norm",
-    "layer_norm_backward", "linear", "linear_backward", "noise_dump", "perturbed_linear_path", "sample",
+    "AdamW", "VNError", "Weight4", "centered_ranks", "clip_gradients", "compute_offsets", "device_status", "es_update", "gradient_norm", "gradient_update", "hash_probe", "layer_norm",
+    "layer_norm_backward", "linear", "linear4", "linear_backward", "noise_dump", "pack4", "perturbed_linear_path", "sample",
     "virtual_bias_gradient", "virtual_flat_gradient", "virtual_perturbed_linear", "virtual_perturbed_mlp",
     "virtual_reduce_metric",
     "virtual_weight_gradient",

@@ -72,6 +72,11 @@ SIGNATURES = {
     "vn_clip_gradients": (_I, [_P, _I64, _I, _D, _P, _P, _I64, _P]),
     "vn_gradient_norm_workspace": (_I64, [_I64]),
     "vn_adamw_clipped": (_I, [_P, _I64, _I, _I, _I, _D, _D, _D, _D, _I64, _I, _D, _P, _P, _I64, _P]),
+    "vn_pack_weight": (_I, [_P, _I, _I64, _I64, _I, _P, _P, _P]),
+    "vn_packed_row_bytes": (_I64, [_I64]),
+    "vn_unpack_weight": (_I, [_P, _P, _I, _I64, _I64, _I, _P, _P]),
+    "vn_linear_packed": (_I, [_P, _P, _P, _I, _I, _P, _I, _P, _I64, _I64, _I64, _I, _P, _P, _I64, _P]),
+    "vn_linear_packed_workspace": (_I64, [_I64, _I64, _I64, _I, _I]),
     "vn_sample": (_I, [_P, _I, _I64, _I64, _P, _D, _P, _I64, _P, _D, _P, _D, _P, _P, _P, _P]),
     "vn_adamw_moments": (_I, [_P, _P, _P, _P, _I64, _P, _P, _P]),
 }

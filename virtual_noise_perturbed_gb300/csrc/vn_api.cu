@@ -208,6 +208,7 @@ class Pieces {
   std::unique_ptr<vn_gradient[]> p_;
 };
 
+constexpr int64_t kMostFeatures = int64_t{1} << 40;  // of packed weights
 constexpr int64_t kMostTensors = int64_t{1} << 32;
 
 vn_status check_norm(int64_t n_tensors, double max_norm, const float* norm, const void* workspace, int64_t workspace_bytes) {
@@ -896,6 +897,80 @@ vn_status vn_adamw_moments(const void* exp_avg, const void* exp_avg_sq, const fl
   if (!disjoint(outs, ins)) return VN_ERR_VALUE;
   return launched(vn::launch_adamw_moments(exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, n, m, v,
                                            static_cast<cudaStream_t>(stream)));
+}
+
+int64_t vn_packed_row_bytes(int64_t in) { return in < 0 || in > kMostFeatures ? -1 : vn::packed_row_bytes(in); }
+
+// The sizes of packed weights, and the bytes of their arrays.
+static vn_status packed_sizes(int64_t out, int64_t in, int group, vn_dtype dt, int64_t* wb, int64_t* cb, int64_t* sb) {
+  if (!dtype_ok(dt)) return VN_ERR_DTYPE;
+  if (group != 32 && group != 64 && group != 128) return VN_ERR_VALUE;
+  if (out < 0 || in < 0) return VN_ERR_SHAPE;
+  if (in > kMostFeatures || !bytes_of(out, in, dt, wb) || !mul(out, vn::packed_row_bytes(in), cb) ||
+      !bytes_of(out, (in + group - 1) / group, dt, sb))
+    return VN_ERR_OVERFLOW;
+  return VN_OK;
+}
+
+vn_status vn_pack_weight(const void* w, vn_dtype dt, int64_t out, int64_t in, int group, void* codes, void* scales,
+                         void* stream) {
+  int64_t wb, cb, sb;
+  const vn_status st = packed_sizes(out, in, group, dt, &wb, &cb, &sb);
+  if (st != VN_OK || wb == 0) return st;
+  if (w == nullptr || codes == nullptr || scales == nullptr) return VN_ERR_NULL;
+  if (!aligned(w, dtype_size(dt)) || !aligned(codes, 16) || !aligned(scales, dtype_size(dt))) return VN_ERR_ALIGN;
+  const Range outs[] = {{codes, cb}, {scales, sb}};
+  const Range ins[] = {{w, wb}};
+  if (!disjoint(outs, ins)) return VN_ERR_VALUE;
+  return launched(vn::launch_pack(w, dt, out, in, group, static_cast<uint8_t*>(codes), scales, static_cast<cudaStream_t>(stream)));
+}
+
+vn_status vn_unpack_weight(const void* codes, const void* scales, vn_dtype dt, int64_t out, int64_t in, int group, void* w,
+                           void* stream) {
+  int64_t wb, cb, sb;
+  const vn_status st = packed_sizes(out, in, group, dt, &wb, &cb, &sb);
+  if (st != VN_OK || wb == 0) return st;
+  if (w == nullptr || codes == nullptr || scales == nullptr) return VN_ERR_NULL;
+  if (!aligned(w, dtype_size(dt)) || !aligned(codes, 16) || !aligned(scales, dtype_size(dt))) return VN_ERR_ALIGN;
+  const Range outs[] = {{w, wb}};
+  const Range ins[] = {{codes, cb}, {scales, sb}};
+  if (!disjoint(outs, ins)) return VN_ERR_VALUE;
+  return launched(vn::launch_unpack(static_cast<const uint8_t*>(codes), scales, dt, out, in, group, w, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t vn_linear_packed_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, int al) {
+  if (check_sizes(rows, in, out, dt) != VN_OK || !features_ok(rows, in, out) || in > kMostFeatures) return -1;
+  return vn::packed_workspace(rows, in, out, dt, al != 0);
+}
+
+vn_status vn_linear_packed(const void* x, const void* codes, const void* scales, vn_dtype dt, int group, const void* b,
+                           vn_dtype b_dt, const void* residual, int64_t rows, int64_t in, int64_t out, vn_act act, void* y,
+                           void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!dtype_ok(dt) || (b != nullptr && !dtype_ok(b_dt))) return VN_ERR_DTYPE;
+  if (!linear_act_ok(act)) return VN_ERR_VALUE;
+  int64_t wb, cb, sb, xb, yb;
+  vn_status st = packed_sizes(out, in, group, dt, &wb, &cb, &sb);
+  if (st != VN_OK) return st;
+  st = check_sizes(rows, in, out, dt);
+  if (st != VN_OK) return st;
+  if (rows == 0 || out == 0) return VN_OK;
+  if (!features_ok(rows, in, out)) return VN_ERR_OVERFLOW;
+  if (y == nullptr || (in > 0 && (x == nullptr || codes == nullptr || scales == nullptr))) return VN_ERR_NULL;
+  const size_t es = dtype_size(dt);
+  if (!aligned(x, es) || !aligned(codes, 16) || !aligned(scales, es) || !aligned(y, es) || !aligned(residual, es) ||
+      (b != nullptr && !aligned(b, dtype_size(b_dt))) || !aligned(workspace, 256))
+    return VN_ERR_ALIGN;
+  if (!bytes_of(rows, in, dt, &xb) || !bytes_of(rows, out, dt, &yb)) return VN_ERR_OVERFLOW;
+  const int64_t need = vn::packed_workspace(rows, in, out, dt, aligned(x, 16));
+  if ((need > 0 && workspace == nullptr) || workspace_bytes < need) return VN_ERR_WORKSPACE;
+  const int64_t bb = b != nullptr ? out * static_cast<int64_t>(dtype_size(b_dt)) : 0;
+  const Range outs[] = {{y, yb}, {workspace, need}};
+  const Range ins[] = {{x, xb}, {codes, cb}, {scales, sb}, {b, bb}, {residual, yb}};
+  if (!disjoint(outs, ins)) return VN_ERR_VALUE;
+  vn::PackedArgs a;
+  a.x = x; a.codes = static_cast<const uint8_t*>(codes); a.scales = scales; a.dt = dt; a.group = group; a.b = b; a.b_dt = b_dt;
+  a.residual = residual; a.rows = rows; a.in = in; a.out = out; a.act = act; a.y = y; a.workspace = workspace;
+  return launched(vn::launch_packed(a, static_cast<cudaStream_t>(stream)));
 }
 
 vn_status vn_sample(const void* logits, vn_dtype dt, int64_t rows, int64_t n, const float* u, double temperature,

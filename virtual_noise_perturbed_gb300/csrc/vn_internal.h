@@ -216,6 +216,28 @@ cudaError_t launch_adamw_moments(const void* exp_avg, const void* exp_avg_sq, co
                                  const float* exp_avg_sq_scale, int64_t n, float* m, float* v,
                                  cudaStream_t stream);
 
+// Weights in 4 bits, and the linear layer on them.
+struct PackedArgs {
+  const void* x;
+  const uint8_t* codes;
+  const void* scales;
+  vn_dtype dt;
+  int group;
+  const void* b;  // may be null
+  vn_dtype b_dt;
+  const void* residual;  // may be null
+  int64_t rows, in, out;
+  vn_act act;
+  void* y;
+  void* workspace;
+};
+int64_t packed_row_bytes(int64_t in);
+cudaError_t launch_pack(const void* w, vn_dtype dt, int64_t out, int64_t in, int group, uint8_t* codes, void* scales, cudaStream_t stream);
+cudaError_t launch_unpack(const uint8_t* codes, const void* scales, vn_dtype dt, int64_t out, int64_t in, int group, void* w,
+                          cudaStream_t stream);
+int64_t packed_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, bool aligned);
+cudaError_t launch_packed(const PackedArgs& a, cudaStream_t stream);
+
 // An index for each row of logits.
 constexpr int64_t kSampleMost = int64_t{1} << 19;  // logits of a row: what a cluster of 16 CTAs holds in shared memory
 struct SampleArgs {

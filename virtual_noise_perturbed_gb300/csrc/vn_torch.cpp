@@ -491,6 +491,85 @@ PyObject* adamw_moments(PyObject* const* a, Py_ssize_t count) {
   return tuple(mo, vo);
 }
 
+// pack_weight(weight, group) -> (codes, scales)
+PyObject* pack_weight(PyObject* const* a, Py_ssize_t count) {
+  counted(count, 2, "pack_weight");
+  const at::Tensor w = input(a[0], "weight");
+  if (w.dim() != 2) raise(PyExc_ValueError, "weight must be (out_features, in_features)");
+  const vn_dtype dt = dtype_of(w, "weight");
+  const int64_t group = whole(a[1]);
+  if (group != 32 && group != 64 && group != 128) raise(PyExc_ValueError, "group must be 32, 64 or 128");
+  const int64_t n = w.size(0), k = w.size(1);
+  const int64_t code_shape[2] = {n, vn_packed_row_bytes(k)}, scale_shape[2] = {n, (k + group - 1) / group};
+  const at::Tensor codes = empty(code_shape, at::kByte, w), scales = empty(scale_shape, w.scalar_type(), w);
+  {
+    const On on(w);
+    check(vn_pack_weight(at_(w), dt, n, k, static_cast<int>(group), at_(codes), at_(scales), on.stream), "vn_pack_weight");
+  }
+  return tuple(codes, scales);
+}
+
+// Packed weights as Python hands them over: codes, scales, in, group.
+struct Packed {
+  Packed(PyObject* c, PyObject* s, PyObject* in, PyObject* g) : codes(input(c, "codes")), scales(input(s, "scales")), k(whole(in)), group(whole(g)) {
+    dt = dtype_of(scales, "scales");
+    n = codes.dim() == 2 ? codes.size(0) : -1;
+    const int64_t want[2] = {n, vn_packed_row_bytes(k)}, want_scales[2] = {n, group > 0 ? (k + group - 1) / group : 0};
+    if (n < 0 || codes.scalar_type() != at::kByte) raise(PyExc_ValueError, "codes must be torch.uint8 of shape (out_features, bytes)");
+    shaped(codes, "codes", want);
+    shaped(scales, "scales", want_scales);
+    beside(scales, codes);
+  }
+  at::Tensor codes, scales;
+  int64_t n, k, group;
+  vn_dtype dt;
+};
+
+// unpack_weight(codes, scales, in, group, out) -> weight
+PyObject* unpack_weight(PyObject* const* a, Py_ssize_t count) {
+  counted(count, 5, "unpack_weight");
+  const Packed p(a[0], a[1], a[2], a[3]);
+  const int64_t shape[2] = {p.n, p.k};
+  const at::Tensor w = result(a[4], shape, p.scales);
+  {
+    const On on(w);
+    check(vn_unpack_weight(at_(p.codes), at_(p.scales), p.dt, p.n, p.k, static_cast<int>(p.group), at_(w), on.stream), "vn_unpack_weight");
+  }
+  return wrap(w);
+}
+
+// linear_packed(x, codes, scales, in, group, bias, activation, residual, out) -> y
+PyObject* linear_packed(PyObject* const* a, Py_ssize_t count) {
+  counted(count, 9, "linear_packed");
+  const at::Tensor x = input(a[0], "x");
+  const Packed p(a[1], a[2], a[3], a[4]);
+  if (x.dim() < 1 || x.size(-1) != p.k)
+    raise(PyExc_ValueError, "x must be (..., " + std::to_string(p.k) + "), got " + text_of(x.sizes()));
+  if (x.scalar_type() != p.scales.scalar_type())
+    raise(PyExc_TypeError, "x and weight must have one dtype, got " + text_of(x.scalar_type()) + " and " + text_of(p.scales.scalar_type()));
+  beside(p.codes, x);
+  int64_t rows = 1;
+  for (int64_t i = 0; i + 1 < x.dim(); ++i) rows *= x.size(i);
+  c10::SmallVector<int64_t, 5> shape(x.sizes().begin(), x.sizes().end());
+  shape.back() = p.n;
+  const auto bias = optional_input(a[5], "bias");
+  vector_of(bias, "bias", p.n, x);
+  const auto residual = optional_input(a[7], "residual");
+  if (residual) like(*residual, "residual", shape, x);
+  const auto act = static_cast<vn_act>(whole(a[6]));
+  const vn_dtype bias_dt = bias ? dtype_of(*bias, "bias") : VN_F32;
+  const at::Tensor y = result(a[8], shape, x);
+  const int64_t need = vn_linear_packed_workspace(rows, p.k, p.n, p.dt, aligned16(at_(x)));
+  const auto ws = workspace(need, x);
+  {
+    const On on(x);
+    check(vn_linear_packed(at_(x), at_(p.codes), at_(p.scales), p.dt, static_cast<int>(p.group), at_(bias), bias_dt, at_(residual),
+                           rows, p.k, p.n, act, at_(y), at_(ws), need > 0 ? need : 0, on.stream),
+          "vn_linear_packed");
+  }
+  return wrap(y);
+}
+
 // A parameter of a draw: a number, None (which stands for `without`), or a tensor with one for each row.
 template <typename V>
 struct PerRow {
@@ -570,6 +649,8 @@ PyMethodDef g_methods[] = {
     method<linear>("linear"),         method<linear_backward>("linear_backward"),
     method<layer_norm>("layer_norm"), method<layer_norm_backward>("layer_norm_backward"),
     method<clip_gradients>("clip_gradients"), method<sample>("sample"),
+    method<pack_weight>("pack_weight"), method<unpack_weight>("unpack_weight"),
+    method<linear_packed>("linear_packed"),
     method<adamw>("adamw"),           method<adamw_moments>("adamw_moments"),
     {nullptr, nullptr, 0, nullptr},
 };

@@ -274,6 +274,47 @@ class AdamW:
         return (_binding or _native()).adamw_moments(s["m"], s["v"], s["m_scale"], s["v_scale"])
 
 
+class Weight4:
+    """A layer's weights in 4 bits with a scale for each ``group`` consecutive elements of a row, as ``pack4`` makes
+    them and ``linear4`` takes them: ``codes`` (uint8, (out, bytes); their order is the library's own), ``scales`` of the weights'
+    dtype, (out, ceil(in / group)), ``shape`` (out, in) and ``group``. A saved handle is made again from those four."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, in_features: int, group: int):
+        if group not in (32, 64, 128):
+            raise ValueError("group must be 32, 64 or 128")
+        self.codes, self.scales, self.group = codes, scales, int(group)
+        self.shape = torch.Size((codes.shape[0], int(in_features)))
+
+    def dequantize(self, *, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The weights that the codes stand for, code times scale, each rounded once to the scales' dtype
+        (``vn_unpack_weight``)."""
+        return (_binding or _native()).unpack_weight(self.codes, self.scales, self.shape[1], self.group, out)
+
+
+def pack4(weight: torch.Tensor, *, group: int = 64) -> Weight4:
+    """``weight`` (out, in), float32 or bfloat16, in 4 bits (``vn_pack_weight``): of each ``group`` (32, 64 or 128) consecutive
+    elements of a row the scale is their largest magnitude over 7, and a code the whole number of -7 .. 7 next to
+    an element over it."""
+    codes, scales = (_binding or _native()).pack_weight(weight, group)
+    return Weight4(codes, scales, weight.shape[1], group)
+
+
+def linear4(x: torch.Tensor, weight: Weight4, bias: Optional[torch.Tensor] = None, *, activation: Optional[str] = None,
+            residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+            check_status: bool = False) -> torch.Tensor:
+    """``linear`` on packed weights, act(x V^T + b) + residual with V code times scale (``vn_linear_packed``): a layer
+    that acts on few rows and is bound by reading its weights reads a quarter of them.
+
+    x is (..., in) of the scales' dtype, the rest as for ``linear``. Up to 64 rows (float32: 21) V is not rounded; with more, V is
+    unpacked first, rounded to x's dtype, and ``linear``'s kernels run. An infinity in x gives NaN in float32.
+    Not recorded by autograd. ``check_status`` as for ``linear``."""
+    y = (_binding or _native()).linear_packed(x, weight.codes, weight.scales, weight.shape[1], weight.group, bias, _act(activation),
+                                              residual, out)
+    if check_status:
+        device_status(x.device)
+    return y
+
+
 PerRow = Union[float, torch.Tensor, None]
 
 
@@ -295,4 +336,5 @@ def sample(logits: torch.Tensor, uniforms: torch.Tensor, *, temperature: PerRow 
     return (_binding or _native()).sample(logits, uniforms, temperature, top_k, top_p, min_p, logprobs, out)
 
 
-__all__ = ["AdamW", "clip_gradients", "gradient_norm", "layer_norm", "layer_norm_backward", "linear", "linear_backward", "sample"]
+__all__ = ["AdamW", "Weight4", "clip_gradients", "gradient_norm", "layer_norm", "layer_norm_backward", "linear", "linear4",
+           "linear_backward", "pack4", "sample"]
