@@ -502,8 +502,8 @@ vn_status vn_unpack_weight(const void* codes, const void* scales, vn_dtype dt, i
 /*
  * vn_linear_packed -- vn_linear on packed weights, without preact:
  *     y[r, j] = act(sum_k x[r, k] code[j, k] scale[j, k / group] + b[j]) + residual[r, j]
- * x [rows, in], scales, residual and y [rows, out] of dt, b [out] of b_dt or NULL. Up to 64 rows (fp32: 21) the products of x
- * and the codes are summed exactly rounded per group and scaled in fp32; with more rows the values are unpacked into
+ * x [rows, in], scales, residual and y [rows, out] of dt, b [out] of b_dt or NULL. Up to 32 rows (fp32: 10) a group's products of x
+ * and codes are summed first and scaled in fp32; with more rows the values are unpacked into
  * the workspace first, in bf16 each rounded to bf16. In fp32 an infinity in x gives NaN. workspace:
  * vn_linear_packed_workspace bytes, 256-byte aligned; errors and status as for vn_linear.
  */

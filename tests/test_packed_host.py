@@ -54,8 +54,8 @@ def test_linear_refusals(lib):
     assert call(rows=100) == 11 and call(rows=100, ws=F + 0x50000, wb=16) == 11
     assert call(rows=0, x=0, y=0) == 0 and call(n=0, y=0) == 0
     w = lib.vn_linear_packed_workspace
-    assert w(64, 512, 256, 1, 1) == 0 and w(21, 512, 256, 0, 1) == 0
-    assert w(65, 512, 256, 1, 1) >= 2 * 512 * 256 and w(22, 512, 256, 0, 1) >= 4 * 512 * 256
+    assert w(32, 512, 256, 1, 1) == 0 and w(10, 512, 256, 0, 1) == 0
+    assert w(33, 512, 256, 1, 1) >= 2 * 512 * 256 and w(11, 512, 256, 0, 1) >= 4 * 512 * 256
     assert w(-1, 4, 4, 0, 1) == -1 and w(4, 4, 4, 9, 1) == -1
 
 

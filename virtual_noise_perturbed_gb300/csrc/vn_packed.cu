@@ -37,6 +37,9 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 __host__ __device__ __forceinline__ int64_t blocks_of(int64_t in) { return (in + kBlock - 1) / kBlock; }
+// A group's length as a power of two, and how many a row has.
+__host__ __device__ __forceinline__ int digits_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
+__host__ __device__ __forceinline__ int64_t groups_of(int64_t in, int digits) { return (in + (1 << digits) - 1) >> digits; }
 
 // ---------------------------------------------------------------- packing
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -45,87 +48,201 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// The whole number next to w / s, halves to even: the quotient's rounding can only miss by one, which the remainder
-// (exact: both are multiples of the smaller one's last bit, and it is at most s) tells.
-__device__ __forceinline__ int code_of(float w, float s) {
+constexpr int kSegment = 2 * kBlock;  // k of a warp's turn: 8 a lane
+constexpr int kTurns = 2;             // of a warp, their loads in flight together
+
+// The whole number next to w / s (halves to even), in the lowest four bits of its two's complement; inv: 1 / s to 2^-22.
+// bf16: w inv corrected by its remainder is off by less than 2^-40, and not at all where the quotient is a half, as other
+// quotients of two bf16 values are 2^-12 away from one.
+__device__ __forceinline__ uint32_t code_of(__nv_bfloat16, float w, float s, float inv) {
+  const float y = __fmul_rn(w, inv);
+  return __float_as_uint(__fadd_rn(__fmaf_rn(__fmaf_rn(-s, y, w), inv, y), 12582912.f));
+}
+// fp32: the product can miss by one next to a half; the remainder (exact: both of its parts are multiples of the
+// smaller one's last bit, and it is at most s) tells.
+__device__ __forceinline__ uint32_t code_of(float, float w, float s, float inv) {
+  const float t = __fmaf_rn(w, inv, 12582912.f);
+  uint32_t q = __float_as_uint(t);
+  const float r = __fmaf_rn(-s, __fsub_rn(t, 12582912.f), w);
+  // Beyond a half, or at one from an odd number (beyond the value below it), one on towards the remainder.
+  const float most = __uint_as_float(__float_as_uint(0.5f * s) - (q & 1u));
+  if (fabsf(r) > most) q += static_cast<uint32_t>((__float_as_int(r) >> 31) | 1);
+  return q;
+}
+// The same for scales whose half or reciprocal fp32 does not hold: in 64 bits (the quotient of two fp32 values cannot
+// round onto a half in them), and clamped, since such a scale may be far from max / 7.
+__device__ __noinline__ uint32_t code_of_tiny(float w, float s) {
   if (s == 0.f || !(s < INFINITY)) return 0;  // 0 times an infinity or a NaN is a NaN
-  float q = rintf(__fdiv_rn(w, s));
-  const float r2 = 2.f * __fmaf_rn(-s, q, w);
-  const bool odd = (static_cast<int>(q) & 1) != 0;
-  if (r2 > s || (r2 == s && odd)) q += 1.f;
-  if (r2 < -s || (r2 == -s && odd)) q -= 1.f;
-  return static_cast<int>(fminf(fmaxf(q, -7.f), 7.f));
+  const double q = rint(static_cast<double>(w) / static_cast<double>(s));
+  return static_cast<uint32_t>(static_cast<int>(fmin(fmax(q, -7.0), 7.0)));
+}
+// max / 7 rounded once: the product with 1/7 corrected by its remainder; the quotient's own rounding where fp32 does not
+// hold that. (bf16's second rounding cannot meet a half between two values: seven of those are odd in nine bits.)
+__device__ __forceinline__ float seventh(float top) {
+  constexpr float inv = 1.f / 7.f;
+  const float y = __fmul_rn(top, inv);
+  return top >= 0x1p-90f && top < INFINITY ? __fmaf_rn(__fmaf_rn(-7.f, y, top), inv, y) : __fdiv_rn(top, 7.f);
+}
+__device__ __forceinline__ float largest(const float (&v)[8]) {
+  float top = 0.f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) top = max_nan(top, fabsf(v[q]));
+  return top;
 }
 
-// A warp a block of 128 k: lane l has the k 4 l .. 4 l + 3.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) pack_kernel(const T* w, int64_t out, int64_t in, int group, uint8_t* codes, T* scales, int vec) {
-  let_next();
-  after_previous();
-  const int lane = threadIdx.x & 31;
-  const int64_t blocks = blocks_of(in), groups = (in + group - 1) / group;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (at >= out * blocks) return;
-  const int64_t row = at / blocks, block = at % blocks;
-  const int64_t k = block * kBlock + lane * 4;
-  const T* from = w + row * in + k;
-  float v[4];
-  if (vec && k + 4 <= in) {
-    if constexpr (sizeof(T) == 2) {
-      const uint2 raw = __ldcs(reinterpret_cast<const uint2*>(from));
-      v[0] = __uint_as_float(raw.x << 16); v[1] = __uint_as_float(raw.x & 0xFFFF0000u);
-      v[2] = __uint_as_float(raw.y << 16); v[3] = __uint_as_float(raw.y & 0xFFFF0000u);
-    } else {
-      const float4 raw = __ldcs(reinterpret_cast<const float4*>(from));
-      v[0] = raw.x; v[1] = raw.y; v[2] = raw.z; v[3] = raw.w;
-    }
-  } else {
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = k + q < in ? value(fetch(from + q)) : 0.f;
+  for (int q = 0; q < 4; ++q) {
+    v[2 * q] = __uint_as_float(w[q] << 16);
+    v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
   }
-  float top = max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3])));
-  for (int o = group / 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  const T stored = narrow<T>(__fdiv_rn(top, 7.f));
-  const float s = value(stored);
-  if (lane % (group / 4) == 0 && k < in) scales[row * groups + k / group] = stored;
-  uint32_t c[4];
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) c[q] = static_cast<uint32_t>(code_of(v[q], s) + 8);
-  // Lane l: word l / 8 of lane l % 4's 16 bytes, its product (l / 4) % 2.
-  uint32_t word = c[0] | (c[2] << 4) | (c[1] << 16) | (c[3] << 20);
-  if (lane & 4) word <<= 8;
-  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-  if ((lane & 4) == 0)
-    *reinterpret_cast<uint32_t*>(codes + at * kBlockBytes + (lane & 3) * 16 + (lane >> 3) * 4) = word;
+  for (int q = 0; q < 4; ++q) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
+    w[q] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-// The same way back.
+// Segments of all rows one after the other, and how a warp finds its row: the quotient by a product with `inverse` (2^64 over
+// the segments of a row, rounded up), exact below 2^32 of them; hundreds of instructions for a division beyond.
+struct Places {
+  int64_t out, in, blocks, groups, segments;
+  unsigned long long inverse;
+  int digits, vec;
+  Places(int64_t rows, int64_t k, int group, bool aligned)
+      : out(rows), in(k), blocks(blocks_of(k)), groups(groups_of(k, digits_of(group))), segments((blocks + 1) / 2),
+        inverse(segments > 1 ? ~0ull / static_cast<unsigned long long>(segments) + 1 : 0), digits(digits_of(group)), vec(aligned) {}
+  int64_t items() const { return out * segments; }
+  __device__ __forceinline__ void find(int64_t at, int64_t* row, int64_t* segment) const {
+    *row = segments == 1 ? at
+           : at <= 0xFFFFFFFFll && segments <= 0xFFFFFFFFll
+               ? static_cast<int64_t>(__umul64hi(static_cast<unsigned long long>(at), inverse))
+               : at / segments;
+    *segment = at - *row * segments;
+  }
+};
+// Of the 256 k of a segment lane l has 8 l .. 8 l + 7: half a product's, for two of the four lanes that read a
+// block. Its word within the codes, once lanes l and l ^ 2 (the products of one word) have exchanged halves.
+__device__ __forceinline__ int word_of(int lane) {
+  const int p = (lane >> 1) & 7, t = 2 * (lane & 1) + (p & 1);
+  return (lane >> 4) * (kBlockBytes / 4) + t * 4 + (p >> 1);
+}
+
+// A warp a segment of a row; a group's lanes find its largest magnitude by shuffles. Bound by memory, and by instructions next
+// to it.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* codes, const T* scales, int64_t out, int64_t in, int group, T* w, int vec) {
+__global__ void __launch_bounds__(kThreads) pack_kernel(const T* w, uint8_t* codes, T* scales, const Places at) {
   let_next();
   after_previous();
   const int lane = threadIdx.x & 31;
-  const int64_t blocks = blocks_of(in), groups = (in + group - 1) / group;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (at >= out * blocks) return;
-  const int64_t row = at / blocks, block = at % blocks;
-  const int64_t k = block * kBlock + lane * 4;
-  if (k >= in) return;
-  uint32_t word = fetch(reinterpret_cast<const uint32_t*>(codes + at * kBlockBytes + (lane & 3) * 16 + (lane >> 3) * 4));
-  if (lane & 4) word >>= 8;
-  const float s = value(fetch(scales + row * groups + k / group));
-  const uint32_t c[4] = {word & 15u, (word >> 16) & 15u, (word >> 4) & 15u, (word >> 20) & 15u};
-  T v[4];
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kTurns;
+  float v[kTurns][8];
+  int64_t row[kTurns], k[kTurns];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) v[q] = narrow<T>(__fmul_rn(static_cast<float>(static_cast<int>(c[q]) - 8), s));
-  T* to = w + row * in + k;
-  if (vec && k + 4 <= in) {
-    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(v);
-    else *reinterpret_cast<float4*>(to) = *reinterpret_cast<const float4*>(v);
-  } else {
+  for (int u = 0; u < kTurns; ++u) {
+    int64_t segment;
+    at.find(first + u, &row[u], &segment);
+    k[u] = segment * kSegment + lane * 8;
+    const T* from = w + row[u] * at.in + k[u];
+    if (row[u] < at.out && at.vec && k[u] + 8 <= at.in) {
+      load8(from, v[u]);
+    } else {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (k + q < in) to[q] = v[q];
+      for (int q = 0; q < 8; ++q) v[u][q] = row[u] < at.out && k[u] + q < at.in ? value(fetch(from + q)) : 0.f;
+    }
+  }
+  const int digits = at.digits;
+#pragma unroll
+  for (int u = 0; u < kTurns; ++u) {
+    if (row[u] >= at.out) break;
+    float top = largest(v[u]);
+    for (int o = 1 << (digits - 4); o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const T stored = narrow<T>(seventh(top));
+    const float s = value(stored);
+    if ((lane & ((1 << (digits - 3)) - 1)) == 0 && k[u] < at.in) scales[row[u] * at.groups + (k[u] >> digits)] = stored;
+    uint32_t c[8];
+    if (s >= 0x1p-100f && s < INFINITY) {
+      const float inv = quick_reciprocal(s);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) c[q] = code_of(T(), v[u][q], s, inv) & 15u;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) c[q] = code_of_tiny(v[u][q], s) & 15u;
+    }
+    // The four codes for each of two reading lanes, of an even product; an odd one's lie 8 bits higher.
+    const uint32_t a = c[0] + c[2] * 16u + c[1] * 65536u + c[3] * 1048576u, b = c[4] + c[6] * 16u + c[5] * 65536u + c[7] * 1048576u;
+    const bool odd = (lane & 2) != 0;
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 2);
+    const uint32_t word = odd ? other | (b << 8) : a | (other << 8);
+    if (k[u] / kBlock < at.blocks)
+      *reinterpret_cast<uint32_t*>(codes + (row[u] * at.blocks + k[u] / kSegment * 2) * kBlockBytes + word_of(lane) * 4) = word ^ kNothing;
+  }
+}
+
+// The same way back. Rows that start off a lane's 16 bytes go through shared memory, from where a warp stores neighbours.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* codes, const T* scales, T* w, const Places at) {
+  __shared__ T staged[kWarps][kSegment];
+  let_next();
+  after_previous();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTurns;
+  uint32_t word[kTurns];
+  float s[kTurns];
+  int64_t row[kTurns], k[kTurns];
+#pragma unroll
+  for (int u = 0; u < kTurns; ++u) {
+    int64_t segment;
+    at.find(first + u, &row[u], &segment);
+    k[u] = segment * kSegment + lane * 8;
+    word[u] = kNothing;
+    s[u] = 0.f;
+    if (row[u] < at.out && k[u] / kBlock < at.blocks)
+      word[u] = __ldcs(reinterpret_cast<const uint32_t*>(codes + (row[u] * at.blocks + segment * 2) * kBlockBytes) + word_of(lane));
+    if (row[u] < at.out && k[u] < at.in) s[u] = value(fetch(scales + row[u] * at.groups + (k[u] >> at.digits)));
+  }
+#pragma unroll
+  for (int u = 0; u < kTurns; ++u) {
+    if (row[u] >= at.out) break;
+    const bool odd = (lane & 2) != 0;
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, word[u], 2);
+    const uint32_t a = odd ? other >> 8 : word[u], b = odd ? word[u] >> 8 : other;
+    // A nibble as the last bits of 2^23.
+    auto code = [](uint32_t v, int shift) { return __uint_as_float(((v >> shift) & 15u) | 0x4B000000u) - 8388616.f; };
+    float v[8] = {code(a, 0), code(a, 16), code(a, 4), code(a, 20), code(b, 0), code(b, 16), code(b, 4), code(b, 20)};
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = __fmul_rn(v[q], s[u]);
+    T* const to = w + row[u] * at.in + k[u];
+    if (at.vec && k[u] + 8 <= at.in) {
+      store8(to, v);
+    } else if (at.vec) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (k[u] + q < at.in) to[q] = narrow<T>(v[q]);
+    } else {
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < 8; ++q) staged[warp][lane * 8 + q] = narrow<T>(v[q]);
+      __syncwarp();
+      const int64_t k0 = k[u] - lane * 8;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (k0 + q * 32 + lane < at.in) to[q * 32 + lane - lane * 8] = staged[warp][q * 32 + lane];
+    }
   }
 }
 
@@ -143,112 +260,167 @@ __device__ __forceinline__ void product(float (&c)[4], const uint32_t (&a)[4], u
 }
 
 constexpr int kFeatures = 16;   // of a CTA
-constexpr int kDepth = 4;       // blocks of a warp in flight
-constexpr int kPad = 16;        // bf16 elements behind a column in shared memory: columns 32 bytes apart in the banks
 
 template <typename T>
 constexpr int kTerms = sizeof(T) == 2 ? 1 : 3;  // bf16 terms of a value of x, each in a column of its own
 
-// A CTA has 16 features, its warps blocks of their k in turn. kTiles: eights of columns (rows of x, times their terms).
-template <typename T, int kTiles>
-__global__ void __launch_bounds__(kThreads) packed_kernel(const PackedArgs a, int chunk) {
-  extern __shared__ __align__(16) uint8_t shared[];
-  __nv_bfloat16* const xs = reinterpret_cast<__nv_bfloat16*>(shared);
+template <typename T>
+struct FourOf { using Type = uint2; };
+template <>
+struct FourOf<float> { using Type = float4; };
+// Four values of x from k on, wherever the row starts, and those at or beyond `in` as zeros.
+__device__ __forceinline__ uint2 four_of(const __nv_bfloat16* x, int64_t k, int64_t in) {
+  uint32_t v[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = k + q < in ? static_cast<uint32_t>(__bfloat16_as_ushort(fetch(x + k + q))) : 0u;
+  return make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
+}
+__device__ __forceinline__ float4 four_of(const float* x, int64_t k, int64_t in) {
+  float v[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = k + q < in ? fetch(x + k + q) : 0.f;
+  return make_float4(v[0], v[1], v[2], v[3]);
+}
+// A lane's values of the eight products of a block, from p on, 16 apart: aligned, or (within the row's inside, since
+// whole words are read) from any address.
+template <typename T>
+__device__ __forceinline__ void aligned_block(const T* p, typename FourOf<T>::Type (&to)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) to[q] = fetch(reinterpret_cast<const typename FourOf<T>::Type*>(p + q * 16));
+}
+__device__ __forceinline__ void shifted_block(const float* p, float4 (&to)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) to[q] = make_float4(fetch(p + q * 16), fetch(p + q * 16 + 1), fetch(p + q * 16 + 2), fetch(p + q * 16 + 3));
+}
+__device__ __forceinline__ void shifted_block(const __nv_bfloat16* p, uint2 (&to)[8]) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const uint2* w = reinterpret_cast<const uint2*>(at & ~static_cast<uintptr_t>(7));
+  const bool word = (at & 4) != 0;
+  const uint32_t bits = (at & 2) * 8;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const uint2 a = fetch(w + q * 4), b = fetch(w + q * 4 + 1);
+    const uint32_t v0 = word ? a.y : a.x, v1 = word ? b.x : a.y, v2 = word ? b.y : b.x;
+    to[q] = make_uint2(__funnelshift_r(v0, v1, bits), __funnelshift_r(v1, v2, bits));
+  }
+}
+// Their operand: for fp32 the column's term of each, the leading bits taken off once or twice by masks.
+__device__ __forceinline__ uint2 operand(const uint2& v, uint32_t, uint32_t) { return v; }
+__device__ __forceinline__ uint2 operand(const float4& v, uint32_t once, uint32_t twice) {
+  auto one = [&](float x) {
+    x -= __uint_as_float(__float_as_uint(x) & once);
+    x -= __uint_as_float(__float_as_uint(x) & twice);
+    return __float_as_uint(x);
+  };
+  return make_uint2(join_terms(one(v.x), one(v.y)), join_terms(one(v.z), one(v.w)));
+}
+
+// A CTA has 16 features, each warp a stretch of their k. kTiles: eights of columns (rows of x, times their terms);
+// columns beyond the last repeat it, and nothing reads their results. Nothing is shared until the end: a warp's lanes read the
+// codes, scales and values of x that their fragments take.
+template <typename T, int kTiles, int kDigits>
+__global__ void __launch_bounds__(kThreads, 2) packed_kernel(const PackedArgs a, int per, int vec) {
+  constexpr int kWide = kTiles * 8 + 1;
+  constexpr int kPerBlock = kBlock >> kDigits;        // groups of a block
+  constexpr int kProducts = 1 << (kDigits - 4);       // products of a group
+  __shared__ float parts[kWarps][kFeatures][kWide];
   let_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int rows = static_cast<int>(a.rows), cols = rows * kTerms<T>;
-  const int pitch = chunk + kPad;
   const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kFeatures;
-  const int64_t blocks = blocks_of(a.in), groups = (a.in + a.group - 1) / a.group;
+  const int64_t blocks = blocks_of(a.in), groups = groups_of(a.in, kDigits);
+  const int64_t first = static_cast<int64_t>(warp) * per;
+  const int count = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(per), blocks - first)));
   const bool there[2] = {j0 + g < a.out, j0 + g + 8 < a.out};
-  const uint8_t* const codes = a.codes + (j0 + g) * blocks * kBlockBytes + t * 16;
+  const uint8_t* const codes = a.codes + ((j0 + g) * blocks + first) * kBlockBytes + t * 16;
+  const int64_t group0 = first * kPerBlock + (t & (kPerBlock - 1));  // lane t of four reads the scale of group t
   const T* const scales = static_cast<const T*>(a.scales) + (j0 + g) * groups;
+  // While the kernel before this one ends, the warp's first codes are asked for into L2 (a hint that reads nothing): a
+  // lane takes one of the first two lines of a feature.
+  if (j0 + (lane >> 1) < a.out && (lane & 1) * 2 < count)
+    prefetch(a.codes + ((j0 + (lane >> 1)) * blocks + first + (lane & 1) * 2) * kBlockBytes);
+  const T* from[kTiles];
+  uint32_t once[kTiles], twice[kTiles];
+#pragma unroll
+  for (int n = 0; n < kTiles; ++n) {
+    const int col = min(n * 8 + g, cols - 1);
+    from[n] = static_cast<const T*>(a.x) + col / kTerms<T> * a.in + first * kBlock + t * 4;
+    once[n] = col % kTerms<T> >= 1 ? 0xFFFF0000u : 0u;
+    twice[n] = col % kTerms<T> >= 2 ? 0xFFFF0000u : 0u;
+  }
   after_previous();
   float sum[kTiles][4] = {};
-  for (int64_t k0 = 0; k0 < a.in; k0 += chunk) {
-    const int64_t first = k0 / kBlock;
-    const int count = static_cast<int>(min(static_cast<int64_t>(chunk / kBlock), blocks - first));
-    bool staged = false;
-    for (int base = 0; base < count; base += kWarps * kDepth) {
-      uint4 c[kDepth][2];
+  constexpr int kInFlight = 2;
+  for (int base = 0; base < count; base += kInFlight) {
+    uint4 c[kInFlight][2];
+    T s[kInFlight][2];
 #pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        const int b = base + d * kWarps + warp;
+    for (int d = 0; d < kInFlight; ++d) {
+      const bool in = base + d < count;
+      const int64_t at = group0 + static_cast<int64_t>(base + d) * kPerBlock;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (b < count && there[h])
-            c[d][h] = __ldcs(reinterpret_cast<const uint4*>(codes + ((first + b) + h * 8 * blocks) * kBlockBytes));
-          else
-            c[d][h] = make_uint4(kNothing, kNothing, kNothing, kNothing);
-        }
+      for (int h = 0; h < 2; ++h) {
+        c[d][h] = make_uint4(kNothing, kNothing, kNothing, kNothing);
+        if (in && there[h]) c[d][h] = __ldcs(reinterpret_cast<const uint4*>(codes + (base + d + h * 8 * blocks) * kBlockBytes));
+        s[d][h] = narrow<T>(0.f);
+        if (in && there[h] && at < groups) s[d][h] = fetch(scales + h * 8 * groups + at);
       }
-      if (!staged) {
-        // The chunk's part of x, while the codes are on their way.
-        staged = true;
-        __syncthreads();
-        const T* const x = static_cast<const T*>(a.x);
-        for (int i = threadIdx.x; i < rows * chunk; i += kThreads) {
-          const int r = i / chunk, k = i % chunk;
-          const T v = k0 + k < a.in ? fetch(x + r * a.in + k0 + k) : narrow<T>(0.f);
-          if constexpr (kTerms<T> == 1) {
-            xs[r * pitch + k] = v;
-          } else {
-            uint32_t terms[3];
-            split3(v, terms);
+    }
 #pragma unroll
-            for (int q = 0; q < 3; ++q) xs[(r * 3 + q) * pitch + k] = __ushort_as_bfloat16(static_cast<unsigned short>(terms[q] >> 16));
-          }
-        }
-        __syncthreads();
+    for (int d = 0; d < kInFlight; ++d) {
+      if (base + d >= count) break;
+      const uint32_t w0[4] = {c[d][0].x, c[d][0].y, c[d][0].z, c[d][0].w}, w1[4] = {c[d][1].x, c[d][1].y, c[d][1].z, c[d][1].w};
+      auto decoded = [&](int p, uint32_t (&op)[4]) {  // of a product of 16 k
+        const int shift = (p & 1) * 8;
+        op[0] = decode(w0[p >> 1], shift);
+        op[1] = decode(w1[p >> 1], shift);
+        op[2] = decode(w0[p >> 1], shift + 4);
+        op[3] = decode(w1[p >> 1], shift + 4);
+      };
+      uint32_t ops[kTiles > 1 ? 8 : 1][4];  // kept where more than one tile takes them
+      if constexpr (kTiles > 1) {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) decoded(p, ops[p]);
       }
+      const float s0 = value(s[d][0]), s1 = value(s[d][1]);
+      const int64_t k = (first + base + d) * kBlock;
 #pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        const int b = base + d * kWarps + warp;
-        if (b >= count) break;
-        float part[kTiles][4];
+      for (int n = 0; n < kTiles; ++n) {
+        typename FourOf<T>::Type x[8];
+        const T* const p0 = from[n] + (base + d) * kBlock;
+        if (vec && k + kBlock <= a.in) {
+          aligned_block(p0, x);
+        } else if (k > 0 && k + kBlock + 4 <= a.in) {
+          shifted_block(p0, x);
+        } else {
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {  // products of 16 k
-          if (p * 16 % a.group == 0) {
+          for (int p = 0; p < 8; ++p) x[p] = four_of(p0 - t * 4 - k, k + p * 16 + t * 4, a.in);
+        }
+        float part[4];
 #pragma unroll
-            for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) part[n][q] = 0.f;
-          }
-          const uint32_t w0[4] = {c[d][0].x, c[d][0].y, c[d][0].z, c[d][0].w}, w1[4] = {c[d][1].x, c[d][1].y, c[d][1].z, c[d][1].w};
-          const int shift = (p & 1) * 8;
-          const uint32_t op[4] = {decode(w0[p >> 1], shift), decode(w1[p >> 1], shift), decode(w0[p >> 1], shift + 4),
-                                  decode(w1[p >> 1], shift + 4)};
-#pragma unroll
-          for (int n = 0; n < kTiles; ++n) {
-            uint2 xv = make_uint2(0u, 0u);
-            if (n * 8 + g < cols) xv = *reinterpret_cast<const uint2*>(xs + (n * 8 + g) * pitch + b * kBlock + p * 16 + t * 4);
-            product(part[n], op, xv.x, xv.y);
-          }
-          if ((p * 16 + 16) % a.group == 0) {
-            const int64_t at = ((first + b) * kBlock + p * 16) / a.group;
-            const float s0 = there[0] && at < groups ? value(fetch(scales + at)) : 0.f;
-            const float s1 = there[1] && at < groups ? value(fetch(scales + 8 * groups + at)) : 0.f;
-#pragma unroll
-            for (int n = 0; n < kTiles; ++n) {
-              sum[n][0] = fmaf(part[n][0], s0, sum[n][0]);
-              sum[n][1] = fmaf(part[n][1], s0, sum[n][1]);
-              sum[n][2] = fmaf(part[n][2], s1, sum[n][2]);
-              sum[n][3] = fmaf(part[n][3], s1, sum[n][3]);
-            }
+        for (int p = 0; p < 8; ++p) {
+          if (p % kProducts == 0) part[0] = part[1] = part[2] = part[3] = 0.f;
+          const uint2 b = operand(x[p], once[n], twice[n]);
+          if constexpr (kTiles == 1) decoded(p, ops[0]);
+          product(part, ops[kTiles > 1 ? p : 0], b.x, b.y);
+          if (p % kProducts == kProducts - 1) {
+            const float f0 = kPerBlock == 1 ? s0 : __shfl_sync(0xFFFFFFFFu, s0, p / kProducts, 4);
+            const float f1 = kPerBlock == 1 ? s1 : __shfl_sync(0xFFFFFFFFu, s1, p / kProducts, 4);
+            sum[n][0] = fmaf(part[0], f0, sum[n][0]);
+            sum[n][1] = fmaf(part[1], f0, sum[n][1]);
+            sum[n][2] = fmaf(part[2], f1, sum[n][2]);
+            sum[n][3] = fmaf(part[3], f1, sum[n][3]);
           }
         }
       }
     }
   }
   // The warps' sums, in order.
-  constexpr int kWide = kTiles * 8 + 1;
-  float* const parts = reinterpret_cast<float*>(shared);  // [kWarps][kFeatures][kWide]
-  __syncthreads();
 #pragma unroll
   for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) parts[(warp * kFeatures + g + (q >> 1) * 8) * kWide + n * 8 + t * 2 + (q & 1)] = sum[n][q];
+    for (int q = 0; q < 4; ++q) parts[warp][g + (q >> 1) * 8][n * 8 + t * 2 + (q & 1)] = sum[n][q];
   __syncthreads();
   for (int i = threadIdx.x; i < rows * kFeatures; i += kThreads) {
     const int r = i / kFeatures, f = i % kFeatures;
@@ -258,7 +430,8 @@ __global__ void __launch_bounds__(kThreads) packed_kernel(const PackedArgs a, in
 #pragma unroll
     for (int q = kTerms<T> - 1; q >= 0; --q) {  // the smallest terms first
       float v = 0.f;
-      for (int w = 0; w < kWarps; ++w) v += parts[(w * kFeatures + f) * kWide + r * kTerms<T> + q];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v += parts[w][f][r * kTerms<T> + q];
       z[0] += v;
     }
     if (a.b != nullptr)
@@ -270,19 +443,23 @@ __global__ void __launch_bounds__(kThreads) packed_kernel(const PackedArgs a, in
   }
 }
 
+bool fits(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+template <typename T, int kTiles, int kDigits>
+cudaError_t run_digits(const PackedArgs& a, cudaStream_t stream) {
+  const int64_t grid = (a.out + kFeatures - 1) / kFeatures, per = (blocks_of(a.in) + kWarps - 1) / kWarps;
+  if (grid > 0x7FFFFFFFll || per > 0x3FFFFFFFll) return cudaErrorInvalidConfiguration;
+  const int vec = a.in % 4 == 0 && fits(a.x, 4 * sizeof(T));
+  return launch_overlapped(packed_kernel<T, kTiles, kDigits>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream, a,
+                           static_cast<int>(per), vec);
+}
 template <typename T, int kTiles>
 cudaError_t run_tiles(const PackedArgs& a, cudaStream_t stream) {
-  static SmemRecord record;
-  const int cols = static_cast<int>(a.rows) * kTerms<T>;
-  // As much of k at once as 96 KB of x take.
-  const int64_t fit = (96 * 1024 / (2 * cols) - kPad) / kBlock * kBlock;
-  const int chunk = static_cast<int>(std::min(fit, blocks_of(a.in) * kBlock));
-  const size_t smem = std::max<size_t>(static_cast<size_t>(cols) * (chunk + kPad) * 2, sizeof(float) * kWarps * kFeatures * (kTiles * 8 + 1));
-  const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(packed_kernel<T, kTiles>), smem, record);
-  if (err != cudaSuccess) return err;
-  const int64_t grid = (a.out + kFeatures - 1) / kFeatures;
-  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  return launch_overlapped(packed_kernel<T, kTiles>, dim3(static_cast<unsigned>(grid)), kThreads, 0, smem, stream, a, chunk);
+  switch (digits_of(a.group)) {
+    case 5: return run_digits<T, kTiles, 5>(a, stream);
+    case 6: return run_digits<T, kTiles, 6>(a, stream);
+    default: return run_digits<T, kTiles, 7>(a, stream);
+  }
 }
 
 template <typename T>
@@ -290,31 +467,28 @@ cudaError_t run_packed(const PackedArgs& a, cudaStream_t stream) {
   const int64_t cols = a.rows * kTerms<T>;
   if (cols <= 8) return run_tiles<T, 1>(a, stream);
   if (cols <= 16) return run_tiles<T, 2>(a, stream);
-  if (cols <= 32) return run_tiles<T, 4>(a, stream);
-  return run_tiles<T, 8>(a, stream);
+  return run_tiles<T, 4>(a, stream);
 }
-
-bool fits(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 template <typename T>
 cudaError_t pack_typed(const void* w, int64_t out, int64_t in, int group, uint8_t* codes, void* scales, cudaStream_t stream) {
-  const int64_t grid = (out * blocks_of(in) + kWarps - 1) / kWarps;
+  const Places at(out, in, group, in % 8 == 0 && fits(w, 16));
+  const int64_t grid = (at.items() + kWarps * kTurns - 1) / (kWarps * kTurns);
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  const int vec = in % 4 == 0 && fits(w, 4 * sizeof(T));
-  return launch_overlapped(pack_kernel<T>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream, static_cast<const T*>(w), out, in,
-                           group, codes, static_cast<T*>(scales), vec);
+  return launch_overlapped(pack_kernel<T>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream, static_cast<const T*>(w), codes,
+                           static_cast<T*>(scales), at);
 }
 template <typename T>
 cudaError_t unpack_typed(const uint8_t* codes, const void* scales, int64_t out, int64_t in, int group, void* w, cudaStream_t stream) {
-  const int64_t grid = (out * blocks_of(in) + kWarps - 1) / kWarps;
+  const Places at(out, in, group, in % 8 == 0 && fits(w, 16));
+  const int64_t grid = (at.items() + kWarps * kTurns - 1) / (kWarps * kTurns);
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  const int vec = in % 4 == 0 && fits(w, 4 * sizeof(T));
   return launch_overlapped(unpack_kernel<T>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream, codes,
-                           static_cast<const T*>(scales), out, in, group, static_cast<T*>(w), vec);
+                           static_cast<const T*>(scales), static_cast<T*>(w), at);
 }
 
 // The most rows that the kernel on packed weights takes.
-int64_t few_rows(vn_dtype dt) { return dt == VN_BF16 ? 64 : 21; }
+int64_t few_rows(vn_dtype dt) { return dt == VN_BF16 ? 32 : 10; }
 
 int64_t padded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
