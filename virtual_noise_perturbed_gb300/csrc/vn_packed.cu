@@ -49,7 +49,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 constexpr int kSegment = 2 * kBlock;  // k of a warp's turn: 8 a lane
-constexpr int kTurns = 2;             // of a warp, their loads in flight together
+// Segments of a warp, their loads in flight together: 67 M weights in bf16 (fp32) take, to pack, 66 us (78) with one, 73 (75)
+// with two, 88 (77) with four; back 48 (51), 43 (46), 42 (46).
+constexpr int kPackTurns = 1, kUnpackTurns = 2;
 
 // The whole number next to w / s (halves to even), in the lowest four bits of its two's complement; inv: 1 / s to 2^-22.
 // bf16: w inv corrected by its remainder is off by less than 2^-40, and not at all where the quotient is a half, as other
@@ -149,11 +151,11 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const T* w, uint8_t* cod
   let_next();
   after_previous();
   const int lane = threadIdx.x & 31;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kTurns;
-  float v[kTurns][8];
-  int64_t row[kTurns], k[kTurns];
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kPackTurns;
+  float v[kPackTurns][8];
+  int64_t row[kPackTurns], k[kPackTurns];
 #pragma unroll
-  for (int u = 0; u < kTurns; ++u) {
+  for (int u = 0; u < kPackTurns; ++u) {
     int64_t segment;
     at.find(first + u, &row[u], &segment);
     k[u] = segment * kSegment + lane * 8;
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const T* w, uint8_t* cod
   }
   const int digits = at.digits;
 #pragma unroll
-  for (int u = 0; u < kTurns; ++u) {
+  for (int u = 0; u < kPackTurns; ++u) {
     if (row[u] >= at.out) break;
     float top = largest(v[u]);
     for (int o = 1 << (digits - 4); o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
@@ -200,12 +202,12 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* codes, 
   let_next();
   after_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTurns;
-  uint32_t word[kTurns];
-  float s[kTurns];
-  int64_t row[kTurns], k[kTurns];
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kUnpackTurns;
+  uint32_t word[kUnpackTurns];
+  float s[kUnpackTurns];
+  int64_t row[kUnpackTurns], k[kUnpackTurns];
 #pragma unroll
-  for (int u = 0; u < kTurns; ++u) {
+  for (int u = 0; u < kUnpackTurns; ++u) {
     int64_t segment;
     at.find(first + u, &row[u], &segment);
     k[u] = segment * kSegment + lane * 8;
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* codes, 
     if (row[u] < at.out && k[u] < at.in) s[u] = value(fetch(scales + row[u] * at.groups + (k[u] >> at.digits)));
   }
 #pragma unroll
-  for (int u = 0; u < kTurns; ++u) {
+  for (int u = 0; u < kUnpackTurns; ++u) {
     if (row[u] >= at.out) break;
     const bool odd = (lane & 2) != 0;
     const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, word[u], 2);
@@ -473,7 +475,7 @@ cudaError_t run_packed(const PackedArgs& a, cudaStream_t stream) {
 template <typename T>
 cudaError_t pack_typed(const void* w, int64_t out, int64_t in, int group, uint8_t* codes, void* scales, cudaStream_t stream) {
   const Places at(out, in, group, in % 8 == 0 && fits(w, 16));
-  const int64_t grid = (at.items() + kWarps * kTurns - 1) / (kWarps * kTurns);
+  const int64_t grid = (at.items() + kWarps * kPackTurns - 1) / (kWarps * kPackTurns);
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   return launch_overlapped(pack_kernel<T>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream, static_cast<const T*>(w), codes,
                            static_cast<T*>(scales), at);
@@ -481,7 +483,7 @@ cudaError_t pack_typed(const void* w, int64_t out, int64_t in, int group, uint8_
 template <typename T>
 cudaError_t unpack_typed(const uint8_t* codes, const void* scales, int64_t out, int64_t in, int group, void* w, cudaStream_t stream) {
   const Places at(out, in, group, in % 8 == 0 && fits(w, 16));
-  const int64_t grid = (at.items() + kWarps * kTurns - 1) / (kWarps * kTurns);
+  const int64_t grid = (at.items() + kWarps * kUnpackTurns - 1) / (kWarps * kUnpackTurns);
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   return launch_overlapped(unpack_kernel<T>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream, codes,
                            static_cast<const T*>(scales), static_cast<T*>(w), at);

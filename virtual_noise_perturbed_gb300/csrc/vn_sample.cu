@@ -21,6 +21,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "vn_act.cuh"
 #include "vn_internal.h"
 #include "vn_launch.cuh"
 
@@ -391,20 +392,32 @@ __global__ void __launch_bounds__(kThreads) warp_kernel(const Rows a) {
 template <typename T>
 constexpr int kVec = 16 / static_cast<int>(sizeof(T));  // logits of 16 bytes
 
+// Bins of a sixteenth of a binary order of the weights, the last one with all that is below; padded in shared memory,
+// so that lanes with sixteen neighbours each read from different banks.
+constexpr int kFine = 512;
+__device__ __forceinline__ int fine_place(int bin) { return bin + (bin >> 4); }
+constexpr int kFinePlaces = kFine + kFine / 16;
+constexpr int kCap = 1024;  // logits that a border is looked for among, one by one
+constexpr int kFew = kThreads;  // with no more than these left, a thread has one of them
+
 // A CTA's shared memory but for its logits.
 struct Shared {
   u64 powers[32];
   u64 sums[kBins];
   uint32_t counts[kBins];
-  u64 warps[2][kWarps];   // of the two reductions at work at most
-  u64 mine[2];            // what this CTA hands to the others of its cluster
-  float warps_max[kWarps];
-  uint32_t warps_key[2][kWarps];
+  uint32_t fine[kFine];
+  float merged[kFinePlaces];  // `fine` over all ranks: counts' bits, or sums
+  u64 list[kCap];             // logits as key and complement of the index: the larger, the earlier in the order
+  u64 list_weights[kCap];
+  uint32_t list_count;
+  u64 edge[2];                // the last one kept, by count and by sum: a rank may still read the one when the other is cleared
+  u64 warps[2][kWarps];       // of the two reductions at work at most
+  u64 few[2][kWarps];
+  u64 mine[2];                // what this CTA hands to the others of its cluster
   // Of the bin that a border falls into:
-  int bin;
-  u64 above_sum, bin_sum, target;
+  int bin, last_bin;
+  u64 above_sum, target;
   uint32_t above_count, bin_count;
-  uint32_t low, high;
 };
 
 // A row's share in a CTA: `vectors` 16-byte words a lane from `mine` on, 32 apart, position = word * kVec + element.
@@ -609,11 +622,12 @@ __device__ __forceinline__ void clear_bins(Shared& s) {
 }
 
 // Cuts `kept` to its first `count` logits, or (by_sum) to those before which less than top_p of its sum lies.
+// Out of line: it is the way for more logits next to a border than kCap, many equal ones above all.
 template <typename T, bool kCluster>
-__device__ __forceinline__ void cut(Team<kCluster>& team, const Part<T>& part, float m, const Wish& w, Kept* kept, bool by_sum, u64 count,
-                                    double top_p) {
-  Shared& s = team.s;
-  const Kept in = *kept;
+__device__ __noinline__ Kept cut(Shared& s, const Part<T> part, float m, const Wish w, const Kept in, bool by_sum, u64 count, double top_p) {
+  Team<kCluster> team(s);
+  __syncthreads();  // its reductions take their places from the first again
+  Kept kept;
   uint32_t low = kLowest, high = kAll;  // keys of the bin
   u64 target = count, above = 0;        // still to be reached within it, and ahead of it
   if (!by_sum && count == 1) {
@@ -675,8 +689,8 @@ __device__ __forceinline__ void cut(Team<kCluster>& team, const Part<T>& part, f
     }
   }
   // Of the logits with that key, how many, and the index of the last one.
-  kept->key = high;
-  kept->last = 0x7FFFFFFF;
+  kept.key = high;
+  kept.last = 0x7FFFFFFF;
   const float edge = __uint_as_float(high & 0x80000000u ? high ^ 0x80000000u : ~high);
   u64 ties = target - above;
   if (by_sum) {
@@ -695,16 +709,243 @@ __device__ __forceinline__ void cut(Team<kCluster>& team, const Part<T>& part, f
            }
          });
     team.sync();
-    kept->last = s.bin;
+    kept.last = s.bin;
     team.sync();
   } else if (in.key == high) {
-    kept->last = in.last;
+    kept.last = in.last;
   }
+  team.sync();
+  return kept;
+}
+
+// A logit's bin, and how far into it (in bins) it lies.
+struct Fine {
+  float m, scale;
+  __device__ __forceinline__ Fine(float top, const Wish& w) : m(top), scale(0.5f * w.ch) {}
+  __device__ __forceinline__ int bin(float x, float* into) const {
+    const float f = x == m ? 0.f : __fmul_rn(__fsub_rn(m, x), scale);
+    const int b = min(kFine - 1, __float2int_rd(f));
+    *into = f - static_cast<float>(b);
+    return b;
+  }
+  __device__ __forceinline__ int bin(float x) const {
+    return x == m ? 0 : min(kFine - 1, __float2int_rd(__fmul_rn(__fsub_rn(m, x), scale)));
+  }
+};
+__device__ __forceinline__ u64 item_of(uint32_t key, int at) { return static_cast<u64>(key) << 32 | static_cast<uint32_t>(~at); }
+__device__ __forceinline__ uint32_t item_key(u64 item) { return static_cast<uint32_t>(item >> 32); }
+__device__ __forceinline__ int item_index(u64 item) { return static_cast<int>(~static_cast<uint32_t>(item)); }
+__device__ __forceinline__ float value_of_key(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+
+// Counts of the kept logits, or (kSums) their weights, in s.merged over all ranks. A sum is held per CTA in 32 bits, in units of
+// 2^-bits of the largest weight of its bin, good to 2^-13 in all.
+template <bool kSums, typename T, bool kCluster>
+__device__ __forceinline__ void fill_bins(Team<kCluster>& team, const Part<T>& part, const Fine& fine, const Kept& in, int bits) {
+  Shared& s = team.s;
+  for (int b = threadIdx.x; b < kFine; b += kThreads) s.fine[b] = 0;
+  if (threadIdx.x == 0) {
+    s.list_count = 0;
+    s.edge[kSums] = 0;
+  }
+  __syncthreads();
+  const float unit = static_cast<float>(1 << bits);
+  part.each([&](float x, int at) {
+    if (!in.holds(key_of(x), at)) return;
+    float into;
+    const int b = fine.bin(x, &into);
+    atomicAdd(&s.fine[b], kSums ? static_cast<uint32_t>(__float2int_rn(unit * quick_exp2(into * -0.0625f))) : 1u);
+  });
+  team.sync();
+  for (int b = threadIdx.x; b < kFine; b += kThreads) {
+    float sum = 0.f;
+    uint32_t count = 0;
+    for (int r = 0; r < team.ranks; ++r) {
+      const uint32_t v = team.of_rank(&s.fine[b], r);
+      count += v;
+      sum += static_cast<float>(v);
+    }
+    s.merged[fine_place(b)] = kSums ? sum * quick_exp2(static_cast<float>(b) * -0.0625f) : __uint_as_float(count);
+  }
+  __syncthreads();
+}
+
+// By count: the bin that the logit number `target` (from 1) of the order is in.
+template <bool kCluster>
+__device__ __forceinline__ void find_count(Team<kCluster>& team, uint32_t target) {
+  Shared& s = team.s;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    uint32_t own[kFine / 32], total = 0;
+#pragma unroll
+    for (int b = 0; b < kFine / 32; ++b) {
+      own[b] = __float_as_uint(s.merged[fine_place(lane * (kFine / 32) + b)]);
+      total += own[b];
+    }
+    uint32_t scan = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(kAll, scan, o);
+      if (lane >= o) scan += t;
+    }
+    const uint32_t reach = __ballot_sync(kAll, scan >= target);
+    if (reach != 0 && lane == __ffs(reach) - 1) {
+      uint32_t at = scan - total;
+      bool found = false;
+#pragma unroll
+      for (int b = 0; b < kFine / 32; ++b) {
+        if (!found && at + own[b] >= target) {
+          found = true;
+          s.bin = s.last_bin = lane * (kFine / 32) + b;
+          s.above_count = at;
+          s.bin_count = own[b];
+        }
+        at += own[b];
+      }
+    }
+  }
+  team.sync();
+}
+// By sum: the bins that the border of top_p may be in, whatever the sums' error does to them.
+template <bool kCluster>
+__device__ __forceinline__ void find_sum(Team<kCluster>& team, double top_p) {
+  Shared& s = team.s;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    float own[kFine / 32], total = 0.f;
+#pragma unroll
+    for (int b = 0; b < kFine / 32; ++b) {
+      own[b] = s.merged[fine_place(lane * (kFine / 32) + b)];
+      total += own[b];
+    }
+    float scan = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float t = __shfl_up_sync(kAll, scan, o);
+      if (lane >= o) scan += t;
+    }
+    const float border = __shfl_sync(kAll, scan, 31) * static_cast<float>(top_p);
+    const float early = border * (1.f - 0x1p-11f), late = border * (1.f + 0x1p-11f);
+    if (lane == 0) {
+      s.bin = 0;
+      s.last_bin = kFine - 1;
+    }
+    __syncwarp();
+    int first = kFine, last = kFine;
+    float at = scan - total;
+#pragma unroll
+    for (int b = 0; b < kFine / 32; ++b) {
+      at += own[b];
+      if (at >= early) first = min(first, lane * (kFine / 32) + b);
+      if (at >= late) last = min(last, lane * (kFine / 32) + b);
+    }
+    first = static_cast<int>(__reduce_min_sync(kAll, static_cast<unsigned>(first)));
+    last = static_cast<int>(__reduce_min_sync(kAll, static_cast<unsigned>(last)));
+    if (lane == 0) {
+      s.bin = min(first, kFine - 1);
+      s.last_bin = min(last, kFine - 1);
+    }
+  }
+  team.sync();
+}
+
+// The kept logits of bins first .. last into rank 0's list; how many there are (beyond kCap only counted).
+template <typename T, bool kCluster>
+__device__ __forceinline__ uint32_t collect(Team<kCluster>& team, const Part<T>& part, const Fine& fine, const Kept& in, int first, int last) {
+  Shared* s = &team.s;
+  if constexpr (kCluster) s = cg::this_cluster().map_shared_rank(&team.s, 0);
+  part.each([&](float x, int at) {
+    const uint32_t key = key_of(x);
+    if (key < kLowest) return;
+    const int b = fine.bin(x);
+    if (b < first || b > last || !in.holds(key, at)) return;
+    const uint32_t to = atomicAdd(&s->list_count, 1u);
+    if (to < kCap) s->list[to] = item_of(key, at);
+  });
+  team.sync();
+  return team.of_rank(&team.s.list_count, 0);
+}
+
+// The sum over a CTA's threads (not over its cluster).
+__device__ __forceinline__ u64 cta_sum(Shared& s, int place, u64 v) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) s.few[place][threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) v += s.few[place][i];
+  return v;
+}
+
+// All of the rest for at most kFew logits that s.list holds, the first top_k of the order among them: a thread has one,
+// and its place in either order, and what lies before it, from a look at every other.
+__device__ __forceinline__ void few(Shared& s, const Rows& a, int64_t row, float m, const Wish& w, int count) {
+  const int i = threadIdx.x;
+  const bool there = i < count;
+  const u64 item = there ? s.list[i] : 0;
+  const float x = value_of_key(item_key(item));
+  const u64 full = there ? weight(x, m, w, s.powers) : 0;
+  if (there) s.list_weights[i] = full;
+  __syncthreads();
+  int64_t rank = 0;
+  u64 before = 0;
+  if (there) {
+    for (int j = 0; j < count; ++j) {
+      const bool earlier = s.list[j] > item;
+      rank += earlier;
+      before += earlier ? s.list_weights[j] : 0;
+    }
+  }
+  bool kept = there && rank < w.top_k;
+  const u64 all = cta_sum(s, 0, kept ? full : 0);
+  if (w.top_p < 1.0) kept = kept && (rank == 0 || before < nucleus(w.top_p, all));
+  if (w.min_p > 0.f) kept = kept && Floor(m, w).above(x, m, w, s.powers);
+  const u64 mine = kept ? full : 0;
+  if (there) s.list_weights[i] = mine;  // every thread has passed the sum above: nobody reads the old ones
+  const u64 total = cta_sum(s, 1, mine);
+  if (!kept) return;
+  const u64 r = share(w.u, total);
+  u64 up_to = 0;
+  for (int j = 0; j < count; ++j)
+    if (item_index(s.list[j]) <= item_index(item)) up_to += s.list_weights[j];
+  if (up_to > r && up_to - mine <= r) {
+    a.index[row] = item_index(item);
+    if (a.logprob != nullptr) a.logprob[row] = logprob_of(x, m, w, total);
+  }
+}
+
+// Of `count` logits in rank 0's list the one with `rank` others before it, or (by_sum) the one in which the sum passes
+// `target`, `above` lying before all of the list: where the prefix ends. 0 if there is none.
+template <bool kCluster>
+__device__ __forceinline__ u64 find_edge(Team<kCluster>& team, int count, bool by_sum, uint32_t rank, u64 above, u64 target, float m,
+                                         const Wish& w) {
+  Shared& s = team.s;
+  if (team.rank == 0) {
+    if (by_sum) {
+      for (int i = threadIdx.x; i < count; i += kThreads)
+        s.list_weights[i] = weight(value_of_key(item_key(s.list[i])), m, w, s.powers);
+      __syncthreads();
+    }
+    for (int i = threadIdx.x; i < count; i += kThreads) {
+      const u64 item = s.list[i];
+      uint32_t place = 0;
+      u64 before = above;
+      for (int j = 0; j < count; ++j) {
+        const bool earlier = s.list[j] > item;
+        place += earlier;
+        if (by_sum) before += earlier ? s.list_weights[j] : 0;
+      }
+      if (by_sum ? before < target && before + s.list_weights[i] >= target : place == rank) s.edge[by_sum] = item;
+    }
+  }
+  team.sync();
+  return team.of_rank(&s.edge[by_sum], 0);
 }
 
 // per: 16-byte words of a warp's lane; the CTA's logits take kWarps * 32 * per of them.
 template <typename T, bool kCluster>
-__global__ void __launch_bounds__(kThreads) cta_kernel(const Rows a, int per) {
+__global__ void __launch_bounds__(kThreads, 3) cta_kernel(const Rows a, int per) {
   extern __shared__ uint4 logits[];
   __shared__ Shared s;
   let_next();
@@ -712,6 +953,8 @@ __global__ void __launch_bounds__(kThreads) cta_kernel(const Rows a, int per) {
   Team<kCluster> team(s);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = static_cast<int>(a.n);
+  // So that no bin's sum passes 32 bits.
+  const int bits = min(16, __clz(per * kThreads * kVec<T>) - 1);
   after_previous();
   for (int64_t row = blockIdx.x / team.ranks; row < a.rows; row += gridDim.x / team.ranks) {
     const T* x = static_cast<const T*>(a.x) + row * n;
@@ -723,19 +966,30 @@ __global__ void __launch_bounds__(kThreads) cta_kernel(const Rows a, int per) {
     part.words = per;
     part.first = ((team.rank * kWarps + warp) * per * 32 + lane) * kVec<T> - shift;
     float m = -INFINITY;
-    for (int it = 0; it < per; ++it) {
-      const int at = part.first + it * 32 * kVec<T>;
-      if (at >= 0 && at + kVec<T> <= n) {
-        mine[it * 32] = __ldcs(reinterpret_cast<const uint4*>(x + at));
-      } else {
-        T* to = reinterpret_cast<T*>(mine + it * 32);
-        for (int q = 0; q < kVec<T>; ++q) {
-          if (at + q >= 0 && at + q < n) {
-            to[q] = fetch(x + at + q);
-          } else if constexpr (sizeof(T) == 2) {
-            reinterpret_cast<uint16_t*>(to)[q] = 0xFFFFu;
-          } else {
-            reinterpret_cast<uint32_t*>(to)[q] = 0xFFFFFFFFu;
+    constexpr int kBatch = 4;  // words of a lane in flight
+    for (int it0 = 0; it0 < per; it0 += kBatch) {
+      uint4 raw[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int at = part.first + (it0 + u) * 32 * kVec<T>;
+        if (it0 + u < per && at >= 0 && at + kVec<T> <= n) raw[u] = __ldcs(reinterpret_cast<const uint4*>(x + at));
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int at = part.first + (it0 + u) * 32 * kVec<T>;
+        if (it0 + u >= per) break;
+        if (at >= 0 && at + kVec<T> <= n) {
+          mine[(it0 + u) * 32] = raw[u];
+        } else {
+          T* to = reinterpret_cast<T*>(mine + (it0 + u) * 32);
+          for (int q = 0; q < kVec<T>; ++q) {
+            if (at + q >= 0 && at + q < n) {
+              to[q] = fetch(x + at + q);
+            } else if constexpr (sizeof(T) == 2) {
+              reinterpret_cast<uint16_t*>(to)[q] = 0xFFFFu;
+            } else {
+              reinterpret_cast<uint32_t*>(to)[q] = 0xFFFFFFFFu;
+            }
           }
         }
       }
@@ -746,13 +1000,11 @@ __global__ void __launch_bounds__(kThreads) cta_kernel(const Rows a, int per) {
       if (v > m) m = v;
       if (v != v && at >= 0 && at < n) nan = true;
     });
-    __syncthreads();  // the powers, in the first round
     const Wish w = wish_of(a, row);
     {
-      const u64 top = team.largest(nan ? ~0ull : static_cast<u64>(key_of(m)));
+      const u64 top = team.largest(nan ? ~0ull : static_cast<u64>(key_of(m)));  // (and the powers are there)
       nan = top == ~0ull;
-      const uint32_t k = static_cast<uint32_t>(top);
-      m = __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+      m = value_of_key(static_cast<uint32_t>(top));
     }
     if (w.bad || nan || m == -INFINITY) {
       if (threadIdx.x == 0 && team.rank == 0) {
@@ -761,9 +1013,67 @@ __global__ void __launch_bounds__(kThreads) cta_kernel(const Rows a, int per) {
       }
       continue;
     }
+    if (w.top_k == 1) {
+      // The first of the largest.
+      u64 first = 0;
+      part.each([&](float v, int at) {
+        if (v == m) first = max(first, static_cast<u64>(static_cast<uint32_t>(~at)));
+      });
+      first = team.largest(first);
+      if (threadIdx.x == 0 && team.rank == 0) {
+        a.index[row] = static_cast<int>(~static_cast<uint32_t>(first));
+        if (a.logprob != nullptr) a.logprob[row] = 0.f;
+      }
+      continue;
+    }
+    const Fine fine(m, w);
     Kept kept;
-    if (w.top_k < n) cut<T, kCluster>(team, part, m, w, &kept, false, static_cast<u64>(w.top_k), -1.0);
-    if (w.top_p < 1.0 && w.top_k > 1) cut<T, kCluster>(team, part, m, w, &kept, true, 0, w.top_p);
+    if (w.top_k < n) {
+      fill_bins<false, T, kCluster>(team, part, fine, kept, 0);
+      find_count<kCluster>(team, static_cast<uint32_t>(w.top_k));
+      const int bin = s.bin;
+      const uint32_t above = s.above_count, inside = s.bin_count;
+      if (above + inside <= kFew) {
+        collect<T, kCluster>(team, part, fine, kept, 0, bin);
+        if (team.rank == 0) few(s, a, row, m, w, static_cast<int>(above + inside));
+        continue;
+      }
+      if (inside <= kCap) {
+        collect<T, kCluster>(team, part, fine, kept, bin, bin);
+        const u64 edge = find_edge<kCluster>(team, static_cast<int>(inside), false, static_cast<uint32_t>(w.top_k) - above - 1, 0, 0, m, w);
+        kept.key = item_key(edge);
+        kept.last = item_index(edge);
+      } else {
+        kept = cut<T, kCluster>(s, part, m, w, kept, false, static_cast<u64>(w.top_k), -1.0);
+      }
+    }
+    u64 own = 0, before;
+    bool summed = false;  // own holds the weights of bins before `first`, and those of first .. last are to be added
+    int first = 0, last = 0;
+    if (w.top_p < 1.0) {
+      fill_bins<true, T, kCluster>(team, part, fine, kept, bits);
+      find_sum<kCluster>(team, w.top_p);
+      first = s.bin;
+      last = s.last_bin;
+      u64 rest = 0;
+      part.each([&](float v, int at) {
+        if (!kept.holds(key_of(v), at)) return;
+        const u64 t = weight(v, m, w, s.powers);
+        if (fine.bin(v) < first) own += t; else rest += t;
+      });
+      const u64 above = team.sum(own, &before);
+      const u64 target = nucleus(w.top_p, above + team.sum(rest, &before));
+      const uint32_t count = collect<T, kCluster>(team, part, fine, kept, first, last);
+      u64 edge = 0;
+      if (count <= kCap) edge = find_edge<kCluster>(team, static_cast<int>(count), true, 0, above, target == 0 ? 1 : target, m, w);
+      if (edge != 0) {
+        kept.key = item_key(edge);
+        kept.last = item_index(edge);
+        summed = true;
+      } else {
+        kept = cut<T, kCluster>(s, part, m, w, kept, true, 0, w.top_p);
+      }
+    }
     if (w.min_p > 0.f) {
       const Floor floor(m, w);
       u64 least = 0;
@@ -774,11 +1084,19 @@ __global__ void __launch_bounds__(kThreads) cta_kernel(const Rows a, int per) {
       if (key > kept.key) {
         kept.key = key;
         kept.last = 0x7FFFFFFF;
+        summed = false;
       }
     }
     auto weigh = [&](float v, int at) { return kept.holds(key_of(v), at) ? weight(v, m, w, s.powers) : 0; };
-    u64 own = 0, before;
-    part.each([&](float v, int at) { own += weigh(v, at); });
+    if (summed) {
+      part.each([&](float v, int at) {
+        const int b = fine.bin(v);
+        if (b >= first && b <= last) own += weigh(v, at);
+      });
+    } else {
+      own = 0;
+      part.each([&](float v, int at) { own += weigh(v, at); });
+    }
     const u64 total = team.sum(own, &before);
     walk(part, share(w.u, total), before, own, weigh, [&](float v, int at) {
       a.index[row] = at;
@@ -794,10 +1112,17 @@ cudaError_t run_warp(const Rows& a, cudaStream_t stream) {
   return launch_overlapped(warp_kernel<T, R>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream, a);
 }
 
+// The 16-byte words of a row: one more where rows start within one.
+template <typename T>
+int64_t words_of(const Rows& a) {
+  const bool aligned = a.n % kVec<T> == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
+  return (a.n + kVec<T> - 1) / kVec<T> + (aligned ? 0 : 1);
+}
+
 template <typename T, bool kCluster>
 cudaError_t run_cta(const Rows& a, int cluster, cudaStream_t stream) {
   static SmemRecord record, wide;
-  const int64_t words = (a.n + kVec<T> - 1) / kVec<T> + 1;  // with a row that starts within a word
+  const int64_t words = words_of<T>(a);
   const int64_t lanes = static_cast<int64_t>(cluster) * kThreads;
   const int per = static_cast<int>((words + lanes - 1) / lanes);
   const size_t smem = static_cast<size_t>(per) * kThreads * 16;
@@ -820,7 +1145,7 @@ cudaError_t run(const Rows& a, cudaStream_t stream) {
   const cudaError_t err = device_info(&dev);
   if (err != cudaSuccess) return err;
   // CTAs a row: until the rows fill the SMs, while a lane has four words or more; at least what holds the row.
-  const int64_t words = (a.n + kVec<T> - 1) / kVec<T> + 1;
+  const int64_t words = words_of<T>(a);
   int cluster = 1;
   while (cluster < 16 && a.rows * cluster * 2 <= dev.sm_count && words >= static_cast<int64_t>(cluster) * kThreads * 8) cluster *= 2;
   while (cluster < 16 && words * 16 > static_cast<int64_t>(cluster) * 160 * 1024) cluster *= 2;
