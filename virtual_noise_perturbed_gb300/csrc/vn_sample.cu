@@ -20,6 +20,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "vn_act.cuh"
 #include "vn_internal.h"
@@ -56,6 +57,9 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   uint32_t b = __float_as_uint(x);
   b = b == 0x80000000u ? 0u : b;
   return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of_key(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 __device__ __forceinline__ float absent() { return __uint_as_float(0xFFFFFFFFu); }
 constexpr uint32_t kLowest = 0x10000;  // below every logit's key
@@ -388,7 +392,44 @@ __global__ void __launch_bounds__(kThreads) warp_kernel(const Rows a) {
   }
 }
 
-// ---------------------------------------------------------------- a CTA, or a cluster of them, a row
+// ---------------------------------------------------------------- a CTA of W warps, or a cluster of them, a row
+// What is kept of a row: logits above `edge`, and of those equal to it the ones at an index up to `last`.
+struct Prefix {
+  float edge = -INFINITY;
+  int32_t last = 0x7FFFFFFF;
+  __device__ __forceinline__ bool holds(float x, int32_t at) const { return x > edge || (x == edge && at <= last); }
+};
+
+// exp((x - m) / T) to 4e-7 of itself, sums of eight included, in a third of the instructions of weight(): what is decided by
+// such sums is sure where it is further than kSure of all from a border, and else decided by weight(). 0 for the
+// largest logits themselves, whose ones would drown a small rest: they are counted.
+constexpr float kSure = 1e-6f;
+__device__ __forceinline__ float coarse(float x, float m, const Wish& w) {
+  float e;
+  const float p = distance(x, m, w, &e) * 0.03125f;  // exact: a power of two
+  const float v = quick_exp2(-p);
+  const float r = __fmaf_rn(v, e * -0.021660849392498290f, v);
+  return p < 44.f && x != m ? r : 0.f;
+}
+__device__ __forceinline__ u64 units(float v) { return __float2ull_rn(v * 0x1p42f); }
+// N weights, those not taken as 0: a sum in pairs, and the largest logits among them.
+template <int N, typename F>
+__device__ __forceinline__ u64 coarse_sum(const float (&x)[N], float m, const Wish& w, F take) {
+  float v[N];
+  int tops = 0;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const bool in = take(x[q], q);
+    v[q] = in ? coarse(x[q], m, w) : 0.f;
+    tops += in && x[q] == m;
+  }
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int q = 0; q < o; ++q) v[q] += v[q + o];
+  return units(v[0]) + (static_cast<u64>(tops) << kUnit);
+}
+
 template <typename T>
 constexpr int kVec = 16 / static_cast<int>(sizeof(T));  // logits of 16 bytes
 
@@ -397,25 +438,39 @@ constexpr int kVec = 16 / static_cast<int>(sizeof(T));  // logits of 16 bytes
 constexpr int kFine = 512;
 __device__ __forceinline__ int fine_place(int bin) { return bin + (bin >> 4); }
 constexpr int kFinePlaces = kFine + kFine / 16;
-constexpr int kCap = 1024;  // logits that a border is looked for among, one by one
-constexpr int kFew = kThreads;  // with no more than these left, a thread has one of them
+// The most logits that a border is looked for among one by one, and the most that all of the rest is done for so.
+template <int W>
+constexpr int kCap = W == 1 ? 256 : 1024;
+constexpr int kFew = 256;
 
+struct NoBins {};
+struct MergedBins {
+  uint32_t fine[kFinePlaces];
+};
 // A CTA's shared memory but for its logits.
+template <int W, bool kCluster>
 struct Shared {
   u64 powers[32];
-  u64 sums[kBins];
-  uint32_t counts[kBins];
-  uint32_t fine[kFine];
-  float merged[kFinePlaces];  // `fine` over all ranks: counts' bits, or sums
-  u64 list[kCap];             // logits as key and complement of the index: the larger, the earlier in the order
-  u64 list_weights[kCap];
+  union {
+    struct {
+      u64 list[kCap<W>];          // logits as key and complement of the index: the larger, the earlier in the order
+      u64 list_weights[kCap<W>];
+    };
+    struct {                      // where more logits than that lie next to a border
+      u64 sums[kBins];
+      uint32_t counts[kBins];
+    };
+  };
+  uint32_t fine[kFinePlaces];     // counts or sums, in the end over all ranks: sums as fp32 bits
+  std::conditional_t<kCluster, MergedBins, NoBins> merged;  // the place for that in a cluster, whose other ranks read `fine`
   uint32_t list_count;
-  u64 edge[2];                // the last one kept, by count and by sum: a rank may still read the one when the other is cleared
-  u64 warps[2][kWarps];       // of the two reductions at work at most
-  u64 few[2][kWarps];
-  u64 mine[2];                // what this CTA hands to the others of its cluster
+  u64 edge[2];                    // the last one kept, by count and by sum: a rank may still read the one when the other is cleared
+  u64 warps[2][W];                // of the two reductions at work at most
+  u64 few[2][W];
+  u64 mine[2];                    // what this CTA hands to the others of its cluster
   // Of the bin that a border falls into:
   int bin, last_bin;
+  int sure;                       // of the draw by coarse sums (rank 0's)
   u64 above_sum, target;
   uint32_t above_count, bin_count;
 };
@@ -440,6 +495,7 @@ struct Part {
       for (int q = 0; q < 4; ++q) v[q] = __uint_as_float(w[q]);
     }
   }
+  __device__ __forceinline__ int index(int it) const { return first + it * 32 * kVec<T>; }
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
     for (int it = 0; it < words; ++it) {
@@ -451,11 +507,11 @@ struct Part {
   }
 };
 
-template <bool kCluster>
+template <int W, bool kCluster>
 struct Team {
-  Shared& s;
+  Shared<W, kCluster>& s;
   int ranks, rank, turn = 0;
-  __device__ __forceinline__ Team(Shared& shared) : s(shared) {
+  __device__ __forceinline__ Team(Shared<W, kCluster>& shared) : s(shared) {
     ranks = kCluster ? static_cast<int>(cg::this_cluster().num_blocks()) : 1;
     rank = kCluster ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
   }
@@ -477,7 +533,7 @@ struct Team {
     __syncthreads();
     u64 mine = 0, ahead = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < W; ++i) {
       const u64 t = s.warps[turn][i];
       if (i < warp) ahead += t;
       mine += t;
@@ -508,7 +564,7 @@ struct Team {
     if ((threadIdx.x & 31) == 0) s.warps[turn][threadIdx.x >> 5] = v;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) v = s.warps[turn][i] > v ? s.warps[turn][i] : v;
+    for (int i = 0; i < W; ++i) v = s.warps[turn][i] > v ? s.warps[turn][i] : v;
     if constexpr (kCluster) {
       if (threadIdx.x == 0) s.mine[turn] = v;
       sync();
@@ -521,50 +577,44 @@ struct Team {
   }
 };
 
-// The index, within the row, of the first logit whose weights up to it pass r; before: the weights ahead of this warp.
-// Only the warp that has it writes.
-template <typename T, typename W, typename F>
-__device__ __forceinline__ void walk(const Part<T>& part, u64 r, u64 before, u64 mine, W weigh, F found) {
+// The first logit whose weights up to it pass r, found by the warp that has it; before: the weights ahead of this warp, total:
+// its own. found(x, index, up to it, its own weight).
+template <typename T, typename S, typename E, typename F>
+__device__ __forceinline__ void walk(const Part<T>& part, u64 r, u64 before, u64 total, S word_sum, E each, F found) {
   const int lane = threadIdx.x & 31;
-  const u64 total = warp_sum(mine);
   if (r < before || r >= before + total) return;
-  r -= before;
   for (int it = 0; it < part.words; ++it) {
     float v[kVec<T>];
     part.unpack(it, v);
-    u64 w[kVec<T>], own = 0;
-#pragma unroll
-    for (int q = 0; q < kVec<T>; ++q) {
-      w[q] = weigh(v[q], part.first + it * 32 * kVec<T> + q);
-      own += w[q];
-    }
+    const u64 own = word_sum(v, part.index(it));
     const u64 scan = warp_scan(own, lane);
     const u64 all = __shfl_sync(kAll, scan, 31);
-    if (r < all) {
-      const uint32_t over = __ballot_sync(kAll, scan > r);
+    if (r < before + all) {
+      const uint32_t over = __ballot_sync(kAll, before + scan > r);
       if (lane == __ffs(over) - 1) {
-        u64 at = scan - own;
-        int which = -1;
+        u64 at = before + scan - own;
+        bool done = false;
 #pragma unroll
         for (int q = 0; q < kVec<T>; ++q) {
-          at += w[q];
-          if (which < 0 && at > r) which = q;
+          const u64 t = each(v[q], part.index(it) + q);
+          if (!done && (at + t > r || q == kVec<T> - 1)) {
+            done = true;
+            found(v[q], part.index(it) + q, at + t, t);
+          }
+          at += t;
         }
-#pragma unroll
-        for (int q = 0; q < kVec<T>; ++q)
-          if (q == which) found(v[q], part.first + it * 32 * kVec<T> + q);
       }
       return;
     }
-    r -= all;
+    before += all;
   }
 }
 
 // The bin of s.counts and s.sums, over all ranks, that the border falls into: by count, the first whose counts from bin 0
 // on reach `target`; by sum likewise.
-template <bool kCluster>
-__device__ __forceinline__ void find_bin(Team<kCluster>& team, bool by_sum, u64 target_count, double top_p) {
-  Shared& s = team.s;
+template <int W, bool kCluster>
+__device__ __forceinline__ void find_bin(Team<W, kCluster>& team, bool by_sum, u64 target_count, double top_p) {
+  Shared<W, kCluster>& s = team.s;
   team.sync();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
@@ -612,9 +662,9 @@ __device__ __forceinline__ void find_bin(Team<kCluster>& team, bool by_sum, u64 
   team.sync();
 }
 
-template <bool kCluster>
-__device__ __forceinline__ void clear_bins(Shared& s) {
-  for (int b = threadIdx.x; b < kBins; b += kThreads) {
+template <int W, bool kCluster>
+__device__ __forceinline__ void clear_bins(Shared<W, kCluster>& s) {
+  for (int b = threadIdx.x; b < kBins; b += W * 32) {
     s.counts[b] = 0;
     s.sums[b] = 0;
   }
@@ -622,28 +672,26 @@ __device__ __forceinline__ void clear_bins(Shared& s) {
 }
 
 // Cuts `kept` to its first `count` logits, or (by_sum) to those before which less than top_p of its sum lies.
-// Out of line: it is the way for more logits next to a border than kCap, many equal ones above all.
-template <typename T, bool kCluster>
-__device__ __noinline__ Kept cut(Shared& s, const Part<T> part, float m, const Wish w, const Kept in, bool by_sum, u64 count, double top_p) {
-  Team<kCluster> team(s);
+// Out of line: it is the way for more logits next to a border than kCap<W>, many equal ones above all.
+template <typename T, int W, bool kCluster>
+__device__ __noinline__ Prefix cut(Shared<W, kCluster>& s, const Part<T> part, float m, const Wish w, const Prefix in, bool by_sum, u64 count, double top_p) {
+  Team<W, kCluster> team(s);
   __syncthreads();  // its reductions take their places from the first again
-  Kept kept;
+  Prefix kept;
   uint32_t low = kLowest, high = kAll;  // keys of the bin
   u64 target = count, above = 0;        // still to be reached within it, and ahead of it
-  if (!by_sum && count == 1) {
-    low = high = key_of(m);
-  } else {
+  {
     // Bins of an eighth of a binary order of the weights, the last one with all that is below.
     const float scale = w.ch * 0.25f;
     auto bin_of = [&](float x) { return x == m ? 0 : min(kBins - 1, __float2int_rd((m - x) * scale)); };
-    clear_bins<kCluster>(s);
+    clear_bins(s);
     part.each([&](float x, int at) {
-      if (!in.holds(key_of(x), at)) return;
+      if (!in.holds(x, at)) return;
       const int b = bin_of(x);
       atomicAdd(&s.counts[b], 1u);
       if (by_sum) atomicAdd(&s.sums[b], weight(x, m, w, s.powers));
     });
-    find_bin<kCluster>(team, by_sum, target, by_sum ? top_p : -1.0);
+    find_bin(team, by_sum, target, by_sum ? top_p : -1.0);
     int bin = s.bin;
     above = s.above_sum;
     target = s.target;
@@ -651,7 +699,7 @@ __device__ __noinline__ Kept cut(Shared& s, const Part<T> part, float m, const W
     u64 most = 0, least = 0;  // the smallest as its complement's largest
     part.each([&](float x, int at) {
       const uint32_t k = key_of(x);
-      if (in.holds(k, at) && bin_of(x) == bin) {
+      if (in.holds(x, at) && bin_of(x) == bin) {
         most = max(most, static_cast<u64>(k));
         least = max(least, static_cast<u64>(~k));
       }
@@ -660,14 +708,14 @@ __device__ __noinline__ Kept cut(Shared& s, const Part<T> part, float m, const W
     low = ~static_cast<uint32_t>(team.largest(least));
     while (low < high) {
       const int shift = max(0, 32 - __clz(high - low) - 8);
-      clear_bins<kCluster>(s);
+      clear_bins(s);
       part.each([&](float x, int at) {
         const uint32_t k = key_of(x);
-        if (k < low || k > high || !in.holds(k, at)) return;
+        if (k < low || k > high || !in.holds(x, at)) return;
         atomicAdd(&s.counts[(high - k) >> shift], 1u);
         if (by_sum) atomicAdd(&s.sums[(high - k) >> shift], weight(x, m, w, s.powers));
       });
-      find_bin<kCluster>(team, by_sum, target - above, -1.0);
+      find_bin(team, by_sum, target - above, -1.0);
       bin = s.bin;
       above += s.above_sum;
       const uint32_t top = high - (static_cast<uint32_t>(bin) << shift);
@@ -678,7 +726,7 @@ __device__ __noinline__ Kept cut(Shared& s, const Part<T> part, float m, const W
         most = least = 0;
         part.each([&](float x, int at) {
           const uint32_t k = key_of(x);
-          if (k <= top && k >= bottom && k >= low && in.holds(k, at)) {
+          if (k <= top && k >= bottom && k >= low && in.holds(x, at)) {
             most = max(most, static_cast<u64>(k));
             least = max(least, static_cast<u64>(~k));
           }
@@ -689,29 +737,36 @@ __device__ __noinline__ Kept cut(Shared& s, const Part<T> part, float m, const W
     }
   }
   // Of the logits with that key, how many, and the index of the last one.
-  kept.key = high;
-  kept.last = 0x7FFFFFFF;
-  const float edge = __uint_as_float(high & 0x80000000u ? high ^ 0x80000000u : ~high);
+  const float edge = value_of_key(high);
+  kept.edge = edge;
   u64 ties = target - above;
   if (by_sum) {
     const u64 each = weight(edge, m, w, s.powers);
     ties = each == 0 ? 1 : (ties + each - 1) / each;
   }
   u64 mine = 0, before;
-  part.each([&](float x, int at) { mine += key_of(x) == high && in.holds(high, at); });
+  auto tied = [&](float x, int at) -> u64 { return x == edge && in.holds(x, at); };
+  part.each([&](float x, int at) { mine += tied(x, at); });
   const u64 all = team.sum(mine, &before);
   if (ties < all) {
-    walk(part, ties - 1, before, mine, [&](float x, int at) { return static_cast<u64>(key_of(x) == high && in.holds(high, at)); },
-         [&](float, int at) {
-           for (int r = 0; r < team.ranks; ++r) {
-             if constexpr (kCluster) *cg::this_cluster().map_shared_rank(&s.bin, r) = at;
-             else s.bin = at;
-           }
-         });
+    walk(
+        part, ties - 1, before, warp_sum(mine),
+        [&](const float(&v)[kVec<T>], int at) {
+          u64 t = 0;
+#pragma unroll
+          for (int q = 0; q < kVec<T>; ++q) t += tied(v[q], at + q);
+          return t;
+        },
+        tied,
+        [&](float, int at, u64, u64) {
+          for (int r = 0; r < team.ranks; ++r) {
+            if constexpr (kCluster) *cg::this_cluster().map_shared_rank(&s.bin, r) = at;
+            else s.bin = at;
+          }
+        });
     team.sync();
     kept.last = s.bin;
-    team.sync();
-  } else if (in.key == high) {
+  } else if (in.edge == edge) {
     kept.last = in.last;
   }
   team.sync();
@@ -735,16 +790,18 @@ struct Fine {
 __device__ __forceinline__ u64 item_of(uint32_t key, int at) { return static_cast<u64>(key) << 32 | static_cast<uint32_t>(~at); }
 __device__ __forceinline__ uint32_t item_key(u64 item) { return static_cast<uint32_t>(item >> 32); }
 __device__ __forceinline__ int item_index(u64 item) { return static_cast<int>(~static_cast<uint32_t>(item)); }
-__device__ __forceinline__ float value_of_key(uint32_t key) {
-  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+
+template <int W, bool kCluster>
+__device__ __forceinline__ uint32_t* bins_of(Shared<W, kCluster>& s) {
+  if constexpr (kCluster) return s.merged.fine; else return s.fine;
 }
 
-// Counts of the kept logits, or (kSums) their weights, in s.merged over all ranks. A sum is held per CTA in 32 bits, in units of
+// Counts of the kept logits, or (kSums) their weights, over all ranks, in bins_of(s). A sum is held per CTA in 32 bits, in units of
 // 2^-bits of the largest weight of its bin, good to 2^-13 in all.
-template <bool kSums, typename T, bool kCluster>
-__device__ __forceinline__ void fill_bins(Team<kCluster>& team, const Part<T>& part, const Fine& fine, const Kept& in, int bits) {
-  Shared& s = team.s;
-  for (int b = threadIdx.x; b < kFine; b += kThreads) s.fine[b] = 0;
+template <bool kSums, typename T, int W, bool kCluster>
+__device__ __forceinline__ void fill_bins(Team<W, kCluster>& team, const Part<T>& part, const Fine& fine, const Prefix& in, int bits) {
+  Shared<W, kCluster>& s = team.s;
+  for (int b = threadIdx.x; b < kFinePlaces; b += W * 32) s.fine[b] = 0;
   if (threadIdx.x == 0) {
     s.list_count = 0;
     s.edge[kSums] = 0;
@@ -752,35 +809,38 @@ __device__ __forceinline__ void fill_bins(Team<kCluster>& team, const Part<T>& p
   __syncthreads();
   const float unit = static_cast<float>(1 << bits);
   part.each([&](float x, int at) {
-    if (!in.holds(key_of(x), at)) return;
+    if (!in.holds(x, at)) return;
     float into;
     const int b = fine.bin(x, &into);
-    atomicAdd(&s.fine[b], kSums ? static_cast<uint32_t>(__float2int_rn(unit * quick_exp2(into * -0.0625f))) : 1u);
+    atomicAdd(&s.fine[fine_place(b)], kSums ? static_cast<uint32_t>(__float2int_rn(unit * quick_exp2(into * -0.0625f))) : 1u);
   });
   team.sync();
-  for (int b = threadIdx.x; b < kFine; b += kThreads) {
-    float sum = 0.f;
-    uint32_t count = 0;
-    for (int r = 0; r < team.ranks; ++r) {
-      const uint32_t v = team.of_rank(&s.fine[b], r);
-      count += v;
-      sum += static_cast<float>(v);
+  if constexpr (kSums || kCluster) {
+    for (int b = threadIdx.x; b < kFine; b += W * 32) {
+      float sum = 0.f;
+      uint32_t count = 0;
+      for (int r = 0; r < team.ranks; ++r) {
+        const uint32_t v = team.of_rank(&s.fine[fine_place(b)], r);
+        count += v;
+        sum += static_cast<float>(v);
+      }
+      const uint32_t v = kSums ? __float_as_uint(sum * quick_exp2(static_cast<float>(b) * -0.0625f)) : count;
+      bins_of(s)[fine_place(b)] = v;
     }
-    s.merged[fine_place(b)] = kSums ? sum * quick_exp2(static_cast<float>(b) * -0.0625f) : __uint_as_float(count);
+    __syncthreads();
   }
-  __syncthreads();
 }
 
 // By count: the bin that the logit number `target` (from 1) of the order is in.
-template <bool kCluster>
-__device__ __forceinline__ void find_count(Team<kCluster>& team, uint32_t target) {
-  Shared& s = team.s;
+template <int W, bool kCluster>
+__device__ __forceinline__ void find_count(Team<W, kCluster>& team, uint32_t target) {
+  Shared<W, kCluster>& s = team.s;
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     uint32_t own[kFine / 32], total = 0;
 #pragma unroll
     for (int b = 0; b < kFine / 32; ++b) {
-      own[b] = __float_as_uint(s.merged[fine_place(lane * (kFine / 32) + b)]);
+      own[b] = bins_of(s)[fine_place(lane * (kFine / 32) + b)];
       total += own[b];
     }
     uint32_t scan = total;
@@ -808,15 +868,15 @@ __device__ __forceinline__ void find_count(Team<kCluster>& team, uint32_t target
   team.sync();
 }
 // By sum: the bins that the border of top_p may be in, whatever the sums' error does to them.
-template <bool kCluster>
-__device__ __forceinline__ void find_sum(Team<kCluster>& team, double top_p) {
-  Shared& s = team.s;
+template <int W, bool kCluster>
+__device__ __forceinline__ void find_sum(Team<W, kCluster>& team, double top_p) {
+  Shared<W, kCluster>& s = team.s;
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     float own[kFine / 32], total = 0.f;
 #pragma unroll
     for (int b = 0; b < kFine / 32; ++b) {
-      own[b] = s.merged[fine_place(lane * (kFine / 32) + b)];
+      own[b] = __uint_as_float(bins_of(s)[fine_place(lane * (kFine / 32) + b)]);
       total += own[b];
     }
     float scan = total;
@@ -850,111 +910,195 @@ __device__ __forceinline__ void find_sum(Team<kCluster>& team, double top_p) {
   team.sync();
 }
 
-// The kept logits of bins first .. last into rank 0's list; how many there are (beyond kCap only counted).
-template <typename T, bool kCluster>
-__device__ __forceinline__ uint32_t collect(Team<kCluster>& team, const Part<T>& part, const Fine& fine, const Kept& in, int first, int last) {
-  Shared* s = &team.s;
+// A logit into rank 0's list, if it is not full; the list counts on.
+template <int W, bool kCluster>
+__device__ __forceinline__ void enlist(Team<W, kCluster>& team, float x, int at) {
+  Shared<W, kCluster>* s = &team.s;
   if constexpr (kCluster) s = cg::this_cluster().map_shared_rank(&team.s, 0);
+  const uint32_t to = atomicAdd(&s->list_count, 1u);
+  if (to < kCap<W>) s->list[to] = item_of(key_of(x), at);
+}
+// The kept logits of bins first .. last.
+template <typename T, int W, bool kCluster>
+__device__ __forceinline__ void collect(Team<W, kCluster>& team, const Part<T>& part, const Fine& fine, const Prefix& in, int first, int last) {
   part.each([&](float x, int at) {
-    const uint32_t key = key_of(x);
-    if (key < kLowest) return;
+    if (!in.holds(x, at)) return;
     const int b = fine.bin(x);
-    if (b < first || b > last || !in.holds(key, at)) return;
-    const uint32_t to = atomicAdd(&s->list_count, 1u);
-    if (to < kCap) s->list[to] = item_of(key, at);
+    if (b >= first && b <= last) enlist(team, x, at);
   });
   team.sync();
-  return team.of_rank(&team.s.list_count, 0);
 }
 
 // The sum over a CTA's threads (not over its cluster).
-__device__ __forceinline__ u64 cta_sum(Shared& s, int place, u64 v) {
+template <int W, bool kCluster>
+__device__ __forceinline__ u64 cta_sum(Shared<W, kCluster>& s, int place, u64 v) {
   v = warp_sum(v);
+  if constexpr (W == 1) {
+    __syncwarp();
+    return v;
+  }
   if ((threadIdx.x & 31) == 0) s.few[place][threadIdx.x >> 5] = v;
   __syncthreads();
   v = 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) v += s.few[place][i];
+  for (int i = 0; i < W; ++i) v += s.few[place][i];
   return v;
 }
 
-// All of the rest for at most kFew logits that s.list holds, the first top_k of the order among them: a thread has one,
-// and its place in either order, and what lies before it, from a look at every other.
-__device__ __forceinline__ void few(Shared& s, const Rows& a, int64_t row, float m, const Wish& w, int count) {
-  const int i = threadIdx.x;
-  const bool there = i < count;
-  const u64 item = there ? s.list[i] : 0;
-  const float x = value_of_key(item_key(item));
-  const u64 full = there ? weight(x, m, w, s.powers) : 0;
-  if (there) s.list_weights[i] = full;
+// All of the rest for at most kFew logits that s.list holds, the first top_k of the order among them: of each its place in
+// either order, and what lies before it, come from a look at every other.
+template <int W, bool kCluster>
+__device__ __forceinline__ void few(Shared<W, kCluster>& s, const Rows& a, int64_t row, float m, const Wish& w, int count) {
+  constexpr int kEach = kFew / (W * 32) > 1 ? kFew / (W * 32) : 1;  // logits of a thread
+  for (int i = threadIdx.x; i < count; i += W * 32)
+    s.list_weights[i] = weight(value_of_key(item_key(s.list[i])), m, w, s.powers);
   __syncthreads();
-  int64_t rank = 0;
-  u64 before = 0;
-  if (there) {
-    for (int j = 0; j < count; ++j) {
-      const bool earlier = s.list[j] > item;
-      rank += earlier;
-      before += earlier ? s.list_weights[j] : 0;
+  int rank[kEach];
+  u64 before[kEach], all = 0;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = threadIdx.x + e * W * 32;
+    rank[e] = 0;
+    before[e] = 0;
+    if (i < count) {
+      const u64 item = s.list[i];
+      for (int j = 0; j < count; ++j) {
+        const bool earlier = s.list[j] > item;
+        rank[e] += earlier;
+        before[e] += earlier ? s.list_weights[j] : 0;
+      }
+      if (rank[e] < w.top_k) all += s.list_weights[i];
     }
   }
-  bool kept = there && rank < w.top_k;
-  const u64 all = cta_sum(s, 0, kept ? full : 0);
-  if (w.top_p < 1.0) kept = kept && (rank == 0 || before < nucleus(w.top_p, all));
-  if (w.min_p > 0.f) kept = kept && Floor(m, w).above(x, m, w, s.powers);
-  const u64 mine = kept ? full : 0;
-  if (there) s.list_weights[i] = mine;  // every thread has passed the sum above: nobody reads the old ones
-  const u64 total = cta_sum(s, 1, mine);
-  if (!kept) return;
+  all = cta_sum(s, 0, all);  // everyone is past the reading of the weights
+  const u64 target = w.top_p < 1.0 ? nucleus(w.top_p, all) : ~0ull;
+  u64 total = 0;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = threadIdx.x + e * W * 32;
+    if (i >= count) break;
+    const float x = value_of_key(item_key(s.list[i]));
+    const bool kept = rank[e] < w.top_k && (rank[e] == 0 || before[e] < target) &&
+                      (!(w.min_p > 0.f) || Floor(m, w).above(x, m, w, s.powers));
+    if (kept) total += s.list_weights[i];
+    else s.list_weights[i] = 0;
+  }
+  total = cta_sum(s, 1, total);
   const u64 r = share(w.u, total);
-  u64 up_to = 0;
-  for (int j = 0; j < count; ++j)
-    if (item_index(s.list[j]) <= item_index(item)) up_to += s.list_weights[j];
-  if (up_to > r && up_to - mine <= r) {
-    a.index[row] = item_index(item);
-    if (a.logprob != nullptr) a.logprob[row] = logprob_of(x, m, w, total);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = threadIdx.x + e * W * 32;
+    if (i >= count) break;
+    const u64 mine = s.list_weights[i];
+    if (mine == 0) continue;
+    const int index = item_index(s.list[i]);
+    u64 up_to = 0;
+    for (int j = 0; j < count; ++j)
+      if (item_index(s.list[j]) <= index) up_to += s.list_weights[j];
+    if (up_to > r && up_to - mine <= r) {
+      a.index[row] = index;
+      if (a.logprob != nullptr) a.logprob[row] = logprob_of(value_of_key(item_key(s.list[i])), m, w, total);
+    }
   }
 }
 
-// Of `count` logits in rank 0's list the one with `rank` others before it, or (by_sum) the one in which the sum passes
-// `target`, `above` lying before all of the list: where the prefix ends. 0 if there is none.
-template <bool kCluster>
-__device__ __forceinline__ u64 find_edge(Team<kCluster>& team, int count, bool by_sum, uint32_t rank, u64 above, u64 target, float m,
-                                         const Wish& w) {
-  Shared& s = team.s;
+// Of `count` logits in rank 0's list the one with `rank` others before it: where a prefix of so many ends.
+template <int W, bool kCluster>
+__device__ __forceinline__ u64 edge_by_count(Team<W, kCluster>& team, int count, uint32_t rank) {
+  Shared<W, kCluster>& s = team.s;
   if (team.rank == 0) {
-    if (by_sum) {
-      for (int i = threadIdx.x; i < count; i += kThreads)
-        s.list_weights[i] = weight(value_of_key(item_key(s.list[i])), m, w, s.powers);
-      __syncthreads();
-    }
-    for (int i = threadIdx.x; i < count; i += kThreads) {
+    for (int i = threadIdx.x; i < count; i += W * 32) {
       const u64 item = s.list[i];
       uint32_t place = 0;
-      u64 before = above;
-      for (int j = 0; j < count; ++j) {
-        const bool earlier = s.list[j] > item;
-        place += earlier;
-        if (by_sum) before += earlier ? s.list_weights[j] : 0;
-      }
-      if (by_sum ? before < target && before + s.list_weights[i] >= target : place == rank) s.edge[by_sum] = item;
+      for (int j = 0; j < count; ++j) place += s.list[j] > item;
+      if (place == rank) s.edge[0] = item;
     }
   }
   team.sync();
-  return team.of_rank(&s.edge[by_sum], 0);
+  return team.of_rank(&s.edge[0], 0);
+}
+// The one in which the sum passes `target`, `above` lying before all of the list. With weigh's weights known to `sure`: 0 if
+// the border is no further than that from one of its sides. 0 too if there is none.
+template <int W, bool kCluster, typename F>
+__device__ __forceinline__ u64 edge_by_sum(Team<W, kCluster>& team, int count, u64 above, u64 target, u64 sure, F weigh) {
+  Shared<W, kCluster>& s = team.s;
+  if (team.rank == 0) {
+    for (int i = threadIdx.x; i < count; i += W * 32) s.list_weights[i] = weigh(value_of_key(item_key(s.list[i])));
+    __syncthreads();
+    for (int i = threadIdx.x; i < count; i += W * 32) {
+      const u64 item = s.list[i];
+      u64 before = above;
+      for (int j = 0; j < count; ++j) before += s.list[j] > item ? s.list_weights[j] : 0;
+      const u64 up_to = before + s.list_weights[i];
+      if (before < target && up_to >= target && (before == 0 || target - before >= sure) && up_to - target >= sure) s.edge[1] = item;
+    }
+  }
+  team.sync();
+  return team.of_rank(&s.edge[1], 0);
 }
 
-// per: 16-byte words of a warp's lane; the CTA's logits take kWarps * 32 * per of them.
-template <typename T, bool kCluster>
-__global__ void __launch_bounds__(kThreads, 3) cta_kernel(const Rows a, int per) {
+// What is kept of a nucleus whose border coarse sums cannot tell, by the list of the logits next to it if it holds them.
+template <typename T, int W, bool kCluster>
+__device__ __noinline__ Prefix exact_nucleus(Shared<W, kCluster>& s, const Part<T> part, float m, const Wish w, const Prefix in, int first,
+                                             int count) {
+  if (count <= kCap<W>) {
+    Team<W, kCluster> team(s);
+    team.sync();  // its reductions take their places from the first again
+    const Fine fine(m, w);
+    u64 own = 0, rest = 0, before;
+    part.each([&](float v, int at) {
+      if (!in.holds(v, at)) return;
+      const u64 t = weight(v, m, w, s.powers);
+      if (fine.bin(v) < first) own += t; else rest += t;
+    });
+    const u64 above = team.sum(own, &before);
+    u64 target = nucleus(w.top_p, above + team.sum(rest, &before));
+    if (target == 0) target = 1;
+    const u64 edge = edge_by_sum(team, count, above, target, 0, [&](float v) { return weight(v, m, w, s.powers); });
+    team.sync();
+    if (edge != 0) return {value_of_key(item_key(edge)), item_index(edge)};
+  }
+  return cut<T, W, kCluster>(s, part, m, w, in, true, 0, w.top_p);
+}
+
+// The draw by weight().
+template <typename T, int W, bool kCluster>
+__device__ __noinline__ void exact_draw(Shared<W, kCluster>& s, const Part<T> part, const Rows& a, int64_t row, float m, const Wish w,
+                                        const Prefix kept) {
+  Team<W, kCluster> team(s);
+  team.sync();
+  auto weigh = [&](float v, int at) { return kept.holds(v, at) ? weight(v, m, w, s.powers) : 0; };
+  u64 own = 0, before;
+  part.each([&](float v, int at) { own += weigh(v, at); });
+  const u64 total = team.sum(own, &before);
+  walk(
+      part, share(w.u, total), before, warp_sum(own),
+      [&](const float(&v)[kVec<T>], int at) {
+        u64 t = 0;
+#pragma unroll
+        for (int q = 0; q < kVec<T>; ++q) t += weigh(v[q], at + q);
+        return t;
+      },
+      weigh,
+      [&](float v, int at, u64, u64) {
+        a.index[row] = at;
+        if (a.logprob != nullptr) a.logprob[row] = logprob_of(v, m, w, total);
+      });
+  team.sync();
+}
+
+// per: 16-byte words of a warp's lane; the CTA's logits take W * 32 * per of them.
+template <typename T, int W, bool kCluster>
+__global__ void __launch_bounds__(W * 32, 24 / W) cta_kernel(const Rows a, int per) {
   extern __shared__ uint4 logits[];
-  __shared__ Shared s;
+  __shared__ Shared<W, kCluster> s;
   let_next();
   if (threadIdx.x < 32) s.powers[threadIdx.x] = kPowersInit[threadIdx.x];
-  Team<kCluster> team(s);
+  Team<W, kCluster> team(s);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = static_cast<int>(a.n);
   // So that no bin's sum passes 32 bits.
-  const int bits = min(16, __clz(per * kThreads * kVec<T>) - 1);
+  const int bits = min(16, __clz(per * W * 32 * kVec<T>) - 1);
   after_previous();
   for (int64_t row = blockIdx.x / team.ranks; row < a.rows; row += gridDim.x / team.ranks) {
     const T* x = static_cast<const T*>(a.x) + row * n;
@@ -964,7 +1108,7 @@ __global__ void __launch_bounds__(kThreads, 3) cta_kernel(const Rows a, int per)
     Part<T> part;
     part.mine = mine;
     part.words = per;
-    part.first = ((team.rank * kWarps + warp) * per * 32 + lane) * kVec<T> - shift;
+    part.first = ((team.rank * W + warp) * per * 32 + lane) * kVec<T> - shift;
     float m = -INFINITY;
     constexpr int kBatch = 4;  // words of a lane in flight
     for (int it0 = 0; it0 < per; it0 += kBatch) {
@@ -1027,52 +1171,56 @@ __global__ void __launch_bounds__(kThreads, 3) cta_kernel(const Rows a, int per)
       continue;
     }
     const Fine fine(m, w);
-    Kept kept;
+    Prefix kept;
     if (w.top_k < n) {
-      fill_bins<false, T, kCluster>(team, part, fine, kept, 0);
-      find_count<kCluster>(team, static_cast<uint32_t>(w.top_k));
+      fill_bins<false>(team, part, fine, kept, 0);
+      find_count(team, static_cast<uint32_t>(w.top_k));
       const int bin = s.bin;
       const uint32_t above = s.above_count, inside = s.bin_count;
       if (above + inside <= kFew) {
-        collect<T, kCluster>(team, part, fine, kept, 0, bin);
+        collect(team, part, fine, kept, 0, bin);
         if (team.rank == 0) few(s, a, row, m, w, static_cast<int>(above + inside));
         continue;
       }
-      if (inside <= kCap) {
-        collect<T, kCluster>(team, part, fine, kept, bin, bin);
-        const u64 edge = find_edge<kCluster>(team, static_cast<int>(inside), false, static_cast<uint32_t>(w.top_k) - above - 1, 0, 0, m, w);
-        kept.key = item_key(edge);
-        kept.last = item_index(edge);
+      if (inside <= kCap<W>) {
+        collect(team, part, fine, kept, bin, bin);
+        const u64 edge = edge_by_count(team, static_cast<int>(inside), static_cast<uint32_t>(w.top_k) - above - 1);
+        kept = {value_of_key(item_key(edge)), item_index(edge)};
       } else {
-        kept = cut<T, kCluster>(s, part, m, w, kept, false, static_cast<u64>(w.top_k), -1.0);
+        kept = cut<T, W, kCluster>(s, part, m, w, kept, false, static_cast<u64>(w.top_k), -1.0);
       }
     }
-    u64 own = 0, before;
-    bool summed = false;  // own holds the weights of bins before `first`, and those of first .. last are to be added
-    int first = 0, last = 0;
     if (w.top_p < 1.0) {
-      fill_bins<true, T, kCluster>(team, part, fine, kept, bits);
-      find_sum<kCluster>(team, w.top_p);
-      first = s.bin;
-      last = s.last_bin;
-      u64 rest = 0;
-      part.each([&](float v, int at) {
-        if (!kept.holds(key_of(v), at)) return;
-        const u64 t = weight(v, m, w, s.powers);
-        if (fine.bin(v) < first) own += t; else rest += t;
-      });
-      const u64 above = team.sum(own, &before);
-      const u64 target = nucleus(w.top_p, above + team.sum(rest, &before));
-      const uint32_t count = collect<T, kCluster>(team, part, fine, kept, first, last);
-      u64 edge = 0;
-      if (count <= kCap) edge = find_edge<kCluster>(team, static_cast<int>(count), true, 0, above, target == 0 ? 1 : target, m, w);
-      if (edge != 0) {
-        kept.key = item_key(edge);
-        kept.last = item_index(edge);
-        summed = true;
-      } else {
-        kept = cut<T, kCluster>(s, part, m, w, kept, true, 0, w.top_p);
+      fill_bins<true>(team, part, fine, kept, bits);
+      find_sum(team, w.top_p);
+      const int first = s.bin, last = s.last_bin;
+      u64 own = 0, rest = 0, before;
+      for (int it = 0; it < part.words; ++it) {
+        float v[kVec<T>];
+        part.unpack(it, v);
+        uint32_t early = 0, late = 0;  // kept ones before the bins of the border, and from there on
+#pragma unroll
+        for (int q = 0; q < kVec<T>; ++q) {
+          const int at = part.index(it) + q;
+          if (!kept.holds(v[q], at)) continue;
+          const int b = fine.bin(v[q]);
+          if (b < first) early |= 1u << q; else late |= 1u << q;
+          if (b >= first && b <= last) enlist(team, v[q], at);
+        }
+        own += coarse_sum(v, m, w, [&](float, int q) { return (early >> q & 1) != 0; });
+        rest += coarse_sum(v, m, w, [&](float, int q) { return (late >> q & 1) != 0; });
       }
+      const u64 above = team.sum(own, &before);
+      const u64 all = above + team.sum(rest, &before);
+      if constexpr (kCluster) team.sync();
+      const u64 target = nucleus(w.top_p, all);
+      const int count = static_cast<int>(team.of_rank(&s.list_count, 0));
+      u64 edge = 0;
+      if (count <= kCap<W>)
+        edge = edge_by_sum(team, count, above, target == 0 ? 1 : target, static_cast<u64>(static_cast<float>(all) * kSure) + 1,
+                           [&](float v) { return v == m ? kOne : units(coarse(v, m, w)); });
+      kept = edge != 0 ? Prefix{value_of_key(item_key(edge)), item_index(edge)}
+                       : exact_nucleus<T, W, kCluster>(s, part, m, w, kept, first, count);
     }
     if (w.min_p > 0.f) {
       const Floor floor(m, w);
@@ -1080,28 +1228,33 @@ __global__ void __launch_bounds__(kThreads, 3) cta_kernel(const Rows a, int per)
       part.each([&](float v, int) {
         if (floor.above(v, m, w, s.powers)) least = max(least, static_cast<u64>(~key_of(v)));
       });
-      const uint32_t key = ~static_cast<uint32_t>(team.largest(least));
-      if (key > kept.key) {
-        kept.key = key;
-        kept.last = 0x7FFFFFFF;
-        summed = false;
-      }
+      const float edge = value_of_key(~static_cast<uint32_t>(team.largest(least)));
+      if (edge > kept.edge) kept = {edge, 0x7FFFFFFF};
     }
-    auto weigh = [&](float v, int at) { return kept.holds(key_of(v), at) ? weight(v, m, w, s.powers) : 0; };
-    if (summed) {
-      part.each([&](float v, int at) {
-        const int b = fine.bin(v);
-        if (b >= first && b <= last) own += weigh(v, at);
-      });
-    } else {
-      own = 0;
-      part.each([&](float v, int at) { own += weigh(v, at); });
+    auto word_sum = [&](const float(&v)[kVec<T>], int at) {
+      return coarse_sum(v, m, w, [&](float x, int q) { return kept.holds(x, at + q); });
+    };
+    u64 own = 0, before;
+    for (int it = 0; it < part.words; ++it) {
+      float v[kVec<T>];
+      part.unpack(it, v);
+      own += word_sum(v, part.index(it));
     }
+    if (threadIdx.x == 0 && team.rank == 0) s.sure = 0;
     const u64 total = team.sum(own, &before);
-    walk(part, share(w.u, total), before, own, weigh, [&](float v, int at) {
-      a.index[row] = at;
-      if (a.logprob != nullptr) a.logprob[row] = logprob_of(v, m, w, total);
-    });
+    const u64 r = share(w.u, total), margin = static_cast<u64>(static_cast<float>(total) * kSure) + 1;
+    walk(
+        part, r, before, warp_sum(own), word_sum,
+        [&](float v, int at) -> u64 { return !kept.holds(v, at) ? 0 : v == m ? kOne : units(coarse(v, m, w)); },
+        [&](float v, int at, u64 up_to, u64 its) {
+          if (up_to <= r + margin || r < up_to - its + margin) return;
+          if constexpr (kCluster) *cg::this_cluster().map_shared_rank(&s.sure, 0) = 1;
+          else s.sure = 1;
+          a.index[row] = at;
+          if (a.logprob != nullptr) a.logprob[row] = logprob_of(v, m, w, total);
+        });
+    team.sync();
+    if (team.of_rank(&s.sure, 0) == 0) exact_draw<T, W, kCluster>(s, part, a, row, m, w, kept);
   }
   if constexpr (kCluster) team.sync();  // no CTA ends while another may read its shared memory
 }
@@ -1119,19 +1272,19 @@ int64_t words_of(const Rows& a) {
   return (a.n + kVec<T> - 1) / kVec<T> + (aligned ? 0 : 1);
 }
 
-template <typename T, bool kCluster>
+template <typename T, int W, bool kCluster>
 cudaError_t run_cta(const Rows& a, int cluster, cudaStream_t stream) {
   static SmemRecord record, wide;
   const int64_t words = words_of<T>(a);
-  const int64_t lanes = static_cast<int64_t>(cluster) * kThreads;
+  const int64_t lanes = static_cast<int64_t>(cluster) * W * 32;
   const int per = static_cast<int>((words + lanes - 1) / lanes);
-  const size_t smem = static_cast<size_t>(per) * kThreads * 16;
-  const void* fn = reinterpret_cast<const void*>(cta_kernel<T, kCluster>);
+  const size_t smem = static_cast<size_t>(per) * W * 32 * 16;
+  const void* fn = reinterpret_cast<const void*>(cta_kernel<T, W, kCluster>);
   cudaError_t err = ensure_dynamic_smem(fn, smem, record);
   if (err == cudaSuccess && cluster > 8) err = allow_wide_clusters(fn, wide);
   if (err != cudaSuccess) return err;
   const int64_t rows = std::min<int64_t>(a.rows, (int64_t{1} << 30) / cluster);
-  return launch_overlapped(cta_kernel<T, kCluster>, dim3(static_cast<unsigned>(rows * cluster)), kThreads, kCluster ? cluster : 0, smem,
+  return launch_overlapped(cta_kernel<T, W, kCluster>, dim3(static_cast<unsigned>(rows * cluster)), W * 32, kCluster ? cluster : 0, smem,
                            stream, a, per);
 }
 
@@ -1149,7 +1302,9 @@ cudaError_t run(const Rows& a, cudaStream_t stream) {
   int cluster = 1;
   while (cluster < 16 && a.rows * cluster * 2 <= dev.sm_count && words >= static_cast<int64_t>(cluster) * kThreads * 8) cluster *= 2;
   while (cluster < 16 && words * 16 > static_cast<int64_t>(cluster) * 160 * 1024) cluster *= 2;
-  return cluster == 1 ? run_cta<T, false>(a, 1, stream) : run_cta<T, true>(a, cluster, stream);
+  if (cluster > 1) return run_cta<T, 8, true>(a, cluster, stream);
+  if (a.rows >= 4 * dev.sm_count && words <= 32 * 32) return run_cta<T, 1, false>(a, 1, stream);
+  return run_cta<T, 8, false>(a, 1, stream);
 }
 
 }  // namespace
