@@ -116,6 +116,14 @@ def test_ties(n, kind):
             check(x, u, f)
 
 
+def test_more_kept_than_there_are_finite_logits():
+    """The border of top-k among the logits of -infinity, far below the finite ones in the order of their bits."""
+    for n in (300, 1021, 5000):
+        x, u = logits(6, n, "fp32", seed=55, masked=0.6)
+        for f in (dict(temperature=0.07, top_k=n * 3 // 4), dict(temperature=1.0, top_k=n - 1, top_p=0.9)):
+            check(x, u, f)
+
+
 @pytest.mark.parametrize("n", [10, 1000])
 def test_zeros_of_both_signs_are_equal(n):
     x = torch.full((2, n), -3.0)

@@ -50,6 +50,14 @@ __constant__ const u64 kPowersInit[32] = {
 
 __device__ __forceinline__ float value(float x) { return x; }
 __device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T narrow(float x);
+template <>
+__device__ __forceinline__ float narrow<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <typename T>
+__device__ __forceinline__ T lowest() { return narrow<T>(-INFINITY); }
 
 // Bits of a float in its order, -0 as +0; below kLowest for the NaN that stands for no logit (a sign and all
 // other bits, in bf16 those of its upper half).
@@ -400,34 +408,41 @@ struct Prefix {
   __device__ __forceinline__ bool holds(float x, int32_t at) const { return x > edge || (x == edge && at <= last); }
 };
 
-// exp((x - m) / T) to 4e-7 of itself, sums of eight included, in a third of the instructions of weight(): what is decided by
-// such sums is sure where it is further than kSure of all from a border, and else decided by weight(). 0 for the
-// largest logits themselves, whose ones would drown a small rest: they are counted.
-constexpr float kSure = 1e-6f;
-__device__ __forceinline__ float coarse(float x, float m, const Wish& w) {
-  float e;
-  const float p = distance(x, m, w, &e) * 0.03125f;  // exact: a power of two
+// exp((x - m) / T) in a quarter of weight()'s instructions. The difference's rounding is left in: with t = (m - x) / (T ln 2) it
+// is t 2^-24 ln 2 of the weight, and the mean of t over the weights of 2^19 logits at most 14.2: 6e-7 of a sum. The
+// exponential is good to 2^-22.5, a sum of eight to 2^-22, so two sums differ from the exact ones by less than kSure of all: what is
+// decided by them is sure where it is further than that from a border, and else decided by weight(). 0 for the largest
+// logits themselves, whose ones would drown a small rest: they are counted.
+constexpr float kSure = 2.2e-6f;
+__device__ __forceinline__ float coarse(float x, float m, float c, float cl) {  // c, cl: log2(e) / T in two parts
+  const float d = __fsub_rn(m, x), p = __fmul_rn(d, c);
+  const float e = __fmaf_rn(d, cl, __fmaf_rn(d, c, -p));
   const float v = quick_exp2(-p);
-  const float r = __fmaf_rn(v, e * -0.021660849392498290f, v);
+  const float r = __fmaf_rn(v, e * -0.69314718055994531f, v);
   return p < 44.f && x != m ? r : 0.f;
 }
 __device__ __forceinline__ u64 units(float v) { return __float2ull_rn(v * 0x1p42f); }
-// N weights, those not taken as 0: a sum in pairs, and the largest logits among them.
-template <int N, typename F>
-__device__ __forceinline__ u64 coarse_sum(const float (&x)[N], float m, const Wish& w, F take) {
-  float v[N];
-  int tops = 0;
-#pragma unroll
-  for (int q = 0; q < N; ++q) {
-    const bool in = take(x[q], q);
-    v[q] = in ? coarse(x[q], m, w) : 0.f;
-    tops += in && x[q] == m;
-  }
+// A sum in pairs.
+template <int N>
+__device__ __forceinline__ float sum_in_pairs(float (&v)[N]) {
 #pragma unroll
   for (int o = N / 2; o > 0; o >>= 1)
 #pragma unroll
     for (int q = 0; q < o; ++q) v[q] += v[q + o];
-  return units(v[0]) + (static_cast<u64>(tops) << kUnit);
+  return v[0];
+}
+// N weights, those not taken as 0, and the largest logits among them.
+template <int N, typename F>
+__device__ __forceinline__ u64 coarse_sum(const float (&x)[N], float m, float c, float cl, F take) {
+  float v[N];
+  uint32_t tops = 0;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const bool in = take(x[q], q);
+    v[q] = in ? coarse(x[q], m, c, cl) : 0.f;
+    tops += in && x[q] == m;
+  }
+  return units(sum_in_pairs(v)) + (static_cast<u64>(tops) << kUnit);
 }
 
 template <typename T>
@@ -584,14 +599,14 @@ __device__ __forceinline__ void walk(const Part<T>& part, u64 r, u64 before, u64
   const int lane = threadIdx.x & 31;
   if (r < before || r >= before + total) return;
   for (int it = 0; it < part.words; ++it) {
-    float v[kVec<T>];
-    part.unpack(it, v);
-    const u64 own = word_sum(v, part.index(it));
+    const u64 own = word_sum(it);
     const u64 scan = warp_scan(own, lane);
     const u64 all = __shfl_sync(kAll, scan, 31);
     if (r < before + all) {
       const uint32_t over = __ballot_sync(kAll, before + scan > r);
       if (lane == __ffs(over) - 1) {
+        float v[kVec<T>];
+        part.unpack(it, v);
         u64 at = before + scan - own;
         bool done = false;
 #pragma unroll
@@ -683,7 +698,7 @@ __device__ __noinline__ Prefix cut(Shared<W, kCluster>& s, const Part<T> part, f
   {
     // Bins of an eighth of a binary order of the weights, the last one with all that is below.
     const float scale = w.ch * 0.25f;
-    auto bin_of = [&](float x) { return x == m ? 0 : min(kBins - 1, __float2int_rd((m - x) * scale)); };
+    auto bin_of = [&](float x) { return min(kBins - 1, __float2int_rd((m - x) * scale)); };
     clear_bins(s);
     part.each([&](float x, int at) {
       if (!in.holds(x, at)) return;
@@ -722,11 +737,11 @@ __device__ __noinline__ Prefix cut(Shared<W, kCluster>& s, const Part<T> part, f
       if (shift == 0) {
         low = high = top;
       } else {
-        const uint32_t bottom = top - ((1u << shift) - 1);
+        const uint32_t span = (1u << shift) - 1, bottom = top - low > span ? top - span : low;
         most = least = 0;
         part.each([&](float x, int at) {
           const uint32_t k = key_of(x);
-          if (k <= top && k >= bottom && k >= low && in.holds(x, at)) {
+          if (k <= top && k >= bottom && in.holds(x, at)) {
             most = max(most, static_cast<u64>(k));
             least = max(least, static_cast<u64>(~k));
           }
@@ -751,10 +766,12 @@ __device__ __noinline__ Prefix cut(Shared<W, kCluster>& s, const Part<T> part, f
   if (ties < all) {
     walk(
         part, ties - 1, before, warp_sum(mine),
-        [&](const float(&v)[kVec<T>], int at) {
+        [&](int it) {
+          float v[kVec<T>];
+          part.unpack(it, v);
           u64 t = 0;
 #pragma unroll
-          for (int q = 0; q < kVec<T>; ++q) t += tied(v[q], at + q);
+          for (int q = 0; q < kVec<T>; ++q) t += tied(v[q], part.index(it) + q);
           return t;
         },
         tied,
@@ -773,19 +790,12 @@ __device__ __noinline__ Prefix cut(Shared<W, kCluster>& s, const Part<T> part, f
   return kept;
 }
 
-// A logit's bin, and how far into it (in bins) it lies.
+// How many bins a logit lies below the largest: its bin and how far into it.
 struct Fine {
   float m, scale;
   __device__ __forceinline__ Fine(float top, const Wish& w) : m(top), scale(0.5f * w.ch) {}
-  __device__ __forceinline__ int bin(float x, float* into) const {
-    const float f = x == m ? 0.f : __fmul_rn(__fsub_rn(m, x), scale);
-    const int b = min(kFine - 1, __float2int_rd(f));
-    *into = f - static_cast<float>(b);
-    return b;
-  }
-  __device__ __forceinline__ int bin(float x) const {
-    return x == m ? 0 : min(kFine - 1, __float2int_rd(__fmul_rn(__fsub_rn(m, x), scale)));
-  }
+  __device__ __forceinline__ float at(float x) const { return __fmul_rn(__fsub_rn(m, x), scale); }
+  __device__ __forceinline__ int bin(float f) const { return min(kFine - 1, __float2int_rd(f)); }
 };
 __device__ __forceinline__ u64 item_of(uint32_t key, int at) { return static_cast<u64>(key) << 32 | static_cast<uint32_t>(~at); }
 __device__ __forceinline__ uint32_t item_key(u64 item) { return static_cast<uint32_t>(item >> 32); }
@@ -810,9 +820,11 @@ __device__ __forceinline__ void fill_bins(Team<W, kCluster>& team, const Part<T>
   const float unit = static_cast<float>(1 << bits);
   part.each([&](float x, int at) {
     if (!in.holds(x, at)) return;
-    float into;
-    const int b = fine.bin(x, &into);
-    atomicAdd(&s.fine[fine_place(b)], kSums ? static_cast<uint32_t>(__float2int_rn(unit * quick_exp2(into * -0.0625f))) : 1u);
+    const float f = fine.at(x);
+    const int b = fine.bin(f);
+    uint32_t add = 1u;
+    if (kSums) add = static_cast<uint32_t>(__float2int_rn(unit * quick_exp2((f - static_cast<float>(b)) * -0.0625f)));
+    atomicAdd(&s.fine[fine_place(b)], add);
   });
   team.sync();
   if constexpr (kSums || kCluster) {
@@ -923,7 +935,7 @@ template <typename T, int W, bool kCluster>
 __device__ __forceinline__ void collect(Team<W, kCluster>& team, const Part<T>& part, const Fine& fine, const Prefix& in, int first, int last) {
   part.each([&](float x, int at) {
     if (!in.holds(x, at)) return;
-    const int b = fine.bin(x);
+    const int b = fine.bin(fine.at(x));
     if (b >= first && b <= last) enlist(team, x, at);
   });
   team.sync();
@@ -1049,7 +1061,7 @@ __device__ __noinline__ Prefix exact_nucleus(Shared<W, kCluster>& s, const Part<
     part.each([&](float v, int at) {
       if (!in.holds(v, at)) return;
       const u64 t = weight(v, m, w, s.powers);
-      if (fine.bin(v) < first) own += t; else rest += t;
+      if (fine.bin(fine.at(v)) < first) own += t; else rest += t;
     });
     const u64 above = team.sum(own, &before);
     u64 target = nucleus(w.top_p, above + team.sum(rest, &before));
@@ -1073,10 +1085,12 @@ __device__ __noinline__ void exact_draw(Shared<W, kCluster>& s, const Part<T> pa
   const u64 total = team.sum(own, &before);
   walk(
       part, share(w.u, total), before, warp_sum(own),
-      [&](const float(&v)[kVec<T>], int at) {
+      [&](int it) {
+        float v[kVec<T>];
+        part.unpack(it, v);
         u64 t = 0;
 #pragma unroll
-        for (int q = 0; q < kVec<T>; ++q) t += weigh(v[q], at + q);
+        for (int q = 0; q < kVec<T>; ++q) t += weigh(v[q], part.index(it) + q);
         return t;
       },
       weigh,
@@ -1099,6 +1113,9 @@ __global__ void __launch_bounds__(W * 32, 24 / W) cta_kernel(const Rows a, int p
   const int n = static_cast<int>(a.n);
   // So that no bin's sum passes 32 bits.
   const int bits = min(16, __clz(per * W * 32 * kVec<T>) - 1);
+  // The words' sums, for the walk, in the list's place where that holds them.
+  u64* const sums = s.list;
+  const bool sums_fit = per * W * 32 <= 2 * kCap<W>;
   after_previous();
   for (int64_t row = blockIdx.x / team.ranks; row < a.rows; row += gridDim.x / team.ranks) {
     const T* x = static_cast<const T*>(a.x) + row * n;
@@ -1127,35 +1144,32 @@ __global__ void __launch_bounds__(W * 32, 24 / W) cta_kernel(const Rows a, int p
         } else {
           T* to = reinterpret_cast<T*>(mine + (it0 + u) * 32);
           for (int q = 0; q < kVec<T>; ++q) {
-            if (at + q >= 0 && at + q < n) {
-              to[q] = fetch(x + at + q);
-            } else if constexpr (sizeof(T) == 2) {
-              reinterpret_cast<uint16_t*>(to)[q] = 0xFFFFu;
-            } else {
-              reinterpret_cast<uint32_t*>(to)[q] = 0xFFFFFFFFu;
-            }
+            // No logit there: one that is never drawn, and after all others in the order.
+            to[q] = at + q >= 0 && at + q < n ? fetch(x + at + q) : lowest<T>();
           }
         }
       }
     }
-    // A NaN of the row is told from the places without a logit by its index.
-    bool nan = false;
-    part.each([&](float v, int at) {
-      if (v > m) m = v;
-      if (v != v && at >= 0 && at < n) nan = true;
-    });
+    part.each([&](float v, int) { m = max_nan(m, v); });
     const Wish w = wish_of(a, row);
     {
-      const u64 top = team.largest(nan ? ~0ull : static_cast<u64>(key_of(m)));  // (and the powers are there)
-      nan = top == ~0ull;
-      m = value_of_key(static_cast<uint32_t>(top));
+      const u64 top = team.largest(m != m ? ~0ull : static_cast<u64>(key_of(m)));  // (and the powers are there)
+      m = top == ~0ull ? NAN : value_of_key(static_cast<uint32_t>(top));
     }
-    if (w.bad || nan || m == -INFINITY) {
+    if (w.bad || m != m || m == -INFINITY) {
       if (threadIdx.x == 0 && team.rank == 0) {
         a.index[row] = -1;
         if (a.logprob != nullptr) a.logprob[row] = NAN;
       }
       continue;
+    }
+    if (m == INFINITY) {
+      // All of the probability is the infinite ones': as if they were 0, and the others -infinity.
+      for (int it = 0; it < per; ++it) {
+        T* to = reinterpret_cast<T*>(mine + it * 32);
+        for (int q = 0; q < kVec<T>; ++q) to[q] = value(to[q]) == INFINITY ? narrow<T>(0.f) : lowest<T>();
+      }
+      m = 0.f;
     }
     if (w.top_k == 1) {
       // The first of the largest.
@@ -1171,6 +1185,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W) cta_kernel(const Rows a, int p
       continue;
     }
     const Fine fine(m, w);
+    const float c = w.ch * 0.03125f, cl = w.cl * 0.03125f;
     Prefix kept;
     if (w.top_k < n) {
       fill_bins<false>(team, part, fine, kept, 0);
@@ -1194,31 +1209,36 @@ __global__ void __launch_bounds__(W * 32, 24 / W) cta_kernel(const Rows a, int p
       fill_bins<true>(team, part, fine, kept, bits);
       find_sum(team, w.top_p);
       const int first = s.bin, last = s.last_bin;
-      u64 own = 0, rest = 0, before;
+      const float from = static_cast<float>(first), to = last == kFine - 1 ? INFINITY : static_cast<float>(last + 1);
+      u64 own = 0, all = 0, before;
       for (int it = 0; it < part.words; ++it) {
-        float v[kVec<T>];
+        float v[kVec<T>], early[kVec<T>];
         part.unpack(it, v);
-        uint32_t early = 0, late = 0;  // kept ones before the bins of the border, and from there on
+        uint32_t tops = 0, early_tops = 0;
 #pragma unroll
         for (int q = 0; q < kVec<T>; ++q) {
           const int at = part.index(it) + q;
-          if (!kept.holds(v[q], at)) continue;
-          const int b = fine.bin(v[q]);
-          if (b < first) early |= 1u << q; else late |= 1u << q;
-          if (b >= first && b <= last) enlist(team, v[q], at);
+          const bool in = kept.holds(v[q], at);
+          const float f = fine.at(v[q]);
+          const bool top = in && v[q] == m;
+          if (in && f >= from && f < to) enlist(team, v[q], at);
+          v[q] = in ? coarse(v[q], m, c, cl) : 0.f;
+          early[q] = f < from ? v[q] : 0.f;
+          tops += top;
+          early_tops += top && f < from;
         }
-        own += coarse_sum(v, m, w, [&](float, int q) { return (early >> q & 1) != 0; });
-        rest += coarse_sum(v, m, w, [&](float, int q) { return (late >> q & 1) != 0; });
+        own += units(sum_in_pairs(early)) + (static_cast<u64>(early_tops) << kUnit);
+        all += units(sum_in_pairs(v)) + (static_cast<u64>(tops) << kUnit);
       }
       const u64 above = team.sum(own, &before);
-      const u64 all = above + team.sum(rest, &before);
+      all = team.sum(all, &before);
       if constexpr (kCluster) team.sync();
       const u64 target = nucleus(w.top_p, all);
       const int count = static_cast<int>(team.of_rank(&s.list_count, 0));
       u64 edge = 0;
       if (count <= kCap<W>)
         edge = edge_by_sum(team, count, above, target == 0 ? 1 : target, static_cast<u64>(static_cast<float>(all) * kSure) + 1,
-                           [&](float v) { return v == m ? kOne : units(coarse(v, m, w)); });
+                           [&](float v) { return v == m ? kOne : units(coarse(v, m, c, cl)); });
       kept = edge != 0 ? Prefix{value_of_key(item_key(edge)), item_index(edge)}
                        : exact_nucleus<T, W, kCluster>(s, part, m, w, kept, first, count);
     }
@@ -1231,21 +1251,31 @@ __global__ void __launch_bounds__(W * 32, 24 / W) cta_kernel(const Rows a, int p
       const float edge = value_of_key(~static_cast<uint32_t>(team.largest(least)));
       if (edge > kept.edge) kept = {edge, 0x7FFFFFFF};
     }
+    const bool whole = kept.edge == -INFINITY;  // then every weight counts, those of -infinity as 0
     auto word_sum = [&](const float(&v)[kVec<T>], int at) {
-      return coarse_sum(v, m, w, [&](float x, int q) { return kept.holds(x, at + q); });
+      return whole ? coarse_sum(v, m, c, cl, [](float, int) { return true; })
+                   : coarse_sum(v, m, c, cl, [&](float x, int q) { return kept.holds(x, at + q); });
     };
     u64 own = 0, before;
     for (int it = 0; it < part.words; ++it) {
       float v[kVec<T>];
       part.unpack(it, v);
-      own += word_sum(v, part.index(it));
+      const u64 sum = word_sum(v, part.index(it));
+      if (sums_fit) sums[it * W * 32 + threadIdx.x] = sum;
+      own += sum;
     }
     if (threadIdx.x == 0 && team.rank == 0) s.sure = 0;
     const u64 total = team.sum(own, &before);
     const u64 r = share(w.u, total), margin = static_cast<u64>(static_cast<float>(total) * kSure) + 1;
     walk(
-        part, r, before, warp_sum(own), word_sum,
-        [&](float v, int at) -> u64 { return !kept.holds(v, at) ? 0 : v == m ? kOne : units(coarse(v, m, w)); },
+        part, r, before, warp_sum(own),
+        [&](int it) {
+          if (sums_fit) return sums[it * W * 32 + threadIdx.x];
+          float v[kVec<T>];
+          part.unpack(it, v);
+          return word_sum(v, part.index(it));
+        },
+        [&](float v, int at) -> u64 { return !kept.holds(v, at) ? 0 : v == m ? kOne : units(coarse(v, m, c, cl)); },
         [&](float v, int at, u64 up_to, u64 its) {
           if (up_to <= r + margin || r < up_to - its + margin) return;
           if constexpr (kCluster) *cg::this_cluster().map_shared_rank(&s.sure, 0) = 1;
