@@ -7,7 +7,8 @@ as a C-ABI CUDA library (``libvn.so``, declared in ``include/vn.h``) with a thin
 Python binding. The noise is regenerated on the fly from (seed, element index)
 and never materialised. Beside it the centre network that the step perturbs, run
 unperturbed and trained by its gradients: the linear layer with bias, activation and
-residual, layer norm, and AdamW.
+residual, layer norm, gradient clipping and AdamW, the layer on weights in 4 bits, and
+the drawing of an action from logits.
 """
 
 from .api import (  # noqa: F401

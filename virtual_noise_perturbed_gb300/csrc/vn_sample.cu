@@ -1379,10 +1379,13 @@ cudaError_t run(const Rows& a, cudaStream_t stream) {
   if (a.n <= 32) return run_warp<T, 1>(a, stream);
   if (a.n <= 64) return run_warp<T, 2>(a, stream);
   if (a.n <= 128) return run_warp<T, 4>(a, stream);
-  if (a.n <= 256) return run_warp<T, 8>(a, stream);
   DeviceInfo dev;
   const cudaError_t err = device_info(&dev);
   if (err != cudaSuccess) return err;
+  // Up to 256 logits where a warp a row does not fill the GPU anyhow: 1024 rows of 256 bf16 take 5.4 us here (13.4 with top-p, 7.2 with
+  // top-k) and 10.0 (10.0, 12.6) by a histogram, 16384 rows 31 (84, 44) and 31 (45, 67).
+  const bool many = a.rows >= 24 * static_cast<int64_t>(dev.sm_count);
+  if (a.n <= 256 && !many) return run_warp<T, 8>(a, stream);
   // CTAs a row: until the rows fill the SMs, while a lane has four words or more; at least what holds the row.
   const int64_t words = words_of<T>(a);
   int cluster = 1;
@@ -1392,7 +1395,7 @@ cudaError_t run(const Rows& a, cudaStream_t stream) {
   // Warps a row. Many rows side by side run best on few warps each, long rows and few of them on more: 16384 rows of 1000
   // bf16 with top-p take 98 us on one warp, 137 on four, 269 on eight; of 4096 436, 269, 365; 1024 rows of 16384 139 on
   // four, 105 on eight; 1024 rows of 1000 24, 17, 24.
-  if (words <= 256 && a.rows >= 24 * static_cast<int64_t>(dev.sm_count)) return run_cta<T, 1, false>(a, 1, stream);
+  if (words <= 256 && many) return run_cta<T, 1, false>(a, 1, stream);
   if (words <= 1024 && a.rows >= 2 * static_cast<int64_t>(dev.sm_count)) return run_cta<T, 4, false>(a, 1, stream);
   return run_cta<T, 8, false>(a, 1, stream);
 }

@@ -14,7 +14,7 @@ laid out as ``compute_offsets`` says, so both phases update the same memory.
 from __future__ import annotations
 
 import argparse
-from typing import List, Sequence
+from typing import List, Optional, Sequence
 
 import torch
 
@@ -73,11 +73,11 @@ class Policy:
 
 def run(widths: Sequence[int] = (64, 256, 256, 8), *, batch: int = 1024, steps: int = 200, pop: int = 1024,
         generations: int = 30, sigma: float = 0.02, lr: float = 2e-3, es_lr: float = 1e-3, state_bits: int = 32,
-        seed: int = 0, device="cuda"):
+        max_norm: Optional[float] = None, seed: int = 0, device="cuda"):
     """Both phases on synthetic data; returns (losses of the warm start, mean returns of the centre).
 
     The losses are one a step; the returns are the centre's on the episode's observations before
-    the first generation and after each."""
+    the first generation and after each. ``max_norm`` bounds the norm of the warm start's gradients."""
     g = torch.Generator().manual_seed(seed)
     teacher = Policy(widths, device, g)
     policy = Policy(widths, device, g)
@@ -87,7 +87,7 @@ def run(widths: Sequence[int] = (64, 256, 256, 8), *, batch: int = 1024, steps: 
     for _ in range(steps):
         obs = (torch.randn(batch, widths[0], generator=g) * 3 + 1).to(device)
         loss, grads = policy.gradients(obs, teacher(obs))
-        optimizer.step(grads)
+        optimizer.step(grads, max_norm=max_norm)
         losses.append(loss)
 
     # The episode: a few observations whose wanted actions differ from the teacher's.
@@ -115,8 +115,9 @@ def main() -> None:
     p.add_argument("--steps", type=int, default=200)
     p.add_argument("--generations", type=int, default=30)
     p.add_argument("--state-bits", type=int, choices=(8, 32), default=32)
+    p.add_argument("--max-norm", type=float, default=None)
     a = p.parse_args()
-    losses, returns = run(steps=a.steps, generations=a.generations, state_bits=a.state_bits)
+    losses, returns = run(steps=a.steps, generations=a.generations, state_bits=a.state_bits, max_norm=a.max_norm)
     print(f"warm start: loss {losses[0]:.4f} -> {losses[-1]:.4f} in {len(losses)} steps")
     print(f"evolution:  return {returns[0]:.4f} -> {returns[-1]:.4f} in {len(returns) - 1} generations")
 

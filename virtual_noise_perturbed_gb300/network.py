@@ -1,7 +1,9 @@
 """The centre network: what the population step perturbs, run unperturbed and trained.
 
-``linear`` and ``layer_norm`` with their gradients, and ``AdamW``, the parameter step for any
-gradient: these, or the population's estimate (``virtual_flat_gradient`` and the others).
+``linear`` and ``layer_norm`` with their gradients, ``gradient_norm`` and ``clip_gradients``, and ``AdamW``, the
+parameter step for any gradient: these, or the population's estimate (``virtual_flat_gradient`` and the others).
+For acting ``pack4`` and ``linear4``, a layer's weights in 4 bits and ``linear`` on them, and ``sample``, an
+index for each row of logits.
 
 Like the rest of the package's Python, these functions only check and marshal arguments and
 call ``libvn.so`` on the current CUDA stream; all arithmetic runs in the library's kernels.
