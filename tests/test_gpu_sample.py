@@ -93,6 +93,7 @@ def test_the_longest_row(kind):
     x, u = logits(1, 524288, kind, seed=30)
     check(x, u, dict(temperature=1.1))
     check(x, u, dict(temperature=0.8, top_k=1000, top_p=0.9))
+    check(x[:, 1:], u, dict(top_p=0.95))  # no row on a vector load's boundary: a word more
 
 
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])

@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 2) packed_kernel(const PackedArgs a,
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) {
         typename FourOf<T>::Type x[8];
-        const T* const p0 = from[n] + (base + d) * kBlock;
+        const T* const p0 = from[n] + static_cast<int64_t>(base + d) * kBlock;
         if (vec && k + kBlock <= a.in) {
           aligned_block(p0, x);
         } else if (k > 0 && k + kBlock + 4 <= a.in) {

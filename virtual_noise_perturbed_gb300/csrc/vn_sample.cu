@@ -472,20 +472,27 @@ __device__ __forceinline__ u64 coarse_sum(const float (&x)[N], float m, float c,
 template <typename T>
 constexpr int kVec = 16 / static_cast<int>(sizeof(T));  // logits of 16 bytes
 
-// Bins of a sixteenth of a binary order of the weights, the last one with all that is below; padded in shared memory,
-// so that lanes with sixteen neighbours each read from different banks.
-constexpr int kFine = 512;
-__device__ __forceinline__ int fine_place(int bin) { return bin + (bin >> 4); }
-constexpr int kFinePlaces = kFine + kFine / 16;
+// Bins of a fraction of a binary order of the weights, over 32 of them, the last bin with all that is below: finer ones for the
+// longer rows, so that few logits share the bin of a border (131071 fp32 with top-p on 512 bins: 9 us a row, on 2048 XX). Padded
+// in shared memory, so that lanes with an order each read from different banks.
+template <int W>
+constexpr int kPerOrder = W < 8 ? 16 : 64;
+template <int W>
+constexpr int kFine = 32 * kPerOrder<W>;
+template <int W>
+__device__ __forceinline__ int fine_place(int bin) { return bin + bin / kPerOrder<W>; }
+template <int W>
+constexpr int kFinePlaces = kFine<W> + 32;
 // The most logits that a border is looked for among one by one, and the most that all of the rest is done for so.
 template <int W>
-constexpr int kCap = W == 1 ? 256 : W < 8 ? 512 : 1024;
+constexpr int kCap = W == 1 ? 256 : 512;
 template <int W>
 constexpr int kFew = W == 1 ? 64 : W < 8 ? 128 : 256;
 
 struct NoBins {};
+template <int W>
 struct MergedBins {
-  uint32_t fine[kFinePlaces];
+  uint32_t fine[kFinePlaces<W>];
 };
 // A CTA's shared memory but for its logits.
 template <int W, bool kCluster>
@@ -501,8 +508,8 @@ struct Shared {
       uint32_t counts[kBins];
     };
   };
-  uint32_t fine[kFinePlaces];     // counts of the bins
-  std::conditional_t<kCluster, MergedBins, NoBins> merged;  // over all ranks, in a cluster
+  uint32_t fine[kFinePlaces<W>];  // counts of the bins, or sums
+  std::conditional_t<kCluster, MergedBins<W>, NoBins> merged;  // over all ranks, in a cluster
   uint32_t list_count;
   u64 edge[2];                    // the last one kept, by count and by sum: a rank may still read the one when the other is cleared
   u64 warps[2][W], warps_too[2][W];  // of the two reductions at work at most
@@ -538,6 +545,7 @@ struct Part {
   __device__ __forceinline__ int index(int it) const { return first + it * 32 * kVec<T>; }
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
+#pragma unroll 1
     for (int it = 0; it < words; ++it) {
       float v[kVec<T>];
       unpack(it, v);
@@ -648,6 +656,7 @@ template <typename T, typename S, typename E, typename F>
 __device__ __forceinline__ void walk(const Part<T>& part, u64 r, u64 before, u64 total, S word_sum, E each, F found) {
   const int lane = threadIdx.x & 31;
   if (r < before || r >= before + total) return;
+#pragma unroll 1
   for (int it = 0; it < part.words; ++it) {
     const u64 own = word_sum(it);
     const u64 scan = warp_scan(own, lane);
@@ -834,12 +843,13 @@ __device__ __noinline__ Prefix cut(Shared<W, kCluster>& s, const Part<T> part, f
   return kept;
 }
 
-// How many bins a logit lies below the largest: its bin and how far into it.
+// How many bins a logit lies below the largest, and its bin.
+template <int W>
 struct Fine {
   float m, scale;
-  __device__ __forceinline__ Fine(float top, const Wish& w) : m(top), scale(0.5f * w.ch) {}
+  __device__ __forceinline__ Fine(float top, const Wish& w) : m(top), scale(w.ch * (kPerOrder<W> * 0.03125f)) {}
   __device__ __forceinline__ float at(float x) const { return __fmul_rn(__fsub_rn(m, x), scale); }
-  __device__ __forceinline__ int bin(float f) const { return min(kFine - 1, __float2int_rd(f)); }
+  __device__ __forceinline__ int bin(float f) const { return min(kFine<W> - 1, __float2int_rd(f)); }
 };
 __device__ __forceinline__ u64 item_of(uint32_t key, int at) { return static_cast<u64>(key) << 32 | static_cast<uint32_t>(~at); }
 __device__ __forceinline__ uint32_t item_key(u64 item) { return static_cast<uint32_t>(item >> 32); }
@@ -853,9 +863,9 @@ __device__ __forceinline__ uint32_t* bins_of(Shared<W, kCluster>& s) {
 // Counts of the logits, or (kSums) their weights, over all ranks, in bins_of(s): sums in units of 2^-bits of the largest
 // weight of their bin, good to 2^-12, in 32 bits.
 template <bool kSums, typename T, int W, bool kCluster>
-__device__ __forceinline__ void fill_bins(Team<W, kCluster>& team, const Part<T>& part, const Fine& fine, int bits) {
+__device__ __forceinline__ void fill_bins(Team<W, kCluster>& team, const Part<T>& part, const Fine<W>& fine, int bits) {
   Shared<W, kCluster>& s = team.s;
-  for (int b = threadIdx.x; b < kFinePlaces; b += W * 32) s.fine[b] = 0;
+  for (int b = threadIdx.x; b < kFinePlaces<W>; b += W * 32) s.fine[b] = 0;
   if (threadIdx.x == 0) {
     s.list_count = 0;
     s.edge[kSums] = 0;
@@ -866,32 +876,30 @@ __device__ __forceinline__ void fill_bins(Team<W, kCluster>& team, const Part<T>
     const float f = fine.at(x);
     const int b = fine.bin(f);
     uint32_t add = 1u;
-    if (kSums) add = static_cast<uint32_t>(__float2int_rn(unit * quick_exp2((f - static_cast<float>(b)) * -0.0625f)));
-    atomicAdd(&s.fine[fine_place(b)], add);
+    if (kSums) add = static_cast<uint32_t>(__float2int_rn(unit * quick_exp2((f - static_cast<float>(b)) * (-1.f / kPerOrder<W>))));
+    atomicAdd(&s.fine[fine_place<W>(b)], add);
   });
   team.sync();
   if constexpr (kCluster) {
-    for (int b = threadIdx.x; b < kFine; b += W * 32) {
+    for (int b = threadIdx.x; b < kFine<W>; b += W * 32) {
       uint32_t count = 0;
-      for (int r = 0; r < team.ranks; ++r) count += team.of_rank(&s.fine[fine_place(b)], r);
-      s.merged.fine[fine_place(b)] = count;
+      for (int r = 0; r < team.ranks; ++r) count += team.of_rank(&s.fine[fine_place<W>(b)], r);
+      s.merged.fine[fine_place<W>(b)] = count;
     }
     __syncthreads();
   }
 }
 
-// By count: the bin that the logit number `target` (from 1) of the order is in.
+// By count: the bin that the logit number `target` (from 1) of the order is in. A lane has the bins of one binary order.
 template <int W, bool kCluster>
 __device__ __forceinline__ void find_count(Team<W, kCluster>& team, uint32_t target) {
   Shared<W, kCluster>& s = team.s;
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    uint32_t own[kFine / 32], total = 0;
-#pragma unroll
-    for (int b = 0; b < kFine / 32; ++b) {
-      own[b] = bins_of(s)[fine_place(lane * (kFine / 32) + b)];
-      total += own[b];
-    }
+    const uint32_t* const own = bins_of(s) + lane * (kPerOrder<W> + 1);
+    uint32_t total = 0;
+#pragma unroll 8
+    for (int b = 0; b < kPerOrder<W>; ++b) total += own[b];
     uint32_t scan = total;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -901,17 +909,11 @@ __device__ __forceinline__ void find_count(Team<W, kCluster>& team, uint32_t tar
     const uint32_t reach = __ballot_sync(kAll, scan >= target);
     if (reach != 0 && lane == __ffs(reach) - 1) {
       uint32_t at = scan - total;
-      bool found = false;
-#pragma unroll
-      for (int b = 0; b < kFine / 32; ++b) {
-        if (!found && at + own[b] >= target) {
-          found = true;
-          s.bin = s.last_bin = lane * (kFine / 32) + b;
-          s.above_count = at;
-          s.bin_count = own[b];
-        }
-        at += own[b];
-      }
+      int b = 0;
+      while (b < kPerOrder<W> - 1 && at + own[b] < target) at += own[b++];
+      s.bin = s.last_bin = lane * kPerOrder<W> + b;
+      s.above_count = at;
+      s.bin_count = own[b];
     }
   }
   team.sync();
@@ -923,15 +925,12 @@ __device__ __forceinline__ void find_sum(Team<W, kCluster>& team, u64 top_p) {
   Shared<W, kCluster>& s = team.s;
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    constexpr float kSteps[16] = {1.000000000f, 0.957603281f, 0.917004043f, 0.878126080f, 0.840896415f, 0.805245166f, 0.771105413f, 0.738413073f,
-                                  0.707106781f, 0.677127773f, 0.648419777f, 0.620928906f, 0.594603558f, 0.569394317f, 0.545253866f, 0.522136891f};
+    const uint32_t* const own = bins_of(s) + lane * (kPerOrder<W> + 1);
     const float unit = quick_exp2(static_cast<float>(-lane));
-    float own[kFine / 32], total = 0.f;
-#pragma unroll
-    for (int b = 0; b < kFine / 32; ++b) {
-      own[b] = static_cast<float>(bins_of(s)[fine_place(lane * (kFine / 32) + b)]) * (kSteps[b] * unit);
-      total += own[b];
-    }
+    auto sum_of = [&](int b) { return static_cast<float>(own[b]) * (quick_exp2(static_cast<float>(b) * (-1.f / kPerOrder<W>)) * unit); };
+    float total = 0.f;
+#pragma unroll 8
+    for (int b = 0; b < kPerOrder<W>; ++b) total += sum_of(b);
     float scan = total;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -941,19 +940,21 @@ __device__ __forceinline__ void find_sum(Team<W, kCluster>& team, u64 top_p) {
     const float all = __shfl_sync(kAll, scan, 31), border = all * (static_cast<float>(static_cast<uint32_t>(top_p >> 32)) * 0x1p-32f);
     const float off = (all - border) * 0x1p-11f + all * 0x1p-19f;
     const float early = border - off, late = border + off;
-    int first = kFine, last = kFine;
+    int first = kFine<W>, last = kFine<W>;
     float at = scan - total;
-#pragma unroll
-    for (int b = 0; b < kFine / 32; ++b) {
-      at += own[b];
-      if (at >= early) first = min(first, lane * (kFine / 32) + b);
-      if (at >= late) last = min(last, lane * (kFine / 32) + b);
+    if (scan >= early) {
+#pragma unroll 4
+      for (int b = 0; b < kPerOrder<W>; ++b) {
+        at += sum_of(b);
+        if (at >= early) first = min(first, lane * kPerOrder<W> + b);
+        if (at >= late) last = min(last, lane * kPerOrder<W> + b);
+      }
     }
     first = static_cast<int>(__reduce_min_sync(kAll, static_cast<unsigned>(first)));
     last = static_cast<int>(__reduce_min_sync(kAll, static_cast<unsigned>(last)));
     if (lane == 0) {
-      s.bin = min(first, kFine - 1);
-      s.last_bin = min(last, kFine - 1);
+      s.bin = min(first, kFine<W> - 1);
+      s.last_bin = min(last, kFine<W> - 1);
     }
   }
   team.sync();
@@ -969,7 +970,7 @@ __device__ __forceinline__ void enlist(Team<W, kCluster>& team, float x, int at)
 }
 // The logits of bins first .. last.
 template <typename T, int W, bool kCluster>
-__device__ __forceinline__ void collect(Team<W, kCluster>& team, const Part<T>& part, const Fine& fine, int first, int last) {
+__device__ __forceinline__ void collect(Team<W, kCluster>& team, const Part<T>& part, const Fine<W>& fine, int first, int last) {
   part.each([&](float x, int at) {
     const int b = fine.bin(fine.at(x));
     if (b >= first && b <= last) enlist(team, x, at);
@@ -996,7 +997,7 @@ __device__ __forceinline__ u64 cta_sum(Shared<W, kCluster>& s, int place, u64 v)
 // All of the rest for at most kFew<W> logits that s.list holds, the first top_k of the order among them: of each its place in
 // either order, and what lies before it, come from a look at every other.
 template <int W, bool kCluster>
-__device__ __forceinline__ void few(Shared<W, kCluster>& s, const Rows& a, int64_t row, float m, const Wish& w, int count) {
+__device__ __noinline__ void few(Shared<W, kCluster>& s, const Rows& a, int64_t row, float m, const Wish w, int count) {
   constexpr int kEach = kFew<W> / (W * 32);  // logits of a thread
   for (int i = threadIdx.x; i < count; i += W * 32)
     s.list_weights[i] = weight(value_of_key(item_key(s.list[i])), m, w, s.powers);
@@ -1091,7 +1092,7 @@ __device__ __noinline__ Prefix exact_nucleus(Shared<W, kCluster>& s, const Part<
   if (count <= kCap<W>) {
     Team<W, kCluster> team(s);
     team.sync();  // its reductions take their places from the first again
-    const Fine fine(m, w);
+    const Fine<W> fine(m, w);
     u64 own = 0, rest = 0, before;
     part.each([&](float v, int) {
       const u64 t = weight(v, m, w, s.powers);
@@ -1198,6 +1199,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W) cta_kernel(const Rows a, int p
     }
     if (m == INFINITY) {
       // All of the probability is the infinite ones': as if they were 0, and the others -infinity.
+#pragma unroll 1
       for (int it = 0; it < per; ++it) {
         T* to = reinterpret_cast<T*>(mine + it * 32);
         for (int q = 0; q < kVec<T>; ++q) to[q] = value(to[q]) == INFINITY ? narrow<T>(0.f) : lowest<T>();
@@ -1217,7 +1219,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W) cta_kernel(const Rows a, int p
       }
       continue;
     }
-    const Fine fine(m, w);
+    const Fine<W> fine(m, w);
     const float c = w.ch * 0.03125f, cl = w.cl * 0.03125f;
     if (w.top_k < n) {
       fill_bins<false>(team, part, fine, 0);
@@ -1238,6 +1240,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W) cta_kernel(const Rows a, int p
         first = cut<T, W, kCluster>(s, part, m, w, false, static_cast<u64>(w.top_k));
       }
       // The others are out for good.
+#pragma unroll 1
       for (int it = 0; it < per; ++it) {
         float v[kVec<T>];
         part.unpack(it, v);
@@ -1254,8 +1257,10 @@ __global__ void __launch_bounds__(W * 32, 24 / W) cta_kernel(const Rows a, int p
       find_sum(team, w.top_p);
       const int first = s.bin, last = s.last_bin;
       // The same borders in units of coarse()'s distance.
-      const float from = static_cast<float>(first) * 0.0625f, to = last == kFine - 1 ? INFINITY : static_cast<float>(last + 1) * 0.0625f;
+      const float from = static_cast<float>(first) * (1.f / kPerOrder<W>);
+      const float to = last == kFine<W> - 1 ? INFINITY : static_cast<float>(last + 1) * (1.f / kPerOrder<W>);
       u64 own = 0, late = 0, above, rest;
+#pragma unroll 1
       for (int it = 0; it < per; ++it) {
         float v[kVec<T>], early[kVec<T>];
         part.unpack(it, v);
@@ -1316,6 +1321,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W) cta_kernel(const Rows a, int p
     }
     const bool whole = kept.edge == -INFINITY;
     u64 own = 0, before;
+#pragma unroll 1
     for (int it = 0; it < per; ++it) {
       if (!summed) {
         float v[kVec<T>];
@@ -1358,6 +1364,11 @@ int64_t words_of(const Rows& a) {
   return (a.n + kVec<T> - 1) / kVec<T> + (aligned ? 0 : 1);
 }
 
+// Shared memory of a CTA for its words and their sums; the rest is for Shared.
+constexpr size_t kMostWords = 200 * 1024;
+static_assert(sizeof(Shared<8, true>) + kMostWords + 1024 <= 227 * 1024, "shared memory of a CTA");
+static_assert(24 * (kSampleMost / 4 + 16 * 256) / 16 <= static_cast<int64_t>(kMostWords), "the longest rows fit a cluster of 16 CTAs");
+
 template <typename T, int W, bool kCluster>
 cudaError_t run_cta(const Rows& a, int cluster, cudaStream_t stream) {
   static SmemRecord record, wide;
@@ -1390,7 +1401,7 @@ cudaError_t run(const Rows& a, cudaStream_t stream) {
   const int64_t words = words_of<T>(a);
   int cluster = 1;
   while (cluster < 16 && a.rows * cluster * 2 <= dev.sm_count && words >= static_cast<int64_t>(cluster) * kThreads * 8) cluster *= 2;
-  while (cluster < 16 && words * 24 > static_cast<int64_t>(cluster) * 200 * 1024) cluster *= 2;
+  while (cluster < 16 && words * 24 > cluster * static_cast<int64_t>(kMostWords)) cluster *= 2;
   if (cluster > 1) return run_cta<T, 8, true>(a, cluster, stream);
   // Warps a row. Many rows side by side run best on few warps each, long rows and few of them on more: 16384 rows of 1000
   // bf16 with top-p take 98 us on one warp, 137 on four, 269 on eight; of 4096 436, 269, 365; 1024 rows of 16384 139 on
