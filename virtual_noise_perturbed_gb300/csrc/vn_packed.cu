@@ -7,6 +7,13 @@
 // four reads the 16 bytes t. Word w of those holds the products 2 w and 2 w + 1, and of product p the k = 16 p + 4 t + 0 .. 3.
 // Each code + 8 is a nibble; a pair of neighbouring k lies 16 bits apart, so one mask and one exponent make two
 // bf16 values 128 + code + 8 of it, and one subtraction the codes (both exact).
+//
+// The layer on few rows (up to 32, fp32 10) is bound by latency and by the instructions that make operands of codes, 17 for the
+// 256 weights of a product, beside reading the codes once: so the rows of x are the product's columns, eight at no
+// more cost than one. fp32 rows take three columns each, for the three bf16 terms of their values; a code is exact in
+// bf16. The sum of a group is scaled in fp32. One row of 4096 to 4096 bf16 5.2 us (8.9 MB: 1.7 TB/s; plain bf16
+// weights take 6.2), 8 rows 6.4, 32 14.9; fp32 6.9, 5 rows 9.6. More rows are quicker on unpacked weights: 64 rows 18 us for
+// 53 so, fp32 16 rows 36 for 113.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -48,10 +55,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-constexpr int kSegment = 2 * kBlock;  // k of a warp's turn: 8 a lane
-// Segments of a warp, their loads in flight together: 67 M weights in bf16 (fp32) take, to pack, 66 us (78) with one, 73 (75)
-// with two, 88 (77) with four; back 48 (51), 43 (46), 42 (46).
-constexpr int kPackTurns = 1, kUnpackTurns = 2;
+constexpr int kSegment = 2 * kBlock;  // k of a warp at once: 8 a lane
+// Segments of a warp, one after the other in a row, their loads in flight together. 67 M weights in fp32 take 56 us to pack with four,
+// 64 with two, and 54 and 46 back; in bf16 44 and 29 with four (one or two, each with a place of its own to find, 66 and 43).
+constexpr int kPackRun = 4;
+template <typename T>
+constexpr int kUnpackRun = sizeof(T) == 2 ? 4 : 2;
 
 // The whole number next to w / s (halves to even), in the lowest four bits of its two's complement; inv: 1 / s to 2^-22.
 // bf16: w inv corrected by its remainder is off by less than 2^-40, and not at all where the quotient is a half, as other
@@ -92,19 +101,47 @@ __device__ __forceinline__ float largest(const float (&v)[8]) {
   return top;
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    v[2 * q] = __uint_as_float(w[q] << 16);
-    v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+// Eight weights as they are in memory.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   }
-}
+  __device__ __forceinline__ void gather(const float* p, int left) {
+    a = make_float4(left > 0 ? fetch(p) : 0.f, left > 1 ? fetch(p + 1) : 0.f, left > 2 ? fetch(p + 2) : 0.f, left > 3 ? fetch(p + 3) : 0.f);
+    b = make_float4(left > 4 ? fetch(p + 4) : 0.f, left > 5 ? fetch(p + 5) : 0.f, left > 6 ? fetch(p + 6) : 0.f, left > 7 ? fetch(p + 7) : 0.f);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 r = __ldcs(reinterpret_cast<const uint4*>(p));
+    w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
+  }
+  __device__ __forceinline__ void gather(const __nv_bfloat16* p, int left) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t low = left > 2 * q ? __bfloat16_as_ushort(fetch(p + 2 * q)) : 0u;
+      const uint32_t high = left > 2 * q + 1 ? __bfloat16_as_ushort(fetch(p + 2 * q + 1)) : 0u;
+      w[q] = low | (high << 16);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[2 * q] = __uint_as_float(w[q] << 16);
+      v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+    }
+  }
+};
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
   __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
@@ -119,22 +156,24 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-// Segments of all rows one after the other, and how a warp finds its row: the quotient by a product with `inverse` (2^64 over
-// the segments of a row, rounded up), exact below 2^32 of them; hundreds of instructions for a division beyond.
+// Runs of segments of all rows one after the other, and how a warp finds its row: the quotient by a product with `inverse` (2^64 over
+// the runs of a row, rounded up), exact below 2^32 of them; hundreds of instructions for a division beyond.
+template <int kRun>
 struct Places {
-  int64_t out, in, blocks, groups, segments;
+  int64_t out, in, blocks, groups, runs;
   unsigned long long inverse;
   int digits, vec;
   Places(int64_t rows, int64_t k, int group, bool aligned)
-      : out(rows), in(k), blocks(blocks_of(k)), groups(groups_of(k, digits_of(group))), segments((blocks + 1) / 2),
-        inverse(segments > 1 ? ~0ull / static_cast<unsigned long long>(segments) + 1 : 0), digits(digits_of(group)), vec(aligned) {}
-  int64_t items() const { return out * segments; }
-  __device__ __forceinline__ void find(int64_t at, int64_t* row, int64_t* segment) const {
-    *row = segments == 1 ? at
-           : at <= 0xFFFFFFFFll && segments <= 0xFFFFFFFFll
+      : out(rows), in(k), blocks(blocks_of(k)), groups(groups_of(k, digits_of(group))), runs((k + kRun * kSegment - 1) / (kRun * kSegment)),
+        inverse(runs > 1 ? ~0ull / static_cast<unsigned long long>(runs) + 1 : 0), digits(digits_of(group)), vec(aligned) {}
+  int64_t items() const { return out * runs; }
+  // A run's row, and its first k.
+  __device__ __forceinline__ void find(int64_t at, int64_t* row, int64_t* k) const {
+    *row = runs == 1 ? at
+           : at <= 0xFFFFFFFFll && runs <= 0xFFFFFFFFll
                ? static_cast<int64_t>(__umul64hi(static_cast<unsigned long long>(at), inverse))
-               : at / segments;
-    *segment = at - *row * segments;
+               : at / runs;
+    *k = (at - *row * runs) * (kRun * kSegment);
   }
 };
 // Of the 256 k of a segment lane l has 8 l .. 8 l + 7: half a product's, for two of the four lanes that read a
@@ -144,106 +183,103 @@ __device__ __forceinline__ int word_of(int lane) {
   return (lane >> 4) * (kBlockBytes / 4) + t * 4 + (p >> 1);
 }
 
-// A warp a segment of a row; a group's lanes find its largest magnitude by shuffles. Bound by memory, and by instructions next
-// to it.
+// A warp a run of segments of a row; a group's lanes find its largest magnitude by shuffles.
+// Bound by instructions next to memory: 67 M weights in bf16 44 us, 3.8 TB/s, in fp32 56, 5.4.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) pack_kernel(const T* w, uint8_t* codes, T* scales, const Places at) {
+__global__ void __launch_bounds__(kThreads) pack_kernel(const T* w, uint8_t* codes, T* scales, const Places<kPackRun> at) {
   let_next();
   after_previous();
-  const int lane = threadIdx.x & 31;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kPackTurns;
-  float v[kPackTurns][8];
-  int64_t row[kPackTurns], k[kPackTurns];
+  const int lane = threadIdx.x & 31, digits = at.digits;
+  int64_t row, k0;
+  at.find(static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), &row, &k0);
+  if (row >= at.out) return;
+  // What is left of the row from this lane's first weight on, as far as the run goes.
+  const int left = static_cast<int>(min(at.in - k0, static_cast<int64_t>(kPackRun * kSegment))) - lane * 8;
+  const T* const from = w + row * at.in + k0 + lane * 8;
+  Eight<T> raw[kPackRun];
 #pragma unroll
-  for (int u = 0; u < kPackTurns; ++u) {
-    int64_t segment;
-    at.find(first + u, &row[u], &segment);
-    k[u] = segment * kSegment + lane * 8;
-    const T* from = w + row[u] * at.in + k[u];
-    if (row[u] < at.out && at.vec && k[u] + 8 <= at.in) {
-      load8(from, v[u]);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[u][q] = row[u] < at.out && k[u] + q < at.in ? value(fetch(from + q)) : 0.f;
-    }
+  for (int u = 0; u < kPackRun; ++u) {
+    if (at.vec && left >= u * kSegment + 8) raw[u].load(from + u * kSegment);
+    else raw[u].gather(from + u * kSegment, left - u * kSegment);
   }
-  const int digits = at.digits;
+  T* const to_scales = scales + row * at.groups + ((k0 + lane * 8) >> digits);
+  uint32_t* const to = reinterpret_cast<uint32_t*>(codes + (row * at.blocks + k0 / kBlock) * kBlockBytes) + word_of(lane);
+  const bool first_of_group = (lane & ((1 << (digits - 3)) - 1)) == 0, odd = (lane & 2) != 0;
 #pragma unroll
-  for (int u = 0; u < kPackTurns; ++u) {
-    if (row[u] >= at.out) break;
-    float top = largest(v[u]);
+  for (int u = 0; u < kPackRun; ++u) {
+    if (left + lane * 8 <= u * kSegment) break;
+    float v[8];
+    raw[u].get(v);
+    float top = largest(v);
     for (int o = 1 << (digits - 4); o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     const T stored = narrow<T>(seventh(top));
     const float s = value(stored);
-    if ((lane & ((1 << (digits - 3)) - 1)) == 0 && k[u] < at.in) scales[row[u] * at.groups + (k[u] >> digits)] = stored;
+    if (first_of_group && left > u * kSegment) to_scales[(u * kSegment) >> digits] = stored;
     uint32_t c[8];
     if (s >= 0x1p-100f && s < INFINITY) {
       const float inv = quick_reciprocal(s);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) c[q] = code_of(T(), v[u][q], s, inv) & 15u;
+      for (int q = 0; q < 8; ++q) c[q] = code_of(T(), v[q], s, inv) & 15u;
     } else {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) c[q] = code_of_tiny(v[u][q], s) & 15u;
+      for (int q = 0; q < 8; ++q) c[q] = code_of_tiny(v[q], s) & 15u;
     }
     // The four codes for each of two reading lanes, of an even product; an odd one's lie 8 bits higher.
     const uint32_t a = c[0] + c[2] * 16u + c[1] * 65536u + c[3] * 1048576u, b = c[4] + c[6] * 16u + c[5] * 65536u + c[7] * 1048576u;
-    const bool odd = (lane & 2) != 0;
     const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 2);
     const uint32_t word = odd ? other | (b << 8) : a | (other << 8);
-    if (k[u] / kBlock < at.blocks)
-      *reinterpret_cast<uint32_t*>(codes + (row[u] * at.blocks + k[u] / kSegment * 2) * kBlockBytes + word_of(lane) * 4) = word ^ kNothing;
+    // The last segment of a row may have one block only.
+    if (lane < 16 || left + lane * 8 > u * kSegment + kBlock) to[u * (2 * kBlockBytes / 4)] = word ^ kNothing;
   }
 }
 
-// The same way back. Rows that start off a lane's 16 bytes go through shared memory, from where a warp stores neighbours.
+// The same way back: 29 us and 5.8 TB/s, in fp32 46 and 6.5. Rows that start off a lane's 16 bytes go through shared
+// memory, from where a warp stores neighbours.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* codes, const T* scales, T* w, const Places at) {
+__global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* codes, const T* scales, T* w, const Places<kUnpackRun<T>> at) {
+  constexpr int kRun = kUnpackRun<T>;
   __shared__ T staged[kWarps][kSegment];
   let_next();
   after_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kUnpackTurns;
-  uint32_t word[kUnpackTurns];
-  float s[kUnpackTurns];
-  int64_t row[kUnpackTurns], k[kUnpackTurns];
+  int64_t row, k0;
+  at.find(static_cast<int64_t>(blockIdx.x) * kWarps + warp, &row, &k0);
+  if (row >= at.out) return;
+  const int run = static_cast<int>(min(at.in - k0, static_cast<int64_t>(kRun * kSegment))), left = run - lane * 8;
+  const uint32_t* const from = reinterpret_cast<const uint32_t*>(codes + (row * at.blocks + k0 / kBlock) * kBlockBytes) + word_of(lane);
+  const T* const scale = scales + row * at.groups + ((k0 + lane * 8) >> at.digits);
+  uint32_t word[kRun];
+  T s[kRun];
 #pragma unroll
-  for (int u = 0; u < kUnpackTurns; ++u) {
-    int64_t segment;
-    at.find(first + u, &row[u], &segment);
-    k[u] = segment * kSegment + lane * 8;
+  for (int u = 0; u < kRun; ++u) {
     word[u] = kNothing;
-    s[u] = 0.f;
-    if (row[u] < at.out && k[u] / kBlock < at.blocks)
-      word[u] = __ldcs(reinterpret_cast<const uint32_t*>(codes + (row[u] * at.blocks + segment * 2) * kBlockBytes) + word_of(lane));
-    if (row[u] < at.out && k[u] < at.in) s[u] = value(fetch(scales + row[u] * at.groups + (k[u] >> at.digits)));
+    s[u] = narrow<T>(0.f);
+    if (run > u * kSegment + (lane >> 4) * kBlock) word[u] = __ldcs(from + u * (2 * kBlockBytes / 4));
+    if (left > u * kSegment) s[u] = fetch(scale + ((u * kSegment) >> at.digits));
   }
+  const bool odd = (lane & 2) != 0;
+  T* const to = w + row * at.in + k0 + lane * 8;
 #pragma unroll
-  for (int u = 0; u < kUnpackTurns; ++u) {
-    if (row[u] >= at.out) break;
-    const bool odd = (lane & 2) != 0;
+  for (int u = 0; u < kRun; ++u) {
+    if (run <= u * kSegment) break;
     const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, word[u], 2);
     const uint32_t a = odd ? other >> 8 : word[u], b = odd ? word[u] >> 8 : other;
     // A nibble as the last bits of 2^23.
     auto code = [](uint32_t v, int shift) { return __uint_as_float(((v >> shift) & 15u) | 0x4B000000u) - 8388616.f; };
     float v[8] = {code(a, 0), code(a, 16), code(a, 4), code(a, 20), code(b, 0), code(b, 16), code(b, 4), code(b, 20)};
+    const float f = value(s[u]);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = __fmul_rn(v[q], s[u]);
-    T* const to = w + row[u] * at.in + k[u];
-    if (at.vec && k[u] + 8 <= at.in) {
-      store8(to, v);
-    } else if (at.vec) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (k[u] + q < at.in) to[q] = narrow<T>(v[q]);
-    } else {
+    for (int q = 0; q < 8; ++q) v[q] = __fmul_rn(v[q], f);
+    if (at.vec && left >= u * kSegment + 8) {
+      store8(to + u * kSegment, v);
+    } else if (!at.vec) {
       __syncwarp();
 #pragma unroll
       for (int q = 0; q < 8; ++q) staged[warp][lane * 8 + q] = narrow<T>(v[q]);
       __syncwarp();
-      const int64_t k0 = k[u] - lane * 8;
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        if (k0 + q * 32 + lane < at.in) to[q * 32 + lane - lane * 8] = staged[warp][q * 32 + lane];
+        if (u * kSegment + q * 32 + lane < run) to[u * kSegment + q * 32 + lane - lane * 8] = staged[warp][q * 32 + lane];
     }
   }
 }
@@ -357,6 +393,19 @@ __global__ void __launch_bounds__(kThreads, 2) packed_kernel(const PackedArgs a,
   for (int base = 0; base < count; base += kInFlight) {
     uint4 c[kInFlight][2];
     T s[kInFlight][2];
+    typename FourOf<T>::Type x[8];
+    auto load_x = [&](int d, int n) {
+      const int64_t k = (first + base + d) * kBlock;
+      const T* const p0 = from[n] + static_cast<int64_t>(base + d) * kBlock;
+      if (vec && k + kBlock <= a.in) {
+        aligned_block(p0, x);
+      } else if (k > 0 && k + kBlock + 4 <= a.in) {
+        shifted_block(p0, x);
+      } else {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) x[p] = four_of(p0 - t * 4 - k, k + p * 16 + t * 4, a.in);
+      }
+    };
 #pragma unroll
     for (int d = 0; d < kInFlight; ++d) {
       const bool in = base + d < count;
@@ -386,19 +435,9 @@ __global__ void __launch_bounds__(kThreads, 2) packed_kernel(const PackedArgs a,
         for (int p = 0; p < 8; ++p) decoded(p, ops[p]);
       }
       const float s0 = value(s[d][0]), s1 = value(s[d][1]);
-      const int64_t k = (first + base + d) * kBlock;
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) {
-        typename FourOf<T>::Type x[8];
-        const T* const p0 = from[n] + static_cast<int64_t>(base + d) * kBlock;
-        if (vec && k + kBlock <= a.in) {
-          aligned_block(p0, x);
-        } else if (k > 0 && k + kBlock + 4 <= a.in) {
-          shifted_block(p0, x);
-        } else {
-#pragma unroll
-          for (int p = 0; p < 8; ++p) x[p] = four_of(p0 - t * 4 - k, k + p * 16 + t * 4, a.in);
-        }
+        load_x(d, n);
         float part[4];
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
@@ -474,22 +513,22 @@ cudaError_t run_packed(const PackedArgs& a, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t pack_typed(const void* w, int64_t out, int64_t in, int group, uint8_t* codes, void* scales, cudaStream_t stream) {
-  const Places at(out, in, group, in % 8 == 0 && fits(w, 16));
-  const int64_t grid = (at.items() + kWarps * kPackTurns - 1) / (kWarps * kPackTurns);
+  const Places<kPackRun> at(out, in, group, in % 8 == 0 && fits(w, 16));
+  const int64_t grid = (at.items() + kWarps - 1) / kWarps;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   return launch_overlapped(pack_kernel<T>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream, static_cast<const T*>(w), codes,
                            static_cast<T*>(scales), at);
 }
 template <typename T>
 cudaError_t unpack_typed(const uint8_t* codes, const void* scales, int64_t out, int64_t in, int group, void* w, cudaStream_t stream) {
-  const Places at(out, in, group, in % 8 == 0 && fits(w, 16));
-  const int64_t grid = (at.items() + kWarps * kUnpackTurns - 1) / (kWarps * kUnpackTurns);
+  const Places<kUnpackRun<T>> at(out, in, group, in % 8 == 0 && fits(w, 16));
+  const int64_t grid = (at.items() + kWarps - 1) / kWarps;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   return launch_overlapped(unpack_kernel<T>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream, codes,
                            static_cast<const T*>(scales), static_cast<T*>(w), at);
 }
 
-// The most rows that the kernel on packed weights takes.
+// The most rows that the kernel on packed weights takes (both sides at the top of this file).
 int64_t few_rows(vn_dtype dt) { return dt == VN_BF16 ? 32 : 10; }
 
 int64_t padded(int64_t bytes) { return (bytes + 255) / 256 * 256; }

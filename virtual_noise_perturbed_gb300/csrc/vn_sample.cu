@@ -8,12 +8,20 @@
 // Which index it is hangs on sums next to a border, so a weight is a whole number: w in units of 2^-42, good
 // to 2^-35 of itself. Sums of whole numbers are exact in any order, whatever adds them: lanes, CTAs of
 // a cluster, atomics. (With sums of fp32 one row in a hundred of 4,096 would differ from float64's index.)
+// Such a weight takes some 45 instructions, so rows beyond 128 logits are decided by coarse weights of 10,
+// whose sums' error is bounded, and by whole ones only where a border lies within that bound: one row in
+// fifty at 4,096 logits, half of them at 131,072.
 //
-// A row is read once, into registers or shared memory, and every later pass goes over that copy. Up to 256
-// logits a warp has a row. Beyond, a CTA or a cluster of CTAs has one: each warp holds a contiguous
-// stretch of it and each lane every 32nd 16 bytes of that, the ones that it read itself. The value that ends a
-// prefix is found by bisection in the warp and by a histogram of 256 bins elsewhere: first over x in units
-// of T, then over what is left in the bin that the border falls into.
+// A row is read once, into registers or shared memory, and every later pass goes over that copy. Up to 128
+// logits (256 where rows are few) a warp has a row in registers, and finds where a prefix ends by bisecting the bits of a logit.
+// Beyond, a CTA or a cluster of CTAs has one: each warp holds a contiguous stretch of it and each lane every 32nd 16 bytes of that,
+// the ones that it read itself. A histogram over x in units of T tells the bin in which a prefix ends; the logits of that
+// bin, some tens, are listed, and each finds its place and what lies before it by a look at all others. With a
+// small top_k everything kept is listed, and the rest of the work is done on the list.
+//
+// Bound by memory in principle (a row once); in fact by instructions, 40 to 80 a logit with what a row costs apart from them, at
+// half of the issue rate: 24 warps an SM that wait for one another's results. 16384 rows of 4096 bf16: 133 us without filters, 171 with
+// top_k 50, 257 with top_p 0.9 (20 for reading them); 32 of 131071 fp32: 26 with top_k; 1024 rows of 8: 2.5; one of 4096: 4.8 to 9.2.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -473,7 +481,7 @@ template <typename T>
 constexpr int kVec = 16 / static_cast<int>(sizeof(T));  // logits of 16 bytes
 
 // Bins of a fraction of a binary order of the weights, over 32 of them, the last bin with all that is below: finer ones for the
-// longer rows, so that few logits share the bin of a border (131071 fp32 with top-p on 512 bins: 9 us a row, on 2048 XX). Padded
+// longer rows, so that few logits share the bin of a border (32 rows of 131071 fp32 with top-p: 337 us on 512 bins, 165 on 2048). Padded
 // in shared memory, so that lanes with an order each read from different banks.
 template <int W>
 constexpr int kPerOrder = W < 8 ? 16 : 64;
@@ -890,30 +898,68 @@ __device__ __forceinline__ void fill_bins(Team<W, kCluster>& team, const Part<T>
   }
 }
 
+template <typename V>
+__device__ __forceinline__ V scan_of(V v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const V t = __shfl_up_sync(kAll, v, o);
+    if (lane >= o) v += t;
+  }
+  return v;
+}
+// Where the sum over bins reaches `target`, by a warp: first the binary order, whose sums the lanes hold (up to it: scan), then its
+// bins, one or a few a lane. The bin, what lies before it, and it itself; -1 if it is not reached.
+template <int W, typename V, typename F>
+__device__ __forceinline__ int reached(V scan, V total, V target, F bin_sum, V* before, V* itself) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t orders = __ballot_sync(kAll, scan >= target);
+  if (orders == 0) return -1;
+  const int order = __ffs(orders) - 1;
+  const V ahead = __shfl_sync(kAll, scan - total, order);
+  constexpr int kEach = kPerOrder<W> > 32 ? kPerOrder<W> / 32 : 1;
+  V own[kEach], sum = 0;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    own[e] = lane * kEach + e < kPerOrder<W> ? bin_sum(order, lane * kEach + e) : V(0);
+    sum += own[e];
+  }
+  V at = ahead + (scan_of(sum, lane) - sum);
+  int mine = kPerOrder<W>;
+  V mine_before = 0, mine_itself = 0;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    if (mine == kPerOrder<W> && at + own[e] >= target) {
+      mine = lane * kEach + e;
+      mine_before = at;
+      mine_itself = own[e];
+    }
+    at += own[e];
+  }
+  // By rounding it may seem to be reached in the order and in none of its bins: the last one then.
+  const uint32_t bins = __ballot_sync(kAll, mine < kPerOrder<W>);
+  const int holder = bins != 0 ? __ffs(bins) - 1 : 31;
+  *before = __shfl_sync(kAll, mine_before, holder);
+  *itself = __shfl_sync(kAll, mine_itself, holder);
+  mine = __shfl_sync(kAll, mine, holder);
+  return order * kPerOrder<W> + min(mine, kPerOrder<W> - 1);
+}
+
 // By count: the bin that the logit number `target` (from 1) of the order is in. A lane has the bins of one binary order.
 template <int W, bool kCluster>
 __device__ __forceinline__ void find_count(Team<W, kCluster>& team, uint32_t target) {
   Shared<W, kCluster>& s = team.s;
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    const uint32_t* const own = bins_of(s) + lane * (kPerOrder<W> + 1);
-    uint32_t total = 0;
-#pragma unroll 8
-    for (int b = 0; b < kPerOrder<W>; ++b) total += own[b];
-    uint32_t scan = total;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t t = __shfl_up_sync(kAll, scan, o);
-      if (lane >= o) scan += t;
-    }
-    const uint32_t reach = __ballot_sync(kAll, scan >= target);
-    if (reach != 0 && lane == __ffs(reach) - 1) {
-      uint32_t at = scan - total;
-      int b = 0;
-      while (b < kPerOrder<W> - 1 && at + own[b] < target) at += own[b++];
-      s.bin = s.last_bin = lane * kPerOrder<W> + b;
-      s.above_count = at;
-      s.bin_count = own[b];
+    const uint32_t* const bins = bins_of(s);
+    uint32_t total = 0, before = 0, itself = 0;
+#pragma unroll 16
+    for (int b = 0; b < kPerOrder<W>; ++b) total += bins[lane * (kPerOrder<W> + 1) + b];
+    const int bin = reached<W>(
+        scan_of(total, lane), total, target, [&](int order, int b) { return bins[order * (kPerOrder<W> + 1) + b]; }, &before, &itself);
+    if (lane == 0) {
+      s.bin = s.last_bin = bin;
+      s.above_count = before;
+      s.bin_count = itself;
     }
   }
   team.sync();
@@ -925,36 +971,22 @@ __device__ __forceinline__ void find_sum(Team<W, kCluster>& team, u64 top_p) {
   Shared<W, kCluster>& s = team.s;
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    const uint32_t* const own = bins_of(s) + lane * (kPerOrder<W> + 1);
-    const float unit = quick_exp2(static_cast<float>(-lane));
-    auto sum_of = [&](int b) { return static_cast<float>(own[b]) * (quick_exp2(static_cast<float>(b) * (-1.f / kPerOrder<W>)) * unit); };
-    float total = 0.f;
-#pragma unroll 8
-    for (int b = 0; b < kPerOrder<W>; ++b) total += sum_of(b);
-    float scan = total;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const float t = __shfl_up_sync(kAll, scan, o);
-      if (lane >= o) scan += t;
-    }
+    const uint32_t* const bins = bins_of(s);
+    auto bin_sum = [&](int order, int b) {
+      return static_cast<float>(bins[order * (kPerOrder<W> + 1) + b]) *
+             (quick_exp2(static_cast<float>(b) * (-1.f / kPerOrder<W>)) * quick_exp2(static_cast<float>(-order)));
+    };
+    float total = 0.f, before, itself;
+#pragma unroll 16
+    for (int b = 0; b < kPerOrder<W>; ++b) total += bin_sum(lane, b);
+    const float scan = scan_of(total, lane);
     const float all = __shfl_sync(kAll, scan, 31), border = all * (static_cast<float>(static_cast<uint32_t>(top_p >> 32)) * 0x1p-32f);
     const float off = (all - border) * 0x1p-11f + all * 0x1p-19f;
-    const float early = border - off, late = border + off;
-    int first = kFine<W>, last = kFine<W>;
-    float at = scan - total;
-    if (scan >= early) {
-#pragma unroll 4
-      for (int b = 0; b < kPerOrder<W>; ++b) {
-        at += sum_of(b);
-        if (at >= early) first = min(first, lane * kPerOrder<W> + b);
-        if (at >= late) last = min(last, lane * kPerOrder<W> + b);
-      }
-    }
-    first = static_cast<int>(__reduce_min_sync(kAll, static_cast<unsigned>(first)));
-    last = static_cast<int>(__reduce_min_sync(kAll, static_cast<unsigned>(last)));
+    const int first = reached<W>(scan, total, border - off, bin_sum, &before, &itself);
+    const int last = reached<W>(scan, total, border + off, bin_sum, &before, &itself);
     if (lane == 0) {
-      s.bin = min(first, kFine<W> - 1);
-      s.last_bin = min(last, kFine<W> - 1);
+      s.bin = first < 0 ? kFine<W> - 1 : first;
+      s.last_bin = last < 0 ? kFine<W> - 1 : last;
     }
   }
   team.sync();
@@ -1405,9 +1437,9 @@ cudaError_t run(const Rows& a, cudaStream_t stream) {
   if (cluster > 1) return run_cta<T, 8, true>(a, cluster, stream);
   // Warps a row. Many rows side by side run best on few warps each, long rows and few of them on more: 16384 rows of 1000
   // bf16 with top-p take 98 us on one warp, 137 on four, 269 on eight; of 4096 436, 269, 365; 1024 rows of 16384 139 on
-  // four, 105 on eight; 1024 rows of 1000 24, 17, 24.
+  // four, 105 on eight; 1024 rows of 1000 24, 17, 24; 200 rows of 4096 20 on four, 16 on eight; one row of 1000 6.5 and 8.2.
   if (words <= 256 && many) return run_cta<T, 1, false>(a, 1, stream);
-  if (words <= 1024 && a.rows >= 2 * static_cast<int64_t>(dev.sm_count)) return run_cta<T, 4, false>(a, 1, stream);
+  if (words <= (a.rows >= 2 * static_cast<int64_t>(dev.sm_count) ? 1024 : 256)) return run_cta<T, 4, false>(a, 1, stream);
   return run_cta<T, 8, false>(a, 1, stream);
 }
 

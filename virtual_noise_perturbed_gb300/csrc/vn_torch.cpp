@@ -336,12 +336,15 @@ struct Gradient {
     tensors.reserve(static_cast<size_t>(n));
     for (Py_ssize_t i = 0; i < n; ++i) {
       PyObject* item = one ? o : PyList_GET_ITEM(o, i);
-      const std::string which = one ? std::string(name) : std::string(name) + "[" + std::to_string(i) + "]";
-      if (written && (!THPVariable_Check(item) || !THPVariable_Unpack(item).is_cuda() || !THPVariable_Unpack(item).is_contiguous()))
-        raise(PyExc_ValueError, which + " must be a contiguous CUDA tensor (written over)");
-      tensors.push_back(input(item, which.c_str()));
-      const at::Tensor& t = tensors.back();
-      dt = dtype_of(t, which.c_str());
+      // Its name is only spelled out for an error: strings for a dozen tensors cost a call half a microsecond.
+      auto which = [&] { return one ? std::string(name) : std::string(name) + "[" + std::to_string(i) + "]"; };
+      const bool cuda = THPVariable_Check(item) && THPVariable_Unpack(item).is_cuda();
+      if (written && !(cuda && THPVariable_Unpack(item).is_contiguous()))
+        raise(PyExc_ValueError, which() + " must be a contiguous CUDA tensor (written over)");
+      if (!cuda) raise(PyExc_ValueError, which() + " must be a CUDA tensor (the library has no CPU path)");
+      const at::Tensor& t = THPVariable_Unpack(item);
+      tensors.push_back(t.is_contiguous() ? t : t.contiguous());
+      if (i == 0) dt = dtype_of(t, which().c_str());
       if (t.scalar_type() != tensors[0].scalar_type()) raise(PyExc_TypeError, std::string(name) + " must have one dtype");
       beside(t, tensors[0]);
     }
@@ -362,7 +365,9 @@ PyObject* clip_gradients(PyObject* const* a, Py_ssize_t count) {
     if (to->tensors.size() != g.tensors.size())
       raise(PyExc_ValueError, std::to_string(g.tensors.size()) + " gradients but " + std::to_string(to->tensors.size()) + " in out");
     for (size_t i = 0; i < g.tensors.size(); ++i)
-      like(to->tensors[i], ("out[" + std::to_string(i) + "]").c_str(), g.tensors[i].sizes(), g.tensors[i]);
+      if (to->tensors[i].sizes() != g.tensors[i].sizes() || to->tensors[i].scalar_type() != g.tensors[i].scalar_type())
+        like(to->tensors[i], ("out[" + std::to_string(i) + "]").c_str(), g.tensors[i].sizes(), g.tensors[i]);
+    beside(to->tensors[0], g.tensors[0]);
   }
   const at::Tensor& first = g.tensors[0];
   const int64_t n = static_cast<int64_t>(g.tensors.size());
