@@ -447,7 +447,7 @@ __device__ __forceinline__ float coarse(float x, float m, float c, float cl) {
   float below;
   return coarse(x, m, c, cl, &below);
 }
-// In units, rounded down, of a sum below 2^20 (the conversion instruction runs at 1/64 of this rate).
+// In units, rounded down, of a sum below 2^20, by its bits.
 __device__ __forceinline__ u64 units(float v) {
   const uint32_t b = __float_as_uint(v);
   const int up = static_cast<int>(b >> 23) - 150 + kUnit;
@@ -1167,9 +1167,9 @@ __device__ __noinline__ void exact_draw(Shared<W, kCluster>& s, const Part<T> pa
   team.sync();
 }
 
-// per: 16-byte words of a warp's lane; the CTA's logits take W * 32 * per of them.
-template <typename T, int W, bool kCluster>
-__global__ void __launch_bounds__(W * 32, 24 / W) cta_kernel(const Rows a, int per) {
+// per: 16-byte words of a warp's lane; the CTA's logits take W * 32 * per of them. kCuts: top_k or top_p may be asked for.
+template <typename T, int W, bool kCluster, bool kCuts>
+__global__ void __launch_bounds__(W * 32, (kCuts ? 24 : 32) / W) cta_kernel(const Rows a, int per) {
   extern __shared__ uint4 logits[];
   __shared__ Shared<W, kCluster> s;
   let_next();
@@ -1251,92 +1251,94 @@ __global__ void __launch_bounds__(W * 32, 24 / W) cta_kernel(const Rows a, int p
       }
       continue;
     }
-    const Fine<W> fine(m, w);
     const float c = w.ch * 0.03125f, cl = w.cl * 0.03125f;
-    if (w.top_k < n) {
-      fill_bins<false>(team, part, fine, 0);
-      find_count(team, static_cast<uint32_t>(w.top_k));
-      const int bin = s.bin;
-      const uint32_t above = s.above_count, inside = s.bin_count;
-      if (above + inside <= kFew<W>) {
-        collect(team, part, fine, 0, bin);
-        if (team.rank == 0) few(s, a, row, m, w, static_cast<int>(above + inside));
-        continue;
-      }
-      Prefix first;
-      if (inside <= kCap<W>) {
-        collect(team, part, fine, bin, bin);
-        const u64 edge = edge_by_count(team, static_cast<int>(inside), static_cast<uint32_t>(w.top_k) - above - 1);
-        first = {value_of_key(item_key(edge)), item_index(edge)};
-      } else {
-        first = cut<T, W, kCluster>(s, part, m, w, false, static_cast<u64>(w.top_k));
-      }
-      // The others are out for good.
-#pragma unroll 1
-      for (int it = 0; it < per; ++it) {
-        float v[kVec<T>];
-        part.unpack(it, v);
-        T* to = reinterpret_cast<T*>(mine + it * 32);
-#pragma unroll
-        for (int q = 0; q < kVec<T>; ++q)
-          if (!first.holds(v[q], part.index(it) + q)) to[q] = lowest<T>();
-      }
-    }
     Prefix kept;
     bool summed = false;  // the words' sums are those of what is kept
-    if (w.top_p != kAllOfIt) {
-      fill_bins<true>(team, part, fine, bits);
-      find_sum(team, w.top_p);
-      const int first = s.bin, last = s.last_bin;
-      // The same borders in units of coarse()'s distance.
-      const float from = static_cast<float>(first) * (1.f / kPerOrder<W>);
-      const float to = last == kFine<W> - 1 ? INFINITY : static_cast<float>(last + 1) * (1.f / kPerOrder<W>);
-      u64 own = 0, late = 0, above, rest;
+    if constexpr (kCuts) {
+      const Fine<W> fine(m, w);
+      if (w.top_k < n) {
+        fill_bins<false>(team, part, fine, 0);
+        find_count(team, static_cast<uint32_t>(w.top_k));
+        const int bin = s.bin;
+        const uint32_t above = s.above_count, inside = s.bin_count;
+        if (above + inside <= kFew<W>) {
+          collect(team, part, fine, 0, bin);
+          if (team.rank == 0) few(s, a, row, m, w, static_cast<int>(above + inside));
+          continue;
+        }
+        Prefix first;
+        if (inside <= kCap<W>) {
+          collect(team, part, fine, bin, bin);
+          const u64 edge = edge_by_count(team, static_cast<int>(inside), static_cast<uint32_t>(w.top_k) - above - 1);
+          first = {value_of_key(item_key(edge)), item_index(edge)};
+        } else {
+          first = cut<T, W, kCluster>(s, part, m, w, false, static_cast<u64>(w.top_k));
+        }
+        // The others are out for good.
 #pragma unroll 1
-      for (int it = 0; it < per; ++it) {
-        float v[kVec<T>], early[kVec<T>];
-        part.unpack(it, v);
-        uint32_t tops = 0;
+        for (int it = 0; it < per; ++it) {
+          float v[kVec<T>];
+          part.unpack(it, v);
+          T* to = reinterpret_cast<T*>(mine + it * 32);
 #pragma unroll
-        for (int q = 0; q < kVec<T>; ++q) {
-          float below;
-          const float t = coarse(v[q], m, c, cl, &below);
-          if (below >= from && below < to) enlist(team, v[q], part.index(it) + q);
-          tops += v[q] == m;
-          early[q] = below < from ? t : 0.f;
-          v[q] = below < from ? 0.f : t;
+          for (int q = 0; q < kVec<T>; ++q)
+            if (!first.holds(v[q], part.index(it) + q)) to[q] = lowest<T>();
         }
-        const u64 ones = static_cast<u64>(tops) << kUnit;
-        const u64 sum = units(sum_in_pairs(early)) + (first > 0 ? ones : 0);
-        sums[it * 32] = sum;
-        own += sum;
-        late += units(sum_in_pairs(v)) + (first > 0 ? 0 : ones);
       }
-      team.sums(own, late, &above, &rest);
-      const u64 target = nucleus(w.top_p, above + rest);
-      const int count = static_cast<int>(team.of_rank(&s.list_count, 0));
-      u64 edge = 0;
-      // How far a logit's `before` is from the target: (1 - p) above + those of the list - p rest. So what counts is the error of
-      // what lies beyond the border and next to it, and not that of all.
-      if (count <= kCap<W>)
-        edge = edge_by_sum(team, count, above, target, static_cast<u64>(static_cast<float>(above + rest - target + rest) * kSure) + 1,
-                           [&](float v) { return v == m ? kOne : units(coarse(v, m, c, cl)); });
-      if (edge != 0) {
-        kept = {value_of_key(item_key(edge)), item_index(edge)};
-        summed = true;
-        // The list's part of what is kept, to its words' sums.
-        if (team.rank == 0) {
-          for (int i = threadIdx.x; i < count; i += W * 32) {
-            if (s.list[i] < edge) continue;
-            const int word = (item_index(s.list[i]) + shift) / kVec<T>, lanes = W * 32 * per;
-            u64* at = word_sums + word % lanes;
-            if constexpr (kCluster) at = cg::this_cluster().map_shared_rank(word_sums, word / lanes) + word % lanes;
-            atomicAdd(at, s.list_weights[i]);
+      if (w.top_p != kAllOfIt) {
+        fill_bins<true>(team, part, fine, bits);
+        find_sum(team, w.top_p);
+        const int first = s.bin, last = s.last_bin;
+        // The same borders in units of coarse()'s distance.
+        const float from = static_cast<float>(first) * (1.f / kPerOrder<W>);
+        const float to = last == kFine<W> - 1 ? INFINITY : static_cast<float>(last + 1) * (1.f / kPerOrder<W>);
+        u64 own = 0, late = 0, above, rest;
+#pragma unroll 1
+        for (int it = 0; it < per; ++it) {
+          float v[kVec<T>], early[kVec<T>];
+          part.unpack(it, v);
+          uint32_t tops = 0;
+#pragma unroll
+          for (int q = 0; q < kVec<T>; ++q) {
+            float below;
+            const float t = coarse(v[q], m, c, cl, &below);
+            if (below >= from && below < to) enlist(team, v[q], part.index(it) + q);
+            tops += v[q] == m;
+            early[q] = below < from ? t : 0.f;
+            v[q] = below < from ? 0.f : t;
           }
+          const u64 ones = static_cast<u64>(tops) << kUnit;
+          const u64 sum = units(sum_in_pairs(early)) + (first > 0 ? ones : 0);
+          sums[it * 32] = sum;
+          own += sum;
+          late += units(sum_in_pairs(v)) + (first > 0 ? 0 : ones);
         }
-        team.sync();
-      } else {
-        kept = exact_nucleus<T, W, kCluster>(s, part, m, w, first, count);
+        team.sums(own, late, &above, &rest);
+        const u64 target = nucleus(w.top_p, above + rest);
+        const int count = static_cast<int>(team.of_rank(&s.list_count, 0));
+        u64 edge = 0;
+        // How far a logit's `before` is from the target: (1 - p) above + those of the list - p rest. So what counts is the error of
+        // what lies beyond the border and next to it, and not that of all.
+        if (count <= kCap<W>)
+          edge = edge_by_sum(team, count, above, target, static_cast<u64>(static_cast<float>(above + rest - target + rest) * kSure) + 1,
+                             [&](float v) { return v == m ? kOne : units(coarse(v, m, c, cl)); });
+        if (edge != 0) {
+          kept = {value_of_key(item_key(edge)), item_index(edge)};
+          summed = true;
+          // The list's part of what is kept, to its words' sums.
+          if (team.rank == 0) {
+            for (int i = threadIdx.x; i < count; i += W * 32) {
+              if (s.list[i] < edge) continue;
+              const int word = (item_index(s.list[i]) + shift) / kVec<T>, lanes = W * 32 * per;
+              u64* at = word_sums + word % lanes;
+              if constexpr (kCluster) at = cg::this_cluster().map_shared_rank(word_sums, word / lanes) + word % lanes;
+              atomicAdd(at, s.list_weights[i]);
+            }
+          }
+          team.sync();
+        } else {
+          kept = exact_nucleus<T, W, kCluster>(s, part, m, w, first, count);
+        }
       }
     }
     if (w.min_p > 0.f) {
@@ -1401,20 +1403,28 @@ constexpr size_t kMostWords = 200 * 1024;
 static_assert(sizeof(Shared<8, true>) + kMostWords + 1024 <= 227 * 1024, "shared memory of a CTA");
 static_assert(24 * (kSampleMost / 4 + 16 * 256) / 16 <= static_cast<int64_t>(kMostWords), "the longest rows fit a cluster of 16 CTAs");
 
-template <typename T, int W, bool kCluster>
-cudaError_t run_cta(const Rows& a, int cluster, cudaStream_t stream) {
+template <typename T, int W, bool kCluster, bool kCuts>
+cudaError_t run_cuts(const Rows& a, int cluster, cudaStream_t stream) {
   static SmemRecord record, wide;
   const int64_t words = words_of<T>(a);
   const int64_t lanes = static_cast<int64_t>(cluster) * W * 32;
   const int per = static_cast<int>((words + lanes - 1) / lanes);
   const size_t smem = static_cast<size_t>(per) * W * 32 * (16 + 8);
-  const void* fn = reinterpret_cast<const void*>(cta_kernel<T, W, kCluster>);
+  const void* fn = reinterpret_cast<const void*>(cta_kernel<T, W, kCluster, kCuts>);
   cudaError_t err = ensure_dynamic_smem(fn, smem, record);
   if (err == cudaSuccess && cluster > 8) err = allow_wide_clusters(fn, wide);
   if (err != cudaSuccess) return err;
   const int64_t rows = std::min<int64_t>(a.rows, (int64_t{1} << 30) / cluster);
-  return launch_overlapped(cta_kernel<T, W, kCluster>, dim3(static_cast<unsigned>(rows * cluster)), W * 32, kCluster ? cluster : 0, smem,
+  return launch_overlapped(cta_kernel<T, W, kCluster, kCuts>, dim3(static_cast<unsigned>(rows * cluster)), W * 32, kCluster ? cluster : 0, smem,
                            stream, a, per);
+}
+
+// Without top_k and top_p a kernel of its own, whose 64 registers leave room for more rows at once: 16384 rows of 4096 bf16 105 us
+// for 133, with min_p 134 for 197.
+template <typename T, int W, bool kCluster>
+cudaError_t run_cta(const Rows& a, int cluster, cudaStream_t stream) {
+  const bool cuts = a.top_ks != nullptr || a.top_ps != nullptr || (a.top_k > 0 && a.top_k < a.n) || a.top_p != kAllOfIt;
+  return cuts ? run_cuts<T, W, kCluster, true>(a, cluster, stream) : run_cuts<T, W, kCluster, false>(a, cluster, stream);
 }
 
 template <typename T>
