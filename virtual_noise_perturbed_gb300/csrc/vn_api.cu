@@ -994,7 +994,8 @@ vn_status vn_sample(const void* logits, vn_dtype dt, int64_t rows, int64_t n, co
   a.temperature = temperature; a.top_p = top_p; a.min_p = min_p; a.top_k = top_k;
   a.temperatures = temperatures; a.top_ks = top_ks; a.top_ps = top_ps; a.min_ps = min_ps;
   a.index = index; a.logprob = logprob;
-  return launched(vn::launch_sample(a, static_cast<cudaStream_t>(stream)));
+  return launched(dt == VN_BF16 ? vn::launch_sample_bf16(a, static_cast<cudaStream_t>(stream))
+                                : vn::launch_sample_f32(a, static_cast<cudaStream_t>(stream)));
 }
 
 vn_status vn_device_status(void* stream) {

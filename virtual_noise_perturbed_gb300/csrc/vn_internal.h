@@ -254,7 +254,8 @@ struct SampleArgs {
   int64_t* index;
   float* logprob;  // may be null
 };
-cudaError_t launch_sample(const SampleArgs& a, cudaStream_t stream);
+cudaError_t launch_sample_f32(const SampleArgs& a, cudaStream_t stream);
+cudaError_t launch_sample_bf16(const SampleArgs& a, cudaStream_t stream);
 
 // The current device's status word, which every bounded wait that runs out sets.
 cudaError_t device_status_word(unsigned int** word);

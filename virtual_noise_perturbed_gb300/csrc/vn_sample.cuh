@@ -1,4 +1,4 @@
-// vn_sample.cu -- an index for each row of logits, drawn with a given random number:
+// vn_sample.cuh -- an index for each row of logits, drawn with a given random number:
 //
 //   w_i = exp((x_i - max x) / T);   order: x descending, index ascending
 //   kept = the first top_k of the order, of those the ones before which less than top_p of the sum lies,
@@ -20,8 +20,11 @@
 // small top_k everything kept is listed, and the rest of the work is done on the list.
 //
 // Bound by memory in principle (a row once); in fact by instructions, 40 to 80 a logit with what a row costs apart from them, at
-// half of the issue rate: 24 warps an SM that wait for one another's results. 16384 rows of 4096 bf16: 133 us without filters, 171 with
-// top_k 50, 257 with top_p 0.9 (20 for reading them); 32 of 131071 fp32: 26 with top_k; 1024 rows of 8: 2.5; one of 4096: 4.8 to 9.2.
+// half of the issue rate: 24 to 32 warps an SM that wait for one another's results. 16384 rows of 4096 bf16: 105 us without filters, 166 with
+// top_k 50, 244 with top_p 0.9 (20 for reading them); 32 of 131071 fp32: 23 with top_k; 1024 rows of 8: 2.5; one of 4096: 3.9 to 8.2.
+// (Compiled once for each type of the logits, vn_sample_f32.cu and vn_sample_bf16.cu, to build in half the time.)
+#pragma once
+
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -1167,9 +1170,9 @@ __device__ __noinline__ void exact_draw(Shared<W, kCluster>& s, const Part<T> pa
   team.sync();
 }
 
-// per: 16-byte words of a warp's lane; the CTA's logits take W * 32 * per of them. kCuts: top_k or top_p may be asked for.
-template <typename T, int W, bool kCluster, bool kCuts>
-__global__ void __launch_bounds__(W * 32, (kCuts ? 24 : 32) / W) cta_kernel(const Rows a, int per) {
+// per: 16-byte words of a warp's lane; the CTA's logits take W * 32 * per of them. kCuts: 1 if top_k may be asked for, 2 if top_p.
+template <typename T, int W, bool kCluster, int kCuts>
+__global__ void __launch_bounds__(W * 32, (kCuts != 0 ? 24 : 32) / W) cta_kernel(const Rows a, int per) {
   extern __shared__ uint4 logits[];
   __shared__ Shared<W, kCluster> s;
   let_next();
@@ -1254,8 +1257,8 @@ __global__ void __launch_bounds__(W * 32, (kCuts ? 24 : 32) / W) cta_kernel(cons
     const float c = w.ch * 0.03125f, cl = w.cl * 0.03125f;
     Prefix kept;
     bool summed = false;  // the words' sums are those of what is kept
-    if constexpr (kCuts) {
-      const Fine<W> fine(m, w);
+    [[maybe_unused]] const Fine<W> fine(m, w);
+    if constexpr ((kCuts & 1) != 0) {
       if (w.top_k < n) {
         fill_bins<false>(team, part, fine, 0);
         find_count(team, static_cast<uint32_t>(w.top_k));
@@ -1285,6 +1288,8 @@ __global__ void __launch_bounds__(W * 32, (kCuts ? 24 : 32) / W) cta_kernel(cons
             if (!first.holds(v[q], part.index(it) + q)) to[q] = lowest<T>();
         }
       }
+    }
+    if constexpr ((kCuts & 2) != 0) {
       if (w.top_p != kAllOfIt) {
         fill_bins<true>(team, part, fine, bits);
         find_sum(team, w.top_p);
@@ -1403,7 +1408,7 @@ constexpr size_t kMostWords = 200 * 1024;
 static_assert(sizeof(Shared<8, true>) + kMostWords + 1024 <= 227 * 1024, "shared memory of a CTA");
 static_assert(24 * (kSampleMost / 4 + 16 * 256) / 16 <= static_cast<int64_t>(kMostWords), "the longest rows fit a cluster of 16 CTAs");
 
-template <typename T, int W, bool kCluster, bool kCuts>
+template <typename T, int W, bool kCluster, int kCuts>
 cudaError_t run_cuts(const Rows& a, int cluster, cudaStream_t stream) {
   static SmemRecord record, wide;
   const int64_t words = words_of<T>(a);
@@ -1419,12 +1424,17 @@ cudaError_t run_cuts(const Rows& a, int cluster, cudaStream_t stream) {
                            stream, a, per);
 }
 
-// Without top_k and top_p a kernel of its own, whose 64 registers leave room for more rows at once: 16384 rows of 4096 bf16 105 us
-// for 133, with min_p 134 for 197.
+// A kernel for each set of cuts that may be asked for: code and registers that a call does not need cost it rows at once. 16384 rows of
+// 4096 bf16 without any take 105 us for 133, with min_p 134 for 197; with top_k 166 for 170, top_p 244 for 258.
 template <typename T, int W, bool kCluster>
 cudaError_t run_cta(const Rows& a, int cluster, cudaStream_t stream) {
-  const bool cuts = a.top_ks != nullptr || a.top_ps != nullptr || (a.top_k > 0 && a.top_k < a.n) || a.top_p != kAllOfIt;
-  return cuts ? run_cuts<T, W, kCluster, true>(a, cluster, stream) : run_cuts<T, W, kCluster, false>(a, cluster, stream);
+  const int cuts = (a.top_ks != nullptr || (a.top_k > 0 && a.top_k < a.n) ? 1 : 0) + (a.top_ps != nullptr || a.top_p != kAllOfIt ? 2 : 0);
+  switch (cuts) {
+    case 0: return run_cuts<T, W, kCluster, 0>(a, cluster, stream);
+    case 1: return run_cuts<T, W, kCluster, 1>(a, cluster, stream);
+    case 2: return run_cuts<T, W, kCluster, 2>(a, cluster, stream);
+    default: return run_cuts<T, W, kCluster, 3>(a, cluster, stream);
+  }
 }
 
 template <typename T>
@@ -1453,9 +1463,8 @@ cudaError_t run(const Rows& a, cudaStream_t stream) {
   return run_cta<T, 8, false>(a, 1, stream);
 }
 
-}  // namespace
-
-cudaError_t launch_sample(const SampleArgs& g, cudaStream_t stream) {
+template <typename T>
+cudaError_t sample_rows(const SampleArgs& g, cudaStream_t stream) {
   Rows a;
   a.x = g.logits; a.rows = g.rows; a.n = g.n; a.u = g.u;
   a.temperature = g.temperature; a.min_p = g.min_p; a.top_k = g.top_k;
@@ -1466,7 +1475,8 @@ cudaError_t launch_sample(const SampleArgs& g, cudaStream_t stream) {
   const double c = g.temperature > 0.0 ? 46.16624130844683 / g.temperature : 46.16624130844683;
   a.ch = static_cast<float>(c);
   a.cl = static_cast<float>(c - static_cast<double>(a.ch));
-  return g.dt == VN_BF16 ? run<__nv_bfloat16>(a, stream) : run<float>(a, stream);
+  return run<T>(a, stream);
 }
 
+}  // namespace
 }  // namespace vn
