@@ -104,6 +104,54 @@ def test_many_rows(rows, n, kind):
     check(x, u, dict(temperature=1.2, top_k=n // 3 + 1, min_p=0.01))
 
 
+def check_repeated(x, u, filters, times):
+    """As many rows as run with one or two warps each: `times` copies of x, of which one is compared and the others have to be like
+    it. Copies start at other places within 16 bytes, so their fp32 sums are of other groups: each log-probability is within
+    check()'s bound of the oracle's, and two of them within twice that."""
+    rows = u.numel()
+    there = {k: v.repeat(times).to(DEV) if isinstance(v, torch.Tensor) else v for k, v in filters.items()}
+    index, logp = vn.sample(x.repeat(times, 1).to(DEV), u.repeat(times).to(DEV), logprobs=True, **there)
+    check(x, u, filters, (index[:rows], logp[:rows]))
+    index, logp = index.view(times, rows).cpu(), logp.double().view(times, rows).cpu()
+    assert torch.equal(index, index[:1].expand(times, rows))
+    t = torch.as_tensor(filters.get("temperature", 1.0), dtype=torch.float64).expand(rows)
+    top = x.double().max(-1).values
+    far = (top - x.double().gather(1, index[0].clamp(min=0)[:, None])[:, 0]) / t
+    far = torch.where((t > 0) & top.isfinite() & (index[0] >= 0), far, 0.0)
+    assert torch.equal(logp.isnan(), (index < 0))
+    off = (logp - logp[:1]).nan_to_num(0.0).abs()
+    assert (off <= 16 * U * (far + (logp[:1].nan_to_num(0.0) + far).abs()) + 2e-12).all()
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("n", [257, 600, 640, 1021, 1284, 2048, 2051, 3001, 4096])
+def test_rows_side_by_side(n, kind):
+    for i, f in enumerate(FILTERS):
+        x, u = logits(12, n, kind, seed=200 + i)
+        check_repeated(x, u, f, 320)
+    x, u = logits(12, n, kind, seed=220)
+    g = torch.Generator().manual_seed(221)
+    check_repeated(x, u, dict(temperature=torch.rand(12, generator=g) * 2, top_k=torch.randint(0, n + 2, (12,), generator=g),
+                              top_p=torch.rand(12, generator=g) * 1.2, min_p=torch.rand(12, generator=g) * 0.2), 320)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("n", [300, 1021, 2051])
+def test_rows_side_by_side_with_ties_and_extreme_values(n, kind):
+    for seed in range(3):
+        x, u = logits(12, n, kind, seed=230 + seed)
+        x = (x * 2).round() / 2
+        x[0] = 1.0
+        x[1, 5] = math.nan
+        x[2] = -math.inf
+        x[3, 7::11] = math.inf
+        x[4, 1:] = -math.inf
+        x[5] *= 1e30
+        for f in ({}, dict(top_k=max(1, n // 5)), dict(top_p=0.37), dict(temperature=0.5, top_k=n // 2 + 1, top_p=0.61),
+                  dict(top_k=3, top_p=0.4, min_p=0.2), dict(temperature=0.0), dict(min_p=0.3)):
+            check_repeated(x, u, f, 320)
+
+
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
 @pytest.mark.parametrize("n", [7, 40, 256, 300, 5000])
 def test_ties(n, kind):

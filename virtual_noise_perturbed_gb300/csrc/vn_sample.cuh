@@ -87,7 +87,7 @@ struct Rows {
   const void* x;
   int64_t rows, n;
   const float* u;
-  double temperature, min_p;
+  float temperature, min_p;
   u64 top_p;  // a share of 2^64, all ones for everything
   int64_t top_k;
   const float* temperatures;
@@ -146,11 +146,11 @@ struct Wish {
 __device__ __forceinline__ Wish wish_of(const Rows& a, int64_t row) {
   Wish w;
   w.u = fetch(a.u + row);
-  w.temperature = static_cast<float>(a.temperature);
+  w.temperature = a.temperature;
   w.ch = a.ch;
   w.cl = a.cl;
   w.top_p = a.top_p;
-  w.min_p = static_cast<float>(a.min_p);
+  w.min_p = a.min_p;
   w.top_k = a.top_k;
   if (a.temperatures != nullptr) {
     const float t = fetch(a.temperatures + row);
@@ -270,6 +270,19 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
+}
+// The largest logit of 16 bytes, NaN if one is.
+template <typename T>
+__device__ __forceinline__ float largest_of(const uint4& raw) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t a, b;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(raw.x), "r"(raw.y));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(raw.z), "r"(raw.w));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    return max_nan(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+  } else {
+    return max_nan(max_nan(__uint_as_float(raw.x), __uint_as_float(raw.y)), max_nan(__uint_as_float(raw.z), __uint_as_float(raw.w)));
+  }
 }
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -496,19 +509,18 @@ template <int W>
 constexpr int kFinePlaces = kFine<W> + 32;
 // The most logits that a border is looked for among one by one, and the most that all of the rest is done for so.
 template <int W>
-constexpr int kCap = W == 1 ? 256 : 512;
+constexpr int kCap = W <= 2 ? 256 : 512;
 template <int W>
-constexpr int kFew = W == 1 ? 64 : W < 8 ? 128 : 256;
+constexpr int kFew = W <= 2 ? 64 : W < 8 ? 128 : 256;
 
-struct NoBins {};
+struct Nothing {};
 template <int W>
 struct MergedBins {
   uint32_t fine[kFinePlaces<W>];
 };
-// A CTA's shared memory but for its logits.
+// What top_k and top_p need: bins, and a list of the logits next to a border.
 template <int W, bool kCluster>
-struct Shared {
-  u64 powers[32];
+struct Lists {
   union {
     struct {
       u64 list[kCap<W>];          // logits as key and complement of the index: the larger, the earlier in the order
@@ -520,17 +532,22 @@ struct Shared {
     };
   };
   uint32_t fine[kFinePlaces<W>];  // counts of the bins, or sums
-  std::conditional_t<kCluster, MergedBins<W>, NoBins> merged;  // over all ranks, in a cluster
+  std::conditional_t<kCluster, MergedBins<W>, Nothing> merged;  // over all ranks, in a cluster
   uint32_t list_count;
   u64 edge[2];                    // the last one kept, by count and by sum: a rank may still read the one when the other is cleared
-  u64 warps[2][W], warps_too[2][W];  // of the two reductions at work at most
   u64 few[2][W];
-  u64 mine[2], mine_too[2];       // what this CTA hands to the others of its cluster
   // Of the bin that a border falls into:
   int bin, last_bin;
-  int sure;                       // of the draw by coarse sums (rank 0's)
   u64 above_sum, target;
   uint32_t above_count, bin_count;
+};
+// A CTA's shared memory but for its logits.
+template <int W, bool kCluster, bool kLists = true>
+struct Shared : std::conditional_t<kLists, Lists<W, kCluster>, Nothing> {
+  u64 powers[32];
+  u64 warps[2][W], warps_too[2][W];  // of the two reductions at work at most
+  u64 mine[2], mine_too[2];       // what this CTA hands to the others of its cluster
+  int sure;                       // of the draw by coarse sums (rank 0's)
 };
 
 // A row's share in a CTA: `vectors` 16-byte words a lane from `mine` on, 32 apart, position = word * kVec + element.
@@ -566,11 +583,11 @@ struct Part {
   }
 };
 
-template <int W, bool kCluster>
+template <int W, bool kCluster, bool kLists = true>
 struct Team {
-  Shared<W, kCluster>& s;
+  Shared<W, kCluster, kLists>& s;
   int ranks, rank, turn = 0;
-  __device__ __forceinline__ Team(Shared<W, kCluster>& shared) : s(shared) {
+  __device__ __forceinline__ Team(Shared<W, kCluster, kLists>& shared) : s(shared) {
     ranks = kCluster ? static_cast<int>(cg::this_cluster().num_blocks()) : 1;
     rank = kCluster ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
   }
@@ -1143,10 +1160,10 @@ __device__ __noinline__ Prefix exact_nucleus(Shared<W, kCluster>& s, const Part<
 }
 
 // The draw by weight().
-template <typename T, int W, bool kCluster>
-__device__ __noinline__ void exact_draw(Shared<W, kCluster>& s, const Part<T> part, const Rows& a, int64_t row, float m, const Wish w,
+template <typename T, int W, bool kCluster, bool kLists>
+__device__ __noinline__ void exact_draw(Shared<W, kCluster, kLists>& s, const Part<T> part, const Rows& a, int64_t row, float m, const Wish w,
                                         const Prefix kept) {
-  Team<W, kCluster> team(s);
+  Team<W, kCluster, kLists> team(s);
   team.sync();
   auto weigh = [&](float v, int at) { return kept.holds(v, at) ? weight(v, m, w, s.powers) : 0; };
   u64 own = 0, before;
@@ -1174,10 +1191,11 @@ __device__ __noinline__ void exact_draw(Shared<W, kCluster>& s, const Part<T> pa
 template <typename T, int W, bool kCluster, int kCuts>
 __global__ void __launch_bounds__(W * 32, (kCuts != 0 ? 24 : 32) / W) cta_kernel(const Rows a, int per) {
   extern __shared__ uint4 logits[];
-  __shared__ Shared<W, kCluster> s;
+  constexpr bool kLists = kCuts != 0;
+  __shared__ Shared<W, kCluster, kLists> s;
   let_next();
   if (threadIdx.x < 32) s.powers[threadIdx.x] = kPowersInit[threadIdx.x];
-  Team<W, kCluster> team(s);
+  Team<W, kCluster, kLists> team(s);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = static_cast<int>(a.n);
   // So that no bin's sum passes 32 bits.
@@ -1210,16 +1228,18 @@ __global__ void __launch_bounds__(W * 32, (kCuts != 0 ? 24 : 32) / W) cta_kernel
         if (it0 + u >= per) break;
         if (at >= 0 && at + kVec<T> <= n) {
           mine[(it0 + u) * 32] = raw[u];
+          m = max_nan(m, largest_of<T>(raw[u]));
         } else {
           T* to = reinterpret_cast<T*>(mine + (it0 + u) * 32);
           for (int q = 0; q < kVec<T>; ++q) {
             // No logit there: one that is never drawn, and after all others in the order.
-            to[q] = at + q >= 0 && at + q < n ? fetch(x + at + q) : lowest<T>();
+            const T v = at + q >= 0 && at + q < n ? fetch(x + at + q) : lowest<T>();
+            to[q] = v;
+            m = max_nan(m, value(v));
           }
         }
       }
     }
-    part.each([&](float v, int) { m = max_nan(m, v); });
     const Wish w = wish_of(a, row);
     {
       const uint32_t top = team.largest(m != m ? kAll : key_of(m));  // (and the powers are there)
@@ -1385,7 +1405,7 @@ __global__ void __launch_bounds__(W * 32, (kCuts != 0 ? 24 : 32) / W) cta_kernel
           if (a.logprob != nullptr) a.logprob[row] = logprob_of(v, m, w, total);
         });
     team.sync();
-    if (team.of_rank(&s.sure, 0) == 0) exact_draw<T, W, kCluster>(s, part, a, row, m, w, kept);
+    if (team.of_rank(&s.sure, 0) == 0) exact_draw<T, W, kCluster, kLists>(s, part, a, row, m, w, kept);
   }
   if constexpr (kCluster) team.sync();  // no CTA ends while another may read its shared memory
 }
@@ -1455,10 +1475,12 @@ cudaError_t run(const Rows& a, cudaStream_t stream) {
   while (cluster < 16 && a.rows * cluster * 2 <= dev.sm_count && words >= static_cast<int64_t>(cluster) * kThreads * 8) cluster *= 2;
   while (cluster < 16 && words * 24 > cluster * static_cast<int64_t>(kMostWords)) cluster *= 2;
   if (cluster > 1) return run_cta<T, 8, true>(a, cluster, stream);
-  // Warps a row. Many rows side by side run best on few warps each, long rows and few of them on more: 16384 rows of 1000
-  // bf16 with top-p take 98 us on one warp, 137 on four, 269 on eight; of 4096 436, 269, 365; 1024 rows of 16384 139 on
-  // four, 105 on eight; 1024 rows of 1000 24, 17, 24; 200 rows of 4096 20 on four, 16 on eight; one row of 1000 6.5 and 8.2.
-  if (words <= 256 && many) return run_cta<T, 1, false>(a, 1, stream);
+  // Warps a row. Many rows side by side run best on few warps each, long rows and few of them on more. 16384 rows with top-p, on one,
+  // two and four warps: of 1000 bf16 86, 91, 131 us; of 1000 fp32 92, 90, 122; of 2048 bf16 150, 134, 165; of 4096 bf16 327, 233, 241,
+  // with top_k 186, 134, 164; of 4096 fp32 442, 279, 245; 1024 rows of 16384 139 on four, 105 on eight; 1024 rows of 1000 24 on one, 17
+  // on four, 24 on eight; 200 rows of 4096 20 on four, 16 on eight; one row of 1000 6.5 and 8.2.
+  if (words <= 160 && many) return run_cta<T, 1, false>(a, 1, stream);
+  if (words <= 512 && many) return run_cta<T, 2, false>(a, 1, stream);
   if (words <= (a.rows >= 2 * static_cast<int64_t>(dev.sm_count) ? 1024 : 256)) return run_cta<T, 4, false>(a, 1, stream);
   return run_cta<T, 8, false>(a, 1, stream);
 }
@@ -1467,7 +1489,7 @@ template <typename T>
 cudaError_t sample_rows(const SampleArgs& g, cudaStream_t stream) {
   Rows a;
   a.x = g.logits; a.rows = g.rows; a.n = g.n; a.u = g.u;
-  a.temperature = g.temperature; a.min_p = g.min_p; a.top_k = g.top_k;
+  a.temperature = static_cast<float>(g.temperature); a.min_p = static_cast<float>(g.min_p); a.top_k = g.top_k;
   a.temperatures = g.temperatures; a.top_ks = g.top_ks; a.top_ps = g.top_ps; a.min_ps = g.min_ps;
   a.index = g.index; a.logprob = g.logprob;
   a.top_p = g.top_p >= 1.0 ? kAllOfIt : static_cast<u64>(std::ldexp(std::max(g.top_p, 0.0), 64));
