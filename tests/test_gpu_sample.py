@@ -97,7 +97,7 @@ def test_the_longest_row(kind):
 
 
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
-@pytest.mark.parametrize("rows,n", [(4099, 8), (3000, 100), (700, 256), (600, 513), (310, 1021), (160, 4096), (80, 9001)])
+@pytest.mark.parametrize("rows,n", [(4099, 8), (3000, 100), (700, 256), (600, 513), (310, 1021), (160, 4096), (80, 9001), (150, 40000)])
 def test_many_rows(rows, n, kind):
     x, u = logits(rows, n, kind, seed=40)
     check(x, u, dict(temperature=0.8, top_p=0.95))

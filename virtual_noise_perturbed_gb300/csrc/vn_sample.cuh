@@ -530,9 +530,9 @@ struct Lists {
       u64 sums[kBins];
       uint32_t counts[kBins];
     };
+    std::conditional_t<kCluster, MergedBins<W>, Nothing> merged;  // bins over all ranks, in a cluster, until a list is begun
   };
   uint32_t fine[kFinePlaces<W>];  // counts of the bins, or sums
-  std::conditional_t<kCluster, MergedBins<W>, Nothing> merged;  // over all ranks, in a cluster
   uint32_t list_count;
   u64 edge[2];                    // the last one kept, by count and by sum: a rank may still read the one when the other is cleared
   u64 few[2][W];
@@ -1050,7 +1050,7 @@ __device__ __forceinline__ u64 cta_sum(Shared<W, kCluster>& s, int place, u64 v)
 // either order, and what lies before it, come from a look at every other.
 template <int W, bool kCluster>
 __device__ __noinline__ void few(Shared<W, kCluster>& s, const Rows& a, int64_t row, float m, const Wish w, int count) {
-  constexpr int kEach = kFew<W> / (W * 32);  // logits of a thread
+  constexpr int kEach = kFew<W> > W * 32 ? kFew<W> / (W * 32) : 1;  // logits of a thread
   for (int i = threadIdx.x; i < count; i += W * 32)
     s.list_weights[i] = weight(value_of_key(item_key(s.list[i])), m, w, s.powers);
   __syncthreads();
@@ -1423,10 +1423,11 @@ int64_t words_of(const Rows& a) {
   return (a.n + kVec<T> - 1) / kVec<T> + (aligned ? 0 : 1);
 }
 
+constexpr int kLongRow = 512;  // threads of a CTA for long rows
 // Shared memory of a CTA for its words and their sums; the rest is for Shared.
-constexpr size_t kMostWords = 200 * 1024;
-static_assert(sizeof(Shared<8, true>) + kMostWords + 1024 <= 227 * 1024, "shared memory of a CTA");
-static_assert(24 * (kSampleMost / 4 + 16 * 256) / 16 <= static_cast<int64_t>(kMostWords), "the longest rows fit a cluster of 16 CTAs");
+constexpr size_t kMostWords = 204 * 1024;
+static_assert(sizeof(Shared<16, true>) + kMostWords <= 227 * 1024 && sizeof(Shared<16, false>) + kMostWords <= 227 * 1024, "shared memory of a CTA");
+static_assert(24 * (kSampleMost / 4 + 16 * kLongRow) / 16 <= static_cast<int64_t>(kMostWords), "the longest rows fit a cluster of 16 CTAs");
 
 template <typename T, int W, bool kCluster, int kCuts>
 cudaError_t run_cuts(const Rows& a, int cluster, cudaStream_t stream) {
@@ -1469,12 +1470,22 @@ cudaError_t run(const Rows& a, cudaStream_t stream) {
   // top-k) and 10.0 (10.0, 12.6) by a histogram, 16384 rows 31 (84, 44) and 31 (45, 67).
   const bool many = a.rows >= 24 * static_cast<int64_t>(dev.sm_count);
   if (a.n <= 256 && !many) return run_warp<T, 8>(a, stream);
-  // CTAs a row: until the rows fill the SMs, while a lane has four words or more; at least what holds the row.
+  // CTAs a row: until the rows fill the SMs, while a lane has eight words or more; at least what holds the row. Beyond eight a cluster's
+  // barriers and the merging of bins cost more: 8 rows of 131072 fp32 with top_k take 13 us on eight CTAs each and 30 on sixteen (with
+  // top-p 54 and 63, without filters 20 and 18); one row of 131071 bf16 with four words a lane 16.9 (41.7, 15.7), with eight 13.9 (43.5,
+  // 17.2), with sixteen 14.8 (49, 23.6).
   const int64_t words = words_of<T>(a);
+  auto bytes = [&](int64_t cluster) {
+    const int64_t lanes = cluster * kLongRow;
+    return (words + lanes - 1) / lanes * kLongRow * 24;
+  };
   int cluster = 1;
-  while (cluster < 16 && a.rows * cluster * 2 <= dev.sm_count && words >= static_cast<int64_t>(cluster) * kThreads * 8) cluster *= 2;
-  while (cluster < 16 && words * 24 > cluster * static_cast<int64_t>(kMostWords)) cluster *= 2;
-  if (cluster > 1) return run_cta<T, 8, true>(a, cluster, stream);
+  while (cluster < 8 && a.rows * cluster * 2 <= dev.sm_count && words >= static_cast<int64_t>(cluster) * kLongRow * 8) cluster *= 2;
+  while (cluster < 16 && bytes(cluster) > static_cast<int64_t>(kMostWords)) cluster *= 2;
+  // Sixteen warps where a CTA has an SM to itself: 32 rows of 131071 fp32 with top_k 17 us, with top-p 137, on eight 25 and 212; 100 rows of
+  // 4096 bf16 6.0 and 11.7, on eight 6.9 and 12.7; of 32768 10.3 and 40, on eight 14.7 and 60; one row of 4096 with all filters 6.2 and 6.4.
+  if (cluster > 1) return run_cta<T, kLongRow / 32, true>(a, cluster, stream);
+  if (a.rows <= dev.sm_count && words >= kLongRow) return run_cta<T, kLongRow / 32, false>(a, 1, stream);
   // Warps a row. Many rows side by side run best on few warps each, long rows and few of them on more. 16384 rows with top-p, on one,
   // two and four warps: of 1000 bf16 86, 91, 131 us; of 1000 fp32 92, 90, 122; of 2048 bf16 150, 134, 165; of 4096 bf16 327, 233, 241,
   // with top_k 186, 134, 164; of 4096 fp32 442, 279, 245; 1024 rows of 16384 139 on four, 105 on eight; 1024 rows of 1000 24 on one, 17
