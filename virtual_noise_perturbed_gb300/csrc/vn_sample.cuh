@@ -19,9 +19,9 @@
 // bin, some tens, are listed, and each finds its place and what lies before it by a look at all others. With a
 // small top_k everything kept is listed, and the rest of the work is done on the list.
 //
-// Bound by memory in principle (a row once); in fact by instructions, 40 to 80 a logit with what a row costs apart from them, at
-// half of the issue rate: 24 to 32 warps an SM that wait for one another's results. 16384 rows of 4096 bf16: 105 us without filters, 166 with
-// top_k 50, 244 with top_p 0.9 (20 for reading them); 32 of 131071 fp32: 23 with top_k; 1024 rows of 8: 2.5; one of 4096: 3.9 to 8.2.
+// Bound by memory in principle (a row once); in fact by instructions, 35 to 70 a logit with what a row costs apart from them, at
+// half of the issue rate: 20 to 32 warps an SM that wait for one another's results. 16384 rows of 4096 bf16: 102 us without filters, 134 with
+// top_k 50, 233 with top_p 0.9 (20 for reading them); 32 of 131071 fp32: 17 with top_k; 1024 rows of 8: 2.5; one of 4096: 4.1 to 8.2.
 // (Compiled once for each type of the logits, vn_sample_f32.cu and vn_sample_bf16.cu, to build in half the time.)
 #pragma once
 
@@ -497,7 +497,7 @@ template <typename T>
 constexpr int kVec = 16 / static_cast<int>(sizeof(T));  // logits of 16 bytes
 
 // Bins of a fraction of a binary order of the weights, over 32 of them, the last bin with all that is below: finer ones for the
-// longer rows, so that few logits share the bin of a border (32 rows of 131071 fp32 with top-p: 337 us on 512 bins, 165 on 2048). Padded
+// longer rows, so that few logits share the bin of a border (32 rows of 131071 fp32 with top-p, on eight warps: 337 us on 512 bins, 165 on 2048). Padded
 // in shared memory, so that lanes with an order each read from different banks.
 template <int W>
 constexpr int kPerOrder = W < 8 ? 16 : 64;
@@ -1445,8 +1445,9 @@ cudaError_t run_cuts(const Rows& a, int cluster, cudaStream_t stream) {
                            stream, a, per);
 }
 
-// A kernel for each set of cuts that may be asked for: code and registers that a call does not need cost it rows at once. 16384 rows of
-// 4096 bf16 without any take 105 us for 133, with min_p 134 for 197; with top_k 166 for 170, top_p 244 for 258.
+// A kernel for each set of cuts that may be asked for: code, registers and shared memory that a call does not need cost it rows at once. With
+// four warps a row 16384 rows of 4096 bf16 without any took 105 us for 133, with min_p 134 for 197, with top_k 166 for 170, with top_p 244
+// for 258; without the lists' shared memory as many of fp32 111 for 124.
 template <typename T, int W, bool kCluster>
 cudaError_t run_cta(const Rows& a, int cluster, cudaStream_t stream) {
   const int cuts = (a.top_ks != nullptr || (a.top_k > 0 && a.top_k < a.n) ? 1 : 0) + (a.top_ps != nullptr || a.top_p != kAllOfIt ? 2 : 0);
@@ -1467,7 +1468,7 @@ cudaError_t run(const Rows& a, cudaStream_t stream) {
   const cudaError_t err = device_info(&dev);
   if (err != cudaSuccess) return err;
   // Up to 256 logits where a warp a row does not fill the GPU anyhow: 1024 rows of 256 bf16 take 5.4 us here (13.4 with top-p, 7.2 with
-  // top-k) and 10.0 (10.0, 12.6) by a histogram, 16384 rows 31 (84, 44) and 31 (45, 67).
+  // top-k) and 10.0 (10.0, 12.6) by a histogram, 16384 rows 31 (84, 44) and 22 (41, 53).
   const bool many = a.rows >= 24 * static_cast<int64_t>(dev.sm_count);
   if (a.n <= 256 && !many) return run_warp<T, 8>(a, stream);
   // CTAs a row: until the rows fill the SMs, while a lane has eight words or more; at least what holds the row. Beyond eight a cluster's
