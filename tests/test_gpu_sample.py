@@ -72,7 +72,7 @@ def check(x, u, filters, got=None):
 
 
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
-@pytest.mark.parametrize("n", [1, 2, 3, 8, 31, 32, 33, 64, 65, 127, 128, 200, 256, 257, 300, 1000, 1021, 2048, 4096, 4097])
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 8, 9, 15, 16, 17, 31, 32, 33, 64, 65, 127, 128, 200, 256, 257, 300, 1000, 1021, 2048, 4096, 4097])
 def test_sizes(n, kind):
     for i, f in enumerate(FILTERS):
         x, u = logits(9, n, kind, seed=i)
@@ -97,7 +97,7 @@ def test_the_longest_row(kind):
 
 
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
-@pytest.mark.parametrize("rows,n", [(4099, 8), (3000, 100), (700, 256), (600, 513), (310, 1021), (160, 4096), (80, 9001), (150, 40000)])
+@pytest.mark.parametrize("rows,n", [(5001, 3), (4099, 8), (2049, 13), (3000, 100), (700, 256), (600, 513), (310, 1021), (160, 4096), (80, 9001), (150, 40000)])
 def test_many_rows(rows, n, kind):
     x, u = logits(rows, n, kind, seed=40)
     check(x, u, dict(temperature=0.8, top_p=0.95))
@@ -153,7 +153,7 @@ def test_rows_side_by_side_with_ties_and_extreme_values(n, kind):
 
 
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
-@pytest.mark.parametrize("n", [7, 40, 256, 300, 5000])
+@pytest.mark.parametrize("n", [4, 7, 16, 40, 256, 300, 5000])
 def test_ties(n, kind):
     """Logits of few values: the borders of the filters fall among equal ones, the lower indices of which are kept."""
     for seed in range(6):
@@ -184,7 +184,7 @@ def test_zeros_of_both_signs_are_equal(n):
 
 
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
-@pytest.mark.parametrize("n", [5, 300, 4096])
+@pytest.mark.parametrize("n", [4, 5, 16, 300, 4096])
 def test_rows_without_an_answer_and_extreme_values(n, kind):
     low = torch.finfo(KINDS[kind]).min
     x, u = logits(12, n, kind, seed=60)
@@ -219,7 +219,7 @@ def test_random_numbers_at_the_ends(n):
 
 
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
-@pytest.mark.parametrize("n", [20, 256, 1021, 4096])
+@pytest.mark.parametrize("n", [3, 8, 13, 20, 256, 1021, 4096])
 def test_parameters_of_each_row(n, kind):
     rows = 60
     x, u = logits(rows, n, kind, seed=80)

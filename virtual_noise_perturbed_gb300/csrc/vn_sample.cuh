@@ -12,7 +12,8 @@
 // whose sums' error is bounded, and by whole ones only where a border lies within that bound: one row in
 // fifty at 4,096 logits, half of them at 131,072.
 //
-// A row is read once, into registers or shared memory, and every later pass goes over that copy. Up to 128
+// A row is read once, into registers or shared memory, and every later pass goes over that copy. Up to 16 logits a part of a warp has
+// a row, and each logit looks at all others. Up to 128
 // logits (256 where rows are few) a warp has a row in registers, and finds where a prefix ends by bisecting the bits of a logit.
 // Beyond, a CTA or a cluster of CTAs has one: each warp holds a contiguous stretch of it and each lane every 32nd 16 bytes of that,
 // the ones that it read itself. A histogram over x in units of T tells the bin in which a prefix ends; the logits of that
@@ -21,7 +22,7 @@
 //
 // Bound by memory in principle (a row once); in fact by instructions, 35 to 70 a logit with what a row costs apart from them, at
 // half of the issue rate: 20 to 32 warps an SM that wait for one another's results. 16384 rows of 4096 bf16: 102 us without filters, 134 with
-// top_k 50, 233 with top_p 0.9 (20 for reading them); 32 of 131071 fp32: 17 with top_k; 1024 rows of 8: 2.5; one of 4096: 4.1 to 8.2.
+// top_k 50, 233 with top_p 0.9 (20 for reading them); 32 of 131071 fp32: 17 with top_k; 1024 rows of 8: 1.9; one of 4096: 4.1 to 8.2.
 // (Compiled once for each type of the logits, vn_sample_f32.cu and vn_sample_bf16.cu, to build in half the time.)
 #pragma once
 
@@ -296,6 +297,71 @@ struct Kept {
   int32_t last = 0x7FFFFFFF;
   __device__ __forceinline__ bool holds(uint32_t k, int32_t at) const { return k > key || (k == key && at <= last); }
 };
+
+// ---------------------------------------------------------------- G lanes a row, up to 16 logits
+// Of each logit its place in the order and what lies before it come from a look at every other. A policy's handful of actions would leave
+// most of a warp idle, and bisection takes a round for each bit: 16384 rows of 8 fp32 take 2.6 us here (with top-p 3.7) and 7.3 (27) with
+// a warp a row, of 16 4.2 (7.1) and 7.3 (28); 1024 rows of 8 1.9 (2.3) and 2.3 (5.3).
+template <typename T, int G>
+__global__ void __launch_bounds__(kThreads) group_kernel(const Rows a) {
+  __shared__ u64 powers[32];
+  let_next();
+  if (threadIdx.x < 32) powers[threadIdx.x] = kPowersInit[threadIdx.x];
+  __syncthreads();
+  after_previous();
+  constexpr int kRows = kThreads / G;
+  const int lane = threadIdx.x % G, n = static_cast<int>(a.n);
+  const uint32_t group = ((1u << G) - 1u) << (threadIdx.x % 32 - lane);  // other groups of the warp go their own ways
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G; row < a.rows; row += static_cast<int64_t>(gridDim.x) * kRows) {
+    const float v = lane < n ? value(fetch(static_cast<const T*>(a.x) + row * n + lane)) : absent();
+    float m = lane < n ? v : -INFINITY;
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(group, m, o));
+    const Wish w = wish_of(a, row);
+    if (w.bad || m != m || m == -INFINITY) {
+      if (lane == 0) {
+        a.index[row] = -1;
+        if (a.logprob != nullptr) a.logprob[row] = NAN;
+      }
+      continue;
+    }
+    u64 mine = weight(v, m, w, powers);
+    bool kept = lane < n;
+    if (w.top_k < n || w.top_p != kAllOfIt) {
+      const uint32_t key = key_of(v);
+      int rank = 0;
+      u64 before = 0;
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const uint32_t other = __shfl_sync(group, key, j, G);
+        const u64 its = __shfl_sync(group, mine, j, G);
+        const bool earlier = other > key || (other == key && j < lane);
+        rank += earlier;
+        before += earlier ? its : 0;
+      }
+      kept = kept && rank < w.top_k;
+      if (w.top_p != kAllOfIt) {
+        u64 all = kept ? mine : 0;
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) all += __shfl_xor_sync(group, all, o);
+        kept = kept && (rank == 0 || before < nucleus(w.top_p, all));
+      }
+    }
+    if (w.min_p > 0.f) kept = kept && Floor(m, w).above(v, m, w, powers);
+    if (!kept) mine = 0;
+    u64 scan = mine;
+#pragma unroll
+    for (int o = 1; o < G; o <<= 1) {
+      const u64 t = __shfl_up_sync(group, scan, o, G);
+      if (lane >= o) scan += t;
+    }
+    const u64 s = __shfl_sync(group, scan, G - 1, G), r = share(w.u, s);
+    if (scan > r && scan - mine <= r) {
+      a.index[row] = lane;
+      if (a.logprob != nullptr) a.logprob[row] = logprob_of(v, m, w, s);
+    }
+  }
+}
 
 // ---------------------------------------------------------------- a warp a row
 // Lane l holds the logits l, l + 32, ..
@@ -1416,6 +1482,12 @@ cudaError_t run_warp(const Rows& a, cudaStream_t stream) {
   return launch_overlapped(warp_kernel<T, R>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream, a);
 }
 
+template <typename T, int G>
+cudaError_t run_group(const Rows& a, cudaStream_t stream) {
+  const int64_t grid = std::min<int64_t>((a.rows + kThreads / G - 1) / (kThreads / G), 0x7FFFFFFFll);
+  return launch_overlapped(group_kernel<T, G>, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream, a);
+}
+
 // The 16-byte words of a row: one more where rows start within one.
 template <typename T>
 int64_t words_of(const Rows& a) {
@@ -1461,6 +1533,9 @@ cudaError_t run_cta(const Rows& a, int cluster, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t run(const Rows& a, cudaStream_t stream) {
+  if (a.n <= 4) return run_group<T, 4>(a, stream);
+  if (a.n <= 8) return run_group<T, 8>(a, stream);
+  if (a.n <= 16) return run_group<T, 16>(a, stream);
   if (a.n <= 32) return run_warp<T, 1>(a, stream);
   if (a.n <= 64) return run_warp<T, 2>(a, stream);
   if (a.n <= 128) return run_warp<T, 4>(a, stream);
