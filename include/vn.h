@@ -504,7 +504,7 @@ vn_status vn_unpack_weight(const void* codes, const void* scales, vn_dtype dt, i
  *     y[r, j] = act(sum_k x[r, k] code[j, k] scale[j, k / group] + b[j]) + residual[r, j]
  * x [rows, in], scales, residual and y [rows, out] of dt, b [out] of b_dt or NULL. Up to 32 rows (fp32: 10) a group's products of x
  * and codes are summed first and scaled in fp32; with more rows the values are unpacked into
- * the workspace first, in bf16 each rounded to bf16. In fp32 an infinity in x gives NaN. workspace:
+ * the workspace first, in bf16 each as the sum of two bf16 values (exact), in fp32 rounded once. In fp32 an infinity in x gives NaN. workspace:
  * vn_linear_packed_workspace bytes, 256-byte aligned; errors and status as for vn_linear.
  */
 vn_status vn_linear_packed(const void* x, const void* codes, const void* scales, vn_dtype dt, int group,

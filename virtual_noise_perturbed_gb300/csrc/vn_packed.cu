@@ -12,8 +12,8 @@
 // 256 weights of a product, beside reading the codes once: so the rows of x are the product's columns, eight at no
 // more cost than one. fp32 rows take three columns each, for the three bf16 terms of their values; a code is exact in
 // bf16. The sum of a group is scaled in fp32. One row of 4096 to 4096 bf16 5.2 us (8.9 MB: 1.7 TB/s; plain bf16
-// weights take 6.2), 8 rows 6.4, 32 14.9; fp32 6.9, 5 rows 9.6. More rows are quicker on unpacked weights: 64 rows 18 us for
-// 53 so, fp32 16 rows 36 for 113.
+// weights take 6.2), 8 rows 6.4, 32 14.9; fp32 6.9, 5 rows 9.6. More rows take unpacked weights, in bf16 as two terms each: 64 rows 27 us
+// and 1024 60 (32 rows at a time 28 and 445), fp32 16 rows 36.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -233,6 +233,17 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const T* w, uint8_t* cod
   }
 }
 
+// The codes of a lane's eight weights, from its word and that of the lane with the other product's.
+__device__ __forceinline__ void codes_of(uint32_t word, int lane, float (&v)[8]) {
+  const bool odd = (lane & 2) != 0;
+  const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, word, 2);
+  const uint32_t a = odd ? other >> 8 : word, b = odd ? word >> 8 : other;
+  // A nibble as the last bits of 2^23.
+  auto code = [](uint32_t n, int shift) { return __uint_as_float(((n >> shift) & 15u) | 0x4B000000u) - 8388616.f; };
+  v[0] = code(a, 0); v[1] = code(a, 16); v[2] = code(a, 4); v[3] = code(a, 20);
+  v[4] = code(b, 0); v[5] = code(b, 16); v[6] = code(b, 4); v[7] = code(b, 20);
+}
+
 // The same way back: 29 us and 5.8 TB/s, in fp32 46 and 6.5. Rows that start off a lane's 16 bytes go through shared
 // memory, from where a warp stores neighbours.
 template <typename T>
@@ -257,16 +268,12 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* codes, 
     if (run > u * kSegment + (lane >> 4) * kBlock) word[u] = __ldcs(from + u * (2 * kBlockBytes / 4));
     if (left > u * kSegment) s[u] = fetch(scale + ((u * kSegment) >> at.digits));
   }
-  const bool odd = (lane & 2) != 0;
   T* const to = w + row * at.in + k0 + lane * 8;
 #pragma unroll
   for (int u = 0; u < kRun; ++u) {
     if (run <= u * kSegment) break;
-    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, word[u], 2);
-    const uint32_t a = odd ? other >> 8 : word[u], b = odd ? word[u] >> 8 : other;
-    // A nibble as the last bits of 2^23.
-    auto code = [](uint32_t v, int shift) { return __uint_as_float(((v >> shift) & 15u) | 0x4B000000u) - 8388616.f; };
-    float v[8] = {code(a, 0), code(a, 16), code(a, 4), code(a, 20), code(b, 0), code(b, 16), code(b, 4), code(b, 20)};
+    float v[8];
+    codes_of(word[u], lane, v);
     const float f = value(s[u]);
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] = __fmul_rn(v[q], f);
@@ -528,10 +535,120 @@ cudaError_t unpack_typed(const uint8_t* codes, const void* scales, int64_t out, 
                            static_cast<const T*>(scales), static_cast<T*>(w), at);
 }
 
+// ---------------------------------------------------------------- many rows
 // The most rows that the kernel on packed weights takes (both sides at the top of this file).
 int64_t few_rows(vn_dtype dt) { return dt == VN_BF16 ? 32 : 10; }
 
 int64_t padded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+
+// In bf16 a value, code times scale, has up to 11 significant bits and would be rounded to 8: so it is taken as the sum of two bf16
+// values, its leading 8 bits and the rest, which is exact (but for a rest below 2^-133). The plain layer runs on rows of twice the length,
+//   [x | x] [leading | rest]^T,
+// with each half padded by zeros to whole 16 bytes, and adds both up in one accumulator: no value is rounded whatever the rows.
+constexpr int64_t kTermRows = 16384;  // rows of x that are laid out at once
+constexpr int kTermRun = 2;
+int64_t half_of(int64_t in) { return (in + 7) / 8 * 8; }
+
+// The first `weight_ctas` CTAs lay out the weights, a warp a run of segments of a row; the others x, eight elements a
+// thread. x's second copy has zeros for infinities (and NaN): the first one's products are theirs, and an infinity times a rest of 0 is none.
+__global__ void __launch_bounds__(kThreads)
+terms_kernel(const uint8_t* codes, const __nv_bfloat16* scales, uint4* w, const Places<kTermRun> at, int64_t weight_ctas,
+             const __nv_bfloat16* x, uint4* xx, int64_t rows, int vec) {
+  let_next();
+  after_previous();
+  const int64_t words = (at.in + 7) / 8;  // 16-byte words of a half
+  if (blockIdx.x >= weight_ctas) {
+    const int64_t i = (blockIdx.x - weight_ctas) * kThreads + threadIdx.x;
+    if (i >= rows * words) return;
+    const int64_t row = i / words, word = i - row * words;
+    Eight<__nv_bfloat16> v;
+    if (vec) v.load(x + row * at.in + word * 8);
+    else v.gather(x + row * at.in + word * 8, static_cast<int>(min(at.in - word * 8, static_cast<int64_t>(8))));
+    uint32_t finite[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      finite[q] = v.w[q] & (((v.w[q] & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu) | ((v.w[q] & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u));
+    uint4* const to = xx + row * 2 * words + word;
+    to[0] = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    to[words] = make_uint4(finite[0], finite[1], finite[2], finite[3]);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  int64_t row, k0;
+  at.find(static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5), &row, &k0);
+  if (row >= at.out) return;
+  const int run = static_cast<int>(min(at.in - k0, static_cast<int64_t>(kTermRun * kSegment))), left = run - lane * 8;
+  const uint32_t* const from = reinterpret_cast<const uint32_t*>(codes + (row * at.blocks + k0 / kBlock) * kBlockBytes) + word_of(lane);
+  const __nv_bfloat16* const scale = scales + row * at.groups + ((k0 + lane * 8) >> at.digits);
+  uint4* const to = w + row * 2 * words + (k0 >> 3) + lane;
+  uint32_t word[kTermRun];
+  float s[kTermRun];
+#pragma unroll
+  for (int u = 0; u < kTermRun; ++u) {
+    word[u] = run > u * kSegment + (lane >> 4) * kBlock ? __ldcs(from + u * (2 * kBlockBytes / 4)) : kNothing;
+    s[u] = left > u * kSegment ? value(fetch(scale + ((u * kSegment) >> at.digits))) : 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < kTermRun; ++u) {
+    if (run <= u * kSegment) break;
+    float v[8];
+    codes_of(word[u], lane, v);
+    if (left <= u * kSegment) continue;
+    uint32_t leading[8], rest[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float z = __fmul_rn(v[q], s[u]);  // exact
+      const uint32_t upper = __float_as_uint(z) & 0xFFFF0000u;
+      leading[q] = upper;
+      rest[q] = (upper & 0x7F800000u) == 0x7F800000u ? 0u : __float_as_uint(__fsub_rn(z, __uint_as_float(upper)));
+    }
+    to[u * (kSegment / 8)] = make_uint4(join_terms(leading[0], leading[1]), join_terms(leading[2], leading[3]),
+                                        join_terms(leading[4], leading[5]), join_terms(leading[6], leading[7]));
+    to[u * (kSegment / 8) + words] = make_uint4(join_terms(rest[0], rest[1]), join_terms(rest[2], rest[3]),
+                                                join_terms(rest[4], rest[5]), join_terms(rest[6], rest[7]));
+  }
+}
+
+cudaError_t run_terms(const PackedArgs& a, cudaStream_t stream) {
+  const int64_t half = half_of(a.in);
+  uint8_t* const w = static_cast<uint8_t*>(a.workspace);
+  uint8_t* const xx = w + padded(a.out * half * 4);
+  const Places<kTermRun> at(a.out, a.in, a.group, true);
+  const int vec = a.in % 8 == 0 && fits(a.x, 16);
+  for (int64_t r = 0; r < a.rows; r += kTermRows) {
+    const int64_t rows = std::min(kTermRows, a.rows - r);
+    const int64_t weight_ctas = r == 0 ? (at.items() + kWarps - 1) / kWarps : 0;
+    const int64_t grid = weight_ctas + (rows * (half / 8) + kThreads - 1) / kThreads;
+    if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+    const __nv_bfloat16* const x = static_cast<const __nv_bfloat16*>(a.x) + r * a.in;
+    cudaError_t err = launch_overlapped(terms_kernel, dim3(static_cast<unsigned>(grid)), kThreads, 0, 0, stream, a.codes,
+                                        static_cast<const __nv_bfloat16*>(a.scales), reinterpret_cast<uint4*>(w), at, weight_ctas, x,
+                                        reinterpret_cast<uint4*>(xx), rows, vec);
+    if (err != cudaSuccess) return err;
+    DenseArgs d = {};
+    d.x = xx; d.w = w; d.dt = VN_BF16; d.b = a.b; d.b_dt = a.b_dt;
+    d.residual = a.residual != nullptr ? static_cast<const __nv_bfloat16*>(a.residual) + r * a.out : nullptr;
+    d.rows = rows; d.in = 2 * half; d.out = a.out; d.act = a.act;
+    d.y = static_cast<__nv_bfloat16*>(a.y) + r * a.out;
+    if ((err = launch_dense(d, stream)) != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+// Rows too long for that: the kernel on packed weights, as many rows as it takes at a time.
+cudaError_t run_slices(const PackedArgs& a, cudaStream_t stream) {
+  for (int64_t r = 0; r < a.rows; r += few_rows(VN_BF16)) {
+    PackedArgs one = a;
+    one.rows = std::min(few_rows(VN_BF16), a.rows - r);
+    one.x = static_cast<const __nv_bfloat16*>(a.x) + r * a.in;
+    if (a.residual != nullptr) one.residual = static_cast<const __nv_bfloat16*>(a.residual) + r * a.out;
+    one.y = static_cast<__nv_bfloat16*>(a.y) + r * a.out;
+    const cudaError_t err = run_packed<__nv_bfloat16>(one, stream);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+bool sliced(vn_dtype dt, int64_t in) { return dt == VN_BF16 && 2 * half_of(in) > kDenseMost; }
 
 }  // namespace
 
@@ -548,19 +665,23 @@ cudaError_t launch_unpack(const uint8_t* codes, const void* scales, vn_dtype dt,
 }
 
 int64_t packed_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, bool aligned) {
-  if (rows <= few_rows(dt)) return 0;
-  return padded(out * in * (dt == VN_BF16 ? 2 : 4)) + dense_workspace(rows, in, out, dt, aligned);
+  if (rows <= few_rows(dt) || sliced(dt, in)) return 0;
+  if (dt == VN_BF16) {  // out and half are below 2^31 here; rows that are as they are need no workspace in the plain layer
+    return padded(out * half_of(in) * 4) + padded(std::min(rows, kTermRows) * half_of(in) * 4);
+  }
+  return padded(out * in * 4) + dense_workspace(rows, in, out, dt, aligned);
 }
 
 // Many rows: the weights' values, then the plain layer.
 cudaError_t launch_packed(const PackedArgs& a, cudaStream_t stream) {
   if (a.rows <= few_rows(a.dt)) return a.dt == VN_BF16 ? run_packed<__nv_bfloat16>(a, stream) : run_packed<float>(a, stream);
+  if (a.dt == VN_BF16) return sliced(a.dt, a.in) ? run_slices(a, stream) : run_terms(a, stream);
   const cudaError_t err = launch_unpack(a.codes, a.scales, a.dt, a.out, a.in, a.group, a.workspace, stream);
   if (err != cudaSuccess) return err;
   DenseArgs d = {};
   d.x = a.x; d.w = a.workspace; d.dt = a.dt; d.b = a.b; d.b_dt = a.b_dt; d.residual = a.residual;
   d.rows = a.rows; d.in = a.in; d.out = a.out; d.act = a.act; d.y = a.y;
-  d.workspace = static_cast<uint8_t*>(a.workspace) + padded(a.out * a.in * (a.dt == VN_BF16 ? 2 : 4));
+  d.workspace = static_cast<uint8_t*>(a.workspace) + padded(a.out * a.in * 4);
   return launch_dense(d, stream);
 }
 

@@ -307,8 +307,8 @@ def linear4(x: torch.Tensor, weight: Weight4, bias: Optional[torch.Tensor] = Non
     """``linear`` on packed weights, act(x V^T + b) + residual with V code times scale (``vn_linear_packed``): a layer
     that acts on few rows and is bound by reading its weights reads a quarter of them.
 
-    x is (..., in) of the scales' dtype, the rest as for ``linear``. Up to 32 rows (float32: 10) V is not rounded; with more, V is
-    unpacked first, rounded to x's dtype, and ``linear``'s kernels run. An infinity in x gives NaN in float32.
+    x is (..., in) of the scales' dtype, the rest as for ``linear``. With more than 32 rows (float32: 10) V is
+    unpacked first, and ``linear``'s kernels run; V is not rounded in bfloat16 (two terms each), and once in float32. An infinity in x gives NaN in float32.
     Not recorded by autograd. ``check_status`` as for ``linear``."""
     y = (_binding or _native()).linear_packed(x, weight.codes, weight.scales, weight.shape[1], weight.group, bias, _act(activation),
                                               residual, out)
