@@ -1,4 +1,4 @@
-"""The layer on weights in 4 bits is as exact with many rows as with few.
+"""The layer on weights in 4 bits is as exact with many rows as with few, and may be empty.
 
 With A = sum |x| |v| of an output. A product on the tensor cores is exact, and each step of 16 k cut below 2^-23 of what it adds up;
 the sums of groups, of splits of k and of warps are fp32. Few rows: as in test_gpu_packed.py. Many rows in bf16: a value is the sum of two
@@ -155,3 +155,14 @@ def test_rows_too_long_for_twice_their_length():
     a = xs.double().abs() @ values.abs().t()
     # Some 200 groups are not zero: as many sums in fp32.
     assert bool(((y - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -16 * a).all())
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 2, 10, 11, 32, 33, 100])
+def test_an_empty_layer_for_any_number_of_rows(rows, kind):
+    empty = vn.pack4(torch.empty(4, 0, dtype=KINDS[kind], device=DEV))
+    b = torch.arange(4.0, device=DEV)
+    r = torch.ones(rows, 4, dtype=KINDS[kind], device=DEV)
+    x = torch.empty(rows, 0, dtype=KINDS[kind], device=DEV)
+    assert torch.equal(vn.linear4(x, empty, b).float(), b.expand(rows, 4))
+    assert torch.equal(vn.linear4(x, empty, b, activation="relu", residual=r).float(), b.expand(rows, 4) + 1)

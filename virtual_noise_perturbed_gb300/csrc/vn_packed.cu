@@ -675,9 +675,11 @@ int64_t packed_workspace(int64_t rows, int64_t in, int64_t out, vn_dtype dt, boo
 // Many rows: the weights' values, then the plain layer.
 cudaError_t launch_packed(const PackedArgs& a, cudaStream_t stream) {
   if (a.rows <= few_rows(a.dt)) return a.dt == VN_BF16 ? run_packed<__nv_bfloat16>(a, stream) : run_packed<float>(a, stream);
-  if (a.dt == VN_BF16) return sliced(a.dt, a.in) ? run_slices(a, stream) : run_terms(a, stream);
-  const cudaError_t err = launch_unpack(a.codes, a.scales, a.dt, a.out, a.in, a.group, a.workspace, stream);
-  if (err != cudaSuccess) return err;
+  if (a.dt == VN_BF16 && a.in > 0) return sliced(a.dt, a.in) ? run_slices(a, stream) : run_terms(a, stream);
+  if (a.in > 0) {  // else there is nothing to unpack, and the sums are zeros
+    const cudaError_t err = launch_unpack(a.codes, a.scales, a.dt, a.out, a.in, a.group, a.workspace, stream);
+    if (err != cudaSuccess) return err;
+  }
   DenseArgs d = {};
   d.x = a.x; d.w = a.workspace; d.dt = a.dt; d.b = a.b; d.b_dt = a.b_dt; d.residual = a.residual;
   d.rows = a.rows; d.in = a.in; d.out = a.out; d.act = a.act; d.y = a.y;
