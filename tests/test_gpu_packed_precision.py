@@ -1,4 +1,4 @@
-"""The layer on weights in 4 bits is as exact with many rows as with few, and may be empty.
+"""The layer on weights in 4 bits is as exact with many rows as with few, over the whole range of x, and may be empty.
 
 With A = sum |x| |v| of an output. A product on the tensor cores is exact, and each step of 16 k cut below 2^-23 of what it adds up;
 the sums of groups, of splits of k and of warps are fp32. Few rows: as in test_gpu_packed.py. Many rows in bf16: a value is the sum of two
@@ -166,3 +166,20 @@ def test_an_empty_layer_for_any_number_of_rows(rows, kind):
     x = torch.empty(rows, 0, dtype=KINDS[kind], device=DEV)
     assert torch.equal(vn.linear4(x, empty, b).float(), b.expand(rows, 4))
     assert torch.equal(vn.linear4(x, empty, b, activation="relu", residual=r).float(), b.expand(rows, 4) + 1)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 5, 20, 40])
+def test_the_whole_range_of_x(rows, kind):
+    """Results that fp32 holds are finite, whatever the size of x: a group's sum of x times codes, up to 7 * 128 |x|, would not be."""
+    k = 256
+    for size, scale in ((3e38, 1e-4), (1e36, 1e-3), (4e36, 0.05), (1e-3, 1e37), (1e-25, 1.0), (1e-25, 1e20)):
+        g = torch.Generator().manual_seed(15)
+        w = (torch.rand(12, k, generator=g) * scale).to(KINDS[kind])
+        w[1] *= -1
+        w[2, ::2] *= -1
+        p, v = packed(w, 128, kind)
+        x = ((torch.rand(rows, k, generator=g) * 0.5 + 0.5) * size).to(KINDS[kind])
+        if size > 1e38:
+            x[:, 3:] *= 0.005
+        check(p, v, x, kind)

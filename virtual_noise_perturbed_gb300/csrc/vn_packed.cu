@@ -6,7 +6,8 @@
 // Codes lie as the tensor cores' warp-level product wants them: a row is blocks of 128 k in 64 bytes, of which lane t of
 // four reads the 16 bytes t. Word w of those holds the products 2 w and 2 w + 1, and of product p the k = 16 p + 4 t + 0 .. 3.
 // Each code + 8 is a nibble; a pair of neighbouring k lies 16 bits apart, so one mask and one exponent make two
-// bf16 values 128 + code + 8 of it, and one subtraction the codes (both exact).
+// bf16 values 2^-3 + (code + 8) 2^-10 of it, and one subtraction the codes in units of 2^-10 (both exact). In these units no sum of a
+// group, of up to 7 times 128 |x|, passes what fp32 holds; they are taken off at the end (of results, 2^-139 a sum may be lost by it).
 //
 // The layer on few rows (up to 32, fp32 10) is bound by latency and by the instructions that make operands of codes, 17 for the
 // 256 weights of a product, beside reading the codes once: so the rows of x are the product's columns, eight at no
@@ -31,7 +32,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kBlock = 128;            // k of a block
 constexpr int kBlockBytes = 64;
-constexpr uint32_t kMagic = 0x43004300u;  // 128 in bf16, twice
+constexpr uint32_t kMagic = 0x3E003E00u;  // 2^-3 in bf16, twice
 constexpr uint32_t kNothing = 0x88888888u;
 
 __device__ __forceinline__ float value(float x) { return x; }
@@ -292,10 +293,10 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t* codes, 
 }
 
 // ---------------------------------------------------------------- the linear layer
-// Codes in bf16 of one product: k pairs 0 and 1 of four, from bits `shift` on.
+// Codes in units of 2^-10 of one product, in bf16: k pairs 0 and 1 of four, from bits `shift` on.
 __device__ __forceinline__ uint32_t decode(uint32_t word, int shift) {
   uint32_t v = ((word >> shift) & 0x000F000Fu) | kMagic;
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __floats2bfloat162_rn(136.f, 136.f));
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __floats2bfloat162_rn(0.1328125f, 0.1328125f));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 __device__ __forceinline__ void product(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -482,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 2) packed_kernel(const PackedArgs a,
       for (int w = 0; w < kWarps; ++w) v += parts[w][f][r * kTerms<T> + q];
       z[0] += v;
     }
+    z[0] *= 1024.f;
     if (a.b != nullptr)
       z[0] += a.b_dt == VN_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.b)[j]) : static_cast<const float*>(a.b)[j];
     activate_all<false>(a.act, z);
