@@ -3,14 +3,13 @@
 //   norm = sqrt(sum over all tensors of g^2),   factor = norm <= bound ? 1 : bound / norm,   out = g factor
 //
 // The norm reads every element once and the scaling reads and writes it, so the bound is memory (the
-// second reading comes from L2 where the gradient fits there). Sums: eight squares in fp32, those sums
-// in pairs of fp32 that carry each other's rounding (exact but for the last bits of the second), a thread's
-// pair, a CTA's threads and the CTAs in 64 bits, in a fixed order: results do not depend on the order
-// of CTAs, and the norm is the exact one rounded once but where that falls within 2^-36 of a border.
-// Eight squares whose sum leaves what fp32 holds to full precision are taken in 64 bits, so the norm is
+// second reading comes from L2 where the gradient fits there). Sums: squares and their sums in pairs of fp32 of which the second
+// carries what the first rounds off, its own roundings below 2^-37; the warps' and the CTAs' in 64 bits, in a fixed order:
+// results do not depend on the order of CTAs, and the norm is the exact one rounded once but where that falls within 2^-36
+// of a border. Eight squares whose sum leaves what fp32 holds to full precision are taken in 64 bits, so the norm is
 // right over the whole range of the types (fp64 has 1/64 of fp32's rate here: no other element sees it).
-// The norm of 805 MB fp32 takes 118 us, 6.8 TB/s; 109 MB of bf16 24 us and, scaled to other buffers, 53 (three launches: squares,
-// their join, scaling); a policy's 0.3 MB 4.4 of the GPU in one launch, and 6.3 with the call on the host.
+// The norm of 805 MB fp32 takes 117 us, 6.9 TB/s; 109 MB of bf16 20 us and, scaled to other buffers, 47 (three launches: squares,
+// their join, scaling); a policy's 0.3 MB 4.5 of the GPU in one launch, and 6.3 with the call on the host.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -57,24 +56,60 @@ __device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162floa
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// A sum of squares: a pair of fp32, and what fp32 cannot hold.
+// A sum of squares: fp32 in two lanes, what its additions round off, and what fp32 cannot hold. `hi` starts from `base`, a power of
+// two above the squares to come. Then, with t = RN(hi + x^2) below 2 hi, t - hi has no rounding, and x^2 - (t - hi), a multiply-add good to
+// 2^-24 of itself, is what t rounds off: four instructions for two elements. Where t is not below 2 hi, the base is raised.
 struct Sum {
-  float hi = 0.f, lo = 0.f;
+  F2 hi = 0, lo = 0;
+  float base = 0.f;  // in each lane of hi
   double wide = 0.0;
   __device__ __forceinline__ void add(const float (&x)[kGroup]) {
+    const F2 minus = f2(-1.f, -1.f);
+#pragma unroll 1
+    for (int turn = 0;; ++turn) {
+      F2 t = hi, rest = 0;
+#pragma unroll
+      for (int q = 0; q < kGroup; q += 2) {
+        const F2 v = f2(x[q], x[q + 1]), next = fma2(v, v, t), r = fma2(v, v, fma2(next, minus, t));
+        rest = q == 0 ? r : add2(rest, r);
+        t = next;
+      }
+      float a, b, c, d;
+      split(t, &a, &b);
+      split(hi, &c, &d);
+      if (a < 2.f * c && b < 2.f * d) {
+        hi = t;
+        lo = add2(lo, rest);
+        return;
+      }
+      if (turn == 1 || !raise(x)) break;
+    }
+    wide += squares(x[0], x[1], x[2], x[3]) + squares(x[4], x[5], x[6], x[7]);
+  }
+  // A base of four to eight times these squares' sum. Below 2^-76 the squares that fp32 cannot hold would count (they are below
+  // 2^-149, however many); from 2^100 on `hi` could pass its largest value; a NaN is neither. (At or above hi the sum is above the old base.)
+  __device__ __forceinline__ bool raise(const float (&x)[kGroup]) {
     F2 s = mul2(f2(x[0], x[1]), f2(x[0], x[1]));
 #pragma unroll
     for (int q = 2; q < kGroup; q += 2) s = fma2(f2(x[q], x[q + 1]), f2(x[q], x[q + 1]), s);
     const float v = sum_of(s);
-    // Below 2^-90 the squares that fp32 cannot hold would count (they are below 2^-126); from 2^100 on the pair
-    // could pass its largest value; a NaN is neither.
-    if (v >= 0x1p-90f && v < 0x1p100f) {
-      const float t = __fadd_rn(hi, v), b = __fsub_rn(t, hi);
-      lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(v, b)));
-      hi = t;
-    } else {
-      wide += squares(x[0], x[1], x[2], x[3]) + squares(x[4], x[5], x[6], x[7]);
-    }
+    if (!(v >= 0x1p-76f && v < 0x1p100f)) return false;
+    const float up = __uint_as_float((__float_as_uint(v) & 0x7F800000u) + (3u << 23));
+    float a, b, c, d;
+    split(hi, &a, &b);
+    split(lo, &c, &d);
+    c += plus(a, up) + plus(a, -base);
+    d += plus(b, up) + plus(b, -base);
+    hi = f2(a, b);
+    lo = f2(c, d);
+    base = up;
+    return true;
+  }
+  // What `lo` has gathered, to `hi`: its own roundings stay below 2^-37 of the sum.
+  __device__ __forceinline__ void settle() {
+    const F2 minus = f2(-1.f, -1.f), t = add2(hi, lo);
+    lo = add2(lo, fma2(t, minus, hi));
+    hi = t;
   }
   // Out of line and by value: the sums of every other element stay in registers.
   static __device__ __noinline__ double squares(float a, float b, float c, float d) {
@@ -82,20 +117,47 @@ struct Sum {
     const double x = a, y = b, z = c, w = d;
     return x * x + y * y + z * z + w * w;
   }
-  __device__ __forceinline__ double total() const { return static_cast<double>(hi) + static_cast<double>(lo) + wide; }
+  // The sum over a warp, in lane 0: pairs of fp32 (below 2^122 here) whose additions are as exact, and 64 bits where a lane has them.
+  __device__ __forceinline__ double warp_total() const {
+    float h, l, o, c, d;
+    split(hi, &h, &o);
+    split(lo, &c, &d);
+    l = (plus(h, -base) + plus(o, -base)) + (c + d);
+    l += plus(h, o);
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) {
+      const float more = l + __shfl_xor_sync(0xFFFFFFFFu, l, i);
+      l = plus(h, __shfl_xor_sync(0xFFFFFFFFu, h, i)) + more;
+    }
+    double w = 0.0;
+    if (__any_sync(0xFFFFFFFFu, wide != 0.0)) {
+      w = wide;
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, i);
+    }
+    return static_cast<double>(h) + (static_cast<double>(l) + w);
+  }
+  // a += b, and what that rounds off.
+  static __device__ __forceinline__ float plus(float& a, float b) {
+    const float t = __fadd_rn(a, b), n = __fsub_rn(t, a);
+    const float rest = __fadd_rn(__fsub_rn(a, __fsub_rn(t, n)), __fsub_rn(b, n));
+    a = t;
+    return rest;
+  }
 };
 
-// The sum over a CTA's threads, in every one of them.
+// The sum over a CTA's warps of what their lanes 0 have, in thread 0. (64 bits are 16 cycles an instruction and warp, so few take part:
+// with every thread adding them up, and lanes in 64 bits too, a norm of 4 M elements took 8.5 us, of 109 MB in bf16 20.5.)
 __device__ __forceinline__ double cta_sum(double v) {
   __shared__ double s[kThreads / 32];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
   __syncthreads();
-  double r = s[0];
+  if (threadIdx.x < 32) {
+    v = threadIdx.x < kThreads / 32 ? s[threadIdx.x] : 0.0;
 #pragma unroll
-  for (int w = 1; w < kThreads / 32; ++w) r += s[w];
-  return r;
+    for (int o = kThreads / 64; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  }
+  return v;
 }
 
 // What a launch reads per thread and 16 bytes.
@@ -159,6 +221,7 @@ __device__ __forceinline__ void square_chunk(const Table<kCap>& t, int64_t chunk
   } else {
     each_single(g, e.n - base, [&](int, int, const float(&x)[kGroup]) { sum.add(x); });
   }
+  sum.settle();
 }
 
 // out = g f over one chunk.
@@ -211,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) square_kernel(const __grid_constant_
   after_previous();
   Sum sum;
   for (int64_t chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) square_chunk<T>(t, chunk, sum);
-  const double total = cta_sum(sum.total());
+  const double total = cta_sum(sum.warp_total());
   if (threadIdx.x == 0) parts[blockIdx.x] = total;
 }
 
@@ -221,6 +284,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const double* parts, int
   after_previous();
   double v = 0.0;
   for (int64_t i = threadIdx.x; i < count; i += kThreads) v += fetch(parts + i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   v = cta_sum(v);
   if (threadIdx.x != 0) return;
   const double n = sqrt(v);
@@ -247,7 +312,7 @@ few_kernel(const __grid_constant__ Table<kCap> t, double bound, float* norm, flo
   after_previous();
   Sum sum;
   for (int64_t chunk = blockIdx.x; chunk < t.chunks; chunk += kCluster) square_chunk<T>(t, chunk, sum);
-  const double total = cta_sum(sum.total());
+  const double total = cta_sum(sum.warp_total());
   if (threadIdx.x == 0) mine = total;
   cluster.sync();
   double parts = 0.0;
