@@ -459,7 +459,7 @@ vn_status vn_gradient_norm(const vn_gradient* tensors, int64_t n_tensors, vn_dty
 /*
  * vn_clip_gradients -- the same, and out = g * factor with
  *     factor = norm <= max_norm ? 1 : max_norm / norm       (norm before its rounding; factor one fp32)
- * for every element, rounded once to dt. out may be the tensor's own grad (in place; nothing is written where
+ * for every element, the product in fp32, then rounded to dt. out may be the tensor's own grad (in place; nothing is written where
  * factor is 1); else no out may share memory with any grad, and no two outs may. max_norm >= 0 (infinite: never
  * clips). An infinite norm gives factor 0 (NaN where the gradient is infinite), a NaN gives NaN everywhere.
  */

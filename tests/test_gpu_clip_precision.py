@@ -81,3 +81,19 @@ def test_the_factor_takes_the_norm_before_its_rounding(n):
         f = np.float64(np.float32(0.3 * want / want))
         scaled = f64(x) * (0.3 * want / want)
         assert np.all(np.abs(f64(out) - scaled) <= (2 * U + 2.0 ** -33) * np.abs(scaled)), f
+
+
+@pytest.mark.parametrize("bound", [0.2, 1e9])
+def test_clipped_elements_are_fp32_products(bound):
+    """out = type(fp32(g factor)) with the factor in fp32, in both types."""
+    for kind in ("fp32", "bf16"):
+        g = torch.Generator().manual_seed(2)
+        x = [torch.randn(s, generator=g).to(KINDS[kind]) for s in ((40, 1000), (7,), (8195,))]
+        out = [torch.empty_like(t, device=DEV) for t in x]
+        vn.clip_gradients([t.to(DEV) for t in x], bound, out=out)
+        norm = math.sqrt(math.fsum(exact(t) ** 2 for t in x))
+        f = torch.tensor(1.0 if norm <= bound else bound / norm, dtype=torch.float32)
+        for o, t in zip(out, x):
+            assert torch.equal(o.cpu(), (t.float() * f).to(KINDS[kind]))
+
+

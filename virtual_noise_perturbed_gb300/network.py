@@ -127,7 +127,8 @@ def gradient_norm(grads: Gradients, *, out: Optional[torch.Tensor] = None) -> to
 
 def clip_gradients(grads: Gradients, max_norm: float, *, out: Optional[Gradients] = None) -> torch.Tensor:
     """Scale ``grads`` to a norm of at most ``max_norm``, and return the norm that they had
-    (``vn_clip_gradients``): each element times max_norm / norm where norm > max_norm, rounded once.
+    (``vn_clip_gradients``): each element times the float32 max_norm / norm where norm > max_norm, a float32 product
+    rounded to the gradient's dtype.
 
     ``grads``: a tensor or a sequence of them, contiguous, of one dtype, written over in place, or with
     ``out``, tensors like them that take the result, only read. An infinite norm makes the factor 0 (NaN where the
