@@ -1,0 +1,52 @@
+"""Drawing an index next to the borders of min-p, against float64."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import acting as ora
+import virtual_noise_perturbed_gb300 as vn
+from virtual_noise_perturbed_gb300.build import build
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build()
+
+
+def neighbours(at, count):
+    """fp32 values around a number, in order."""
+    bits = np.float32(at).view(np.int32) + np.arange(-count, count + 1, dtype=np.int32)
+    return bits.view(np.float32)
+
+
+@pytest.mark.parametrize("each", [False, True])
+@pytest.mark.parametrize("n", [12, 60, 200, 401, 4096])
+@pytest.mark.parametrize("min_p,t,top", [(0.999, 1.0, 0.0), (0.97, 0.5, 0.0), (0.7, 1.3, 1e-3), (0.02, 1.0, 3.0), (0.999, 1.0, -0.25)])
+def test_logits_next_to_where_min_p_ends(min_p, t, top, n, each):
+    """Logits around top + T ln(min_p). The promised 3e-11 decides: those nearer than 4e-11 to min_p are left out."""
+    if each:
+        min_p = float(np.float32(min_p))
+    v = neighbours(top + t * math.log(min_p), 150)
+    w = np.exp((v.astype(np.float64) - np.float32(top)) / t)
+    v = v[np.abs(w - min_p) > 4e-11]
+    assert (np.exp((v.astype(np.float64) - np.float32(top)) / t) >= min_p).any()
+    g = torch.Generator().manual_seed(n)
+    rows = 40
+    x = torch.full((rows, n), top - 8 * t)  # below every min_p here
+    x[:, 0] = top
+    take = min(n - 1, 300)
+    for r in range(rows):
+        x[r, 1:1 + take] = torch.from_numpy(v)[torch.randint(0, len(v), (take,), generator=g)]
+    u = torch.rand(rows, generator=g)
+    arg = torch.full((rows,), min_p, device=DEV) if each else min_p
+    tt = torch.full((rows,), t, device=DEV) if each else t
+    got = vn.sample(x.to(DEV), u.to(DEV), temperature=tt, min_p=arg).cpu().numpy()
+    t64 = float(np.float32(t)) if each else t
+    want = [ora.sample(x[r].double().numpy(), float(u[r]), temperature=t64, min_p=min_p)[0] for r in range(rows)]
+    assert got.tolist() == want

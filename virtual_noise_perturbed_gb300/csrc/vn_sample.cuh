@@ -237,13 +237,13 @@ __device__ __forceinline__ float logprob_of(float x, float m, const Wish& w, u64
 }
 
 // Where the min-p prefix ends, for logits next to its border by their weights. The estimate is off by a few
-// roundings of |m| and T ln(min_p); `sure` is 2^-20 of them.
+// roundings of |m| and T ln(min_p), `sure` has 2^-20 of them, and by min_p's own rounding to fp32, which is 2^-24 T: `sure` has 2^-23 T.
 struct Floor {
   float at, sure;
   __device__ __forceinline__ Floor(float m, const Wish& w) {
     const float drop = logf(w.min_p) * w.temperature;
     at = m + drop;
-    sure = 0x1p-20f * (fabsf(m) + fabsf(drop)) + 1e-37f;
+    sure = 0x1p-20f * (fabsf(m) + fabsf(drop)) + 0x1p-23f * fabsf(w.temperature) + 1e-37f;
   }
   __device__ __forceinline__ bool above(float x, float m, const Wish& w, const u64* powers) const {
     if (x == m || x >= at + sure) return true;
