@@ -50,3 +50,13 @@ def test_logits_next_to_where_min_p_ends(min_p, t, top, n, each):
     t64 = float(np.float32(t)) if each else t
     want = [ora.sample(x[r].double().numpy(), float(u[r]), temperature=t64, min_p=min_p)[0] for r in range(rows)]
     assert got.tolist() == want
+
+
+@pytest.mark.parametrize("n", [8, 100, 500])
+def test_min_p_at_an_infinite_temperature(n):
+    """All finite logits weigh as much as the largest, so none is filtered."""
+    x = torch.arange(float(n)).expand(5, n).clone()
+    u = torch.tensor([0.0, 0.3, 0.5, 0.77, 0.999])
+    for p in (0.5, 1.0):
+        got = vn.sample(x.to(DEV), u.to(DEV), temperature=torch.full((5,), math.inf, device=DEV), min_p=p)
+        assert got.tolist() == [int(v * n) for v in u.double().tolist()]

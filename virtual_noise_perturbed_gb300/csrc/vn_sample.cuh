@@ -245,9 +245,10 @@ struct Floor {
     at = m + drop;
     sure = 0x1p-20f * (fabsf(m) + fabsf(drop)) + 0x1p-23f * fabsf(w.temperature) + 1e-37f;
   }
+  // (At an infinite temperature with a min_p of 1 the estimate is a NaN, and weights decide; so they do for no logit, which has none.)
   __device__ __forceinline__ bool above(float x, float m, const Wish& w, const u64* powers) const {
     if (x == m || x >= at + sure) return true;
-    if (!(x >= at - sure)) return false;
+    if (x < at - sure) return false;
     return weight(x, m, w, powers) >= w.min_units;
   }
 };
