@@ -523,8 +523,10 @@ int64_t vn_linear_packed_workspace(int64_t rows, int64_t in, int64_t out, vn_dty
  *           (the first one always); of those the ones with w_i >= min_p
  *     index = the smallest i, in index order, with  sum_{j <= i, kept} w_j > u S,   S = sum_kept w
  *     logprob = ln(w_index / S)                                       (fp32 [rows], or NULL)
- * index [rows] int64. The index is float64's but where u S, or a border of a filter, lies within about
- * 2e-11 of it: weights are whole numbers in units of 2^-42, and weights below half a unit are never drawn.
+ * index [rows] int64. The index is float64's but where u S, or a border of a filter, lies within 3e-11 S + n 2^-43 of
+ * another: weights are whole numbers in units of 2^-42, and weights below half a unit are never drawn, nor is a logit that
+ * lies further below the largest than fp32's largest value. logprob: beyond 128 logits S - 1 may be off by 2.2e-6 of itself (so
+ * logprob by as much at most), up to there by the same as an index; then fp32's roundings of its two terms.
  * temperature <= 0 takes the largest logit; top_k <= 0 or >= n, top_p >= 1 and min_p <= 0 filter nothing;
  * top_p <= 0 and min_p >= 1 keep the first and the largest ones; u below 0 is 0, u >= 1 the last index of the sum.
  * A logit of -infinity is never drawn, infinite ones share all of the probability. A row with a NaN, without any

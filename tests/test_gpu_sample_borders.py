@@ -1,4 +1,4 @@
-"""Drawing an index next to the borders of min-p, against float64."""
+"""Drawing an index next to the borders of min-p, and how exact it is on the longest rows, against float64."""
 
 import math
 
@@ -60,3 +60,32 @@ def test_min_p_at_an_infinite_temperature(n):
     for p in (0.5, 1.0):
         got = vn.sample(x.to(DEV), u.to(DEV), temperature=torch.full((5,), math.inf, device=DEV), min_p=p)
         assert got.tolist() == [int(v * n) for v in u.double().tolist()]
+
+
+@pytest.mark.parametrize("n", [5000, 131071, 524288])
+@pytest.mark.parametrize("tail", [-29.2, -28.9, -20.0])
+def test_long_flat_tails(n, tail):
+    """By float64's sums u S lies between those at the index and before it, to within n 2^-43 of the largest weight, for the rounding of
+    each weight to a whole unit of 2^-42, and 3e-11 of S."""
+    x = torch.full((1, n), tail)
+    x[0, 0] = 0.0
+    w = np.exp(x[0].double().numpy())
+    c = np.cumsum(w)
+    us = [1.0 - 2.0 ** -24, 1.0 - 2.0 ** -23, 1.0 - 2.0 ** -20, 0.5, 0.0]
+    index, logp = vn.sample(x.to(DEV).expand(len(us), n), torch.tensor(us).to(DEV), logprobs=True)
+    bound = n * 2.0 ** -43 + 3e-11 * c[-1]
+    for i, u in zip(index.tolist(), us):
+        assert c[i] >= u * c[-1] - bound and (i == 0 or c[i - 1] <= u * c[-1] + bound), (u, i)
+    # The share's logarithm: S is known to 2.2e-6 of what it has beyond the largest, then a few roundings.
+    for i, l in zip(index.tolist(), logp.tolist()):
+        want = math.log(w[i] / c[-1])
+        assert abs(l - want) <= 2.2e-6 * (c[-1] - 1) / c[-1] + 8 * 2.0 ** -24 * (abs(want) + abs(tail)) + 1e-12
+
+
+def test_logits_further_apart_than_fp32_reaches():
+    """Beyond 3.4e38 below the largest a logit is never drawn, at any temperature."""
+    for n in (6, 60, 600):
+        x = torch.full((3, n), -3e38)
+        x[:, 2] = 3e38
+        got = vn.sample(x.to(DEV), torch.tensor([0.0, 0.5, 1 - 2.0 ** -24]).to(DEV), temperature=1e38)
+        assert got.tolist() == [2, 2, 2]

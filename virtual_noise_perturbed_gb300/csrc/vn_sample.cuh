@@ -6,8 +6,9 @@
 //   index = the smallest i, in index order, with  sum_{j <= i, kept} w_j > u S,  S the sum of all kept w
 //
 // Which index it is hangs on sums next to a border, so a weight is a whole number: w in units of 2^-42, good
-// to 2^-35 of itself. Sums of whole numbers are exact in any order, whatever adds them: lanes, CTAs of
-// a cluster, atomics. (With sums of fp32 one row in a hundred of 4,096 would differ from float64's index.)
+// to 2^-35 of itself and half a unit. Sums of whole numbers are exact in any order, whatever adds them: lanes, CTAs of
+// a cluster, atomics. So a sum over a row is good to 2^-35 of itself and n 2^-43 (the largest weight is 1): 2^-24 on the longest
+// rows, where all of it lies in a flat tail some 29 T below the largest logit. (With sums of fp32 one row in a hundred of 4,096 would differ from float64's index.)
 // Such a weight takes some 45 instructions, so rows beyond 128 logits are decided by coarse weights of 10,
 // whose sums' error is bounded, and by whole ones only where a border lies within that bound: one row in
 // fifty at 4,096 logits, half of them at 131,072.

@@ -330,7 +330,8 @@ def sample(logits: torch.Tensor, uniforms: torch.Tensor, *, temperature: PerRow 
     The weights are exp(logits / temperature). ``top_k`` keeps the k largest logits (of equal ones those with the lower
     index), ``top_p`` of those the largest ones until their sum reaches that share, ``min_p`` those whose weight is at
     least that share of the largest's. The index is the first at which the sum of the kept weights passes
-    ``uniforms`` times the whole: float64's index, whatever the sizes. Each parameter is a number, None (no filter) or a
+    ``uniforms`` times the whole: float64's index, but where sums next to a border are closer than 3e-11 of the whole and
+    n 2^-43 of the largest weight. Each parameter is a number, None (no filter) or a
     tensor of the leading shape (float32, ``top_k`` int64). A temperature of 0 takes the largest logit. With ``logprobs=True`` the result is
     (index, log of the kept weights' share that it has), the latter float32.
 
