@@ -183,3 +183,11 @@ def test_the_whole_range_of_x(rows, kind):
         if size > 1e38:
             x[:, 3:] *= 0.005
         check(p, v, x, kind)
+
+
+@pytest.mark.parametrize("rows", [16384, 16385, 50001])
+def test_more_rows_than_are_laid_out_at_once(rows):
+    w = randn(24, 70, kind="bf16", seed=19, scale=0.1)
+    p, v = packed(w, 32, "bf16")
+    x = randn(rows, 70, kind="bf16", seed=20)
+    check(p, v, x, "bf16", randn(24, seed=21), "tanh", randn(rows, 24, kind="bf16", seed=22))

@@ -30,10 +30,10 @@ constexpr int kGroup = 8;                      // elements that are squared and 
 constexpr int kLoads = 4;                      // 16-byte loads of a thread in flight
 template <typename T>
 constexpr int kChunkOf = kThreads * kLoads * 16 / static_cast<int>(sizeof(T));  // elements of a CTA's turn
-constexpr int kPerSm = 6;                      // CTAs an SM that sum squares: 805 MB of fp32 126 us with 4, 118 with 6, 135 with 8
+constexpr int kPerSm = 6;                      // CTAs an SM that sum squares: 805 MB of fp32 127 us with 4, 117 with 6, 135 with 8
 constexpr int kCluster = 16;                   // CTAs of the kernel for few chunks
-// Up to here (1 MB) that kernel: clipping 8, 32 and 64 chunks takes 4.4, 5.3 and 7.0 us of the device for 5.8, 5.9 and 6.2
-// of the three launches, which cost 10 us of the host for 7; with 128 chunks 10.2 for 7.2.
+// Up to here (1 MB) that kernel: clipping 8, 32 and 64 chunks takes 3.3, 3.8 and 5.0 us of the device for 4.6, 5.1 and 5.6
+// of the three launches, which cost 9 us of the host for 4 to 6; with 128 chunks 6.4 for 6.6.
 constexpr int64_t kFewChunks = 64;
 constexpr int kSmall = 16, kLarge = 896;       // tensors of a launch
 
@@ -147,7 +147,7 @@ struct Sum {
 };
 
 // The sum over a CTA's warps of what their lanes 0 have, in thread 0. (64 bits are 16 cycles an instruction and warp, so few take part:
-// with every thread adding them up, and lanes in 64 bits too, a norm of 4 M elements took 8.5 us, of 109 MB in bf16 20.5.)
+// with every thread adding them up, and lanes in 64 bits too, the norm of 4 M elements in fp32 took 8.5 us for 6.8.)
 __device__ __forceinline__ double cta_sum(double v) {
   __shared__ double s[kThreads / 32];
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
