@@ -449,7 +449,7 @@ typedef struct vn_gradient {
 /*
  * vn_gradient_norm -- the norm over all elements of n_tensors tensors (a HOST array, read during the
  * call), norm = sqrt(sum g^2), one fp32 on the device: the exact norm rounded once, but for a last bit
- * where it falls next to a border. A norm beyond fp32's largest value is infinite, one of a gradient with a
+ * where it falls within 2^-36 of itself of a border. A norm beyond fp32's largest value is infinite, one of a gradient with a
  * NaN is NaN; no tensors, or empty ones, have norm 0. Sums have a fixed order.
  * workspace: vn_gradient_norm_workspace bytes, 256-byte aligned. n_tensors up to 2^32.
  */

@@ -12,9 +12,10 @@
 // The layer on few rows (up to 32, fp32 10) is bound by latency and by the instructions that make operands of codes, 17 for the
 // 256 weights of a product, beside reading the codes once: so the rows of x are the product's columns, eight at no
 // more cost than one. fp32 rows take three columns each, for the three bf16 terms of their values; a code is exact in
-// bf16. The sum of a group is scaled in fp32. One row of 4096 to 4096 bf16 5.2 us (8.9 MB: 1.7 TB/s; plain bf16
-// weights take 6.2), 8 rows 6.4, 32 14.9; fp32 6.9, 5 rows 9.6. More rows take unpacked weights, in bf16 as two terms each: 64 rows 27 us
-// and 1024 60 (32 rows at a time 28 and 445), fp32 16 rows 36.
+// bf16. The sum of a group is scaled in fp32. 4096 to 4096 in a replayed graph, bf16: one row 4.5 us (8.9 MB: 2.0 TB/s; plain
+// weights take 5.2), 8 rows 5.6, 32 13.9; fp32 5.9, 5 rows 8.5, 10 rows 14.4. More rows take unpacked weights, in bf16 as two terms
+// each: 64 rows 28 us, 256 43, 1024 60 (32 rows at a time 28, 111 and 445; 64 rows of 1024 to 1024 12.6 and 10.0, of 256 to 256 4.9 and 5.8),
+// fp32 16 rows 37 and 64 42 (ten rows at a time 28 and 93).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
