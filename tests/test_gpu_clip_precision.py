@@ -97,3 +97,20 @@ def test_clipped_elements_are_fp32_products(bound):
             assert torch.equal(o.cpu(), (t.float() * f).to(KINDS[kind]))
 
 
+
+
+@pytest.mark.parametrize("grow", [1.9, 1.4])
+def test_squares_that_grow_beyond_what_fp32_sums_hold(grow):
+    """Every eight elements of a thread (4096 a CTA's turn in fp32, two eights a thread; 912 turns side by side) have larger squares than
+    those before them, from 2^96 to beyond 2^127."""
+    rounds = int(math.ceil(32 / math.log2(grow)))
+    square = 2.0 ** 96 * grow ** np.arange(rounds)
+    value = np.sqrt(square).astype(np.float32)
+    per = torch.from_numpy(value).to(DEV)
+    x = per.view(-1, 2).repeat_interleave(912, 0) if rounds % 2 == 0 else per[:-1].view(-1, 2).repeat_interleave(912, 0)
+    x = x[:, :, None].expand(-1, 2, 2048).reshape(-1)
+    used = value[:rounds // 2 * 2].astype(np.float64)
+    want = math.sqrt(math.fsum((used ** 2 * (912 * 2048)).tolist()))
+    assert want < 3e38
+    got = float(vn.gradient_norm(x))
+    assert abs(got - want) <= U * (1 + 2.0 ** -10) * want, (got, want)

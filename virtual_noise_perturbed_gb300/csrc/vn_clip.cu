@@ -77,7 +77,7 @@ struct Sum {
       float a, b, c, d;
       split(t, &a, &b);
       split(hi, &c, &d);
-      if (a < 2.f * c && b < 2.f * d) {
+      if (a < 2.f * c && b < 2.f * d && fmaxf(a, b) < kMost) {
         hi = t;
         lo = add2(lo, rest);
         return;
@@ -86,8 +86,10 @@ struct Sum {
     }
     wide += squares(x[0], x[1], x[2], x[3]) + squares(x[4], x[5], x[6], x[7]);
   }
+  // A warp adds 64 lanes up. (A thread's squares that are below 2^100 by eights do not get there; ones that grow from eight to eight may.)
+  static constexpr float kMost = 0x1p118f;
   // A base of four to eight times these squares' sum. Below 2^-76 the squares that fp32 cannot hold would count (they are below
-  // 2^-149, however many); from 2^100 on `hi` could pass its largest value; a NaN is neither. (At or above hi the sum is above the old base.)
+  // 2^-149, however many); from 2^100 on `hi` could pass its largest value; a NaN is neither.
   __device__ __forceinline__ bool raise(const float (&x)[kGroup]) {
     F2 s = mul2(f2(x[0], x[1]), f2(x[0], x[1]));
 #pragma unroll
@@ -95,6 +97,7 @@ struct Sum {
     const float v = sum_of(s);
     if (!(v >= 0x1p-76f && v < 0x1p100f)) return false;
     const float up = __uint_as_float((__float_as_uint(v) & 0x7F800000u) + (3u << 23));
+    if (up <= base) return false;  // it was kMost
     float a, b, c, d;
     split(hi, &a, &b);
     split(lo, &c, &d);
@@ -117,7 +120,7 @@ struct Sum {
     const double x = a, y = b, z = c, w = d;
     return x * x + y * y + z * z + w * w;
   }
-  // The sum over a warp, in lane 0: pairs of fp32 (below 2^122 here) whose additions are as exact, and 64 bits where a lane has them.
+  // The sum over a warp, in lane 0: pairs of fp32 (below 2^124) whose additions are as exact, and 64 bits where a lane has them.
   __device__ __forceinline__ double warp_total() const {
     float h, l, o, c, d;
     split(hi, &h, &o);
